@@ -245,7 +245,7 @@ def _gated_plain(s):
     out = {"y": h.to(io), "h_final": h[:, -1].contiguous()}
     if case["mode"] == "prefill":
         return out
-    g = s["dy"].float()
+    g = s["dy"].to(F32, copy=True)  # overwritten below
     if s["dh_final"] is not None:
         g[:, -1] += s["dh_final"]
     later = torch.cat([a[:, 1:], torch.zeros_like(a[:, :1])], 1)
