@@ -582,6 +582,138 @@ ssm_status ssm_scan_fwd_mimo_profiled(const void *x, const void *dt, const float
                                       void *workspace, size_t workspace_bytes, void *hip_stream,
                                       void *const *events, int32_t n_events);
 
+/* ------------------------------------------------------------------ gated linear recurrence
+ * A diagonal recurrence whose decay comes from a gate, per channel d:
+ *     k_t = c softplus(decay[d]) sigmoid(r_t),    a_t = exp(-k_t),
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,    y_t = h_t.
+ *   x, r, i, y  : [batch, L, d_inner] of io (r and i before their sigmoid)
+ *   decay       : [d_inner] float32 (any sign);  c: finite, > 0
+ *   h0, h_final : [batch, d_inner] float32, NULL = zero / not wanted
+ *   reset       : [batch, L] bytes, NULL = none. A non-zero byte marks the first step of a
+ *                 document: h_{t-1} is taken as 0 there, so that nothing of an earlier
+ *                 document, NaN and Inf included, reaches a later one, in the outputs or
+ *                 in the gradients.
+ *   states      : NULL, or what ssm_gated_bwd needs: the state entering every
+ *                 SSM_GATED_STATE_EVERY-th step, [batch, ceil(L / SSM_GATED_STATE_EVERY),
+ *                 d_inner] float32 (ssm_gated_states_bytes bytes).
+ * 1 - a^2 is formed as -expm1(-2k): it keeps its relative precision where a is close to 1.
+ * The recurrence runs in float32; y is rounded once. workspace: at least
+ * ssm_gated_fwd_workspace(...) / ssm_gated_bwd_workspace(...) bytes, 256-byte aligned (0 is
+ * possible, then it may be NULL); its contents on entry are ignored.
+ * ssm_gated_bwd gives the gradients of sum(dy y) + sum(dh_final h_final): dx, dr, di of io,
+ * ddecay [d_inner] and dh0 [batch, d_inner] float32 (dh0 NULL = not wanted, dh_final NULL
+ * = 0). It reads x, r, i, decay, reset and c as the forward had them, and its states. Sums
+ * run in a fixed order: equal calls give equal bits.
+ * Outputs must not overlap inputs or each other (SSM_ERR_UNSUPPORTED). Alignment: float32
+ * arrays 4 bytes, the others one element. L == 0 writes h_final = h0 (dh0 = dh_final,
+ * ddecay = 0). batch is at most 65535, d_inner at most 2^28. */
+#define SSM_GATED_STATE_EVERY 64
+size_t ssm_gated_states_bytes(int64_t batch, int64_t L, int64_t d_inner);
+size_t ssm_gated_fwd_workspace(int64_t batch, int64_t L, int64_t d_inner);
+size_t ssm_gated_bwd_workspace(int64_t batch, int64_t L, int64_t d_inner);
+ssm_status ssm_gated_fwd(const void *x, const void *r, const void *i, const float *decay,
+                         const float *h0, const uint8_t *reset, float c, void *y, float *h_final,
+                         float *states, int64_t batch, int64_t L, int64_t d_inner, ssm_dtype io,
+                         void *workspace, size_t workspace_bytes, void *hip_stream);
+ssm_status ssm_gated_bwd(const void *x, const void *r, const void *i, const float *decay,
+                         const float *states, const uint8_t *reset, float c, const void *dy,
+                         const float *dh_final, void *dx, void *dr, void *di, float *ddecay,
+                         float *dh0, int64_t batch, int64_t L, int64_t d_inner, ssm_dtype io,
+                         void *workspace, size_t workspace_bytes, void *hip_stream);
+/* One token for every (layer, sequence): h [n_layers, n_seq, d_inner] float32 in place;
+ * x_t, r_t, i_t, y_t [n_layers, n_seq, d_inner] of io; decay [n_layers, d_inner]. n_layers
+ * and n_seq are at most 65535 each. */
+ssm_status ssm_gated_step(float *h, const void *x_t, const void *r_t, const void *i_t,
+                          const float *decay, float c, void *y_t, int64_t n_layers,
+                          int64_t n_seq, int64_t d_inner, ssm_dtype io, void *hip_stream);
+
+/* ------------------------------------------------------------------ vocabulary cross entropy
+ * The loss of a linear head, without a [tokens, vocab] array of logits:
+ *     logit_t[v] = sum_k hidden[t][k] weight[v][k],    lse_t = log sum_v exp(logit_t[v]),
+ *     loss_t = lse_t - logit_t[targets[t]], and 0 where targets[t] == ignore_index.
+ *   hidden : [tokens, dim] of io     weight : [vocab, dim] of io
+ *   targets: [tokens] int64. A target outside 0..vocab-1 that is not ignore_index is an
+ *            error in the data: its loss and its gradients are NaN (nothing is read out
+ *            of range).
+ *   loss, lse : [tokens] float32
+ *   mean   : [2] float32: the mean loss over the tokens that are not ignored, and 1 over
+ *            their number (both 0 where every token is ignored)
+ * Products are accumulated in float32 from the operands' own bits (a float32 operand is
+ * multiplied as a sum of three bfloat16 parts, which hold its 24 bits); the maximum, the
+ * sum and the loss are float32.
+ * ssm_xent_bwd gives the gradients of sum(dloss loss) + dmean * mean[0]:
+ *     dlogit_t[v] = w_t (exp(logit_t[v] - lse_t) - [v == targets[t]]),
+ *     w_t = dloss[t] + dmean / count, 0 where ignored,
+ *     dhidden = dlogit weight,    dweight = dlogit^T hidden    (both of io).
+ *   dloss  : [tokens] float32, NULL = 0;  dmean: one float32 on the device, NULL = 0
+ *   dhidden, dweight: either may be NULL (not wanted)
+ * The logits are computed again, a piece of the vocabulary at a time; with bfloat16
+ * operands a piece's dlogits are rounded to bfloat16 as the operand of the two products.
+ * The workspace (ssm_xent_fwd_workspace / ssm_xent_bwd_workspace bytes, 256-byte aligned)
+ * holds one piece at a time. Sums run in a fixed order. Outputs must not overlap inputs or
+ * each other. Alignment: targets 8 bytes, float32 arrays 4 bytes, the others one element.
+ * tokens, dim and vocab are at most 2^30; tokens == 0 gives mean = 0 and dweight = 0. */
+size_t ssm_xent_fwd_workspace(int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io);
+size_t ssm_xent_bwd_workspace(int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io);
+ssm_status ssm_xent_fwd(const void *hidden, const void *weight, const int64_t *targets,
+                        int64_t ignore_index, float *loss, float *lse, float *mean,
+                        int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io,
+                        void *workspace, size_t workspace_bytes, void *hip_stream);
+ssm_status ssm_xent_bwd(const void *hidden, const void *weight, const int64_t *targets,
+                        int64_t ignore_index, const float *lse, const float *mean,
+                        const float *dloss, const float *dmean, void *dhidden, void *dweight,
+                        int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io,
+                        void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/* ------------------------------------------------------------------ AdamW over many tensors
+ * One step of Adam with decoupled weight decay over n_tensors parameters:
+ *     g = grad * grad_scale
+ *     m = beta1 m + (1 - beta1) g,    v = beta2 v + ((1 - beta2) g) g
+ *     param = param (1 - lr weight_decay)
+ *             - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *   params, grads : HOST arrays of n_tensors device pointers; sizes: their element counts
+ *                   (host; 0 is allowed, its pointers are ignored). A NULL gradient leaves
+ *                   its parameter and its moments as they are.
+ *   param_io, grad_io : HOST arrays of n_tensors ssm_dtype values
+ *   exp_avg, exp_avg_sq : the moments of all tensors, one array each. Tensor k starts at the
+ *                   sum over j < k of sizes[j] rounded up to SSM_ADAMW_BLOCK, and
+ *                   ssm_adamw_state_size gives the total. What lies between two tensors
+ *                   belongs to the arrays; it is neither read nor written, except that an
+ *                   8-bit code there is set to 0.
+ *   avg_scale, avg_sq_scale : both NULL: the moments are float32. Both given ([total /
+ *                   SSM_ADAMW_BLOCK] float32): they are codes of 8 bits, each block of
+ *                   SSM_ADAMW_BLOCK with a scale s:
+ *                       exp_avg    int8  q: m = s u|u|, u = q (1/127)
+ *                       exp_avg_sq uint8 q: v = s (u u)(u u), u = q (1/255)
+ *                   with s the block's largest |m| or v (0 if that is below 1e-35), and
+ *                       q_m = sign(m) rint(127 sqrt(|m| (1/s))),
+ *                       q_v = rint(255 sqrt(sqrt(v (1/s)))), at least 1 where v (1/s) > 0.
+ *                   A NaN or an infinity in a block's moment makes its scale, and so the
+ *                   whole block's values, NaN or infinite.
+ *   grad_scale    : one float32 on the device (a clip coefficient), NULL = 1
+ *   step          : 1 for the first step
+ * Every operation above is one float32 operation rounded to nearest, in the order written
+ * (multiplications and additions are not fused; (1/127), (1/255), 1 - beta and the
+ * bias corrections are computed in double and rounded to float32), so the codes are
+ * reproducible bit for bit. A bfloat16 parameter is updated in float32 and rounded once.
+ * The step takes one launch for every SSM_ADAMW_TENSORS tensors, needs no workspace and
+ * copies the tables by value, so the host arrays may be reused at once.
+ * Alignment: params and grads one element; exp_avg, exp_avg_sq 16 bytes; scales 4 bytes.
+ * params, grads and the state must not overlap. */
+#define SSM_ADAMW_BLOCK 256
+#define SSM_ADAMW_TENSORS 96
+int64_t ssm_adamw_state_size(int32_t n_tensors, const int64_t *sizes);
+ssm_status ssm_adamw_step(int32_t n_tensors, void *const *params, const void *const *grads,
+                          const int64_t *sizes, const int32_t *param_io, const int32_t *grad_io,
+                          void *exp_avg, void *exp_avg_sq, float *avg_scale, float *avg_sq_scale,
+                          const float *grad_scale, double lr, double beta1, double beta2,
+                          double eps, double weight_decay, int64_t step, void *hip_stream);
+/* The values that 8-bit moments stand for: n codes (a multiple of SSM_ADAMW_BLOCK) of each
+ * to float32. */
+ssm_status ssm_adamw_values(const int8_t *exp_avg, const uint8_t *exp_avg_sq,
+                            const float *avg_scale, const float *avg_sq_scale, float *avg_out,
+                            float *avg_sq_out, int64_t n, void *hip_stream);
+
 /* ------------------------------------------------------------------ misc */
 const char *ssm_status_str(ssm_status s);   /* static string, never NULL */
 const char *ssm_last_error(void);           /* this thread's last detail, "" if none */

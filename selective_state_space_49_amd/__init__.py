@@ -32,6 +32,12 @@ __all__ = [
     "ssm_scan_fwd_save", "ssm_scan_fwd_save_workspace", "ssm_scan_fwd_save_states_bytes",
     "ssm_scan_bwd_saved", "ssm_scan_bwd_saved_workspace", "STATE_EVERY",
     "ssm_scan_fwd_fused_save", "ssm_scan_bwd_fused_saved", "ssm_scan_bwd_fused_saved_workspace",
+    "ssm_gated_fwd", "ssm_gated_fwd_save", "ssm_gated_bwd", "ssm_gated_step",
+    "ssm_gated_fwd_workspace", "ssm_gated_bwd_workspace", "ssm_gated_states_bytes",
+    "gated_scan", "GATED_STATE_EVERY",
+    "ssm_xent_fwd", "ssm_xent_bwd", "ssm_xent_fwd_workspace", "ssm_xent_bwd_workspace",
+    "linear_cross_entropy",
+    "ssm_adamw_step", "ssm_adamw_values", "ssm_adamw_state_size", "ADAMW_BLOCK", "AdamW",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -55,6 +61,10 @@ EXPORTED_SYMBOLS = [
     "ssm_scan_fwd_save", "ssm_scan_fwd_save_workspace", "ssm_scan_fwd_save_states_bytes",
     "ssm_scan_bwd_saved", "ssm_scan_bwd_saved_workspace",
     "ssm_scan_fwd_fused_save", "ssm_scan_bwd_fused_saved", "ssm_scan_bwd_fused_saved_workspace",
+    "ssm_gated_fwd", "ssm_gated_bwd", "ssm_gated_step", "ssm_gated_fwd_workspace",
+    "ssm_gated_bwd_workspace", "ssm_gated_states_bytes",
+    "ssm_xent_fwd", "ssm_xent_bwd", "ssm_xent_fwd_workspace", "ssm_xent_bwd_workspace",
+    "ssm_adamw_step", "ssm_adamw_values", "ssm_adamw_state_size",
 ]
 # Steps between the states ssm_scan_fwd_save stores for ssm_scan_bwd_saved.
 STATE_EVERY = 8
@@ -135,6 +145,18 @@ def load_library():
     step_fused = [vp] * 11 + [i32, vp, vp, i64, i64, i64, i32, ci, vp]
     for name in ("ssm_step_fused", "ssm_step_fused_replay"):
         sig[name] = (step_fused, ci)
+    sig["ssm_gated_fwd_workspace"] = sig["ssm_gated_bwd_workspace"] = ([i64, i64, i64], sz)
+    sig["ssm_gated_states_bytes"] = ([i64, i64, i64], sz)
+    f32, f64 = ctypes.c_float, ctypes.c_double
+    sig["ssm_gated_fwd"] = ([vp] * 6 + [f32] + [vp] * 3 + [i64, i64, i64, ci, vp, sz, vp], ci)
+    sig["ssm_gated_bwd"] = ([vp] * 6 + [f32] + [vp] * 7 + [i64, i64, i64, ci, vp, sz, vp], ci)
+    sig["ssm_gated_step"] = ([vp] * 5 + [f32, vp, i64, i64, i64, ci, vp], ci)
+    sig["ssm_xent_fwd_workspace"] = sig["ssm_xent_bwd_workspace"] = ([i64, i64, i64, ci], sz)
+    sig["ssm_xent_fwd"] = ([vp] * 3 + [i64] + [vp] * 3 + [i64, i64, i64, ci, vp, sz, vp], ci)
+    sig["ssm_xent_bwd"] = ([vp] * 3 + [i64] + [vp] * 6 + [i64, i64, i64, ci, vp, sz, vp], ci)
+    sig["ssm_adamw_state_size"] = ([i32, vp], i64)
+    sig["ssm_adamw_step"] = ([i32] + [vp] * 10 + [f64] * 5 + [i64, vp], ci)
+    sig["ssm_adamw_values"] = ([vp] * 6 + [i64, vp], ci)
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
@@ -932,3 +954,10 @@ def ssm_step_mimo(h, x_t, dt_t, A, B_t, C_t, D, z_t=None, *, y_t=None):
                            _ptr(z_t), _ptr(y_t), Ln, S, Dn, N, R, io, _stream(x_t))
     _check(st)
     return y_t
+
+
+from .training import (  # noqa: E402  (the training operators use the helpers above)
+    ADAMW_BLOCK, GATED_STATE_EVERY, AdamW, gated_scan, linear_cross_entropy, ssm_adamw_state_size,
+    ssm_adamw_step, ssm_adamw_values, ssm_gated_bwd, ssm_gated_bwd_workspace, ssm_gated_fwd,
+    ssm_gated_fwd_save, ssm_gated_fwd_workspace, ssm_gated_states_bytes, ssm_gated_step,
+    ssm_xent_bwd, ssm_xent_bwd_workspace, ssm_xent_fwd, ssm_xent_fwd_workspace)

@@ -14,8 +14,9 @@
 
 #include "ssm_internal.h"
 #include "ssm_scan.h"
+#include "ssm_status.h"
 
-namespace {
+namespace ssm {
 
 thread_local char g_err[512] = "";
 
@@ -32,7 +33,16 @@ ssm_status ok() {
     return SSM_OK;
 }
 
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+}  // namespace ssm
+
+namespace {
+
+using ssm::aligned;
+using ssm::fail;
+using ssm::g_err;
+using ssm::launch_status;
+using ssm::ok;
+using ssm::overlaps;
 
 bool valid_state(int32_t n) { return n == 1 || n == 2 || n == 4 || n == 8 || n == 16; }
 
@@ -158,11 +168,6 @@ ssm_status make_plan(int64_t batch, int64_t L, int64_t d_inner, int32_t d_state,
     return ok();
 }
 
-ssm_status launch_status(hipError_t e, const char *what) {
-    if (e != hipSuccess) return fail(SSM_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-    return ok();
-}
-
 // The MambaBlock input stage of the fused entry points.
 struct InputStage {
     const float *conv_w, *conv_b, *dt_bias;
@@ -178,12 +183,6 @@ struct InputStage {
 struct Trap {
     const void *x_prev, *B_prev, *lam;
 };
-
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t pa = (uintptr_t)a, pb = (uintptr_t)b;
-    return pa < pb + nb && pb < pa + na;
-}
 
 ssm_status check_input_stage(const InputStage &in, size_t eb) {
     if (in.conv_k < 0 || in.conv_k > 4) return fail(SSM_ERR_UNSUPPORTED, "conv_k %d not in 0..4", in.conv_k);

@@ -1,0 +1,348 @@
+"""Binding of the training operators beside the scan: the gated linear recurrence, the cross
+entropy of a linear head over a vocabulary, and the AdamW step over many tensors.
+
+Like the rest of the binding, it marshals arguments only: shapes, dtypes and devices are
+checked, outputs and workspaces are allocated with torch where the caller gives none, and
+the C entry points of ``include/ssm_scan.h`` run on torch's current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import SSM_BF16, SSM_F32, _check, _dev, _io, _ptr, _stream, load_library
+
+# SSM_GATED_STATE_EVERY and SSM_ADAMW_BLOCK of ssm_scan.h.
+GATED_STATE_EVERY = 64
+ADAMW_BLOCK = 256
+
+_f32 = torch.float32
+
+
+def _workspace(workspace, need: int, device):
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+def ssm_gated_fwd_workspace(batch, L, d_inner) -> int:
+    return int(load_library().ssm_gated_fwd_workspace(batch, L, d_inner))
+
+
+def ssm_gated_bwd_workspace(batch, L, d_inner) -> int:
+    return int(load_library().ssm_gated_bwd_workspace(batch, L, d_inner))
+
+
+def ssm_gated_states_bytes(batch, L, d_inner) -> int:
+    return int(load_library().ssm_gated_states_bytes(batch, L, d_inner))
+
+
+def _states_rows(L: int) -> int:
+    return -(-L // GATED_STATE_EVERY)
+
+
+def _reset(reset: Optional[torch.Tensor], shape):
+    if reset is not None and reset.dtype not in (torch.bool, torch.uint8):
+        raise TypeError(f"reset: expected bool or uint8, got {reset.dtype}")
+    return _dev(reset, "reset", shape)
+
+
+def ssm_gated_fwd(x, r, i, decay, h0=None, reset=None, *, c=8.0, y=None, h_final=None, states=None,
+                  workspace=None, want_h_final=True):
+    """The gated recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t with
+    a_t = exp(-c softplus(decay) sigmoid(r_t)): y [b, L, D] and h_final [b, D] float32.
+    reset [b, L] (bool): steps that start a document. states: see ssm_gated_fwd_save."""
+    lib = load_library()
+    b, L, D = x.shape
+    _dev(x, "x"); _dev(r, "r", (b, L, D)); _dev(i, "i", (b, L, D))
+    _dev(decay, "decay", (D,), _f32); _dev(h0, "h0", (b, D), _f32); _reset(reset, (b, L))
+    io = _io(x, r, i)
+    if y is None:
+        y = torch.empty_like(x)
+    _dev(y, "y", (b, L, D), x.dtype)
+    if h_final is None and want_h_final:
+        h_final = torch.empty((b, D), dtype=_f32, device=x.device)
+    _dev(h_final, "h_final", (b, D), _f32)
+    _dev(states, "states", (b, _states_rows(L), D), _f32)
+    workspace, ws_bytes = _workspace(workspace, lib.ssm_gated_fwd_workspace(b, L, D), x.device)
+    _check(lib.ssm_gated_fwd(_ptr(x), _ptr(r), _ptr(i), _ptr(decay), _ptr(h0), _ptr(reset), c, _ptr(y),
+                             _ptr(h_final), _ptr(states), b, L, D, io, _ptr(workspace), ws_bytes,
+                             _stream(x)))
+    return y, h_final
+
+
+def ssm_gated_fwd_save(x, r, i, decay, h0=None, reset=None, *, c=8.0, y=None, h_final=None, states=None,
+                       workspace=None):
+    """The training forward: ssm_gated_fwd, and the state entering every 64th step
+    [b, ceil(L / 64), D] float32 for ssm_gated_bwd."""
+    b, L, D = x.shape
+    if states is None:
+        states = torch.empty((b, _states_rows(L), D), dtype=_f32, device=x.device)
+    y, h_final = ssm_gated_fwd(x, r, i, decay, h0, reset, c=c, y=y, h_final=h_final, states=states,
+                               workspace=workspace)
+    return y, h_final, states
+
+
+def ssm_gated_bwd(x, r, i, decay, states, reset=None, *, dy, dh_final=None, c=8.0, want_dh0=True,
+                  workspace=None):
+    """Gradients of sum(dy y) + sum(dh_final h_final): a dict of dx, dr, di (x's dtype),
+    ddecay [D] and dh0 [b, D] (float32; None unless want_dh0)."""
+    lib = load_library()
+    b, L, D = x.shape
+    _dev(x, "x"); _dev(r, "r", (b, L, D)); _dev(i, "i", (b, L, D)); _dev(dy, "dy", (b, L, D))
+    _dev(decay, "decay", (D,), _f32); _dev(states, "states", (b, _states_rows(L), D), _f32)
+    _reset(reset, (b, L)); _dev(dh_final, "dh_final", (b, D), _f32)
+    io = _io(x, r, i, dy)
+    dx, dr, di = (torch.empty_like(x) for _ in range(3))
+    ddecay = torch.empty_like(decay)
+    dh0 = torch.empty((b, D), dtype=_f32, device=x.device) if want_dh0 else None
+    workspace, ws_bytes = _workspace(workspace, lib.ssm_gated_bwd_workspace(b, L, D), x.device)
+    _check(lib.ssm_gated_bwd(_ptr(x), _ptr(r), _ptr(i), _ptr(decay), _ptr(states), _ptr(reset), c, _ptr(dy),
+                             _ptr(dh_final), _ptr(dx), _ptr(dr), _ptr(di), _ptr(ddecay), _ptr(dh0), b, L, D,
+                             io, _ptr(workspace), ws_bytes, _stream(x)))
+    return {"dx": dx, "dr": dr, "di": di, "ddecay": ddecay, "dh0": dh0}
+
+
+def ssm_gated_step(h, x_t, r_t, i_t, decay, *, c=8.0, y_t=None):
+    """One token for every (layer, sequence): h [Ln, S, D] float32 in place; x_t, r_t, i_t
+    [Ln, S, D]; decay [Ln, D]. Returns y_t."""
+    lib = load_library()
+    Ln, S, D = x_t.shape
+    _dev(h, "h", (Ln, S, D), _f32); _dev(decay, "decay", (Ln, D), _f32)
+    _dev(x_t, "x_t"); _dev(r_t, "r_t", (Ln, S, D)); _dev(i_t, "i_t", (Ln, S, D))
+    io = _io(x_t, r_t, i_t)
+    if y_t is None:
+        y_t = torch.empty_like(x_t)
+    _dev(y_t, "y_t", (Ln, S, D), x_t.dtype)
+    _check(lib.ssm_gated_step(_ptr(h), _ptr(x_t), _ptr(r_t), _ptr(i_t), _ptr(decay), c, _ptr(y_t), Ln, S, D,
+                              io, _stream(x_t)))
+    return y_t
+
+
+class _GatedScan(torch.autograd.Function):
+    """ssm_gated_fwd_save forwards, ssm_gated_bwd backwards."""
+
+    @staticmethod
+    def forward(ctx, x, r, i, decay, h0, reset, c):
+        y, h_final, states = ssm_gated_fwd_save(x, r, i, decay, h0, reset, c=c)
+        ctx.save_for_backward(x, r, i, decay, states, reset)
+        ctx.c, ctx.has_h0 = c, h0 is not None
+        return y, h_final
+
+    @staticmethod
+    def backward(ctx, dy, dh_final):
+        x, r, i, decay, states, reset = ctx.saved_tensors
+        dy = torch.zeros_like(x) if dy is None else dy.to(x.dtype).contiguous()
+        g = ssm_gated_bwd(x, r, i, decay, states, reset, dy=dy, c=ctx.c,
+                          dh_final=None if dh_final is None else dh_final.float().contiguous(),
+                          want_dh0=ctx.has_h0 and ctx.needs_input_grad[4])
+        grads = (g["dx"], g["dr"], g["di"], g["ddecay"], g["dh0"], None, None)
+        return tuple(gr if need else None for gr, need in zip(grads, ctx.needs_input_grad))
+
+
+def gated_scan(x, r, i, decay, h0=None, reset=None, *, c=8.0):
+    """The gated recurrence as a differentiable function: (y, h_final), with gradients for x,
+    r, i, decay and h0."""
+    return _GatedScan.apply(x, r, i, decay, h0, reset, c)
+
+
+# ------------------------------------------------------------------ vocabulary cross entropy
+def ssm_xent_fwd_workspace(tokens, dim, vocab, io=SSM_BF16) -> int:
+    return int(load_library().ssm_xent_fwd_workspace(tokens, dim, vocab, io))
+
+
+def ssm_xent_bwd_workspace(tokens, dim, vocab, io=SSM_BF16) -> int:
+    return int(load_library().ssm_xent_bwd_workspace(tokens, dim, vocab, io))
+
+
+def _head(hidden, weight, targets):
+    T, K = hidden.shape
+    V = weight.shape[0]
+    _dev(hidden, "hidden"); _dev(weight, "weight", (V, K)); _dev(targets, "targets", (T,), torch.int64)
+    return T, K, V, _io(hidden, weight)
+
+
+def ssm_xent_fwd(hidden, weight, targets, *, ignore_index=-100, loss=None, lse=None, mean=None,
+                 workspace=None):
+    """Cross entropy of the logits hidden [T, K] weight [V, K]^T against targets [T], without
+    the logits in memory: loss [T], lse [T] and mean [2] (the mean over the tokens that are
+    not ignored, and 1 over their number), all float32."""
+    lib = load_library()
+    T, K, V, io = _head(hidden, weight, targets)
+    dev = hidden.device
+    loss = torch.empty(T, dtype=_f32, device=dev) if loss is None else _dev(loss, "loss", (T,), _f32)
+    lse = torch.empty(T, dtype=_f32, device=dev) if lse is None else _dev(lse, "lse", (T,), _f32)
+    mean = torch.empty(2, dtype=_f32, device=dev) if mean is None else _dev(mean, "mean", (2,), _f32)
+    workspace, ws_bytes = _workspace(workspace, lib.ssm_xent_fwd_workspace(T, K, V, io), dev)
+    _check(lib.ssm_xent_fwd(_ptr(hidden), _ptr(weight), _ptr(targets), ignore_index, _ptr(loss), _ptr(lse),
+                            _ptr(mean), T, K, V, io, _ptr(workspace), ws_bytes, _stream(hidden)))
+    return loss, lse, mean
+
+
+def ssm_xent_bwd(hidden, weight, targets, lse, mean, *, dloss=None, dmean=None, ignore_index=-100,
+                 want_dhidden=True, want_dweight=True, workspace=None):
+    """Gradients of sum(dloss loss) + dmean mean[0] (dloss [T] float32, dmean one float32 on
+    the GPU; None = 0): dhidden [T, K] and dweight [V, K] (None where not wanted)."""
+    lib = load_library()
+    T, K, V, io = _head(hidden, weight, targets)
+    _dev(lse, "lse", (T,), _f32); _dev(mean, "mean", (2,), _f32); _dev(dloss, "dloss", (T,), _f32)
+    if dmean is not None and (_dev(dmean, "dmean", None, _f32)).numel() != 1:
+        raise ValueError("dmean must hold one value")
+    dhidden = torch.empty_like(hidden) if want_dhidden else None
+    dweight = torch.empty_like(weight) if want_dweight else None
+    workspace, ws_bytes = _workspace(workspace, lib.ssm_xent_bwd_workspace(T, K, V, io), hidden.device)
+    _check(lib.ssm_xent_bwd(_ptr(hidden), _ptr(weight), _ptr(targets), ignore_index, _ptr(lse), _ptr(mean),
+                            _ptr(dloss), _ptr(dmean), _ptr(dhidden), _ptr(dweight), T, K, V, io,
+                            _ptr(workspace), ws_bytes, _stream(hidden)))
+    return dhidden, dweight
+
+
+class _LinearCrossEntropy(torch.autograd.Function):
+    """ssm_xent_fwd forwards, ssm_xent_bwd backwards."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, targets, ignore_index):
+        loss, lse, mean = ssm_xent_fwd(hidden, weight, targets, ignore_index=ignore_index)
+        ctx.save_for_backward(hidden, weight, targets, lse, mean)
+        ctx.ignore_index = ignore_index
+        return mean[0], loss
+
+    @staticmethod
+    def backward(ctx, dmean, dloss):
+        hidden, weight, targets, lse, mean = ctx.saved_tensors
+        one = lambda t: None if t is None else t.float().contiguous()  # noqa: E731
+        dhidden, dweight = ssm_xent_bwd(hidden, weight, targets, lse, mean, dloss=one(dloss), dmean=one(dmean),
+                                        ignore_index=ctx.ignore_index, want_dhidden=ctx.needs_input_grad[0],
+                                        want_dweight=ctx.needs_input_grad[1])
+        return dhidden, dweight, None, None
+
+
+def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, reduction="mean"):
+    """Softmax cross entropy of a linear head, differentiable in hidden [..., K] and weight
+    [V, K]: the mean over the tokens that are not ignored (0 where all are), or with
+    reduction="none" every token's loss in targets' shape."""
+    if reduction not in ("mean", "none"):
+        raise ValueError(f"reduction must be 'mean' or 'none', got {reduction!r}")
+    mean, loss = _LinearCrossEntropy.apply(hidden.reshape(-1, hidden.shape[-1]), weight, targets.reshape(-1),
+                                           ignore_index)
+    return mean if reduction == "mean" else loss.view(targets.shape)
+
+
+# ------------------------------------------------------------------ AdamW
+def ssm_adamw_state_size(sizes) -> int:
+    """Elements of the moments' arrays for tensors of these sizes."""
+    sizes = list(sizes)
+    return int(load_library().ssm_adamw_state_size(len(sizes), (ctypes.c_int64 * len(sizes))(*sizes)))
+
+
+def _table(params, grads):
+    """The host arrays of ssm_adamw_step. A gradient may be None."""
+    n = len(params)
+    if len(grads) != n:
+        raise ValueError(f"{n} parameters and {len(grads)} gradients")
+    kinds = {_f32: SSM_F32, torch.bfloat16: SSM_BF16}
+    p_at, g_at, size, p_io, g_io = [], [], [], [], []
+    dev = params[0].device if n else None
+    for k, (p, g) in enumerate(zip(params, grads)):
+        if p.dtype not in kinds or p.device != dev or not p.is_cuda or not p.is_contiguous():
+            raise ValueError(f"parameter {k} must be a contiguous float32 or bfloat16 tensor on one GPU")
+        p_at.append(p.data_ptr())
+        size.append(p.numel())
+        p_io.append(kinds[p.dtype])
+        if g is None:
+            g_at.append(None)
+            g_io.append(SSM_F32)
+            continue
+        if g.dtype not in kinds or g.device != dev or g.shape != p.shape or not g.is_contiguous():
+            raise ValueError(f"gradient {k} must be a contiguous float32 or bfloat16 tensor of its "
+                             "parameter's shape and device")
+        g_at.append(g.data_ptr())
+        g_io.append(kinds[g.dtype])
+    arr = lambda kind, v: (kind * n)(*v)  # noqa: E731
+    return (n, arr(ctypes.c_void_p, p_at), arr(ctypes.c_void_p, g_at), arr(ctypes.c_int64, size),
+            arr(ctypes.c_int32, p_io), arr(ctypes.c_int32, g_io)), sum(-(-s // ADAMW_BLOCK) for s in size)
+
+
+def ssm_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_scale=None, *, lr, beta1, beta2,
+                   eps, weight_decay, step, grad_scale=None):
+    """One AdamW step over a list of tensors, in place. exp_avg, exp_avg_sq: the moments of
+    all of them in one array each, a tensor starting at a multiple of 256 elements
+    (ssm_adamw_state_size): float32, or, with avg_scale and avg_sq_scale (float32, one for
+    256 elements), int8 and uint8 codes. grad_scale: one float32 on the GPU."""
+    lib = load_library()
+    if not params:
+        return
+    table, blocks = _table(params, grads)
+    codes = avg_scale is not None
+    total = (blocks * ADAMW_BLOCK,)
+    _dev(exp_avg, "exp_avg", total, torch.int8 if codes else _f32)
+    _dev(exp_avg_sq, "exp_avg_sq", total, torch.uint8 if codes else _f32)
+    _dev(avg_scale, "avg_scale", (blocks,), _f32); _dev(avg_sq_scale, "avg_sq_scale", (blocks,), _f32)
+    if grad_scale is not None and _dev(grad_scale, "grad_scale", None, _f32).numel() != 1:
+        raise ValueError("grad_scale must hold one value")
+    _check(lib.ssm_adamw_step(*table, _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(avg_scale), _ptr(avg_sq_scale),
+                              _ptr(grad_scale), lr, beta1, beta2, eps, weight_decay, step, _stream(params[0])))
+
+
+def ssm_adamw_values(exp_avg, exp_avg_sq, avg_scale, avg_sq_scale):
+    """The float32 values that 8-bit moments stand for."""
+    lib = load_library()
+    n = exp_avg.numel()
+    _dev(exp_avg, "exp_avg", (n,), torch.int8); _dev(exp_avg_sq, "exp_avg_sq", (n,), torch.uint8)
+    _dev(avg_scale, "avg_scale", (n // ADAMW_BLOCK,), _f32)
+    _dev(avg_sq_scale, "avg_sq_scale", (n // ADAMW_BLOCK,), _f32)
+    m, v = (torch.empty(n, dtype=_f32, device=exp_avg.device) for _ in range(2))
+    _check(lib.ssm_adamw_values(_ptr(exp_avg), _ptr(exp_avg_sq), _ptr(avg_scale), _ptr(avg_sq_scale), _ptr(m),
+                                _ptr(v), n, _stream(exp_avg)))
+    return m, v
+
+
+class AdamW:
+    """AdamW over a list of parameters (float32 and bfloat16, on one GPU), one library call a
+    step. bits: 32, or 8 for moments held in 8-bit codes with a scale for 256 of them."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32):
+        if bits not in (8, 32):
+            raise ValueError(f"bits must be 8 or 32, got {bits}")
+        self.params = list(params)
+        self.lr, self.betas, self.eps, self.weight_decay, self.bits = lr, betas, eps, weight_decay, bits
+        self.steps = 0
+        n = ssm_adamw_state_size(p.numel() for p in self.params)
+        dev = self.params[0].device if self.params else None
+        zeros = lambda k, dtype: torch.zeros(k, dtype=dtype, device=dev)  # noqa: E731
+        self.exp_avg = zeros(n, torch.int8 if bits == 8 else _f32)
+        self.exp_avg_sq = zeros(n, torch.uint8 if bits == 8 else _f32)
+        self.avg_scale = zeros(n // ADAMW_BLOCK, _f32) if bits == 8 else None
+        self.avg_sq_scale = zeros(n // ADAMW_BLOCK, _f32) if bits == 8 else None
+
+    @torch.no_grad()
+    def step(self, grad_scale=None):
+        """Updates every parameter that has a gradient; grad_scale multiplies the gradients."""
+        self.steps += 1
+        ssm_adamw_step([p.detach() for p in self.params], [p.grad for p in self.params], self.exp_avg,
+                       self.exp_avg_sq, self.avg_scale, self.avg_sq_scale, lr=self.lr, beta1=self.betas[0],
+                       beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay, step=self.steps,
+                       grad_scale=grad_scale)
+
+    def zero_grad(self):
+        for p in self.params:
+            p.grad = None
+
+    def state_dict(self):
+        return {"steps": self.steps, "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq,
+                "avg_scale": self.avg_scale, "avg_sq_scale": self.avg_sq_scale}
+
+    def load_state_dict(self, state):
+        names = ("exp_avg", "exp_avg_sq", "avg_scale", "avg_sq_scale")
+        for name in names:  # refuse a state of another layout before anything is copied
+            mine, theirs = getattr(self, name), state[name]
+            if (mine is None) != (theirs is None) or (
+                    mine is not None and (mine.shape != theirs.shape or mine.dtype != theirs.dtype)):
+                raise ValueError(f"{name} does not fit this optimizer's parameters and bits")
+        for name in names:
+            if getattr(self, name) is not None:
+                getattr(self, name).copy_(state[name])
+        self.steps = int(state["steps"])

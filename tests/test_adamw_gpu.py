@@ -1,0 +1,209 @@
+"""The AdamW step over many tensors: bit for bit against float32 operations in the
+documented order (numpy's are IEEE's), and within their rounding of the 64-bit form (a
+dozen operations: 2e-6 of a moment, and of the parameter plus the step)."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_49_amd as ssm
+from tests import train_ref
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+BLOCK = 256
+OPT = dict(lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8, weight_decay=0.1, step=3)
+SIZES = [1, 2, 255, 256, 257, 0, 2047, 2048, 2049, 5000, 64 * 64, 100001]
+
+
+def bf16(a):
+    return torch.from_numpy(a).to(torch.bfloat16)
+
+
+class Problem:
+    """Parameters of mixed types, their gradients, and moments, on the host as float32."""
+
+    def __init__(self, sizes, seed, bits, kinds=None, shift=0):
+        rng = np.random.RandomState(seed)
+        self.bits, self.at, at = bits, [], 0
+        self.p, self.g, self.kinds = [], [], []
+        for k, n in enumerate(sizes):
+            self.at.append((at, n))
+            at += -(-n // BLOCK) * BLOCK
+            kind = (kinds or [(0, 0), (1, 1), (0, 1), (1, 0)])[k % (len(kinds) if kinds else 4)]
+            one = lambda t, b: bf16(t).float().numpy() if b else t  # noqa: E731
+            self.p.append(one(rng.randn(n).astype(np.float32), kind[0]))
+            self.g.append(one((rng.randn(n) * 10.0 ** rng.uniform(-4, 1, n)).astype(np.float32), kind[1]))
+            self.kinds.append(kind)
+        self.total = at
+        m, v = np.zeros(at, np.float32), np.zeros(at, np.float32)
+        for a, n in self.at:
+            m[a:a + n] = rng.randn(n)
+            v[a:a + n] = rng.rand(n) ** 4
+        if bits == 8:
+            self.mq, self.vq, self.ms, self.vs = train_ref.adam_codes(m, v)
+            m, v = train_ref.adam_values(self.mq, self.vq, self.ms, self.vs)
+        self.m, self.v = m, v
+        kind = lambda a, b: (bf16(a) if b else torch.from_numpy(a.copy())).cuda()  # noqa: E731
+
+        def place(t):
+            flat = torch.empty(t.numel() + shift, dtype=t.dtype, device="cuda")
+            flat[shift:] = t
+            return flat[shift:]
+        self.params = [place(kind(p, k[0])) for p, k in zip(self.p, self.kinds)]
+        self.grads = [place(kind(g, k[1])) for g, k in zip(self.g, self.kinds)]
+        cuda = lambda a: torch.from_numpy(a.copy()).cuda()  # noqa: E731
+        self.state = [cuda(self.m), cuda(self.v)] if bits == 32 else [cuda(t) for t in (self.mq, self.vq, self.ms, self.vs)]
+
+    def step(self, **opt):
+        ssm.ssm_adamw_step(self.params, self.grads, *self.state, **opt)
+        torch.cuda.synchronize()
+
+    def expect(self, fn, **opt):
+        """Parameters, and flat moments with 0 between tensors."""
+        ps, m, v = [], np.zeros(self.total), np.zeros(self.total)
+        for (a, n), p, g in zip(self.at, self.p, self.g):
+            q, mm, vv = fn(p, g, self.m[a:a + n], self.v[a:a + n], **opt)
+            ps.append(q)
+            m[a:a + n], v[a:a + n] = mm, vv
+        return ps, m, v
+
+
+def check_bits(pr, opt):
+    ps, m, v = pr.expect(train_ref.adam32, **opt)
+    m, v = m.astype(np.float32), v.astype(np.float32)
+    for k, (p, q, kind) in enumerate(zip(pr.params, ps, pr.kinds)):
+        q = bf16(q) if kind[0] else torch.from_numpy(q)
+        assert torch.equal(p.cpu(), q), k
+    if pr.bits == 32:
+        assert np.array_equal(pr.state[0].cpu().numpy(), m) and np.array_equal(pr.state[1].cpu().numpy(), v)
+    else:
+        for got, want in zip(pr.state, train_ref.adam_codes(m, v)):
+            assert np.array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_bit_for_bit(bits, shift):
+    say("adamw", bits, shift)
+    pr = Problem(SIZES, seed=bits + shift, bits=bits, shift=shift)
+    pr.step(**OPT)
+    check_bits(pr, OPT)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_against_64_bits(bits):
+    pr = Problem(SIZES, seed=3, bits=bits)
+    ps, m, v = pr.expect(train_ref.adam64, **OPT)
+    pr.step(**OPT)
+    for p, q, old, kind in zip(pr.params, ps, pr.p, pr.kinds):
+        tol = 2e-6 * (np.abs(old) + np.abs(q - old)) + (2.0 ** -8 * np.abs(q) if kind[0] else 0.0)
+        assert np.all(np.abs(p.double().cpu().numpy() - q) <= tol)
+    if bits == 32:
+        for got, want in zip(pr.state, (m, v)):
+            assert np.all(np.abs(got.double().cpu().numpy() - want) <= 2e-6 * (np.abs(want) + np.abs(pr.m)) + 1e-30)
+    else:
+        # half a code of the root's scale: 1/254 of the largest root, 1/510 of the fourth one
+        gm, gv = (t.double().cpu().numpy() for t in ssm.ssm_adamw_values(*pr.state))
+        ms, vs = (np.repeat(np.abs(t.reshape(-1, BLOCK)).max(1), BLOCK) for t in (m, v))
+        root = lambda t, s, e: (np.abs(t) / np.maximum(s, 1e-300)) ** e  # noqa: E731
+        assert np.all(np.abs(root(gm, ms, 0.5) - root(m, ms, 0.5)) <= 1 / 254 + 1e-5)
+        assert np.all(np.abs(root(gv, vs, 0.25) - root(v, vs, 0.25)) <= 1 / 255 + 1e-5)
+        assert np.all(np.sign(gm) * np.sign(m) >= 0) and np.all((gv > 0) == (v > 0))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_more_tensors_than_one_launch_takes(bits):
+    say("adamw many", bits)
+    rng = np.random.RandomState(4)
+    pr = Problem([int(n) for n in rng.randint(0, 700, 250)], seed=5, bits=bits)
+    pr.step(**OPT)
+    check_bits(pr, OPT)
+
+
+def test_one_large_tensor():
+    for bits in (32, 8):
+        say("adamw large", bits)
+        pr = Problem([3_000_003], seed=6, bits=bits, kinds=[(1, 1)])
+        pr.step(**OPT)
+        check_bits(pr, OPT)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_grad_scale_and_no_decay(bits):
+    opt = dict(OPT, weight_decay=0.0, step=1000)
+    pr = Problem(SIZES, seed=7, bits=bits)
+    pr.step(**opt, grad_scale=torch.full((), 0.125, device="cuda"))
+    check_bits(pr, dict(opt, grad_scale=0.125))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_zeros_and_missing_gradients(bits):
+    # fresh moments, gradients of zero, and tensors without a gradient
+    pr = Problem(SIZES, seed=8, bits=bits)
+    for t in pr.state:
+        t.zero_()
+    pr.m[:], pr.v[:] = 0, 0
+    for k in range(0, len(SIZES), 2):
+        pr.g[k][:] = 0
+        pr.grads[k].zero_()
+    before = [t.clone() for t in pr.params], [t.clone() for t in pr.state]
+    skipped = 9
+    pr.grads[skipped] = None
+    pr.step(**dict(OPT, step=1))
+    at, n = pr.at[skipped]
+    assert torch.equal(pr.params[skipped], before[0][skipped])
+    assert torch.equal(pr.state[0][at:at + n], before[1][0][at:at + n])
+    pr.grads[skipped] = torch.from_numpy(pr.g[skipped]).to(pr.params[skipped].dtype).cuda()
+    for k, (p, q) in enumerate(zip(pr.params, pr.expect(train_ref.adam32, **dict(OPT, step=1))[0])):
+        if k != skipped:
+            q = bf16(q) if pr.kinds[k][0] else torch.from_numpy(q)
+            assert torch.equal(p.cpu(), q) and not bool(p.isnan().any())
+
+
+def test_nan_stays_in_its_block():
+    pr = Problem([2000], seed=9, bits=8, kinds=[(0, 0)])
+    want = Problem([2000], seed=9, bits=8, kinds=[(0, 0)])
+    want.step(**OPT)
+    pr.grads[0][700] = float("nan")
+    pr.step(**OPT)
+    m, v = ssm.ssm_adamw_values(*pr.state)
+    m2, v2 = ssm.ssm_adamw_values(*want.state)
+    keep = torch.ones(2048, dtype=torch.bool)
+    keep[512:768] = False
+    assert torch.equal(m.cpu()[keep], m2.cpu()[keep]) and torch.equal(v.cpu()[keep], v2.cpu()[keep])
+    assert bool(m[512:768].isnan().all()) and bool(v[512:768].isnan().all())
+    p, q = pr.params[0].cpu(), want.params[0].cpu()
+    others = torch.arange(2000) != 700
+    assert torch.equal(p[others], q[others]) and bool(p[700].isnan())
+
+
+def test_optimizer():
+    # the class: a quadratic falls, a checkpoint resumes with the same bits
+    for bits in (32, 8):
+        torch.manual_seed(0)
+        goal = [torch.randn(300, 7, device="cuda"), torch.randn(33, device="cuda")]
+        params = [torch.zeros_like(t).requires_grad_() for t in goal]
+        opt = ssm.AdamW(params, lr=0.05, weight_decay=0.0, bits=bits)
+        loss = lambda: sum(((p - t) ** 2).sum() for p, t in zip(params, goal))  # noqa: E731
+
+        def run(n):
+            for _ in range(n):
+                opt.zero_grad()
+                loss().backward()
+                opt.step()
+        first = float(loss())
+        run(100)
+        saved = [p.detach().clone() for p in params], {k: v.clone() if torch.is_tensor(v) else v
+                                                       for k, v in opt.state_dict().items()}
+        run(20)
+        assert float(loss()) < 0.05 * first
+        end = [p.detach().clone() for p in params]
+        with torch.no_grad():
+            for p, t in zip(params, saved[0]):
+                p.copy_(t)
+        opt.load_state_dict(saved[1])
+        run(20)
+        assert all(torch.equal(p, t) for p, t in zip(params, end))
+        with pytest.raises(ValueError):
+            ssm.AdamW(params, bits=40 - bits).load_state_dict(saved[1])

@@ -1,0 +1,210 @@
+"""The cross entropy of a linear head against its 64-bit form.
+
+Tolerances. A logit is a float32 sum of K products: its rounding wanders by about
+2^-24 sqrt(K) |h||w|, and four times that is allowed for the largest of all, plus 2e-6 of
+the logarithm of the sum. Gradients: an output's own rounding (2^-9 of the largest value in
+bfloat16, 2^-24 in float32, twice that allowed), and the rounding of the dlogits that enter
+the products, e = 2^-9 (bfloat16) or the relative error of exp(logit - lse), about
+2^-18 (float32), which over a sum adds up to e |g|_2 max|w|; three times that."""
+import pytest
+import torch
+
+import selective_state_space_49_amd as ssm
+from tests import train_ref
+from tests.gpu_util import bitwise_equal, say
+
+pytestmark = pytest.mark.gpu
+
+
+def make(T, K, V, io, seed, ignored=0.2, lean=3.0):
+    g = torch.Generator().manual_seed(seed)
+    weight = (torch.randn(V, K, generator=g) / K ** 0.5).to(io)
+    target = torch.randint(0, V, (T,), generator=g)
+    hidden = (torch.randn(T, K, generator=g) + lean * weight[target].float()).to(io)
+    target[torch.rand(T, generator=g) < ignored] = -100
+    return hidden, weight, target
+
+
+def check(hidden, weight, target, ref, got, io, w_max):
+    K = hidden.shape[1]
+    hn, wn = float(hidden.double().norm(dim=1).max()), float(weight.double().norm(dim=1).max())
+    tol = 4 * 2.0 ** -24 * K ** 0.5 * hn * wn + 2e-6 * (1 + float(ref["lse"].abs().max()))
+    for k in ("loss", "lse"):
+        assert float((got[k].double().cpu() - ref[k]).abs().max()) <= tol, k
+    assert abs(float(got["mean"][0]) - ref["mean"]) <= tol
+    assert abs(float(got["mean"][1]) - (1 / ref["count"] if ref["count"] else 0.0)) <= 1e-6
+    out, e = (2.0 ** -8, 2.0 ** -9) if io == torch.bfloat16 else (2.0 ** -23, 2.0 ** -18)
+    g = ref["dlogits"]
+    for k, other, axis in (("dhidden", weight, 1), ("dweight", hidden, 0)):
+        bound = out * float(ref[k].abs().max()) + 3 * e * float(g.norm(dim=axis).max()) * float(other.abs().max())
+        err = float((got[k].double().cpu() - ref[k]).abs().max())
+        assert err <= bound + 1e-30, (k, err, bound)
+
+
+def call(hidden, weight, target, dloss=None, dmean=None):
+    h, w, t = hidden.cuda(), weight.cuda(), target.cuda()
+    loss, lse, mean = ssm.ssm_xent_fwd(h, w, t)
+    dh, dw = ssm.ssm_xent_bwd(h, w, t, lse, mean, dloss=dloss, dmean=dmean)
+    torch.cuda.synchronize()
+    return {"loss": loss, "lse": lse, "mean": mean, "dhidden": dh, "dweight": dw}
+
+
+SIZES = [(1, 1, 1), (1, 64, 2), (3, 5, 7), (64, 64, 64), (65, 72, 63), (100, 256, 1000), (257, 130, 300),
+         (128, 128, 257), (130, 64, 5000), (31, 1000, 2049), (513, 96, 515), (1030, 200, 777)]
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,K,V", SIZES)
+def test_against_64_bits(T, K, V, io):
+    say("xent", T, K, V, io)
+    hidden, weight, target = make(T, K, V, io, seed=T + K + V)
+    dmean = torch.tensor(2.0, device="cuda")
+    dloss = torch.randn(T, generator=torch.Generator().manual_seed(1))
+    ref = train_ref.xent(hidden, weight, target, dloss=dloss, dmean=2.0)
+    check(hidden, weight, target, ref, call(hidden, weight, target, dloss.cuda(), dmean), io, 1)
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+def test_large_against_64_bits(io):
+    # several tiles and pieces in every direction
+    say("xent large", io)
+    hidden, weight, target = make(1500, 320, 9000, io, seed=3)
+    ref = train_ref.xent(hidden, weight, target, dmean=1.0)
+    check(hidden, weight, target, ref, call(hidden, weight, target, None, torch.ones((), device="cuda")), io, 1)
+
+
+def test_all_ignored():
+    for T in (1, 70):
+        hidden, weight, target = make(T, 64, 100, torch.bfloat16, seed=4, ignored=2.0)
+        got = call(hidden, weight, target, None, torch.ones((), device="cuda"))
+        assert not bool(got["loss"].any()) and not bool(got["mean"].any())
+        assert not bool(got["dhidden"].any()) and not bool(got["dweight"].any())
+
+
+def test_ignored_rows_keep_their_garbage_to_themselves():
+    # a padded row may hold anything: NaN and infinities there must not reach the gradients
+    for io in (torch.float32, torch.bfloat16):
+        hidden, weight, target = make(200, 96, 500, io, seed=5)
+        target[:3] = torch.tensor([-100, -100, 1])
+        hidden[0], hidden[1] = 0.0, 0.0
+        want = call(hidden, weight, target, None, torch.ones((), device="cuda"))
+        hidden[0], hidden[1] = float("nan"), float("inf")
+        say("xent garbage", io)
+        got = call(hidden, weight, target, None, torch.ones((), device="cuda"))
+        for k in ("loss", "dhidden", "dweight"):
+            assert bitwise_equal(got[k], want[k]), k
+        assert bitwise_equal(got["lse"][2:], want["lse"][2:])
+
+
+def test_target_out_of_range_is_loud():
+    hidden, weight, target = make(10, 32, 40, torch.float32, seed=6, ignored=0.0)
+    target[4], target[7] = 40, -1
+    got = call(hidden, weight, target, None, torch.ones((), device="cuda"))
+    bad = torch.tensor([t in (4, 7) for t in range(10)])
+    assert bool(got["loss"].cpu()[bad].isnan().all()) and not bool(got["loss"].cpu()[~bad].isnan().any())
+    assert bool(got["dhidden"].cpu()[bad].isnan().all()) and not bool(got["dhidden"].cpu()[~bad].isnan().any())
+
+
+def test_wide_logits():
+    # logits of several hundred: the maximum is taken out before the exponential
+    for io in (torch.float32, torch.bfloat16):
+        hidden, weight, target = make(50, 64, 700, io, seed=7)
+        hidden = (hidden * 100).to(io)
+        ref = train_ref.xent(hidden, weight, target, dmean=1.0)
+        got = call(hidden, weight, target, None, torch.ones((), device="cuda"))
+        tol = 4 * 2.0 ** -24 * 8 * float(hidden.double().norm(dim=1).max()) * float(weight.double().norm(dim=1).max())
+        tol += 2e-6 * float(ref["lse"].abs().max())
+        assert float((got["loss"].double().cpu() - ref["loss"]).abs().max()) <= tol
+        assert not bool(got["dweight"].isnan().any())
+
+
+def test_unaligned_rows():
+    # odd widths and element-aligned pointers
+    for io in (torch.float32, torch.bfloat16):
+        hidden, weight, target = make(70, 65, 130, io, seed=8)
+        ref = train_ref.xent(hidden, weight, target, dmean=1.0)
+
+        def shifted(t):
+            flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+            out = flat[1:].view(t.shape)
+            out.copy_(t)
+            return out
+        say("xent shifted", io)
+        h, w, t = shifted(hidden), shifted(weight), target.cuda()
+        loss, lse, mean = ssm.ssm_xent_fwd(h, w, t)
+        dh, dw = ssm.ssm_xent_bwd(h, w, t, lse, mean, dmean=torch.ones((), device="cuda"))
+        check(hidden, weight, target, ref, {"loss": loss, "lse": lse, "mean": mean, "dhidden": dh, "dweight": dw}, io, 1)
+
+
+def test_gradients_against_differences():
+    hidden, weight, target = make(60, 48, 200, torch.float32, seed=9)
+    got = call(hidden, weight, target, None, torch.ones((), device="cuda"))
+    gen = torch.Generator().manual_seed(10)
+    for j, k in enumerate(("dhidden", "dweight")):
+        vals = [hidden.double(), weight.double()]
+        v = torch.randn(vals[j].shape, generator=gen, dtype=torch.float64)
+        up, down = list(vals), list(vals)
+        up[j], down[j] = vals[j] + 1e-5 * v, vals[j] - 1e-5 * v
+        slope = (train_ref.xent(*up, target)["mean"] - train_ref.xent(*down, target)["mean"]) / 2e-5
+        ours = float((got[k].double().cpu() * v).sum())
+        assert abs(slope - ours) <= 1e-4 * float(got[k].double().norm()), (k, slope, ours)
+
+
+def test_autograd_function_and_partial_gradients():
+    hidden, weight, target = (t.cuda() for t in make(90, 64, 300, torch.bfloat16, seed=11))
+    h3 = hidden.view(3, 30, 64).clone().requires_grad_()
+    w = weight.clone().requires_grad_()
+    loss = ssm.linear_cross_entropy(h3, w, target.view(3, 30))
+    (3 * loss).backward()
+    _, lse, mean = ssm.ssm_xent_fwd(hidden, weight, target)
+    dh, dw = ssm.ssm_xent_bwd(hidden, weight, target, lse, mean, dmean=torch.full((), 3.0, device="cuda"))
+    assert bitwise_equal(h3.grad.view(90, 64), dh) and bitwise_equal(w.grad, dw)
+    each = ssm.linear_cross_entropy(hidden, weight, target, reduction="none")
+    assert each.shape == target.shape
+    assert abs(float(each.sum() * mean[1]) - float(loss.detach())) <= 1e-5 * float(loss.detach())
+    none, dw2 = ssm.ssm_xent_bwd(hidden, weight, target, lse, mean, dmean=torch.full((), 3.0, device="cuda"),
+                                 want_dhidden=False)
+    dh2, none2 = ssm.ssm_xent_bwd(hidden, weight, target, lse, mean, dmean=torch.full((), 3.0, device="cuda"),
+                                  want_dweight=False)
+    assert none is None and none2 is None and bitwise_equal(dw, dw2) and bitwise_equal(dh, dh2)
+
+
+def test_same_bits_and_clean_workspace():
+    hidden, weight, target = (t.cuda() for t in make(300, 136, 1111, torch.bfloat16, seed=12))
+    one = call(hidden, weight, target, None, torch.ones((), device="cuda"))
+    ws = lambda n: torch.full((max(n, 256),), 255, dtype=torch.uint8, device="cuda")  # noqa: E731
+    loss, lse, mean = ssm.ssm_xent_fwd(hidden, weight, target, workspace=ws(ssm.ssm_xent_fwd_workspace(300, 136, 1111)))
+    dh, dw = ssm.ssm_xent_bwd(hidden, weight, target, lse, mean, dmean=torch.ones((), device="cuda"),
+                              workspace=ws(ssm.ssm_xent_bwd_workspace(300, 136, 1111)))
+    for k, t in {"loss": loss, "lse": lse, "mean": mean, "dhidden": dh, "dweight": dw}.items():
+        assert bitwise_equal(t, one[k]), k
+
+
+def test_no_tokens():
+    w = torch.randn(20, 16, device="cuda")
+    h, t = torch.empty(0, 16, device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")
+    loss, lse, mean = ssm.ssm_xent_fwd(h, w, t)
+    dh, dw = ssm.ssm_xent_bwd(h, w, t, lse, mean, dmean=torch.ones((), device="cuda"))
+    assert loss.numel() == 0 and not bool(mean.any()) and dh.numel() == 0 and not bool(dw.any())
+
+
+def test_captured_in_a_graph():
+    hidden, weight, target = (t.cuda() for t in make(200, 128, 700, torch.bfloat16, seed=13))
+    one = torch.ones((), device="cuda")
+    want = call(hidden, weight, target, None, one)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        ssm.ssm_xent_fwd(hidden, weight, target)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, lse, mean = ssm.ssm_xent_fwd(hidden, weight, target)
+        dh, dw = ssm.ssm_xent_bwd(hidden, weight, target, lse, mean, dmean=one)
+    for _ in range(4):
+        loss.zero_(); dh.zero_(); dw.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, t in {"loss": loss, "mean": mean, "dhidden": dh, "dweight": dw}.items():
+            assert bitwise_equal(t, want[k]), k
+        call(hidden, weight, target, None, one)
