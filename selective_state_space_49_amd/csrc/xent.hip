@@ -1,11 +1,19 @@
 // xent.hip -- softmax cross entropy of a linear head over a vocabulary, without keeping the
 // logits, and its gradients.
 //
-// Forward: each thread block makes a 64 x 64 tile of logits and leaves its rows' maximum and
-// sum of exponentials; a second kernel joins a token's partial pairs (m, s), (m', s') to
-// M = max(m, m'), s e^(m-M) + s' e^(m'-M).
-// Backward: for a piece of the vocabulary at a time, dlogits = w (exp(logit - lse) - onehot)
-// go to the workspace, and two products make this piece's rows of dweight and add to dhidden.
+// Everything large is a matrix product on the matrix cores, C[n][m] = sum_k A[m][k] B[n][k]
+// with both operands' rows contiguous in k (k_product), and what differs is its epilogue:
+//   forward    A = weight, B = hidden: a wave's tile of logits leaves, per token, the
+//              maximum and the sum of exponentials over its vocabulary rows; a small kernel
+//              joins a token's pairs: M = max(m, m'), s e^(m-M) + s' e^(m'-M).
+//   backward   for a piece of the vocabulary at a time: the same product again, with
+//              dlogits = w (exp(logit - lse) - onehot) written twice, as G [token][vocab] and
+//              G^T; then dweight rows = G^T hidden (A = hidden^T, B = G^T) and
+//              dhidden += G weight (A = weight^T, B = G).
+// The matrix cores take bfloat16. A float32 operand x is split into x1 + x2 + x3, each the
+// rounded rest of the one before (3 x 8 bits hold its 24), and the product is the sum of
+// the six partial products above 2^-24: x1y1, x1y2, x2y1, x2y2, x1y3, x3y1, as a longer sum
+// over k.
 #include <math.h>
 
 #include <algorithm>
@@ -16,102 +24,427 @@
 namespace ssm {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
-constexpr int64_t kPiece = 2048;  // vocabulary rows of one piece of the backward
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+#define SSM_LDS __attribute__((address_space(3)))
+#define SSM_GLB __attribute__((address_space(1)))
 
-// acc[i][j] += sum_k A(row0 + 4 ty + i, k) B(col0 + 4 tx + j, k) for k < K, in 256 threads;
-// la, lb load one element (0 outside).
-template <typename LA, typename LB>
-__device__ __forceinline__ void tile_product(float (&acc)[4][4], int64_t K, LA la, LB lb) {
-    __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1];
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    for (int64_t k0 = 0; k0 < K; k0 += kDepth) {
-        for (int e = tid; e < kTile * kDepth; e += 256) {
-            const int k = e % kDepth, m = e / kDepth;
-            sa[k][m] = k0 + k < K ? la(m, k0 + k) : 0.0f;
-            sb[k][m] = k0 + k < K ? lb(m, k0 + k) : 0.0f;
-        }
-        __syncthreads();
-        for (int k = 0; k < kDepth; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][4 * ty + i], sb[k][4 * tx + j], acc[i][j]);
-        __syncthreads();
-    }
-}
+constexpr int kBK = 64;        // k per stage: rows of 128 bytes in LDS
+constexpr int kMaxParts = 3;   // bfloat16 planes of a float32 operand
+constexpr uint32_t kRsrcWord3 = 0x00027000;  // raw buffer, 32-bit data
 
-struct Shape {
-    int64_t T, K, V;
+// One operand: rows of ld elements, contiguous in k, 16-byte aligned, ld a multiple of 64;
+// planes `plane` elements apart.
+struct Operand {
+    const bf16_bits *p;
+    int64_t ld, plane;
 };
 
-template <typename IO>
-__device__ __forceinline__ void logits_tile(float (&acc)[4][4], const void *hidden, const void *weight, Shape n,
-                                            int64_t t0, int64_t v0) {
-    tile_product(
-        acc, n.K,
-        [&](int m, int64_t k) { return t0 + m < n.T ? Io<IO>::ld((const IO *)hidden + (t0 + m) * n.K + k) : 0.0f; },
-        [&](int m, int64_t k) { return v0 + m < n.V ? Io<IO>::ld((const IO *)weight + (v0 + m) * n.K + k) : 0.0f; });
+enum class Epi { Lse, Dlogits, Out };
+
+struct ProductArgs {
+    Operand a, b;
+    int64_t M, N;           // rows of A and of B
+    int32_t steps;          // ceil(K / kBK)
+    int32_t parts;          // 1, or 3: six partial products
+    int32_t tiles_m, tiles_n, splits;
+    // Lse, Dlogits: m = vocabulary row - v0, n = token
+    const int32_t *target;  // [N]: vocabulary row, -1 ignored, -2 out of range
+    float2 *part;           // Lse: [tiles_m * waves][N]
+    float *at;              // Lse: [N] logit of the target
+    const float *lse, *w;   // Dlogits: [N]
+    int64_t v0;
+    bf16_bits *g, *gt;      // Dlogits: G [N][ldg], G^T [M][ldgt], planes apart
+    int64_t ldg, ldgt, gplane, gtplane;
+    // Out: C [N][ldc] of float32 or bfloat16 at split * cstride
+    void *c;
+    int64_t ldc, cstride;
+    bool c_bf16;
+    float *sum;             // with `add`: C = sum + product
+    bool add;
+};
+
+// The raw part of v that a bfloat16 holds, and what is left.
+__device__ __forceinline__ bf16_bits take(float &v) {
+    const bf16_bits b = f32_to_bf16(v);
+    v -= bf16_to_f32(b);
+    return b;
 }
 
-// part[t][tile] = (max, sum of exp(logit - max)) over the tile's columns; at[t] = the
-// target's logit.
-template <typename IO>
-__global__ void __launch_bounds__(256) k_xent_part(const void *hidden, const void *weight, const int64_t *targets,
-                                                   Shape n, float2 *part, float *at) {
-    const int64_t t0 = (int64_t)blockIdx.y * kTile, v0 = (int64_t)blockIdx.x * kTile;
-    float acc[4][4] = {};
-    logits_tile<IO>(acc, hidden, weight, n, t0, v0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int i = 0; i < 4; ++i) {
-        const int64_t t = t0 + 4 * ty + i;
-        float m = -INFINITY;
-        for (int j = 0; j < 4; ++j)
-            if (v0 + 4 * tx + j < n.V) m = m > acc[i][j] || m != m ? m : acc[i][j];
-        for (int o = 8; o > 0; o >>= 1) {
-            const float w = __shfl_xor(m, o);
-            m = m > w || m != m ? m : w;
+// Waves stand WM x WN over a BM x BN tile; each makes TM x TN blocks of 32 x 32 with
+// v_mfma_f32_32x32x16_bf16. Operand tiles go from global memory straight to LDS, 16 bytes a
+// lane, double buffered; the 16-byte chunk c of row r lies at chunk c ^ (r & 7), so the 8
+// rows that a group of lanes reads at one k fall on 8 different chunks.
+template <int BM, int BN, int WM, int WN>
+struct Shape {
+    static constexpr int kThreads = 64 * WM * WN;
+    static constexpr int kWaves = WM * WN;
+    static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
+    static constexpr int kStage = (BM + BN) * kBK * 2;   // bytes
+    static constexpr int kRow = BM + 2;                  // staging of G: elements of a token's row
+    static constexpr int kLds = std::max(2 * kStage, BN * kRow * 2);
+    static constexpr int kLoadsA = BM * kBK * 2 / (1024 * kWaves), kLoadsB = BN * kBK * 2 / (1024 * kWaves);
+};
+
+template <typename S, Epi E, int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::TM][S::TN], SSM_LDS char *lds,
+                                         int64_t m0, int64_t n0, int wm, int wn, int split);
+
+template <int BM, int BN, int WM, int WN, Epi E>
+__device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char *lds) {
+    using S = Shape<BM, BN, WM, WN>;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave % WM, wn = wave / WM;
+
+    // Tiles of one XCD (blocks are dealt to the 8 of them in turn) are neighbours, in groups
+    // of 8 tile rows, so that its L2 sees an operand row several times.
+    const int nt = p.tiles_m * p.tiles_n, bid = blockIdx.x, xcd = bid & 7, q = nt >> 3, rest = nt & 7;
+    const int id = xcd * q + min(xcd, rest) + (bid >> 3);
+    const int width = 8 * p.tiles_n, group = id / width, gm = min(p.tiles_m - group * 8, 8), in = id % width;
+    const int64_t m0 = (int64_t)(group * 8 + in % gm) * BM, n0 = (int64_t)(in / gm) * BN;
+
+    const int total = p.steps * (p.parts == 1 ? 1 : 6);
+    const int split = blockIdx.y;
+    const int first = (int)((int64_t)total * split / p.splits), last = (int)((int64_t)total * (split + 1) / p.splits);
+
+    // A load instruction of a wave fills 8 rows of 8 chunks. Rows past the operand's end read
+    // its last row: their products are never used.
+    uint32_t va[S::kLoadsA], vb[S::kLoadsB];
+    const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16u;
+#pragma unroll
+    for (int j = 0; j < S::kLoadsA; ++j) {
+        const int64_t r = min((int64_t)((j * S::kWaves + wave) * 8 + (lane >> 3)), p.M - 1 - m0);
+        va[j] = (uint32_t)(r * p.a.ld * 2) + chunk;
+    }
+#pragma unroll
+    for (int j = 0; j < S::kLoadsB; ++j) {
+        const int64_t r = min((int64_t)((j * S::kWaves + wave) * 8 + (lane >> 3)), p.N - 1 - n0);
+        vb[j] = (uint32_t)(r * p.b.ld * 2) + chunk;
+    }
+    auto stage = [&](int kt) {
+        const int seg = kt / p.steps, k = kt - seg * p.steps;
+        // parts of (A, B) by segment: (0,0) (0,1) (1,0) (1,1) (0,2) (2,0)
+        const int pa = (0x201100 >> (4 * seg)) & 15, pb = (0x021010 >> (4 * seg)) & 15;
+        __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(p.a.p + pa * p.a.plane + m0 * p.a.ld), 0, -1, kRsrcWord3);
+        __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+            (void *)(p.b.p + pb * p.b.plane + n0 * p.b.ld), 0, -1, kRsrcWord3);
+        SSM_LDS char *to = lds + (kt & 1) * S::kStage + wave * 1024;
+#pragma unroll
+        for (int j = 0; j < S::kLoadsA; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (SSM_LDS void *)(to + j * S::kWaves * 1024), 16, va[j],
+                                                     k * (kBK * 2), 0, 0);
+        to += BM * kBK * 2;
+#pragma unroll
+        for (int j = 0; j < S::kLoadsB; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (SSM_LDS void *)(to + j * S::kWaves * 1024), 16, vb[j],
+                                                     k * (kBK * 2), 0, 0);
+    };
+
+    // Fragments: lane l holds row l % 32 of a block, 8 consecutive k of half l / 32.
+    const int row = lane & 31, half = lane >> 5;
+    uint32_t fa[4], fb[4];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t c = (uint32_t)(((2 * ks + half) ^ (row & 7)) * 16 + row * 128);
+        fa[ks] = c + wm * S::TM * 4096;
+        fb[ks] = c + wn * S::TN * 4096 + BM * kBK * 2;
+    }
+    f32x16 acc[S::TM][S::TN];
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    bf16x8 a[2][S::TM], b[2][S::TN];
+    auto fetch = [&](int set, int kt, int ks) {
+        const SSM_LDS char *at = lds + (kt & 1) * S::kStage;
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) a[set][i] = *(const SSM_LDS bf16x8 *)(at + fa[ks] + i * 4096);
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j) b[set][j] = *(const SSM_LDS bf16x8 *)(at + fb[ks] + j * 4096);
+    };
+    auto multiply = [&](int set) {
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[set][i], b[set][j], acc[i][j], 0, 0, 0);
+    };
+    // Every wave's loads into the next stage and reads of this one are done.
+    auto meet = [&]() {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+    };
+    if (first < last) {
+        stage(first);
+        meet();
+        if (first + 1 < last) stage(first + 1);
+        fetch(0, first, 0);
+        for (int kt = first; kt < last; ++kt) {
+            fetch(1, kt, 1);
+            multiply(0);
+            fetch(0, kt, 2);
+            multiply(1);
+            fetch(1, kt, 3);
+            multiply(0);
+            if (kt + 1 < last) {
+                // the last fragments of this stage are in registers once everybody is here
+                meet();
+                if (kt + 2 < last) stage(kt + 2);
+                fetch(0, kt + 1, 0);
+            }
+            multiply(1);
         }
-        float s = 0.0f;
-        for (int j = 0; j < 4; ++j)
-            if (v0 + 4 * tx + j < n.V) s += m == -INFINITY ? 0.0f : e2((acc[i][j] - m) * kLog2e);
-        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor(s, o);
-        if (t >= n.T) continue;
-        if (tx == 0) part[t * gridDim.x + blockIdx.x] = make_float2(m, s);
-        const int64_t y = targets[t] - (v0 + 4 * tx);
-        if (y >= 0 && y < 4) at[t] = y < 2 ? (y == 0 ? acc[i][0] : acc[i][1]) : (y == 2 ? acc[i][2] : acc[i][3]);
+        meet();  // the epilogue may use the LDS
+    }
+    epilogue<S, E, BM, BN, WM, WN>(p, acc, lds, m0, n0, wm, wn, split);
+}
+
+template <int BM, int BN, int WM, int WN, Epi E>
+__global__ void __launch_bounds__(64 * WM * WN) k_product(ProductArgs p) {
+    __shared__ __attribute__((aligned(1024))) char lds[Shape<BM, BN, WM, WN>::kLds];
+    product_tile<BM, BN, WM, WN, E>(p, (SSM_LDS char *)lds);
+}
+
+// A block's element e of lane l is row m = 8 (e / 4) + 4 (l / 32) + e % 4, column n = l % 32.
+template <typename S, Epi E, int BM, int BN, int WM, int WN>
+__device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::TM][S::TN], SSM_LDS char *lds,
+                                         int64_t m0, int64_t n0, int wm, int wn, int split) {
+    const int lane = threadIdx.x & 63, half = lane >> 5;
+    const int64_t mw = m0 + wm * S::TM * 32 + 4 * half;  // the lane's first row
+    const int64_t nw = n0 + wn * S::TN * 32 + (lane & 31);
+    if constexpr (E == Epi::Lse) {
+        const int64_t slot = (m0 / BM) * WM + wm;
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j) {
+            const int64_t n = nw + j * 32;
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float v = acc[i][j][e];
+                    if (mw + i * 32 + 8 * (e / 4) + e % 4 < p.M) top = top > v || top != top ? top : v;
+                }
+            const float o = __shfl_xor(top, 32);
+            top = top > o || top != top ? top : o;
+            float s = 0.0f;
+            // a maximum of -inf (no rows, or all of them) has no terms
+            const float off = top == -INFINITY ? 0.0f : top * kLog2e;
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (mw + i * 32 + 8 * (e / 4) + e % 4 < p.M) s += e2(fmaf(acc[i][j][e], kLog2e, -off));
+            s += __shfl_xor(s, 32);
+            if (n >= p.N) continue;
+            if (half == 0) p.part[slot * p.N + n] = make_float2(top, s);
+            const int64_t t = p.target[n] - mw;  // the lane's rows are t = 32 i + 8 (e / 4) + e % 4
+            if (p.target[n] >= 0 && t >= 0 && t < S::TM * 32 && (t & 4) == 0) {
+#pragma unroll
+                for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (t == i * 32 + 8 * (e / 4) + e % 4) p.at[n] = acc[i][j][e];
+            }
+        }
+    }
+    if constexpr (E == Epi::Dlogits) {
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j) {
+            const int64_t n = nw + j * 32;
+            const bool in = n < p.N;
+            const int32_t target = in ? p.target[n] : -1;
+            const float lse = in ? p.lse[n] : 0.0f, w = in ? p.w[n] : 0.0f;
+            const int64_t t = target - p.v0 - mw;
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int at = i * 32 + 8 * (e / 4) + e % 4;
+                    const float q = e2((acc[i][j][e] - lse) * kLog2e) - (t == at ? 1.0f : 0.0f);
+                    // an ignored token and the padding are exactly 0, whatever the logit
+                    acc[i][j][e] = target == -1 || mw + at >= p.M ? 0.0f : w * q;
+                }
+        }
+        // Through LDS, a token's row of kRow elements (an odd number of words, so that 8
+        // tokens at one pair of columns fall on different banks), and out both ways.
+        constexpr int kWords = S::kRow / 2;
+        SSM_LDS uint32_t *words = (SSM_LDS uint32_t *)lds;
+        for (int part = 0; part < p.parts; ++part) {
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+#pragma unroll
+                for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const int n = wn * S::TN * 32 + j * 32 + (lane & 31);
+                        const int m = wm * S::TM * 32 + 4 * half + i * 32 + 8 * (e / 4) + e % 4;
+                        float v0 = acc[i][j][e], v1 = acc[i][j][e + 1];
+                        const uint32_t lo = take(v0), hi = take(v1);
+                        acc[i][j][e] = v0;
+                        acc[i][j][e + 1] = v1;
+                        words[n * kWords + m / 2] = lo | hi << 16;
+                    }
+            __syncthreads();
+            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+            bf16_bits *g = p.g + part * p.gplane, *gt = p.gt + part * p.gtplane;
+            for (int c = threadIdx.x; c < BN * (BM / 8); c += S::kThreads) {  // 8 columns of a token
+                const int n = c / (BM / 8), m = c % (BM / 8) * 8;
+                if (n0 + n >= p.N || m0 + m >= p.ldg) continue;
+                const SSM_LDS uint32_t *from = words + n * kWords + m / 2;
+                *(u32x4 *)(g + (n0 + n) * p.ldg + m0 + m) = u32x4{from[0], from[1], from[2], from[3]};
+            }
+            if (p.gt)
+                for (int c = threadIdx.x; c < (BM / 2) * (BN / 8); c += S::kThreads) {  // 8 tokens of 2 columns
+                    // 8 lanes cover 64 tokens of one pair of columns: a whole line of G^T
+                    const int m = (c / 8) % (BM / 2) * 2, n = (c / 8 / (BM / 2) * 8 + c % 8) * 8;
+                    if (m0 + m >= p.M || n0 + n >= p.ldgt) continue;
+                    uint32_t v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = words[(n + k) * kWords + m / 2];
+                    u32x4 lo, hi;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        lo[k] = __builtin_amdgcn_perm(v[2 * k + 1], v[2 * k], 0x05040100);
+                        hi[k] = __builtin_amdgcn_perm(v[2 * k + 1], v[2 * k], 0x07060302);
+                    }
+                    bf16_bits *to = gt + (m0 + m) * p.ldgt + n0 + n;
+                    *(u32x4 *)to = lo;
+                    if (m0 + m + 1 < p.M) *(u32x4 *)(to + p.ldgt) = hi;
+                }
+            __syncthreads();
+        }
+    }
+    if constexpr (E == Epi::Out) {
+        const bool vec = p.ldc % 4 == 0 && ((uintptr_t)p.c & 15) == 0;
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j) {
+            const int64_t n = nw + j * 32;
+            if (n >= p.N) continue;
+#pragma unroll
+            for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const int64_t m = mw + i * 32 + 2 * e;
+                    if (m >= p.M) continue;
+                    const int64_t at = n * p.ldc + m;
+                    float v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = acc[i][j][e + k];
+                    if (p.add)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (m + k < p.M) v[k] += p.sum[at + k];
+                    if (vec && m + 3 < p.M) {
+                        if (p.c_bf16) {
+                            uint2 w;
+                            w.x = f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16;
+                            w.y = f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16;
+                            *(uint2 *)((bf16_bits *)p.c + split * p.cstride + at) = w;
+                        } else {
+                            *(float4 *)((float *)p.c + split * p.cstride + at) = make_float4(v[0], v[1], v[2], v[3]);
+                        }
+                    } else {
+                        for (int k = 0; k < 4 && m + k < p.M; ++k) {
+                            if (p.c_bf16) ((bf16_bits *)p.c)[split * p.cstride + at + k] = f32_to_bf16(v[k]);
+                            else ((float *)p.c)[split * p.cstride + at + k] = v[k];
+                        }
+                    }
+                }
+        }
     }
 }
 
-// A wave per token joins its partial pairs.
-__global__ void __launch_bounds__(64) k_xent_join(const float2 *part, const float *at, const int64_t *targets,
-                                                  int64_t ignore, Shape n, int64_t tiles, float *loss, float *lse) {
-    const int64_t t = blockIdx.x;
-    float m = -INFINITY, s = 0.0f;
-    for (int64_t j = threadIdx.x; j < tiles; j += 64) {
-        const float2 q = part[t * tiles + j];
-        const float M = m > q.x || m != m ? m : q.x;
-        const float f = m == M ? 1.0f : e2((m - M) * kLog2e), g = q.x == M ? 1.0f : e2((q.x - M) * kLog2e);
-        s = s * f + q.y * g;
-        m = M;
+// ---------------------------------------------------------------- operands
+// dst[part][r][ld] = parts of src [rows][cols], 0 past its columns.
+template <typename IO>
+__global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64_t cols, bf16_bits *dst, int64_t ld,
+                                              int64_t plane, int parts) {
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= ld) return;
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+        float v = c < cols ? Io<IO>::ld(src + r * cols + c) : 0.0f;
+        for (int k = 0; k < parts; ++k) dst[k * plane + r * ld + c] = take(v);
     }
-    for (int o = 32; o > 0; o >>= 1) {
-        const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o);
-        const float M = m > m2 || m != m ? m : m2;
-        const float f = m == M ? 1.0f : e2((m - M) * kLog2e), g = m2 == M ? 1.0f : e2((m2 - M) * kLog2e);
-        s = s * f + s2 * g;
-        m = M;
+}
+
+// dst[part][c][ld] = parts of src^T, src [rows][cols]; 0 past its rows, and for the rows
+// whose target is ignored: they may hold anything, and 0 times it must not reach a sum.
+template <typename IO>
+__global__ void __launch_bounds__(256) k_pack_t(const IO *src, int64_t rows, int64_t cols, const int32_t *target,
+                                                bf16_bits *dst, int64_t ld, int64_t plane, int parts) {
+    __shared__ float sh[64][65];
+    const int64_t c0 = (int64_t)blockIdx.x * 64;
+    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    for (int64_t r0 = (int64_t)blockIdx.y * 64; r0 < ld; r0 += (int64_t)gridDim.y * 64) {
+        for (int k = y; k < 64; k += 4) {
+            const int64_t r = r0 + k;
+            const bool in = r < rows && c0 + x < cols && !(target && target[r] == -1);
+            sh[k][x] = in ? Io<IO>::ld(src + r * cols + c0 + x) : 0.0f;
+        }
+        __syncthreads();
+        for (int k = y; k < 64; k += 4) {
+            if (c0 + k >= cols) break;
+            float v = sh[x][k];
+            for (int q = 0; q < parts; ++q) dst[q * plane + (c0 + k) * ld + r0 + x] = take(v);
+        }
+        __syncthreads();
     }
-    if (threadIdx.x) return;
-    const float l = m + logf(s);
+}
+
+// target[t] = the row, -1 where ignored, -2 where out of range; w[t] = the loss's weight.
+__global__ void __launch_bounds__(256) k_xent_tokens(const int64_t *targets, int64_t ignore, int64_t T, int64_t V,
+                                                     const float *dloss, const float *dmean, const float *mean,
+                                                     int32_t *target, float *w) {
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= T) return;
     const int64_t y = targets[t];
+    const int32_t to = y == ignore ? -1 : y >= 0 && y < V ? (int32_t)y : -2;
+    target[t] = to;
+    if (w) w[t] = to == -2 ? NAN : (dloss ? dloss[t] : 0.0f) + (dmean ? *dmean * mean[1] : 0.0f);
+}
+
+// (m, s) += (m2, s2): sums of exponentials under their maxima.
+__device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
+    const float M = m > m2 || m != m ? m : m2;
+    const float f = m == M ? 1.0f : e2((m - M) * kLog2e), g = m2 == M ? 1.0f : e2((m2 - M) * kLog2e);
+    s = s * f + s2 * g;
+    m = M;
+}
+
+// 16 threads for a token join its n partial pairs.
+__global__ void __launch_bounds__(256) k_xent_join(const float2 *part, int64_t n, const float *at,
+                                                   const int32_t *target, int64_t T, float *loss, float *lse) {
+    __shared__ float2 sh[16][16];
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
+    const int64_t t = (int64_t)blockIdx.x * 16 + x;
+    float m = -INFINITY, s = 0.0f;
+    if (t < T)
+        for (int64_t j = y; j < n; j += 16) {
+            const float2 q = part[j * T + t];
+            join(m, s, q.x, q.y);
+        }
+    sh[y][x] = make_float2(m, s);
+    __syncthreads();
+    if (y || t >= T) return;
+    for (int j = 1; j < 16; ++j) join(m, s, sh[j][x].x, sh[j][x].y);
+    const float l = m + logf(s);
     lse[t] = l;
-    loss[t] = y == ignore ? 0.0f : y >= 0 && y < n.V ? l - at[t] : NAN;
+    loss[t] = target[t] == -1 ? 0.0f : target[t] >= 0 ? l - at[t] : NAN;
 }
 
 // mean[0] = mean loss over the tokens that are not ignored, mean[1] = 1 / their number.
 __global__ void __launch_bounds__(1024) k_xent_mean(const float *loss, const int64_t *targets, int64_t ignore,
                                                     int64_t T, float *mean) {
-    __shared__ double sh[1024];
-    __shared__ int64_t sn[1024];
+    __shared__ double sh[16];
+    __shared__ int64_t sn[16];
     double s = 0.0;
     int64_t c = 0;
     for (int64_t t = threadIdx.x; t < T; t += 1024)
@@ -119,84 +452,33 @@ __global__ void __launch_bounds__(1024) k_xent_mean(const float *loss, const int
             s += loss[t];
             ++c;
         }
-    sh[threadIdx.x] = s;
-    sn[threadIdx.x] = c;
+    for (int o = 32; o > 0; o >>= 1) {
+        s += __shfl_xor(s, o);
+        c += __shfl_xor(c, o);
+    }
+    if ((threadIdx.x & 63) == 0) {
+        sh[threadIdx.x >> 6] = s;
+        sn[threadIdx.x >> 6] = c;
+    }
     __syncthreads();
-    for (int o = 512; o > 0; o >>= 1) {
-        if ((int)threadIdx.x < o) {
-            sh[threadIdx.x] += sh[threadIdx.x + o];
-            sn[threadIdx.x] += sn[threadIdx.x + o];
-        }
-        __syncthreads();
+    if (threadIdx.x) return;
+    for (int j = 1; j < 16; ++j) {
+        s += sh[j];
+        c += sn[j];
     }
-    if (threadIdx.x == 0) {
-        mean[0] = sn[0] ? (float)(sh[0] / (double)sn[0]) : 0.0f;
-        mean[1] = sn[0] ? (float)(1.0 / (double)sn[0]) : 0.0f;
-    }
+    mean[0] = c ? (float)(s / (double)c) : 0.0f;
+    mean[1] = c ? (float)(1.0 / (double)c) : 0.0f;
 }
 
-// g[t][v - v0] = w_t (exp(logit - lse_t) - [v == target]) for one piece of n_v columns.
-template <typename IO>
-__global__ void __launch_bounds__(256) k_xent_dlogits(XentArgs a, int64_t v0, int64_t n_v, float *g, int64_t ldg) {
-    const int64_t t0 = (int64_t)blockIdx.y * kTile, c0 = (int64_t)blockIdx.x * kTile;
-    float acc[4][4] = {};
-    const Shape n{a.T, a.K, v0 + n_v};
-    logits_tile<IO>(acc, a.hidden, a.weight, n, t0, v0 + c0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int i = 0; i < 4; ++i) {
-        const int64_t t = t0 + 4 * ty + i;
-        if (t >= a.T) continue;
-        const int64_t y = a.targets[t];
-        const bool skip = y == a.ignore, bad = !skip && (y < 0 || y >= a.V);
-        float w = (a.dloss ? a.dloss[t] : 0.0f) + (a.dmean ? *a.dmean * a.mean[1] : 0.0f);
-        if (bad) w = NAN;
-        for (int j = 0; j < 4; ++j) {
-            const int64_t c = c0 + 4 * tx + j;
-            if (c >= n_v) continue;
-            const float q = e2((acc[i][j] - a.lse[t]) * kLog2e) - (y == v0 + c ? 1.0f : 0.0f);
-            g[t * ldg + c] = skip ? 0.0f : w * q;
-        }
-    }
-}
-
-// dweight rows [v0, v0 + n_v) = g^T hidden.
-template <typename IO>
-__global__ void __launch_bounds__(256) k_xent_dweight(XentArgs a, int64_t v0, int64_t n_v, const float *g, int64_t ldg) {
-    const int64_t r0 = (int64_t)blockIdx.y * kTile, c0 = (int64_t)blockIdx.x * kTile;
-    float acc[4][4] = {};
-    tile_product(
-        acc, a.T, [&](int m, int64_t t) { return r0 + m < n_v ? g[t * ldg + r0 + m] : 0.0f; },
-        [&](int m, int64_t t) {  // an ignored token's hidden row may hold anything
-            return c0 + m < a.K && a.targets[t] != a.ignore ? Io<IO>::ld((const IO *)a.hidden + t * a.K + c0 + m) : 0.0f;
-        });
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + 4 * ty + i, c = c0 + 4 * tx + j;
-            if (r < n_v && c < a.K) Io<IO>::st((IO *)a.dweight + (v0 + r) * a.K + c, acc[i][j]);
-        }
-}
-
-// sum (+)= g weight[v0 ..]; the last piece writes dhidden.
-template <typename IO>
-__global__ void __launch_bounds__(256) k_xent_dhidden(XentArgs a, int64_t v0, int64_t n_v, const float *g, int64_t ldg,
-                                                      float *sum, bool first, bool last) {
-    const int64_t r0 = (int64_t)blockIdx.y * kTile, c0 = (int64_t)blockIdx.x * kTile;
-    float acc[4][4] = {};
-    tile_product(
-        acc, n_v, [&](int m, int64_t v) { return r0 + m < a.T ? g[(r0 + m) * ldg + v] : 0.0f; },
-        [&](int m, int64_t v) {
-            return c0 + m < a.K ? Io<IO>::ld((const IO *)a.weight + (v0 + v) * a.K + c0 + m) : 0.0f;
-        });
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int64_t r = r0 + 4 * ty + i, c = c0 + 4 * tx + j;
-            if (r >= a.T || c >= a.K) continue;
-            const float q = first ? acc[i][j] : sum[r * a.K + c] + acc[i][j];
-            if (last) Io<IO>::st((IO *)a.dhidden + r * a.K + c, q);
-            else sum[r * a.K + c] = q;
-        }
+// dst = (sum +) the n partial products in order; float32 or bfloat16.
+__global__ void __launch_bounds__(256) k_join_splits(const float *part, int n, int64_t stride, int64_t count,
+                                                     const float *sum, void *dst, bool bf16) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= count) return;
+    float v = sum ? sum[e] : 0.0f;
+    for (int k = 0; k < n; ++k) v += part[k * stride + e];
+    if (bf16) ((bf16_bits *)dst)[e] = f32_to_bf16(v);
+    else ((float *)dst)[e] = v;
 }
 
 template <typename IO>
@@ -205,54 +487,245 @@ __global__ void __launch_bounds__(256) k_zero(IO *p, int64_t n) {
     if (e < n) p[e] = IO(0);
 }
 
-unsigned tiles(int64_t n) { return (unsigned)((n + kTile - 1) / kTile); }
+// ---------------------------------------------------------------- host
+int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per); }
+
+constexpr int kBig = 256, kSmall = 128;
+
+// 256 x 256 tiles where they fill the device's compute units, else 128 x 128.
+struct Tiling {
+    int tile, splits;
+};
+constexpr int64_t kCus = 256;
+Tiling tiling(int64_t M, int64_t N, int64_t steps, bool may_split) {
+    if ((int64_t)blocks(M, kBig) * blocks(N, kBig) >= kCus) return {kBig, 1};
+    const int64_t n = (int64_t)blocks(M, kSmall) * blocks(N, kSmall);
+    int64_t s = 1;
+    // a split keeps at least 8 steps of k, and its partial sums are written and read again
+    if (may_split) s = std::max<int64_t>(1, std::min(std::min<int64_t>(2 * kCus / n, steps / 8), (int64_t)16));
+    return {kSmall, (int)s};
+}
+
+template <Epi E>
+hipError_t product(ProductArgs p, int tile, hipStream_t s) {
+    p.tiles_m = (int32_t)blocks(p.M, tile);
+    p.tiles_n = (int32_t)blocks(p.N, tile);
+    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits);
+    if (tile == kBig) k_product<256, 256, 2, 4, E><<<grid, 512, 0, s>>>(p);
+    else k_product<128, 128, 2, 2, E><<<grid, 256, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+// A bump allocator over the workspace; with no base it only counts.
+struct Arena {
+    char *base;
+    size_t used = 0;
+    template <typename P>
+    P *take(int64_t n) {
+        P *p = base ? (P *)(base + used) : nullptr;
+        used += round_up((size_t)n * sizeof(P), kTrainWsAlign);
+        return p;
+    }
+};
+
+// What a call lays out in its workspace.
+struct Layout {
+    int parts;
+    int64_t ldk, ldt, piece;   // padded dim, tokens; vocabulary rows of a piece
+    Tiling lse, out_w, out_h;
+    bool pack;                 // hidden and weight are copied: float32, or rows not in steps of 64
+    bf16_bits *hidden, *weight;
+    int32_t *target;
+    float *at, *w, *sum, *split;
+    float2 *part;
+    bf16_bits *ht, *wt, *g, *gt;
+    size_t bytes;
+};
+
+// G and G^T of a piece hold about 2^26 values each: 8192 tokens take pieces of 8192 rows, whose
+// three products are 512 and 1024 tiles of 256 x 256, whole rounds of the compute units.
+constexpr int64_t kPieceValues = (int64_t)1 << 26;
+
+Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, char *ws) {
+    Layout l{};
+    Arena a{ws};
+    l.parts = io ? 1 : kMaxParts;
+    l.ldk = up(K, kBK);
+    l.ldt = up(T, kBK);
+    l.pack = !io || K % kBK != 0 || !aligned;
+    l.target = a.take<int32_t>(T);
+    // sized as if the operands had to be copied: their alignment is not known to the query
+    l.hidden = a.take<bf16_bits>(T * l.ldk * l.parts);
+    l.weight = a.take<bf16_bits>(V * l.ldk * l.parts);
+    if (!bwd) {
+        l.lse = tiling(V, T, l.ldk / kBK, false);
+        l.part = a.take<float2>((int64_t)blocks(V, l.lse.tile) * 2 * T);
+        l.at = a.take<float>(T);
+    } else {
+        l.piece = std::min(up(V, kBig), std::max<int64_t>(1024, kPieceValues / std::max<int64_t>(T, 1) / kBig * kBig));
+        const int64_t most = std::min(V, l.piece);
+        l.out_w = tiling(K, most, l.ldt / kBK * (l.parts == 1 ? 1 : 6), true);
+        l.out_h = tiling(K, T, up(most, kBK) / kBK * (l.parts == 1 ? 1 : 6), true);
+        l.w = a.take<float>(T);
+        l.sum = a.take<float>(V > l.piece ? T * K : 0);
+        l.ht = a.take<bf16_bits>(K * l.ldt * l.parts);
+        l.wt = a.take<bf16_bits>(K * up(most, kBK) * l.parts);
+        l.g = a.take<bf16_bits>(T * up(most, kBK) * l.parts);
+        l.gt = a.take<bf16_bits>(most * l.ldt * l.parts);
+        const int64_t sw = l.out_w.splits > 1 ? l.out_w.splits * most * K : 0;
+        const int64_t sh = l.out_h.splits > 1 ? l.out_h.splits * T * K : 0;
+        l.split = a.take<float>(std::max(sw, sh));
+    }
+    l.bytes = a.used;
+    return l;
+}
 
 template <typename IO>
-hipError_t xent_fwd(const XentArgs &a, hipStream_t s) {
+hipError_t pack(const void *src, int64_t rows, int64_t cols, bf16_bits *dst, int64_t ld, int parts, hipStream_t s) {
+    k_pack<IO><<<dim3(blocks(ld, 256), (unsigned)std::min<int64_t>(rows, 65535)), 256, 0, s>>>((const IO *)src, rows, cols,
+                                                                                               dst, ld, rows * ld, parts);
+    return hipGetLastError();
+}
+template <typename IO>
+hipError_t pack_t(const void *src, int64_t rows, int64_t cols, const int32_t *target, bf16_bits *dst, int64_t ld,
+                  int parts, hipStream_t s) {
+    k_pack_t<IO><<<dim3(blocks(cols, 64), (unsigned)std::min<int64_t>(ld / 64, 65535)), 256, 0, s>>>(
+        (const IO *)src, rows, cols, target, dst, ld, cols * ld, parts);
+    return hipGetLastError();
+}
+
+#define SSM_TRY(x)                                 \
+    do {                                           \
+        const hipError_t try_e = (x);              \
+        if (try_e != hipSuccess) return try_e;     \
+    } while (0)
+
+bool rows_aligned(const XentArgs &a) { return ((uintptr_t)a.hidden | (uintptr_t)a.weight) % 16 == 0; }
+
+// The operands of the logits: hidden and weight as they are, or their packed copies.
+template <typename IO>
+hipError_t logits_operands(const XentArgs &a, const Layout &l, ProductArgs &p, hipStream_t s) {
+    const bf16_bits *h = (const bf16_bits *)a.hidden, *w = (const bf16_bits *)a.weight;
+    if (l.pack) {
+        SSM_TRY(pack<IO>(a.hidden, a.T, a.K, l.hidden, l.ldk, l.parts, s));
+        SSM_TRY(pack<IO>(a.weight, a.V, a.K, l.weight, l.ldk, l.parts, s));
+        h = l.hidden;
+        w = l.weight;
+    }
+    p.a = {w, l.ldk, a.V * l.ldk};
+    p.b = {h, l.ldk, a.T * l.ldk};
+    p.steps = (int32_t)(l.ldk / kBK);
+    p.parts = l.parts;
+    p.splits = 1;
+    p.target = l.target;
+    return hipSuccess;
+}
+
+template <typename IO>
+hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
     if (a.T > 0) {
-        const Shape n{a.T, a.K, a.V};
-        float2 *part = (float2 *)a.ws;
-        float *at = (float *)(part + (size_t)a.T * tiles(a.V));
-        k_xent_part<IO><<<dim3(tiles(a.V), tiles(a.T)), 256, 0, s>>>(a.hidden, a.weight, a.targets, n, part, at);
-        k_xent_join<<<dim3((unsigned)a.T), 64, 0, s>>>(part, at, a.targets, a.ignore, n, tiles(a.V), a.loss, a.lse);
+        const Layout l = lay_out(a.T, a.K, a.V, io, false, rows_aligned(a), (char *)a.ws);
+        k_xent_tokens<<<dim3(blocks(a.T, 256)), 256, 0, s>>>(a.targets, a.ignore, a.T, a.V, nullptr, nullptr, nullptr,
+                                                            l.target, nullptr);
+        ProductArgs p{};
+        SSM_TRY(logits_operands<IO>(a, l, p, s));
+        p.M = a.V;
+        p.N = a.T;
+        p.part = l.part;
+        p.at = l.at;
+        SSM_TRY(product<Epi::Lse>(p, l.lse.tile, s));
+        k_xent_join<<<dim3(blocks(a.T, 16)), 256, 0, s>>>(l.part, (int64_t)blocks(a.V, l.lse.tile) * 2, l.at, l.target,
+                                                         a.T, a.loss, a.lse);
     }
     k_xent_mean<<<dim3(1), 1024, 0, s>>>(a.loss, a.targets, a.ignore, a.T, a.mean);
     return hipGetLastError();
 }
 
+// C [N][M] = (sum +) A B^T through partial sums over k where it is split.
+hipError_t product_out(ProductArgs p, Tiling t, float *split, void *dst, bool bf16, float *sum, bool add, hipStream_t s) {
+    p.splits = t.splits;
+    p.ldc = p.M;
+    p.sum = sum;
+    p.add = add && t.splits == 1;
+    p.c = t.splits == 1 ? dst : split;
+    p.c_bf16 = bf16 && t.splits == 1;
+    p.cstride = p.M * p.N;
+    SSM_TRY(product<Epi::Out>(p, t.tile, s));
+    if (t.splits > 1)
+        k_join_splits<<<dim3(blocks(p.M * p.N, 256)), 256, 0, s>>>(split, t.splits, p.cstride, p.M * p.N,
+                                                                  add ? sum : nullptr, dst, bf16);
+    return hipGetLastError();
+}
+
 template <typename IO>
-hipError_t xent_bwd(const XentArgs &a, hipStream_t s) {
+hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
     if (a.T == 0) {
-        if (a.dweight)
-            k_zero<IO><<<dim3((unsigned)((a.V * a.K + 255) / 256)), 256, 0, s>>>((IO *)a.dweight, a.V * a.K);
+        if (a.dweight) k_zero<IO><<<dim3(blocks(a.V * a.K, 256)), 256, 0, s>>>((IO *)a.dweight, a.V * a.K);
         return hipGetLastError();
     }
-    const int64_t ldg = std::min(a.V, kPiece);
-    float *g = (float *)a.ws, *sum = g + (size_t)a.T * ldg;
-    for (int64_t v0 = 0; v0 < a.V; v0 += kPiece) {
-        const int64_t n_v = std::min(kPiece, a.V - v0);
-        k_xent_dlogits<IO><<<dim3(tiles(n_v), tiles(a.T)), 256, 0, s>>>(a, v0, n_v, g, ldg);
-        if (a.dweight) k_xent_dweight<IO><<<dim3(tiles(a.K), tiles(n_v)), 256, 0, s>>>(a, v0, n_v, g, ldg);
-        if (a.dhidden)
-            k_xent_dhidden<IO><<<dim3(tiles(a.K), tiles(a.T)), 256, 0, s>>>(a, v0, n_v, g, ldg, sum, v0 == 0,
-                                                                           v0 + n_v == a.V);
+    const Layout l = lay_out(a.T, a.K, a.V, io, true, rows_aligned(a), (char *)a.ws);
+    k_xent_tokens<<<dim3(blocks(a.T, 256)), 256, 0, s>>>(a.targets, a.ignore, a.T, a.V, a.dloss, a.dmean, a.mean,
+                                                        l.target, l.w);
+    ProductArgs logits{};
+    SSM_TRY(logits_operands<IO>(a, l, logits, s));
+    logits.N = a.T;
+    logits.lse = a.lse;
+    logits.w = l.w;
+    if (a.dweight) SSM_TRY(pack_t<IO>(a.hidden, a.T, a.K, l.target, l.ht, l.ldt, l.parts, s));
+    for (int64_t v0 = 0; v0 < a.V; v0 += l.piece) {
+        const int64_t nv = std::min(l.piece, a.V - v0), ldg = up(nv, kBK);
+        ProductArgs p = logits;
+        p.a.p += v0 * l.ldk;
+        p.M = nv;
+        p.v0 = v0;
+        p.g = l.g;
+        p.gt = a.dweight ? l.gt : nullptr;
+        p.ldg = ldg;
+        p.ldgt = l.ldt;
+        p.gplane = a.T * ldg;
+        p.gtplane = nv * l.ldt;
+        const bool big = (int64_t)blocks(nv, kBig) * blocks(a.T, kBig) >= kCus;
+        SSM_TRY(product<Epi::Dlogits>(p, big ? kBig : kSmall, s));
+        if (a.dweight) {
+            ProductArgs q{};
+            q.a = {l.ht, l.ldt, a.K * l.ldt};
+            q.b = {l.gt, l.ldt, nv * l.ldt};
+            q.M = a.K;
+            q.N = nv;
+            q.steps = (int32_t)(l.ldt / kBK);
+            q.parts = l.parts;
+            SSM_TRY(product_out(q, l.out_w, l.split, (IO *)a.dweight + v0 * a.K, io, nullptr, false, s));
+        }
+        if (a.dhidden) {
+            SSM_TRY(pack_t<IO>((const IO *)a.weight + v0 * a.K, nv, a.K, nullptr, l.wt, ldg, l.parts, s));
+            ProductArgs q{};
+            q.a = {l.wt, ldg, a.K * ldg};
+            q.b = {l.g, ldg, a.T * ldg};
+            q.M = a.K;
+            q.N = a.T;
+            q.steps = (int32_t)(ldg / kBK);
+            q.parts = l.parts;
+            const bool end = v0 + nv == a.V;
+            SSM_TRY(product_out(q, l.out_h, l.split, end ? a.dhidden : l.sum, end && io, l.sum, v0 > 0, s));
+        }
     }
-    return hipGetLastError();
+    return hipSuccess;
 }
 
 }  // namespace
 
-size_t xent_fwd_ws(int64_t T, int64_t, int64_t V, int) {
-    return round_up((size_t)T * (tiles(V) * sizeof(float2) + sizeof(float)), kTrainWsAlign);
+size_t xent_fwd_ws(int64_t T, int64_t K, int64_t V, int io) {
+    return T > 0 ? lay_out(T, K, V, io, false, false, nullptr).bytes : 0;
 }
-size_t xent_bwd_ws(int64_t T, int64_t K, int64_t V, int) {
-    return round_up((size_t)T * (std::min(V, kPiece) + K) * sizeof(float), kTrainWsAlign);
+size_t xent_bwd_ws(int64_t T, int64_t K, int64_t V, int io) {
+    return T > 0 ? lay_out(T, K, V, io, true, false, nullptr).bytes : 0;
 }
 hipError_t launch_xent_fwd(const XentArgs &a, int io, hipStream_t s) {
-    return io ? xent_fwd<bf16_bits>(a, s) : xent_fwd<float>(a, s);
+    return io ? xent_fwd<bf16_bits>(a, io, s) : xent_fwd<float>(a, io, s);
 }
 hipError_t launch_xent_bwd(const XentArgs &a, int io, hipStream_t s) {
-    return io ? xent_bwd<bf16_bits>(a, s) : xent_bwd<float>(a, s);
+    return io ? xent_bwd<bf16_bits>(a, io, s) : xent_bwd<float>(a, io, s);
 }
 
 }  // namespace ssm
