@@ -52,13 +52,15 @@ ssm_status check_workspace(const void *ws, size_t have, size_t need) {
 
 bool gated_shape_ok(int64_t batch, int64_t L, int64_t D) {
     return batch >= 0 && batch <= 65535 && L >= 0 && D >= 1 && D <= ((int64_t)1 << 28) &&
-           (double)batch * (double)L * (double)D <= 4.0e17;
+           (double)batch * (double)L * (double)D <= 4.0e17 &&
+           // one thread block for at least 64 steps x 64 channels
+           (double)batch * (double)(L / 64 + 1) * (double)(D / 64 + 1) <= 2147483647.0;
 }
 
 ssm_status check_gated(int64_t batch, int64_t L, int64_t D, ssm_dtype io, float c) {
     if (!valid_io(io)) return fail(SSM_ERR_DTYPE, "io dtype %d unknown", (int)io);
     if (!gated_shape_ok(batch, L, D))
-        return fail(SSM_ERR_SHAPE, "batch must be in 0..65535, L >= 0, d_inner in 1..2^28");
+        return fail(SSM_ERR_SHAPE, "batch must be in 0..65535, L >= 0, d_inner in 1..2^28, and their product within the grid");
     if (!(c > 0.0f) || isinf(c)) return fail(SSM_ERR_UNSUPPORTED, "c must be finite and positive");
     return SSM_OK;
 }

@@ -42,75 +42,438 @@ __device__ __forceinline__ Gate gate(float r, float i, float ck) {
     return g;
 }
 
-constexpr int kThreads = 64;
+// ---------------------------------------------------------------- tiles
+// One pass over the data. A thread block owns a tile of R W steps x 64 CPL channels: W waves,
+// each with R consecutive steps, a lane with CPL channels, every value of the tile in
+// registers. A wave reduces its steps to the pair (P, H): the state leaving them is
+// P h_in + H, P = prod a. The waves' pairs meet in LDS, the tiles' pairs in global memory:
+// a tile publishes its pair, takes the state that enters it from its predecessors' words,
+// publishes the state that leaves it, and only then walks its steps with the true state. So each input is read once, where summary and rescan passes read it twice.
+//
+// A published word is 64 bits, {H, P | flags}, written and read whole by relaxed atomics at
+// device scope: P lies in [0, 1], which leaves the two top bits of its float free for
+// "valid" and "final state" (P not needed), and nothing else has to be ordered. The words
+// start at 0. Blocks take their tiles from a counter in the order of the walk, so the tile
+// that a block waits for belongs to a block that already runs: every wait ends.
+constexpr uint64_t kValid = 1ull << 63, kFinal = 1ull << 62;
 
-template <typename IO>
-__global__ void __launch_bounds__(kThreads) k_gated_fwd(GatedArgs p) {
-    const int64_t d = (int64_t)blockIdx.x * kThreads + threadIdx.x, b = blockIdx.y;
-    if (d >= p.D) return;
-    const float ck = p.c * softplus(p.decay[d]);
-    const int64_t rows = (p.L + SSM_GATED_STATE_EVERY - 1) / SSM_GATED_STATE_EVERY;
-    float h = p.h0 ? p.h0[b * p.D + d] : 0.0f;
-    for (int64_t t = 0; t < p.L; ++t) {
-        const int64_t e = (b * p.L + t) * p.D + d;
-        if (p.states && t % SSM_GATED_STATE_EVERY == 0)
-            p.states[(b * rows + t / SSM_GATED_STATE_EVERY) * p.D + d] = h;
-        const Gate g = gate(Io<IO>::ld((const IO *)p.r + e), Io<IO>::ld((const IO *)p.i + e), ck);
-        const float in = g.beta * g.si * Io<IO>::ld((const IO *)p.x + e);
-        h = p.reset && p.reset[b * p.L + t] ? in : fmaf(g.a, h, in);
-        Io<IO>::st((IO *)p.y + e, h);
-    }
-    if (p.h_final) p.h_final[b * p.D + d] = h;
+__device__ __forceinline__ uint64_t pack_word(float P, float H, uint64_t flags) {
+    // a NaN decay has made H a NaN too, and P's bits must stay clear of the flags
+    const uint32_t p = P == P ? __float_as_uint(P) : 0u;
+    return flags | (uint64_t)p << 32 | __float_as_uint(H);
+}
+__device__ __forceinline__ float word_H(uint64_t w) { return __uint_as_float((uint32_t)w); }
+__device__ __forceinline__ float word_P(uint64_t w) { return __uint_as_float((uint32_t)(w >> 32) & 0x3fffffffu); }
+
+// c after steps with the pair (P, H). With resets a P of 0 cuts: nothing of c passes, a NaN
+// neither.
+template <bool RESET>
+__device__ __forceinline__ float through(float P, float H, float c) {
+    return RESET && P == 0.0f ? H : fmaf(P, c, H);
 }
 
-template <typename IO>
-__global__ void __launch_bounds__(kThreads) k_gated_bwd(GatedArgs p) {
-    const int64_t d = (int64_t)blockIdx.x * kThreads + threadIdx.x, b = blockIdx.y;
-    if (d >= p.D) return;
-    const float ck = p.c * softplus(p.decay[d]);
-    const int64_t rows = (p.L + SSM_GATED_STATE_EVERY - 1) / SSM_GATED_STATE_EVERY;
-    float u = p.dh_final ? p.dh_final[b * p.D + d] : 0.0f, sum = 0.0f;
-    float before[SSM_GATED_STATE_EVERY];
-    for (int64_t row = rows - 1; row >= 0; --row) {
-        const int64_t t0 = row * SSM_GATED_STATE_EVERY;
-        const int n = (int)min((int64_t)SSM_GATED_STATE_EVERY, p.L - t0);
-        float h = p.states[(b * rows + row) * p.D + d];
-        for (int j = 0; j < n; ++j) {
-            const int64_t e = (b * p.L + t0 + j) * p.D + d;
-            before[j] = h;
-            const Gate g = gate(Io<IO>::ld((const IO *)p.r + e), Io<IO>::ld((const IO *)p.i + e), ck);
-            const float in = g.beta * g.si * Io<IO>::ld((const IO *)p.x + e);
-            h = p.reset && p.reset[b * p.L + t0 + j] ? in : fmaf(g.a, h, in);
+// The state that enters a tile of the walk, for a lane's CPL channels; word j is the j-th tile
+// at words + j stride, and `carry` comes in as the state before the first. Reads the words
+// of kAhead predecessors until a final state is among them with every word after it there,
+// and takes it forward: c <- P c + H, tile by tile. The value does not depend on which final
+// state was met, since that one was made by the same steps; composing pairs on the way
+// back would round differently from run to run.
+constexpr int kAhead = 8;
+template <bool RESET, int CPL>
+__device__ __forceinline__ void look_back(const uint64_t *words, int64_t stride, int64_t tile, bool in,
+                                          float (&carry)[CPL]) {
+    for (;;) {
+        uint64_t w[kAhead][CPL];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            const int64_t j = tile - 1 - q;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c)
+                w[q][c] = j >= 0 ? __hip_atomic_load(words + j * stride + c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                                 : pack_word(0.0f, carry[c], kValid | kFinal);
         }
-        for (int j = n - 1; j >= 0; --j) {
-            const int64_t e = (b * p.L + t0 + j) * p.D + d;
-            const bool cut = p.reset && p.reset[b * p.L + t0 + j];
-            const Gate g = gate(Io<IO>::ld((const IO *)p.r + e), Io<IO>::ld((const IO *)p.i + e), ck);
-            const float x = Io<IO>::ld((const IO *)p.x + e);
-            const float gt = Io<IO>::ld((const IO *)p.dy + e) + u;
-            const float gb = gt * g.beta, kb = g.beta > 0.0f ? g.k / g.beta : 0.0f;
-            const float ah = cut ? 0.0f : g.a * before[j];
-            const float kd = gt * (g.a * g.a * kb * g.si * x - g.k * ah);
-            Io<IO>::st((IO *)p.dx + e, gb * g.si);
-            Io<IO>::st((IO *)p.di + e, gb * x * g.si * (1.0f - g.si));
-            Io<IO>::st((IO *)p.dr + e, kd * (1.0f - g.sr));
-            sum += kd;
-            u = cut ? 0.0f : g.a * gt;
+        bool all = true;
+        float state[CPL];
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            bool have = false;
+            state[c] = 0.0f;
+#pragma unroll
+            for (int q = kAhead - 1; q >= 0; --q) {
+                const float P = word_P(w[q][c]), H = word_H(w[q][c]);
+                const bool valid = w[q][c] & kValid, last = (w[q][c] & kFinal) || (RESET && P == 0.0f);
+                state[c] = last ? H : through<RESET>(P, H, state[c]);
+                have = valid && (last || have);
+            }
+            all = all && have;
         }
+        if (__all(all || !in)) {
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) carry[c] = state[c];
+            return;
+        }
+        __builtin_amdgcn_s_sleep(1);
     }
-    if (p.dh0) p.dh0[b * p.D + d] = u;
-    ((float *)p.ws)[b * p.D + d] = sum;
 }
 
-// ddecay[d] = sigmoid(decay) / softplus(decay) * sum over n partial rows, in order.
-__global__ void __launch_bounds__(kThreads) k_gated_ddecay(const float *part, const float *decay, float *out,
-                                                           int64_t n, int64_t D) {
-    const int64_t d = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (d >= D) return;
-    float s = 0.0f;
-    for (int64_t j = 0; j < n; ++j) s += part[j * D + d];
+// CPL neighbouring elements of a row.
+template <typename IO, int CPL> struct Lane;
+template <typename IO> struct Lane<IO, 1> {
+    typedef IO raw;
+    static __device__ __forceinline__ raw ld(const IO *p) { return *p; }
+    static __device__ __forceinline__ void get(raw w, float (&v)[1]) { v[0] = Io<IO>::ld(&w); }
+    static __device__ __forceinline__ void st(IO *p, const float (&v)[1]) { Io<IO>::st(p, v[0]); }
+};
+template <> struct Lane<bf16_bits, 2> {
+    typedef uint32_t raw;
+    static __device__ __forceinline__ raw ld(const bf16_bits *p) { return *(const uint32_t *)p; }
+    static __device__ __forceinline__ void get(raw w, float (&v)[2]) {
+        v[0] = __uint_as_float(w << 16);
+        v[1] = __uint_as_float(w & 0xffff0000u);
+    }
+    static __device__ __forceinline__ void st(bf16_bits *p, const float (&v)[2]) {
+        *(uint32_t *)p = f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16;
+    }
+};
+
+// Where a block works: the j-th tile of the walk of batch row b, channels from d0.
+struct Place {
+    int64_t j, b, d0;
+};
+__device__ __forceinline__ Place take_tile(const GatedArgs &p, uint32_t *ticket, int cols, int *sh) {
+    uint32_t id = blockIdx.x;
+    if (ticket) {
+        if (threadIdx.x == 0) *sh = (int)__hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        id = (uint32_t)__builtin_amdgcn_readfirstlane(*sh);
+    }
+    const uint32_t per = (uint32_t)(cols * p.batch), j = id / per, rest = id - j * per, b = rest / cols;
+    return {(int64_t)j, (int64_t)b, (int64_t)(rest - b * cols)};
+}
+
+constexpr int kWaves = 8;
+constexpr int kFwdRows = 16, kBwdRows = 8;  // steps of a wave
+constexpr int kFwdTile = kFwdRows * kWaves, kBwdTile = kBwdRows * kWaves;
+static_assert(kFwdTile % SSM_GATED_STATE_EVERY == 0 && SSM_GATED_STATE_EVERY % kFwdRows == 0 &&
+                  kBwdTile == SSM_GATED_STATE_EVERY,
+              "states are stored where waves of the forward and tiles of the backward begin");
+
+// The workspace: a counter (256 bytes), then the words [batch][tiles][D], then the
+// backward's sums.
+__host__ __device__ inline int64_t tiles_of(int64_t L, int tile) { return (L + tile - 1) / tile; }
+size_t words_bytes(int64_t batch, int64_t L, int64_t D, int tile) {
+    const int64_t n = tiles_of(L, tile);
+    return n > 1 ? kTrainWsAlign + round_up((size_t)(batch * n * D) * 8, kTrainWsAlign) : 0;
+}
+
+// 16 steps of a wave, 128 of a tile: at two bfloat16 channels a lane, 48 loads of 4 bytes a
+// lane are in flight before the first gate, and the 2 x 32 floats of (a, b) still leave room
+// for four waves a SIMD.
+template <typename IO, int CPL, bool RESET>
+__global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint32_t *ticket, uint64_t *words) {
+    constexpr int R = kFwdRows, CW = 64 * CPL;
+    __shared__ float sP[kWaves][CW], sH[kWaves][CW], sC[CW];
+    __shared__ int sid;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int cols = (int)((p.D + CW - 1) / CW);
+    const Place at = take_tile(p, ticket, cols, &sid);
+    const int64_t d = at.d0 * CW + lane * CPL, n_tiles = tiles_of(p.L, kFwdTile);
+    const int64_t dc = min(d, p.D - CPL);  // lanes past the last channel work on it and store nothing
+    const bool in = d < p.D;
+    const int64_t t0 = at.j * kFwdTile + wave * R, row0 = at.b * p.L + t0;
+    const int rows = (int)max((int64_t)0, min((int64_t)R, p.L - t0));
+
+    typedef Lane<IO, CPL> Ld;
+    typename Ld::raw x[R], r[R], i[R];
+    if (rows > 0) {
+        const int64_t e = row0 * p.D + dc;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t o = e + min(k, rows - 1) * p.D;
+            r[k] = Ld::ld((const IO *)p.r + o);
+            i[k] = Ld::ld((const IO *)p.i + o);
+            x[k] = Ld::ld((const IO *)p.x + o);
+        }
+    }
+    uint64_t cut = 0;
+    if (RESET) cut = __ballot(lane < rows && p.reset[row0 + min(lane, rows - 1)] != 0);
+    float ck[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) ck[c] = p.c * softplus(p.decay[dc + c]);
+
+    float a[R][CPL], b[R][CPL], P[CPL], H[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        P[c] = 1.0f;
+        H[c] = 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        if (k >= rows) break;
+        float xv[CPL], rv[CPL], iv[CPL];
+        Ld::get(x[k], xv);
+        Ld::get(r[k], rv);
+        Ld::get(i[k], iv);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            const Gate g = gate(rv[c], iv[c], ck[c]);
+            a[k][c] = RESET && (cut >> k & 1) ? 0.0f : g.a;
+            b[k][c] = g.beta * g.si * xv[c];
+            H[c] = RESET && (cut >> k & 1) ? b[k][c] : fmaf(a[k][c], H[c], b[k][c]);
+            P[c] *= a[k][c];
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        sP[wave][lane * CPL + c] = P[c];
+        sH[wave][lane * CPL + c] = H[c];
+    }
+    __syncthreads();
+    // the first wave: the tile's pair, the state that enters the tile, the state that leaves
+    if (wave == 0) {
+        float tP[CPL], tH[CPL], carry[CPL];
+        uint64_t *mine = words ? words + (at.b * n_tiles + at.j) * p.D + d : nullptr;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            tP[c] = P[c];
+            tH[c] = H[c];
+            carry[c] = p.h0 ? p.h0[at.b * p.D + dc + c] : 0.0f;
+            for (int w = 1; w < kWaves; ++w) {
+                tH[c] = through<RESET>(sP[w][lane * CPL + c], sH[w][lane * CPL + c], tH[c]);
+                tP[c] *= sP[w][lane * CPL + c];
+            }
+            if (in && at.j > 0 && at.j + 1 < n_tiles)
+                __hip_atomic_store(mine + c, pack_word(tP[c], tH[c], kValid), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        if (at.j > 0) look_back<RESET, CPL>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            const float out = through<RESET>(tP[c], tH[c], carry[c]);
+            sC[lane * CPL + c] = carry[c];
+            if (!in) continue;
+            if (at.j + 1 < n_tiles)
+                __hip_atomic_store(mine + c, pack_word(0.0f, out, kValid | kFinal), __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+            else if (p.h_final)
+                p.h_final[at.b * p.D + d + c] = out;
+        }
+    }
+    __syncthreads();
+    if (rows == 0) return;
+    float h[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        h[c] = sC[lane * CPL + c];
+        for (int w = 0; w < wave; ++w) h[c] = through<RESET>(sP[w][lane * CPL + c], sH[w][lane * CPL + c], h[c]);
+    }
+    if (!in) return;
+    if (p.states && t0 % SSM_GATED_STATE_EVERY == 0)
+#pragma unroll
+        for (int c = 0; c < CPL; ++c)
+            p.states[(at.b * tiles_of(p.L, SSM_GATED_STATE_EVERY) + t0 / SSM_GATED_STATE_EVERY) * p.D + d + c] = h[c];
+    IO *y = (IO *)p.y + row0 * p.D + d;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        if (k >= rows) break;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) h[c] = RESET && (cut >> k & 1) ? b[k][c] : fmaf(a[k][c], h[c], b[k][c]);
+        Ld::st(y + k * p.D, h);
+    }
+}
+
+// The same from the right: u_t = a_t g_t is what step t passes to its left, g_t = dy_t +
+// u_{t+1}. The states come from the stored row that enters the tile, through the waves'
+// forward pairs.
+template <typename IO, int CPL, bool RESET>
+__global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint32_t *ticket, uint64_t *words,
+                                                              float *sums) {
+    constexpr int R = kBwdRows, CW = 64 * CPL;
+    __shared__ float sP[kWaves][CW], sH[kWaves][CW], sU[kWaves][CW], sC[CW];
+    __shared__ int sid;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int cols = (int)((p.D + CW - 1) / CW);
+    const Place at = take_tile(p, ticket, cols, &sid);
+    const int64_t d = at.d0 * CW + lane * CPL, n_tiles = tiles_of(p.L, kBwdTile);
+    const int64_t dc = min(d, p.D - CPL), tile = n_tiles - 1 - at.j;
+    const bool in = d < p.D;
+    const int64_t t0 = tile * kBwdTile + wave * R, row0 = at.b * p.L + t0;
+    const int rows = (int)max((int64_t)0, min((int64_t)R, p.L - t0));
+
+    typedef Lane<IO, CPL> Ld;
+    typename Ld::raw x[R], r[R], i[R], dy[R];
+    if (rows > 0) {
+        const int64_t e = row0 * p.D + dc;
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int64_t o = e + min(k, rows - 1) * p.D;
+            r[k] = Ld::ld((const IO *)p.r + o);
+            i[k] = Ld::ld((const IO *)p.i + o);
+            x[k] = Ld::ld((const IO *)p.x + o);
+            dy[k] = Ld::ld((const IO *)p.dy + o);
+        }
+    }
+    uint64_t cut = 0;
+    if (RESET) cut = __ballot(lane < rows && p.reset[row0 + min(lane, rows - 1)] != 0);
+    float ck[CPL], h[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        ck[c] = p.c * softplus(p.decay[dc + c]);
+        h[c] = p.states[(at.b * n_tiles + tile) * p.D + dc + c];
+    }
+    float sr[R][CPL], si[R][CPL], a[R][CPL], beta[R][CPL], P[CPL], H[CPL], U[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        P[c] = 1.0f;
+        H[c] = U[c] = 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+        if (k >= rows) break;
+        float xv[CPL], rv[CPL], iv[CPL];
+        Ld::get(x[k], xv);
+        Ld::get(r[k], rv);
+        Ld::get(i[k], iv);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            const Gate g = gate(rv[c], iv[c], ck[c]);
+            sr[k][c] = g.sr;
+            si[k][c] = g.si;
+            a[k][c] = g.a;
+            beta[k][c] = g.beta;
+            const float b = g.beta * g.si * xv[c];
+            const bool z = RESET && (cut >> k & 1);
+            H[c] = z ? b : fmaf(g.a, H[c], b);
+            P[c] = z ? 0.0f : P[c] * g.a;
+        }
+    }
+#pragma unroll
+    for (int k = R - 1; k >= 0; --k) {
+        if (k >= rows) continue;
+        float gv[CPL];
+        Ld::get(dy[k], gv);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) U[c] = RESET && (cut >> k & 1) ? 0.0f : a[k][c] * (gv[c] + U[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        sP[wave][lane * CPL + c] = P[c];
+        sH[wave][lane * CPL + c] = H[c];
+        sU[wave][lane * CPL + c] = U[c];
+    }
+    __syncthreads();
+    if (wave == 0) {
+        float tP[CPL], tU[CPL], carry[CPL];
+        uint64_t *mine = words ? words + (at.b * n_tiles + at.j) * p.D + d : nullptr;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            tP[c] = 1.0f;
+            tU[c] = 0.0f;
+            carry[c] = p.dh_final ? p.dh_final[at.b * p.D + dc + c] : 0.0f;
+            for (int w = kWaves - 1; w >= 0; --w) {
+                tU[c] = through<RESET>(sP[w][lane * CPL + c], sU[w][lane * CPL + c], tU[c]);
+                tP[c] *= sP[w][lane * CPL + c];
+            }
+            if (in && at.j > 0 && at.j + 1 < n_tiles)
+                __hip_atomic_store(mine + c, pack_word(tP[c], tU[c], kValid), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        if (at.j > 0) look_back<RESET, CPL>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            const float out = through<RESET>(tP[c], tU[c], carry[c]);
+            sC[lane * CPL + c] = carry[c];
+            if (!in) continue;
+            if (at.j + 1 < n_tiles)
+                __hip_atomic_store(mine + c, pack_word(0.0f, out, kValid | kFinal), __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+            else if (p.dh0)
+                p.dh0[at.b * p.D + d + c] = out;
+        }
+    }
+    __syncthreads();
+    float u[CPL], sum[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) {
+        u[c] = sC[lane * CPL + c];
+        sum[c] = 0.0f;
+        for (int w = kWaves - 1; w > wave; --w) u[c] = through<RESET>(sP[w][lane * CPL + c], sU[w][lane * CPL + c], u[c]);
+        for (int w = 0; w < wave; ++w) h[c] = through<RESET>(sP[w][lane * CPL + c], sH[w][lane * CPL + c], h[c]);
+    }
+    if (rows > 0) {
+        float before[R][CPL];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            if (k >= rows) break;
+            float xv[CPL];
+            Ld::get(x[k], xv);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                before[k][c] = h[c];
+                const float b = beta[k][c] * si[k][c] * xv[c];
+                h[c] = RESET && (cut >> k & 1) ? b : fmaf(a[k][c], h[c], b);
+            }
+        }
+        const int64_t e = row0 * p.D + dc;
+#pragma unroll
+        for (int k = R - 1; k >= 0; --k) {
+            if (k >= rows) continue;
+            float xv[CPL], gv[CPL], dx[CPL], di[CPL], dr[CPL];
+            Ld::get(x[k], xv);
+            Ld::get(dy[k], gv);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                const bool z = RESET && (cut >> k & 1);
+                const float g = gv[c] + u[c], s = si[k][c], ak = a[k][c], kk = ck[c] * sr[k][c];
+                const float kb = beta[k][c] > 0.0f ? kk * rcp(beta[k][c]) : 0.0f;
+                const float ah = z ? 0.0f : ak * before[k][c];
+                const float kd = g * (ak * ak * kb * s * xv[c] - kk * ah);
+                dx[c] = g * beta[k][c] * s;
+                di[c] = dx[c] * xv[c] * (1.0f - s);
+                dr[c] = kd * (1.0f - sr[k][c]);
+                sum[c] += kd;
+                u[c] = z ? 0.0f : ak * g;
+            }
+            if (in) {
+                Ld::st((IO *)p.dx + e + k * p.D, dx);
+                Ld::st((IO *)p.di + e + k * p.D, di);
+                Ld::st((IO *)p.dr + e + k * p.D, dr);
+            }
+        }
+    }
+    // the tile's sum of k dLoss/dk: the waves' sums in order
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) sP[wave][lane * CPL + c] = sum[c];
+    __syncthreads();
+    if (wave == 0 && in)
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) {
+            float s = 0.0f;
+            for (int w = 0; w < kWaves; ++w) s += sP[w][lane * CPL + c];
+            sums[(at.b * n_tiles + tile) * p.D + d + c] = s;
+        }
+}
+
+// ddecay[d] = sigmoid(decay) / softplus(decay) * sum over the n tiles' sums: 16 threads for a
+// channel, in double, so that the order of thousands of them costs nothing.
+__global__ void __launch_bounds__(1024) k_gated_ddecay(const float *sums, const float *decay, float *out, int64_t n,
+                                                       int64_t D) {
+    __shared__ double sh[16][64];
+    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    const int64_t d = (int64_t)blockIdx.x * 64 + x;
+    double s = 0.0;
+    if (d < D)
+        for (int64_t j = y; j < n; j += 16) s += (double)sums[j * D + d];
+    sh[y][x] = s;
+    __syncthreads();
+    if (y || d >= D) return;
+    for (int j = 1; j < 16; ++j) s += sh[j][x];
     const float sp = softplus(decay[d]);  // 0 where exp(decay) underflows: the ratio tends to 1
-    out[d] = s * (sp > 0.0f ? 1.0f / (1.0f + expf(-decay[d])) / sp : 1.0f);
+    out[d] = (float)s * (sp > 0.0f ? 1.0f / (1.0f + expf(-decay[d])) / sp : 1.0f);
+}
+
+__global__ void __launch_bounds__(256) k_clear(uint4 *p, int64_t n) {
+    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (j < n) p[j] = make_uint4(0, 0, 0, 0);
 }
 
 // dst = src (or 0), n floats.
@@ -138,16 +501,52 @@ __global__ void __launch_bounds__(256) k_gated_step(GatedStepArgs p) {
 
 }  // namespace
 
-size_t gated_fwd_ws(int64_t, int64_t, int64_t) { return 0; }
+size_t gated_fwd_ws(int64_t batch, int64_t L, int64_t D) { return words_bytes(batch, L, D, kFwdTile); }
 size_t gated_bwd_ws(int64_t batch, int64_t L, int64_t D) {
-    return L > 0 ? round_up((size_t)batch * D * sizeof(float), kTrainWsAlign) : 0;
+    return words_bytes(batch, L, D, kBwdTile) +
+           round_up((size_t)(batch * tiles_of(L, kBwdTile) * D) * sizeof(float), kTrainWsAlign);
 }
+
+namespace {
+
+// Two bfloat16 channels a lane where every row of every array starts on 4 bytes, else one: a
+// wave then covers 128 bytes of a row instead of 256.
+bool pairs(const GatedArgs &a, int io) {
+    return io && a.D % 2 == 0 && (((uintptr_t)a.x | (uintptr_t)a.r | (uintptr_t)a.i | (uintptr_t)a.y | (uintptr_t)a.dy |
+                                   (uintptr_t)a.dx | (uintptr_t)a.dr | (uintptr_t)a.di) & 3) == 0;
+}
+
+template <typename IO, int CPL>
+void run_fwd(const GatedArgs &a, uint32_t *ticket, uint64_t *words, hipStream_t s) {
+    const dim3 grid((unsigned)(tiles_of(a.D, 64 * CPL) * a.batch * tiles_of(a.L, kFwdTile)));
+    if (a.reset) k_gated_fwd<IO, CPL, true><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words);
+    else k_gated_fwd<IO, CPL, false><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words);
+}
+template <typename IO, int CPL>
+void run_bwd(const GatedArgs &a, uint32_t *ticket, uint64_t *words, float *sums, hipStream_t s) {
+    const dim3 grid((unsigned)(tiles_of(a.D, 64 * CPL) * a.batch * tiles_of(a.L, kBwdTile)));
+    if (a.reset) k_gated_bwd<IO, CPL, true><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words, sums);
+    else k_gated_bwd<IO, CPL, false><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words, sums);
+}
+
+// The counter and the words of a call with several tiles, cleared; null for one tile.
+void set_up(const GatedArgs &a, int tile, uint32_t **ticket, uint64_t **words, hipStream_t s) {
+    const size_t n = words_bytes(a.batch, a.L, a.D, tile);
+    *ticket = n ? (uint32_t *)a.ws : nullptr;
+    *words = n ? (uint64_t *)((char *)a.ws + kTrainWsAlign) : nullptr;
+    if (n) k_clear<<<dim3((unsigned)((n / 16 + 255) / 256)), 256, 0, s>>>((uint4 *)a.ws, (int64_t)(n / 16));
+}
+
+}  // namespace
 
 hipError_t launch_gated_fwd(const GatedArgs &a, int io, hipStream_t s) {
     if (a.L == 0) return fill(a.h_final, a.h0, a.batch * a.D, s);
-    const dim3 grid((unsigned)((a.D + kThreads - 1) / kThreads), (unsigned)a.batch);
-    if (io) k_gated_fwd<bf16_bits><<<grid, kThreads, 0, s>>>(a);
-    else k_gated_fwd<float><<<grid, kThreads, 0, s>>>(a);
+    uint32_t *ticket;
+    uint64_t *words;
+    set_up(a, kFwdTile, &ticket, &words, s);
+    if (!io) run_fwd<float, 1>(a, ticket, words, s);
+    else if (pairs(a, io)) run_fwd<bf16_bits, 2>(a, ticket, words, s);
+    else run_fwd<bf16_bits, 1>(a, ticket, words, s);
     return hipGetLastError();
 }
 
@@ -156,10 +555,15 @@ hipError_t launch_gated_bwd(const GatedArgs &a, int io, hipStream_t s) {
         const hipError_t e = fill(a.dh0, a.dh_final, a.batch * a.D, s);
         return e != hipSuccess ? e : fill(a.ddecay, nullptr, a.D, s);
     }
-    const dim3 grid((unsigned)((a.D + kThreads - 1) / kThreads), (unsigned)a.batch);
-    if (io) k_gated_bwd<bf16_bits><<<grid, kThreads, 0, s>>>(a);
-    else k_gated_bwd<float><<<grid, kThreads, 0, s>>>(a);
-    k_gated_ddecay<<<dim3(grid.x), kThreads, 0, s>>>((const float *)a.ws, a.decay, a.ddecay, a.batch, a.D);
+    uint32_t *ticket;
+    uint64_t *words;
+    set_up(a, kBwdTile, &ticket, &words, s);
+    float *sums = (float *)((char *)a.ws + words_bytes(a.batch, a.L, a.D, kBwdTile));
+    if (!io) run_bwd<float, 1>(a, ticket, words, sums, s);
+    else if (pairs(a, io)) run_bwd<bf16_bits, 2>(a, ticket, words, sums, s);
+    else run_bwd<bf16_bits, 1>(a, ticket, words, sums, s);
+    k_gated_ddecay<<<dim3((unsigned)((a.D + 63) / 64)), 1024, 0, s>>>(sums, a.decay, a.ddecay,
+                                                                     a.batch * tiles_of(a.L, kBwdTile), a.D);
     return hipGetLastError();
 }
 
