@@ -7,6 +7,8 @@
 //     dx = g beta si,  di = g beta x si (1 - si)
 //     kd = k dLoss/dk = g (a^2 (k / beta) si x - k a h_{t-1}),  dr = kd (1 - sr)
 //     ddecay = sum kd sigmoid(decay) / softplus(decay),  dh0 = a_1 g_1
+#include <type_traits>
+
 #include "ssm_device.h"
 #include "ssm_train.h"
 
@@ -18,11 +20,11 @@ namespace {
 // factor of 5.
 __device__ __forceinline__ float one_minus_a2(float k, float a) {
     const float x = k + k;
-    float p = fmaf(x, -1.0f / 6.0f, 1.0f);
-    p = fmaf(x * p, -1.0f / 5.0f, 1.0f);
-    p = fmaf(x * p, -1.0f / 4.0f, 1.0f);
-    p = fmaf(x * p, -1.0f / 3.0f, 1.0f);
-    p = fmaf(x * p, -1.0f / 2.0f, 1.0f);
+    float p = fmaf(x, -1.0f / 720.0f, 1.0f / 120.0f);
+    p = fmaf(x, p, -1.0f / 24.0f);
+    p = fmaf(x, p, 1.0f / 6.0f);
+    p = fmaf(x, p, -0.5f);
+    p = fmaf(x, p, 1.0f);
     return x < 0.25f ? x * p : fmaf(-a, a, 1.0f);
 }
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + e2(-v * kLog2e)); }
@@ -78,8 +80,7 @@ __device__ __forceinline__ float through(float P, float H, float c) {
 // and takes it forward: c <- P c + H, tile by tile. The value does not depend on which final
 // state was met, since that one was made by the same steps; composing pairs on the way
 // back would round differently from run to run.
-constexpr int kAhead = 8;
-template <bool RESET, int CPL>
+template <bool RESET, int CPL, int kAhead>
 __device__ __forceinline__ void look_back(const uint64_t *words, int64_t stride, int64_t tile, bool in,
                                           float (&carry)[CPL]) {
     for (;;) {
@@ -116,25 +117,33 @@ __device__ __forceinline__ void look_back(const uint64_t *words, int64_t stride,
     }
 }
 
-// CPL neighbouring elements of a row.
+// CPL neighbouring elements of a row, at a uniform address plus the lane's byte offset.
 template <typename IO, int CPL> struct Lane;
 template <typename IO> struct Lane<IO, 1> {
     typedef IO raw;
-    static __device__ __forceinline__ raw ld(const IO *p) { return *p; }
+    static __device__ __forceinline__ raw ld(const char *p, uint32_t off) { return *(const IO *)(p + off); }
     static __device__ __forceinline__ void get(raw w, float (&v)[1]) { v[0] = Io<IO>::ld(&w); }
-    static __device__ __forceinline__ void st(IO *p, const float (&v)[1]) { Io<IO>::st(p, v[0]); }
+    static __device__ __forceinline__ void st(char *p, uint32_t off, const float (&v)[1]) { Io<IO>::st((IO *)(p + off), v[0]); }
 };
 template <> struct Lane<bf16_bits, 2> {
     typedef uint32_t raw;
-    static __device__ __forceinline__ raw ld(const bf16_bits *p) { return *(const uint32_t *)p; }
+    static __device__ __forceinline__ raw ld(const char *p, uint32_t off) { return *(const uint32_t *)(p + off); }
     static __device__ __forceinline__ void get(raw w, float (&v)[2]) {
         v[0] = __uint_as_float(w << 16);
         v[1] = __uint_as_float(w & 0xffff0000u);
     }
-    static __device__ __forceinline__ void st(bf16_bits *p, const float (&v)[2]) {
-        *(uint32_t *)p = f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16;
+    static __device__ __forceinline__ void st(char *p, uint32_t off, const float (&v)[2]) {
+        *(uint32_t *)(p + off) = f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16;
     }
 };
+
+// fn(std::true_type) for a wave whose R steps are all there, else fn(std::false_type): the
+// common case compiles without a test per step.
+template <int R, typename F>
+__device__ __forceinline__ void by_rows(int rows, F fn) {
+    if (rows == R) fn(std::true_type{});
+    else if (rows > 0) fn(std::false_type{});
+}
 
 // Where a block works: the j-th tile of the walk of batch row b, channels from d0.
 struct Place {
@@ -185,44 +194,44 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint3
 
     typedef Lane<IO, CPL> Ld;
     typename Ld::raw x[R], r[R], i[R];
-    if (rows > 0) {
-        const int64_t e = row0 * p.D + dc;
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const int64_t o = e + min(k, rows - 1) * p.D;
-            r[k] = Ld::ld((const IO *)p.r + o);
-            i[k] = Ld::ld((const IO *)p.i + o);
-            x[k] = Ld::ld((const IO *)p.x + o);
-        }
-    }
-    uint64_t cut = 0;
-    if (RESET) cut = __ballot(lane < rows && p.reset[row0 + min(lane, rows - 1)] != 0);
-    float ck[CPL];
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) ck[c] = p.c * softplus(p.decay[dc + c]);
-
-    float a[R][CPL], b[R][CPL], P[CPL], H[CPL];
+    const int64_t base = (row0 * p.D + at.d0 * CW) * (int64_t)sizeof(IO), step = p.D * (int64_t)sizeof(IO);
+    const uint32_t off = (uint32_t)(dc - at.d0 * CW) * (uint32_t)sizeof(IO);
+    float a[R][CPL], b[R][CPL], P[CPL], H[CPL], ck[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
         P[c] = 1.0f;
         H[c] = 0.0f;
     }
+    uint64_t cut = 0;
+    by_rows<R>(rows, [&](auto full) {
+        int64_t o = base;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        if (k >= rows) break;
-        float xv[CPL], rv[CPL], iv[CPL];
-        Ld::get(x[k], xv);
-        Ld::get(r[k], rv);
-        Ld::get(i[k], iv);
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-            const Gate g = gate(rv[c], iv[c], ck[c]);
-            a[k][c] = RESET && (cut >> k & 1) ? 0.0f : g.a;
-            b[k][c] = g.beta * g.si * xv[c];
-            H[c] = RESET && (cut >> k & 1) ? b[k][c] : fmaf(a[k][c], H[c], b[k][c]);
-            P[c] *= a[k][c];
+        for (int k = 0; k < R; ++k) {
+            r[k] = Ld::ld((const char *)p.r + o, off);
+            i[k] = Ld::ld((const char *)p.i + o, off);
+            x[k] = Ld::ld((const char *)p.x + o, off);
+            if (full || k + 1 < rows) o += step;  // a step past the end reads the last one
         }
-    }
+        if (RESET) cut = __ballot(lane < rows && p.reset[row0 + min(lane, rows - 1)] != 0);
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) ck[c] = p.c * softplus(p.decay[dc + c]);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const bool there = full || k < rows, z = RESET && (cut >> k & 1);
+            float xv[CPL], rv[CPL], iv[CPL];
+            Ld::get(x[k], xv);
+            Ld::get(r[k], rv);
+            Ld::get(i[k], iv);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+                const Gate g = gate(rv[c], iv[c], ck[c]);
+                a[k][c] = there ? (z ? 0.0f : g.a) : 1.0f;
+                b[k][c] = there ? g.beta * g.si * xv[c] : 0.0f;
+                H[c] = z ? b[k][c] : fmaf(a[k][c], H[c], b[k][c]);
+                P[c] *= a[k][c];
+            }
+        }
+    });
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
         sP[wave][lane * CPL + c] = P[c];
@@ -245,7 +254,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint3
             if (in && at.j > 0 && at.j + 1 < n_tiles)
                 __hip_atomic_store(mine + c, pack_word(tP[c], tH[c], kValid), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (at.j > 0) look_back<RESET, CPL>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
+        if (at.j > 0) look_back<RESET, CPL, 8>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
             const float out = through<RESET>(tP[c], tH[c], carry[c]);
@@ -271,14 +280,17 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint3
 #pragma unroll
         for (int c = 0; c < CPL; ++c)
             p.states[(at.b * tiles_of(p.L, SSM_GATED_STATE_EVERY) + t0 / SSM_GATED_STATE_EVERY) * p.D + d + c] = h[c];
-    IO *y = (IO *)p.y + row0 * p.D + d;
+    by_rows<R>(rows, [&](auto full) {
+        char *y = (char *)p.y + base;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        if (k >= rows) break;
+        for (int k = 0; k < R; ++k) {
+            if (!full && k >= rows) continue;
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) h[c] = RESET && (cut >> k & 1) ? b[k][c] : fmaf(a[k][c], h[c], b[k][c]);
-        Ld::st(y + k * p.D, h);
-    }
+            for (int c = 0; c < CPL; ++c) h[c] = RESET && (cut >> k & 1) ? b[k][c] : fmaf(a[k][c], h[c], b[k][c]);
+            Ld::st(y, off, h);
+            y += step;
+        }
+    });
 }
 
 // The same from the right: u_t = a_t g_t is what step t passes to its left, g_t = dy_t +
@@ -300,20 +312,9 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
     const int rows = (int)max((int64_t)0, min((int64_t)R, p.L - t0));
 
     typedef Lane<IO, CPL> Ld;
-    typename Ld::raw x[R], r[R], i[R], dy[R];
-    if (rows > 0) {
-        const int64_t e = row0 * p.D + dc;
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const int64_t o = e + min(k, rows - 1) * p.D;
-            r[k] = Ld::ld((const IO *)p.r + o);
-            i[k] = Ld::ld((const IO *)p.i + o);
-            x[k] = Ld::ld((const IO *)p.x + o);
-            dy[k] = Ld::ld((const IO *)p.dy + o);
-        }
-    }
-    uint64_t cut = 0;
-    if (RESET) cut = __ballot(lane < rows && p.reset[row0 + min(lane, rows - 1)] != 0);
+    typename Ld::raw x[R], dy[R];
+    const int64_t base = (row0 * p.D + at.d0 * CW) * (int64_t)sizeof(IO), step = p.D * (int64_t)sizeof(IO);
+    const uint32_t off = (uint32_t)(dc - at.d0 * CW) * (uint32_t)sizeof(IO);
     float ck[CPL], h[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
@@ -326,34 +327,48 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
         P[c] = 1.0f;
         H[c] = U[c] = 0.0f;
     }
+    uint64_t cut = 0;
+    by_rows<R>(rows, [&](auto full) {
+        typename Ld::raw r[R], i[R];
+        int64_t o = base;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-        if (k >= rows) break;
-        float xv[CPL], rv[CPL], iv[CPL];
-        Ld::get(x[k], xv);
-        Ld::get(r[k], rv);
-        Ld::get(i[k], iv);
-#pragma unroll
-        for (int c = 0; c < CPL; ++c) {
-            const Gate g = gate(rv[c], iv[c], ck[c]);
-            sr[k][c] = g.sr;
-            si[k][c] = g.si;
-            a[k][c] = g.a;
-            beta[k][c] = g.beta;
-            const float b = g.beta * g.si * xv[c];
-            const bool z = RESET && (cut >> k & 1);
-            H[c] = z ? b : fmaf(g.a, H[c], b);
-            P[c] = z ? 0.0f : P[c] * g.a;
+        for (int k = 0; k < R; ++k) {
+            r[k] = Ld::ld((const char *)p.r + o, off);
+            i[k] = Ld::ld((const char *)p.i + o, off);
+            x[k] = Ld::ld((const char *)p.x + o, off);
+            dy[k] = Ld::ld((const char *)p.dy + o, off);
+            if (full || k + 1 < rows) o += step;  // a step past the end reads the last one
         }
-    }
+        if (RESET) cut = __ballot(lane < rows && p.reset[row0 + min(lane, rows - 1)] != 0);
 #pragma unroll
-    for (int k = R - 1; k >= 0; --k) {
-        if (k >= rows) continue;
-        float gv[CPL];
-        Ld::get(dy[k], gv);
+        for (int k = 0; k < R; ++k) {
+            const bool there = full || k < rows, z = RESET && (cut >> k & 1);
+            float xv[CPL], rv[CPL], iv[CPL];
+            Ld::get(x[k], xv);
+            Ld::get(r[k], rv);
+            Ld::get(i[k], iv);
 #pragma unroll
-        for (int c = 0; c < CPL; ++c) U[c] = RESET && (cut >> k & 1) ? 0.0f : a[k][c] * (gv[c] + U[c]);
-    }
+            for (int c = 0; c < CPL; ++c) {
+                const Gate g = gate(rv[c], iv[c], ck[c]);
+                sr[k][c] = g.sr;
+                si[k][c] = g.si;
+                a[k][c] = g.a;
+                beta[k][c] = g.beta;
+                if (!there) continue;
+                const float b = g.beta * g.si * xv[c];
+                H[c] = z ? b : fmaf(g.a, H[c], b);
+                P[c] = z ? 0.0f : P[c] * g.a;
+            }
+        }
+#pragma unroll
+        for (int k = R - 1; k >= 0; --k) {
+            if (!full && k >= rows) continue;
+            float gv[CPL];
+            Ld::get(dy[k], gv);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) U[c] = RESET && (cut >> k & 1) ? 0.0f : a[k][c] * (gv[c] + U[c]);
+        }
+    });
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
         sP[wave][lane * CPL + c] = P[c];
@@ -376,7 +391,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
             if (in && at.j > 0 && at.j + 1 < n_tiles)
                 __hip_atomic_store(mine + c, pack_word(tP[c], tU[c], kValid), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (at.j > 0) look_back<RESET, CPL>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
+        if (at.j > 0) look_back<RESET, CPL, 4>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
             const float out = through<RESET>(tP[c], tU[c], carry[c]);
@@ -398,11 +413,11 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
         for (int w = kWaves - 1; w > wave; --w) u[c] = through<RESET>(sP[w][lane * CPL + c], sU[w][lane * CPL + c], u[c]);
         for (int w = 0; w < wave; ++w) h[c] = through<RESET>(sP[w][lane * CPL + c], sH[w][lane * CPL + c], h[c]);
     }
-    if (rows > 0) {
+    by_rows<R>(rows, [&](auto full) {
         float before[R][CPL];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
-            if (k >= rows) break;
+            if (!full && k >= rows) continue;
             float xv[CPL];
             Ld::get(x[k], xv);
 #pragma unroll
@@ -412,10 +427,10 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
                 h[c] = RESET && (cut >> k & 1) ? b : fmaf(a[k][c], h[c], b);
             }
         }
-        const int64_t e = row0 * p.D + dc;
+        int64_t o = base + (int64_t)(rows - 1) * step;
 #pragma unroll
         for (int k = R - 1; k >= 0; --k) {
-            if (k >= rows) continue;
+            if (!full && k >= rows) continue;
             float xv[CPL], gv[CPL], dx[CPL], di[CPL], dr[CPL];
             Ld::get(x[k], xv);
             Ld::get(dy[k], gv);
@@ -433,12 +448,13 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
                 u[c] = z ? 0.0f : ak * g;
             }
             if (in) {
-                Ld::st((IO *)p.dx + e + k * p.D, dx);
-                Ld::st((IO *)p.di + e + k * p.D, di);
-                Ld::st((IO *)p.dr + e + k * p.D, dr);
+                Ld::st((char *)p.dx + o, off, dx);
+                Ld::st((char *)p.di + o, off, di);
+                Ld::st((char *)p.dr + o, off, dr);
             }
+            o -= step;
         }
-    }
+    });
     // the tile's sum of k dLoss/dk: the waves' sums in order
     __syncthreads();
 #pragma unroll
