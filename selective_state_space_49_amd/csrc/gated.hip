@@ -7,6 +7,7 @@
 //     dx = g beta si,  di = g beta x si (1 - si)
 //     kd = k dLoss/dk = g (a^2 (k / beta) si x - k a h_{t-1}),  dr = kd (1 - sr)
 //     ddecay = sum kd sigmoid(decay) / softplus(decay),  dh0 = a_1 g_1
+#include <algorithm>
 #include <type_traits>
 
 #include "ssm_device.h"
@@ -28,7 +29,19 @@ __device__ __forceinline__ float one_minus_a2(float k, float a) {
     return x < 0.25f ? x * p : fmaf(-a, a, 1.0f);
 }
 __device__ __forceinline__ float sigmoid(float v) { return rcp(1.0f + e2(-v * kLog2e)); }
-__device__ __forceinline__ float softplus(float v) { return fmaxf(v, 0.0f) + log1pf(expf(-fabsf(v))); }
+// softplus(v) = max(v, 0) + log(1 + e), e = exp(-|v|) in (0, 1], with log(1 + e) =
+// 2 atanh(s), s = e / (2 + e) <= 1/3: relative precision also where e is small, as it is for
+// slow decays. The first term of the series left out is below 2e-8 of the sum.
+__device__ __forceinline__ float softplus(float v) {
+    const float e = e2(-fabsf(v) * kLog2e), s = e * rcp(2.0f + e), q = s * s;
+    float p = fmaf(q, 1.0f / 13.0f, 1.0f / 11.0f);
+    p = fmaf(q, p, 1.0f / 9.0f);
+    p = fmaf(q, p, 1.0f / 7.0f);
+    p = fmaf(q, p, 1.0f / 5.0f);
+    p = fmaf(q, p, 1.0f / 3.0f);
+    p = fmaf(q, p, 1.0f);
+    return fmaxf(v, 0.0f) + (s + s) * p;
+}
 
 struct Gate {
     float sr, si, k, a, beta;
@@ -502,17 +515,47 @@ hipError_t fill(float *dst, const float *src, int64_t n, hipStream_t s) {
     return hipGetLastError();
 }
 
-// One token: a lane per (layer, sequence, channel).
-template <typename IO>
+// One token. A lane has N neighbouring channels of a layer, makes their decays once for S
+// sequences, and has the loads of all of them in flight. What bounds it is the bytes: 16 a
+// channel in bfloat16, half of them the state.
+template <typename IO, int N, int S>
 __global__ void __launch_bounds__(256) k_gated_step(GatedStepArgs p) {
-    const int64_t d = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t d = ((int64_t)blockIdx.x * 256 + threadIdx.x) * N;
     if (d >= p.D) return;
-    const int64_t e = ((int64_t)blockIdx.z * p.n_seq + blockIdx.y) * p.D + d;
-    const float ck = p.c * softplus(p.decay[(int64_t)blockIdx.z * p.D + d]);
-    const Gate g = gate(Io<IO>::ld((const IO *)p.r + e), Io<IO>::ld((const IO *)p.i + e), ck);
-    const float h = fmaf(g.a, p.h[e], g.beta * g.si * Io<IO>::ld((const IO *)p.x + e));
-    p.h[e] = h;
-    Io<IO>::st((IO *)p.y + e, h);
+    const int64_t s0 = (int64_t)blockIdx.y * S, left = p.n_seq - s0;
+    const int64_t e0 = ((int64_t)blockIdx.z * p.n_seq + s0) * p.D + d;
+    typedef IO iov __attribute__((ext_vector_type(N)));
+    typedef float f32v __attribute__((ext_vector_type(N)));
+    iov r[S], i[S], x[S];
+    f32v h[S];
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+        const int64_t e = e0 + min((int64_t)k, left - 1) * p.D;
+        r[k] = *(const iov *)((const IO *)p.r + e);
+        i[k] = *(const iov *)((const IO *)p.i + e);
+        x[k] = *(const iov *)((const IO *)p.x + e);
+        h[k] = *(const f32v *)(p.h + e);
+    }
+    const f32v dec = *(const f32v *)(p.decay + blockIdx.z * p.D + d);
+    float ck[N];
+#pragma unroll
+    for (int c = 0; c < N; ++c) ck[c] = p.c * softplus(dec[c]);
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+        if (k >= left) break;
+        iov y;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            const IO rc = r[k][c], ic = i[k][c], xc = x[k][c];
+            const Gate g = gate(Io<IO>::ld(&rc), Io<IO>::ld(&ic), ck[c]);
+            h[k][c] = fmaf(g.a, h[k][c], g.beta * g.si * Io<IO>::ld(&xc));
+            IO yc;
+            Io<IO>::st(&yc, h[k][c]);
+            y[c] = yc;
+        }
+        *(f32v *)(p.h + e0 + k * p.D) = h[k];
+        *(iov *)((IO *)p.y + e0 + k * p.D) = y;
+    }
 }
 
 }  // namespace
@@ -583,10 +626,24 @@ hipError_t launch_gated_bwd(const GatedArgs &a, int io, hipStream_t s) {
     return hipGetLastError();
 }
 
+namespace {
+template <typename IO, int N>
+void run_step(const GatedStepArgs &a, hipStream_t s) {
+    // four sequences a lane where that still leaves 8 waves for each of 256 compute units
+    const int64_t lanes = tiles_of(a.D, N), waves = a.n_layers * tiles_of(a.n_seq, 4) * tiles_of(lanes, 64);
+    const int per = waves >= 256 * 8 ? 4 : 1;
+    const dim3 grid((unsigned)tiles_of(lanes, 256), (unsigned)tiles_of(a.n_seq, per), (unsigned)a.n_layers);
+    if (per == 4) k_gated_step<IO, N, 4><<<grid, 256, 0, s>>>(a);
+    else k_gated_step<IO, N, 1><<<grid, 256, 0, s>>>(a);
+}
+}  // namespace
+
 hipError_t launch_gated_step(const GatedStepArgs &a, int io, hipStream_t s) {
-    const dim3 grid((unsigned)((a.D + 255) / 256), (unsigned)a.n_seq, (unsigned)a.n_layers);
-    if (io) k_gated_step<bf16_bits><<<grid, 256, 0, s>>>(a);
-    else k_gated_step<float><<<grid, 256, 0, s>>>(a);
+    // four channels a lane, 16 bytes of state at a time, where every row allows it
+    const uintptr_t any = (uintptr_t)a.x | (uintptr_t)a.r | (uintptr_t)a.i | (uintptr_t)a.y;
+    const bool wide = a.D % 4 == 0 && any % (io ? 8 : 16) == 0 && ((uintptr_t)a.h | (uintptr_t)a.decay) % 16 == 0;
+    if (io) wide ? run_step<bf16_bits, 4>(a, s) : run_step<bf16_bits, 1>(a, s);
+    else wide ? run_step<float, 4>(a, s) : run_step<float, 1>(a, s);
     return hipGetLastError();
 }
 
