@@ -1,11 +1,18 @@
 // adamw.hip -- one AdamW step over many tensors, moments in float32 or in 8-bit codes.
 //
 // The launch's tensors travel in the kernel arguments, so a step needs no copy of a table and
-// no workspace. A thread block of 256 works on kPer blocks of 256 values of one tensor, which
-// it finds by bisection over the tensors' first thread blocks (uniform, in scalar registers).
+// no workspace. A thread block works on kPer blocks of 256 values of one tensor, which it
+// finds by bisection over the tensors' first thread blocks (uniform, in scalar registers). A
+// wave has a block of 256 values, four a lane, so that a block's scale is a reduction within
+// the wave and nothing meets in LDS.
+//
 // Every operation is one IEEE float32 operation in the order of ssm_scan.h (contraction is
 // off, divisions and square roots are the correctly rounded ones): an 8-bit code flips where
 // an input of its rounding moves by an ulp, so only a fixed order gives reproducible codes.
+// With 8-bit moments an element has four square roots and a division, more vector
+// instructions than its 10 bytes leave time for. The roots of the codes go
+// through the hardware's approximation, and only where a rounding could depend on its last
+// bits are they made again exactly (code_root).
 #include "ssm_device.h"
 #include "ssm_train.h"
 
@@ -13,31 +20,114 @@ namespace ssm {
 namespace {
 
 constexpr int kBlock = SSM_ADAMW_BLOCK;
-constexpr int kPer = 8;
+constexpr int kPer = 8;      // blocks of 256 values of a thread block: two for each of its waves
+constexpr int kUnroll = kPer / 4;
+constexpr float kScaleMin = 1e-35f;
+static_assert(kBlock == 64 * 4, "a wave holds a block, four values a lane");
 
-__device__ __forceinline__ float ld_any(const void *p, int64_t e, bool bf16) {
-    return bf16 ? Io<bf16_bits>::ld((const bf16_bits *)p + e) : ((const float *)p)[e];
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef int8_t i8x4 __attribute__((ext_vector_type(4)));
+typedef uint8_t u8x4 __attribute__((ext_vector_type(4)));
+
+// The largest of non-negative values by their bits, which order like the values; a NaN's (its
+// sign cleared) lie above all of them, so it stays.
+__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// Over the wave, uniform: rotations within rows of 16 lanes, then row to row (row_ror 0x120 + n,
+// row_bcast 0x142 and 0x143), and the last lane has it.
+__device__ __forceinline__ float wave_max(uint32_t v) {
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xf, 0xf, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xf, 0xf, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xf, 0xf, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xf, 0xf, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));
+    v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)v, 63));
 }
 
-// The largest of a value over the 256 threads; a NaN anywhere gives NaN.
-__device__ __forceinline__ float block_max(float v, float *sh) {
-    for (int o = 32; o > 0; o >>= 1) {
-        const float w = __shfl_xor(v, o);
-        v = v > w || v != v ? v : w;
+// Four values from e on; n of them exist. vec: all four, aligned.
+__device__ __forceinline__ f32x4 load4(const void *p, int64_t e, bool bf16, bool vec, int n) {
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (vec) {
+        if (!bf16) return *(const f32x4 *)((const float *)p + e);
+        const u16x4 w = *(const u16x4 *)((const bf16_bits *)p + e);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = bf16_to_f32(w[c]);
+        return v;
     }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = sh[0];
-    for (int k = 1; k < 4; ++k) v = v > sh[k] || v != v ? v : sh[k];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (c < n) v[c] = bf16 ? Io<bf16_bits>::ld((const bf16_bits *)p + e + c) : ((const float *)p)[e + c];
+    return v;
+}
+__device__ __forceinline__ void store4(void *p, int64_t e, bool bf16, bool vec, int n, f32x4 v) {
+    if (vec) {
+        if (bf16) {
+            u16x4 w;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) w[c] = f32_to_bf16(v[c]);
+            *(u16x4 *)((bf16_bits *)p + e) = w;
+        } else {
+            *(f32x4 *)((float *)p + e) = v;
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (c < n) {
+            if (bf16) Io<bf16_bits>::st((bf16_bits *)p + e + c, v[c]);
+            else ((float *)p)[e + c] = v[c];
+        }
+}
+
+__device__ __forceinline__ f32x4 m_values(i8x4 q, float scale) {
+    f32x4 v;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float u = (float)q[c] * (float)(1.0 / 127.0);
+        v[c] = scale * (u * fabsf(u));
+    }
+    return v;
+}
+__device__ __forceinline__ f32x4 v_values(u8x4 q, float scale) {
+    f32x4 v;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float w = (float)q[c] * (float)(1.0 / 255.0);
+        w = w * w;
+        v[c] = scale * (w * w);
+    }
     return v;
 }
 
-constexpr float kScaleMin = 1e-35f;
+// rint(top * root(r)) for r in [0, 1], root = the square root, or with FOURTH its square
+// root. The approximate roots are within 2^-22 of the exact ones, so 255 times them within
+// 1e-4: only where that reaches a half between two integers (one wave in ten has such a
+// value) do the exact ones decide.
+template <bool FOURTH>
+__device__ __forceinline__ f32x4 code_root(f32x4 r, float top) {
+    f32x4 q;
+    bool close = false;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float u = __builtin_amdgcn_sqrtf(r[c]);
+        if (FOURTH) u = __builtin_amdgcn_sqrtf(u);
+        u *= top;
+        q[c] = rintf(u);
+        close |= fabsf(u - q[c]) > 0.4995f;
+    }
+    if (__any(close))
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float u = sqrtf(r[c]);
+            if (FOURTH) u = sqrtf(u);
+            q[c] = rintf(u * top);
+        }
+    return q;
+}
 
 template <bool CODES>
-__global__ void __launch_bounds__(kBlock) k_adamw(AdamwArgs a) {
-    __shared__ float sh[4];
+__global__ void __launch_bounds__(256) k_adamw(AdamwArgs a) {
     int lo = 0, hi = a.n_tensors;
     while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
@@ -45,70 +135,99 @@ __global__ void __launch_bounds__(kBlock) k_adamw(AdamwArgs a) {
         else hi = mid;
     }
     const AdamwTensor t = a.t[lo];
+    const bool p16 = t.io & 1, g16 = t.io & 2, vec = t.io & 4;
     const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
-    const int64_t base = (int64_t)((int)blockIdx.x - t.block0) * (kPer * kBlock);
-    for (int j = 0; j < kPer; ++j) {
-        const int64_t e = base + j * kBlock + threadIdx.x;
-        if (base + j * kBlock >= t.n) break;  // the same for every thread
-        const bool in = e < t.n;
-        const int64_t s = t.at + e;
-        float m = 0.0f, v = 0.0f;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t base = ((int64_t)((int)blockIdx.x - t.block0) * kPer + wave * kUnroll) * kBlock;
+
+    f32x4 g[kUnroll], p[kUnroll], m[kUnroll], v[kUnroll];
+    i8x4 mq[kUnroll];
+    u8x4 vq[kUnroll];
+    float ms[kUnroll], vs[kUnroll];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+        const int64_t b = base + j * kBlock, e = b + lane * 4, s = t.at + e;
+        if (b >= t.n) break;
+        const int n = (int)min((int64_t)4, t.n - e);  // of this lane's four; may be negative
+        const bool four = vec && n == 4;
+        g[j] = load4(t.g, e, g16, four, n);
+        p[j] = load4(t.p, e, p16, four, n);
         if (CODES) {
-            const float u = (float)((const int8_t *)a.m)[s] * (float)(1.0 / 127.0);
-            float w = (float)((const uint8_t *)a.v)[s] * (float)(1.0 / 255.0);
-            w = w * w;
-            m = a.m_scale[s / kBlock] * (u * fabsf(u));
-            v = a.v_scale[s / kBlock] * (w * w);
-        } else if (in) {
-            m = ((const float *)a.m)[s];
-            v = ((const float *)a.v)[s];
-        }
-        if (in) {
-            const float g = ld_any(t.g, e, t.io & 2) * gs;
-            m = m * a.beta1 + g * a.omb1;
-            v = v * a.beta2 + (g * a.omb2) * g;
-            const float denom = sqrtf(v) * a.rs2 + a.eps;
-            const float p = ld_any(t.p, e, t.io & 1) * a.keep - (m / denom) * a.rate;
-            if (t.io & 1) Io<bf16_bits>::st((bf16_bits *)t.p + e, p);
-            else ((float *)t.p)[e] = p;
+            mq[j] = *(const i8x4 *)((const int8_t *)a.m + s);
+            vq[j] = *(const u8x4 *)((const uint8_t *)a.v + s);
+            ms[j] = a.m_scale[(t.at + b) / kBlock];
+            vs[j] = a.v_scale[(t.at + b) / kBlock];
         } else {
-            m = v = 0.0f;
+            m[j] = load4(a.m, s, false, n == 4, n);
+            v[j] = load4(a.v, s, false, n == 4, n);
         }
+    }
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+        const int64_t b = base + j * kBlock, e = b + lane * 4, s = t.at + e;
+        if (b >= t.n) break;
+        const int n = (int)min((int64_t)4, t.n - e);
+        const bool four = vec && n == 4;
+        if (CODES) {
+            m[j] = m_values(mq[j], ms[j]);
+            v[j] = v_values(vq[j], vs[j]);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float gc = g[j][c] * gs;
+            const float mc = m[j][c] * a.beta1 + gc * a.omb1;
+            const float vc = v[j][c] * a.beta2 + (gc * a.omb2) * gc;
+            const float denom = sqrtf(vc) * a.rs2 + a.eps;
+            p[j][c] = p[j][c] * a.keep - (mc / denom) * a.rate;
+            m[j][c] = c < n ? mc : 0.0f;
+            v[j][c] = c < n ? vc : 0.0f;
+        }
+        store4(t.p, e, p16, four, n, p[j]);
         if (!CODES) {
-            if (in) {
-                ((float *)a.m)[s] = m;
-                ((float *)a.v)[s] = v;
-            }
+            store4(a.m, s, false, n == 4, n, m[j]);
+            store4(a.v, s, false, n == 4, n, v[j]);
             continue;
         }
-        float ms = block_max(fabsf(m), sh), vs = block_max(v, sh);
-        ms = ms < kScaleMin ? 0.0f : ms;
-        vs = vs < kScaleMin ? 0.0f : vs;
-        const float mi = ms == 0.0f ? 0.0f : 1.0f / ms, vi = vs == 0.0f ? 0.0f : 1.0f / vs;
-        const float um = fminf(rintf(sqrtf(fabsf(m) * mi) * 127.0f), 127.0f);
-        const float r = v * vi;
-        float uv = fminf(rintf(sqrtf(sqrtf(r)) * 255.0f), 255.0f);
-        if (r > 0.0f) uv = fmaxf(uv, 1.0f);
-        // a NaN leaves fminf as 127 or 255: its block's scale is NaN or infinite, and so
-        // are all its values
-        ((int8_t *)a.m)[s] = (int8_t)(m < 0.0f ? -um : m > 0.0f ? um : m != m ? 127.0f : 0.0f);
-        ((uint8_t *)a.v)[s] = (uint8_t)uv;
-        if (threadIdx.x == 0) {
-            a.m_scale[s / kBlock] = ms;
-            a.v_scale[s / kBlock] = vs;
+        float mt = wave_max(max(max(bits(m[j][0]), bits(m[j][1])), max(bits(m[j][2]), bits(m[j][3]))));
+        float vt = wave_max(max(max(bits(v[j][0]), bits(v[j][1])), max(bits(v[j][2]), bits(v[j][3]))));
+        mt = mt < kScaleMin ? 0.0f : mt;
+        vt = vt < kScaleMin ? 0.0f : vt;
+        // both reciprocals in one division, each in half of the lanes
+        const float top = lane < 32 ? mt : vt, inv = top == 0.0f ? 0.0f : 1.0f / top;
+        const float mi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), 0));
+        const float vi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), 63));
+        f32x4 mr, vr;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            mr[c] = fabsf(m[j][c]) * mi;
+            vr[c] = v[j][c] * vi;
+        }
+        const f32x4 um = code_root<false>(mr, 127.0f), uv = code_root<true>(vr, 255.0f);
+        // Codes are whole numbers up to 127 or 255 here: r <= 1 but for a rounding, which
+        // rint takes back. A block with a NaN or an infinity gets some codes: its scale makes
+        // every value of them NaN or infinite.
+        uint32_t wm = 0, wv = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            wm = __builtin_amdgcn_cvt_pk_u8_f32(copysignf(um[c], m[j][c]) + 128.0f, c, wm);
+            wv = __builtin_amdgcn_cvt_pk_u8_f32(vr[c] > 0.0f ? fmaxf(uv[c], 1.0f) : 0.0f, c, wv);
+        }
+        *(uint32_t *)((int8_t *)a.m + s) = wm ^ 0x80808080u;  // q + 128 as an unsigned byte
+        *(uint32_t *)((uint8_t *)a.v + s) = wv;
+        if (lane == 0) {
+            a.m_scale[(t.at + b) / kBlock] = mt;
+            a.v_scale[(t.at + b) / kBlock] = vt;
         }
     }
 }
 
+// Four codes of each moment a lane.
 __global__ void __launch_bounds__(256) k_adamw_values(const int8_t *m, const uint8_t *v, const float *ms,
                                                       const float *vs, float *mo, float *vo, int64_t n) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t e = (int64_t)blockIdx.x * 1024 + threadIdx.x * 4;
     if (e >= n) return;
-    const float u = (float)m[e] * (float)(1.0 / 127.0);
-    float w = (float)v[e] * (float)(1.0 / 255.0);
-    w = w * w;
-    mo[e] = ms[e / kBlock] * (u * fabsf(u));
-    vo[e] = vs[e / kBlock] * (w * w);
+    *(f32x4 *)(mo + e) = m_values(*(const i8x4 *)(m + e), ms[e / kBlock]);
+    *(f32x4 *)(vo + e) = v_values(*(const u8x4 *)(v + e), vs[e / kBlock]);
 }
 
 }  // namespace
@@ -123,7 +242,7 @@ hipError_t launch_adamw(const AdamwArgs &a, int32_t blocks, hipStream_t s) {
 
 hipError_t launch_adamw_values(const int8_t *m, const uint8_t *v, const float *ms, const float *vs, float *mo,
                                float *vo, int64_t n, hipStream_t s) {
-    k_adamw_values<<<dim3((unsigned)((n + 255) / 256)), 256, 0, s>>>(m, v, ms, vs, mo, vo, n);
+    k_adamw_values<<<dim3((unsigned)((n + 1023) / 1024)), 256, 0, s>>>(m, v, ms, vs, mo, vo, n);
     return hipGetLastError();
 }
 

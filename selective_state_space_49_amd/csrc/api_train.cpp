@@ -299,7 +299,8 @@ ssm_status ssm_adamw_step(int32_t n_tensors, void *const *params, const void *co
             t.n = n;
             t.at = at + from;
             t.block0 = (int32_t)blocks;
-            t.io = (param_io[k] == SSM_BF16 ? 1 : 0) | (grad_io[k] == SSM_BF16 ? 2 : 0);
+            t.io = (param_io[k] == SSM_BF16 ? 1 : 0) | (grad_io[k] == SSM_BF16 ? 2 : 0) |
+                   (aligned(t.p, 4 * io_bytes(param_io[k])) && aligned(t.g, 4 * io_bytes(grad_io[k])) ? 4 : 0);
             blocks += nb;
             from += n;
         }

@@ -63,7 +63,8 @@ struct AdamwTensor {
     int64_t n;       // elements
     int64_t at;      // first element of its moments
     int32_t block0;  // first thread block that works on it
-    int32_t io;      // bit 0: the parameter is bfloat16, bit 1: the gradient
+    int32_t io;      // bit 0: the parameter is bfloat16, bit 1: the gradient, bit 2: four
+                     // values of each can be read at once
 };
 struct AdamwArgs {
     AdamwTensor t[SSM_ADAMW_TENSORS];

@@ -8,6 +8,8 @@ the C entry points of ``include/ssm_scan.h`` run on torch's current stream.
 from __future__ import annotations
 
 import ctypes
+import operator
+from array import array
 from typing import Optional
 
 import torch
@@ -238,32 +240,44 @@ def ssm_adamw_state_size(sizes) -> int:
     return int(load_library().ssm_adamw_state_size(len(sizes), (ctypes.c_int64 * len(sizes))(*sizes)))
 
 
+_KINDS = {_f32: SSM_F32, torch.bfloat16: SSM_BF16}
+# A step marshals hundreds of tensors: attributes are taken by C-level maps, not in a loop.
+_at, _numel, _device = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device
+_contiguous, _dtype = torch.Tensor.is_contiguous, operator.attrgetter("dtype")
+_shape = operator.attrgetter("shape")
+
+
+def _kinds(tensors, device: int, what: str):
+    """The tensors' dtypes as ssm_dtype values, all of them contiguous on one GPU."""
+    kinds = list(map(_KINDS.get, map(_dtype, tensors)))
+    if None in kinds or not all(map(_contiguous, tensors)) or device < 0 or set(map(_device, tensors)) != {device}:
+        raise ValueError(f"{what} must be contiguous float32 or bfloat16 tensors on one GPU")
+    return kinds
+
+
 def _table(params, grads):
-    """The host arrays of ssm_adamw_step. A gradient may be None."""
-    n = len(params)
+    """The host arrays of ssm_adamw_step, and the tensors' blocks of state. A gradient may be
+    None."""
+    n, device = len(params), params[0].get_device()
     if len(grads) != n:
         raise ValueError(f"{n} parameters and {len(grads)} gradients")
-    kinds = {_f32: SSM_F32, torch.bfloat16: SSM_BF16}
-    p_at, g_at, size, p_io, g_io = [], [], [], [], []
-    dev = params[0].device if n else None
-    for k, (p, g) in enumerate(zip(params, grads)):
-        if p.dtype not in kinds or p.device != dev or not p.is_cuda or not p.is_contiguous():
-            raise ValueError(f"parameter {k} must be a contiguous float32 or bfloat16 tensor on one GPU")
-        p_at.append(p.data_ptr())
-        size.append(p.numel())
-        p_io.append(kinds[p.dtype])
-        if g is None:
-            g_at.append(None)
-            g_io.append(SSM_F32)
-            continue
-        if g.dtype not in kinds or g.device != dev or g.shape != p.shape or not g.is_contiguous():
-            raise ValueError(f"gradient {k} must be a contiguous float32 or bfloat16 tensor of its "
-                             "parameter's shape and device")
-        g_at.append(g.data_ptr())
-        g_io.append(kinds[g.dtype])
-    arr = lambda kind, v: (kind * n)(*v)  # noqa: E731
-    return (n, arr(ctypes.c_void_p, p_at), arr(ctypes.c_void_p, g_at), arr(ctypes.c_int64, size),
-            arr(ctypes.c_int32, p_io), arr(ctypes.c_int32, g_io)), sum(-(-s // ADAMW_BLOCK) for s in size)
+    p_io = _kinds(params, device, "parameters")
+    sizes = list(map(_numel, params))
+    if type(None) in set(map(type, grads)):  # `None in grads` would compare tensors
+        here = [k for k, g in enumerate(grads) if g is not None]
+        found = [grads[k] for k in here]
+        g_at, g_io = [0] * n, [SSM_F32] * n
+        if found:
+            for k, at, io in zip(here, map(_at, found), _kinds(found, device, "gradients")):
+                g_at[k], g_io[k] = at, io
+        same = all(grads[k].shape == params[k].shape for k in here)
+    else:
+        g_at, g_io = list(map(_at, grads)), _kinds(grads, device, "gradients")
+        same = list(map(_shape, grads)) == list(map(_shape, params))
+    if not same:
+        raise ValueError("a gradient must have its parameter's shape")
+    tables = (array("Q", map(_at, params)), array("Q", g_at), array("q", sizes), array("i", p_io), array("i", g_io))
+    return tables, sum([-(-k // ADAMW_BLOCK) for k in sizes])
 
 
 def ssm_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_scale=None, *, lr, beta1, beta2,
@@ -275,7 +289,7 @@ def ssm_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_sc
     lib = load_library()
     if not params:
         return
-    table, blocks = _table(params, grads)
+    tables, blocks = _table(params, grads)
     codes = avg_scale is not None
     total = (blocks * ADAMW_BLOCK,)
     _dev(exp_avg, "exp_avg", total, torch.int8 if codes else _f32)
@@ -283,8 +297,9 @@ def ssm_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_sc
     _dev(avg_scale, "avg_scale", (blocks,), _f32); _dev(avg_sq_scale, "avg_sq_scale", (blocks,), _f32)
     if grad_scale is not None and _dev(grad_scale, "grad_scale", None, _f32).numel() != 1:
         raise ValueError("grad_scale must hold one value")
-    _check(lib.ssm_adamw_step(*table, _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(avg_scale), _ptr(avg_sq_scale),
-                              _ptr(grad_scale), lr, beta1, beta2, eps, weight_decay, step, _stream(params[0])))
+    _check(lib.ssm_adamw_step(len(params), *(t.buffer_info()[0] for t in tables), _ptr(exp_avg), _ptr(exp_avg_sq),
+                              _ptr(avg_scale), _ptr(avg_sq_scale), _ptr(grad_scale), lr, beta1, beta2, eps,
+                              weight_decay, step, _stream(params[0])))
 
 
 def ssm_adamw_values(exp_avg, exp_avg_sq, avg_scale, avg_sq_scale):
