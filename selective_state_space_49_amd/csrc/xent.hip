@@ -17,6 +17,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ssm_device.h"
 #include "ssm_train.h"
@@ -73,8 +74,9 @@ __device__ __forceinline__ bf16_bits take(float &v) {
 
 // Waves stand WM x WN over a BM x BN tile; each makes TM x TN blocks of 32 x 32 with
 // v_mfma_f32_32x32x16_bf16. Operand tiles go from global memory straight to LDS, 16 bytes a
-// lane, double buffered; the 16-byte chunk c of row r lies at chunk c ^ (r & 7), so the 8
-// rows that a group of lanes reads at one k fall on 8 different chunks.
+// lane, double buffered; the 16-byte chunk c of row r lies at chunk c ^ (r / 2 & 7), so the 16
+// rows that a group of lanes reads at one k fall on the 16 chunks of LDS's 64 banks (two
+// rows of 128 bytes fill them once).
 template <int BM, int BN, int WM, int WN>
 struct Shape {
     static constexpr int kThreads = 64 * WM * WN;
@@ -110,7 +112,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
     // A load instruction of a wave fills 8 rows of 8 chunks. Rows past the operand's end read
     // its last row: their products are never used.
     uint32_t va[S::kLoadsA], vb[S::kLoadsB];
-    const uint32_t chunk = (uint32_t)((lane & 7) ^ (lane >> 3)) * 16u;
+    static_assert(S::kWaves % 2 == 0, "a wave's 8 rows all start at an even or all at an odd multiple of 8");
+    const uint32_t chunk = (uint32_t)((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) * 16u;
 #pragma unroll
     for (int j = 0; j < S::kLoadsA; ++j) {
         const int64_t r = min((int64_t)((j * S::kWaves + wave) * 8 + (lane >> 3)), p.M - 1 - m0);
@@ -121,14 +124,19 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         const int64_t r = min((int64_t)((j * S::kWaves + wave) * 8 + (lane >> 3)), p.N - 1 - n0);
         vb[j] = (uint32_t)(r * p.b.ld * 2) + chunk;
     }
+    const bf16_bits *const pa = p.a.p + m0 * p.a.ld, *const pb = p.b.p + n0 * p.b.ld;
     auto stage = [&](int kt) {
-        const int seg = kt / p.steps, k = kt - seg * p.steps;
-        // parts of (A, B) by segment: (0,0) (0,1) (1,0) (1,1) (0,2) (2,0)
-        const int pa = (0x201100 >> (4 * seg)) & 15, pb = (0x021010 >> (4 * seg)) & 15;
-        __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(p.a.p + pa * p.a.plane + m0 * p.a.ld), 0, -1, kRsrcWord3);
-        __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(p.b.p + pb * p.b.plane + n0 * p.b.ld), 0, -1, kRsrcWord3);
+        int64_t oa = 0, ob = 0;
+        int k = kt;
+        if (p.parts > 1) {
+            const int seg = kt / p.steps;
+            k -= seg * p.steps;
+            // parts of (A, B) by segment: (0,0) (0,1) (1,0) (1,1) (0,2) (2,0)
+            oa = ((0x201100 >> (4 * seg)) & 15) * p.a.plane;
+            ob = ((0x021010 >> (4 * seg)) & 15) * p.b.plane;
+        }
+        __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void *)(pa + oa), 0, -1, kRsrcWord3);
+        __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void *)(pb + ob), 0, -1, kRsrcWord3);
         SSM_LDS char *to = lds + (kt & 1) * S::kStage + wave * 1024;
 #pragma unroll
         for (int j = 0; j < S::kLoadsA; ++j)
@@ -146,7 +154,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
     uint32_t fa[4], fb[4];
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t c = (uint32_t)(((2 * ks + half) ^ (row & 7)) * 16 + row * 128);
+        const uint32_t c = (uint32_t)(((2 * ks + half) ^ (row >> 1 & 7)) * 16 + row * 128);
         fa[ks] = c + wm * S::TM * 4096;
         fb[ks] = c + wn * S::TN * 4096 + BM * kBK * 2;
     }
@@ -181,26 +189,48 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
     };
+    // One stage of k: every fragment is read while the products of the one before it run. The
+    // last one is in registers once all waves meet; then the stage's buffer is loaded again
+    // and the next stage's first fragments are read behind the last products.
+    constexpr int kFrag = S::TM + S::TN, kMul = S::TM * S::TN, kLoads = (S::kLoadsA + S::kLoadsB) / kMul;
+    static_assert(kFrag <= kMul, "a fragment read for each product");
+    auto weave = [&](auto loads) {  // one fragment read (and the loads' share) between products
+#pragma unroll
+        for (int j = 0; j < kMul; ++j) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (j < kFrag) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (loads) __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);
+        }
+    };
+    auto step = [&](int kt, auto more, auto next) {
+        fetch(1, kt, 1);
+        multiply(0);
+        fetch(0, kt, 2);
+        multiply(1);
+        fetch(1, kt, 3);
+        multiply(0);
+        weave(std::false_type{});
+        weave(std::false_type{});
+        weave(std::false_type{});
+        if (next) {
+            meet();
+            fetch(0, kt + 1, 0);
+            if (more) stage(kt + 2);
+        }
+        multiply(1);
+        if (next) weave(more);
+    };
     if (first < last) {
+        typedef std::true_type yes;
+        typedef std::false_type no;
         stage(first);
         meet();
         if (first + 1 < last) stage(first + 1);
         fetch(0, first, 0);
-        for (int kt = first; kt < last; ++kt) {
-            fetch(1, kt, 1);
-            multiply(0);
-            fetch(0, kt, 2);
-            multiply(1);
-            fetch(1, kt, 3);
-            multiply(0);
-            if (kt + 1 < last) {
-                // the last fragments of this stage are in registers once everybody is here
-                meet();
-                if (kt + 2 < last) stage(kt + 2);
-                fetch(0, kt + 1, 0);
-            }
-            multiply(1);
-        }
+        int kt = first;
+        for (; kt + 2 < last; ++kt) step(kt, yes{}, yes{});
+        if (kt + 1 < last) step(kt++, no{}, yes{});
+        step(kt, no{}, no{});
         meet();  // the epilogue may use the LDS
     }
     epilogue<S, E, BM, BN, WM, WN>(p, acc, lds, m0, n0, wm, wn, split);
