@@ -125,18 +125,16 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         vb[j] = (uint32_t)(r * p.b.ld * 2) + chunk;
     }
     const bf16_bits *const pa = p.a.p + m0 * p.a.ld, *const pb = p.b.p + n0 * p.b.ld;
+    // Stages are loaded in order: k is the next one's step within its partial product seg,
+    // whose parts of (A, B) are (0,0) (0,1) (1,0) (1,1) (0,2) (2,0).
+    int seg = first / p.steps, k = first - seg * p.steps;
+    __amdgpu_buffer_rsrc_t ra, rb;
+    auto enter = [&]() {
+        const int64_t oa = (0x201100 >> (4 * seg) & 15) * p.a.plane, ob = (0x021010 >> (4 * seg) & 15) * p.b.plane;
+        ra = __builtin_amdgcn_make_buffer_rsrc((void *)(pa + oa), 0, -1, kRsrcWord3);
+        rb = __builtin_amdgcn_make_buffer_rsrc((void *)(pb + ob), 0, -1, kRsrcWord3);
+    };
     auto stage = [&](int kt) {
-        int64_t oa = 0, ob = 0;
-        int k = kt;
-        if (p.parts > 1) {
-            const int seg = kt / p.steps;
-            k -= seg * p.steps;
-            // parts of (A, B) by segment: (0,0) (0,1) (1,0) (1,1) (0,2) (2,0)
-            oa = ((0x201100 >> (4 * seg)) & 15) * p.a.plane;
-            ob = ((0x021010 >> (4 * seg)) & 15) * p.b.plane;
-        }
-        __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void *)(pa + oa), 0, -1, kRsrcWord3);
-        __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void *)(pb + ob), 0, -1, kRsrcWord3);
         SSM_LDS char *to = lds + (kt & 1) * S::kStage + wave * 1024;
 #pragma unroll
         for (int j = 0; j < S::kLoadsA; ++j)
@@ -147,6 +145,13 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         for (int j = 0; j < S::kLoadsB; ++j)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (SSM_LDS void *)(to + j * S::kWaves * 1024), 16, vb[j],
                                                      k * (kBK * 2), 0, 0);
+        ++k;
+    };
+    auto turn = [&]() {  // to the next partial product after its last step
+        if (k < p.steps) return;
+        k = 0;
+        ++seg;
+        enter();
     };
 
     // Fragments: lane l holds row l % 32 of a block, 8 consecutive k of half l / 32.
@@ -223,12 +228,18 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
     if (first < last) {
         typedef std::true_type yes;
         typedef std::false_type no;
+        enter();
         stage(first);
+        turn();
         meet();
         if (first + 1 < last) stage(first + 1);
         fetch(0, first, 0);
         int kt = first;
-        for (; kt + 2 < last; ++kt) step(kt, yes{}, yes{});
+        while (kt + 2 < last) {
+            turn();
+            const int until = kt + min(last - 2 - kt, p.steps - k);
+            for (; kt < until; ++kt) step(kt, yes{}, yes{});
+        }
         if (kt + 1 < last) step(kt++, no{}, yes{});
         step(kt, no{}, no{});
         meet();  // the epilogue may use the LDS
@@ -237,7 +248,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
 }
 
 template <int BM, int BN, int WM, int WN, Epi E>
-__global__ void __launch_bounds__(64 * WM * WN) k_product(ProductArgs p) {
+__global__ void __launch_bounds__(64 * WM * WN, 1) k_product(ProductArgs p) {
     __shared__ __attribute__((aligned(1024))) char lds[Shape<BM, BN, WM, WN>::kLds];
     product_tile<BM, BN, WM, WN, E>(p, (SSM_LDS char *)lds);
 }
@@ -286,42 +297,39 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
         }
     }
     if constexpr (E == Epi::Dlogits) {
-#pragma unroll
-        for (int j = 0; j < S::TN; ++j) {
-            const int64_t n = nw + j * 32;
-            const bool in = n < p.N;
-            const int32_t target = in ? p.target[n] : -1;
-            const float lse = in ? p.lse[n] : 0.0f, w = in ? p.w[n] : 0.0f;
-            const int64_t t = target - p.v0 - mw;
-#pragma unroll
-            for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int at = i * 32 + 8 * (e / 4) + e % 4;
-                    const float q = e2((acc[i][j][e] - lse) * kLog2e) - (t == at ? 1.0f : 0.0f);
-                    // an ignored token and the padding are exactly 0, whatever the logit
-                    acc[i][j][e] = target == -1 || mw + at >= p.M ? 0.0f : w * q;
-                }
-        }
         // Through LDS, a token's row of kRow elements (an odd number of words, so that 8
-        // tokens at one pair of columns fall on different banks), and out both ways.
+        // tokens at one pair of columns fall on different banks), and out both ways. The
+        // later parts of a float32 operand start from the product again.
         constexpr int kWords = S::kRow / 2;
         SSM_LDS uint32_t *words = (SSM_LDS uint32_t *)lds;
         for (int part = 0; part < p.parts; ++part) {
 #pragma unroll
-            for (int j = 0; j < S::TN; ++j)
+            for (int j = 0; j < S::TN; ++j) {
+                const int64_t n = nw + j * 32;
+                const bool in = n < p.N;
+                const int32_t target = in ? p.target[n] : -1;
+                const float lse = in ? p.lse[n] : 0.0f, w = in ? p.w[n] : 0.0f;
+                const int t = (int)max((int64_t)-1, min((int64_t)S::TM * 32, target - p.v0 - mw));
+                // an ignored token and the padding are exactly 0, whatever the logit
+                const int rows = target == -1 ? 0 : (int)max((int64_t)0, min((int64_t)S::TM * 32, p.M - mw));
+                SSM_LDS uint32_t *to = words + (wn * S::TN * 32 + j * 32 + (lane & 31)) * kWords +
+                                       (wm * S::TM * 32 + 4 * half) / 2;
 #pragma unroll
                 for (int i = 0; i < S::TM; ++i)
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
-                        const int n = wn * S::TN * 32 + j * 32 + (lane & 31);
-                        const int m = wm * S::TM * 32 + 4 * half + i * 32 + 8 * (e / 4) + e % 4;
-                        float v0 = acc[i][j][e], v1 = acc[i][j][e + 1];
-                        const uint32_t lo = take(v0), hi = take(v1);
-                        acc[i][j][e] = v0;
-                        acc[i][j][e + 1] = v1;
-                        words[n * kWords + m / 2] = lo | hi << 16;
+                        const int at = i * 32 + 8 * (e / 4) + e % 4;
+                        uint32_t word = 0;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float q = e2((acc[i][j][e + k] - lse) * kLog2e) - (t == at + k ? 1.0f : 0.0f);
+                            float v = at + k < rows ? w * q : 0.0f;
+                            for (int skip = 0; skip < part; ++skip) take(v);
+                            word |= (uint32_t)take(v) << (16 * k);
+                        }
+                        to[at / 2] = word;
                     }
+            }
             __syncthreads();
             typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
             bf16_bits *g = p.g + part * p.gplane, *gt = p.gt + part * p.gtplane;
