@@ -638,17 +638,20 @@ ssm_status ssm_gated_step(float *h, const void *x_t, const void *r_t, const void
  *   loss, lse : [tokens] float32
  *   mean   : [2] float32: the mean loss over the tokens that are not ignored, and 1 over
  *            their number (both 0 where every token is ignored)
- * Products are accumulated in float32 from the operands' own bits (a float32 operand is
- * multiplied as a sum of three bfloat16 parts, which hold its 24 bits); the maximum, the
- * sum and the loss are float32.
+ * Products are accumulated in float32. Logits of bfloat16 operands are formed from their own
+ * bits; a float32 operand is multiplied as a sum of two float16 parts, which hold 22 of its
+ * 24 bits and of small values what lies above 2^-39 of the array's largest finite value. The
+ * maximum, the sum and the loss are float32.
  * ssm_xent_bwd gives the gradients of sum(dloss loss) + dmean * mean[0]:
  *     dlogit_t[v] = w_t (exp(logit_t[v] - lse_t) - [v == targets[t]]),
  *     w_t = dloss[t] + dmean / count, 0 where ignored,
  *     dhidden = dlogit weight,    dweight = dlogit^T hidden    (both of io).
  *   dloss  : [tokens] float32, NULL = 0;  dmean: one float32 on the device, NULL = 0
  *   dhidden, dweight: either may be NULL (not wanted)
- * The logits are computed again, a piece of the vocabulary at a time; with bfloat16
- * operands a piece's dlogits are rounded to bfloat16 as the operand of the two products.
+ * The logits are computed again, a piece of the vocabulary at a time, and a piece's dlogits / w
+ * are rounded as the operand of the two products: with float32 operands to two float16 parts
+ * as above, with bfloat16 ones to bfloat16, or to one float16 part where dloss gives the
+ * tokens weights of their own.
  * The workspace (ssm_xent_fwd_workspace / ssm_xent_bwd_workspace bytes, 256-byte aligned)
  * holds one piece at a time. Sums run in a fixed order. Outputs must not overlap inputs or
  * each other. Alignment: targets 8 bytes, float32 arrays 4 bytes, the others one element.

@@ -10,10 +10,19 @@
 //              dlogits = w (exp(logit - lse) - onehot) written twice, as G [token][vocab] and
 //              G^T; then dweight rows = G^T hidden (A = hidden^T, B = G^T) and
 //              dhidden += G weight (A = weight^T, B = G).
-// The matrix cores take bfloat16. A float32 operand x is split into x1 + x2 + x3, each the
-// rounded rest of the one before (3 x 8 bits hold its 24), and the product is the sum of
-// the six partial products above 2^-24: x1y1, x1y2, x2y1, x2y2, x1y3, x3y1, as a longer sum
-// over k.
+// The matrix cores take 16 bits. Logits of bfloat16 operands are products of their own bits. In
+// the gradients' products, a token's weight w stays out of G, whose values dlogits / w lie in
+// [-1, 1]: dhidden takes it as a factor of its row.
+//   bfloat16, every token of one weight (a mean loss): G, hidden^T and weight^T are bfloat16,
+//   and w is a factor of dweight. (With w in G, the large values w (p - 1) of all tokens round
+//   alike, and their error was 2.1e-3 where dweight's own rounding is 1.7e-3.)
+//   otherwise: float16 planes, scaled by a power of two that brings the largest of the array to
+//   2^14 .. 2^15, which leaves small values an absolute error of 2^-39 of the largest. dweight
+//   takes w with hidden^T. One plane each for bfloat16 operands: 11 bits. Two for float32, x =
+//   x1 + x2, the rounded value and the rounded rest, 22 bits, and a product is the sum of x1y1,
+//   x1y2, x2y1 as a longer sum over k; x2y2 is below 2^-22 of x1y1. (Three bfloat16 parts need
+//   six partial products for 24 bits.) float16 products take 9 % longer than bfloat16 ones
+//   (489 against 450 us for 8192 x 8192 x 4096: the clock falls under their power).
 #include <math.h>
 
 #include <algorithm>
@@ -26,19 +35,23 @@ namespace ssm {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 #define SSM_LDS __attribute__((address_space(3)))
 #define SSM_GLB __attribute__((address_space(1)))
 
 constexpr int kBK = 64;        // k per stage: rows of 128 bytes in LDS
-constexpr int kMaxParts = 3;   // bfloat16 planes of a float32 operand
+constexpr int kParts = 2;      // float16 planes of a float32 operand
+enum { kPeakW, kPeakH, kPeakWH, kPeakPiece };  // peaks of weight, hidden, w hidden, pieces of weight
+constexpr int kPeak = 14;      // a scaled array's largest value is in 2^kPeak .. 2^(kPeak + 1)
 constexpr uint32_t kRsrcWord3 = 0x00027000;  // raw buffer, 32-bit data
 
 // One operand: rows of ld elements, contiguous in k, 16-byte aligned, ld a multiple of 64;
 // planes `plane` elements apart.
 struct Operand {
-    const bf16_bits *p;
+    const uint16_t *p;
     int64_t ld, plane;
+    const uint32_t *peak;  // float16 planes: the largest value's bits; null: scaled by 2^kPeak
 };
 
 enum class Epi { Lse, Dlogits, Out };
@@ -47,15 +60,16 @@ struct ProductArgs {
     Operand a, b;
     int64_t M, N;           // rows of A and of B
     int32_t steps;          // ceil(K / kBK)
-    int32_t parts;          // 1, or 3: six partial products
+    int32_t terms;          // partial products: 1, or 3 of two planes each
+    int32_t planes;         // Dlogits: float16 planes of G, 0: bfloat16
     int32_t tiles_m, tiles_n, splits;
     // Lse, Dlogits: m = vocabulary row - v0, n = token
     const int32_t *target;  // [N]: vocabulary row, -1 ignored, -2 out of range
     float2 *part;           // Lse: [tiles_m * waves][N]
     float *at;              // Lse: [N] logit of the target
-    const float *lse, *w;   // Dlogits: [N]
+    const float *lse;       // Dlogits: [N]
     int64_t v0;
-    bf16_bits *g, *gt;      // Dlogits: G [N][ldg], G^T [M][ldgt], planes apart
+    uint16_t *g, *gt;       // Dlogits: G [N][ldg], G^T [M][ldgt], planes apart
     int64_t ldg, ldgt, gplane, gtplane;
     // Out: C [N][ldc] of float32 or bfloat16 at split * cstride
     void *c;
@@ -63,13 +77,26 @@ struct ProductArgs {
     bool c_bf16;
     float *sum;             // with `add`: C = sum + product
     bool add;
+    const float *row;       // Out: a factor for each n, or null
+    const float *scale;     // Out: a factor, or null
 };
 
-// The raw part of v that a bfloat16 holds, and what is left.
-__device__ __forceinline__ bf16_bits take(float &v) {
-    const bf16_bits b = f32_to_bf16(v);
-    v -= bf16_to_f32(b);
-    return b;
+// The float16 that holds the most of v, and what is left of it.
+__device__ __forceinline__ uint16_t take_f16(float &v) {
+    const _Float16 h = (_Float16)v;
+    v -= (float)h;
+    return __builtin_bit_cast(uint16_t, h);
+}
+
+// The power of two that brings the value with these bits to 2^kPeak .. 2^(kPeak + 1), as an
+// exponent.
+__device__ __forceinline__ int scale_exp(uint32_t peak) {
+    return peak == 0 ? 0 : min(kPeak + 127 - (int)(peak >> 23), 126);
+}
+__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+template <bool F16>
+__device__ __forceinline__ float unscale(const Operand &o) {
+    return !F16 ? 1.0f : o.peak ? exp2i(-scale_exp(*o.peak)) : exp2i(-kPeak);
 }
 
 // Waves stand WM x WN over a BM x BN tile; each makes TM x TN blocks of 32 x 32 with
@@ -88,11 +115,11 @@ struct Shape {
     static constexpr int kLoadsA = BM * kBK * 2 / (1024 * kWaves), kLoadsB = BN * kBK * 2 / (1024 * kWaves);
 };
 
-template <typename S, Epi E, int BM, int BN, int WM, int WN>
+template <typename S, Epi E, bool F16, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::TM][S::TN], SSM_LDS char *lds,
                                          int64_t m0, int64_t n0, int wm, int wn, int split);
 
-template <int BM, int BN, int WM, int WN, Epi E>
+template <int BM, int BN, int WM, int WN, Epi E, bool F16>
 __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char *lds) {
     using S = Shape<BM, BN, WM, WN>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -105,7 +132,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
     const int width = 8 * p.tiles_n, group = id / width, gm = min(p.tiles_m - group * 8, 8), in = id % width;
     const int64_t m0 = (int64_t)(group * 8 + in % gm) * BM, n0 = (int64_t)(in / gm) * BN;
 
-    const int total = p.steps * (p.parts == 1 ? 1 : 6);
+    const int total = p.steps * p.terms;
     const int split = blockIdx.y;
     const int first = (int)((int64_t)total * split / p.splits), last = (int)((int64_t)total * (split + 1) / p.splits);
 
@@ -124,13 +151,13 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         const int64_t r = min((int64_t)((j * S::kWaves + wave) * 8 + (lane >> 3)), p.N - 1 - n0);
         vb[j] = (uint32_t)(r * p.b.ld * 2) + chunk;
     }
-    const bf16_bits *const pa = p.a.p + m0 * p.a.ld, *const pb = p.b.p + n0 * p.b.ld;
+    const uint16_t *const pa = p.a.p + m0 * p.a.ld, *const pb = p.b.p + n0 * p.b.ld;
     // Stages are loaded in order: k is the next one's step within its partial product seg,
-    // whose parts of (A, B) are (0,0) (0,1) (1,0) (1,1) (0,2) (2,0).
+    // whose planes of (A, B) are (0,0) (0,1) (1,0).
     int seg = first / p.steps, k = first - seg * p.steps;
     __amdgpu_buffer_rsrc_t ra, rb;
     auto enter = [&]() {
-        const int64_t oa = (0x201100 >> (4 * seg) & 15) * p.a.plane, ob = (0x021010 >> (4 * seg) & 15) * p.b.plane;
+        const int64_t oa = seg == 2 ? p.a.plane : 0, ob = seg == 1 ? p.b.plane : 0;
         ra = __builtin_amdgcn_make_buffer_rsrc((void *)(pa + oa), 0, -1, kRsrcWord3);
         rb = __builtin_amdgcn_make_buffer_rsrc((void *)(pb + ob), 0, -1, kRsrcWord3);
     };
@@ -183,7 +210,12 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         for (int i = 0; i < S::TM; ++i)
 #pragma unroll
             for (int j = 0; j < S::TN; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[set][i], b[set][j], acc[i][j], 0, 0, 0);
+                if constexpr (F16)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a[set][i]),
+                                                                       __builtin_bit_cast(f16x8, b[set][j]), acc[i][j], 0,
+                                                                       0, 0);
+                else
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[set][i], b[set][j], acc[i][j], 0, 0, 0);
     };
     // Every wave's loads into the next stage and reads of this one are done.
     auto meet = [&]() {
@@ -244,22 +276,24 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         step(kt, no{}, no{});
         meet();  // the epilogue may use the LDS
     }
-    epilogue<S, E, BM, BN, WM, WN>(p, acc, lds, m0, n0, wm, wn, split);
+    epilogue<S, E, F16, BM, BN, WM, WN>(p, acc, lds, m0, n0, wm, wn, split);
 }
 
-template <int BM, int BN, int WM, int WN, Epi E>
+template <int BM, int BN, int WM, int WN, Epi E, bool F16>
 __global__ void __launch_bounds__(64 * WM * WN, 1) k_product(ProductArgs p) {
     __shared__ __attribute__((aligned(1024))) char lds[Shape<BM, BN, WM, WN>::kLds];
-    product_tile<BM, BN, WM, WN, E>(p, (SSM_LDS char *)lds);
+    product_tile<BM, BN, WM, WN, E, F16>(p, (SSM_LDS char *)lds);
 }
 
 // A block's element e of lane l is row m = 8 (e / 4) + 4 (l / 32) + e % 4, column n = l % 32.
-template <typename S, Epi E, int BM, int BN, int WM, int WN>
+template <typename S, Epi E, bool F16, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::TM][S::TN], SSM_LDS char *lds,
                                          int64_t m0, int64_t n0, int wm, int wn, int split) {
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int64_t mw = m0 + wm * S::TM * 32 + 4 * half;  // the lane's first row
     const int64_t nw = n0 + wn * S::TN * 32 + (lane & 31);
+    const float ua = unscale<F16>(p.a), ub = unscale<F16>(p.b);
+    auto value = [&](float v) { return F16 ? v * ua * ub : v; };
     if constexpr (E == Epi::Lse) {
         const int64_t slot = (m0 / BM) * WM + wm;
 #pragma unroll
@@ -270,7 +304,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
             for (int i = 0; i < S::TM; ++i)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float v = acc[i][j][e];
+                    const float v = acc[i][j][e] = value(acc[i][j][e]);
                     if (mw + i * 32 + 8 * (e / 4) + e % 4 < p.M) top = top > v || top != top ? top : v;
                 }
             const float o = __shfl_xor(top, 32);
@@ -299,16 +333,20 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
     if constexpr (E == Epi::Dlogits) {
         // Through LDS, a token's row of kRow elements (an odd number of words, so that 8
         // tokens at one pair of columns fall on different banks), and out both ways. The
-        // later parts of a float32 operand start from the product again.
+        // second plane starts from the product again. The token's weight stays out of G
+        // (dhidden takes it as a factor, dweight with hidden^T), so that its values lie in
+        // [-1, 1] and need no peak of their own.
         constexpr int kWords = S::kRow / 2;
+        const float unit = p.planes ? (float)(1 << kPeak) : 1.0f;
         SSM_LDS uint32_t *words = (SSM_LDS uint32_t *)lds;
-        for (int part = 0; part < p.parts; ++part) {
+        for (int part = 0; part < max(p.planes, 1); ++part) {
 #pragma unroll
             for (int j = 0; j < S::TN; ++j) {
                 const int64_t n = nw + j * 32;
                 const bool in = n < p.N;
                 const int32_t target = in ? p.target[n] : -1;
-                const float lse = in ? p.lse[n] : 0.0f, w = in ? p.w[n] : 0.0f;
+                const float lse = in ? p.lse[n] : 0.0f;
+                const float scale = target == -2 ? NAN : unit;  // out of range: loud
                 const int t = (int)max((int64_t)-1, min((int64_t)S::TM * 32, target - p.v0 - mw));
                 // an ignored token and the padding are exactly 0, whatever the logit
                 const int rows = target == -1 ? 0 : (int)max((int64_t)0, min((int64_t)S::TM * 32, p.M - mw));
@@ -322,17 +360,17 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
                         uint32_t word = 0;
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const float q = e2((acc[i][j][e + k] - lse) * kLog2e) - (t == at + k ? 1.0f : 0.0f);
-                            float v = at + k < rows ? w * q : 0.0f;
-                            for (int skip = 0; skip < part; ++skip) take(v);
-                            word |= (uint32_t)take(v) << (16 * k);
+                            const float q = e2((value(acc[i][j][e + k]) - lse) * kLog2e) - (t == at + k ? 1.0f : 0.0f);
+                            float v = at + k < rows ? q * scale : 0.0f;
+                            if (part > 0) take_f16(v);
+                            word |= (uint32_t)(p.planes ? take_f16(v) : f32_to_bf16(v)) << (16 * k);
                         }
                         to[at / 2] = word;
                     }
             }
             __syncthreads();
             typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-            bf16_bits *g = p.g + part * p.gplane, *gt = p.gt + part * p.gtplane;
+            uint16_t *g = p.g + part * p.gplane, *gt = p.gt + part * p.gtplane;
             for (int c = threadIdx.x; c < BN * (BM / 8); c += S::kThreads) {  // 8 columns of a token
                 const int n = c / (BM / 8), m = c % (BM / 8) * 8;
                 if (n0 + n >= p.N || m0 + m >= p.ldg) continue;
@@ -353,7 +391,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
                         lo[k] = __builtin_amdgcn_perm(v[2 * k + 1], v[2 * k], 0x05040100);
                         hi[k] = __builtin_amdgcn_perm(v[2 * k + 1], v[2 * k], 0x07060302);
                     }
-                    bf16_bits *to = gt + (m0 + m) * p.ldgt + n0 + n;
+                    uint16_t *to = gt + (m0 + m) * p.ldgt + n0 + n;
                     *(u32x4 *)to = lo;
                     if (m0 + m + 1 < p.M) *(u32x4 *)(to + p.ldgt) = hi;
                 }
@@ -361,11 +399,13 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
         }
     }
     if constexpr (E == Epi::Out) {
+        const float scale = p.scale ? *p.scale : 1.0f;
         const bool vec = p.ldc % 4 == 0 && ((uintptr_t)p.c & 15) == 0;
 #pragma unroll
         for (int j = 0; j < S::TN; ++j) {
             const int64_t n = nw + j * 32;
             if (n >= p.N) continue;
+            const float row = p.row ? p.row[n] : scale;
 #pragma unroll
             for (int i = 0; i < S::TM; ++i)
 #pragma unroll
@@ -375,7 +415,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
                     const int64_t at = n * p.ldc + m;
                     float v[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = acc[i][j][e + k];
+                    for (int k = 0; k < 4; ++k) v[k] = value(acc[i][j][e + k]) * row;
                     if (p.add)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -401,52 +441,121 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
 }
 
 // ---------------------------------------------------------------- operands
-// dst[part][r][ld] = parts of src [rows][cols], 0 past its columns.
+// dst[plane][r][ld] = src [rows][cols], 0 past its columns: a copy of bfloat16, or the scaled
+// planes of float32.
 template <typename IO>
-__global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64_t cols, bf16_bits *dst, int64_t ld,
-                                              int64_t plane, int parts) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+__global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64_t cols, const uint32_t *peak,
+                                              uint16_t *dst, int64_t ld, int64_t plane) {
+    constexpr bool F32 = sizeof(IO) == 4;
+    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
     if (c >= ld) return;
+    const float scale = F32 ? exp2i(scale_exp(*peak)) : 1.0f;
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-        float v = c < cols ? Io<IO>::ld(src + r * cols + c) : 0.0f;
-        for (int k = 0; k < parts; ++k) dst[k * plane + r * ld + c] = take(v);
+        const IO *from = src + r * cols + c;
+        uint16_t *to = dst + r * ld + c;
+        if constexpr (F32) {
+            float v0 = c < cols ? from[0] * scale : 0.0f, v1 = c + 1 < cols ? from[1] * scale : 0.0f;
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) {
+                const uint32_t lo = take_f16(v0), hi = take_f16(v1);
+                *(uint32_t *)(to + q * plane) = lo | hi << 16;
+            }
+        } else {
+            const uint32_t lo = c < cols ? from[0] : 0, hi = c + 1 < cols ? from[1] : 0;
+            *(uint32_t *)to = lo | hi << 16;
+        }
     }
 }
 
-// dst[part][c][ld] = parts of src^T, src [rows][cols]; 0 past its rows, and for the rows
-// whose target is ignored: they may hold anything, and 0 times it must not reach a sum.
+// dst[plane][c][ld] = src^T, src [rows][cols]: with a peak its scaled planes, without one a copy of
+// bfloat16; 0 past its rows, and for the rows whose target is ignored: they may hold anything,
+// and 0 times it must not reach a sum. w: a factor for each row of the planes.
 template <typename IO>
 __global__ void __launch_bounds__(256) k_pack_t(const IO *src, int64_t rows, int64_t cols, const int32_t *target,
-                                                bf16_bits *dst, int64_t ld, int64_t plane, int parts) {
+                                                const float *w, const uint32_t *peak, uint16_t *dst, int64_t ld,
+                                                int64_t plane) {
     __shared__ float sh[64][65];
     const int64_t c0 = (int64_t)blockIdx.x * 64;
     const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    const float scale = peak ? exp2i(scale_exp(*peak)) : 1.0f;
     for (int64_t r0 = (int64_t)blockIdx.y * 64; r0 < ld; r0 += (int64_t)gridDim.y * 64) {
+#pragma unroll 4
         for (int k = y; k < 64; k += 4) {
             const int64_t r = r0 + k;
             const bool in = r < rows && c0 + x < cols && !(target && target[r] == -1);
-            sh[k][x] = in ? Io<IO>::ld(src + r * cols + c0 + x) : 0.0f;
+            float v = in ? Io<IO>::ld(src + r * cols + c0 + x) : 0.0f;
+            if (w && in) v *= w[r];
+            sh[k][x] = v * scale;
         }
         __syncthreads();
-        for (int k = y; k < 64; k += 4) {
+        const int px = threadIdx.x & 31, py = threadIdx.x >> 5;  // two rows of src a lane
+#pragma unroll 4
+        for (int k = py; k < 64; k += 8) {
             if (c0 + k >= cols) break;
-            float v = sh[x][k];
-            for (int q = 0; q < parts; ++q) dst[q * plane + (c0 + k) * ld + r0 + x] = take(v);
+            float v0 = sh[2 * px][k], v1 = sh[2 * px + 1][k];
+            uint16_t *to = dst + (c0 + k) * ld + r0 + 2 * px;
+            if (sizeof(IO) == 2 && !peak) {
+                *(uint32_t *)to = f32_to_bf16(v0) | (uint32_t)f32_to_bf16(v1) << 16;
+                continue;
+            }
+#pragma unroll
+            for (int q = 0; q < (sizeof(IO) == 4 ? kParts : 1); ++q) {
+                const uint32_t lo = take_f16(v0), hi = take_f16(v1);
+                *(uint32_t *)(to + q * plane) = lo | hi << 16;
+            }
         }
         __syncthreads();
     }
 }
 
-// target[t] = the row, -1 where ignored, -2 where out of range; w[t] = the loss's weight.
+// peak = the bits of the largest finite |src| (times the row's w) over the rows whose target
+// is not ignored. An integer maximum: its order does not matter. A block of 1024 has
+// 1024 / across rows at a time, N columns a lane; few blocks, since each ends on one address.
+constexpr int kPeakThreads = 1024, kPeakBlocks = 256;
+template <typename IO, int N>
+__global__ void __launch_bounds__(kPeakThreads) k_peak(const IO *src, int64_t rows, int64_t cols, int across,
+                                                       const int32_t *target, const float *w, uint32_t *peak) {
+    typedef IO iov __attribute__((ext_vector_type(N)));
+    __shared__ uint32_t sh[kPeakThreads / 64];
+    const int down = kPeakThreads / across;
+    const int64_t c0 = (int64_t)(threadIdx.x % across) * N;
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int64_t r = (int64_t)blockIdx.x * down + threadIdx.x / across; r < rows; r += (int64_t)gridDim.x * down) {
+        if (target && target[r] == -1) continue;
+        const float f = w ? w[r] : 1.0f;
+        for (int64_t c = c0; c < cols; c += across * N) {
+            const iov v = *(const iov *)(src + r * cols + c);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const IO e = v[k];
+                const uint32_t b = __float_as_uint(Io<IO>::ld(&e) * f) & 0x7fffffffu;
+                top = b < 0x7f800000u ? max(top, b) : top;
+            }
+        }
+    }
+    for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int k = 1; k < kPeakThreads / 64; ++k) top = max(top, sh[k]);
+    if (top) atomicMax(peak, top);
+}
+
+// target[t] = the row, -1 where ignored, -2 where out of range; w[t] = the loss's weight, all[0]
+// the one that every token has without dloss; the peaks start at 0.
 __global__ void __launch_bounds__(256) k_xent_tokens(const int64_t *targets, int64_t ignore, int64_t T, int64_t V,
                                                      const float *dloss, const float *dmean, const float *mean,
-                                                     int32_t *target, float *w) {
+                                                     int32_t *target, float *w, float *all, uint32_t *peak, int64_t n_peaks) {
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    for (int64_t k = t; k < n_peaks; k += (int64_t)gridDim.x * 256) peak[k] = 0;
+    const float same = dmean ? *dmean * mean[1] : 0.0f;
+    if (t == 0 && all) *all = same;
     if (t >= T) return;
     const int64_t y = targets[t];
     const int32_t to = y == ignore ? -1 : y >= 0 && y < V ? (int32_t)y : -2;
     target[t] = to;
-    if (w) w[t] = to == -2 ? NAN : (dloss ? dloss[t] : 0.0f) + (dmean ? *dmean * mean[1] : 0.0f);
+    if (w) w[t] = to == -1 ? 0.0f : to == -2 ? NAN : (dloss ? dloss[t] : 0.0f) + same;
 }
 
 // (m, s) += (m2, s2): sums of exponentials under their maxima.
@@ -531,27 +640,30 @@ unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per)
 
 constexpr int kBig = 256, kSmall = 128;
 
-// 256 x 256 tiles where they fill the device's compute units, else 128 x 128.
+// Tiles of 256 x 256 or 128 x 128, whichever takes less time on 256 compute units by their
+// rounds: a compute unit makes a quarter of the work in about a third of the time with the
+// small tiles (measured on 8192 x 8192 x 4096: 1250 against 950 TFLOP/s), which waste less
+// at the edges and in the last round.
 struct Tiling {
     int tile, splits;
 };
 constexpr int64_t kCus = 256;
 Tiling tiling(int64_t M, int64_t N, int64_t steps, bool may_split) {
-    if ((int64_t)blocks(M, kBig) * blocks(N, kBig) >= kCus) return {kBig, 1};
-    const int64_t n = (int64_t)blocks(M, kSmall) * blocks(N, kSmall);
+    const int64_t nb = (int64_t)blocks(M, kBig) * blocks(N, kBig), n = (int64_t)blocks(M, kSmall) * blocks(N, kSmall);
+    if (3 * blocks(nb, kCus) <= blocks(n, kCus)) return {kBig, 1};
     int64_t s = 1;
     // a split keeps at least 8 steps of k, and its partial sums are written and read again
     if (may_split) s = std::max<int64_t>(1, std::min(std::min<int64_t>(2 * kCus / n, steps / 8), (int64_t)16));
     return {kSmall, (int)s};
 }
 
-template <Epi E>
+template <Epi E, bool F16>
 hipError_t product(ProductArgs p, int tile, hipStream_t s) {
     p.tiles_m = (int32_t)blocks(p.M, tile);
     p.tiles_n = (int32_t)blocks(p.N, tile);
     const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits);
-    if (tile == kBig) k_product<256, 256, 2, 4, E><<<grid, 512, 0, s>>>(p);
-    else k_product<128, 128, 2, 2, E><<<grid, 256, 0, s>>>(p);
+    if (tile == kBig) k_product<256, 256, 2, 4, E, F16><<<grid, 512, 0, s>>>(p);
+    else k_product<128, 128, 2, 2, E, F16><<<grid, 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -569,15 +681,17 @@ struct Arena {
 
 // What a call lays out in its workspace.
 struct Layout {
-    int parts;
+    int planes, terms;         // of an operand, of a product
     int64_t ldk, ldt, piece;   // padded dim, tokens; vocabulary rows of a piece
     Tiling lse, out_w, out_h;
     bool pack;                 // hidden and weight are copied: float32, or rows not in steps of 64
-    bf16_bits *hidden, *weight;
+    uint16_t *hidden, *weight;
     int32_t *target;
-    float *at, *w, *sum, *split;
+    uint32_t *peak;
+    int64_t peaks;
+    float *at, *w, *all, *sum, *split;
     float2 *part;
-    bf16_bits *ht, *wt, *g, *gt;
+    uint16_t *ht, *wt, *g, *gt;
     size_t bytes;
 };
 
@@ -588,48 +702,66 @@ constexpr int64_t kPieceValues = (int64_t)1 << 26;
 Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, char *ws) {
     Layout l{};
     Arena a{ws};
-    l.parts = io ? 1 : kMaxParts;
+    l.planes = io ? 1 : kParts;
+    l.terms = io ? 1 : 3;
     l.ldk = up(K, kBK);
     l.ldt = up(T, kBK);
     l.pack = !io || K % kBK != 0 || !aligned;
     l.target = a.take<int32_t>(T);
     // sized as if the operands had to be copied: their alignment is not known to the query
-    l.hidden = a.take<bf16_bits>(T * l.ldk * l.parts);
-    l.weight = a.take<bf16_bits>(V * l.ldk * l.parts);
+    l.hidden = a.take<uint16_t>(T * l.ldk * l.planes);
+    l.weight = a.take<uint16_t>(V * l.ldk * l.planes);
+    l.peaks = kPeakPiece;
     if (!bwd) {
-        l.lse = tiling(V, T, l.ldk / kBK, false);
+        l.lse = tiling(V, T, l.ldk / kBK * l.terms, false);
         l.part = a.take<float2>((int64_t)blocks(V, l.lse.tile) * 2 * T);
         l.at = a.take<float>(T);
     } else {
         l.piece = std::min(up(V, kBig), std::max<int64_t>(1024, kPieceValues / std::max<int64_t>(T, 1) / kBig * kBig));
         const int64_t most = std::min(V, l.piece);
-        l.out_w = tiling(K, most, l.ldt / kBK * (l.parts == 1 ? 1 : 6), true);
-        l.out_h = tiling(K, T, up(most, kBK) / kBK * (l.parts == 1 ? 1 : 6), true);
+        l.peaks += blocks(V, l.piece);
+        l.out_w = tiling(K, most, l.ldt / kBK * l.terms, true);
+        l.out_h = tiling(K, T, up(most, kBK) / kBK * l.terms, true);
         l.w = a.take<float>(T);
+        l.all = a.take<float>(1);
         l.sum = a.take<float>(V > l.piece ? T * K : 0);
-        l.ht = a.take<bf16_bits>(K * l.ldt * l.parts);
-        l.wt = a.take<bf16_bits>(K * up(most, kBK) * l.parts);
-        l.g = a.take<bf16_bits>(T * up(most, kBK) * l.parts);
-        l.gt = a.take<bf16_bits>(most * l.ldt * l.parts);
+        l.ht = a.take<uint16_t>(K * l.ldt * l.planes);
+        l.wt = a.take<uint16_t>(K * up(most, kBK) * l.planes);
+        l.g = a.take<uint16_t>(T * up(most, kBK) * l.planes);
+        l.gt = a.take<uint16_t>(most * l.ldt * l.planes);
         const int64_t sw = l.out_w.splits > 1 ? l.out_w.splits * most * K : 0;
         const int64_t sh = l.out_h.splits > 1 ? l.out_h.splits * T * K : 0;
         l.split = a.take<float>(std::max(sw, sh));
     }
+    l.peak = a.take<uint32_t>(l.peaks);
     l.bytes = a.used;
     return l;
 }
 
 template <typename IO>
-hipError_t pack(const void *src, int64_t rows, int64_t cols, bf16_bits *dst, int64_t ld, int parts, hipStream_t s) {
-    k_pack<IO><<<dim3(blocks(ld, 256), (unsigned)std::min<int64_t>(rows, 65535)), 256, 0, s>>>((const IO *)src, rows, cols,
-                                                                                               dst, ld, rows * ld, parts);
+hipError_t pack(const void *src, int64_t rows, int64_t cols, const uint32_t *peak, uint16_t *dst, int64_t ld,
+                hipStream_t s) {
+    k_pack<IO><<<dim3(blocks(ld, 512), (unsigned)std::min<int64_t>(rows, 65535)), 256, 0, s>>>((const IO *)src, rows, cols,
+                                                                                               peak, dst, ld, rows * ld);
     return hipGetLastError();
 }
 template <typename IO>
-hipError_t pack_t(const void *src, int64_t rows, int64_t cols, const int32_t *target, bf16_bits *dst, int64_t ld,
-                  int parts, hipStream_t s) {
+hipError_t pack_t(const void *src, int64_t rows, int64_t cols, const int32_t *target, const float *w,
+                  const uint32_t *peak, uint16_t *dst, int64_t ld, hipStream_t s) {
     k_pack_t<IO><<<dim3(blocks(cols, 64), (unsigned)std::min<int64_t>(ld / 64, 65535)), 256, 0, s>>>(
-        (const IO *)src, rows, cols, target, dst, ld, cols * ld, parts);
+        (const IO *)src, rows, cols, target, w, peak, dst, ld, cols * ld);
+    return hipGetLastError();
+}
+template <typename IO>
+hipError_t find_peak(const void *src, int64_t rows, int64_t cols, const int32_t *target, const float *w, uint32_t *peak,
+                     hipStream_t s) {
+    const bool wide = cols % 4 == 0 && (uintptr_t)src % (4 * sizeof(IO)) == 0;
+    const int64_t lanes = wide ? cols / 4 : cols;
+    int across = 16;
+    while (across < lanes && across < kPeakThreads) across *= 2;
+    const dim3 grid((unsigned)std::min<int64_t>(blocks(rows, kPeakThreads / across), kPeakBlocks));
+    if (wide) k_peak<IO, 4><<<grid, kPeakThreads, 0, s>>>((const IO *)src, rows, cols, across, target, w, peak);
+    else k_peak<IO, 1><<<grid, kPeakThreads, 0, s>>>((const IO *)src, rows, cols, across, target, w, peak);
     return hipGetLastError();
 }
 
@@ -644,17 +776,21 @@ bool rows_aligned(const XentArgs &a) { return ((uintptr_t)a.hidden | (uintptr_t)
 // The operands of the logits: hidden and weight as they are, or their packed copies.
 template <typename IO>
 hipError_t logits_operands(const XentArgs &a, const Layout &l, ProductArgs &p, hipStream_t s) {
-    const bf16_bits *h = (const bf16_bits *)a.hidden, *w = (const bf16_bits *)a.weight;
+    const uint16_t *h = (const uint16_t *)a.hidden, *w = (const uint16_t *)a.weight;
+    if (sizeof(IO) == 4) {
+        SSM_TRY(find_peak<IO>(a.hidden, a.T, a.K, l.target, nullptr, l.peak + kPeakH, s));
+        SSM_TRY(find_peak<IO>(a.weight, a.V, a.K, nullptr, nullptr, l.peak + kPeakW, s));
+    }
     if (l.pack) {
-        SSM_TRY(pack<IO>(a.hidden, a.T, a.K, l.hidden, l.ldk, l.parts, s));
-        SSM_TRY(pack<IO>(a.weight, a.V, a.K, l.weight, l.ldk, l.parts, s));
+        SSM_TRY(pack<IO>(a.hidden, a.T, a.K, l.peak + kPeakH, l.hidden, l.ldk, s));
+        SSM_TRY(pack<IO>(a.weight, a.V, a.K, l.peak + kPeakW, l.weight, l.ldk, s));
         h = l.hidden;
         w = l.weight;
     }
-    p.a = {w, l.ldk, a.V * l.ldk};
-    p.b = {h, l.ldk, a.T * l.ldk};
+    p.a = {w, l.ldk, a.V * l.ldk, l.peak + kPeakW};
+    p.b = {h, l.ldk, a.T * l.ldk, l.peak + kPeakH};
     p.steps = (int32_t)(l.ldk / kBK);
-    p.parts = l.parts;
+    p.terms = l.terms;
     p.splits = 1;
     p.target = l.target;
     return hipSuccess;
@@ -665,14 +801,14 @@ hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
     if (a.T > 0) {
         const Layout l = lay_out(a.T, a.K, a.V, io, false, rows_aligned(a), (char *)a.ws);
         k_xent_tokens<<<dim3(blocks(a.T, 256)), 256, 0, s>>>(a.targets, a.ignore, a.T, a.V, nullptr, nullptr, nullptr,
-                                                            l.target, nullptr);
+                                                            l.target, nullptr, nullptr, l.peak, l.peaks);
         ProductArgs p{};
         SSM_TRY(logits_operands<IO>(a, l, p, s));
         p.M = a.V;
         p.N = a.T;
         p.part = l.part;
         p.at = l.at;
-        SSM_TRY(product<Epi::Lse>(p, l.lse.tile, s));
+        SSM_TRY((product<Epi::Lse, sizeof(IO) == 4>(p, l.lse.tile, s)));
         k_xent_join<<<dim3(blocks(a.T, 16)), 256, 0, s>>>(l.part, (int64_t)blocks(a.V, l.lse.tile) * 2, l.at, l.target,
                                                          a.T, a.loss, a.lse);
     }
@@ -681,7 +817,7 @@ hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
 }
 
 // C [N][M] = (sum +) A B^T through partial sums over k where it is split.
-hipError_t product_out(ProductArgs p, Tiling t, float *split, void *dst, bool bf16, float *sum, bool add, hipStream_t s) {
+hipError_t product_out(ProductArgs p, bool f16, Tiling t, float *split, void *dst, bool bf16, float *sum, bool add, hipStream_t s) {
     p.splits = t.splits;
     p.ldc = p.M;
     p.sum = sum;
@@ -689,7 +825,7 @@ hipError_t product_out(ProductArgs p, Tiling t, float *split, void *dst, bool bf
     p.c = t.splits == 1 ? dst : split;
     p.c_bf16 = bf16 && t.splits == 1;
     p.cstride = p.M * p.N;
-    SSM_TRY(product<Epi::Out>(p, t.tile, s));
+    SSM_TRY((f16 ? product<Epi::Out, true>(p, t.tile, s) : product<Epi::Out, false>(p, t.tile, s)));
     if (t.splits > 1)
         k_join_splits<<<dim3(blocks(p.M * p.N, 256)), 256, 0, s>>>(split, t.splits, p.cstride, p.M * p.N,
                                                                   add ? sum : nullptr, dst, bf16);
@@ -704,13 +840,19 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
     }
     const Layout l = lay_out(a.T, a.K, a.V, io, true, rows_aligned(a), (char *)a.ws);
     k_xent_tokens<<<dim3(blocks(a.T, 256)), 256, 0, s>>>(a.targets, a.ignore, a.T, a.V, a.dloss, a.dmean, a.mean,
-                                                        l.target, l.w);
+                                                        l.target, l.w, l.all, l.peak, l.peaks);
     ProductArgs logits{};
     SSM_TRY(logits_operands<IO>(a, l, logits, s));
     logits.N = a.T;
     logits.lse = a.lse;
-    logits.w = l.w;
-    if (a.dweight) SSM_TRY(pack_t<IO>(a.hidden, a.T, a.K, l.target, l.ht, l.ldt, l.parts, s));
+    // one weight for all tokens: it is a factor at the end, and bfloat16 serves for the rest
+    const bool f16 = sizeof(IO) == 4 || a.dloss;
+    logits.planes = f16 ? l.planes : 0;
+    if (a.dweight) {
+        uint32_t *peak = f16 ? l.peak + kPeakWH : nullptr;
+        if (f16) SSM_TRY(find_peak<IO>(a.hidden, a.T, a.K, l.target, l.w, peak, s));
+        SSM_TRY(pack_t<IO>(a.hidden, a.T, a.K, l.target, f16 ? l.w : nullptr, peak, l.ht, l.ldt, s));
+    }
     for (int64_t v0 = 0; v0 < a.V; v0 += l.piece) {
         const int64_t nv = std::min(l.piece, a.V - v0), ldg = up(nv, kBK);
         ProductArgs p = logits;
@@ -723,29 +865,35 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
         p.ldgt = l.ldt;
         p.gplane = a.T * ldg;
         p.gtplane = nv * l.ldt;
-        const bool big = (int64_t)blocks(nv, kBig) * blocks(a.T, kBig) >= kCus;
-        SSM_TRY(product<Epi::Dlogits>(p, big ? kBig : kSmall, s));
+        SSM_TRY((product<Epi::Dlogits, sizeof(IO) == 4>(p, tiling(nv, a.T, p.steps * l.terms, false).tile, s)));
         if (a.dweight) {
             ProductArgs q{};
-            q.a = {l.ht, l.ldt, a.K * l.ldt};
-            q.b = {l.gt, l.ldt, nv * l.ldt};
+            q.a = {l.ht, l.ldt, a.K * l.ldt, l.peak + kPeakWH};
+            q.b = {l.gt, l.ldt, nv * l.ldt, nullptr};
             q.M = a.K;
             q.N = nv;
             q.steps = (int32_t)(l.ldt / kBK);
-            q.parts = l.parts;
-            SSM_TRY(product_out(q, l.out_w, l.split, (IO *)a.dweight + v0 * a.K, io, nullptr, false, s));
+            q.terms = l.terms;
+            q.scale = f16 ? nullptr : l.all;
+            SSM_TRY(product_out(q, f16, l.out_w, l.split, (IO *)a.dweight + v0 * a.K, io, nullptr, false, s));
         }
         if (a.dhidden) {
-            SSM_TRY(pack_t<IO>((const IO *)a.weight + v0 * a.K, nv, a.K, nullptr, l.wt, ldg, l.parts, s));
+            // float32 weights have their peak from the logits; a piece's is read twice here
+            // while the caches still hold it
+            const IO *piece = (const IO *)a.weight + v0 * a.K;
+            uint32_t *peak = !f16 ? nullptr : l.peak + (sizeof(IO) == 4 ? (int64_t)kPeakW : kPeakPiece + v0 / l.piece);
+            if (f16 && sizeof(IO) == 2) SSM_TRY(find_peak<IO>(piece, nv, a.K, nullptr, nullptr, peak, s));
+            SSM_TRY(pack_t<IO>(piece, nv, a.K, nullptr, nullptr, peak, l.wt, ldg, s));
             ProductArgs q{};
-            q.a = {l.wt, ldg, a.K * ldg};
-            q.b = {l.g, ldg, a.T * ldg};
+            q.a = {l.wt, ldg, a.K * ldg, peak};
+            q.b = {l.g, ldg, a.T * ldg, nullptr};
+            q.row = l.w;
             q.M = a.K;
             q.N = a.T;
             q.steps = (int32_t)(ldg / kBK);
-            q.parts = l.parts;
+            q.terms = l.terms;
             const bool end = v0 + nv == a.V;
-            SSM_TRY(product_out(q, l.out_h, l.split, end ? a.dhidden : l.sum, end && io, l.sum, v0 > 0, s));
+            SSM_TRY(product_out(q, f16, l.out_h, l.split, end ? a.dhidden : l.sum, end && io, l.sum, v0 > 0, s));
         }
     }
     return hipSuccess;

@@ -132,6 +132,7 @@ class _GatedScan(torch.autograd.Function):
         y, h_final, states = ssm_gated_fwd_save(x, r, i, decay, h0, reset, c=c)
         ctx.save_for_backward(x, r, i, decay, states, reset)
         ctx.c, ctx.has_h0 = c, h0 is not None
+        ctx.set_materialize_grads(False)
         return y, h_final
 
     @staticmethod
@@ -210,6 +211,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
         loss, lse, mean = ssm_xent_fwd(hidden, weight, targets, ignore_index=ignore_index)
         ctx.save_for_backward(hidden, weight, targets, lse, mean)
         ctx.ignore_index = ignore_index
+        ctx.set_materialize_grads(False)  # a loss that is not used has no gradient: the mean's alone is cheaper
         return mean[0], loss
 
     @staticmethod
