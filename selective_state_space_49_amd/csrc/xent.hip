@@ -469,28 +469,43 @@ __global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64
 
 // dst[plane][c][ld] = src^T, src [rows][cols]: with a peak its scaled planes, without one a copy of
 // bfloat16; 0 past its rows, and for the rows whose target is ignored: they may hold anything,
-// and 0 times it must not reach a sum. w: a factor for each row of the planes.
-template <typename IO>
+// and 0 times it must not reach a sum. w: a factor for each row of the planes. Blocks of 64 x 64 go through
+// LDS, N columns a lane on the way in (2 where rows start on pairs), two rows on the way out.
+template <typename IO, int N>
 __global__ void __launch_bounds__(256) k_pack_t(const IO *src, int64_t rows, int64_t cols, const int32_t *target,
                                                 const float *w, const uint32_t *peak, uint16_t *dst, int64_t ld,
                                                 int64_t plane) {
     __shared__ float sh[64][65];
     const int64_t c0 = (int64_t)blockIdx.x * 64;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+    typedef IO iov __attribute__((ext_vector_type(N)));
+    constexpr int kLanes = 64 / N, kRows = 256 / kLanes;
+    const int x = threadIdx.x % kLanes * N, y = threadIdx.x / kLanes;
     const float scale = peak ? exp2i(scale_exp(*peak)) : 1.0f;
     for (int64_t r0 = (int64_t)blockIdx.y * 64; r0 < ld; r0 += (int64_t)gridDim.y * 64) {
-#pragma unroll 4
-        for (int k = y; k < 64; k += 4) {
-            const int64_t r = r0 + k;
+        iov from[64 / kRows];
+#pragma unroll
+        for (int k = 0; k < 64 / kRows; ++k) {
+            const int64_t r = r0 + y + k * kRows;
             const bool in = r < rows && c0 + x < cols && !(target && target[r] == -1);
-            float v = in ? Io<IO>::ld(src + r * cols + c0 + x) : 0.0f;
-            if (w && in) v *= w[r];
-            sh[k][x] = v * scale;
+#pragma unroll
+            for (int q = 0; q < N; ++q) from[k][q] = 0;
+            if (in) from[k] = *(const iov *)(src + r * cols + c0 + x);
+        }
+#pragma unroll
+        for (int k = 0; k < 64 / kRows; ++k) {
+            const int64_t r = r0 + y + k * kRows;
+            const float f = w && r < rows ? w[r] : 1.0f;  // 0 for an ignored row
+#pragma unroll
+            for (int q = 0; q < N; ++q) {
+                const IO e = from[k][q];
+                sh[y + k * kRows][x + q] = Io<IO>::ld(&e) * f * scale;
+            }
         }
         __syncthreads();
         const int px = threadIdx.x & 31, py = threadIdx.x >> 5;  // two rows of src a lane
-#pragma unroll 4
-        for (int k = py; k < 64; k += 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int k = py + 8 * j;
             if (c0 + k >= cols) break;
             float v0 = sh[2 * px][k], v1 = sh[2 * px + 1][k];
             uint16_t *to = dst + (c0 + k) * ld + r0 + 2 * px;
@@ -748,8 +763,11 @@ hipError_t pack(const void *src, int64_t rows, int64_t cols, const uint32_t *pea
 template <typename IO>
 hipError_t pack_t(const void *src, int64_t rows, int64_t cols, const int32_t *target, const float *w,
                   const uint32_t *peak, uint16_t *dst, int64_t ld, hipStream_t s) {
-    k_pack_t<IO><<<dim3(blocks(cols, 64), (unsigned)std::min<int64_t>(ld / 64, 65535)), 256, 0, s>>>(
-        (const IO *)src, rows, cols, target, w, peak, dst, ld, cols * ld);
+    const dim3 grid(blocks(cols, 64), (unsigned)std::min<int64_t>(ld / 64, 65535));
+    if (cols % 2 == 0 && (uintptr_t)src % (2 * sizeof(IO)) == 0)
+        k_pack_t<IO, 2><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, target, w, peak, dst, ld, cols * ld);
+    else
+        k_pack_t<IO, 1><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, target, w, peak, dst, ld, cols * ld);
     return hipGetLastError();
 }
 template <typename IO>
