@@ -1,4 +1,5 @@
-"""Build libssmscan.so (HIP kernels for gfx950 + the C ABI) in the package directory.
+"""Build libssmscan.so (HIP kernels for gfx950 + the C ABI) and the _tensor_table extension in
+the package directory.
 
     python -m selective_state_space_49_amd.build
 
@@ -12,6 +13,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +21,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libssmscan.so")
+TABLE = os.path.join(HERE, "_tensor_table.so")
 OBJDIR = os.path.join(HERE, "_build")
 
 ARCH = "gfx950"
@@ -50,8 +53,27 @@ def _compile(src: str, verbose: bool, objdir: str, defines) -> str:
     return obj
 
 
+def build_table(verbose: bool = False) -> str:
+    """Compile the extension that reads lists of torch tensors (host code only)."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = TABLE + ".tmp"
+    cmd = [_hipcc(), "-O2", "-fPIC", "-std=c++17", "-shared", "-w", f"-I{root}/include",
+           f"-I{root}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           os.path.join(CSRC, "tensor_table.cpp"), "-o", tmp, f"-L{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling tensor_table.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TABLE)
+    return TABLE
+
+
 def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
-    """Compile every source and link libssmscan.so; returns the library path.
+    """Compile every source, link libssmscan.so, and build the extension beside it; returns the
+    library path.
 
     out and defines (NAME=VALUE strings, e.g. build-time tuning knobs) allow
     building variants elsewhere; the default is the package's own library.
@@ -59,7 +81,10 @@ def build(verbose: bool = False, out: str = LIB, defines=()) -> str:
     objdir = OBJDIR if out == LIB else out + ".objs"
     os.makedirs(objdir, exist_ok=True)
     with ThreadPoolExecutor(max_workers=8) as ex:
+        table = ex.submit(build_table, verbose) if out == LIB else None
         objs = list(ex.map(lambda s: _compile(s, verbose, objdir, defines), HIP_SOURCES + CPP_SOURCES))
+        if table:
+            table.result()
     tmp = out + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:

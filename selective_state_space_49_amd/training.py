@@ -8,25 +8,54 @@ the C entry points of ``include/ssm_scan.h`` run on torch's current stream.
 from __future__ import annotations
 
 import ctypes
-import operator
-from array import array
+import importlib
+import os
 from typing import Optional
 
 import torch
 
-from . import SSM_BF16, SSM_F32, _check, _dev, _io, _ptr, _stream, load_library
+from . import SSM_BF16, SSM_F32, _check, _dev, load_library
 
 # SSM_GATED_STATE_EVERY and SSM_ADAMW_BLOCK of ssm_scan.h.
 GATED_STATE_EVERY = 64
 ADAMW_BLOCK = 256
 
 _f32 = torch.float32
+_IO = {_f32: SSM_F32, torch.bfloat16: SSM_BF16}
 
 
-def _workspace(workspace, need: int, device):
-    if workspace is None and need:
+# The step of a token, or of an optimizer over a small model, is shorter than a careful
+# marshalling of its arguments, so these take the short way: one comparison where an argument
+# is right, and _dev's checks only to say what is wrong with it.
+def _need(t: Optional[torch.Tensor], name: str, shape, dtype):
+    """The address of a contiguous GPU tensor of this shape and dtype, or None."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _dev(t, name, shape, dtype)
+    return t.data_ptr()
+
+
+def _kind(t: torch.Tensor) -> int:
+    kind = _IO.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"io dtype must be float32 or bfloat16, got {t.dtype}")
+    return kind
+
+
+def _stream(t: torch.Tensor) -> int:
+    """torch's current stream on the tensor's GPU, as a hipStream_t."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _scratch(workspace, need: int, device):
+    """The caller's workspace or a new one (which must live until the call is enqueued), its
+    address and its bytes."""
+    if workspace is None:
+        if not need:
+            return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # ------------------------------------------------------------------ gated linear recurrence
@@ -49,7 +78,7 @@ def _states_rows(L: int) -> int:
 def _reset(reset: Optional[torch.Tensor], shape):
     if reset is not None and reset.dtype not in (torch.bool, torch.uint8):
         raise TypeError(f"reset: expected bool or uint8, got {reset.dtype}")
-    return _dev(reset, "reset", shape)
+    return None if reset is None else _need(reset, "reset", shape, reset.dtype)
 
 
 def ssm_gated_fwd(x, r, i, decay, h0=None, reset=None, *, c=8.0, y=None, h_final=None, states=None,
@@ -58,21 +87,19 @@ def ssm_gated_fwd(x, r, i, decay, h0=None, reset=None, *, c=8.0, y=None, h_final
     a_t = exp(-c softplus(decay) sigmoid(r_t)): y [b, L, D] and h_final [b, D] float32.
     reset [b, L] (bool): steps that start a document. states: see ssm_gated_fwd_save."""
     lib = load_library()
-    b, L, D = x.shape
-    _dev(x, "x"); _dev(r, "r", (b, L, D)); _dev(i, "i", (b, L, D))
-    _dev(decay, "decay", (D,), _f32); _dev(h0, "h0", (b, D), _f32); _reset(reset, (b, L))
-    io = _io(x, r, i)
+    shape, io, kind = x.shape, x.dtype, _kind(x)
+    b, L, D = shape
     if y is None:
         y = torch.empty_like(x)
-    _dev(y, "y", (b, L, D), x.dtype)
     if h_final is None and want_h_final:
         h_final = torch.empty((b, D), dtype=_f32, device=x.device)
-    _dev(h_final, "h_final", (b, D), _f32)
-    _dev(states, "states", (b, _states_rows(L), D), _f32)
-    workspace, ws_bytes = _workspace(workspace, lib.ssm_gated_fwd_workspace(b, L, D), x.device)
-    _check(lib.ssm_gated_fwd(_ptr(x), _ptr(r), _ptr(i), _ptr(decay), _ptr(h0), _ptr(reset), c, _ptr(y),
-                             _ptr(h_final), _ptr(states), b, L, D, io, _ptr(workspace), ws_bytes,
-                             _stream(x)))
+    ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_gated_fwd_workspace(b, L, D), x.device)
+    _check(lib.ssm_gated_fwd(_need(x, "x", shape, io), _need(r, "r", shape, io), _need(i, "i", shape, io),
+                             _need(decay, "decay", (D,), _f32), _need(h0, "h0", (b, D), _f32),
+                             _reset(reset, (b, L)), c, _need(y, "y", shape, io),
+                             _need(h_final, "h_final", (b, D), _f32),
+                             _need(states, "states", (b, _states_rows(L), D), _f32), b, L, D, kind, ws_at,
+                             ws_bytes, _stream(x)))
     return y, h_final
 
 
@@ -93,34 +120,32 @@ def ssm_gated_bwd(x, r, i, decay, states, reset=None, *, dy, dh_final=None, c=8.
     """Gradients of sum(dy y) + sum(dh_final h_final): a dict of dx, dr, di (x's dtype),
     ddecay [D] and dh0 [b, D] (float32; None unless want_dh0)."""
     lib = load_library()
-    b, L, D = x.shape
-    _dev(x, "x"); _dev(r, "r", (b, L, D)); _dev(i, "i", (b, L, D)); _dev(dy, "dy", (b, L, D))
-    _dev(decay, "decay", (D,), _f32); _dev(states, "states", (b, _states_rows(L), D), _f32)
-    _reset(reset, (b, L)); _dev(dh_final, "dh_final", (b, D), _f32)
-    io = _io(x, r, i, dy)
-    dx, dr, di = (torch.empty_like(x) for _ in range(3))
+    shape, io, kind = x.shape, x.dtype, _kind(x)
+    b, L, D = shape
+    dx, dr, di = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
     ddecay = torch.empty_like(decay)
     dh0 = torch.empty((b, D), dtype=_f32, device=x.device) if want_dh0 else None
-    workspace, ws_bytes = _workspace(workspace, lib.ssm_gated_bwd_workspace(b, L, D), x.device)
-    _check(lib.ssm_gated_bwd(_ptr(x), _ptr(r), _ptr(i), _ptr(decay), _ptr(states), _ptr(reset), c, _ptr(dy),
-                             _ptr(dh_final), _ptr(dx), _ptr(dr), _ptr(di), _ptr(ddecay), _ptr(dh0), b, L, D,
-                             io, _ptr(workspace), ws_bytes, _stream(x)))
+    ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_gated_bwd_workspace(b, L, D), x.device)
+    _check(lib.ssm_gated_bwd(_need(x, "x", shape, io), _need(r, "r", shape, io), _need(i, "i", shape, io),
+                             _need(decay, "decay", (D,), _f32),
+                             _need(states, "states", (b, _states_rows(L), D), _f32), _reset(reset, (b, L)), c,
+                             _need(dy, "dy", shape, io), _need(dh_final, "dh_final", (b, D), _f32),
+                             dx.data_ptr(), dr.data_ptr(), di.data_ptr(), ddecay.data_ptr(),
+                             None if dh0 is None else dh0.data_ptr(), b, L, D, kind, ws_at, ws_bytes, _stream(x)))
     return {"dx": dx, "dr": dr, "di": di, "ddecay": ddecay, "dh0": dh0}
 
 
 def ssm_gated_step(h, x_t, r_t, i_t, decay, *, c=8.0, y_t=None):
     """One token for every (layer, sequence): h [Ln, S, D] float32 in place; x_t, r_t, i_t
     [Ln, S, D]; decay [Ln, D]. Returns y_t."""
-    lib = load_library()
-    Ln, S, D = x_t.shape
-    _dev(h, "h", (Ln, S, D), _f32); _dev(decay, "decay", (Ln, D), _f32)
-    _dev(x_t, "x_t"); _dev(r_t, "r_t", (Ln, S, D)); _dev(i_t, "i_t", (Ln, S, D))
-    io = _io(x_t, r_t, i_t)
+    shape, io, kind = x_t.shape, x_t.dtype, _kind(x_t)
+    Ln, S, D = shape
     if y_t is None:
         y_t = torch.empty_like(x_t)
-    _dev(y_t, "y_t", (Ln, S, D), x_t.dtype)
-    _check(lib.ssm_gated_step(_ptr(h), _ptr(x_t), _ptr(r_t), _ptr(i_t), _ptr(decay), c, _ptr(y_t), Ln, S, D,
-                              io, _stream(x_t)))
+    _check(load_library().ssm_gated_step(
+        _need(h, "h", shape, _f32), _need(x_t, "x_t", shape, io), _need(r_t, "r_t", shape, io),
+        _need(i_t, "i_t", shape, io), _need(decay, "decay", (Ln, D), _f32), c, _need(y_t, "y_t", shape, io), Ln, S,
+        D, kind, _stream(x_t)))
     return y_t
 
 
@@ -162,10 +187,17 @@ def ssm_xent_bwd_workspace(tokens, dim, vocab, io=SSM_BF16) -> int:
 
 
 def _head(hidden, weight, targets):
-    T, K = hidden.shape
-    V = weight.shape[0]
-    _dev(hidden, "hidden"); _dev(weight, "weight", (V, K)); _dev(targets, "targets", (T,), torch.int64)
-    return T, K, V, _io(hidden, weight)
+    """The sizes, the io type, and the addresses of a head's inputs."""
+    (T, K), V, io = hidden.shape, weight.shape[0], hidden.dtype
+    return T, K, V, _kind(hidden), (_need(hidden, "hidden", (T, K), io), _need(weight, "weight", (V, K), io),
+                                    _need(targets, "targets", (T,), torch.int64))
+
+
+def _one(t: Optional[torch.Tensor], name: str):
+    """The address of one float32 value on the GPU, or None."""
+    if t is not None and t.numel() != 1:
+        raise ValueError(f"{name} must hold one value")
+    return None if t is None else _need(t, name, t.shape, _f32)
 
 
 def ssm_xent_fwd(hidden, weight, targets, *, ignore_index=-100, loss=None, lse=None, mean=None,
@@ -174,14 +206,14 @@ def ssm_xent_fwd(hidden, weight, targets, *, ignore_index=-100, loss=None, lse=N
     the logits in memory: loss [T], lse [T] and mean [2] (the mean over the tokens that are
     not ignored, and 1 over their number), all float32."""
     lib = load_library()
-    T, K, V, io = _head(hidden, weight, targets)
+    T, K, V, kind, inputs = _head(hidden, weight, targets)
     dev = hidden.device
-    loss = torch.empty(T, dtype=_f32, device=dev) if loss is None else _dev(loss, "loss", (T,), _f32)
-    lse = torch.empty(T, dtype=_f32, device=dev) if lse is None else _dev(lse, "lse", (T,), _f32)
-    mean = torch.empty(2, dtype=_f32, device=dev) if mean is None else _dev(mean, "mean", (2,), _f32)
-    workspace, ws_bytes = _workspace(workspace, lib.ssm_xent_fwd_workspace(T, K, V, io), dev)
-    _check(lib.ssm_xent_fwd(_ptr(hidden), _ptr(weight), _ptr(targets), ignore_index, _ptr(loss), _ptr(lse),
-                            _ptr(mean), T, K, V, io, _ptr(workspace), ws_bytes, _stream(hidden)))
+    loss = torch.empty(T, dtype=_f32, device=dev) if loss is None else loss
+    lse = torch.empty(T, dtype=_f32, device=dev) if lse is None else lse
+    mean = torch.empty(2, dtype=_f32, device=dev) if mean is None else mean
+    ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_xent_fwd_workspace(T, K, V, kind), dev)
+    _check(lib.ssm_xent_fwd(*inputs, ignore_index, _need(loss, "loss", (T,), _f32), _need(lse, "lse", (T,), _f32),
+                            _need(mean, "mean", (2,), _f32), T, K, V, kind, ws_at, ws_bytes, _stream(hidden)))
     return loss, lse, mean
 
 
@@ -190,16 +222,15 @@ def ssm_xent_bwd(hidden, weight, targets, lse, mean, *, dloss=None, dmean=None, 
     """Gradients of sum(dloss loss) + dmean mean[0] (dloss [T] float32, dmean one float32 on
     the GPU; None = 0): dhidden [T, K] and dweight [V, K] (None where not wanted)."""
     lib = load_library()
-    T, K, V, io = _head(hidden, weight, targets)
-    _dev(lse, "lse", (T,), _f32); _dev(mean, "mean", (2,), _f32); _dev(dloss, "dloss", (T,), _f32)
-    if dmean is not None and (_dev(dmean, "dmean", None, _f32)).numel() != 1:
-        raise ValueError("dmean must hold one value")
+    T, K, V, kind, inputs = _head(hidden, weight, targets)
     dhidden = torch.empty_like(hidden) if want_dhidden else None
     dweight = torch.empty_like(weight) if want_dweight else None
-    workspace, ws_bytes = _workspace(workspace, lib.ssm_xent_bwd_workspace(T, K, V, io), hidden.device)
-    _check(lib.ssm_xent_bwd(_ptr(hidden), _ptr(weight), _ptr(targets), ignore_index, _ptr(lse), _ptr(mean),
-                            _ptr(dloss), _ptr(dmean), _ptr(dhidden), _ptr(dweight), T, K, V, io,
-                            _ptr(workspace), ws_bytes, _stream(hidden)))
+    ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_xent_bwd_workspace(T, K, V, kind), hidden.device)
+    _check(lib.ssm_xent_bwd(*inputs, ignore_index, _need(lse, "lse", (T,), _f32), _need(mean, "mean", (2,), _f32),
+                            _need(dloss, "dloss", (T,), _f32), _one(dmean, "dmean"),
+                            None if dhidden is None else dhidden.data_ptr(),
+                            None if dweight is None else dweight.data_ptr(), T, K, V, kind, ws_at, ws_bytes,
+                            _stream(hidden)))
     return dhidden, dweight
 
 
@@ -236,50 +267,24 @@ def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, reductio
 
 
 # ------------------------------------------------------------------ AdamW
+_table_loaded = None
+
+
+def _table_module():
+    """The extension that reads lists of tensors (csrc/tensor_table.cpp)."""
+    global _table_loaded
+    if _table_loaded is None:
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_tensor_table.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m selective_state_space_49_amd.build`")
+        _table_loaded = importlib.import_module("._tensor_table", __package__)
+    return _table_loaded
+
+
 def ssm_adamw_state_size(sizes) -> int:
     """Elements of the moments' arrays for tensors of these sizes."""
     sizes = list(sizes)
     return int(load_library().ssm_adamw_state_size(len(sizes), (ctypes.c_int64 * len(sizes))(*sizes)))
-
-
-_KINDS = {_f32: SSM_F32, torch.bfloat16: SSM_BF16}
-# A step marshals hundreds of tensors: attributes are taken by C-level maps, not in a loop.
-_at, _numel, _device = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device
-_contiguous, _dtype = torch.Tensor.is_contiguous, operator.attrgetter("dtype")
-_shape = operator.attrgetter("shape")
-
-
-def _kinds(tensors, device: int, what: str):
-    """The tensors' dtypes as ssm_dtype values, all of them contiguous on one GPU."""
-    kinds = list(map(_KINDS.get, map(_dtype, tensors)))
-    if None in kinds or not all(map(_contiguous, tensors)) or device < 0 or set(map(_device, tensors)) != {device}:
-        raise ValueError(f"{what} must be contiguous float32 or bfloat16 tensors on one GPU")
-    return kinds
-
-
-def _table(params, grads):
-    """The host arrays of ssm_adamw_step, and the tensors' blocks of state. A gradient may be
-    None."""
-    n, device = len(params), params[0].get_device()
-    if len(grads) != n:
-        raise ValueError(f"{n} parameters and {len(grads)} gradients")
-    p_io = _kinds(params, device, "parameters")
-    sizes = list(map(_numel, params))
-    if type(None) in set(map(type, grads)):  # `None in grads` would compare tensors
-        here = [k for k, g in enumerate(grads) if g is not None]
-        found = [grads[k] for k in here]
-        g_at, g_io = [0] * n, [SSM_F32] * n
-        if found:
-            for k, at, io in zip(here, map(_at, found), _kinds(found, device, "gradients")):
-                g_at[k], g_io[k] = at, io
-        same = all(grads[k].shape == params[k].shape for k in here)
-    else:
-        g_at, g_io = list(map(_at, grads)), _kinds(grads, device, "gradients")
-        same = list(map(_shape, grads)) == list(map(_shape, params))
-    if not same:
-        raise ValueError("a gradient must have its parameter's shape")
-    tables = (array("Q", map(_at, params)), array("Q", g_at), array("q", sizes), array("i", p_io), array("i", g_io))
-    return tables, sum([-(-k // ADAMW_BLOCK) for k in sizes])
 
 
 def ssm_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_scale=None, *, lr, beta1, beta2,
@@ -288,32 +293,27 @@ def ssm_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_sc
     all of them in one array each, a tensor starting at a multiple of 256 elements
     (ssm_adamw_state_size): float32, or, with avg_scale and avg_sq_scale (float32, one for
     256 elements), int8 and uint8 codes. grad_scale: one float32 on the GPU."""
-    lib = load_library()
     if not params:
         return
-    tables, blocks = _table(params, grads)
-    codes = avg_scale is not None
-    total = (blocks * ADAMW_BLOCK,)
-    _dev(exp_avg, "exp_avg", total, torch.int8 if codes else _f32)
-    _dev(exp_avg_sq, "exp_avg_sq", total, torch.uint8 if codes else _f32)
-    _dev(avg_scale, "avg_scale", (blocks,), _f32); _dev(avg_sq_scale, "avg_sq_scale", (blocks,), _f32)
-    if grad_scale is not None and _dev(grad_scale, "grad_scale", None, _f32).numel() != 1:
-        raise ValueError("grad_scale must hold one value")
-    _check(lib.ssm_adamw_step(len(params), *(t.buffer_info()[0] for t in tables), _ptr(exp_avg), _ptr(exp_avg_sq),
-                              _ptr(avg_scale), _ptr(avg_sq_scale), _ptr(grad_scale), lr, beta1, beta2, eps,
-                              weight_decay, step, _stream(params[0])))
+    table, at, blocks = _table_module().table(list(params), list(grads), ADAMW_BLOCK)  # at: where table's bytes are
+    n, total, codes = len(params), (blocks * ADAMW_BLOCK,), avg_scale is not None
+    _check(load_library().ssm_adamw_step(
+        n, at, at + 8 * n, at + 16 * n, at + 24 * n, at + 28 * n,
+        _need(exp_avg, "exp_avg", total, torch.int8 if codes else _f32),
+        _need(exp_avg_sq, "exp_avg_sq", total, torch.uint8 if codes else _f32),
+        _need(avg_scale, "avg_scale", (blocks,), _f32), _need(avg_sq_scale, "avg_sq_scale", (blocks,), _f32),
+        _one(grad_scale, "grad_scale"), lr, beta1, beta2, eps, weight_decay, step, _stream(params[0])))
 
 
 def ssm_adamw_values(exp_avg, exp_avg_sq, avg_scale, avg_sq_scale):
     """The float32 values that 8-bit moments stand for."""
-    lib = load_library()
     n = exp_avg.numel()
-    _dev(exp_avg, "exp_avg", (n,), torch.int8); _dev(exp_avg_sq, "exp_avg_sq", (n,), torch.uint8)
-    _dev(avg_scale, "avg_scale", (n // ADAMW_BLOCK,), _f32)
-    _dev(avg_sq_scale, "avg_sq_scale", (n // ADAMW_BLOCK,), _f32)
+    scales = (n // ADAMW_BLOCK,)
     m, v = (torch.empty(n, dtype=_f32, device=exp_avg.device) for _ in range(2))
-    _check(lib.ssm_adamw_values(_ptr(exp_avg), _ptr(exp_avg_sq), _ptr(avg_scale), _ptr(avg_sq_scale), _ptr(m),
-                                _ptr(v), n, _stream(exp_avg)))
+    _check(load_library().ssm_adamw_values(
+        _need(exp_avg, "exp_avg", (n,), torch.int8), _need(exp_avg_sq, "exp_avg_sq", (n,), torch.uint8),
+        _need(avg_scale, "avg_scale", scales, _f32), _need(avg_sq_scale, "avg_sq_scale", scales, _f32),
+        m.data_ptr(), v.data_ptr(), n, _stream(exp_avg)))
     return m, v
 
 
