@@ -9,10 +9,12 @@
 // Every operation is one IEEE float32 operation in the order of ssm_scan.h (contraction is
 // off, divisions and square roots are the correctly rounded ones): an 8-bit code flips where
 // an input of its rounding moves by an ulp, so only a fixed order gives reproducible codes.
-// With 8-bit moments an element has four square roots and a division, more vector
-// instructions than its 10 bytes leave time for. The roots of the codes go
-// through the hardware's approximation, and only where a rounding could depend on its last
-// bits are they made again exactly (code_root).
+// With 8-bit moments an element has four square roots and a division, and the kernel is bound
+// by its vector instructions (112 an element in the compiler's general forms, at 99 % of the
+// issue slots). The roots of the codes go through the hardware's approximation, and only
+// where a rounding could depend on its last bits are they made again exactly (m_code, v_code);
+// the root and the division of the update have short exact forms for the range in which all
+// but exotic values lie (sqrt_in_range, div_in_range), and the general ones outside.
 #include "ssm_device.h"
 #include "ssm_train.h"
 
@@ -100,29 +102,63 @@ __device__ __forceinline__ f32x4 v_values(u8x4 q, float scale) {
     return v;
 }
 
-// rint(top * root(r)) for r in [0, 1], root = the square root, or with FOURTH its square
-// root. The approximate roots are within 2^-22 of the exact ones, so 255 times them within
-// 1e-4: only where that reaches a half between two integers (one wave in ten has such a
-// value) do the exact ones decide.
-template <bool FOURTH>
-__device__ __forceinline__ f32x4 code_root(f32x4 r, float top) {
+// Correctly rounded sqrt(v) and m / d without the general forms' scaling and special cases:
+// v is 0 or in [2^-96, 2^96], |m| is 0 or in [2^-60, 2^60], d in [2^-60, 2^60] (in_range).
+// Each ends with the exact remainder of a value that is right to within an ulp, times an
+// approximate root or reciprocal.
+__device__ __forceinline__ float sqrt_in_range(float v) {
+    const float y = __builtin_amdgcn_rsqf(fmaxf(v, 0x1p-100f));
+    float g = v * y, h = 0.5f * y;
+    const float r = fmaf(-g, h, 0.5f);
+    g = fmaf(g, r, g);
+    h = fmaf(h, r, h);
+    return fmaf(fmaf(-g, g, v), h, g);
+}
+__device__ __forceinline__ float div_in_range(float m, float d) {
+    float y = rcp(d);
+    y = fmaf(fmaf(-d, y, 1.0f), y, y);
+    float q = m * y;
+    q = fmaf(fmaf(-d, q, m), y, q);
+    return fmaf(fmaf(-d, q, m), y, q);
+}
+// Whether all four values are 0 or at least `least`, by their bits: 0 - 1 is the largest.
+__device__ __forceinline__ bool none_below(f32x4 v, float least) {
+    uint32_t low = 0xffffffffu;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) low = min(low, bits(v[c]) - 1u);
+    return low >= __float_as_uint(least) - 1u;
+}
+
+// rint(127 sqrt(r)), r in [0, 1], from an approximate root: it is within 2^-23 of the exact
+// one, so u within 4e-5 of the u that the exact root gives. Only where that can reach a half
+// between two integers (one wave in twenty has such a value) does the exact one decide.
+__device__ __forceinline__ f32x4 m_code(f32x4 r) {
     f32x4 q;
-    bool close = false;
+    float far = 0.0f;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        float u = __builtin_amdgcn_sqrtf(r[c]);
-        if (FOURTH) u = __builtin_amdgcn_sqrtf(u);
-        u *= top;
+        const float u = __builtin_amdgcn_sqrtf(r[c]) * 127.0f;
         q[c] = rintf(u);
-        close |= fabsf(u - q[c]) > 0.4995f;
+        far = fmaxf(far, fabsf(u - q[c]));
     }
-    if (__any(close))
+    if (__any(far > 0.4999f))
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float u = sqrtf(r[c]);
-            if (FOURTH) u = sqrtf(u);
-            q[c] = rintf(u * top);
-        }
+        for (int c = 0; c < 4; ++c) q[c] = rintf(sqrtf(r[c]) * 127.0f);
+    return q;
+}
+// rint(255 sqrt(sqrt(r))): the approximation is within 1e-4 (one wave in ten).
+__device__ __forceinline__ f32x4 v_code(f32x4 r) {
+    f32x4 q;
+    float far = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float u = __builtin_amdgcn_sqrtf(__builtin_amdgcn_sqrtf(r[c])) * 255.0f;
+        q[c] = rintf(u);
+        far = fmaxf(far, fabsf(u - q[c]));
+    }
+    if (__any(far > 0.4998f))
+#pragma unroll
+        for (int c = 0; c < 4; ++c) q[c] = rintf(sqrtf(sqrtf(r[c])) * 255.0f);
     return q;
 }
 
@@ -175,12 +211,30 @@ __global__ void __launch_bounds__(256) k_adamw(AdamwArgs a) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const float gc = g[j][c] * gs;
-            const float mc = m[j][c] * a.beta1 + gc * a.omb1;
-            const float vc = v[j][c] * a.beta2 + (gc * a.omb2) * gc;
-            const float denom = sqrtf(vc) * a.rs2 + a.eps;
-            p[j][c] = p[j][c] * a.keep - (mc / denom) * a.rate;
-            m[j][c] = c < n ? mc : 0.0f;
-            v[j][c] = c < n ? vc : 0.0f;
+            m[j][c] = m[j][c] * a.beta1 + gc * a.omb1;
+            v[j][c] = v[j][c] * a.beta2 + (gc * a.omb2) * gc;
+        }
+        if (b + kBlock > t.n)  // the tensor's last block, the same for every lane
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                m[j][c] = c < n ? m[j][c] : 0.0f;
+                v[j][c] = c < n ? v[j][c] : 0.0f;
+            }
+        float mt = wave_max(max(max(bits(m[j][0]), bits(m[j][1])), max(bits(m[j][2]), bits(m[j][3]))));
+        float vt = wave_max(max(max(bits(v[j][0]), bits(v[j][1])), max(bits(v[j][2]), bits(v[j][3]))));
+        const bool in_range = a.plain && mt <= 0x1p60f && vt <= 0x1p96f;  // false for a NaN
+        if (in_range && __all(none_below(m[j], 0x1p-60f) && none_below(v[j], 0x1p-96f))) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float denom = sqrt_in_range(v[j][c]) * a.rs2 + a.eps;
+                p[j][c] = p[j][c] * a.keep - div_in_range(m[j][c], denom) * a.rate;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float denom = sqrtf(v[j][c]) * a.rs2 + a.eps;
+                p[j][c] = p[j][c] * a.keep - (m[j][c] / denom) * a.rate;
+            }
         }
         store4(t.p, e, p16, four, n, p[j]);
         if (!CODES) {
@@ -188,8 +242,6 @@ __global__ void __launch_bounds__(256) k_adamw(AdamwArgs a) {
             store4(a.v, s, false, n == 4, n, v[j]);
             continue;
         }
-        float mt = wave_max(max(max(bits(m[j][0]), bits(m[j][1])), max(bits(m[j][2]), bits(m[j][3]))));
-        float vt = wave_max(max(max(bits(v[j][0]), bits(v[j][1])), max(bits(v[j][2]), bits(v[j][3]))));
         mt = mt < kScaleMin ? 0.0f : mt;
         vt = vt < kScaleMin ? 0.0f : vt;
         // both reciprocals in one division, each in half of the lanes
@@ -202,7 +254,7 @@ __global__ void __launch_bounds__(256) k_adamw(AdamwArgs a) {
             mr[c] = fabsf(m[j][c]) * mi;
             vr[c] = v[j][c] * vi;
         }
-        const f32x4 um = code_root<false>(mr, 127.0f), uv = code_root<true>(vr, 255.0f);
+        const f32x4 um = m_code(mr), uv = v_code(vr);
         // Codes are whole numbers up to 127 or 255 here: r <= 1 but for a rounding, which
         // rint takes back. A block with a NaN or an infinity gets some codes: its scale makes
         // every value of them NaN or infinite.

@@ -278,6 +278,7 @@ ssm_status ssm_adamw_step(int32_t n_tensors, void *const *params, const void *co
     a.beta2 = (float)beta2; a.omb2 = (float)(1.0 - beta2);
     a.rs2 = (float)(1.0 / sqrt(1.0 - pow(beta2, (double)step)));
     a.eps = (float)eps;
+    a.plain = a.eps >= 0x1p-60f && a.eps <= 1.0f && a.rs2 <= 0x1p10f;
     a.keep = (float)(1.0 - lr * weight_decay);
     a.rate = (float)(lr / (1.0 - pow(beta1, (double)step)));
     int64_t at = 0, blocks = 0;

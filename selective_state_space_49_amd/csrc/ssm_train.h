@@ -73,6 +73,7 @@ struct AdamwArgs {
     float *m_scale, *v_scale;  // null: moments in float32
     const float *grad_scale;
     float beta1, omb1, beta2, omb2, rs2, eps, keep, rate;  // in the order of the formula
+    bool plain;                // eps >= 2^-60, rs2 <= 2^10: no extreme denominators
 };
 int32_t adamw_blocks(int64_t n, bool codes);  // thread blocks of a tensor of n elements
 hipError_t launch_adamw(const AdamwArgs &a, int32_t blocks, hipStream_t s);
