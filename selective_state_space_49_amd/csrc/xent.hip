@@ -64,7 +64,8 @@ struct ProductArgs {
     int32_t planes;         // Dlogits: float16 planes of G, 0: bfloat16
     int32_t tiles_m, tiles_n, splits;
     // Lse, Dlogits: m = vocabulary row - v0, n = token
-    const int32_t *target;  // [N]: vocabulary row, -1 ignored, -2 out of range
+    const int64_t *targets; // Lse: [N]
+    const int32_t *target;  // Dlogits: [N]: vocabulary row, -1 ignored, -2 out of range
     float2 *part;           // Lse: [tiles_m * waves][N]
     float *at;              // Lse: [N] logit of the target
     const float *lse;       // Dlogits: [N]
@@ -218,10 +219,11 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[set][i], b[set][j], acc[i][j], 0, 0, 0);
     };
     // Every wave's loads into the next stage and reads of this one are done.
-    auto meet = [&]() {
+    // But for the `newer` youngest loads, which may still be on their way: loads complete in order.
+    auto meet = [&](auto newer) {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+        __builtin_amdgcn_s_waitcnt(0x0070 | (newer & 15) | (newer >> 4) << 14);  // vmcnt(newer) lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
@@ -239,6 +241,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
             if (loads) __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);
         }
     };
+    typedef std::integral_constant<int, 0> none;
     auto step = [&](int kt, auto more, auto next) {
         fetch(1, kt, 1);
         multiply(0);
@@ -250,7 +253,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         weave(std::false_type{});
         weave(std::false_type{});
         if (next) {
-            meet();
+            meet(none{});
             fetch(0, kt + 1, 0);
             if (more) stage(kt + 2);
         }
@@ -262,9 +265,13 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         typedef std::false_type no;
         enter();
         stage(first);
-        turn();
-        meet();
-        if (first + 1 < last) stage(first + 1);
+        if (first + 1 < last) {
+            turn();
+            stage(first + 1);
+            meet(std::integral_constant<int, S::kLoadsA + S::kLoadsB>{});
+        } else {
+            meet(none{});
+        }
         fetch(0, first, 0);
         int kt = first;
         while (kt + 2 < last) {
@@ -274,13 +281,19 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         }
         if (kt + 1 < last) step(kt++, no{}, yes{});
         step(kt, no{}, no{});
-        meet();  // the epilogue may use the LDS
+        meet(none{});  // the epilogue may use the LDS
     }
     epilogue<S, E, F16, BM, BN, WM, WN>(p, acc, lds, m0, n0, wm, wn, split);
 }
 
+// Two products that do not wait for each other share a launch: blockIdx.z chooses.
+struct ProductPair {
+    ProductArgs p[2];
+};
 template <int BM, int BN, int WM, int WN, Epi E, bool F16>
-__global__ void __launch_bounds__(64 * WM * WN, 1) k_product(ProductArgs p) {
+__global__ void __launch_bounds__(64 * WM * WN, 1) k_product(ProductPair pair) {
+    const ProductArgs &p = pair.p[blockIdx.z];
+    if ((int)blockIdx.x >= p.tiles_m * p.tiles_n || (int)blockIdx.y >= p.splits) return;
     __shared__ __attribute__((aligned(1024))) char lds[Shape<BM, BN, WM, WN>::kLds];
     product_tile<BM, BN, WM, WN, E, F16>(p, (SSM_LDS char *)lds);
 }
@@ -320,8 +333,8 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
             s += __shfl_xor(s, 32);
             if (n >= p.N) continue;
             if (half == 0) p.part[slot * p.N + n] = make_float2(top, s);
-            const int64_t t = p.target[n] - mw;  // the lane's rows are t = 32 i + 8 (e / 4) + e % 4
-            if (p.target[n] >= 0 && t >= 0 && t < S::TM * 32 && (t & 4) == 0) {
+            const int64_t t = p.targets[n] - mw;  // the lane's rows are t = 32 i + 8 (e / 4) + e % 4
+            if (t >= 0 && t < S::TM * 32 && (t & 4) == 0) {
 #pragma unroll
                 for (int i = 0; i < S::TM; ++i)
 #pragma unroll
@@ -583,7 +596,8 @@ __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
 
 // 16 threads for a token join its n partial pairs.
 __global__ void __launch_bounds__(256) k_xent_join(const float2 *part, int64_t n, const float *at,
-                                                   const int32_t *target, int64_t T, float *loss, float *lse) {
+                                                   const int64_t *targets, int64_t ignore, int64_t T, int64_t V,
+                                                   float *loss, float *lse) {
     __shared__ float2 sh[16][16];
     const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
     const int64_t t = (int64_t)blockIdx.x * 16 + x;
@@ -599,7 +613,8 @@ __global__ void __launch_bounds__(256) k_xent_join(const float2 *part, int64_t n
     for (int j = 1; j < 16; ++j) join(m, s, sh[j][x].x, sh[j][x].y);
     const float l = m + logf(s);
     lse[t] = l;
-    loss[t] = target[t] == -1 ? 0.0f : target[t] >= 0 ? l - at[t] : NAN;
+    const int64_t to = targets[t];
+    loss[t] = to == ignore ? 0.0f : to >= 0 && to < V ? l - at[t] : NAN;
 }
 
 // mean[0] = mean loss over the tokens that are not ignored, mean[1] = 1 / their number.
@@ -632,15 +647,27 @@ __global__ void __launch_bounds__(1024) k_xent_mean(const float *loss, const int
     mean[1] = c ? (float)(1.0 / (double)c) : 0.0f;
 }
 
-// dst = (sum +) the n partial products in order; float32 or bfloat16.
-__global__ void __launch_bounds__(256) k_join_splits(const float *part, int n, int64_t stride, int64_t count,
-                                                     const float *sum, void *dst, bool bf16) {
+// dst = (sum +) the n partial products in order; float32 or bfloat16. Two of them side by side.
+struct JoinArgs {
+    const float *part;
+    int n;
+    int64_t count;  // elements; 0: nothing to join
+    const float *sum;
+    void *dst;
+    bool bf16;
+};
+struct JoinPair {
+    JoinArgs j[2];
+};
+__global__ void __launch_bounds__(256) k_join_splits(JoinPair pair) {
+    const JoinArgs &a = pair.j[blockIdx.y];
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (e >= count) return;
-    float v = sum ? sum[e] : 0.0f;
-    for (int k = 0; k < n; ++k) v += part[k * stride + e];
-    if (bf16) ((bf16_bits *)dst)[e] = f32_to_bf16(v);
-    else ((float *)dst)[e] = v;
+    if (e >= a.count) return;
+    float v = a.sum ? a.sum[e] : 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < a.n; ++k) v += a.part[k * a.count + e];
+    if (a.bf16) ((bf16_bits *)a.dst)[e] = f32_to_bf16(v);
+    else ((float *)a.dst)[e] = v;
 }
 
 template <typename IO>
@@ -655,31 +682,52 @@ unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per)
 
 constexpr int kBig = 256, kSmall = 128;
 
-// Tiles of 256 x 256 or 128 x 128, whichever takes less time on 256 compute units by their
-// rounds: a compute unit makes a quarter of the work in about a third of the time with the
-// small tiles (measured on 8192 x 8192 x 4096: 1250 against 950 TFLOP/s), which waste less
-// at the edges and in the last round.
+// Tiles of 256 x 256 or 128 x 128 and a split of k, whichever takes less time on 256 compute
+// units by their rounds: a compute unit makes a quarter of the work in about a third of the
+// time with the small tiles (measured on 8192 x 8192 x 4096: 1250 against 950 TFLOP/s), which
+// waste less at the edges and in the last round. Only small tiles are split (1000 x 1000 x 48000:
+// 134 us in 8 parts of small tiles, 170 in 16 of large ones); a split keeps at least 8 steps of k.
 struct Tiling {
     int tile, splits;
 };
 constexpr int64_t kCus = 256;
 Tiling tiling(int64_t M, int64_t N, int64_t steps, bool may_split) {
-    const int64_t nb = (int64_t)blocks(M, kBig) * blocks(N, kBig), n = (int64_t)blocks(M, kSmall) * blocks(N, kSmall);
-    if (3 * blocks(nb, kCus) <= blocks(n, kCus)) return {kBig, 1};
-    int64_t s = 1;
-    // a split keeps at least 8 steps of k, and its partial sums are written and read again
-    if (may_split) s = std::max<int64_t>(1, std::min(std::min<int64_t>(2 * kCus / n, steps / 8), (int64_t)16));
-    return {kSmall, (int)s};
+    Tiling best{};
+    double least = 0;
+    for (const int tile : {kSmall, kBig}) {
+        const int64_t n = (int64_t)blocks(M, tile) * blocks(N, tile), room = 2 * kCus / n;
+        const int64_t s = !may_split || tile == kBig ? 1 : std::max<int64_t>(1, std::min(std::min(room, steps / 8), (int64_t)16));
+        const double time = (double)blocks(n * s, kCus) / (double)s * (tile == kBig ? 3.0 : 1.0);
+        if (!best.tile || time < least) {
+            best = {tile, (int)s};
+            least = time;
+        }
+    }
+    return best;
 }
 
-template <Epi E, bool F16>
-hipError_t product(ProductArgs p, int tile, hipStream_t s) {
+void set_tiles(ProductArgs &p, int tile) {
     p.tiles_m = (int32_t)blocks(p.M, tile);
     p.tiles_n = (int32_t)blocks(p.N, tile);
-    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits);
-    if (tile == kBig) k_product<256, 256, 2, 4, E, F16><<<grid, 512, 0, s>>>(p);
-    else k_product<128, 128, 2, 2, E, F16><<<grid, 256, 0, s>>>(p);
+}
+template <Epi E, bool F16>
+hipError_t product(const ProductPair &pair, int n, int tile, hipStream_t s) {
+    int32_t tiles = 0, splits = 0;
+    for (int k = 0; k < n; ++k) {
+        tiles = std::max(tiles, pair.p[k].tiles_m * pair.p[k].tiles_n);
+        splits = std::max(splits, pair.p[k].splits);
+    }
+    const dim3 grid((unsigned)tiles, (unsigned)splits, (unsigned)n);
+    if (tile == kBig) k_product<256, 256, 2, 4, E, F16><<<grid, 512, 0, s>>>(pair);
+    else k_product<128, 128, 2, 2, E, F16><<<grid, 256, 0, s>>>(pair);
     return hipGetLastError();
+}
+template <Epi E, bool F16>
+hipError_t product(const ProductArgs &p, int tile, hipStream_t s) {
+    ProductPair pair{};
+    pair.p[0] = p;
+    set_tiles(pair.p[0], tile);
+    return product<E, F16>(pair, 1, tile, s);
 }
 
 // A bump allocator over the workspace; with no base it only counts.
@@ -704,7 +752,7 @@ struct Layout {
     int32_t *target;
     uint32_t *peak;
     int64_t peaks;
-    float *at, *w, *all, *sum, *split;
+    float *at, *w, *all, *sum, *split_w, *split_h;
     float2 *part;
     uint16_t *ht, *wt, *g, *gt;
     size_t bytes;
@@ -746,7 +794,8 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
         l.gt = a.take<uint16_t>(most * l.ldt * l.planes);
         const int64_t sw = l.out_w.splits > 1 ? l.out_w.splits * most * K : 0;
         const int64_t sh = l.out_h.splits > 1 ? l.out_h.splits * T * K : 0;
-        l.split = a.take<float>(std::max(sw, sh));
+        l.split_w = a.take<float>(sw);
+        l.split_h = a.take<float>(sh);
     }
     l.peak = a.take<uint32_t>(l.peaks);
     l.bytes = a.used;
@@ -811,6 +860,7 @@ hipError_t logits_operands(const XentArgs &a, const Layout &l, ProductArgs &p, h
     p.terms = l.terms;
     p.splits = 1;
     p.target = l.target;
+    p.targets = a.targets;
     return hipSuccess;
 }
 
@@ -818,8 +868,9 @@ template <typename IO>
 hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
     if (a.T > 0) {
         const Layout l = lay_out(a.T, a.K, a.V, io, false, rows_aligned(a), (char *)a.ws);
-        k_xent_tokens<<<dim3(blocks(a.T, 256)), 256, 0, s>>>(a.targets, a.ignore, a.T, a.V, nullptr, nullptr, nullptr,
-                                                            l.target, nullptr, nullptr, l.peak, l.peaks);
+        if (!io)  // for the peaks
+            k_xent_tokens<<<dim3(blocks(a.T, 256)), 256, 0, s>>>(a.targets, a.ignore, a.T, a.V, nullptr, nullptr, nullptr,
+                                                                l.target, nullptr, nullptr, l.peak, l.peaks);
         ProductArgs p{};
         SSM_TRY(logits_operands<IO>(a, l, p, s));
         p.M = a.V;
@@ -827,26 +878,49 @@ hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
         p.part = l.part;
         p.at = l.at;
         SSM_TRY((product<Epi::Lse, sizeof(IO) == 4>(p, l.lse.tile, s)));
-        k_xent_join<<<dim3(blocks(a.T, 16)), 256, 0, s>>>(l.part, (int64_t)blocks(a.V, l.lse.tile) * 2, l.at, l.target,
-                                                         a.T, a.loss, a.lse);
+        k_xent_join<<<dim3(blocks(a.T, 16)), 256, 0, s>>>(l.part, (int64_t)blocks(a.V, l.lse.tile) * 2, l.at, a.targets,
+                                                         a.ignore, a.T, a.V, a.loss, a.lse);
     }
     k_xent_mean<<<dim3(1), 1024, 0, s>>>(a.loss, a.targets, a.ignore, a.T, a.mean);
     return hipGetLastError();
 }
 
-// C [N][M] = (sum +) A B^T through partial sums over k where it is split.
-hipError_t product_out(ProductArgs p, bool f16, Tiling t, float *split, void *dst, bool bf16, float *sum, bool add, hipStream_t s) {
-    p.splits = t.splits;
-    p.ldc = p.M;
-    p.sum = sum;
-    p.add = add && t.splits == 1;
-    p.c = t.splits == 1 ? dst : split;
-    p.c_bf16 = bf16 && t.splits == 1;
-    p.cstride = p.M * p.N;
-    SSM_TRY((f16 ? product<Epi::Out, true>(p, t.tile, s) : product<Epi::Out, false>(p, t.tile, s)));
-    if (t.splits > 1)
-        k_join_splits<<<dim3(blocks(p.M * p.N, 256)), 256, 0, s>>>(split, t.splits, p.cstride, p.M * p.N,
-                                                                  add ? sum : nullptr, dst, bf16);
+// One of the gradients' products: C [N][M] = (sum +) A B^T, through partial sums over k where it
+// is split.
+struct Gradient {
+    ProductArgs p;
+    Tiling t;
+    JoinArgs join;
+};
+Gradient gradient(ProductArgs p, Tiling t, float *split, void *dst, bool bf16, float *sum, bool add) {
+    Gradient g{p, t, {}};
+    g.p.splits = t.splits;
+    g.p.ldc = p.M;
+    g.p.sum = sum;
+    g.p.add = add && t.splits == 1;
+    g.p.c = t.splits == 1 ? dst : split;
+    g.p.c_bf16 = bf16 && t.splits == 1;
+    g.p.cstride = p.M * p.N;
+    set_tiles(g.p, t.tile);
+    if (t.splits > 1) g.join = {split, t.splits, p.M * p.N, add ? sum : nullptr, dst, bf16};
+    return g;
+}
+// One or both of them, in one launch where their tiles agree.
+hipError_t run_gradients(const Gradient *g, int n, bool f16, hipStream_t s) {
+    if (n == 2 && g[0].t.tile != g[1].t.tile) {
+        SSM_TRY(run_gradients(g, 1, f16, s));
+        return run_gradients(g + 1, 1, f16, s);
+    }
+    ProductPair pair{};
+    JoinPair join{};
+    int64_t most = 0;
+    for (int k = 0; k < n; ++k) {
+        pair.p[k] = g[k].p;
+        join.j[k] = g[k].join;
+        most = std::max(most, g[k].join.count);
+    }
+    SSM_TRY((f16 ? product<Epi::Out, true>(pair, n, g[0].t.tile, s) : product<Epi::Out, false>(pair, n, g[0].t.tile, s)));
+    if (most > 0) k_join_splits<<<dim3(blocks(most, 256), (unsigned)n), 256, 0, s>>>(join);
     return hipGetLastError();
 }
 
@@ -884,6 +958,8 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
         p.gplane = a.T * ldg;
         p.gtplane = nv * l.ldt;
         SSM_TRY((product<Epi::Dlogits, sizeof(IO) == 4>(p, tiling(nv, a.T, p.steps * l.terms, false).tile, s)));
+        Gradient grads[2];
+        int n = 0;
         if (a.dweight) {
             ProductArgs q{};
             q.a = {l.ht, l.ldt, a.K * l.ldt, l.peak + kPeakWH};
@@ -893,7 +969,7 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
             q.steps = (int32_t)(l.ldt / kBK);
             q.terms = l.terms;
             q.scale = f16 ? nullptr : l.all;
-            SSM_TRY(product_out(q, f16, l.out_w, l.split, (IO *)a.dweight + v0 * a.K, io, nullptr, false, s));
+            grads[n++] = gradient(q, l.out_w, l.split_w, (IO *)a.dweight + v0 * a.K, io, nullptr, false);
         }
         if (a.dhidden) {
             // float32 weights have their peak from the logits; a piece's is read twice here
@@ -911,8 +987,9 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
             q.steps = (int32_t)(ldg / kBK);
             q.terms = l.terms;
             const bool end = v0 + nv == a.V;
-            SSM_TRY(product_out(q, f16, l.out_h, l.split, end ? a.dhidden : l.sum, end && io, l.sum, v0 > 0, s));
+            grads[n++] = gradient(q, l.out_h, l.split_h, end ? a.dhidden : l.sum, end && io, l.sum, v0 > 0);
         }
+        SSM_TRY(run_gradients(grads, n, f16, s));
     }
     return hipSuccess;
 }
