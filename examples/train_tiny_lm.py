@@ -1,0 +1,148 @@
+"""Trains a small language model on synthetic text with the library's training path:
+
+    python examples/train_tiny_lm.py [--steps 100] [--bits 8]
+
+Each layer mixes the sequence with a selective scan (the MambaBlock's) and a gated linear
+recurrence; documents are packed into rows, and the recurrence is reset where one starts. The
+head's loss is linear_cross_entropy, which keeps no logits, the optimizer AdamW, one launch for
+all parameters. Afterwards the recurrence of the first layer is run token by token, as a decoder
+would, and compared with the whole-sequence call.
+
+The text: a document begins with one of four keys, and every token after it follows from the
+token before by the key's own permutation of the vocabulary. A model learns it by its bigrams
+and by carrying the key; nothing of the document before helps.
+"""
+from __future__ import annotations
+
+import argparse
+import os
+import sys
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+import selective_state_space_49_amd as ssm  # noqa: E402
+
+IGNORE = -100
+
+
+KEYS = 4
+
+
+def batch(rows, length, table, doc, generator, device):
+    """Tokens [rows, length], targets (the next token; none across documents), document starts.
+    table [KEYS, vocab]: what follows a token under each key; keys are the first tokens."""
+    vocab, n = table.shape[1], -(-(length + 1) // doc)
+    key = torch.randint(0, KEYS, (rows, n), generator=generator)
+    token = torch.randint(KEYS, vocab, (rows, n), generator=generator)
+    columns = [key, token]
+    while len(columns) < doc:
+        token = table[key, token]
+        columns.append(token)
+    text = torch.stack(columns, -1).reshape(rows, n * doc)[:, :length + 1]
+    at = torch.arange(length + 1)
+    reset = (at[:-1] % doc == 0).expand(rows, length).contiguous()
+    target = text[:, 1:].clone()
+    target[:, at[1:] % doc <= 1] = IGNORE  # keys and first tokens follow from nothing
+    return text[:, :-1].contiguous().to(device), target.to(device), reset.to(device)
+
+
+class Layer(torch.nn.Module):
+    """x + out(scan(x)) + out(gated(x)): both mixers on D channels, bfloat16."""
+
+    def __init__(self, dim, inner, states, device):
+        super().__init__()
+        bf16 = dict(device=device, dtype=torch.bfloat16)
+        self.states = states
+        self.scan_in = torch.nn.Linear(dim, 2 * inner + 2 * states, bias=False, **bf16)
+        self.dt = torch.nn.Linear(dim, inner, **bf16)
+        self.gated_in = torch.nn.Linear(dim, 3 * inner, **bf16)
+        self.out = torch.nn.Linear(2 * inner, dim, bias=False, **bf16)
+        self.A_log = torch.nn.Parameter(torch.log(torch.arange(1.0, states + 1, device=device)).repeat(inner, 1))
+        self.D = torch.nn.Parameter(torch.ones(inner, device=device))
+        # a = exp(-8 softplus(decay) / 2) between about 0.9 and 0.999 at a half-open gate
+        self.decay = torch.nn.Parameter(torch.linspace(-8.0, -3.6, inner, device=device))
+
+    def gates(self, x):
+        return [t.contiguous() for t in self.gated_in(x).chunk(3, -1)]
+
+    def forward(self, x, reset):
+        u = torch.nn.functional.layer_norm(x, x.shape[-1:])
+        inner = self.D.numel()
+        v, z, B, C = self.scan_in(u).split([inner, inner, self.states, self.states], -1)
+        dt = torch.nn.functional.softplus(self.dt(u) - 2.0)
+        y, _ = ssm.selective_scan(v.contiguous(), dt, -torch.exp(self.A_log), B.contiguous(), C.contiguous(), self.D,
+                                  z.contiguous())
+        h, _ = ssm.gated_scan(*self.gates(u), self.decay, reset=reset)
+        return x + self.out(torch.cat([y, h], -1))
+
+
+class Model(torch.nn.Module):
+    def __init__(self, vocab, dim, inner, states, layers, device):
+        super().__init__()
+        self.embed = torch.nn.Parameter(torch.randn(vocab, dim, device=device).mul_(0.5).to(torch.bfloat16))
+        self.layers = torch.nn.ModuleList(Layer(dim, inner, states, device) for _ in range(layers))
+        self.head = torch.nn.Parameter(torch.randn(vocab, dim, device=device).mul_(dim ** -0.5).to(torch.bfloat16))
+
+    def forward(self, tokens, targets, reset):
+        x = self.embed[tokens]
+        for layer in self.layers:
+            x = layer(x, reset)
+        x = torch.nn.functional.layer_norm(x, x.shape[-1:])
+        return ssm.linear_cross_entropy(x, self.head, targets, ignore_index=IGNORE)
+
+
+def clip_scale(params, most=1.0):
+    """The factor that brings the gradients' norm to at most `most`, as a value on the GPU."""
+    norm = torch.stack([p.grad.float().norm() for p in params]).norm()
+    return (most / norm.clamp(min=most)).reshape(1)
+
+
+def decode_matches(layer, x, reset, tokens=64):
+    """The largest difference between the recurrence token by token and over the sequence."""
+    with torch.no_grad():
+        xs, r, i = layer.gates(torch.nn.functional.layer_norm(x, x.shape[-1:]))
+        y, _ = ssm.ssm_gated_fwd(xs, r, i, layer.decay, reset=reset)
+        h = torch.zeros((1, x.shape[0], layer.decay.numel()), device=x.device)
+        worst = 0.0
+        for t in range(tokens):
+            if bool(reset[0, t]):
+                h.zero_()
+            step = [v[None, :, t].contiguous() for v in (xs, r, i)]
+            y_t = ssm.ssm_gated_step(h, *step, layer.decay[None])
+            worst = max(worst, float((y_t[0].float() - y[:, t].float()).abs().max()))
+        return worst
+
+
+def train(steps=100, bits=8, vocab=256, dim=128, inner=256, states=16, layers=2, rows=16, length=512, doc=40, lr=5e-3,
+          seed=0, device="cuda", log=print):
+    """Returns the losses of the steps, and decode_matches() of the trained first layer."""
+    torch.manual_seed(seed)
+    g = torch.Generator().manual_seed(seed)
+    table = torch.stack([torch.cat([torch.arange(KEYS), KEYS + torch.randperm(vocab - KEYS, generator=g)])
+                         for _ in range(KEYS)])
+    model = Model(vocab, dim, inner, states, layers, device)
+    params = list(model.parameters())
+    opt = ssm.AdamW(params, lr=lr, betas=(0.9, 0.95), weight_decay=0.01, bits=bits)
+    losses = []
+    for step in range(steps):
+        tokens, targets, reset = batch(rows, length, table, doc, g, device)
+        opt.zero_grad()
+        loss = model(tokens, targets, reset)
+        loss.backward()
+        opt.step(grad_scale=clip_scale(params))
+        losses.append(loss.detach())
+        if step % 10 == 0 or step == steps - 1:
+            log(f"step {step:4d}  loss {float(losses[-1]):.4f}")
+    gap = decode_matches(model.layers[0], model.embed[tokens], reset)
+    log(f"{sum(p.numel() for p in params)} parameters in {len(params)} tensors, moments in {bits} bits; "
+        f"token by token against the sequence: {gap:.1e}")
+    return [float(v) for v in losses], gap
+
+
+if __name__ == "__main__":
+    ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
+    ap.add_argument("--steps", type=int, default=100)
+    ap.add_argument("--bits", type=int, choices=(8, 32), default=8)
+    a = ap.parse_args()
+    train(steps=a.steps, bits=a.bits)

@@ -161,6 +161,28 @@ def test_zeros_and_missing_gradients(bits):
             assert torch.equal(p.cpu(), q) and not bool(p.isnan().any())
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_extreme_magnitudes(bits):
+    # gradients from 1e-22 to 1e14 in blocks of their own: moments down to float32's smallest
+    # and large ones take the general forms of the root and the division, others the short ones
+    for power in (-22, -18, -10, 4, 9, 14):
+        pr = Problem([700, 256], seed=60 + power, bits=bits, kinds=[(0, 0)])
+        for k, (at, n) in enumerate(pr.at):
+            pr.g[k] = (pr.g[k] * np.float32(10.0) ** np.float32(power)).astype(np.float32)
+            pr.grads[k].copy_(torch.from_numpy(pr.g[k]))
+        for t in pr.state:
+            t.zero_()
+        pr.m[:], pr.v[:] = 0, 0
+        say("adamw extreme", bits, power)
+        pr.step(**dict(OPT, step=1))
+        check_bits(pr, dict(OPT, step=1))
+    # no eps, and an eps outside the short forms' range
+    for eps in (1e-30, 2.0):
+        pr = Problem([700], seed=40, bits=bits, kinds=[(0, 0)])
+        pr.step(**dict(OPT, eps=eps))
+        check_bits(pr, dict(OPT, eps=eps))
+
+
 def test_nan_stays_in_its_block():
     pr = Problem([2000], seed=9, bits=8, kinds=[(0, 0)])
     want = Problem([2000], seed=9, bits=8, kinds=[(0, 0)])
