@@ -67,13 +67,16 @@ ssm_status check_gated(int64_t batch, int64_t L, int64_t D, ssm_dtype io, float 
 
 bool xent_shape_ok(int64_t T, int64_t K, int64_t V) {
     const int64_t most = (int64_t)1 << 30;
-    return T >= 0 && T <= most && K >= 1 && K <= most && V >= 1 && V <= most;
+    return T >= 0 && T <= most && K >= 1 && K <= ((int64_t)1 << 22) && V >= 1 && V <= most &&
+           // rows of a tile by 32-bit offsets, tiles of 128 x 128 and blocks of a fill within the grid
+           (double)(T / 128 + 1) * (double)(V / 128 + 1) <= 2147483647.0 &&
+           (double)(K / 128 + 1) * (double)((T > V ? T : V) / 128 + 1) <= 2147483647.0 && (double)V * K <= 2.7e11;
 }
 
 ssm_status check_xent(const void *hidden, const void *weight, const int64_t *targets, int64_t T, int64_t K,
                       int64_t V, ssm_dtype io) {
     if (!valid_io(io)) return fail(SSM_ERR_DTYPE, "io dtype %d unknown", (int)io);
-    if (!xent_shape_ok(T, K, V)) return fail(SSM_ERR_SHAPE, "tokens must be in 0..2^30, dim and vocab in 1..2^30");
+    if (!xent_shape_ok(T, K, V)) return fail(SSM_ERR_SHAPE, "tokens must be in 0..2^30, dim in 1..2^22, vocab in 1..2^30, and their products within the grid");
     if (T > 0 && (!hidden || !weight || !targets)) return fail(SSM_ERR_NULL, "hidden, weight and targets are required");
     const size_t eb = io_bytes(io);
     if (!aligned(hidden, eb) || !aligned(weight, eb) || !aligned(targets, 8))

@@ -1,24 +1,24 @@
 // xent.hip -- softmax cross entropy of a linear head over a vocabulary, without keeping the
 // logits, and its gradients.
 //
-// Everything large is a matrix product on the matrix cores, C[n][m] = sum_k A[m][k] B[n][k]
-// with both operands' rows contiguous in k (k_product), and what differs is its epilogue:
+// Everything large is a matrix product on the matrix cores, C[n][m] = sum_k A(m, k) B(n, k)
+// (k_product), where an operand's rows run along k, or (transposed) its rows are the k. What
+// differs is the epilogue:
 //   forward    A = weight, B = hidden: a wave's tile of logits leaves, per token, the
 //              maximum and the sum of exponentials over its vocabulary rows; a small kernel
 //              joins a token's pairs: M = max(m, m'), s e^(m-M) + s' e^(m'-M).
 //   backward   for a piece of the vocabulary at a time: the same product again, with
-//              dlogits = w (exp(logit - lse) - onehot) written twice, as G [token][vocab] and
-//              G^T; then dweight rows = G^T hidden (A = hidden^T, B = G^T) and
-//              dhidden += G weight (A = weight^T, B = G).
+//              G [token][vocab] = dlogits / w = exp(logit - lse) - onehot; then dweight rows =
+//              G^T (w hidden), both transposed, and dhidden += w G weight, weight transposed.
 // The matrix cores take 16 bits. Logits of bfloat16 operands are products of their own bits. In
-// the gradients' products, a token's weight w stays out of G, whose values dlogits / w lie in
-// [-1, 1]: dhidden takes it as a factor of its row.
-//   bfloat16, every token of one weight (a mean loss): G, hidden^T and weight^T are bfloat16,
-//   and w is a factor of dweight. (With w in G, the large values w (p - 1) of all tokens round
-//   alike, and their error was 2.1e-3 where dweight's own rounding is 1.7e-3.)
+// the gradients' products, a token's weight w stays out of G, whose values lie in [-1, 1]:
+// dhidden takes it as a factor of its row.
+//   bfloat16, every token of one weight (a mean loss): G, hidden and weight are bfloat16, and w
+//   is a factor of dweight. (With w in G, the large values w (p - 1) of all tokens round alike,
+//   and their error was 2.1e-3 where dweight's own rounding is 1.7e-3.)
 //   otherwise: float16 planes, scaled by a power of two that brings the largest of the array to
 //   2^14 .. 2^15, which leaves small values an absolute error of 2^-39 of the largest. dweight
-//   takes w with hidden^T. One plane each for bfloat16 operands: 11 bits. Two for float32, x =
+//   takes w with hidden. One plane each for bfloat16 operands: 11 bits. Two for float32, x =
 //   x1 + x2, the rounded value and the rounded rest, 22 bits, and a product is the sum of x1y1,
 //   x1y2, x2y1 as a longer sum over k; x2y2 is below 2^-22 of x1y1. (Three bfloat16 parts need
 //   six partial products for 24 bits.) float16 products take 9 % longer than bfloat16 ones
@@ -36,29 +36,33 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #define SSM_LDS __attribute__((address_space(3)))
-#define SSM_GLB __attribute__((address_space(1)))
 
-constexpr int kBK = 64;        // k per stage: rows of 128 bytes in LDS
+constexpr int kBK = 64;        // k per stage
 constexpr int kParts = 2;      // float16 planes of a float32 operand
 enum { kPeakW, kPeakH, kPeakWH, kPeakPiece };  // peaks of weight, hidden, w hidden, pieces of weight
 constexpr int kPeak = 14;      // a scaled array's largest value is in 2^kPeak .. 2^(kPeak + 1)
 constexpr uint32_t kRsrcWord3 = 0x00027000;  // raw buffer, 32-bit data
 
-// One operand: rows of ld elements, contiguous in k, 16-byte aligned, ld a multiple of 64;
-// planes `plane` elements apart.
+// One operand, 16-byte aligned: rows of ld elements (a multiple of 64), planes `plane` elements
+// apart. Its rows run along k, all of ld there; or, transposed, row k holds the values of all
+// m (or n), and `rows` of them are there to be read.
 struct Operand {
     const uint16_t *p;
     int64_t ld, plane;
     const uint32_t *peak;  // float16 planes: the largest value's bits; null: scaled by 2^kPeak
+    int64_t rows;
 };
 
 enum class Epi { Lse, Dlogits, Out };
 
 struct ProductArgs {
     Operand a, b;
-    int64_t M, N;           // rows of A and of B
+    int64_t M, N;           // of C
     int32_t steps;          // ceil(K / kBK)
     int32_t terms;          // partial products: 1, or 3 of two planes each
     int32_t planes;         // Dlogits: float16 planes of G, 0: bfloat16
@@ -70,8 +74,8 @@ struct ProductArgs {
     float *at;              // Lse: [N] logit of the target
     const float *lse;       // Dlogits: [N]
     int64_t v0;
-    uint16_t *g, *gt;       // Dlogits: G [N][ldg], G^T [M][ldgt], planes apart
-    int64_t ldg, ldgt, gplane, gtplane;
+    uint16_t *g;            // Dlogits: G [rows_g][ldg], planes apart; 0 outside of N x M
+    int64_t ldg, rows_g, gplane;
     // Out: C [N][ldc] of float32 or bfloat16 at split * cstride
     void *c;
     int64_t ldc, cstride;
@@ -101,26 +105,95 @@ __device__ __forceinline__ float unscale(const Operand &o) {
 }
 
 // Waves stand WM x WN over a BM x BN tile; each makes TM x TN blocks of 32 x 32 with
-// v_mfma_f32_32x32x16_bf16. Operand tiles go from global memory straight to LDS, 16 bytes a
-// lane, double buffered; the 16-byte chunk c of row r lies at chunk c ^ (r / 2 & 7), so the 16
-// rows that a group of lanes reads at one k fall on the 16 chunks of LDS's 64 banks (two
-// rows of 128 bytes fill them once).
+// v_mfma_f32_32x32x16. Operand tiles go from global memory straight to LDS, 16 bytes a lane,
+// double buffered.
 template <int BM, int BN, int WM, int WN>
 struct Shape {
     static constexpr int kThreads = 64 * WM * WN;
     static constexpr int kWaves = WM * WN;
     static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
-    static constexpr int kStage = (BM + BN) * kBK * 2;   // bytes
-    static constexpr int kRow = BM + 2;                  // staging of G: elements of a token's row
+    static constexpr int kStage = (BM + BN) * kBK * 2;  // bytes
+    static constexpr int kRow = BM + 8;                 // staging of G: elements of a token's row
     static constexpr int kLds = std::max(2 * kStage, BN * kRow * 2);
-    static constexpr int kLoadsA = BM * kBK * 2 / (1024 * kWaves), kLoadsB = BN * kBK * 2 / (1024 * kWaves);
+};
+
+// One operand's way into LDS and into fragments: B of its m (or n), kBK of k a stage.
+//   Along k: LDS rows of 128 bytes, one for each m; the 16-byte chunk c of row r lies at chunk
+//   c ^ (r / 2 & 7), so the 16 rows that a group of lanes reads at one k fall on the 16 chunks of
+//   LDS's 64 banks (two rows of 128 bytes fill them once).
+//   Transposed: LDS rows of 2 B bytes, one for each k; chunk c of row r lies at c ^ 4 (r & 3). The
+//   transposing read gives a group of 16 lanes 4 k of 16 m from 4 rows of 32 bytes, and two
+//   groups together read all 256 bytes of the banks.
+// Rows (of m, or of k in the last step) past the operand's end read its last one, columns past
+// its width the last ones: those products are never used, or the other operand is 0 there.
+template <int B, bool TR, int WAVES, int BLOCKS>
+struct Feed {
+    static constexpr int kLoads = B * kBK * 2 / (1024 * WAVES);  // of a wave in a stage
+    static constexpr int kReads = TR ? 2 : 1;                    // for a fragment
+    const char *base, *next;  // plane 0 and the next step's address, uniform
+    int64_t stride;           // bytes of a step
+    uint32_t off[kLoads], last[kLoads], frag[4];
+
+    __device__ __forceinline__ Feed(const Operand &o, int64_t at, int64_t end, int steps, int lane, int wave, int block0) {
+        if (TR) {
+            constexpr int kLanes = B / 8;  // of a row
+            const int64_t there = o.rows - (int64_t)(steps - 1) * kBK - 1;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int r = (j * WAVES + wave) * (64 / kLanes) + lane / kLanes;
+                const int64_t c = min(at + ((lane % kLanes) ^ (r & 3) * 4) * 8, o.ld - 8);
+                off[j] = (uint32_t)((r * o.ld + c) * 2);
+                last[j] = (uint32_t)((min((int64_t)r, there) * o.ld + c) * 2);
+            }
+            base = (const char *)o.p;
+            stride = o.ld * kBK * 2;
+            const int i = lane & 15, r = i >> 2, low = (lane >> 4 & 1) * 2 + (i & 3) / 2;
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k)
+                frag[k] = ((lane >> 5) * 8 + r) * (B * 2) + (((block0 + k) ^ r) * 4 + low) * 16 + (i & 1) * 8;
+        } else {
+            static_assert(WAVES % 2 == 0, "a wave's 8 rows all start at an even or all at an odd multiple of 8");
+            const uint32_t chunk = (uint32_t)((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) * 16u;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const int64_t r = min((int64_t)((j * WAVES + wave) * 8 + (lane >> 3)), end - 1 - at);
+                off[j] = (uint32_t)(r * o.ld * 2) + chunk;
+            }
+            base = (const char *)(o.p + at * o.ld);
+            stride = kBK * 2;
+            const int row = lane & 31, half = lane >> 5;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks)
+                frag[ks] = (uint32_t)(((2 * ks + half) ^ (row >> 1 & 7)) * 16 + row * 128) + block0 * 4096;
+        }
+    }
+    __device__ __forceinline__ void enter(int64_t plane, int k) { next = base + plane * 2 + k * stride; }
+    __device__ __forceinline__ void load(SSM_LDS char *to, bool final) {
+        __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void *)next, 0, -1, kRsrcWord3);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (SSM_LDS void *)(to + j * WAVES * 1024), 16,
+                                                     TR && final ? last[j] : off[j], 0, 0, 0);
+        next += stride;
+    }
+    // Block k's fragment of step ks: lane l holds row l % 32, 8 consecutive k of half l / 32.
+    __device__ __forceinline__ bf16x8 read(const SSM_LDS char *at, int ks, int k) const {
+        if constexpr (TR) {
+            const SSM_LDS char *from = at + frag[k] + ks * 16 * B * 2;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)from);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)(from + 4 * B * 2));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            return *(const SSM_LDS bf16x8 *)(at + frag[ks] + k * 4096);
+        }
+    }
 };
 
 template <typename S, Epi E, bool F16, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::TM][S::TN], SSM_LDS char *lds,
                                          int64_t m0, int64_t n0, int wm, int wn, int split);
 
-template <int BM, int BN, int WM, int WN, Epi E, bool F16>
+template <int BM, int BN, int WM, int WN, Epi E, bool F16, bool TA, bool TB>
 __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char *lds) {
     using S = Shape<BM, BN, WM, WN>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -137,43 +210,22 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
     const int split = blockIdx.y;
     const int first = (int)((int64_t)total * split / p.splits), last = (int)((int64_t)total * (split + 1) / p.splits);
 
-    // A load instruction of a wave fills 8 rows of 8 chunks. Rows past the operand's end read
-    // its last row: their products are never used.
-    uint32_t va[S::kLoadsA], vb[S::kLoadsB];
-    static_assert(S::kWaves % 2 == 0, "a wave's 8 rows all start at an even or all at an odd multiple of 8");
-    const uint32_t chunk = (uint32_t)((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) * 16u;
-#pragma unroll
-    for (int j = 0; j < S::kLoadsA; ++j) {
-        const int64_t r = min((int64_t)((j * S::kWaves + wave) * 8 + (lane >> 3)), p.M - 1 - m0);
-        va[j] = (uint32_t)(r * p.a.ld * 2) + chunk;
-    }
-#pragma unroll
-    for (int j = 0; j < S::kLoadsB; ++j) {
-        const int64_t r = min((int64_t)((j * S::kWaves + wave) * 8 + (lane >> 3)), p.N - 1 - n0);
-        vb[j] = (uint32_t)(r * p.b.ld * 2) + chunk;
-    }
-    const uint16_t *const pa = p.a.p + m0 * p.a.ld, *const pb = p.b.p + n0 * p.b.ld;
+    typedef Feed<BM, TA, S::kWaves, S::TM> FeedA;
+    typedef Feed<BN, TB, S::kWaves, S::TN> FeedB;
+    FeedA fa(p.a, m0, p.M, p.steps, lane, wave, wm * S::TM);
+    FeedB fb(p.b, n0, p.N, p.steps, lane, wave, wn * S::TN);
     // Stages are loaded in order: k is the next one's step within its partial product seg,
     // whose planes of (A, B) are (0,0) (0,1) (1,0).
     int seg = first / p.steps, k = first - seg * p.steps;
-    __amdgpu_buffer_rsrc_t ra, rb;
     auto enter = [&]() {
-        const int64_t oa = seg == 2 ? p.a.plane : 0, ob = seg == 1 ? p.b.plane : 0;
-        ra = __builtin_amdgcn_make_buffer_rsrc((void *)(pa + oa), 0, -1, kRsrcWord3);
-        rb = __builtin_amdgcn_make_buffer_rsrc((void *)(pb + ob), 0, -1, kRsrcWord3);
+        fa.enter(seg == 2 ? p.a.plane : 0, k);
+        fb.enter(seg == 1 ? p.b.plane : 0, k);
     };
     auto stage = [&](int kt) {
         SSM_LDS char *to = lds + (kt & 1) * S::kStage + wave * 1024;
-#pragma unroll
-        for (int j = 0; j < S::kLoadsA; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (SSM_LDS void *)(to + j * S::kWaves * 1024), 16, va[j],
-                                                     k * (kBK * 2), 0, 0);
-        to += BM * kBK * 2;
-#pragma unroll
-        for (int j = 0; j < S::kLoadsB; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (SSM_LDS void *)(to + j * S::kWaves * 1024), 16, vb[j],
-                                                     k * (kBK * 2), 0, 0);
         ++k;
+        fa.load(to, k == p.steps);
+        fb.load(to + BM * kBK * 2, k == p.steps);
     };
     auto turn = [&]() {  // to the next partial product after its last step
         if (k < p.steps) return;
@@ -182,15 +234,6 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         enter();
     };
 
-    // Fragments: lane l holds row l % 32 of a block, 8 consecutive k of half l / 32.
-    const int row = lane & 31, half = lane >> 5;
-    uint32_t fa[4], fb[4];
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t c = (uint32_t)(((2 * ks + half) ^ (row >> 1 & 7)) * 16 + row * 128);
-        fa[ks] = c + wm * S::TM * 4096;
-        fb[ks] = c + wn * S::TN * 4096 + BM * kBK * 2;
-    }
     f32x16 acc[S::TM][S::TN];
 #pragma unroll
     for (int i = 0; i < S::TM; ++i)
@@ -202,9 +245,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
     auto fetch = [&](int set, int kt, int ks) {
         const SSM_LDS char *at = lds + (kt & 1) * S::kStage;
 #pragma unroll
-        for (int i = 0; i < S::TM; ++i) a[set][i] = *(const SSM_LDS bf16x8 *)(at + fa[ks] + i * 4096);
+        for (int i = 0; i < S::TM; ++i) a[set][i] = fa.read(at, ks, i);
 #pragma unroll
-        for (int j = 0; j < S::TN; ++j) b[set][j] = *(const SSM_LDS bf16x8 *)(at + fb[ks] + j * 4096);
+        for (int j = 0; j < S::TN; ++j) b[set][j] = fb.read(at + BM * kBK * 2, ks, j);
     };
     auto multiply = [&](int set) {
 #pragma unroll
@@ -218,8 +261,8 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
                 else
                     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[set][i], b[set][j], acc[i][j], 0, 0, 0);
     };
-    // Every wave's loads into the next stage and reads of this one are done.
-    // But for the `newer` youngest loads, which may still be on their way: loads complete in order.
+    // All waves' loads into the next stage and reads of this one are done, but for the `newer`
+    // youngest loads of each, which may still be on their way: loads complete in order.
     auto meet = [&](auto newer) {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_sched_barrier(0);
@@ -231,13 +274,13 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
     // One stage of k: every fragment is read while the products of the one before it run. The
     // last one is in registers once all waves meet; then the stage's buffer is loaded again
     // and the next stage's first fragments are read behind the last products.
-    constexpr int kFrag = S::TM + S::TN, kMul = S::TM * S::TN, kLoads = (S::kLoadsA + S::kLoadsB) / kMul;
-    static_assert(kFrag <= kMul, "a fragment read for each product");
-    auto weave = [&](auto loads) {  // one fragment read (and the loads' share) between products
+    constexpr int kMul = S::TM * S::TN, kReads = S::TM * FeedA::kReads + S::TN * FeedB::kReads;
+    constexpr int kPer = (kReads + kMul - 1) / kMul, kLoads = (FeedA::kLoads + FeedB::kLoads) / kMul;
+    auto weave = [&](auto loads) {  // fragment reads (and the loads' share) between the products
 #pragma unroll
         for (int j = 0; j < kMul; ++j) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            if (j < kFrag) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (j * kPer < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kPer, 0);
             if (loads) __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);
         }
     };
@@ -268,7 +311,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         if (first + 1 < last) {
             turn();
             stage(first + 1);
-            meet(std::integral_constant<int, S::kLoadsA + S::kLoadsB>{});
+            meet(std::integral_constant<int, FeedA::kLoads + FeedB::kLoads>{});
         } else {
             meet(none{});
         }
@@ -286,16 +329,10 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
     epilogue<S, E, F16, BM, BN, WM, WN>(p, acc, lds, m0, n0, wm, wn, split);
 }
 
-// Two products that do not wait for each other share a launch: blockIdx.z chooses.
-struct ProductPair {
-    ProductArgs p[2];
-};
-template <int BM, int BN, int WM, int WN, Epi E, bool F16>
-__global__ void __launch_bounds__(64 * WM * WN, 1) k_product(ProductPair pair) {
-    const ProductArgs &p = pair.p[blockIdx.z];
-    if ((int)blockIdx.x >= p.tiles_m * p.tiles_n || (int)blockIdx.y >= p.splits) return;
+template <int BM, int BN, int WM, int WN, Epi E, bool F16, bool TA, bool TB>
+__global__ void __launch_bounds__(64 * WM * WN, 1) k_product(ProductArgs p) {
     __shared__ __attribute__((aligned(1024))) char lds[Shape<BM, BN, WM, WN>::kLds];
-    product_tile<BM, BN, WM, WN, E, F16>(p, (SSM_LDS char *)lds);
+    product_tile<BM, BN, WM, WN, E, F16, TA, TB>(p, (SSM_LDS char *)lds);
 }
 
 // A block's element e of lane l is row m = 8 (e / 4) + 4 (l / 32) + e % 4, column n = l % 32.
@@ -344,14 +381,11 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
         }
     }
     if constexpr (E == Epi::Dlogits) {
-        // Through LDS, a token's row of kRow elements (an odd number of words, so that 8
-        // tokens at one pair of columns fall on different banks), and out both ways. The
-        // second plane starts from the product again. The token's weight stays out of G
-        // (dhidden takes it as a factor, dweight with hidden^T), so that its values lie in
-        // [-1, 1] and need no peak of their own.
-        constexpr int kWords = S::kRow / 2;
+        // Through LDS, a token's row of kRow elements, and out in whole rows. The second plane
+        // starts from the product again. The token's weight stays out of G (dhidden takes it as
+        // a factor, dweight with hidden), so that its values lie in [-1, 1] and need no peak of
+        // their own.
         const float unit = p.planes ? (float)(1 << kPeak) : 1.0f;
-        SSM_LDS uint32_t *words = (SSM_LDS uint32_t *)lds;
         for (int part = 0; part < max(p.planes, 1); ++part) {
 #pragma unroll
             for (int j = 0; j < S::TN; ++j) {
@@ -363,176 +397,146 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
                 const int t = (int)max((int64_t)-1, min((int64_t)S::TM * 32, target - p.v0 - mw));
                 // an ignored token and the padding are exactly 0, whatever the logit
                 const int rows = target == -1 ? 0 : (int)max((int64_t)0, min((int64_t)S::TM * 32, p.M - mw));
-                SSM_LDS uint32_t *to = words + (wn * S::TN * 32 + j * 32 + (lane & 31)) * kWords +
-                                       (wm * S::TM * 32 + 4 * half) / 2;
+                SSM_LDS char *to = lds + (wn * S::TN * 32 + j * 32 + (lane & 31)) * (S::kRow * 2) +
+                                   (wm * S::TM * 32 + 4 * half) * 2;
 #pragma unroll
                 for (int i = 0; i < S::TM; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const int at = i * 32 + 8 * (e / 4) + e % 4;
-                        uint32_t word = 0;
+                    for (int e = 0; e < 16; e += 4) {
+                        const int at = i * 32 + 2 * e;
+                        uint32_t v16[4];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
+                        for (int k = 0; k < 4; ++k) {
                             const float q = e2((value(acc[i][j][e + k]) - lse) * kLog2e) - (t == at + k ? 1.0f : 0.0f);
                             float v = at + k < rows ? q * scale : 0.0f;
                             if (part > 0) take_f16(v);
-                            word |= (uint32_t)(p.planes ? take_f16(v) : f32_to_bf16(v)) << (16 * k);
+                            v16[k] = p.planes ? take_f16(v) : f32_to_bf16(v);
                         }
-                        to[at / 2] = word;
+                        *(SSM_LDS u32x2 *)(to + at * 2) = u32x2{v16[0] | v16[1] << 16, v16[2] | v16[3] << 16};
                     }
             }
             __syncthreads();
-            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-            uint16_t *g = p.g + part * p.gplane, *gt = p.gt + part * p.gtplane;
+            uint16_t *g = p.g + part * p.gplane;
             for (int c = threadIdx.x; c < BN * (BM / 8); c += S::kThreads) {  // 8 columns of a token
                 const int n = c / (BM / 8), m = c % (BM / 8) * 8;
-                if (n0 + n >= p.N || m0 + m >= p.ldg) continue;
-                const SSM_LDS uint32_t *from = words + n * kWords + m / 2;
-                *(u32x4 *)(g + (n0 + n) * p.ldg + m0 + m) = u32x4{from[0], from[1], from[2], from[3]};
+                if (n0 + n < p.rows_g && m0 + m < p.ldg)
+                    *(u32x4 *)(g + (n0 + n) * p.ldg + m0 + m) = *(const SSM_LDS u32x4 *)(lds + n * (S::kRow * 2) + m * 2);
             }
-            if (p.gt)
-                for (int c = threadIdx.x; c < (BM / 2) * (BN / 8); c += S::kThreads) {  // 8 tokens of 2 columns
-                    // 8 lanes cover 64 tokens of one pair of columns: a whole line of G^T
-                    const int m = (c / 8) % (BM / 2) * 2, n = (c / 8 / (BM / 2) * 8 + c % 8) * 8;
-                    if (m0 + m >= p.M || n0 + n >= p.ldgt) continue;
-                    uint32_t v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = words[(n + k) * kWords + m / 2];
-                    u32x4 lo, hi;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        lo[k] = __builtin_amdgcn_perm(v[2 * k + 1], v[2 * k], 0x05040100);
-                        hi[k] = __builtin_amdgcn_perm(v[2 * k + 1], v[2 * k], 0x07060302);
-                    }
-                    uint16_t *to = gt + (m0 + m) * p.ldgt + n0 + n;
-                    *(u32x4 *)to = lo;
-                    if (m0 + m + 1 < p.M) *(u32x4 *)(to + p.ldgt) = hi;
-                }
             __syncthreads();
         }
     }
     if constexpr (E == Epi::Out) {
         const float scale = p.scale ? *p.scale : 1.0f;
-        const bool vec = p.ldc % 4 == 0 && ((uintptr_t)p.c & 15) == 0;
+        const size_t eb = p.c_bf16 ? 2 : 4;
+        char *const c = (char *)p.c + (size_t)split * p.cstride * eb;
+        if (p.ldc % 4 == 0 && ((uintptr_t)c & (4 * eb - 1)) == 0) {
+            // four neighbours of a row at a time
 #pragma unroll
-        for (int j = 0; j < S::TN; ++j) {
-            const int64_t n = nw + j * 32;
-            if (n >= p.N) continue;
-            const float row = p.row ? p.row[n] : scale;
+            for (int j = 0; j < S::TN; ++j) {
+                const int64_t n = nw + j * 32;
+                if (n >= p.N) continue;
+                const float row = p.row ? p.row[n] : scale;
 #pragma unroll
-            for (int i = 0; i < S::TM; ++i)
+                for (int i = 0; i < S::TM; ++i)
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                    const int64_t m = mw + i * 32 + 2 * e;
-                    if (m >= p.M) continue;
-                    const int64_t at = n * p.ldc + m;
-                    float v[4];
+                    for (int e = 0; e < 16; e += 4) {
+                        const int64_t m = mw + i * 32 + 2 * e;
+                        if (m >= p.M) continue;  // M = ldc: all four or none
+                        const int64_t at = n * p.ldc + m;
+                        float v[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = value(acc[i][j][e + k]) * row;
-                    if (p.add)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (m + k < p.M) v[k] += p.sum[at + k];
-                    if (vec && m + 3 < p.M) {
-                        if (p.c_bf16) {
-                            uint2 w;
-                            w.x = f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16;
-                            w.y = f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16;
-                            *(uint2 *)((bf16_bits *)p.c + split * p.cstride + at) = w;
-                        } else {
-                            *(float4 *)((float *)p.c + split * p.cstride + at) = make_float4(v[0], v[1], v[2], v[3]);
+                        for (int k = 0; k < 4; ++k) v[k] = value(acc[i][j][e + k]) * row;
+                        if (p.add) {
+                            const float4 s = *(const float4 *)(p.sum + at);
+                            v[0] += s.x, v[1] += s.y, v[2] += s.z, v[3] += s.w;
                         }
-                    } else {
-                        for (int k = 0; k < 4 && m + k < p.M; ++k) {
-                            if (p.c_bf16) ((bf16_bits *)p.c)[split * p.cstride + at + k] = f32_to_bf16(v[k]);
-                            else ((float *)p.c)[split * p.cstride + at + k] = v[k];
-                        }
+                        if (p.c_bf16)
+                            *(u32x2 *)(c + at * 2) = u32x2{f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                                                           f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
+                        else
+                            *(float4 *)(c + at * 4) = make_float4(v[0], v[1], v[2], v[3]);
+                    }
+            }
+        } else {
+            // Rows that do not start on four elements: a wave turns 32 of its rows in LDS and
+            // writes them element by element, a lane beside the next. (The lanes' own four
+            // elements, each row apart, took 201 us for the 142 MB that this writes in 60.)
+            constexpr int kTurn = S::TM * 32 + 1;
+            SSM_LDS float *mine = (SSM_LDS float *)lds + (wn * WM + wm) * 32 * kTurn;
+            static_assert(S::kWaves * 32 * kTurn * 4 <= S::kLds, "the turned rows fit");
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j) {
+#pragma unroll
+                for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        mine[(lane & 31) * kTurn + 4 * half + i * 32 + 8 * (e / 4) + e % 4] = value(acc[i][j][e]);
+                __syncthreads();
+                for (int r = 0; r < 32; ++r) {
+                    const int64_t n = n0 + (wn * S::TN + j) * 32 + r;
+                    if (n >= p.N) break;
+                    const float row = p.row ? p.row[n] : scale;
+#pragma unroll
+                    for (int i = 0; i < S::TM * 32; i += 64) {
+                        const int64_t m = m0 + wm * S::TM * 32 + i + lane, at = n * p.ldc + m;
+                        if (m >= p.M) continue;
+                        float v = mine[r * kTurn + i + lane] * row;
+                        if (p.add) v += p.sum[at];
+                        if (p.c_bf16) ((bf16_bits *)c)[at] = f32_to_bf16(v);
+                        else ((float *)c)[at] = v;
                     }
                 }
+                __syncthreads();
+            }
         }
     }
 }
 
 // ---------------------------------------------------------------- operands
-// dst[plane][r][ld] = src [rows][cols], 0 past its columns: a copy of bfloat16, or the scaled
-// planes of float32.
-template <typename IO>
-__global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64_t cols, const uint32_t *peak,
-                                              uint16_t *dst, int64_t ld, int64_t plane) {
-    constexpr bool F32 = sizeof(IO) == 4;
-    const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
-    if (c >= ld) return;
-    const float scale = F32 ? exp2i(scale_exp(*peak)) : 1.0f;
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-        const IO *from = src + r * cols + c;
-        uint16_t *to = dst + r * ld + c;
-        if constexpr (F32) {
-            float v0 = c < cols ? from[0] * scale : 0.0f, v1 = c + 1 < cols ? from[1] * scale : 0.0f;
-#pragma unroll
-            for (int q = 0; q < kParts; ++q) {
-                const uint32_t lo = take_f16(v0), hi = take_f16(v1);
-                *(uint32_t *)(to + q * plane) = lo | hi << 16;
-            }
-        } else {
-            const uint32_t lo = c < cols ? from[0] : 0, hi = c + 1 < cols ? from[1] : 0;
-            *(uint32_t *)to = lo | hi << 16;
-        }
-    }
-}
-
-// dst[plane][c][ld] = src^T, src [rows][cols]: with a peak its scaled planes, without one a copy of
-// bfloat16; 0 past its rows, and for the rows whose target is ignored: they may hold anything,
-// and 0 times it must not reach a sum. w: a factor for each row of the planes. Blocks of 64 x 64 go through
-// LDS, N columns a lane on the way in (2 where rows start on pairs), two rows on the way out.
-template <typename IO, int N>
-__global__ void __launch_bounds__(256) k_pack_t(const IO *src, int64_t rows, int64_t cols, const int32_t *target,
-                                                const float *w, const uint32_t *peak, uint16_t *dst, int64_t ld,
-                                                int64_t plane) {
-    __shared__ float sh[64][65];
-    const int64_t c0 = (int64_t)blockIdx.x * 64;
-    typedef IO iov __attribute__((ext_vector_type(N)));
-    constexpr int kLanes = 64 / N, kRows = 256 / kLanes;
-    const int x = threadIdx.x % kLanes * N, y = threadIdx.x / kLanes;
+// dst[plane][r][ld] for r < rows_out: src [rows][cols] and 0 past its columns and rows. With a
+// peak, its scaled planes; without one, a copy of bfloat16. The rows whose target is ignored
+// are 0: they may hold anything, and 0 times it must not reach a sum. w: a factor for each row
+// of the planes. Four columns a thread.
+template <typename IO, bool WIDE>
+__global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64_t cols, int64_t rows_out,
+                                              const int32_t *target, const float *w, const uint32_t *peak, uint16_t *dst,
+                                              int64_t ld, int64_t plane) {
+    typedef IO iov __attribute__((ext_vector_type(4)));
+    const int64_t across = ld / 4, total = rows_out * across;
     const float scale = peak ? exp2i(scale_exp(*peak)) : 1.0f;
-    for (int64_t r0 = (int64_t)blockIdx.y * 64; r0 < ld; r0 += (int64_t)gridDim.y * 64) {
-        iov from[64 / kRows];
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+        const int64_t r = e / across, c = (e - r * across) * 4;
+        const bool in = r < rows && c < cols && !(target && target[r] == -1);
+        iov from = {IO(0), IO(0), IO(0), IO(0)};
+        if (in) {
+            const IO *at = src + r * cols + c;
+            if (WIDE) {
+                from = *(const iov *)at;
+            } else {
 #pragma unroll
-        for (int k = 0; k < 64 / kRows; ++k) {
-            const int64_t r = r0 + y + k * kRows;
-            const bool in = r < rows && c0 + x < cols && !(target && target[r] == -1);
-#pragma unroll
-            for (int q = 0; q < N; ++q) from[k][q] = 0;
-            if (in) from[k] = *(const iov *)(src + r * cols + c0 + x);
-        }
-#pragma unroll
-        for (int k = 0; k < 64 / kRows; ++k) {
-            const int64_t r = r0 + y + k * kRows;
-            const float f = w && r < rows ? w[r] : 1.0f;  // 0 for an ignored row
-#pragma unroll
-            for (int q = 0; q < N; ++q) {
-                const IO e = from[k][q];
-                sh[y + k * kRows][x + q] = Io<IO>::ld(&e) * f * scale;
+                for (int k = 0; k < 4; ++k)
+                    if (c + k < cols) from[k] = at[k];
             }
         }
-        __syncthreads();
-        const int px = threadIdx.x & 31, py = threadIdx.x >> 5;  // two rows of src a lane
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int k = py + 8 * j;
-            if (c0 + k >= cols) break;
-            float v0 = sh[2 * px][k], v1 = sh[2 * px + 1][k];
-            uint16_t *to = dst + (c0 + k) * ld + r0 + 2 * px;
-            if (sizeof(IO) == 2 && !peak) {
-                *(uint32_t *)to = f32_to_bf16(v0) | (uint32_t)f32_to_bf16(v1) << 16;
-                continue;
-            }
-#pragma unroll
-            for (int q = 0; q < (sizeof(IO) == 4 ? kParts : 1); ++q) {
-                const uint32_t lo = take_f16(v0), hi = take_f16(v1);
-                *(uint32_t *)(to + q * plane) = lo | hi << 16;
-            }
+        uint16_t *to = dst + r * ld + c;
+        if (sizeof(IO) == 2 && !peak) {
+            *(u32x2 *)to = u32x2{(uint32_t)from[0] | (uint32_t)from[1] << 16, (uint32_t)from[2] | (uint32_t)from[3] << 16};
+            continue;
         }
-        __syncthreads();
+        const float f = w && in ? w[r] : 1.0f;
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const IO x = from[k];
+            v[k] = Io<IO>::ld(&x) * f * scale;
+        }
+#pragma unroll
+        for (int q = 0; q < (sizeof(IO) == 4 ? kParts : 1); ++q) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = take_f16(v[k]);
+            *(u32x2 *)(to + q * plane) = u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16};
+        }
     }
 }
 
@@ -594,23 +598,30 @@ __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
     m = M;
 }
 
-// 16 threads for a token join its n partial pairs.
+// A block of 256 joins the n partial pairs of TX tokens, 256 / TX threads for each.
+template <int TX>
 __global__ void __launch_bounds__(256) k_xent_join(const float2 *part, int64_t n, const float *at,
                                                    const int64_t *targets, int64_t ignore, int64_t T, int64_t V,
                                                    float *loss, float *lse) {
-    __shared__ float2 sh[16][16];
-    const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
-    const int64_t t = (int64_t)blockIdx.x * 16 + x;
+    constexpr int TY = 256 / TX;
+    __shared__ float2 sh[TY][TX];
+    const int x = threadIdx.x % TX, y = threadIdx.x / TX;
+    const int64_t t = (int64_t)blockIdx.x * TX + x;
     float m = -INFINITY, s = 0.0f;
     if (t < T)
-        for (int64_t j = y; j < n; j += 16) {
+        for (int64_t j = y; j < n; j += TY) {
             const float2 q = part[j * T + t];
             join(m, s, q.x, q.y);
         }
     sh[y][x] = make_float2(m, s);
-    __syncthreads();
+    for (int half = TY / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (y < half) {
+            join(m, s, sh[y + half][x].x, sh[y + half][x].y);
+            sh[y][x] = make_float2(m, s);
+        }
+    }
     if (y || t >= T) return;
-    for (int j = 1; j < 16; ++j) join(m, s, sh[j][x].x, sh[j][x].y);
     const float l = m + logf(s);
     lse[t] = l;
     const int64_t to = targets[t];
@@ -706,28 +717,14 @@ Tiling tiling(int64_t M, int64_t N, int64_t steps, bool may_split) {
     return best;
 }
 
-void set_tiles(ProductArgs &p, int tile) {
+template <Epi E, bool F16, bool TA = false, bool TB = false>
+hipError_t product(ProductArgs p, int tile, hipStream_t s) {
     p.tiles_m = (int32_t)blocks(p.M, tile);
     p.tiles_n = (int32_t)blocks(p.N, tile);
-}
-template <Epi E, bool F16>
-hipError_t product(const ProductPair &pair, int n, int tile, hipStream_t s) {
-    int32_t tiles = 0, splits = 0;
-    for (int k = 0; k < n; ++k) {
-        tiles = std::max(tiles, pair.p[k].tiles_m * pair.p[k].tiles_n);
-        splits = std::max(splits, pair.p[k].splits);
-    }
-    const dim3 grid((unsigned)tiles, (unsigned)splits, (unsigned)n);
-    if (tile == kBig) k_product<256, 256, 2, 4, E, F16><<<grid, 512, 0, s>>>(pair);
-    else k_product<128, 128, 2, 2, E, F16><<<grid, 256, 0, s>>>(pair);
+    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits);
+    if (tile == kBig) k_product<256, 256, 2, 4, E, F16, TA, TB><<<grid, 512, 0, s>>>(p);
+    else k_product<128, 128, 2, 2, E, F16, TA, TB><<<grid, 256, 0, s>>>(p);
     return hipGetLastError();
-}
-template <Epi E, bool F16>
-hipError_t product(const ProductArgs &p, int tile, hipStream_t s) {
-    ProductPair pair{};
-    pair.p[0] = p;
-    set_tiles(pair.p[0], tile);
-    return product<E, F16>(pair, 1, tile, s);
 }
 
 // A bump allocator over the workspace; with no base it only counts.
@@ -744,22 +741,22 @@ struct Arena {
 
 // What a call lays out in its workspace.
 struct Layout {
-    int planes, terms;         // of an operand, of a product
-    int64_t ldk, ldt, piece;   // padded dim, tokens; vocabulary rows of a piece
+    int planes, terms;           // of an operand, of a product
+    int64_t ldk, rows_t, piece;  // padded dim and tokens; vocabulary rows of a piece
     Tiling lse, out_w, out_h;
-    bool pack;                 // hidden and weight are copied: float32, or rows not in steps of 64
-    uint16_t *hidden, *weight;
+    bool pack;                   // weight is copied: float32, or rows not in steps of 64
+    uint16_t *hidden, *weight;   // copies for the logits
+    uint16_t *hidden_w, *piece_w, *g;  // for the gradients: hidden, a piece of weight, G
     int32_t *target;
     uint32_t *peak;
     int64_t peaks;
     float *at, *w, *all, *sum, *split_w, *split_h;
     float2 *part;
-    uint16_t *ht, *wt, *g, *gt;
     size_t bytes;
 };
 
-// G and G^T of a piece hold about 2^26 values each: 8192 tokens take pieces of 8192 rows, whose
-// three products are 512 and 1024 tiles of 256 x 256, whole rounds of the compute units.
+// G of a piece holds about 2^26 values: 8192 tokens take pieces of 8192 rows, whose three products
+// are 512 and 1024 tiles of 256 x 256, whole rounds of the compute units.
 constexpr int64_t kPieceValues = (int64_t)1 << 26;
 
 Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, char *ws) {
@@ -768,7 +765,7 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
     l.planes = io ? 1 : kParts;
     l.terms = io ? 1 : 3;
     l.ldk = up(K, kBK);
-    l.ldt = up(T, kBK);
+    l.rows_t = up(T, kBK);
     l.pack = !io || K % kBK != 0 || !aligned;
     l.target = a.take<int32_t>(T);
     // sized as if the operands had to be copied: their alignment is not known to the query
@@ -783,19 +780,16 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
         l.piece = std::min(up(V, kBig), std::max<int64_t>(1024, kPieceValues / std::max<int64_t>(T, 1) / kBig * kBig));
         const int64_t most = std::min(V, l.piece);
         l.peaks += blocks(V, l.piece);
-        l.out_w = tiling(K, most, l.ldt / kBK * l.terms, true);
+        l.out_w = tiling(K, most, l.rows_t / kBK * l.terms, true);
         l.out_h = tiling(K, T, up(most, kBK) / kBK * l.terms, true);
         l.w = a.take<float>(T);
         l.all = a.take<float>(1);
         l.sum = a.take<float>(V > l.piece ? T * K : 0);
-        l.ht = a.take<uint16_t>(K * l.ldt * l.planes);
-        l.wt = a.take<uint16_t>(K * up(most, kBK) * l.planes);
-        l.g = a.take<uint16_t>(T * up(most, kBK) * l.planes);
-        l.gt = a.take<uint16_t>(most * l.ldt * l.planes);
-        const int64_t sw = l.out_w.splits > 1 ? l.out_w.splits * most * K : 0;
-        const int64_t sh = l.out_h.splits > 1 ? l.out_h.splits * T * K : 0;
-        l.split_w = a.take<float>(sw);
-        l.split_h = a.take<float>(sh);
+        l.hidden_w = a.take<uint16_t>(l.rows_t * l.ldk * l.planes);
+        l.piece_w = a.take<uint16_t>(io ? most * l.ldk : 0);
+        l.g = a.take<uint16_t>(l.rows_t * up(most, kBK) * l.planes);
+        l.split_w = a.take<float>(l.out_w.splits > 1 ? l.out_w.splits * most * K : 0);
+        l.split_h = a.take<float>(l.out_h.splits > 1 ? l.out_h.splits * T * K : 0);
     }
     l.peak = a.take<uint32_t>(l.peaks);
     l.bytes = a.used;
@@ -803,20 +797,13 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
 }
 
 template <typename IO>
-hipError_t pack(const void *src, int64_t rows, int64_t cols, const uint32_t *peak, uint16_t *dst, int64_t ld,
-                hipStream_t s) {
-    k_pack<IO><<<dim3(blocks(ld, 512), (unsigned)std::min<int64_t>(rows, 65535)), 256, 0, s>>>((const IO *)src, rows, cols,
-                                                                                               peak, dst, ld, rows * ld);
-    return hipGetLastError();
-}
-template <typename IO>
-hipError_t pack_t(const void *src, int64_t rows, int64_t cols, const int32_t *target, const float *w,
-                  const uint32_t *peak, uint16_t *dst, int64_t ld, hipStream_t s) {
-    const dim3 grid(blocks(cols, 64), (unsigned)std::min<int64_t>(ld / 64, 65535));
-    if (cols % 2 == 0 && (uintptr_t)src % (2 * sizeof(IO)) == 0)
-        k_pack_t<IO, 2><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, target, w, peak, dst, ld, cols * ld);
+hipError_t pack(const void *src, int64_t rows, int64_t cols, int64_t rows_out, const int32_t *target, const float *w,
+                const uint32_t *peak, uint16_t *dst, int64_t ld, hipStream_t s) {
+    const dim3 grid((unsigned)std::min<int64_t>((rows_out * ld / 4 + 255) / 256, (int64_t)1 << 20));
+    if (cols % 4 == 0 && (uintptr_t)src % (4 * sizeof(IO)) == 0)
+        k_pack<IO, true><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, rows_out, target, w, peak, dst, ld, rows_out * ld);
     else
-        k_pack_t<IO, 1><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, target, w, peak, dst, ld, cols * ld);
+        k_pack<IO, false><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, rows_out, target, w, peak, dst, ld, rows_out * ld);
     return hipGetLastError();
 }
 template <typename IO>
@@ -840,22 +827,27 @@ hipError_t find_peak(const void *src, int64_t rows, int64_t cols, const int32_t 
 
 bool rows_aligned(const XentArgs &a) { return ((uintptr_t)a.hidden | (uintptr_t)a.weight) % 16 == 0; }
 
-// The operands of the logits: hidden and weight as they are, or their packed copies.
+// The operands of the logits: hidden and weight as they are, or their packed copies. `made`: a
+// copy of hidden that is there already.
 template <typename IO>
-hipError_t logits_operands(const XentArgs &a, const Layout &l, ProductArgs &p, hipStream_t s) {
-    const uint16_t *h = (const uint16_t *)a.hidden, *w = (const uint16_t *)a.weight;
+hipError_t logits_operands(const XentArgs &a, const Layout &l, const uint16_t *made, ProductArgs &p, hipStream_t s) {
+    const uint16_t *h = made ? made : (const uint16_t *)a.hidden, *w = (const uint16_t *)a.weight;
     if (sizeof(IO) == 4) {
         SSM_TRY(find_peak<IO>(a.hidden, a.T, a.K, l.target, nullptr, l.peak + kPeakH, s));
         SSM_TRY(find_peak<IO>(a.weight, a.V, a.K, nullptr, nullptr, l.peak + kPeakW, s));
     }
     if (l.pack) {
-        SSM_TRY(pack<IO>(a.hidden, a.T, a.K, l.peak + kPeakH, l.hidden, l.ldk, s));
-        SSM_TRY(pack<IO>(a.weight, a.V, a.K, l.peak + kPeakW, l.weight, l.ldk, s));
-        h = l.hidden;
+        const bool planes = sizeof(IO) == 4;
+        if (!made) {
+            SSM_TRY(pack<IO>(a.hidden, a.T, a.K, a.T, nullptr, nullptr, planes ? l.peak + kPeakH : nullptr, l.hidden, l.ldk, s));
+            h = l.hidden;
+        }
+        SSM_TRY(pack<IO>(a.weight, a.V, a.K, a.V, nullptr, nullptr, planes ? l.peak + kPeakW : nullptr, l.weight, l.ldk, s));
         w = l.weight;
     }
-    p.a = {w, l.ldk, a.V * l.ldk, l.peak + kPeakW};
-    p.b = {h, l.ldk, a.T * l.ldk, l.peak + kPeakH};
+    p.a = {w, l.ldk, a.V * l.ldk, l.peak + kPeakW, a.V};
+    p.b = {h, l.ldk, a.T * l.ldk, l.peak + kPeakH, a.T};
+    p.N = a.T;
     p.steps = (int32_t)(l.ldk / kBK);
     p.terms = l.terms;
     p.splits = 1;
@@ -872,56 +864,37 @@ hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
             k_xent_tokens<<<dim3(blocks(a.T, 256)), 256, 0, s>>>(a.targets, a.ignore, a.T, a.V, nullptr, nullptr, nullptr,
                                                                 l.target, nullptr, nullptr, l.peak, l.peaks);
         ProductArgs p{};
-        SSM_TRY(logits_operands<IO>(a, l, p, s));
+        SSM_TRY(logits_operands<IO>(a, l, nullptr, p, s));
         p.M = a.V;
-        p.N = a.T;
         p.part = l.part;
         p.at = l.at;
         SSM_TRY((product<Epi::Lse, sizeof(IO) == 4>(p, l.lse.tile, s)));
-        k_xent_join<<<dim3(blocks(a.T, 16)), 256, 0, s>>>(l.part, (int64_t)blocks(a.V, l.lse.tile) * 2, l.at, a.targets,
-                                                         a.ignore, a.T, a.V, a.loss, a.lse);
+        const int64_t n = (int64_t)blocks(a.V, l.lse.tile) * 2;
+        // whole lines of the partial pairs where there are many tokens, many threads for each
+        // where there are few
+        if (a.T >= 4096)
+            k_xent_join<16><<<dim3(blocks(a.T, 16)), 256, 0, s>>>(l.part, n, l.at, a.targets, a.ignore, a.T, a.V, a.loss, a.lse);
+        else
+            k_xent_join<2><<<dim3(blocks(a.T, 2)), 256, 0, s>>>(l.part, n, l.at, a.targets, a.ignore, a.T, a.V, a.loss, a.lse);
     }
     k_xent_mean<<<dim3(1), 1024, 0, s>>>(a.loss, a.targets, a.ignore, a.T, a.mean);
     return hipGetLastError();
 }
 
-// One of the gradients' products: C [N][M] = (sum +) A B^T, through partial sums over k where it
-// is split.
-struct Gradient {
-    ProductArgs p;
-    Tiling t;
-    JoinArgs join;
-};
-Gradient gradient(ProductArgs p, Tiling t, float *split, void *dst, bool bf16, float *sum, bool add) {
-    Gradient g{p, t, {}};
-    g.p.splits = t.splits;
-    g.p.ldc = p.M;
-    g.p.sum = sum;
-    g.p.add = add && t.splits == 1;
-    g.p.c = t.splits == 1 ? dst : split;
-    g.p.c_bf16 = bf16 && t.splits == 1;
-    g.p.cstride = p.M * p.N;
-    set_tiles(g.p, t.tile);
-    if (t.splits > 1) g.join = {split, t.splits, p.M * p.N, add ? sum : nullptr, dst, bf16};
-    return g;
-}
-// One or both of them, in one launch where their tiles agree.
-hipError_t run_gradients(const Gradient *g, int n, bool f16, hipStream_t s) {
-    if (n == 2 && g[0].t.tile != g[1].t.tile) {
-        SSM_TRY(run_gradients(g, 1, f16, s));
-        return run_gradients(g + 1, 1, f16, s);
-    }
-    ProductPair pair{};
-    JoinPair join{};
-    int64_t most = 0;
-    for (int k = 0; k < n; ++k) {
-        pair.p[k] = g[k].p;
-        join.j[k] = g[k].join;
-        most = std::max(most, g[k].join.count);
-    }
-    SSM_TRY((f16 ? product<Epi::Out, true>(pair, n, g[0].t.tile, s) : product<Epi::Out, false>(pair, n, g[0].t.tile, s)));
-    if (most > 0) k_join_splits<<<dim3(blocks(most, 256), (unsigned)n), 256, 0, s>>>(join);
-    return hipGetLastError();
+// One of the gradients' products: C [N][M] = (sum +) A B, through partial sums over k where it is
+// split. Returns what is left to join.
+template <bool TB>
+hipError_t gradient(ProductArgs p, bool f16, Tiling t, float *split, void *dst, bool bf16, float *sum, bool add,
+                    JoinArgs *join, hipStream_t s) {
+    p.splits = t.splits;
+    p.ldc = p.M;
+    p.sum = sum;
+    p.add = add && t.splits == 1;
+    p.c = t.splits == 1 ? dst : split;
+    p.c_bf16 = bf16 && t.splits == 1;
+    p.cstride = p.M * p.N;
+    *join = t.splits > 1 ? JoinArgs{split, t.splits, p.M * p.N, add ? sum : nullptr, dst, bf16} : JoinArgs{};
+    return f16 ? product<Epi::Out, true, true, TB>(p, t.tile, s) : product<Epi::Out, false, true, TB>(p, t.tile, s);
 }
 
 template <typename IO>
@@ -933,65 +906,66 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
     const Layout l = lay_out(a.T, a.K, a.V, io, true, rows_aligned(a), (char *)a.ws);
     k_xent_tokens<<<dim3(blocks(a.T, 256)), 256, 0, s>>>(a.targets, a.ignore, a.T, a.V, a.dloss, a.dmean, a.mean,
                                                         l.target, l.w, l.all, l.peak, l.peaks);
-    ProductArgs logits{};
-    SSM_TRY(logits_operands<IO>(a, l, logits, s));
-    logits.N = a.T;
-    logits.lse = a.lse;
     // one weight for all tokens: it is a factor at the end, and bfloat16 serves for the rest
     const bool f16 = sizeof(IO) == 4 || a.dloss;
-    logits.planes = f16 ? l.planes : 0;
     if (a.dweight) {
         uint32_t *peak = f16 ? l.peak + kPeakWH : nullptr;
         if (f16) SSM_TRY(find_peak<IO>(a.hidden, a.T, a.K, l.target, l.w, peak, s));
-        SSM_TRY(pack_t<IO>(a.hidden, a.T, a.K, l.target, f16 ? l.w : nullptr, peak, l.ht, l.ldt, s));
+        SSM_TRY(pack<IO>(a.hidden, a.T, a.K, l.rows_t, l.target, f16 ? l.w : nullptr, peak, l.hidden_w, l.ldk, s));
     }
+    ProductArgs logits{};
+    SSM_TRY(logits_operands<IO>(a, l, a.dweight && !f16 ? l.hidden_w : nullptr, logits, s));
+    logits.lse = a.lse;
+    logits.planes = f16 ? l.planes : 0;
+    logits.g = l.g;
+    logits.rows_g = l.rows_t;
     for (int64_t v0 = 0; v0 < a.V; v0 += l.piece) {
         const int64_t nv = std::min(l.piece, a.V - v0), ldg = up(nv, kBK);
         ProductArgs p = logits;
         p.a.p += v0 * l.ldk;
+        p.a.rows = nv;
         p.M = nv;
         p.v0 = v0;
-        p.g = l.g;
-        p.gt = a.dweight ? l.gt : nullptr;
         p.ldg = ldg;
-        p.ldgt = l.ldt;
-        p.gplane = a.T * ldg;
-        p.gtplane = nv * l.ldt;
+        p.gplane = l.rows_t * ldg;
         SSM_TRY((product<Epi::Dlogits, sizeof(IO) == 4>(p, tiling(nv, a.T, p.steps * l.terms, false).tile, s)));
-        Gradient grads[2];
-        int n = 0;
+        const Operand g{l.g, ldg, p.gplane, nullptr, l.rows_t};
+        JoinPair join{};
         if (a.dweight) {
             ProductArgs q{};
-            q.a = {l.ht, l.ldt, a.K * l.ldt, l.peak + kPeakWH};
-            q.b = {l.gt, l.ldt, nv * l.ldt, nullptr};
+            q.a = {l.hidden_w, l.ldk, l.rows_t * l.ldk, l.peak + kPeakWH, l.rows_t};
+            q.b = g;
             q.M = a.K;
             q.N = nv;
-            q.steps = (int32_t)(l.ldt / kBK);
+            q.steps = (int32_t)(l.rows_t / kBK);
             q.terms = l.terms;
             q.scale = f16 ? nullptr : l.all;
-            grads[n++] = gradient(q, l.out_w, l.split_w, (IO *)a.dweight + v0 * a.K, io, nullptr, false);
+            SSM_TRY(gradient<true>(q, f16, l.out_w, l.split_w, (IO *)a.dweight + v0 * a.K, io, nullptr, false, &join.j[0], s));
         }
         if (a.dhidden) {
-            // float32 weights have their peak from the logits; a piece's is read twice here
-            // while the caches still hold it
-            const IO *piece = (const IO *)a.weight + v0 * a.K;
-            uint32_t *peak = !f16 ? nullptr : l.peak + (sizeof(IO) == 4 ? (int64_t)kPeakW : kPeakPiece + v0 / l.piece);
-            if (f16 && sizeof(IO) == 2) SSM_TRY(find_peak<IO>(piece, nv, a.K, nullptr, nullptr, peak, s));
-            SSM_TRY(pack_t<IO>(piece, nv, a.K, nullptr, nullptr, peak, l.wt, ldg, s));
             ProductArgs q{};
-            q.a = {l.wt, ldg, a.K * ldg, peak};
-            q.b = {l.g, ldg, a.T * ldg, nullptr};
+            q.a = p.a;
+            if (f16 && sizeof(IO) == 2) {  // the logits' operand is bfloat16: a plane of this piece
+                const IO *piece = (const IO *)a.weight + v0 * a.K;
+                uint32_t *peak = l.peak + kPeakPiece + v0 / l.piece;
+                SSM_TRY(find_peak<IO>(piece, nv, a.K, nullptr, nullptr, peak, s));
+                SSM_TRY(pack<IO>(piece, nv, a.K, nv, nullptr, nullptr, peak, l.piece_w, l.ldk, s));
+                q.a = {l.piece_w, l.ldk, nv * l.ldk, peak, nv};
+            }
+            q.b = g;
             q.row = l.w;
             q.M = a.K;
             q.N = a.T;
             q.steps = (int32_t)(ldg / kBK);
             q.terms = l.terms;
             const bool end = v0 + nv == a.V;
-            grads[n++] = gradient(q, l.out_h, l.split_h, end ? a.dhidden : l.sum, end && io, l.sum, v0 > 0);
+            SSM_TRY(gradient<false>(q, f16, l.out_h, l.split_h, end ? a.dhidden : l.sum, end && io, l.sum, v0 > 0,
+                                    &join.j[1], s));
         }
-        SSM_TRY(run_gradients(grads, n, f16, s));
+        const int64_t most = std::max(join.j[0].count, join.j[1].count);
+        if (most > 0) k_join_splits<<<dim3(blocks(most, 256), 2), 256, 0, s>>>(join);
     }
-    return hipSuccess;
+    return hipGetLastError();
 }
 
 }  // namespace
