@@ -429,56 +429,56 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
         const float scale = p.scale ? *p.scale : 1.0f;
         const size_t eb = p.c_bf16 ? 2 : 4;
         char *const c = (char *)p.c + (size_t)split * p.cstride * eb;
-        if (p.ldc % 4 == 0 && ((uintptr_t)c & (4 * eb - 1)) == 0) {
-            // four neighbours of a row at a time
+        // A wave turns 32 rows of C at a time in LDS and writes them along the rows: four elements
+        // a lane where every row starts on four, else one. (Writing each lane's own four, a row
+        // apart from the next lane's, took 112 us for 262 MB, and 201 us for 142 MB element by
+        // element.)
+        const bool wide = p.ldc % 4 == 0 && ((uintptr_t)c & (4 * eb - 1)) == 0;
+        constexpr int kWide = S::TM * 32, kTurn = kWide + 4;
+        SSM_LDS float *mine = (SSM_LDS float *)lds + (wn * WM + wm) * 32 * kTurn;
+        static_assert(S::kWaves * 32 * kTurn * 4 <= S::kLds, "the turned rows fit");
 #pragma unroll
-            for (int j = 0; j < S::TN; ++j) {
-                const int64_t n = nw + j * 32;
-                if (n >= p.N) continue;
-                const float row = p.row ? p.row[n] : scale;
+        for (int j = 0; j < S::TN; ++j) {
+            const int64_t first = n0 + (wn * S::TN + j) * 32, mb = m0 + wm * kWide;
+            typedef float f32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-                for (int i = 0; i < S::TM; ++i)
+            for (int i = 0; i < S::TM; ++i)
 #pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const int64_t m = mw + i * 32 + 2 * e;
-                        if (m >= p.M) continue;  // M = ldc: all four or none
-                        const int64_t at = n * p.ldc + m;
-                        float v[4];
+                for (int e = 0; e < 16; e += 4)
+                    *(SSM_LDS f32x4 *)(mine + (lane & 31) * kTurn + 4 * half + i * 32 + 2 * e) =
+                        f32x4{value(acc[i][j][e]), value(acc[i][j][e + 1]), value(acc[i][j][e + 2]), value(acc[i][j][e + 3])};
+            __syncthreads();
+            if (wide) {
+                constexpr int kLanes = kWide / 4, kRows = 64 / kLanes;
+                const int64_t m = mb + lane % kLanes * 4;
+#pragma unroll 4
+                for (int r = lane / kLanes; r < 32; r += kRows) {
+                    const int64_t n = first + r, at = n * p.ldc + m;
+                    if (n >= p.N || m >= p.M) break;  // M = ldc: all four or none
+                    const f32x4 from = *(const SSM_LDS f32x4 *)(mine + r * kTurn + lane % kLanes * 4);
+                    const float row = p.row ? p.row[n] : scale;
+                    float v[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) v[k] = value(acc[i][j][e + k]) * row;
-                        if (p.add) {
-                            const float4 s = *(const float4 *)(p.sum + at);
-                            v[0] += s.x, v[1] += s.y, v[2] += s.z, v[3] += s.w;
-                        }
-                        if (p.c_bf16)
-                            *(u32x2 *)(c + at * 2) = u32x2{f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
-                                                           f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
-                        else
-                            *(float4 *)(c + at * 4) = make_float4(v[0], v[1], v[2], v[3]);
+                    for (int k = 0; k < 4; ++k) v[k] = from[k] * row;
+                    if (p.add) {
+                        const float4 s = *(const float4 *)(p.sum + at);
+                        v[0] += s.x, v[1] += s.y, v[2] += s.z, v[3] += s.w;
                     }
-            }
-        } else {
-            // Rows that do not start on four elements: a wave turns 32 of its rows in LDS and
-            // writes them element by element, a lane beside the next. (The lanes' own four
-            // elements, each row apart, took 201 us for the 142 MB that this writes in 60.)
-            constexpr int kTurn = S::TM * 32 + 1;
-            SSM_LDS float *mine = (SSM_LDS float *)lds + (wn * WM + wm) * 32 * kTurn;
-            static_assert(S::kWaves * 32 * kTurn * 4 <= S::kLds, "the turned rows fit");
-#pragma unroll
-            for (int j = 0; j < S::TN; ++j) {
-#pragma unroll
-                for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        mine[(lane & 31) * kTurn + 4 * half + i * 32 + 8 * (e / 4) + e % 4] = value(acc[i][j][e]);
-                __syncthreads();
-                for (int r = 0; r < 32; ++r) {
-                    const int64_t n = n0 + (wn * S::TN + j) * 32 + r;
-                    if (n >= p.N) break;
+                    if (p.c_bf16)
+                        *(u32x2 *)(c + at * 2) = u32x2{f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                                                       f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
+                    else
+                        *(float4 *)(c + at * 4) = make_float4(v[0], v[1], v[2], v[3]);
+                }
+            } else {
+                const int last = (int)min((int64_t)32, p.N - first);
+#pragma unroll 4
+                for (int r = 0; r < last; ++r) {
+                    const int64_t n = first + r;
                     const float row = p.row ? p.row[n] : scale;
 #pragma unroll
-                    for (int i = 0; i < S::TM * 32; i += 64) {
-                        const int64_t m = m0 + wm * S::TM * 32 + i + lane, at = n * p.ldc + m;
+                    for (int i = 0; i < kWide; i += 64) {
+                        const int64_t m = mb + i + lane, at = n * p.ldc + m;
                         if (m >= p.M) continue;
                         float v = mine[r * kTurn + i + lane] * row;
                         if (p.add) v += p.sum[at];
@@ -486,8 +486,8 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
                         else ((float *)c)[at] = v;
                     }
                 }
-                __syncthreads();
             }
+            __syncthreads();
         }
     }
 }
@@ -512,6 +512,17 @@ __global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64
             const IO *at = src + r * cols + c;
             if (WIDE) {
                 from = *(const iov *)at;
+            } else if (sizeof(IO) == 2 && ((uintptr_t)src & 3) == 0 && c + 4 <= cols && r * cols + c + 6 <= rows * cols) {
+                // bfloat16 rows that start anywhere: the whole words around the four
+                const int64_t first = r * cols + c;
+                const uint32_t *word = (const uint32_t *)src + (first >> 1);
+                uint32_t lo = word[0], hi = word[1];
+                if (first & 1) {
+                    const uint32_t end = word[2];
+                    lo = lo >> 16 | hi << 16;
+                    hi = hi >> 16 | end << 16;
+                }
+                from[0] = (IO)(lo & 0xffffu), from[1] = (IO)(lo >> 16), from[2] = (IO)(hi & 0xffffu), from[3] = (IO)(hi >> 16);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -707,7 +718,7 @@ Tiling tiling(int64_t M, int64_t N, int64_t steps, bool may_split) {
     double least = 0;
     for (const int tile : {kSmall, kBig}) {
         const int64_t n = (int64_t)blocks(M, tile) * blocks(N, tile), room = 2 * kCus / n;
-        const int64_t s = !may_split || tile == kBig ? 1 : std::max<int64_t>(1, std::min(std::min(room, steps / 8), (int64_t)16));
+        const int64_t s = !may_split || tile == kBig ? 1 : std::max<int64_t>(1, std::min(std::min(room, steps / 8), (int64_t)64));
         const double time = (double)blocks(n * s, kCus) / (double)s * (tile == kBig ? 3.0 : 1.0);
         if (!best.tile || time < least) {
             best = {tile, (int)s};
