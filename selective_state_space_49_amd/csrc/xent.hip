@@ -58,7 +58,26 @@ struct Operand {
     int64_t rows;
 };
 
+// The tokens' targets and the weights of their losses, as the caller gave them.
+struct Tokens {
+    const int64_t *targets;
+    int64_t ignore, V;
+    const float *dloss, *dmean, *mean;
+    // The vocabulary row; -1: ignored, -2: out of range.
+    __device__ __forceinline__ int32_t target(int64_t t) const {
+        const int64_t y = targets[t];
+        return y == ignore ? -1 : y >= 0 && y < V ? (int32_t)y : -2;
+    }
+    // The weight that every token has without dloss.
+    __device__ __forceinline__ float same() const { return dmean ? *dmean * mean[1] : 0.0f; }
+    __device__ __forceinline__ float weight(int64_t t, float same) const {
+        const int32_t y = target(t);
+        return y == -1 ? 0.0f : y == -2 ? NAN : (dloss ? dloss[t] : 0.0f) + same;
+    }
+};
+
 enum class Epi { Lse, Dlogits, Out };
+enum class Factor { None, Same, Row };  // of Out: the tokens' one weight, the weight of token n
 
 struct ProductArgs {
     Operand a, b;
@@ -68,8 +87,7 @@ struct ProductArgs {
     int32_t planes;         // Dlogits: float16 planes of G, 0: bfloat16
     int32_t tiles_m, tiles_n, splits;
     // Lse, Dlogits: m = vocabulary row - v0, n = token
-    const int64_t *targets; // Lse: [N]
-    const int32_t *target;  // Dlogits: [N]: vocabulary row, -1 ignored, -2 out of range
+    Tokens tokens;
     float2 *part;           // Lse: [tiles_m * waves][N]
     float *at;              // Lse: [N] logit of the target
     const float *lse;       // Dlogits: [N]
@@ -82,8 +100,7 @@ struct ProductArgs {
     bool c_bf16;
     float *sum;             // with `add`: C = sum + product
     bool add;
-    const float *row;       // Out: a factor for each n, or null
-    const float *scale;     // Out: a factor, or null
+    Factor factor;
 };
 
 // The float16 that holds the most of v, and what is left of it.
@@ -370,7 +387,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
             s += __shfl_xor(s, 32);
             if (n >= p.N) continue;
             if (half == 0) p.part[slot * p.N + n] = make_float2(top, s);
-            const int64_t t = p.targets[n] - mw;  // the lane's rows are t = 32 i + 8 (e / 4) + e % 4
+            const int64_t t = p.tokens.targets[n] - mw;  // the lane's rows are t = 32 i + 8 (e / 4) + e % 4
             if (t >= 0 && t < S::TM * 32 && (t & 4) == 0) {
 #pragma unroll
                 for (int i = 0; i < S::TM; ++i)
@@ -391,7 +408,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
             for (int j = 0; j < S::TN; ++j) {
                 const int64_t n = nw + j * 32;
                 const bool in = n < p.N;
-                const int32_t target = in ? p.target[n] : -1;
+                const int32_t target = in ? p.tokens.target(n) : -1;
                 const float lse = in ? p.lse[n] : 0.0f;
                 const float scale = target == -2 ? NAN : unit;  // out of range: loud
                 const int t = (int)max((int64_t)-1, min((int64_t)S::TM * 32, target - p.v0 - mw));
@@ -426,13 +443,13 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
         }
     }
     if constexpr (E == Epi::Out) {
-        const float scale = p.scale ? *p.scale : 1.0f;
+        const float same = p.factor == Factor::None ? 1.0f : p.tokens.same();
         const size_t eb = p.c_bf16 ? 2 : 4;
         char *const c = (char *)p.c + (size_t)split * p.cstride * eb;
         // A wave turns 32 rows of C at a time in LDS and writes them along the rows: four elements
-        // a lane where every row starts on four, else one. (Writing each lane's own four, a row
-        // apart from the next lane's, took 112 us for 262 MB, and 201 us for 142 MB element by
-        // element.)
+        // a lane where every row starts on four, else one: 99 us for 262 MB and 128 us for 142 MB.
+        // (Writing each lane's own four, a row apart from the next lane's, took 112 us for the
+        // 262 MB, and 201 us for the 142 MB element by element.)
         const bool wide = p.ldc % 4 == 0 && ((uintptr_t)c & (4 * eb - 1)) == 0;
         constexpr int kWide = S::TM * 32, kTurn = kWide + 4;
         SSM_LDS float *mine = (SSM_LDS float *)lds + (wn * WM + wm) * 32 * kTurn;
@@ -456,7 +473,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
                     const int64_t n = first + r, at = n * p.ldc + m;
                     if (n >= p.N || m >= p.M) break;  // M = ldc: all four or none
                     const f32x4 from = *(const SSM_LDS f32x4 *)(mine + r * kTurn + lane % kLanes * 4);
-                    const float row = p.row ? p.row[n] : scale;
+                    const float row = p.factor == Factor::Row ? p.tokens.weight(n, same) : same;
                     float v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[k] = from[k] * row;
@@ -475,7 +492,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
 #pragma unroll 4
                 for (int r = 0; r < last; ++r) {
                     const int64_t n = first + r;
-                    const float row = p.row ? p.row[n] : scale;
+                    const float row = p.factor == Factor::Row ? p.tokens.weight(n, same) : same;
 #pragma unroll
                     for (int i = 0; i < kWide; i += 64) {
                         const int64_t m = mb + i + lane, at = n * p.ldc + m;
@@ -494,19 +511,19 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
 
 // ---------------------------------------------------------------- operands
 // dst[plane][r][ld] for r < rows_out: src [rows][cols] and 0 past its columns and rows. With a
-// peak, its scaled planes; without one, a copy of bfloat16. The rows whose target is ignored
-// are 0: they may hold anything, and 0 times it must not reach a sum. w: a factor for each row
-// of the planes. Four columns a thread.
+// peak, its scaled planes; without one, a copy of bfloat16. With `mask`, a row is a token's: it
+// is 0 where the token is ignored, since it may hold anything there and 0 times it must not
+// reach a sum, and with `weigh` it is multiplied by the token's weight. Four columns a thread.
 template <typename IO, bool WIDE>
 __global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64_t cols, int64_t rows_out,
-                                              const int32_t *target, const float *w, const uint32_t *peak, uint16_t *dst,
-                                              int64_t ld, int64_t plane) {
+                                              Tokens tokens, bool mask, bool weigh, const uint32_t *peak,
+                                              uint16_t *dst, int64_t ld, int64_t plane) {
     typedef IO iov __attribute__((ext_vector_type(4)));
     const int64_t across = ld / 4, total = rows_out * across;
-    const float scale = peak ? exp2i(scale_exp(*peak)) : 1.0f;
+    const float scale = peak ? exp2i(scale_exp(*peak)) : 1.0f, same = weigh ? tokens.same() : 0.0f;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
         const int64_t r = e / across, c = (e - r * across) * 4;
-        const bool in = r < rows && c < cols && !(target && target[r] == -1);
+        const bool in = r < rows && c < cols && !(mask && tokens.target(r) == -1);
         iov from = {IO(0), IO(0), IO(0), IO(0)};
         if (in) {
             const IO *at = src + r * cols + c;
@@ -534,7 +551,7 @@ __global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64
             *(u32x2 *)to = u32x2{(uint32_t)from[0] | (uint32_t)from[1] << 16, (uint32_t)from[2] | (uint32_t)from[3] << 16};
             continue;
         }
-        const float f = w && in ? w[r] : 1.0f;
+        const float f = weigh && in ? tokens.weight(r, same) : 1.0f;
         float v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -551,22 +568,24 @@ __global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64
     }
 }
 
-// peak = the bits of the largest finite |src| (times the row's w) over the rows whose target
-// is not ignored. An integer maximum: its order does not matter. A block of 1024 has
-// 1024 / across rows at a time, N columns a lane; few blocks, since each ends on one address.
+// peak = the bits of the largest finite |src|; with `mask` over the rows of tokens that are not
+// ignored, with `weigh` times their weights. An integer maximum: its order does not matter. A
+// block of 1024 has 1024 / across rows at a time, N columns a lane; few blocks, since each ends
+// on one address.
 constexpr int kPeakThreads = 1024, kPeakBlocks = 256;
 template <typename IO, int N>
 __global__ void __launch_bounds__(kPeakThreads) k_peak(const IO *src, int64_t rows, int64_t cols, int across,
-                                                       const int32_t *target, const float *w, uint32_t *peak) {
+                                                       Tokens tokens, bool mask, bool weigh, uint32_t *peak) {
     typedef IO iov __attribute__((ext_vector_type(N)));
     __shared__ uint32_t sh[kPeakThreads / 64];
     const int down = kPeakThreads / across;
     const int64_t c0 = (int64_t)(threadIdx.x % across) * N;
+    const float same = weigh ? tokens.same() : 0.0f;
     uint32_t top = 0;
 #pragma unroll 4
     for (int64_t r = (int64_t)blockIdx.x * down + threadIdx.x / across; r < rows; r += (int64_t)gridDim.x * down) {
-        if (target && target[r] == -1) continue;
-        const float f = w ? w[r] : 1.0f;
+        if (mask && tokens.target(r) == -1) continue;
+        const float f = weigh ? tokens.weight(r, same) : 1.0f;
         for (int64_t c = c0; c < cols; c += across * N) {
             const iov v = *(const iov *)(src + r * cols + c);
 #pragma unroll
@@ -585,20 +604,9 @@ __global__ void __launch_bounds__(kPeakThreads) k_peak(const IO *src, int64_t ro
     if (top) atomicMax(peak, top);
 }
 
-// target[t] = the row, -1 where ignored, -2 where out of range; w[t] = the loss's weight, all[0]
-// the one that every token has without dloss; the peaks start at 0.
-__global__ void __launch_bounds__(256) k_xent_tokens(const int64_t *targets, int64_t ignore, int64_t T, int64_t V,
-                                                     const float *dloss, const float *dmean, const float *mean,
-                                                     int32_t *target, float *w, float *all, uint32_t *peak, int64_t n_peaks) {
-    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    for (int64_t k = t; k < n_peaks; k += (int64_t)gridDim.x * 256) peak[k] = 0;
-    const float same = dmean ? *dmean * mean[1] : 0.0f;
-    if (t == 0 && all) *all = same;
-    if (t >= T) return;
-    const int64_t y = targets[t];
-    const int32_t to = y == ignore ? -1 : y >= 0 && y < V ? (int32_t)y : -2;
-    target[t] = to;
-    if (w) w[t] = to == -1 ? 0.0f : to == -2 ? NAN : (dloss ? dloss[t] : 0.0f) + same;
+__global__ void __launch_bounds__(256) k_clear_peaks(uint32_t *peak, int64_t n) {
+    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (k < n) peak[k] = 0;
 }
 
 // (m, s) += (m2, s2): sums of exponentials under their maxima.
@@ -612,8 +620,7 @@ __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
 // A block of 256 joins the n partial pairs of TX tokens, 256 / TX threads for each.
 template <int TX>
 __global__ void __launch_bounds__(256) k_xent_join(const float2 *part, int64_t n, const float *at,
-                                                   const int64_t *targets, int64_t ignore, int64_t T, int64_t V,
-                                                   float *loss, float *lse) {
+                                                   Tokens tokens, int64_t T, float *loss, float *lse) {
     constexpr int TY = 256 / TX;
     __shared__ float2 sh[TY][TX];
     const int x = threadIdx.x % TX, y = threadIdx.x / TX;
@@ -635,8 +642,8 @@ __global__ void __launch_bounds__(256) k_xent_join(const float2 *part, int64_t n
     if (y || t >= T) return;
     const float l = m + logf(s);
     lse[t] = l;
-    const int64_t to = targets[t];
-    loss[t] = to == ignore ? 0.0f : to >= 0 && to < V ? l - at[t] : NAN;
+    const int32_t to = tokens.target(t);
+    loss[t] = to == -1 ? 0.0f : to >= 0 ? l - at[t] : NAN;
 }
 
 // mean[0] = mean loss over the tokens that are not ignored, mean[1] = 1 / their number.
@@ -758,10 +765,9 @@ struct Layout {
     bool pack;                   // weight is copied: float32, or rows not in steps of 64
     uint16_t *hidden, *weight;   // copies for the logits
     uint16_t *hidden_w, *piece_w, *g;  // for the gradients: hidden, a piece of weight, G
-    int32_t *target;
     uint32_t *peak;
     int64_t peaks;
-    float *at, *w, *all, *sum, *split_w, *split_h;
+    float *at, *sum, *split_w, *split_h;
     float2 *part;
     size_t bytes;
 };
@@ -778,7 +784,6 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
     l.ldk = up(K, kBK);
     l.rows_t = up(T, kBK);
     l.pack = !io || K % kBK != 0 || !aligned;
-    l.target = a.take<int32_t>(T);
     // sized as if the operands had to be copied: their alignment is not known to the query
     l.hidden = a.take<uint16_t>(T * l.ldk * l.planes);
     l.weight = a.take<uint16_t>(V * l.ldk * l.planes);
@@ -793,8 +798,6 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
         l.peaks += blocks(V, l.piece);
         l.out_w = tiling(K, most, l.rows_t / kBK * l.terms, true);
         l.out_h = tiling(K, T, up(most, kBK) / kBK * l.terms, true);
-        l.w = a.take<float>(T);
-        l.all = a.take<float>(1);
         l.sum = a.take<float>(V > l.piece ? T * K : 0);
         l.hidden_w = a.take<uint16_t>(l.rows_t * l.ldk * l.planes);
         l.piece_w = a.take<uint16_t>(io ? most * l.ldk : 0);
@@ -808,25 +811,27 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
 }
 
 template <typename IO>
-hipError_t pack(const void *src, int64_t rows, int64_t cols, int64_t rows_out, const int32_t *target, const float *w,
+hipError_t pack(const void *src, int64_t rows, int64_t cols, int64_t rows_out, const Tokens &tokens, bool mask, bool weigh,
                 const uint32_t *peak, uint16_t *dst, int64_t ld, hipStream_t s) {
     const dim3 grid((unsigned)std::min<int64_t>((rows_out * ld / 4 + 255) / 256, (int64_t)1 << 20));
     if (cols % 4 == 0 && (uintptr_t)src % (4 * sizeof(IO)) == 0)
-        k_pack<IO, true><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, rows_out, target, w, peak, dst, ld, rows_out * ld);
+        k_pack<IO, true><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, rows_out, tokens, mask, weigh, peak, dst, ld,
+                                                  rows_out * ld);
     else
-        k_pack<IO, false><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, rows_out, target, w, peak, dst, ld, rows_out * ld);
+        k_pack<IO, false><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, rows_out, tokens, mask, weigh, peak, dst, ld,
+                                                  rows_out * ld);
     return hipGetLastError();
 }
 template <typename IO>
-hipError_t find_peak(const void *src, int64_t rows, int64_t cols, const int32_t *target, const float *w, uint32_t *peak,
+hipError_t find_peak(const void *src, int64_t rows, int64_t cols, const Tokens &tokens, bool mask, bool weigh, uint32_t *peak,
                      hipStream_t s) {
     const bool wide = cols % 4 == 0 && (uintptr_t)src % (4 * sizeof(IO)) == 0;
     const int64_t lanes = wide ? cols / 4 : cols;
     int across = 16;
     while (across < lanes && across < kPeakThreads) across *= 2;
     const dim3 grid((unsigned)std::min<int64_t>(blocks(rows, kPeakThreads / across), kPeakBlocks));
-    if (wide) k_peak<IO, 4><<<grid, kPeakThreads, 0, s>>>((const IO *)src, rows, cols, across, target, w, peak);
-    else k_peak<IO, 1><<<grid, kPeakThreads, 0, s>>>((const IO *)src, rows, cols, across, target, w, peak);
+    if (wide) k_peak<IO, 4><<<grid, kPeakThreads, 0, s>>>((const IO *)src, rows, cols, across, tokens, mask, weigh, peak);
+    else k_peak<IO, 1><<<grid, kPeakThreads, 0, s>>>((const IO *)src, rows, cols, across, tokens, mask, weigh, peak);
     return hipGetLastError();
 }
 
@@ -844,16 +849,18 @@ template <typename IO>
 hipError_t logits_operands(const XentArgs &a, const Layout &l, const uint16_t *made, ProductArgs &p, hipStream_t s) {
     const uint16_t *h = made ? made : (const uint16_t *)a.hidden, *w = (const uint16_t *)a.weight;
     if (sizeof(IO) == 4) {
-        SSM_TRY(find_peak<IO>(a.hidden, a.T, a.K, l.target, nullptr, l.peak + kPeakH, s));
-        SSM_TRY(find_peak<IO>(a.weight, a.V, a.K, nullptr, nullptr, l.peak + kPeakW, s));
+        SSM_TRY(find_peak<IO>(a.hidden, a.T, a.K, p.tokens, true, false, l.peak + kPeakH, s));
+        SSM_TRY(find_peak<IO>(a.weight, a.V, a.K, p.tokens, false, false, l.peak + kPeakW, s));
     }
     if (l.pack) {
         const bool planes = sizeof(IO) == 4;
         if (!made) {
-            SSM_TRY(pack<IO>(a.hidden, a.T, a.K, a.T, nullptr, nullptr, planes ? l.peak + kPeakH : nullptr, l.hidden, l.ldk, s));
+            SSM_TRY(pack<IO>(a.hidden, a.T, a.K, a.T, p.tokens, false, false, planes ? l.peak + kPeakH : nullptr, l.hidden,
+                             l.ldk, s));
             h = l.hidden;
         }
-        SSM_TRY(pack<IO>(a.weight, a.V, a.K, a.V, nullptr, nullptr, planes ? l.peak + kPeakW : nullptr, l.weight, l.ldk, s));
+        SSM_TRY(pack<IO>(a.weight, a.V, a.K, a.V, p.tokens, false, false, planes ? l.peak + kPeakW : nullptr, l.weight,
+                         l.ldk, s));
         w = l.weight;
     }
     p.a = {w, l.ldk, a.V * l.ldk, l.peak + kPeakW, a.V};
@@ -862,8 +869,6 @@ hipError_t logits_operands(const XentArgs &a, const Layout &l, const uint16_t *m
     p.steps = (int32_t)(l.ldk / kBK);
     p.terms = l.terms;
     p.splits = 1;
-    p.target = l.target;
-    p.targets = a.targets;
     return hipSuccess;
 }
 
@@ -871,10 +876,9 @@ template <typename IO>
 hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
     if (a.T > 0) {
         const Layout l = lay_out(a.T, a.K, a.V, io, false, rows_aligned(a), (char *)a.ws);
-        if (!io)  // for the peaks
-            k_xent_tokens<<<dim3(blocks(a.T, 256)), 256, 0, s>>>(a.targets, a.ignore, a.T, a.V, nullptr, nullptr, nullptr,
-                                                                l.target, nullptr, nullptr, l.peak, l.peaks);
+        if (!io) k_clear_peaks<<<dim3(blocks(l.peaks, 256)), 256, 0, s>>>(l.peak, l.peaks);
         ProductArgs p{};
+        p.tokens = {a.targets, a.ignore, a.V, nullptr, nullptr, nullptr};
         SSM_TRY(logits_operands<IO>(a, l, nullptr, p, s));
         p.M = a.V;
         p.part = l.part;
@@ -884,9 +888,9 @@ hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
         // whole lines of the partial pairs where there are many tokens, many threads for each
         // where there are few
         if (a.T >= 4096)
-            k_xent_join<16><<<dim3(blocks(a.T, 16)), 256, 0, s>>>(l.part, n, l.at, a.targets, a.ignore, a.T, a.V, a.loss, a.lse);
+            k_xent_join<16><<<dim3(blocks(a.T, 16)), 256, 0, s>>>(l.part, n, l.at, p.tokens, a.T, a.loss, a.lse);
         else
-            k_xent_join<2><<<dim3(blocks(a.T, 2)), 256, 0, s>>>(l.part, n, l.at, a.targets, a.ignore, a.T, a.V, a.loss, a.lse);
+            k_xent_join<2><<<dim3(blocks(a.T, 2)), 256, 0, s>>>(l.part, n, l.at, p.tokens, a.T, a.loss, a.lse);
     }
     k_xent_mean<<<dim3(1), 1024, 0, s>>>(a.loss, a.targets, a.ignore, a.T, a.mean);
     return hipGetLastError();
@@ -915,16 +919,17 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
         return hipGetLastError();
     }
     const Layout l = lay_out(a.T, a.K, a.V, io, true, rows_aligned(a), (char *)a.ws);
-    k_xent_tokens<<<dim3(blocks(a.T, 256)), 256, 0, s>>>(a.targets, a.ignore, a.T, a.V, a.dloss, a.dmean, a.mean,
-                                                        l.target, l.w, l.all, l.peak, l.peaks);
+    const Tokens tokens{a.targets, a.ignore, a.V, a.dloss, a.dmean, a.mean};
     // one weight for all tokens: it is a factor at the end, and bfloat16 serves for the rest
     const bool f16 = sizeof(IO) == 4 || a.dloss;
+    if (f16) k_clear_peaks<<<dim3(blocks(l.peaks, 256)), 256, 0, s>>>(l.peak, l.peaks);
     if (a.dweight) {
         uint32_t *peak = f16 ? l.peak + kPeakWH : nullptr;
-        if (f16) SSM_TRY(find_peak<IO>(a.hidden, a.T, a.K, l.target, l.w, peak, s));
-        SSM_TRY(pack<IO>(a.hidden, a.T, a.K, l.rows_t, l.target, f16 ? l.w : nullptr, peak, l.hidden_w, l.ldk, s));
+        if (f16) SSM_TRY(find_peak<IO>(a.hidden, a.T, a.K, tokens, true, true, peak, s));
+        SSM_TRY(pack<IO>(a.hidden, a.T, a.K, l.rows_t, tokens, true, f16, peak, l.hidden_w, l.ldk, s));
     }
     ProductArgs logits{};
+    logits.tokens = tokens;
     SSM_TRY(logits_operands<IO>(a, l, a.dweight && !f16 ? l.hidden_w : nullptr, logits, s));
     logits.lse = a.lse;
     logits.planes = f16 ? l.planes : 0;
@@ -944,27 +949,29 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
         JoinPair join{};
         if (a.dweight) {
             ProductArgs q{};
+            q.tokens = tokens;
             q.a = {l.hidden_w, l.ldk, l.rows_t * l.ldk, l.peak + kPeakWH, l.rows_t};
             q.b = g;
             q.M = a.K;
             q.N = nv;
             q.steps = (int32_t)(l.rows_t / kBK);
             q.terms = l.terms;
-            q.scale = f16 ? nullptr : l.all;
+            q.factor = f16 ? Factor::None : Factor::Same;
             SSM_TRY(gradient<true>(q, f16, l.out_w, l.split_w, (IO *)a.dweight + v0 * a.K, io, nullptr, false, &join.j[0], s));
         }
         if (a.dhidden) {
             ProductArgs q{};
+            q.tokens = tokens;
             q.a = p.a;
             if (f16 && sizeof(IO) == 2) {  // the logits' operand is bfloat16: a plane of this piece
                 const IO *piece = (const IO *)a.weight + v0 * a.K;
                 uint32_t *peak = l.peak + kPeakPiece + v0 / l.piece;
-                SSM_TRY(find_peak<IO>(piece, nv, a.K, nullptr, nullptr, peak, s));
-                SSM_TRY(pack<IO>(piece, nv, a.K, nv, nullptr, nullptr, peak, l.piece_w, l.ldk, s));
+                SSM_TRY(find_peak<IO>(piece, nv, a.K, tokens, false, false, peak, s));
+                SSM_TRY(pack<IO>(piece, nv, a.K, nv, tokens, false, false, peak, l.piece_w, l.ldk, s));
                 q.a = {l.piece_w, l.ldk, nv * l.ldk, peak, nv};
             }
             q.b = g;
-            q.row = l.w;
+            q.factor = Factor::Row;
             q.M = a.K;
             q.N = a.T;
             q.steps = (int32_t)(ldg / kBK);
