@@ -44,7 +44,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBK = 64;        // k per stage
 constexpr int kParts = 2;      // float16 planes of a float32 operand
-enum { kPeakW, kPeakH, kPeakWH, kPeakPiece };  // peaks of weight, hidden, w hidden, pieces of weight
+enum { kPeakW, kPeakH, kPeakWH, kPeaks };  // peaks of weight, hidden, w hidden
+constexpr int kPeakThreads = 1024, kPeakBlocks = 256;
 constexpr int kPeak = 14;      // a scaled array's largest value is in 2^kPeak .. 2^(kPeak + 1)
 constexpr uint32_t kRsrcWord3 = 0x00027000;  // raw buffer, 32-bit data
 
@@ -90,6 +91,7 @@ struct ProductArgs {
     Tokens tokens;
     float2 *part;           // Lse: [tiles_m * waves][N]
     float *at;              // Lse: [N] logit of the target
+    uint32_t *done;         // Lse: set to 0 for the launch that joins
     const float *lse;       // Dlogits: [N]
     int64_t v0;
     uint16_t *g;            // Dlogits: G [rows_g][ldg], planes apart; 0 outside of N x M
@@ -122,16 +124,16 @@ __device__ __forceinline__ float unscale(const Operand &o) {
 }
 
 // Waves stand WM x WN over a BM x BN tile; each makes TM x TN blocks of 32 x 32 with
-// v_mfma_f32_32x32x16. Operand tiles go from global memory straight to LDS, 16 bytes a lane,
-// double buffered.
-template <int BM, int BN, int WM, int WN>
+// v_mfma_f32_32x32x16. Operand tiles go from global memory straight to LDS, 16 bytes a lane, into
+// one of D buffers.
+template <int BM, int BN, int WM, int WN, int D>
 struct Shape {
     static constexpr int kThreads = 64 * WM * WN;
     static constexpr int kWaves = WM * WN;
     static constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
     static constexpr int kStage = (BM + BN) * kBK * 2;  // bytes
     static constexpr int kRow = BM + 8;                 // staging of G: elements of a token's row
-    static constexpr int kLds = std::max(2 * kStage, BN * kRow * 2);
+    static constexpr int kLds = std::max(D * kStage, BN * kRow * 2);
 };
 
 // One operand's way into LDS and into fragments: B of its m (or n), kBK of k a stage.
@@ -210,9 +212,10 @@ template <typename S, Epi E, bool F16, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::TM][S::TN], SSM_LDS char *lds,
                                          int64_t m0, int64_t n0, int wm, int wn, int split);
 
-template <int BM, int BN, int WM, int WN, Epi E, bool F16, bool TA, bool TB>
+template <int BM, int BN, int WM, int WN, int D, Epi E, bool F16, bool TA, bool TB>
 __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char *lds) {
-    using S = Shape<BM, BN, WM, WN>;
+    using S = Shape<BM, BN, WM, WN, D>;
+    static_assert((D & (D - 1)) == 0, "a step's buffer is its last bits");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave % WM, wn = wave / WM;
 
@@ -239,7 +242,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         fb.enter(seg == 1 ? p.b.plane : 0, k);
     };
     auto stage = [&](int kt) {
-        SSM_LDS char *to = lds + (kt & 1) * S::kStage + wave * 1024;
+        SSM_LDS char *to = lds + (kt & (D - 1)) * S::kStage + wave * 1024;
         ++k;
         fa.load(to, k == p.steps);
         fb.load(to + BM * kBK * 2, k == p.steps);
@@ -260,7 +263,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     bf16x8 a[2][S::TM], b[2][S::TN];
     auto fetch = [&](int set, int kt, int ks) {
-        const SSM_LDS char *at = lds + (kt & 1) * S::kStage;
+        const SSM_LDS char *at = lds + (kt & (D - 1)) * S::kStage;
 #pragma unroll
         for (int i = 0; i < S::TM; ++i) a[set][i] = fa.read(at, ks, i);
 #pragma unroll
@@ -301,8 +304,9 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
             if (loads) __builtin_amdgcn_sched_group_barrier(0x020, kLoads, 0);
         }
     };
-    typedef std::integral_constant<int, 0> none;
-    auto step = [&](int kt, auto more, auto next) {
+    constexpr int kStageLoads = FeedA::kLoads + FeedB::kLoads;
+    // `ahead` of the stages after this one have been asked for, `more`: another one is now.
+    auto step = [&](int kt, auto more, auto ahead) {
         fetch(1, kt, 1);
         multiply(0);
         fetch(0, kt, 2);
@@ -312,44 +316,50 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         weave(std::false_type{});
         weave(std::false_type{});
         weave(std::false_type{});
-        if (next) {
-            meet(none{});
+        if constexpr (ahead > 0) {
+            meet(std::integral_constant<int, (ahead - 1) * kStageLoads>{});
             fetch(0, kt + 1, 0);
-            if (more) stage(kt + 2);
+            if (more) stage(kt + D);
         }
         multiply(1);
-        if (next) weave(more);
+        if constexpr (ahead > 0) weave(more);
     };
     if (first < last) {
-        typedef std::true_type yes;
-        typedef std::false_type no;
+        const int count = min(D, last - first);
         enter();
-        stage(first);
-        if (first + 1 < last) {
-            turn();
-            stage(first + 1);
-            meet(std::integral_constant<int, FeedA::kLoads + FeedB::kLoads>{});
-        } else {
-            meet(none{});
+        for (int i = 0; i < count; ++i) {
+            if (i) turn();
+            stage(first + i);
         }
+        // fn(left) for left = count .. 1
+        auto each = [&](auto fn) {
+            if constexpr (D > 2) {
+                if (count == 4) fn(std::integral_constant<int, 4>{});
+                if (count >= 3) fn(std::integral_constant<int, 3>{});
+            }
+            if (count >= 2) fn(std::integral_constant<int, 2>{});
+            fn(std::integral_constant<int, 1>{});
+        };
+        each([&](auto left) {
+            if (left == count) meet(std::integral_constant<int, (left - 1) * kStageLoads>{});
+        });
         fetch(0, first, 0);
         int kt = first;
-        while (kt + 2 < last) {
+        while (kt + D < last) {
             turn();
-            const int until = kt + min(last - 2 - kt, p.steps - k);
-            for (; kt < until; ++kt) step(kt, yes{}, yes{});
+            const int until = kt + min(last - D - kt, p.steps - k);
+            for (; kt < until; ++kt) step(kt, std::true_type{}, std::integral_constant<int, D - 1>{});
         }
-        if (kt + 1 < last) step(kt++, no{}, yes{});
-        step(kt, no{}, no{});
-        meet(none{});  // the epilogue may use the LDS
+        each([&](auto left) { step(kt++, std::false_type{}, std::integral_constant<int, left - 1>{}); });
+        meet(std::integral_constant<int, 0>{});  // the epilogue may use the LDS
     }
     epilogue<S, E, F16, BM, BN, WM, WN>(p, acc, lds, m0, n0, wm, wn, split);
 }
 
-template <int BM, int BN, int WM, int WN, Epi E, bool F16, bool TA, bool TB>
+template <int BM, int BN, int WM, int WN, int D, Epi E, bool F16, bool TA, bool TB>
 __global__ void __launch_bounds__(64 * WM * WN, 1) k_product(ProductArgs p) {
-    __shared__ __attribute__((aligned(1024))) char lds[Shape<BM, BN, WM, WN>::kLds];
-    product_tile<BM, BN, WM, WN, E, F16, TA, TB>(p, (SSM_LDS char *)lds);
+    __shared__ __attribute__((aligned(1024))) char lds[Shape<BM, BN, WM, WN, D>::kLds];
+    product_tile<BM, BN, WM, WN, D, E, F16, TA, TB>(p, (SSM_LDS char *)lds);
 }
 
 // A block's element e of lane l is row m = 8 (e / 4) + 4 (l / 32) + e % 4, column n = l % 32.
@@ -362,6 +372,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
     const float ua = unscale<F16>(p.a), ub = unscale<F16>(p.b);
     auto value = [&](float v) { return F16 ? v * ua * ub : v; };
     if constexpr (E == Epi::Lse) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
         const int64_t slot = (m0 / BM) * WM + wm;
 #pragma unroll
         for (int j = 0; j < S::TN; ++j) {
@@ -510,24 +521,62 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
 }
 
 // ---------------------------------------------------------------- operands
-// dst[plane][r][ld] for r < rows_out: src [rows][cols] and 0 past its columns and rows. With a
-// peak, its scaled planes; without one, a copy of bfloat16. With `mask`, a row is a token's: it
-// is 0 where the token is ignored, since it may hold anything there and 0 times it must not
-// reach a sum, and with `weigh` it is multiplied by the token's weight. Four columns a thread.
-template <typename IO, bool WIDE>
-__global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64_t cols, int64_t rows_out,
-                                              Tokens tokens, bool mask, bool weigh, const uint32_t *peak,
-                                              uint16_t *dst, int64_t ld, int64_t plane) {
+// What a row of an array is: of the vocabulary; a token, where an ignored one may hold anything
+// and does not count for the largest value; in Used it is 0 in the copy too, so that nothing of
+// it reaches a sum; in Weighed the others are multiplied by their tokens' weights.
+enum class Rows { Vocabulary, Tokens, Used, Weighed };
+
+// An array to be copied; with a peak, its largest value is found first and the copy is scaled. The
+// arrays of a call share a launch: blocks first .. of its grid are this one's.
+struct Array {
+    const void *src;         // [rows][cols]
+    int64_t rows, cols;
+    Rows kind;
+    bool wide;               // four columns at once are aligned
+    uint32_t *peak, *part;   // null: not scaled; part[kPeakBlocks]: the blocks' largest
+    unsigned peak_first, peak_blocks;
+    int across;              // lanes along a row in the search
+    uint16_t *dst;           // [planes][rows_out][ld], planes `plane` apart
+    int64_t rows_out, ld, plane;
+    unsigned first, blocks;
+};
+struct Arrays {
+    Array a[4];
+    int n;
+};
+
+// dst[plane][r][ld] for r < rows_out: src and 0 past its columns and rows. With a peak, its scaled
+// planes; without one, a copy of bfloat16. Four columns a thread.
+template <typename IO>
+__global__ void __launch_bounds__(256) k_pack(Arrays arrays, Tokens tokens) {
     typedef IO iov __attribute__((ext_vector_type(4)));
-    const int64_t across = ld / 4, total = rows_out * across;
-    const float scale = peak ? exp2i(scale_exp(*peak)) : 1.0f, same = weigh ? tokens.same() : 0.0f;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < total; e += (int64_t)gridDim.x * 256) {
+    int n = 0;
+    while (n + 1 < arrays.n && blockIdx.x >= arrays.a[n + 1].first) ++n;
+    const Array &a = arrays.a[n];
+    const unsigned block = blockIdx.x - a.first;
+    float scale = 1.0f;
+    if (a.peak) {
+        __shared__ uint32_t sh[4];
+        uint32_t top = threadIdx.x < a.peak_blocks ? a.part[threadIdx.x] : 0;
+        static_assert(kPeakBlocks <= 256, "one for each thread");
+        for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
+        __syncthreads();
+        top = max(max(sh[0], sh[1]), max(sh[2], sh[3]));
+        if (block == 0 && threadIdx.x == 0) *a.peak = top;
+        scale = exp2i(scale_exp(top));
+    }
+    const IO *src = (const IO *)a.src;
+    const int64_t rows = a.rows, cols = a.cols, across = a.ld / 4, total = a.rows_out * across;
+    const bool drop = a.kind == Rows::Used || a.kind == Rows::Weighed, weigh = a.kind == Rows::Weighed;
+    const float same = weigh ? tokens.same() : 0.0f;
+    for (int64_t e = (int64_t)block * 256 + threadIdx.x; e < total; e += (int64_t)a.blocks * 256) {
         const int64_t r = e / across, c = (e - r * across) * 4;
-        const bool in = r < rows && c < cols && !(mask && tokens.target(r) == -1);
+        const bool in = r < rows && c < cols && !(drop && tokens.target(r) == -1);
         iov from = {IO(0), IO(0), IO(0), IO(0)};
         if (in) {
             const IO *at = src + r * cols + c;
-            if (WIDE) {
+            if (a.wide) {
                 from = *(const iov *)at;
             } else if (sizeof(IO) == 2 && ((uintptr_t)src & 3) == 0 && c + 4 <= cols && r * cols + c + 6 <= rows * cols) {
                 // bfloat16 rows that start anywhere: the whole words around the four
@@ -546,8 +595,8 @@ __global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64
                     if (c + k < cols) from[k] = at[k];
             }
         }
-        uint16_t *to = dst + r * ld + c;
-        if (sizeof(IO) == 2 && !peak) {
+        uint16_t *to = a.dst + r * a.ld + c;
+        if (sizeof(IO) == 2 && !a.peak) {
             *(u32x2 *)to = u32x2{(uint32_t)from[0] | (uint32_t)from[1] << 16, (uint32_t)from[2] | (uint32_t)from[3] << 16};
             continue;
         }
@@ -563,31 +612,27 @@ __global__ void __launch_bounds__(256) k_pack(const IO *src, int64_t rows, int64
             uint32_t h[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) h[k] = take_f16(v[k]);
-            *(u32x2 *)(to + q * plane) = u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16};
+            *(u32x2 *)(to + q * a.plane) = u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16};
         }
     }
 }
 
-// peak = the bits of the largest finite |src|; with `mask` over the rows of tokens that are not
-// ignored, with `weigh` times their weights. An integer maximum: its order does not matter. A
-// block of 1024 has 1024 / across rows at a time, N columns a lane; few blocks, since each ends
-// on one address.
-constexpr int kPeakThreads = 1024, kPeakBlocks = 256;
+// The largest finite |value| of a block's rows, N columns a lane.
 template <typename IO, int N>
-__global__ void __launch_bounds__(kPeakThreads) k_peak(const IO *src, int64_t rows, int64_t cols, int across,
-                                                       Tokens tokens, bool mask, bool weigh, uint32_t *peak) {
+__device__ __forceinline__ uint32_t peak_of_rows(const Array &a, const Tokens &tokens) {
     typedef IO iov __attribute__((ext_vector_type(N)));
-    __shared__ uint32_t sh[kPeakThreads / 64];
-    const int down = kPeakThreads / across;
-    const int64_t c0 = (int64_t)(threadIdx.x % across) * N;
+    const IO *src = (const IO *)a.src;
+    const int down = kPeakThreads / a.across;
+    const int64_t c0 = (int64_t)(threadIdx.x % a.across) * N, step = (int64_t)a.peak_blocks * down;
+    const bool mask = a.kind != Rows::Vocabulary, weigh = a.kind == Rows::Weighed;
     const float same = weigh ? tokens.same() : 0.0f;
     uint32_t top = 0;
 #pragma unroll 4
-    for (int64_t r = (int64_t)blockIdx.x * down + threadIdx.x / across; r < rows; r += (int64_t)gridDim.x * down) {
+    for (int64_t r = (int64_t)(blockIdx.x - a.peak_first) * down + threadIdx.x / a.across; r < a.rows; r += step) {
         if (mask && tokens.target(r) == -1) continue;
         const float f = weigh ? tokens.weight(r, same) : 1.0f;
-        for (int64_t c = c0; c < cols; c += across * N) {
-            const iov v = *(const iov *)(src + r * cols + c);
+        for (int64_t c = c0; c < a.cols; c += a.across * N) {
+            const iov v = *(const iov *)(src + r * a.cols + c);
 #pragma unroll
             for (int k = 0; k < N; ++k) {
                 const IO e = v[k];
@@ -596,17 +641,25 @@ __global__ void __launch_bounds__(kPeakThreads) k_peak(const IO *src, int64_t ro
             }
         }
     }
+    return top;
+}
+
+// part[block] = the bits of the largest finite |value|. A block of 1024 has 1024 / across rows at
+// a time. Its few blocks leave so few values that every block that needs the largest of them
+// looks through all: no atomics, and nothing to be cleared first.
+template <typename IO>
+__global__ void __launch_bounds__(kPeakThreads) k_peak(Arrays arrays, Tokens tokens) {
+    __shared__ uint32_t sh[kPeakThreads / 64];
+    int n = 0;
+    while (n + 1 < arrays.n && blockIdx.x >= arrays.a[n + 1].peak_first) ++n;
+    const Array &a = arrays.a[n];
+    uint32_t top = a.wide ? peak_of_rows<IO, 4>(a, tokens) : peak_of_rows<IO, 1>(a, tokens);
     for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
     __syncthreads();
     if (threadIdx.x) return;
     for (int k = 1; k < kPeakThreads / 64; ++k) top = max(top, sh[k]);
-    if (top) atomicMax(peak, top);
-}
-
-__global__ void __launch_bounds__(256) k_clear_peaks(uint32_t *peak, int64_t n) {
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k < n) peak[k] = 0;
+    a.part[blockIdx.x - a.peak_first] = top;
 }
 
 // (m, s) += (m2, s2): sums of exponentials under their maxima.
@@ -617,16 +670,33 @@ __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
     m = M;
 }
 
-// A block of 256 joins the n partial pairs of TX tokens, 256 / TX threads for each.
+// A block of 256 joins the n partial pairs of TX tokens, 256 / TX threads for each, and sums their
+// losses. The block that ends last makes the means of the blocks' sums, in their order:
+// mean[0] = mean loss over the tokens that are not ignored, mean[1] = 1 / their number.
+struct Losses {
+    double sum;
+    int64_t n;
+};
+__device__ __forceinline__ void put(Losses *p, const Losses &v) {
+    __hip_atomic_store(&p->sum, v.sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(&p->n, v.n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ Losses get(Losses *p) {
+    return {__hip_atomic_load(&p->sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+            __hip_atomic_load(&p->n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)};
+}
 template <int TX>
-__global__ void __launch_bounds__(256) k_xent_join(const float2 *part, int64_t n, const float *at,
-                                                   Tokens tokens, int64_t T, float *loss, float *lse) {
+__global__ void __launch_bounds__(256) k_xent_join(const float2 *part, int64_t n, const float *at, Tokens tokens, int64_t T,
+                                                   float *loss, float *lse, Losses *sums, uint32_t *done, float *mean) {
     constexpr int TY = 256 / TX;
     __shared__ float2 sh[TY][TX];
+    __shared__ Losses wave_sum[4];
+    __shared__ bool is_last;
     const int x = threadIdx.x % TX, y = threadIdx.x / TX;
     const int64_t t = (int64_t)blockIdx.x * TX + x;
     float m = -INFINITY, s = 0.0f;
     if (t < T)
+#pragma unroll 4
         for (int64_t j = y; j < n; j += TY) {
             const float2 q = part[j * T + t];
             join(m, s, q.x, q.y);
@@ -639,41 +709,45 @@ __global__ void __launch_bounds__(256) k_xent_join(const float2 *part, int64_t n
             sh[y][x] = make_float2(m, s);
         }
     }
-    if (y || t >= T) return;
-    const float l = m + logf(s);
-    lse[t] = l;
-    const int32_t to = tokens.target(t);
-    loss[t] = to == -1 ? 0.0f : to >= 0 ? l - at[t] : NAN;
-}
-
-// mean[0] = mean loss over the tokens that are not ignored, mean[1] = 1 / their number.
-__global__ void __launch_bounds__(1024) k_xent_mean(const float *loss, const int64_t *targets, int64_t ignore,
-                                                    int64_t T, float *mean) {
-    __shared__ double sh[16];
-    __shared__ int64_t sn[16];
-    double s = 0.0;
-    int64_t c = 0;
-    for (int64_t t = threadIdx.x; t < T; t += 1024)
-        if (targets[t] != ignore) {
-            s += loss[t];
-            ++c;
-        }
-    for (int o = 32; o > 0; o >>= 1) {
-        s += __shfl_xor(s, o);
-        c += __shfl_xor(c, o);
+    Losses own{0.0, 0};
+    if (y == 0 && t < T) {
+        const float l = m + logf(s);
+        const int32_t to = tokens.target(t);
+        const float v = to == -1 ? 0.0f : to >= 0 ? l - at[t] : NAN;
+        lse[t] = l;
+        loss[t] = v;
+        if (to != -1) own = {v, 1};
     }
-    if ((threadIdx.x & 63) == 0) {
-        sh[threadIdx.x >> 6] = s;
-        sn[threadIdx.x >> 6] = c;
+    for (int o = TX / 2; o > 0; o >>= 1) {
+        own.sum += __shfl_xor(own.sum, o);
+        own.n += __shfl_xor(own.n, o);
+    }
+    if (threadIdx.x == 0) {
+        put(sums + blockIdx.x, own);
+        is_last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
     }
     __syncthreads();
-    if (threadIdx.x) return;
-    for (int j = 1; j < 16; ++j) {
-        s += sh[j];
-        c += sn[j];
+    if (!is_last) return;
+    own = {0.0, 0};
+#pragma unroll 4
+    for (unsigned b = threadIdx.x; b < gridDim.x; b += 256) {
+        const Losses q = get(sums + b);
+        own.sum += q.sum;
+        own.n += q.n;
     }
-    mean[0] = c ? (float)(s / (double)c) : 0.0f;
-    mean[1] = c ? (float)(1.0 / (double)c) : 0.0f;
+    for (int o = 32; o > 0; o >>= 1) {
+        own.sum += __shfl_xor(own.sum, o);
+        own.n += __shfl_xor(own.n, o);
+    }
+    if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6] = own;
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int j = 1; j < 4; ++j) {
+        own.sum += wave_sum[j].sum;
+        own.n += wave_sum[j].n;
+    }
+    mean[0] = own.n ? (float)(own.sum / (double)own.n) : 0.0f;
+    mean[1] = own.n ? (float)(1.0 / (double)own.n) : 0.0f;
 }
 
 // dst = (sum +) the n partial products in order; float32 or bfloat16. Two of them side by side.
@@ -701,8 +775,7 @@ __global__ void __launch_bounds__(256) k_join_splits(JoinPair pair) {
 
 template <typename IO>
 __global__ void __launch_bounds__(256) k_zero(IO *p, int64_t n) {
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (e < n) p[e] = IO(0);
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) p[e] = IO(0);
 }
 
 // ---------------------------------------------------------------- host
@@ -715,7 +788,8 @@ constexpr int kBig = 256, kSmall = 128;
 // units by their rounds: a compute unit makes a quarter of the work in about a third of the
 // time with the small tiles (measured on 8192 x 8192 x 4096: 1250 against 950 TFLOP/s), which
 // waste less at the edges and in the last round. Only small tiles are split (1000 x 1000 x 48000:
-// 134 us in 8 parts of small tiles, 170 in 16 of large ones); a split keeps at least 8 steps of k.
+// 134 us in 8 parts of small tiles, 170 in 16 of large ones); a split keeps at least 2 steps of k
+// (with 8, 100 x 256 x 1000 took 49 us a training step, with 2 it takes 44).
 struct Tiling {
     int tile, splits;
 };
@@ -725,7 +799,7 @@ Tiling tiling(int64_t M, int64_t N, int64_t steps, bool may_split) {
     double least = 0;
     for (const int tile : {kSmall, kBig}) {
         const int64_t n = (int64_t)blocks(M, tile) * blocks(N, tile), room = 2 * kCus / n;
-        const int64_t s = !may_split || tile == kBig ? 1 : std::max<int64_t>(1, std::min(std::min(room, steps / 8), (int64_t)64));
+        const int64_t s = !may_split || tile == kBig ? 1 : std::max<int64_t>(1, std::min(std::min(room, steps / 2), (int64_t)64));
         const double time = (double)blocks(n * s, kCus) / (double)s * (tile == kBig ? 3.0 : 1.0);
         if (!best.tile || time < least) {
             best = {tile, (int)s};
@@ -740,8 +814,9 @@ hipError_t product(ProductArgs p, int tile, hipStream_t s) {
     p.tiles_m = (int32_t)blocks(p.M, tile);
     p.tiles_n = (int32_t)blocks(p.N, tile);
     const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits);
-    if (tile == kBig) k_product<256, 256, 2, 4, E, F16, TA, TB><<<grid, 512, 0, s>>>(p);
-    else k_product<128, 128, 2, 2, E, F16, TA, TB><<<grid, 256, 0, s>>>(p);
+    if (tile == kBig) k_product<256, 256, 2, 4, 2, E, F16, TA, TB><<<grid, 512, 0, s>>>(p);
+    else if ((int64_t)grid.x * grid.y <= kCus) k_product<128, 128, 2, 2, 4, E, F16, TA, TB><<<grid, 256, 0, s>>>(p);
+    else k_product<128, 128, 2, 2, 2, E, F16, TA, TB><<<grid, 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -765,8 +840,8 @@ struct Layout {
     bool pack;                   // weight is copied: float32, or rows not in steps of 64
     uint16_t *hidden, *weight;   // copies for the logits
     uint16_t *hidden_w, *piece_w, *g;  // for the gradients: hidden, a piece of weight, G
-    uint32_t *peak;
-    int64_t peaks;
+    uint32_t *peak, *peak_part, *done;
+    Losses *losses;
     float *at, *sum, *split_w, *split_h;
     float2 *part;
     size_t bytes;
@@ -775,6 +850,10 @@ struct Layout {
 // G of a piece holds about 2^26 values: 8192 tokens take pieces of 8192 rows, whose three products
 // are 512 and 1024 tiles of 256 x 256, whole rounds of the compute units.
 constexpr int64_t kPieceValues = (int64_t)1 << 26;
+
+// Tokens of a block that joins: whole lines of the partial pairs and few blocks where there are
+// many tokens, many threads for each where there are few.
+int join_tokens(int64_t T) { return T >= 4096 ? 32 : T >= 256 ? 16 : 2; }
 
 Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, char *ws) {
     Layout l{};
@@ -787,15 +866,17 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
     // sized as if the operands had to be copied: their alignment is not known to the query
     l.hidden = a.take<uint16_t>(T * l.ldk * l.planes);
     l.weight = a.take<uint16_t>(V * l.ldk * l.planes);
-    l.peaks = kPeakPiece;
+    l.peak = a.take<uint32_t>(kPeaks);
+    l.peak_part = a.take<uint32_t>(kPeaks * kPeakBlocks);
     if (!bwd) {
         l.lse = tiling(V, T, l.ldk / kBK * l.terms, false);
         l.part = a.take<float2>((int64_t)blocks(V, l.lse.tile) * 2 * T);
         l.at = a.take<float>(T);
+        l.losses = a.take<Losses>(blocks(T, join_tokens(T)));
+        l.done = a.take<uint32_t>(1);
     } else {
         l.piece = std::min(up(V, kBig), std::max<int64_t>(1024, kPieceValues / std::max<int64_t>(T, 1) / kBig * kBig));
         const int64_t most = std::min(V, l.piece);
-        l.peaks += blocks(V, l.piece);
         l.out_w = tiling(K, most, l.rows_t / kBK * l.terms, true);
         l.out_h = tiling(K, T, up(most, kBK) / kBK * l.terms, true);
         l.sum = a.take<float>(V > l.piece ? T * K : 0);
@@ -805,35 +886,53 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
         l.split_w = a.take<float>(l.out_w.splits > 1 ? l.out_w.splits * most * K : 0);
         l.split_h = a.take<float>(l.out_h.splits > 1 ? l.out_h.splits * T * K : 0);
     }
-    l.peak = a.take<uint32_t>(l.peaks);
     l.bytes = a.used;
     return l;
 }
 
+constexpr int64_t kMostBlocks = (int64_t)1 << 20;
+
+// The arrays that a call copies, gathered and then launched together.
 template <typename IO>
-hipError_t pack(const void *src, int64_t rows, int64_t cols, int64_t rows_out, const Tokens &tokens, bool mask, bool weigh,
-                const uint32_t *peak, uint16_t *dst, int64_t ld, hipStream_t s) {
-    const dim3 grid((unsigned)std::min<int64_t>((rows_out * ld / 4 + 255) / 256, (int64_t)1 << 20));
-    if (cols % 4 == 0 && (uintptr_t)src % (4 * sizeof(IO)) == 0)
-        k_pack<IO, true><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, rows_out, tokens, mask, weigh, peak, dst, ld,
-                                                  rows_out * ld);
-    else
-        k_pack<IO, false><<<grid, 256, 0, s>>>((const IO *)src, rows, cols, rows_out, tokens, mask, weigh, peak, dst, ld,
-                                                  rows_out * ld);
-    return hipGetLastError();
-}
-template <typename IO>
-hipError_t find_peak(const void *src, int64_t rows, int64_t cols, const Tokens &tokens, bool mask, bool weigh, uint32_t *peak,
-                     hipStream_t s) {
-    const bool wide = cols % 4 == 0 && (uintptr_t)src % (4 * sizeof(IO)) == 0;
-    const int64_t lanes = wide ? cols / 4 : cols;
-    int across = 16;
-    while (across < lanes && across < kPeakThreads) across *= 2;
-    const dim3 grid((unsigned)std::min<int64_t>(blocks(rows, kPeakThreads / across), kPeakBlocks));
-    if (wide) k_peak<IO, 4><<<grid, kPeakThreads, 0, s>>>((const IO *)src, rows, cols, across, tokens, mask, weigh, peak);
-    else k_peak<IO, 1><<<grid, kPeakThreads, 0, s>>>((const IO *)src, rows, cols, across, tokens, mask, weigh, peak);
-    return hipGetLastError();
-}
+struct Copies {
+    Arrays list{};
+    unsigned peak_grid = 0, grid = 0;
+    // src [rows][cols] to dst [planes][rows_out][ld]; peak: of l.peak, or -1 for a plain copy.
+    // Returns the copy as an operand.
+    Operand add(const Layout &l, const void *src, int64_t rows, int64_t cols, uint16_t *dst, int64_t rows_out, int peak,
+                Rows kind) {
+        Array &a = list.a[list.n++];
+        a.src = src;
+        a.rows = rows;
+        a.cols = cols;
+        a.kind = kind;
+        a.wide = cols % 4 == 0 && (uintptr_t)src % (4 * sizeof(IO)) == 0;
+        a.dst = dst;
+        a.rows_out = rows_out;
+        a.ld = l.ldk;
+        a.plane = rows_out * l.ldk;
+        a.first = grid;
+        // a scaled one looks through the largest values first: more rows for a block
+        a.blocks = (unsigned)std::min<int64_t>((rows_out * l.ldk / 4 + 255) / 256, peak < 0 ? kMostBlocks : 4096);
+        grid += a.blocks;
+        a.peak_first = peak_grid;
+        if (peak >= 0) {
+            const int64_t lanes = a.wide ? cols / 4 : cols;
+            a.peak = l.peak + peak;
+            a.part = l.peak_part + peak * kPeakBlocks;
+            a.across = 16;
+            while (a.across < lanes && a.across < kPeakThreads) a.across *= 2;
+            a.peak_blocks = (unsigned)std::min<int64_t>(blocks(rows, kPeakThreads / a.across), kPeakBlocks);
+            peak_grid += a.peak_blocks;
+        }
+        return {dst, l.ldk, a.plane, a.peak, rows_out};
+    }
+    hipError_t launch(const Tokens &tokens, hipStream_t s) {
+        if (peak_grid) k_peak<IO><<<dim3(peak_grid), kPeakThreads, 0, s>>>(list, tokens);
+        if (grid) k_pack<IO><<<dim3(grid), 256, 0, s>>>(list, tokens);
+        return hipGetLastError();
+    }
+};
 
 #define SSM_TRY(x)                                 \
     do {                                           \
@@ -843,56 +942,47 @@ hipError_t find_peak(const void *src, int64_t rows, int64_t cols, const Tokens &
 
 bool rows_aligned(const XentArgs &a) { return ((uintptr_t)a.hidden | (uintptr_t)a.weight) % 16 == 0; }
 
-// The operands of the logits: hidden and weight as they are, or their packed copies. `made`: a
-// copy of hidden that is there already.
+// The product of the logits, its operands as they are or copied. `made`: a copy of hidden that is
+// there already.
 template <typename IO>
-hipError_t logits_operands(const XentArgs &a, const Layout &l, const uint16_t *made, ProductArgs &p, hipStream_t s) {
-    const uint16_t *h = made ? made : (const uint16_t *)a.hidden, *w = (const uint16_t *)a.weight;
-    if (sizeof(IO) == 4) {
-        SSM_TRY(find_peak<IO>(a.hidden, a.T, a.K, p.tokens, true, false, l.peak + kPeakH, s));
-        SSM_TRY(find_peak<IO>(a.weight, a.V, a.K, p.tokens, false, false, l.peak + kPeakW, s));
-    }
+ProductArgs logits_product(const XentArgs &a, const Layout &l, const Tokens &tokens, const Operand *made, Copies<IO> &copies) {
+    constexpr bool planes = sizeof(IO) == 4;
+    ProductArgs p{};
+    p.tokens = tokens;
     if (l.pack) {
-        const bool planes = sizeof(IO) == 4;
-        if (!made) {
-            SSM_TRY(pack<IO>(a.hidden, a.T, a.K, a.T, p.tokens, false, false, planes ? l.peak + kPeakH : nullptr, l.hidden,
-                             l.ldk, s));
-            h = l.hidden;
-        }
-        SSM_TRY(pack<IO>(a.weight, a.V, a.K, a.V, p.tokens, false, false, planes ? l.peak + kPeakW : nullptr, l.weight,
-                         l.ldk, s));
-        w = l.weight;
+        p.a = copies.add(l, a.weight, a.V, a.K, l.weight, a.V, planes ? kPeakW : -1, Rows::Vocabulary);
+        p.b = made ? *made : copies.add(l, a.hidden, a.T, a.K, l.hidden, a.T, planes ? kPeakH : -1, Rows::Tokens);
+    } else {
+        p.a = {(const uint16_t *)a.weight, l.ldk, 0, nullptr, a.V};
+        p.b = made ? *made : Operand{(const uint16_t *)a.hidden, l.ldk, 0, nullptr, a.T};
     }
-    p.a = {w, l.ldk, a.V * l.ldk, l.peak + kPeakW, a.V};
-    p.b = {h, l.ldk, a.T * l.ldk, l.peak + kPeakH, a.T};
     p.N = a.T;
     p.steps = (int32_t)(l.ldk / kBK);
     p.terms = l.terms;
     p.splits = 1;
-    return hipSuccess;
+    return p;
 }
 
 template <typename IO>
 hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
-    if (a.T > 0) {
-        const Layout l = lay_out(a.T, a.K, a.V, io, false, rows_aligned(a), (char *)a.ws);
-        if (!io) k_clear_peaks<<<dim3(blocks(l.peaks, 256)), 256, 0, s>>>(l.peak, l.peaks);
-        ProductArgs p{};
-        p.tokens = {a.targets, a.ignore, a.V, nullptr, nullptr, nullptr};
-        SSM_TRY(logits_operands<IO>(a, l, nullptr, p, s));
-        p.M = a.V;
-        p.part = l.part;
-        p.at = l.at;
-        SSM_TRY((product<Epi::Lse, sizeof(IO) == 4>(p, l.lse.tile, s)));
-        const int64_t n = (int64_t)blocks(a.V, l.lse.tile) * 2;
-        // whole lines of the partial pairs where there are many tokens, many threads for each
-        // where there are few
-        if (a.T >= 4096)
-            k_xent_join<16><<<dim3(blocks(a.T, 16)), 256, 0, s>>>(l.part, n, l.at, p.tokens, a.T, a.loss, a.lse);
-        else
-            k_xent_join<2><<<dim3(blocks(a.T, 2)), 256, 0, s>>>(l.part, n, l.at, p.tokens, a.T, a.loss, a.lse);
+    if (a.T == 0) {
+        k_zero<<<dim3(1), 256, 0, s>>>(a.mean, (int64_t)2);
+        return hipGetLastError();
     }
-    k_xent_mean<<<dim3(1), 1024, 0, s>>>(a.loss, a.targets, a.ignore, a.T, a.mean);
+    const Layout l = lay_out(a.T, a.K, a.V, io, false, rows_aligned(a), (char *)a.ws);
+    const Tokens tokens{a.targets, a.ignore, a.V, nullptr, nullptr, nullptr};
+    Copies<IO> copies;
+    ProductArgs p = logits_product<IO>(a, l, tokens, nullptr, copies);
+    SSM_TRY(copies.launch(tokens, s));
+    p.M = a.V;
+    p.part = l.part;
+    p.at = l.at;
+    p.done = l.done;
+    SSM_TRY((product<Epi::Lse, sizeof(IO) == 4>(p, l.lse.tile, s)));
+    const int64_t n = (int64_t)blocks(a.V, l.lse.tile) * 2;
+    const int most = join_tokens(a.T);
+    auto join = most == 32 ? k_xent_join<32> : most == 16 ? k_xent_join<16> : k_xent_join<2>;
+    join<<<dim3(blocks(a.T, most)), 256, 0, s>>>(l.part, n, l.at, tokens, a.T, a.loss, a.lse, l.losses, l.done, a.mean);
     return hipGetLastError();
 }
 
@@ -922,15 +1012,19 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
     const Tokens tokens{a.targets, a.ignore, a.V, a.dloss, a.dmean, a.mean};
     // one weight for all tokens: it is a factor at the end, and bfloat16 serves for the rest
     const bool f16 = sizeof(IO) == 4 || a.dloss;
-    if (f16) k_clear_peaks<<<dim3(blocks(l.peaks, 256)), 256, 0, s>>>(l.peak, l.peaks);
-    if (a.dweight) {
-        uint32_t *peak = f16 ? l.peak + kPeakWH : nullptr;
-        if (f16) SSM_TRY(find_peak<IO>(a.hidden, a.T, a.K, tokens, true, true, peak, s));
-        SSM_TRY(pack<IO>(a.hidden, a.T, a.K, l.rows_t, tokens, true, f16, peak, l.hidden_w, l.ldk, s));
-    }
-    ProductArgs logits{};
-    logits.tokens = tokens;
-    SSM_TRY(logits_operands<IO>(a, l, a.dweight && !f16 ? l.hidden_w : nullptr, logits, s));
+    Copies<IO> copies;
+    Operand hidden_w{}, piece_w{};
+    if (a.dweight)
+        hidden_w = copies.add(l, a.hidden, a.T, a.K, l.hidden_w, l.rows_t, f16 ? kPeakWH : -1, f16 ? Rows::Weighed : Rows::Used);
+    ProductArgs logits = logits_product<IO>(a, l, tokens, a.dweight && !f16 ? &hidden_w : nullptr, copies);
+    // where the logits' operand is bfloat16 and the gradient's float16: a plane of a piece
+    const auto copy_piece = [&](int64_t v0, Copies<IO> &c) {
+        const int64_t nv = std::min(l.piece, a.V - v0);
+        piece_w = c.add(l, (const IO *)a.weight + v0 * a.K, nv, a.K, l.piece_w, nv, kPeakW, Rows::Vocabulary);
+    };
+    const bool pieces = a.dhidden && f16 && sizeof(IO) == 2;
+    if (pieces) copy_piece(0, copies);
+    SSM_TRY(copies.launch(tokens, s));
     logits.lse = a.lse;
     logits.planes = f16 ? l.planes : 0;
     logits.g = l.g;
@@ -950,7 +1044,7 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
         if (a.dweight) {
             ProductArgs q{};
             q.tokens = tokens;
-            q.a = {l.hidden_w, l.ldk, l.rows_t * l.ldk, l.peak + kPeakWH, l.rows_t};
+            q.a = hidden_w;
             q.b = g;
             q.M = a.K;
             q.N = nv;
@@ -962,14 +1056,12 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
         if (a.dhidden) {
             ProductArgs q{};
             q.tokens = tokens;
-            q.a = p.a;
-            if (f16 && sizeof(IO) == 2) {  // the logits' operand is bfloat16: a plane of this piece
-                const IO *piece = (const IO *)a.weight + v0 * a.K;
-                uint32_t *peak = l.peak + kPeakPiece + v0 / l.piece;
-                SSM_TRY(find_peak<IO>(piece, nv, a.K, tokens, false, false, peak, s));
-                SSM_TRY(pack<IO>(piece, nv, a.K, nv, tokens, false, false, peak, l.piece_w, l.ldk, s));
-                q.a = {l.piece_w, l.ldk, nv * l.ldk, peak, nv};
+            if (pieces && v0 > 0) {
+                Copies<IO> next;
+                copy_piece(v0, next);
+                SSM_TRY(next.launch(tokens, s));
             }
+            q.a = pieces ? piece_w : p.a;
             q.b = g;
             q.factor = Factor::Row;
             q.M = a.K;
