@@ -532,7 +532,6 @@ struct Array {
     const void *src;         // [rows][cols]
     int64_t rows, cols;
     Rows kind;
-    bool wide;               // four columns at once are aligned
     uint32_t *peak, *part;   // null: not scaled; part[kPeakBlocks]: the blocks' largest
     unsigned peak_first, peak_blocks;
     int across;              // lanes along a row in the search
@@ -546,10 +545,12 @@ struct Arrays {
 };
 
 // dst[plane][r][ld] for r < rows_out: src and 0 past its columns and rows. With a peak, its scaled
-// planes; without one, a copy of bfloat16. Four columns a thread.
+// planes; without one, a copy of bfloat16. 16 bytes of a row a thread; the loads may start at any
+// element.
 template <typename IO>
 __global__ void __launch_bounds__(256) k_pack(Arrays arrays, Tokens tokens) {
-    typedef IO iov __attribute__((ext_vector_type(4)));
+    constexpr int N = 16 / sizeof(IO);
+    typedef IO iov __attribute__((ext_vector_type(N), aligned(sizeof(IO))));
     int n = 0;
     while (n + 1 < arrays.n && blockIdx.x >= arrays.a[n + 1].first) ++n;
     const Array &a = arrays.a[n];
@@ -567,60 +568,54 @@ __global__ void __launch_bounds__(256) k_pack(Arrays arrays, Tokens tokens) {
         scale = exp2i(scale_exp(top));
     }
     const IO *src = (const IO *)a.src;
-    const int64_t rows = a.rows, cols = a.cols, across = a.ld / 4, total = a.rows_out * across;
+    const int64_t rows = a.rows, cols = a.cols, across = a.ld / N, total = a.rows_out * across;
     const bool drop = a.kind == Rows::Used || a.kind == Rows::Weighed, weigh = a.kind == Rows::Weighed;
     const float same = weigh ? tokens.same() : 0.0f;
     for (int64_t e = (int64_t)block * 256 + threadIdx.x; e < total; e += (int64_t)a.blocks * 256) {
-        const int64_t r = e / across, c = (e - r * across) * 4;
+        const int64_t r = e / across, c = (e - r * across) * N;
         const bool in = r < rows && c < cols && !(drop && tokens.target(r) == -1);
-        iov from = {IO(0), IO(0), IO(0), IO(0)};
+        iov from;
+#pragma unroll
+        for (int k = 0; k < N; ++k) from[k] = IO(0);
         if (in) {
             const IO *at = src + r * cols + c;
-            if (a.wide) {
+            if (c + N <= cols) {
                 from = *(const iov *)at;
-            } else if (sizeof(IO) == 2 && ((uintptr_t)src & 3) == 0 && c + 4 <= cols && r * cols + c + 6 <= rows * cols) {
-                // bfloat16 rows that start anywhere: the whole words around the four
-                const int64_t first = r * cols + c;
-                const uint32_t *word = (const uint32_t *)src + (first >> 1);
-                uint32_t lo = word[0], hi = word[1];
-                if (first & 1) {
-                    const uint32_t end = word[2];
-                    lo = lo >> 16 | hi << 16;
-                    hi = hi >> 16 | end << 16;
-                }
-                from[0] = (IO)(lo & 0xffffu), from[1] = (IO)(lo >> 16), from[2] = (IO)(hi & 0xffffu), from[3] = (IO)(hi >> 16);
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < N; ++k)
                     if (c + k < cols) from[k] = at[k];
             }
         }
         uint16_t *to = a.dst + r * a.ld + c;
-        if (sizeof(IO) == 2 && !a.peak) {
-            *(u32x2 *)to = u32x2{(uint32_t)from[0] | (uint32_t)from[1] << 16, (uint32_t)from[2] | (uint32_t)from[3] << 16};
-            continue;
-        }
+        typedef uint16_t u16xN __attribute__((ext_vector_type(N)));
+        if constexpr (sizeof(IO) == 2)
+            if (!a.peak) {
+                *(u16xN *)to = from;
+                continue;
+            }
         const float f = weigh && in ? tokens.weight(r, same) : 1.0f;
-        float v[4];
+        float v[N];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < N; ++k) {
             const IO x = from[k];
             v[k] = Io<IO>::ld(&x) * f * scale;
         }
 #pragma unroll
         for (int q = 0; q < (sizeof(IO) == 4 ? kParts : 1); ++q) {
-            uint32_t h[4];
+            u16xN h;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = take_f16(v[k]);
-            *(u32x2 *)(to + q * a.plane) = u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16};
+            for (int k = 0; k < N; ++k) h[k] = (uint16_t)take_f16(v[k]);
+            *(u16xN *)(to + q * a.plane) = h;
         }
     }
 }
 
-// The largest finite |value| of a block's rows, N columns a lane.
-template <typename IO, int N>
+// The largest finite |value| of a block's rows, 16 bytes of a row a lane.
+template <typename IO>
 __device__ __forceinline__ uint32_t peak_of_rows(const Array &a, const Tokens &tokens) {
-    typedef IO iov __attribute__((ext_vector_type(N)));
+    constexpr int N = 16 / sizeof(IO);
+    typedef IO iov __attribute__((ext_vector_type(N), aligned(sizeof(IO))));
     const IO *src = (const IO *)a.src;
     const int down = kPeakThreads / a.across;
     const int64_t c0 = (int64_t)(threadIdx.x % a.across) * N, step = (int64_t)a.peak_blocks * down;
@@ -632,12 +627,17 @@ __device__ __forceinline__ uint32_t peak_of_rows(const Array &a, const Tokens &t
         if (mask && tokens.target(r) == -1) continue;
         const float f = weigh ? tokens.weight(r, same) : 1.0f;
         for (int64_t c = c0; c < a.cols; c += a.across * N) {
-            const iov v = *(const iov *)(src + r * a.cols + c);
-#pragma unroll
-            for (int k = 0; k < N; ++k) {
-                const IO e = v[k];
+            const IO *at = src + r * a.cols + c;
+            const auto see = [&](IO e) {
                 const uint32_t b = __float_as_uint(Io<IO>::ld(&e) * f) & 0x7fffffffu;
                 top = b < 0x7f800000u ? max(top, b) : top;
+            };
+            if (c + N <= a.cols) {
+                const iov v = *(const iov *)at;
+#pragma unroll
+                for (int k = 0; k < N; ++k) see(v[k]);
+            } else {
+                for (int64_t k = c; k < a.cols; ++k) see(src[r * a.cols + k]);
             }
         }
     }
@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(kPeakThreads) k_peak(Arrays arrays, Tokens tok
     int n = 0;
     while (n + 1 < arrays.n && blockIdx.x >= arrays.a[n + 1].peak_first) ++n;
     const Array &a = arrays.a[n];
-    uint32_t top = a.wide ? peak_of_rows<IO, 4>(a, tokens) : peak_of_rows<IO, 1>(a, tokens);
+    uint32_t top = peak_of_rows<IO>(a, tokens);
     for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
     __syncthreads();
@@ -785,11 +785,11 @@ unsigned blocks(int64_t n, int64_t per) { return (unsigned)((n + per - 1) / per)
 constexpr int kBig = 256, kSmall = 128;
 
 // Tiles of 256 x 256 or 128 x 128 and a split of k, whichever takes less time on 256 compute
-// units by their rounds: a compute unit makes a quarter of the work in about a third of the
-// time with the small tiles (measured on 8192 x 8192 x 4096: 1250 against 950 TFLOP/s), which
-// waste less at the edges and in the last round. Only small tiles are split (1000 x 1000 x 48000:
-// 134 us in 8 parts of small tiles, 170 in 16 of large ones); a split keeps at least 2 steps of k
-// (with 8, 100 x 256 x 1000 took 49 us a training step, with 2 it takes 44).
+// units, in microseconds as measured: a step of k takes 1.72 with a large tile and 1.14 with two
+// small ones, which share a compute unit (8192 x 8192 x 4096: 1250 against 950 TFLOP/s) but waste
+// less at the edges and in the last round, or 0.9 with one alone; each round has its start and its
+// end; the partial products of a split go through memory and a launch that joins them. Only small tiles are split (1000 x 1000 x 48000:
+// 134 us in 8 parts of small tiles, 170 in 16 of large ones), into parts of 2 steps at least.
 struct Tiling {
     int tile, splits;
 };
@@ -798,12 +798,18 @@ Tiling tiling(int64_t M, int64_t N, int64_t steps, bool may_split) {
     Tiling best{};
     double least = 0;
     for (const int tile : {kSmall, kBig}) {
-        const int64_t n = (int64_t)blocks(M, tile) * blocks(N, tile), room = 2 * kCus / n;
-        const int64_t s = !may_split || tile == kBig ? 1 : std::max<int64_t>(1, std::min(std::min(room, steps / 2), (int64_t)64));
-        const double time = (double)blocks(n * s, kCus) / (double)s * (tile == kBig ? 3.0 : 1.0);
-        if (!best.tile || time < least) {
-            best = {tile, (int)s};
-            least = time;
+        const int64_t n = (int64_t)blocks(M, tile) * blocks(N, tile);
+        const int64_t most = !may_split || tile == kBig ? 1 : std::min(std::min(2 * kCus / n, steps / 2), (int64_t)64);
+        for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
+            const double k = (double)steps / (double)s;
+            const int64_t rounds = (int64_t)blocks(n * s, kCus), pairs = rounds / 2;
+            const double join = s == 1 ? 0.0 : 4.0 + (double)s * (double)M * (double)N * 8.0 / 5e6;
+            const double time = join + (tile == kBig ? (double)rounds * (8.0 + 1.72 * k)
+                                                     : (double)pairs * (5.0 + 1.14 * k) + (double)(rounds % 2) * (5.0 + 0.9 * k));
+            if (!best.tile || time < least) {
+                best = {tile, (int)s};
+                least = time;
+            }
         }
     }
     return best;
@@ -896,6 +902,7 @@ constexpr int64_t kMostBlocks = (int64_t)1 << 20;
 template <typename IO>
 struct Copies {
     Arrays list{};
+    static constexpr int kWide = 16 / sizeof(IO);  // elements of a load
     unsigned peak_grid = 0, grid = 0;
     // src [rows][cols] to dst [planes][rows_out][ld]; peak: of l.peak, or -1 for a plain copy.
     // Returns the copy as an operand.
@@ -906,18 +913,17 @@ struct Copies {
         a.rows = rows;
         a.cols = cols;
         a.kind = kind;
-        a.wide = cols % 4 == 0 && (uintptr_t)src % (4 * sizeof(IO)) == 0;
         a.dst = dst;
         a.rows_out = rows_out;
         a.ld = l.ldk;
         a.plane = rows_out * l.ldk;
         a.first = grid;
         // a scaled one looks through the largest values first: more rows for a block
-        a.blocks = (unsigned)std::min<int64_t>((rows_out * l.ldk / 4 + 255) / 256, peak < 0 ? kMostBlocks : 4096);
+        a.blocks = (unsigned)std::min<int64_t>((rows_out * l.ldk / kWide + 255) / 256, peak < 0 ? kMostBlocks : 4096);
         grid += a.blocks;
         a.peak_first = peak_grid;
         if (peak >= 0) {
-            const int64_t lanes = a.wide ? cols / 4 : cols;
+            const int64_t lanes = blocks(cols, kWide);
             a.peak = l.peak + peak;
             a.part = l.peak_part + peak * kPeakBlocks;
             a.across = 16;
