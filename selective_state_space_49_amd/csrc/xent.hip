@@ -1011,7 +1011,7 @@ hipError_t gradient(ProductArgs p, bool f16, Tiling t, float *split, void *dst, 
 template <typename IO>
 hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
     if (a.T == 0) {
-        if (a.dweight) k_zero<IO><<<dim3(blocks(a.V * a.K, 256)), 256, 0, s>>>((IO *)a.dweight, a.V * a.K);
+        if (a.dweight) k_zero<IO><<<dim3((unsigned)std::min((a.V * a.K + 255) / 256, kMostBlocks)), 256, 0, s>>>((IO *)a.dweight, a.V * a.K);
         return hipGetLastError();
     }
     const Layout l = lay_out(a.T, a.K, a.V, io, true, rows_aligned(a), (char *)a.ws);
