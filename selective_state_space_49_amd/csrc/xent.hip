@@ -853,9 +853,11 @@ struct Layout {
     size_t bytes;
 };
 
-// G of a piece holds about 2^26 values: 8192 tokens take pieces of 8192 rows, whose three products
-// are 512 and 1024 tiles of 256 x 256, whole rounds of the compute units.
-constexpr int64_t kPieceValues = (int64_t)1 << 26;
+// G of a piece holds about 2^27 values, 256 MB in bfloat16: 8192 tokens take pieces of 16384 rows.
+// dhidden's partial sum is read and written once for each piece, so that more of them cost more
+// (2^26, 2^27 and 2^28 values: 7.32, 7.27 and 7.22 ms for 8192 x 4096 x 32000, 8.34, 8.05 and
+// 8.05 ms for 2000 x 4096 x 128000), and larger ones would begin to be the whole array.
+constexpr int64_t kPieceValues = (int64_t)1 << 27;
 
 // Tokens of a block that joins: whole lines of the partial pairs and few blocks where there are
 // many tokens, many threads for each where there are few.
@@ -881,7 +883,7 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
         l.losses = a.take<Losses>(blocks(T, join_tokens(T)));
         l.done = a.take<uint32_t>(1);
     } else {
-        l.piece = std::min(up(V, kBig), std::max<int64_t>(1024, kPieceValues / std::max<int64_t>(T, 1) / kBig * kBig));
+        l.piece = std::min(up(V, kBig), std::max<int64_t>(1024, kPieceValues / l.rows_t / kBig * kBig));
         const int64_t most = std::min(V, l.piece);
         l.out_w = tiling(K, most, l.rows_t / kBK * l.terms, true);
         l.out_h = tiling(K, T, up(most, kBK) / kBK * l.terms, true);

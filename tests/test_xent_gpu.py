@@ -208,3 +208,15 @@ def test_captured_in_a_graph():
         for k, t in {"loss": loss, "mean": mean, "dhidden": dh, "dweight": dw}.items():
             assert bitwise_equal(t, want[k]), k
         call(hidden, weight, target, None, one)
+
+
+@pytest.mark.parametrize("T,K,V", [(9000, 72, 16000), (2, 24, (1 << 21) + 777)])
+@pytest.mark.parametrize("io,each", [(torch.float32, False), (torch.bfloat16, False), (torch.bfloat16, True)])
+def test_several_pieces_of_the_vocabulary(T, K, V, io, each):
+    # two pieces: dhidden is a running sum over them
+    say("xent pieces", T, K, V, io, each)
+    hidden, weight, target = make(T, K, V, io, seed=13, ignored=0.2 if T > 2 else 0.0)
+    dloss = torch.randn(T, generator=torch.Generator().manual_seed(1)) if each else None
+    ref = train_ref.xent(hidden, weight, target, dloss=dloss, dmean=2.0)
+    got = call(hidden, weight, target, None if dloss is None else dloss.cuda(), torch.tensor(2.0, device="cuda"))
+    check(hidden, weight, target, ref, got, io, 1)
