@@ -803,8 +803,8 @@ constexpr int kBig = 256, kSmall = 128;
 // units, in microseconds as measured: a step of k takes 1.72 with a large tile and 1.14 with two
 // small ones, which share a compute unit (8192 x 8192 x 4096: 1250 against 950 TFLOP/s) but waste
 // less at the edges and in the last round, or 0.9 with one alone; each round has its start and its
-// end; the partial products of a split go through memory and a launch that joins them. Only small tiles are split (1000 x 1000 x 48000:
-// 134 us in 8 parts of small tiles, 170 in 16 of large ones), into parts of 2 steps at least.
+// end; the partial products of a split go through memory and a launch that joins them (1000 x 1000 x 48000 in float16: 140 us in 8 parts
+// of small tiles, 112 in 16 of large ones). A part has 2 steps at least.
 struct Tiling {
     int tile, splits;
 };
@@ -814,7 +814,7 @@ Tiling tiling(int64_t M, int64_t N, int64_t steps, bool may_split) {
     double least = 0;
     for (const int tile : {kSmall, kBig}) {
         const int64_t n = (int64_t)blocks(M, tile) * blocks(N, tile);
-        const int64_t most = !may_split || tile == kBig ? 1 : std::min(std::min(2 * kCus / n, steps / 2), (int64_t)64);
+        const int64_t most = !may_split ? 1 : std::min(std::min((tile == kBig ? 1 : 2) * kCus / n, steps / 2), (int64_t)64);
         for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
             const double k = (double)steps / (double)s;
             const int64_t rounds = (int64_t)blocks(n * s, kCus), pairs = rounds / 2;
