@@ -4,7 +4,7 @@
 
 Each layer mixes the sequence with a selective scan (the MambaBlock's) and a gated linear
 recurrence; documents are packed into rows, and the recurrence is reset where one starts. The
-head's loss is linear_cross_entropy, which keeps no logits, the optimizer AdamW, one launch for
+head's loss is linear_cross_entropy, which keeps no logits, the optimizer AdamW, one call for
 all parameters. Afterwards the recurrence of the first layer is run token by token, as a decoder
 would, and compared with the whole-sequence call.
 
