@@ -54,11 +54,11 @@ def _compile(src: str, verbose: bool, objdir: str, defines) -> str:
 
 
 def build_table(verbose: bool = False) -> str:
-    """Compile the extension that reads lists of torch tensors (host code only)."""
+    """Compile the extension that reads torch tensors for short calls (host code only)."""
     import torch
     root = os.path.dirname(torch.__file__)
     tmp = TABLE + ".tmp"
-    cmd = [_hipcc(), "-O2", "-fPIC", "-std=c++17", "-shared", "-w", f"-I{root}/include",
+    cmd = [_hipcc(), "-O2", "-fPIC", "-std=c++17", "-shared", "-w", f"-I{INCLUDE}", f"-I{root}/include",
            f"-I{root}/include/torch/csrc/api/include", f"-I{sysconfig.get_paths()['include']}",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            os.path.join(CSRC, "tensor_table.cpp"), "-o", tmp, f"-L{root}/lib", "-ltorch_python", "-ltorch_cpu", "-lc10"]

@@ -24,9 +24,9 @@ _f32 = torch.float32
 _IO = {_f32: SSM_F32, torch.bfloat16: SSM_BF16}
 
 
-# The step of a token, or of an optimizer over a small model, is shorter than a careful
-# marshalling of its arguments, so these take the short way: one comparison where an argument
-# is right, and _dev's checks only to say what is wrong with it.
+# Small calls are shorter than a careful marshalling of their arguments, so these take the short
+# way: one comparison where an argument is right, and _dev's checks only to say what is wrong
+# with it. The step of a token and of an optimizer go through the _tensor_table extension.
 def _need(t: Optional[torch.Tensor], name: str, shape, dtype):
     """The address of a contiguous GPU tensor of this shape and dtype, or None."""
     if t is None:
@@ -46,6 +46,31 @@ def _kind(t: torch.Tensor) -> int:
 def _stream(t: torch.Tensor) -> int:
     """torch's current stream on the tensor's GPU, as a hipStream_t."""
     return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+_table_loaded = None
+
+
+def _table_module():
+    """The extension that reads tensors for short calls (csrc/tensor_table.cpp)."""
+    global _table_loaded
+    if _table_loaded is None:
+        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_tensor_table.so")
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it with `python -m selective_state_space_49_amd.build`")
+        _table_loaded = importlib.import_module("._tensor_table", __package__)
+    return _table_loaded
+
+
+_entries: dict = {}
+
+
+def _entry(name: str) -> int:
+    """The address of one of the library's entry points."""
+    at = _entries.get(name)
+    if at is None:
+        at = _entries[name] = ctypes.cast(getattr(load_library(), name), ctypes.c_void_p).value
+    return at
 
 
 def _scratch(workspace, need: int, device):
@@ -138,15 +163,18 @@ def ssm_gated_bwd(x, r, i, decay, states, reset=None, *, dy, dh_final=None, c=8.
 def ssm_gated_step(h, x_t, r_t, i_t, decay, *, c=8.0, y_t=None):
     """One token for every (layer, sequence): h [Ln, S, D] float32 in place; x_t, r_t, i_t
     [Ln, S, D]; decay [Ln, D]. Returns y_t."""
-    shape, io, kind = x_t.shape, x_t.dtype, _kind(x_t)
-    Ln, S, D = shape
-    if y_t is None:
-        y_t = torch.empty_like(x_t)
-    _check(load_library().ssm_gated_step(
-        _need(h, "h", shape, _f32), _need(x_t, "x_t", shape, io), _need(r_t, "r_t", shape, io),
-        _need(i_t, "i_t", shape, io), _need(decay, "decay", (Ln, D), _f32), c, _need(y_t, "y_t", shape, io), Ln, S,
-        D, kind, _stream(x_t)))
-    return y_t
+    got = _table_module().gated_step(_entry("ssm_gated_step"), _stream(x_t) if x_t.is_cuda else 0, h, x_t, r_t, i_t,
+                                     decay, c, y_t)
+    if got is None:  # say what is wrong
+        (Ln, S, D), shape, io = x_t.shape, x_t.shape, x_t.dtype
+        _kind(x_t)
+        for t, name, of, dtype in ((h, "h", shape, _f32), (x_t, "x_t", shape, io), (r_t, "r_t", shape, io),
+                                   (i_t, "i_t", shape, io), (decay, "decay", (Ln, D), _f32), (y_t, "y_t", shape, io)):
+            _need(t, name, of, dtype)
+        raise ValueError("h, r_t, i_t, decay and y_t must be on x_t's GPU")
+    if isinstance(got, int):
+        _check(got)
+    return got
 
 
 class _GatedScan(torch.autograd.Function):
@@ -267,20 +295,6 @@ def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, reductio
 
 
 # ------------------------------------------------------------------ AdamW
-_table_loaded = None
-
-
-def _table_module():
-    """The extension that reads lists of tensors (csrc/tensor_table.cpp)."""
-    global _table_loaded
-    if _table_loaded is None:
-        path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_tensor_table.so")
-        if not os.path.exists(path):
-            raise ImportError(f"{path} is missing: build it with `python -m selective_state_space_49_amd.build`")
-        _table_loaded = importlib.import_module("._tensor_table", __package__)
-    return _table_loaded
-
-
 def ssm_adamw_state_size(sizes) -> int:
     """Elements of the moments' arrays for tensors of these sizes."""
     sizes = list(sizes)
@@ -295,14 +309,20 @@ def ssm_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_sc
     256 elements), int8 and uint8 codes. grad_scale: one float32 on the GPU."""
     if not params:
         return
-    table, at, blocks = _table_module().table(list(params), list(grads), ADAMW_BLOCK)  # at: where table's bytes are
-    n, total, codes = len(params), (blocks * ADAMW_BLOCK,), avg_scale is not None
-    _check(load_library().ssm_adamw_step(
-        n, at, at + 8 * n, at + 16 * n, at + 24 * n, at + 28 * n,
-        _need(exp_avg, "exp_avg", total, torch.int8 if codes else _f32),
-        _need(exp_avg_sq, "exp_avg_sq", total, torch.uint8 if codes else _f32),
-        _need(avg_scale, "avg_scale", (blocks,), _f32), _need(avg_sq_scale, "avg_sq_scale", (blocks,), _f32),
-        _one(grad_scale, "grad_scale"), lr, beta1, beta2, eps, weight_decay, step, _stream(params[0])))
+    params, grads = list(params), list(grads)
+    status = _table_module().adamw_step(
+        _entry("ssm_adamw_step"), _stream(params[0]) if params[0].is_cuda else 0, ADAMW_BLOCK, params, grads, exp_avg,
+        exp_avg_sq, avg_scale, avg_sq_scale, grad_scale, lr, beta1, beta2, eps, weight_decay, step)
+    if status is None:  # say what is wrong
+        total, codes = ssm_adamw_state_size(p.numel() for p in params), avg_scale is not None
+        for t, name, n, dtype in ((exp_avg, "exp_avg", total, torch.int8 if codes else _f32),
+                                  (exp_avg_sq, "exp_avg_sq", total, torch.uint8 if codes else _f32),
+                                  (avg_scale, "avg_scale", total // ADAMW_BLOCK, _f32),
+                                  (avg_sq_scale, "avg_sq_scale", total // ADAMW_BLOCK, _f32)):
+            _need(t, name, (n,), dtype)
+        _one(grad_scale, "grad_scale")
+        raise ValueError("the moments, their scales and grad_scale must be given and on the parameters' GPU")
+    _check(status)
 
 
 def ssm_adamw_values(exp_avg, exp_avg_sq, avg_scale, avg_sq_scale):

@@ -229,3 +229,25 @@ def test_optimizer():
         assert all(torch.equal(p, t) for p, t in zip(params, end))
         with pytest.raises(ValueError):
             ssm.AdamW(params, bits=40 - bits).load_state_dict(saved[1])
+
+
+def test_step_refuses_what_does_not_fit():
+    opt = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1)
+    p, g = torch.ones(300, device="cuda"), torch.ones(300, device="cuda")
+    codes = lambda n, dtype: torch.zeros(n, dtype=dtype, device="cuda")  # noqa: E731
+    m, v, s = codes(512, torch.float32), codes(512, torch.float32), codes(2, torch.float32)
+    mq, vq = codes(512, torch.int8), codes(512, torch.uint8)
+    bad = [([p], [g], m[:256], v), ([p], [g], m, v.double()), ([p], [g], m.cpu(), v), ([p], [g], mq, vq),
+           ([p], [g], m, v, s, s), ([p], [g], mq, vq, s[:1], s), ([p], [g], mq, vq, s, s.cpu()),
+           ([p], [g[:299]], m, v), ([p], [g.cpu()], m, v), ([p.half()], [g], m, v), ([p[::2]], [g[::2]], m, v),
+           ([p], [g, g], m, v), ([p], ["g"], m, v)]
+    for args in bad:
+        with pytest.raises((ValueError, TypeError)):
+            ssm.ssm_adamw_step(*args, **opt)
+    for scale in (torch.ones(2, device="cuda"), torch.ones(1), torch.ones(1, device="cuda").double()):
+        with pytest.raises((ValueError, TypeError)):
+            ssm.ssm_adamw_step([p], [g], m, v, grad_scale=scale, **opt)
+    with pytest.raises(ssm.SsmError):
+        ssm.ssm_adamw_step([p], [g], m, v, **{**opt, "step": 0})
+    torch.cuda.synchronize()
+    assert bool((p == 1).all()) and not bool(m.any()) and not bool(v.any())

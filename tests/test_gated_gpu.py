@@ -272,3 +272,25 @@ def test_captured_in_a_graph():
         assert bitwise_equal(y, want["y"]) and bitwise_equal(hf, want["h_final"])
         assert bitwise_equal(g["dx"], want["dx"]) and bitwise_equal(g["ddecay"], want["ddecay"])
         call(d)  # eager work between the replays
+
+
+def test_step_refuses_what_does_not_fit():
+    shape = (2, 3, 64)
+    rand = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+    good = {"h": rand(*shape), "x_t": rand(*shape), "r_t": rand(*shape), "i_t": rand(*shape), "decay": rand(2, 64),
+            "y_t": torch.zeros(shape, device="cuda")}
+    before = good["h"].clone()
+    for name, t in good.items():
+        wrong = [t[..., :63].contiguous(), t.to(torch.float16), t.cpu(), t.double()]
+        if name != "x_t":  # x_t's dtype is the call's
+            wrong.append(t.bfloat16())
+        if name not in ("x_t", "decay"):
+            wrong += [t[0], torch.empty(2, 3, 128, device="cuda")[..., ::2]]
+        for bad in wrong:
+            with pytest.raises((ValueError, TypeError)):
+                ssm.ssm_gated_step(**{**good, name: bad})
+    for bad in (0.0, -1.0, float("inf"), float("nan")):
+        with pytest.raises(ssm.SsmError):
+            ssm.ssm_gated_step(**good, c=bad)
+    assert bitwise_equal(good["h"], before) and not bool(good["y_t"].any())
+    assert ssm.ssm_gated_step(**good) is good["y_t"] and bool(good["y_t"].any())
