@@ -6,7 +6,9 @@
 // 281), longer than the step's kernels; here it takes 0.02 us. A single token's call has seven
 // tensors and a kernel of 2.6 us.
 //
-// The entry points of the library come as addresses, from the binding that has loaded it.
+// The entry points of the library come as addresses, from the binding that has loaded it. A call
+// returns what it has made; the status where the library refuses; None where an argument is not
+// as it should be.
 #include "ssm_scan.h"
 
 #define PY_SSIZE_T_CLEAN
@@ -17,6 +19,7 @@
 
 #include <cstdint>
 #include <exception>
+#include <initializer_list>
 #include <vector>
 
 namespace {
@@ -116,8 +119,7 @@ PyObject *no_exceptions(F fn) {
     }
 }
 
-// gated_step(entry, stream, h, x_t, r_t, i_t, decay, c, y_t or None): y_t; the status where the
-// library refuses; None where an argument is not as it should be.
+// gated_step(entry, stream, h, x_t, r_t, i_t, decay, c, y_t or None): y_t.
 PyObject *gated_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 9) return PyErr_Format(PyExc_TypeError, "9 arguments expected, got %zd", n);
     return no_exceptions([&]() -> PyObject * {
@@ -158,8 +160,8 @@ PyObject *gated_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
 }
 
 // adamw_step(entry, stream, block, params, grads, exp_avg, exp_avg_sq, avg_scale, avg_sq_scale,
-// grad_scale, lr, beta1, beta2, eps, weight_decay, step): the status; None where an array of the
-// moments is not as it should be; a Python error where a parameter or gradient is not.
+// grad_scale, lr, beta1, beta2, eps, weight_decay, step): the status; a Python error where a
+// parameter or a gradient is not as it should be.
 PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 16) return PyErr_Format(PyExc_TypeError, "16 arguments expected, got %zd", n);
     return no_exceptions([&]() -> PyObject * {
@@ -194,7 +196,197 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
     });
 }
 
+// What the larger calls share: the first tensor's device and type, what is read of the arguments,
+// new tensors, and the workspace, which lives until the call is enqueued.
+struct Call {
+    const at::Tensor &first;
+    const at::ScalarType io;
+    const int device;
+    bool ok;
+    explicit Call(PyObject *o, size_t dims)
+        : first(THPVariable_Unpack(o)), io(first.scalar_type()), device(first.is_cuda() ? (int)first.get_device() : -1),
+          ok(device >= 0 && first.sizes().size() == dims && (io == at::kFloat || io == at::kBFloat16)) {}
+    ssm_dtype kind() const { return io == at::kFloat ? SSM_F32 : SSM_BF16; }
+    void *in(PyObject *o, at::ScalarType type, at::IntArrayRef sizes) { return optional(o, type, sizes, device, &ok); }
+    void *need(PyObject *o, at::ScalarType type, at::IntArrayRef sizes) { return address(o, type, sizes, device, &ok); }
+    // The caller's tensor or, for None, a new one.
+    at::Tensor out(PyObject *o, at::ScalarType type, at::IntArrayRef sizes) {
+        if (o == Py_None) return fresh(type, sizes);
+        need(o, type, sizes);
+        return ok ? THPVariable_Unpack(o) : at::Tensor();
+    }
+    at::Tensor fresh(at::ScalarType type, at::IntArrayRef sizes) const {
+        return at::empty(sizes, first.options().dtype(type).requires_grad(false));
+    }
+};
+void *at_of(const at::Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
+PyObject *wrap(const at::Tensor &t) {
+    if (t.defined()) return THPVariable_Wrap(t);
+    Py_RETURN_NONE;
+}
+// The status, or the tensors where it is SSM_OK; an undefined one is None.
+PyObject *result(ssm_status st, std::initializer_list<at::Tensor> outs) {
+    if (st != SSM_OK) return PyLong_FromLong(st);
+    PyObject *tuple = PyTuple_New((Py_ssize_t)outs.size());
+    Py_ssize_t k = 0;
+    for (const at::Tensor &t : outs) {
+        PyObject *o = tuple ? wrap(t) : nullptr;
+        if (!o) {
+            Py_XDECREF(tuple);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(tuple, k++, o);
+    }
+    return tuple;
+}
+at::ScalarType byte_type(PyObject *o) {  // bool or uint8
+    return THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kBool ? at::kBool : at::kByte;
+}
+
+// gated_fwd(entry, workspace size's entry, stream, x, r, i, decay, h0, reset, c, y, h_final, states,
+// want_h_final, save): (y, h_final, states).
+PyObject *gated_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 15) return PyErr_Format(PyExc_TypeError, "15 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_gated_fwd))PyLong_AsVoidPtr(args[0]);
+        const auto size = (decltype(&ssm_gated_fwd_workspace))PyLong_AsVoidPtr(args[1]);
+        void *const stream = PyLong_AsVoidPtr(args[2]);
+        const float c = (float)PyFloat_AsDouble(args[9]);
+        if (PyErr_Occurred()) return nullptr;
+        if (!THPVariable_Check(args[3])) Py_RETURN_NONE;
+        Call k(args[3], 3);
+        if (!k.ok) Py_RETURN_NONE;
+        const at::IntArrayRef all = k.first.sizes();
+        const int64_t b = all[0], L = all[1], D = all[2], ends[2] = {b, D}, steps[2] = {b, L},
+                      rows[3] = {b, (L + SSM_GATED_STATE_EVERY - 1) / SSM_GATED_STATE_EVERY, D};
+        const void *const x = k.need(args[3], k.io, all), *const r = k.need(args[4], k.io, all), *const i = k.need(args[5], k.io, all);
+        const float *const decay = (const float *)k.need(args[6], at::kFloat, D);
+        const float *const h0 = (const float *)k.in(args[7], at::kFloat, ends);
+        const uint8_t *const reset = (const uint8_t *)k.in(args[8], byte_type(args[8]), steps);
+        if (!k.ok) Py_RETURN_NONE;
+        const at::Tensor y = k.out(args[10], k.io, all);
+        const at::Tensor h = args[11] != Py_None || args[13] == Py_True ? k.out(args[11], at::kFloat, ends) : at::Tensor();
+        const at::Tensor states = args[12] != Py_None || args[14] == Py_True ? k.out(args[12], at::kFloat, rows) : at::Tensor();
+        if (!k.ok) Py_RETURN_NONE;
+        const size_t bytes = size(b, L, D);
+        const at::Tensor ws = bytes ? k.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(x, r, i, decay, h0, reset, c, at_of(y), (float *)at_of(h), (float *)at_of(states), b, L, D, k.kind(),
+                   at_of(ws), bytes, stream);
+        Py_END_ALLOW_THREADS
+        return result(st, {y, h, states});
+    });
+}
+
+// gated_bwd(entry, workspace size's entry, stream, x, r, i, decay, states, reset, dy, dh_final, c,
+// want_dh0): (dx, dr, di, ddecay, dh0).
+PyObject *gated_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 13) return PyErr_Format(PyExc_TypeError, "13 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_gated_bwd))PyLong_AsVoidPtr(args[0]);
+        const auto size = (decltype(&ssm_gated_bwd_workspace))PyLong_AsVoidPtr(args[1]);
+        void *const stream = PyLong_AsVoidPtr(args[2]);
+        const float c = (float)PyFloat_AsDouble(args[11]);
+        if (PyErr_Occurred()) return nullptr;
+        if (!THPVariable_Check(args[3])) Py_RETURN_NONE;
+        Call k(args[3], 3);
+        if (!k.ok) Py_RETURN_NONE;
+        const at::IntArrayRef all = k.first.sizes();
+        const int64_t b = all[0], L = all[1], D = all[2], ends[2] = {b, D}, steps[2] = {b, L},
+                      rows[3] = {b, (L + SSM_GATED_STATE_EVERY - 1) / SSM_GATED_STATE_EVERY, D};
+        const void *const x = k.need(args[3], k.io, all), *const r = k.need(args[4], k.io, all), *const i = k.need(args[5], k.io, all);
+        const float *const decay = (const float *)k.need(args[6], at::kFloat, D);
+        const float *const states = (const float *)k.need(args[7], at::kFloat, rows);
+        const uint8_t *const reset = (const uint8_t *)k.in(args[8], byte_type(args[8]), steps);
+        const void *const dy = k.need(args[9], k.io, all);
+        const float *const dh = (const float *)k.in(args[10], at::kFloat, ends);
+        if (!k.ok) Py_RETURN_NONE;
+        const at::Tensor dx = k.fresh(k.io, all), dr = k.fresh(k.io, all), di = k.fresh(k.io, all), dd = k.fresh(at::kFloat, D);
+        const at::Tensor dh0 = args[12] == Py_True ? k.fresh(at::kFloat, ends) : at::Tensor();
+        const size_t bytes = size(b, L, D);
+        const at::Tensor ws = bytes ? k.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(x, r, i, decay, states, reset, c, dy, dh, at_of(dx), at_of(dr), at_of(di), (float *)at_of(dd),
+                   (float *)at_of(dh0), b, L, D, k.kind(), at_of(ws), bytes, stream);
+        Py_END_ALLOW_THREADS
+        return result(st, {dx, dr, di, dd, dh0});
+    });
+}
+
+// xent_fwd(entry, workspace size's entry, stream, hidden, weight, targets, ignore_index, loss, lse,
+// mean): (loss, lse, mean).
+PyObject *xent_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 10) return PyErr_Format(PyExc_TypeError, "10 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_xent_fwd))PyLong_AsVoidPtr(args[0]);
+        const auto size = (decltype(&ssm_xent_fwd_workspace))PyLong_AsVoidPtr(args[1]);
+        void *const stream = PyLong_AsVoidPtr(args[2]);
+        const int64_t ignore = PyLong_AsLongLong(args[6]);
+        if (PyErr_Occurred()) return nullptr;
+        if (!THPVariable_Check(args[3]) || !THPVariable_Check(args[4]) || THPVariable_Unpack(args[4]).dim() != 2) Py_RETURN_NONE;
+        Call k(args[3], 2);
+        if (!k.ok) Py_RETURN_NONE;
+        const int64_t T = k.first.size(0), K = k.first.size(1), V = THPVariable_Unpack(args[4]).size(0), head[2] = {V, K};
+        const void *const hidden = k.need(args[3], k.io, k.first.sizes()), *const weight = k.need(args[4], k.io, head);
+        const int64_t *const targets = (const int64_t *)k.need(args[5], at::kLong, T);
+        if (!k.ok) Py_RETURN_NONE;
+        const at::Tensor loss = k.out(args[7], at::kFloat, T), lse = k.out(args[8], at::kFloat, T), mean = k.out(args[9], at::kFloat, 2);
+        if (!k.ok) Py_RETURN_NONE;
+        const size_t bytes = size(T, K, V, k.kind());
+        const at::Tensor ws = bytes ? k.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(hidden, weight, targets, ignore, (float *)at_of(loss), (float *)at_of(lse), (float *)at_of(mean), T, K, V,
+                   k.kind(), at_of(ws), bytes, stream);
+        Py_END_ALLOW_THREADS
+        return result(st, {loss, lse, mean});
+    });
+}
+
+// xent_bwd(entry, workspace size's entry, stream, hidden, weight, targets, ignore_index, lse, mean,
+// dloss, dmean, want_dhidden, want_dweight): (dhidden, dweight).
+PyObject *xent_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 13) return PyErr_Format(PyExc_TypeError, "13 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_xent_bwd))PyLong_AsVoidPtr(args[0]);
+        const auto size = (decltype(&ssm_xent_bwd_workspace))PyLong_AsVoidPtr(args[1]);
+        void *const stream = PyLong_AsVoidPtr(args[2]);
+        const int64_t ignore = PyLong_AsLongLong(args[6]);
+        if (PyErr_Occurred()) return nullptr;
+        if (!THPVariable_Check(args[3]) || !THPVariable_Check(args[4]) || THPVariable_Unpack(args[4]).dim() != 2) Py_RETURN_NONE;
+        Call k(args[3], 2);
+        if (!k.ok) Py_RETURN_NONE;
+        const int64_t T = k.first.size(0), K = k.first.size(1), V = THPVariable_Unpack(args[4]).size(0), head[2] = {V, K};
+        const void *const hidden = k.need(args[3], k.io, k.first.sizes()), *const weight = k.need(args[4], k.io, head);
+        const int64_t *const targets = (const int64_t *)k.need(args[5], at::kLong, T);
+        const float *const lse = (const float *)k.need(args[7], at::kFloat, T), *const mean = (const float *)k.need(args[8], at::kFloat, 2);
+        const float *const dloss = (const float *)k.in(args[9], at::kFloat, T);
+        const float *dmean = nullptr;
+        if (args[10] != Py_None) {
+            if (!THPVariable_Check(args[10]) || THPVariable_Unpack(args[10]).numel() != 1) Py_RETURN_NONE;
+            dmean = (const float *)k.need(args[10], at::kFloat, THPVariable_Unpack(args[10]).sizes());
+        }
+        if (!k.ok) Py_RETURN_NONE;
+        const at::Tensor dh = args[11] == Py_True ? k.fresh(k.io, k.first.sizes()) : at::Tensor();
+        const at::Tensor dw = args[12] == Py_True ? k.fresh(k.io, head) : at::Tensor();
+        const size_t bytes = size(T, K, V, k.kind());
+        const at::Tensor ws = bytes ? k.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(hidden, weight, targets, ignore, lse, mean, dloss, dmean, at_of(dh), at_of(dw), T, K, V, k.kind(),
+                   at_of(ws), bytes, stream);
+        Py_END_ALLOW_THREADS
+        return result(st, {dh, dw});
+    });
+}
+
 PyMethodDef methods[] = {
+    {"gated_fwd", (PyCFunction)(void (*)(void))gated_fwd, METH_FASTCALL, "ssm_gated_fwd for tensors."},
+    {"gated_bwd", (PyCFunction)(void (*)(void))gated_bwd, METH_FASTCALL, "ssm_gated_bwd for tensors."},
+    {"xent_fwd", (PyCFunction)(void (*)(void))xent_fwd, METH_FASTCALL, "ssm_xent_fwd for tensors."},
+    {"xent_bwd", (PyCFunction)(void (*)(void))xent_bwd, METH_FASTCALL, "ssm_xent_bwd for tensors."},
     {"gated_step", (PyCFunction)(void (*)(void))gated_step, METH_FASTCALL, "ssm_gated_step for tensors."},
     {"adamw_step", (PyCFunction)(void (*)(void))adamw_step, METH_FASTCALL, "ssm_adamw_step for lists of tensors."},
     {nullptr, nullptr, 0, nullptr}};

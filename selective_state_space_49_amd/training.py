@@ -25,8 +25,9 @@ _IO = {_f32: SSM_F32, torch.bfloat16: SSM_BF16}
 
 
 # Small calls are shorter than a careful marshalling of their arguments, so these take the short
-# way: one comparison where an argument is right, and _dev's checks only to say what is wrong
-# with it. The step of a token and of an optimizer go through the _tensor_table extension.
+# way: through the _tensor_table extension, which takes a call whose arguments are right and whose
+# workspace is not the caller's. What it does not take goes on here, argument by argument: one
+# comparison where it is right, and _dev's checks only to say what is wrong with it.
 def _need(t: Optional[torch.Tensor], name: str, shape, dtype):
     """The address of a contiguous GPU tensor of this shape and dtype, or None."""
     if t is None:
@@ -63,6 +64,13 @@ def _table_module():
 
 
 _entries: dict = {}
+
+
+def _made(got):
+    """What a call of the extension made, or SsmError."""
+    if isinstance(got, int):
+        _check(got)
+    return got
 
 
 def _entry(name: str) -> int:
@@ -111,6 +119,15 @@ def ssm_gated_fwd(x, r, i, decay, h0=None, reset=None, *, c=8.0, y=None, h_final
     """The gated recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t with
     a_t = exp(-c softplus(decay) sigmoid(r_t)): y [b, L, D] and h_final [b, D] float32.
     reset [b, L] (bool): steps that start a document. states: see ssm_gated_fwd_save."""
+    return _gated_fwd(x, r, i, decay, h0, reset, c, y, h_final, states, workspace, want_h_final, False)[:2]
+
+
+def _gated_fwd(x, r, i, decay, h0, reset, c, y, h_final, states, workspace, want_h_final, save):
+    if workspace is None and x.is_cuda:
+        got = _table_module().gated_fwd(_entry("ssm_gated_fwd"), _entry("ssm_gated_fwd_workspace"), _stream(x), x, r, i,
+                                        decay, h0, reset, c, y, h_final, states, bool(want_h_final), save)
+        if got is not None:
+            return _made(got)
     lib = load_library()
     shape, io, kind = x.shape, x.dtype, _kind(x)
     b, L, D = shape
@@ -118,6 +135,8 @@ def ssm_gated_fwd(x, r, i, decay, h0=None, reset=None, *, c=8.0, y=None, h_final
         y = torch.empty_like(x)
     if h_final is None and want_h_final:
         h_final = torch.empty((b, D), dtype=_f32, device=x.device)
+    if states is None and save:
+        states = torch.empty((b, _states_rows(L), D), dtype=_f32, device=x.device)
     ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_gated_fwd_workspace(b, L, D), x.device)
     _check(lib.ssm_gated_fwd(_need(x, "x", shape, io), _need(r, "r", shape, io), _need(i, "i", shape, io),
                              _need(decay, "decay", (D,), _f32), _need(h0, "h0", (b, D), _f32),
@@ -125,25 +144,25 @@ def ssm_gated_fwd(x, r, i, decay, h0=None, reset=None, *, c=8.0, y=None, h_final
                              _need(h_final, "h_final", (b, D), _f32),
                              _need(states, "states", (b, _states_rows(L), D), _f32), b, L, D, kind, ws_at,
                              ws_bytes, _stream(x)))
-    return y, h_final
+    return y, h_final, states
 
 
 def ssm_gated_fwd_save(x, r, i, decay, h0=None, reset=None, *, c=8.0, y=None, h_final=None, states=None,
                        workspace=None):
     """The training forward: ssm_gated_fwd, and the state entering every 64th step
     [b, ceil(L / 64), D] float32 for ssm_gated_bwd."""
-    b, L, D = x.shape
-    if states is None:
-        states = torch.empty((b, _states_rows(L), D), dtype=_f32, device=x.device)
-    y, h_final = ssm_gated_fwd(x, r, i, decay, h0, reset, c=c, y=y, h_final=h_final, states=states,
-                               workspace=workspace)
-    return y, h_final, states
+    return _gated_fwd(x, r, i, decay, h0, reset, c, y, h_final, states, workspace, True, True)
 
 
 def ssm_gated_bwd(x, r, i, decay, states, reset=None, *, dy, dh_final=None, c=8.0, want_dh0=True,
                   workspace=None):
     """Gradients of sum(dy y) + sum(dh_final h_final): a dict of dx, dr, di (x's dtype),
     ddecay [D] and dh0 [b, D] (float32; None unless want_dh0)."""
+    if workspace is None and x.is_cuda:
+        got = _table_module().gated_bwd(_entry("ssm_gated_bwd"), _entry("ssm_gated_bwd_workspace"), _stream(x), x, r, i,
+                                        decay, states, reset, dy, dh_final, c, bool(want_dh0))
+        if got is not None:
+            return dict(zip(("dx", "dr", "di", "ddecay", "dh0"), _made(got)))
     lib = load_library()
     shape, io, kind = x.shape, x.dtype, _kind(x)
     b, L, D = shape
@@ -172,9 +191,7 @@ def ssm_gated_step(h, x_t, r_t, i_t, decay, *, c=8.0, y_t=None):
                                    (i_t, "i_t", shape, io), (decay, "decay", (Ln, D), _f32), (y_t, "y_t", shape, io)):
             _need(t, name, of, dtype)
         raise ValueError("h, r_t, i_t, decay and y_t must be on x_t's GPU")
-    if isinstance(got, int):
-        _check(got)
-    return got
+    return _made(got)
 
 
 class _GatedScan(torch.autograd.Function):
@@ -233,6 +250,11 @@ def ssm_xent_fwd(hidden, weight, targets, *, ignore_index=-100, loss=None, lse=N
     """Cross entropy of the logits hidden [T, K] weight [V, K]^T against targets [T], without
     the logits in memory: loss [T], lse [T] and mean [2] (the mean over the tokens that are
     not ignored, and 1 over their number), all float32."""
+    if workspace is None and hidden.is_cuda:
+        got = _table_module().xent_fwd(_entry("ssm_xent_fwd"), _entry("ssm_xent_fwd_workspace"), _stream(hidden), hidden,
+                                       weight, targets, ignore_index, loss, lse, mean)
+        if got is not None:
+            return _made(got)
     lib = load_library()
     T, K, V, kind, inputs = _head(hidden, weight, targets)
     dev = hidden.device
@@ -249,6 +271,12 @@ def ssm_xent_bwd(hidden, weight, targets, lse, mean, *, dloss=None, dmean=None, 
                  want_dhidden=True, want_dweight=True, workspace=None):
     """Gradients of sum(dloss loss) + dmean mean[0] (dloss [T] float32, dmean one float32 on
     the GPU; None = 0): dhidden [T, K] and dweight [V, K] (None where not wanted)."""
+    if workspace is None and hidden.is_cuda:
+        got = _table_module().xent_bwd(_entry("ssm_xent_bwd"), _entry("ssm_xent_bwd_workspace"), _stream(hidden), hidden,
+                                       weight, targets, ignore_index, lse, mean, dloss, dmean, bool(want_dhidden),
+                                       bool(want_dweight))
+        if got is not None:
+            return _made(got)
     lib = load_library()
     T, K, V, kind, inputs = _head(hidden, weight, targets)
     dhidden = torch.empty_like(hidden) if want_dhidden else None
