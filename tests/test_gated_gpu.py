@@ -294,3 +294,30 @@ def test_step_refuses_what_does_not_fit():
             ssm.ssm_gated_step(**good, c=bad)
     assert bitwise_equal(good["h"], before) and not bool(good["y_t"].any())
     assert ssm.ssm_gated_step(**good) is good["y_t"] and bool(good["y_t"].any())
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("b,L,D,h0,reset", [(34, 300, 66, True, True), (33, 290, 65, True, True), (1, 200, 2178, True, False),
+                                            (40, 1, 70, False, True)])
+def test_many_channels_side_by_side(b, L, D, h0, reset, io):
+    say("gated wide", b, L, D, io)
+    d = make(b, L, D, io, seed=b + L + D, h0=h0, reset=reset)
+    check(call(dev(d)), train_ref.gated(**d), io)
+
+
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("D", [64, 65])
+def test_rows_do_not_depend_on_their_neighbours(D, io):
+    # the same rows in a batch of 40 and in batches of 4: the same bits, with a NaN before a reset too
+    say("gated rows", D, io)
+    d = dev(make(40, 700, D, io, seed=D, h0=True, reset=True))
+    d["x"][7, 30] = float("nan")
+    d["reset"][7, 31] = True
+    all_rows = call(d)
+    for first in (0, 4, 36):
+        some = {k: t if k == "decay" else t[first:first + 4].contiguous() for k, t in d.items()}
+        part = call(some)
+        for k in ("y", "h_final", "states", "dx", "dr", "di", "dh0"):
+            a, b = all_rows[k][first:first + 4].contiguous(), part[k]
+            assert bool((a.isnan() == b.isnan()).all()) and bitwise_equal(a.nan_to_num(), b.nan_to_num()), (first, k)
+    assert not bool(all_rows["y"][7, 31:].isnan().any()) and bool(all_rows["y"][7, 30].isnan().all())
