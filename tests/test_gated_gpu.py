@@ -321,3 +321,20 @@ def test_rows_do_not_depend_on_their_neighbours(D, io):
             a, b = all_rows[k][first:first + 4].contiguous(), part[k]
             assert bool((a.isnan() == b.isnan()).all()) and bitwise_equal(a.nan_to_num(), b.nan_to_num()), (first, k)
     assert not bool(all_rows["y"][7, 31:].isnan().any()) and bool(all_rows["y"][7, 30].isnan().all())
+
+
+def test_calls_refuse_what_does_not_fit():
+    d = dev(make(2, 70, 10, torch.float32, seed=1, h0=True, reset=True))
+    y, hf, st = ssm.ssm_gated_fwd_save(d["x"], d["r"], d["i"], d["decay"], d["h0"], d["reset"])
+    fwd = {k: d[k] for k in ("x", "r", "i", "decay", "h0", "reset")} | {"y": y, "h_final": hf, "states": st}
+    bwd = {k: d[k] for k in ("x", "r", "i", "decay", "reset", "dy", "dh_final")} | {"states": st}
+    for fn, good in ((ssm.ssm_gated_fwd, fwd), (ssm.ssm_gated_bwd, bwd)):
+        for name, t in good.items():
+            wrong = [t[..., :-1].contiguous(), t.cpu(), t.to(torch.float64), torch.stack([t, t], -1)[..., 0]]
+            for bad in wrong[1:] if name == "x" else wrong:  # x's sizes are the call's
+                with pytest.raises((ValueError, TypeError)):
+                    fn(**{**good, name: bad})
+        with pytest.raises(ssm.SsmError):
+            fn(**good, c=-1.0)
+    with pytest.raises(ssm.SsmError):  # an output that is an input
+        ssm.ssm_gated_fwd(**{**fwd, "y": d["x"]})

@@ -220,3 +220,21 @@ def test_several_pieces_of_the_vocabulary(T, K, V, io, each):
     ref = train_ref.xent(hidden, weight, target, dloss=dloss, dmean=2.0)
     got = call(hidden, weight, target, None if dloss is None else dloss.cuda(), torch.tensor(2.0, device="cuda"))
     check(hidden, weight, target, ref, got, io, 1)
+
+
+def test_calls_refuse_what_does_not_fit():
+    hidden, weight, target = (t.cuda() for t in make(20, 16, 50, torch.float32, seed=14))
+    loss, lse, mean = ssm.ssm_xent_fwd(hidden, weight, target)
+    one = torch.ones((), device="cuda")
+    fwd = {"hidden": hidden, "weight": weight, "targets": target, "loss": loss, "lse": lse, "mean": mean}
+    bwd = {k: fwd[k] for k in ("hidden", "weight", "targets", "lse", "mean")} | {"dloss": loss, "dmean": one}
+    for fn, good in ((ssm.ssm_xent_fwd, fwd), (ssm.ssm_xent_bwd, bwd)):
+        for name, t in good.items():
+            wrong = [t.cpu(), t.to(torch.float64), torch.stack([t, t], -1)[..., 0] if t.dim() else t.expand(2)]
+            if t.dim():
+                wrong.append(t[..., :-1].contiguous())
+            for bad in wrong:
+                with pytest.raises((ValueError, TypeError)):
+                    fn(**{**good, name: bad})
+    with pytest.raises(ssm.SsmError):  # an output that is an input
+        ssm.ssm_xent_fwd(hidden, weight, target, loss=weight.view(-1)[:20])
