@@ -639,41 +639,55 @@ __global__ void __launch_bounds__(256) k_pack(Arrays arrays, Tokens tokens) {
     }
 }
 
-// The largest finite |value| of a block's rows, 16 bytes of a row a lane.
+// The largest finite |value| that a thread sees, 16 bytes at a time.
 template <typename IO>
-__device__ __forceinline__ uint32_t peak_of_rows(const Array &a, const Tokens &tokens) {
-    constexpr int N = 16 / sizeof(IO);
+struct Peak {
+    static constexpr int N = 16 / sizeof(IO);
     typedef IO iov __attribute__((ext_vector_type(N), aligned(sizeof(IO))));
-    const IO *src = (const IO *)a.src;
-    const int down = kPeakThreads / a.across;
-    const int64_t c0 = (int64_t)(threadIdx.x % a.across) * N, step = (int64_t)a.peak_blocks * down;
-    const bool mask = a.kind != Rows::Vocabulary, weigh = a.kind == Rows::Weighed;
-    const float same = weigh ? tokens.same() : 0.0f;
     uint32_t top = 0;
+    __device__ __forceinline__ void see(IO e, float f) {
+        const uint32_t b = __float_as_uint(Io<IO>::ld(&e) * f) & 0x7fffffffu;
+        top = b < 0x7f800000u ? max(top, b) : top;
+    }
+    // Of an array whose rows are all alike: as one row.
+    __device__ __forceinline__ void flat(const Array &a) {
+        const IO *src = (const IO *)a.src;
+        const int64_t total = a.rows * a.cols, whole = total / N, step = (int64_t)a.peak_blocks * kPeakThreads;
+        const int64_t at = (int64_t)(blockIdx.x - a.peak_first) * kPeakThreads + threadIdx.x;
 #pragma unroll 4
-    for (int64_t r = (int64_t)(blockIdx.x - a.peak_first) * down + threadIdx.x / a.across; r < a.rows; r += step) {
-        if (mask && tokens.target(r) == -1) continue;
-        const float f = weigh ? tokens.weight(r, same) : 1.0f;
-        for (int64_t c = c0; c < a.cols; c += a.across * N) {
-            const IO *at = src + r * a.cols + c;
-            const auto see = [&](IO e) {
-                const uint32_t b = __float_as_uint(Io<IO>::ld(&e) * f) & 0x7fffffffu;
-                top = b < 0x7f800000u ? max(top, b) : top;
-            };
-            if (c + N <= a.cols) {
-                const iov v = *(const iov *)at;
+        for (int64_t e = at; e < whole; e += step) {
+            const iov v = *(const iov *)(src + e * N);
 #pragma unroll
-                for (int k = 0; k < N; ++k) see(v[k]);
-            } else {
-                for (int64_t k = c; k < a.cols; ++k) see(src[r * a.cols + k]);
+            for (int k = 0; k < N; ++k) see(v[k], 1.0f);
+        }
+        if (at < total - whole * N) see(src[whole * N + at], 1.0f);
+    }
+    // Of the rows of tokens.
+    __device__ __forceinline__ void by_rows(const Array &a, const Tokens &tokens) {
+        const IO *src = (const IO *)a.src;
+        const int down = kPeakThreads / a.across;
+        const int64_t c0 = (int64_t)(threadIdx.x % a.across) * N, step = (int64_t)a.peak_blocks * down;
+        const bool weigh = a.kind == Rows::Weighed;
+        const float same = weigh ? tokens.same() : 0.0f;
+        for (int64_t r = (int64_t)(blockIdx.x - a.peak_first) * down + threadIdx.x / a.across; r < a.rows; r += step) {
+            if (tokens.target(r) == -1) continue;
+            const float f = weigh ? tokens.weight(r, same) : 1.0f;
+            for (int64_t c = c0; c < a.cols; c += a.across * N) {
+                const IO *at = src + r * a.cols + c;
+                if (c + N <= a.cols) {
+                    const iov v = *(const iov *)at;
+#pragma unroll
+                    for (int k = 0; k < N; ++k) see(v[k], f);
+                } else {
+                    for (int64_t k = c; k < a.cols; ++k) see(src[r * a.cols + k], f);
+                }
             }
         }
     }
-    return top;
-}
+};
 
-// part[block] = the bits of the largest finite |value|. A block of 1024 has 1024 / across rows at
-// a time. Its few blocks leave so few values that every block that needs the largest of them
+// part[block] = the bits of the largest finite |value|. Of tokens, a block of 1024 has
+// 1024 / across rows at a time. Its few blocks leave so few values that every block that needs the largest of them
 // looks through all: no atomics, and nothing to be cleared first.
 template <typename IO>
 __global__ void __launch_bounds__(kPeakThreads) k_peak(Arrays arrays, Tokens tokens) {
@@ -681,7 +695,10 @@ __global__ void __launch_bounds__(kPeakThreads) k_peak(Arrays arrays, Tokens tok
     int n = 0;
     while (n + 1 < arrays.n && blockIdx.x >= arrays.a[n + 1].peak_first) ++n;
     const Array &a = arrays.a[n];
-    uint32_t top = peak_of_rows<IO>(a, tokens);
+    Peak<IO> peak;
+    if (a.kind == Rows::Vocabulary) peak.flat(a);
+    else peak.by_rows(a, tokens);
+    uint32_t top = peak.top;
     for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
     if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
     __syncthreads();
@@ -827,11 +844,11 @@ Tiling tiling(int64_t M, int64_t N, int64_t steps, bool may_split) {
     double least = 0;
     for (const int tile : {kSmall, kBig}) {
         const int64_t n = (int64_t)blocks(M, tile) * blocks(N, tile);
-        const int64_t most = !may_split ? 1 : std::min(std::min((tile == kBig ? 1 : 2) * kCus / n, steps / 2), (int64_t)64);
+        const int64_t most = !may_split ? 1 : std::min(std::min((tile == kBig ? 1 : 2) * kCus / n, steps / 2), (int64_t)128);
         for (int64_t s = 1; s <= std::max<int64_t>(most, 1); ++s) {
             const double k = (double)steps / (double)s;
             const int64_t rounds = (int64_t)blocks(n * s, kCus), pairs = rounds / 2;
-            const double join = s == 1 ? 0.0 : 4.0 + (double)s * (double)M * (double)N * 8.0 / 5e6;
+            const double join = s == 1 ? 0.0 : 4.0 + 0.05 * (double)s + (double)s * (double)M * (double)N * 8.0 / 5e6;
             const double time = join + (tile == kBig ? (double)rounds * (8.0 + 1.72 * k)
                                                      : (double)pairs * (5.0 + 1.14 * k) + (double)(rounds % 2) * (5.0 + 0.9 * k));
             if (!best.tile || time < least) {
@@ -958,7 +975,9 @@ struct Copies {
             a.part = l.peak_part + peak * kPeakBlocks;
             a.across = 16;
             while (a.across < lanes && a.across < kPeakThreads) a.across *= 2;
-            a.peak_blocks = (unsigned)std::min<int64_t>(blocks(rows, kPeakThreads / a.across), kPeakBlocks);
+            const int64_t most = kind == Rows::Vocabulary ? (rows * cols / kWide + kPeakThreads) / kPeakThreads
+                                                          : blocks(rows, kPeakThreads / a.across);
+            a.peak_blocks = (unsigned)std::min<int64_t>(most, kPeakBlocks);
             peak_grid += a.peak_blocks;
         }
         return {dst, l.ldk, a.plane, a.peak, rows_out};
