@@ -66,7 +66,7 @@ __device__ __forceinline__ Gate gate(float r, float i, float ck) {
 // publishes the state that leaves it, and only then walks its steps with the true state. So each
 // input is read once, where summary and rescan passes read it twice. What bounds it is the
 // bytes: 8 a step and channel in bfloat16 forwards, 14 backwards. 262144 steps of 4096 channels
-// take 1.60 ms (8.6 GB at 5.4 TB/s, where a large copy moves 4.9), and 2 x 4096 steps of 8192
+// take 1.61 ms (8.6 GB at 5.3 TB/s, where a large copy moves 4.9), and 2 x 4096 steps of 8192
 // channels, forwards with the stored states and backwards, 0.316 ms (1.5 GB at 4.7 TB/s).
 //
 // A published word is 64 bits, {H, P | flags}, written and read whole by relaxed atomics at
@@ -526,7 +526,8 @@ hipError_t fill(float *dst, const float *src, int64_t n, hipStream_t s) {
 
 // One token. A lane has N neighbouring channels of a layer, makes their decays once for S
 // sequences, and has the loads of all of them in flight. What bounds it is the bytes: 16 a
-// channel in bfloat16, half of them the state.
+// channel in bfloat16, half of them the state: 28 layers x 256 sequences x 8192 channels take
+// 170 us, 0.94 GB at 5.5 TB/s.
 template <typename IO, int N, int S>
 __global__ void __launch_bounds__(256) k_gated_step(GatedStepArgs p) {
     const int64_t d = ((int64_t)blockIdx.x * 256 + threadIdx.x) * N;

@@ -10,6 +10,10 @@
 //   backward   for a piece of the vocabulary at a time: the same product again, with
 //              G [token][vocab] = dlogits / w = exp(logit - lse) - onehot; then dweight rows =
 //              G^T (w hidden), both transposed, and dhidden += w G weight, weight transposed.
+// What bounds it is the matrix cores' power: 8192 tokens x 4096 x 32000 in bfloat16 take 1.72 ms
+// forwards and 5.1 ms backwards, 1.25 PFLOP/s, with the cores 64 to 75 % busy and the clock at
+// 1.5 to 1.75 of 2.4 GHz; with few tokens it is the weight's bytes (8 x 4096 x 32000: 0.26 ms for
+// 1.05 GB), with little of both the launches (100 x 256 x 1000: 37 us for six).
 // The matrix cores take 16 bits. Logits of bfloat16 operands are products of their own bits. In
 // the gradients' products, a token's weight w stays out of G, whose values lie in [-1, 1]:
 // dhidden takes it as a factor of its row.
