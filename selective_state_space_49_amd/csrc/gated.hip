@@ -182,7 +182,6 @@ __device__ __forceinline__ Place take_tile(const GatedArgs &p, uint32_t *ticket,
 }
 
 constexpr int kWaves = 8;
-constexpr int kFar = 12;
 constexpr int kFwdRows = 16, kBwdRows = 8;  // steps of a wave
 constexpr int kFwdTile = kFwdRows * kWaves, kBwdTile = kBwdRows * kWaves;
 static_assert(kFwdTile % SSM_GATED_STATE_EVERY == 0 && SSM_GATED_STATE_EVERY % kFwdRows == 0 &&
@@ -200,7 +199,7 @@ size_t words_bytes(int64_t batch, int64_t L, int64_t D, int tile) {
 // 16 steps of a wave, 128 of a tile: at two bfloat16 channels a lane, 48 loads of 4 bytes a
 // lane are in flight before the first gate, and the 2 x 32 floats of (a, b) still leave room
 // for four waves a SIMD.
-template <typename IO, int CPL, bool RESET, bool FAR>
+template <typename IO, int CPL, bool RESET, int FAR>
 __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint32_t *ticket, uint64_t *words) {
     constexpr int R = kFwdRows, CW = 64 * CPL;
     __shared__ float sP[kWaves][CW], sH[kWaves][CW], sC[CW];
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint3
             if (in && at.j > 0 && at.j + 1 < n_tiles)
                 __hip_atomic_store(mine + c, pack_word(tP[c], tH[c], kValid), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (at.j > 0) look_back<RESET, CPL, FAR ? kFar : 3>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
+        if (at.j > 0) look_back<RESET, CPL, FAR ? FAR : 3>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
             const float out = through<RESET>(tP[c], tH[c], carry[c]);
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint3
 // The same from the right: u_t = a_t g_t is what step t passes to its left, g_t = dy_t +
 // u_{t+1}. The states come from the stored row that enters the tile, through the waves'
 // forward pairs.
-template <typename IO, int CPL, bool RESET, bool FAR>
+template <typename IO, int CPL, bool RESET, int FAR>
 __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint32_t *ticket, uint64_t *words,
                                                               float *sums) {
     constexpr int R = kBwdRows, CW = 64 * CPL;
@@ -413,7 +412,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
             if (in && at.j > 0 && at.j + 1 < n_tiles)
                 __hip_atomic_store(mine + c, pack_word(tP[c], tU[c], kValid), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (at.j > 0) look_back<RESET, CPL, FAR ? kFar : 2>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
+        if (at.j > 0) look_back<RESET, CPL, FAR ? FAR : 2>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
             const float out = through<RESET>(tP[c], tU[c], carry[c]);
@@ -585,19 +584,23 @@ bool pairs(const GatedArgs &a, int io) {
                                    (uintptr_t)a.dx | (uintptr_t)a.dr | (uintptr_t)a.di) & 3) == 0;
 }
 
-// Up to 32 blocks of 64 channels side by side, 12 words at a time and one channel a lane: training
-// on 262144 steps of 256 channels takes 0.68 ms so, 0.79 with 8 words, and 2.21 as for many
-// channels; on 65536 steps of 1024 channels 0.45, 0.43 and 0.67; on 16384 steps of 4096 channels
-// (64 blocks) 0.39 with 8 words and 0.35 as for many.
-bool far(const GatedArgs &a) { return a.batch * tiles_of(a.D, 64) <= 32; }
+// The words read at a time, 0 for two or three, by the blocks of 64 channels side by side: 12 up to
+// 8 of them, 8 up to 32, with one channel a lane. Training on 262144 steps of 256 channels takes
+// 0.68 ms with 12, 0.79 with 8 and 2.21 as for many channels, on 16384 steps of 4096 channels 0.39
+// with 8 and 0.35 as for many; the forward alone on 262144 steps of 512 channels 0.30, 0.31 and
+// 0.61, of 1024 channels 0.56, 0.48 and 0.69, of 2048 channels 1.08, 0.92 and 0.90.
+int far(const GatedArgs &a) {
+    const int64_t side = a.batch * tiles_of(a.D, 64);
+    return side <= 8 ? 12 : side <= 32 ? 8 : 0;
+}
 
-template <typename IO, int CPL, bool FAR>
+template <typename IO, int CPL, int FAR>
 void run_fwd(const GatedArgs &a, uint32_t *ticket, uint64_t *words, hipStream_t s) {
     const dim3 grid((unsigned)(tiles_of(a.D, 64 * CPL) * a.batch * tiles_of(a.L, kFwdTile)));
     if (a.reset) k_gated_fwd<IO, CPL, true, FAR><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words);
     else k_gated_fwd<IO, CPL, false, FAR><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words);
 }
-template <typename IO, int CPL, bool FAR>
+template <typename IO, int CPL, int FAR>
 void run_bwd(const GatedArgs &a, uint32_t *ticket, uint64_t *words, float *sums, hipStream_t s) {
     const dim3 grid((unsigned)(tiles_of(a.D, 64 * CPL) * a.batch * tiles_of(a.L, kBwdTile)));
     if (a.reset) k_gated_bwd<IO, CPL, true, FAR><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words, sums);
@@ -619,10 +622,12 @@ hipError_t launch_gated_fwd(const GatedArgs &a, int io, hipStream_t s) {
     uint32_t *ticket;
     uint64_t *words;
     set_up(a, kFwdTile, &ticket, &words, s);
-    if (far(a)) io ? run_fwd<bf16_bits, 1, true>(a, ticket, words, s) : run_fwd<float, 1, true>(a, ticket, words, s);
-    else if (!io) run_fwd<float, 1, false>(a, ticket, words, s);
-    else if (pairs(a, io)) run_fwd<bf16_bits, 2, false>(a, ticket, words, s);
-    else run_fwd<bf16_bits, 1, false>(a, ticket, words, s);
+    const int ahead = far(a);
+    if (ahead == 12) io ? run_fwd<bf16_bits, 1, 12>(a, ticket, words, s) : run_fwd<float, 1, 12>(a, ticket, words, s);
+    else if (ahead == 8) io ? run_fwd<bf16_bits, 1, 8>(a, ticket, words, s) : run_fwd<float, 1, 8>(a, ticket, words, s);
+    else if (!io) run_fwd<float, 1, 0>(a, ticket, words, s);
+    else if (pairs(a, io)) run_fwd<bf16_bits, 2, 0>(a, ticket, words, s);
+    else run_fwd<bf16_bits, 1, 0>(a, ticket, words, s);
     return hipGetLastError();
 }
 
@@ -635,10 +640,12 @@ hipError_t launch_gated_bwd(const GatedArgs &a, int io, hipStream_t s) {
     uint64_t *words;
     set_up(a, kBwdTile, &ticket, &words, s);
     float *sums = (float *)((char *)a.ws + words_bytes(a.batch, a.L, a.D, kBwdTile));
-    if (far(a)) io ? run_bwd<bf16_bits, 1, true>(a, ticket, words, sums, s) : run_bwd<float, 1, true>(a, ticket, words, sums, s);
-    else if (!io) run_bwd<float, 1, false>(a, ticket, words, sums, s);
-    else if (pairs(a, io)) run_bwd<bf16_bits, 2, false>(a, ticket, words, sums, s);
-    else run_bwd<bf16_bits, 1, false>(a, ticket, words, sums, s);
+    const int ahead = far(a);
+    if (ahead == 12) io ? run_bwd<bf16_bits, 1, 12>(a, ticket, words, sums, s) : run_bwd<float, 1, 12>(a, ticket, words, sums, s);
+    else if (ahead == 8) io ? run_bwd<bf16_bits, 1, 8>(a, ticket, words, sums, s) : run_bwd<float, 1, 8>(a, ticket, words, sums, s);
+    else if (!io) run_bwd<float, 1, 0>(a, ticket, words, sums, s);
+    else if (pairs(a, io)) run_bwd<bf16_bits, 2, 0>(a, ticket, words, sums, s);
+    else run_bwd<bf16_bits, 1, 0>(a, ticket, words, sums, s);
     k_gated_ddecay<<<dim3((unsigned)((a.D + 63) / 64)), 1024, 0, s>>>(sums, a.decay, a.ddecay,
                                                                      a.batch * tiles_of(a.L, kBwdTile), a.D);
     return hipGetLastError();

@@ -338,3 +338,11 @@ def test_calls_refuse_what_does_not_fit():
             fn(**good, c=-1.0)
     with pytest.raises(ssm.SsmError):  # an output that is an input
         ssm.ssm_gated_fwd(**{**fwd, "y": d["x"]})
+
+
+@pytest.mark.parametrize("b,D", [(10, 64), (10, 66), (1, 700), (3, 321)])
+def test_some_channels_side_by_side(b, D):
+    say("gated some", b, D)
+    for io in (torch.float32, torch.bfloat16):
+        d = make(b, 1500, D, io, seed=b + D, h0=True, reset=b > 1)
+        check(call(dev(d)), train_ref.gated(**d), io)
