@@ -639,9 +639,10 @@ ssm_status ssm_gated_step(float *h, const void *x_t, const void *r_t, const void
  *   mean   : [2] float32: the mean loss over the tokens that are not ignored, and 1 over
  *            their number (both 0 where every token is ignored)
  * Products are accumulated in float32. Logits of bfloat16 operands are formed from their own
- * bits; a float32 operand is multiplied as a sum of two float16 parts, which hold 22 of its
- * 24 bits and of small values what lies above 2^-39 of the array's largest finite value. The
- * maximum, the sum and the loss are float32.
+ * bits; a float32 operand is multiplied as the sum of three bfloat16 parts, which hold its 24
+ * bits, in six partial products (what they leave out is below 2^-23 of |x||y|). A float32
+ * operand's infinity makes the logits that it enters infinite or NaN. The maximum, the sum and
+ * the loss are float32; lse is given for ignored tokens too.
  * ssm_xent_bwd gives the gradients of sum(dloss loss) + dmean * mean[0]:
  *     dlogit_t[v] = w_t (exp(logit_t[v] - lse_t) - [v == targets[t]]),
  *     w_t = dloss[t] + dmean / count, 0 where ignored,
@@ -649,9 +650,10 @@ ssm_status ssm_gated_step(float *h, const void *x_t, const void *r_t, const void
  *   dloss  : [tokens] float32, NULL = 0;  dmean: one float32 on the device, NULL = 0
  *   dhidden, dweight: either may be NULL (not wanted)
  * The logits are computed again, a piece of the vocabulary at a time, and a piece's dlogits / w
- * are rounded as the operand of the two products: with float32 operands to two float16 parts
- * as above, with bfloat16 ones to bfloat16, or to one float16 part where dloss gives the
- * tokens weights of their own.
+ * enter the two products rounded: with float32 operands to three bfloat16 parts as above, with
+ * bfloat16 ones to bfloat16 (relative 2^-8 of each), or to two such parts (2^-16) where there are
+ * 64 tokens or fewer. Where dloss gives the tokens weights of their own, w hidden enters dweight
+ * as two parts (bfloat16) or three (float32).
  * The workspace (ssm_xent_fwd_workspace / ssm_xent_bwd_workspace bytes, 256-byte aligned)
  * holds one piece at a time. Sums run in a fixed order. Outputs must not overlap inputs or
  * each other. Alignment: targets 8 bytes, float32 arrays 4 bytes, the others one element.

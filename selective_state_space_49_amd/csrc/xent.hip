@@ -12,21 +12,27 @@
 //              G^T (w hidden), both transposed, and dhidden += w G weight, weight transposed.
 // What bounds it is the matrix cores' power: 8192 tokens x 4096 x 32000 in bfloat16 take 1.72 ms
 // forwards and 5.1 ms backwards, 1.25 PFLOP/s, with the cores 64 to 75 % busy and the clock at
-// 1.5 to 1.75 of 2.4 GHz; with few tokens it is the weight's bytes (8 x 4096 x 32000: 0.26 ms for
+// 1.5 to 1.75 of 2.4 GHz; with few tokens it is the weight's bytes (8 x 4096 x 32000: 0.29 ms for
 // 1.05 GB), with little of both the launches (100 x 256 x 1000: 37 us for six).
-// The matrix cores take 16 bits. Logits of bfloat16 operands are products of their own bits. In
-// the gradients' products, a token's weight w stays out of G, whose values lie in [-1, 1]:
-// dhidden takes it as a factor of its row.
-//   bfloat16, every token of one weight (a mean loss): G, hidden and weight are bfloat16, and w
-//   is a factor of dweight. (With w in G, the large values w (p - 1) of all tokens round alike,
-//   and their error was 2.1e-3 where dweight's own rounding is 1.7e-3.)
-//   otherwise: float16 planes, scaled by a power of two that brings the largest of the array to
-//   2^14 .. 2^15, which leaves small values an absolute error of 2^-39 of the largest. dweight
-//   takes w with hidden. One plane each for bfloat16 operands: 11 bits. Two for float32, x =
-//   x1 + x2, the rounded value and the rounded rest, 22 bits, and a product is the sum of x1y1,
-//   x1y2, x2y1 as a longer sum over k; x2y2 is below 2^-22 of x1y1. (Three bfloat16 parts need
-//   six partial products for 24 bits.) float16 products take 3 to 6 % longer than bfloat16 ones
-//   (485 against 457 us for 8192 x 8192 x 4096: the clock falls under their power).
+// The matrix cores take 16 bits, here always bfloat16: its exponents are float32's, so that no value
+// needs a scale, and none is lost beside a larger one. An operand is the sum of one to three
+// parts, x = x1 + x2 + x3, each the rounded rest of the ones before (8, 16, 24 bits), and a
+// product the sum of those partial products x_i y_j that the operands' bits reach, as one longer
+// sum over k, the small ones first. In the gradients' products, a token's weight w stays out of
+// G, whose values lie in [-1, 1]: dhidden takes it as a factor of its row.
+//   float32: three parts of each operand and of G, six partial products; those left out are below
+//   2^-23 of |x||y|. That is 200 TFLOP/s; the float32 matrix instruction's peak is 157. (Two float16
+//   parts, scaled by the array's largest value, need three partial products, but lose what is
+//   small beside that value: an entry of G below 2^-28 its relative precision, a token its
+//   own beside one 10^6 times as large.)
+//   bfloat16: its own bits. G is rounded to bfloat16, and w is a factor of dweight where all tokens
+//   have one (a mean loss): 2.0e-3 of dweight, where its own rounding is 1.7e-3. (With w in G, the
+//   large values w (p - 1) of all tokens round alike, 2.1e-3 by themselves.) Where tokens have
+//   weights of their own, dweight takes them with hidden, as two parts, so that no weight is lost
+//   beside a larger one (8192 x 4096 x 32000: 8.5 ms instead of 6.9).
+//   G has a second part where there are few tokens (kFewTokens): an entry of it then carries a whole
+//   row of a gradient, and its rounding, up to 2^-8, would be the row's (3.5e-3 of dweight for one
+//   token; 1.7e-3 so), and where the weight's bytes, not the products, bound the call.
 #include <math.h>
 
 #include <algorithm>
@@ -39,7 +45,6 @@ namespace ssm {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -47,19 +52,15 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #define SSM_LDS __attribute__((address_space(3)))
 
 constexpr int kBK = 64;        // k per stage
-constexpr int kParts = 2;      // float16 planes of a float32 operand
-enum { kPeakW, kPeakH, kPeakWH, kPeaks };  // peaks of weight, hidden, w hidden
-constexpr int kPeakThreads = 1024, kPeakBlocks = 256;
-constexpr int kPeak = 14;      // a scaled array's largest value is in 2^kPeak .. 2^(kPeak + 1)
+constexpr int kMostParts = 3;  // bfloat16 parts of a float32 operand
 constexpr uint32_t kRsrcWord3 = 0x00027000;  // raw buffer, 32-bit data
 
-// One operand, 16-byte aligned: rows of ld elements (a multiple of 64), planes `plane` elements
+// One operand, 16-byte aligned: rows of ld elements (a multiple of 64), its parts `plane` elements
 // apart. Its rows run along k, all of ld there; or, transposed, row k holds the values of all
 // m (or n), and `rows` of them are there to be read.
 struct Operand {
     const uint16_t *p;
     int64_t ld, plane;
-    const uint32_t *peak;  // float16 planes: the largest value's bits; null: scaled by 2^kPeak
     int64_t rows;
 };
 
@@ -84,12 +85,18 @@ struct Tokens {
 enum class Epi { Lse, Dlogits, Out };
 enum class Factor { None, Same, Row };  // of Out: the tokens' one weight, the weight of token n
 
+// Partial products: which parts of the operands the n of them take, two bits each.
+struct Terms {
+    int32_t n;
+    uint32_t a, b;
+};
+
 struct ProductArgs {
     Operand a, b;
     int64_t M, N;           // of C
     int32_t steps;          // ceil(K / kBK)
-    int32_t terms;          // partial products: 1, or 3 of two planes each
-    int32_t planes;         // Dlogits: float16 planes of G, 0: bfloat16
+    Terms terms;
+    int32_t parts;          // Dlogits: of G
     int32_t tiles_m, tiles_n, splits;
     // Lse, Dlogits: m = vocabulary row - v0, n = token
     Tokens tokens;
@@ -98,7 +105,7 @@ struct ProductArgs {
     uint32_t *done;         // Lse: set to 0 for the launch that joins
     const float *lse;       // Dlogits: [N]
     int64_t v0;
-    uint16_t *g;            // Dlogits: G [rows_g][ldg], planes apart; 0 outside of N x M
+    uint16_t *g;            // Dlogits: G [rows_g][ldg], its parts gplane apart; 0 outside of N x M
     int64_t ldg, rows_g, gplane;
     // Out: C [N][ldc] of float32 or bfloat16 at split * cstride
     void *c;
@@ -109,22 +116,19 @@ struct ProductArgs {
     Factor factor;
 };
 
-// The float16 that holds the most of v, and what is left of it.
-__device__ __forceinline__ uint16_t take_f16(float &v) {
-    const _Float16 h = (_Float16)v;
-    v -= (float)h;
-    return __builtin_bit_cast(uint16_t, h);
-}
-
-// The power of two that brings the value with these bits to 2^kPeak .. 2^(kPeak + 1), as an
-// exponent.
-__device__ __forceinline__ int scale_exp(uint32_t peak) {
-    return peak == 0 ? 0 : min(kPeak + 127 - (int)(peak >> 23), 126);
-}
-__device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-template <bool F16>
-__device__ __forceinline__ float unscale(const Operand &o) {
-    return !F16 ? 1.0f : o.peak ? exp2i(-scale_exp(*o.peak)) : exp2i(-kPeak);
+// The bfloat16 that holds the most of v, and what is left of it. A finite value that would round
+// to infinity is cut off instead; of an infinity or a NaN nothing is left.
+__device__ __forceinline__ uint16_t take_part(float &v) {
+    uint32_t h = f32_to_bf16(v);
+    float rest = v - bf16_to_f32(h);
+    if ((h & 0x7f80u) == 0x7f80u) {
+        const uint32_t u = __float_as_uint(v);
+        const bool finite = (u & 0x7f800000u) != 0x7f800000u;
+        h = finite ? u >> 16 : h;
+        rest = finite ? v - bf16_to_f32(h) : 0.0f;
+    }
+    v = rest;
+    return (uint16_t)h;
 }
 
 // Waves stand WM x WN over a BM x BN tile; each makes TM x TN blocks of 32 x 32 with
@@ -212,11 +216,11 @@ struct Feed {
     }
 };
 
-template <typename S, Epi E, bool F16, int BM, int BN, int WM, int WN>
+template <typename S, Epi E, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::TM][S::TN], SSM_LDS char *lds,
                                          int64_t m0, int64_t n0, int wm, int wn, int split);
 
-template <int BM, int BN, int WM, int WN, int D, Epi E, bool F16, bool TA, bool TB>
+template <int BM, int BN, int WM, int WN, int D, Epi E, bool TA, bool TB>
 __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char *lds, int bid, int split) {
     using S = Shape<BM, BN, WM, WN, D>;
     static_assert((D & (D - 1)) == 0, "a step's buffer is its last bits");
@@ -230,19 +234,18 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
     const int width = 8 * p.tiles_n, group = id / width, gm = min(p.tiles_m - group * 8, 8), in = id % width;
     const int64_t m0 = (int64_t)(group * 8 + in % gm) * BM, n0 = (int64_t)(in / gm) * BN;
 
-    const int total = p.steps * p.terms;
+    const int total = p.steps * p.terms.n;
     const int first = (int)((int64_t)total * split / p.splits), last = (int)((int64_t)total * (split + 1) / p.splits);
 
     typedef Feed<BM, TA, S::kWaves, S::TM> FeedA;
     typedef Feed<BN, TB, S::kWaves, S::TN> FeedB;
     FeedA fa(p.a, m0, p.M, p.steps, lane, wave, wm * S::TM);
     FeedB fb(p.b, n0, p.N, p.steps, lane, wave, wn * S::TN);
-    // Stages are loaded in order: k is the next one's step within its partial product seg,
-    // whose planes of (A, B) are (0,0) (0,1) (1,0).
+    // Stages are loaded in order: k is the next one's step within its partial product seg.
     int seg = first / p.steps, k = first - seg * p.steps;
     auto enter = [&]() {
-        fa.enter(seg == 2 ? p.a.plane : 0, k);
-        fb.enter(seg == 1 ? p.b.plane : 0, k);
+        fa.enter((p.terms.a >> 2 * seg & 3) * p.a.plane, k);
+        fb.enter((p.terms.b >> 2 * seg & 3) * p.b.plane, k);
     };
     auto buffer = [&](int kt) { return lds + (kt & (D - 1)) * S::kStage; };
     auto stage = [&](SSM_LDS char *to) {
@@ -277,12 +280,7 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         for (int i = 0; i < S::TM; ++i)
 #pragma unroll
             for (int j = 0; j < S::TN; ++j)
-                if constexpr (F16)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a[set][i]),
-                                                                       __builtin_bit_cast(f16x8, b[set][j]), acc[i][j], 0,
-                                                                       0, 0);
-                else
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[set][i], b[set][j], acc[i][j], 0, 0, 0);
+                acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[set][i], b[set][j], acc[i][j], 0, 0, 0);
     };
     // All waves' loads into the next stage and reads of this one are done, but for the `newer`
     // youngest loads of each, which may still be on their way: loads complete in order.
@@ -371,38 +369,36 @@ __device__ __forceinline__ void product_tile(const ProductArgs &p, SSM_LDS char 
         multiply(1);
         meet(std::integral_constant<int, 0>{});  // the epilogue may use the LDS
     }
-    epilogue<S, E, F16, BM, BN, WM, WN>(p, acc, lds, m0, n0, wm, wn, split);
+    epilogue<S, E, BM, BN, WM, WN>(p, acc, lds, m0, n0, wm, wn, split);
 }
 
-template <int BM, int BN, int WM, int WN, int D, Epi E, bool F16, bool TA, bool TB>
+template <int BM, int BN, int WM, int WN, int D, Epi E, bool TA, bool TB>
 __global__ void __launch_bounds__(64 * WM * WN, 1) k_product(ProductArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host has no buffer descriptors
     __shared__ __attribute__((aligned(1024))) char lds[Shape<BM, BN, WM, WN, D>::kLds];
-    product_tile<BM, BN, WM, WN, D, E, F16, TA, TB>(p, (SSM_LDS char *)lds, blockIdx.x, blockIdx.y);
+    product_tile<BM, BN, WM, WN, D, E, TA, TB>(p, (SSM_LDS char *)lds, blockIdx.x, blockIdx.y);
 #endif
 }
 
 // Both gradients of a piece by small tiles in one launch: alone, each of them leaves compute units
 // idle in its last round (100 x 256 x 1000: 44 us a training step in two launches, 37 in one).
-template <int D, bool F16>
+template <int D>
 __global__ void __launch_bounds__(256, 1) k_gradients(ProductArgs w, ProductArgs h) {
 #ifdef __HIP_DEVICE_COMPILE__
     __shared__ __attribute__((aligned(1024))) char lds[Shape<128, 128, 2, 2, D>::kLds];
     const int nw = w.tiles_m * w.tiles_n, nh = h.tiles_m * h.tiles_n, id = blockIdx.x, at = id - nw * w.splits;
-    if (at < 0) product_tile<128, 128, 2, 2, D, Epi::Out, F16, true, true>(w, (SSM_LDS char *)lds, id % nw, id / nw);
-    else product_tile<128, 128, 2, 2, D, Epi::Out, F16, true, false>(h, (SSM_LDS char *)lds, at % nh, at / nh);
+    if (at < 0) product_tile<128, 128, 2, 2, D, Epi::Out, true, true>(w, (SSM_LDS char *)lds, id % nw, id / nw);
+    else product_tile<128, 128, 2, 2, D, Epi::Out, true, false>(h, (SSM_LDS char *)lds, at % nh, at / nh);
 #endif
 }
 
 // A block's element e of lane l is row m = 8 (e / 4) + 4 (l / 32) + e % 4, column n = l % 32.
-template <typename S, Epi E, bool F16, int BM, int BN, int WM, int WN>
+template <typename S, Epi E, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::TM][S::TN], SSM_LDS char *lds,
                                          int64_t m0, int64_t n0, int wm, int wn, int split) {
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int64_t mw = m0 + wm * S::TM * 32 + 4 * half;  // the lane's first row
     const int64_t nw = n0 + wn * S::TN * 32 + (lane & 31);
-    const float ua = unscale<F16>(p.a), ub = unscale<F16>(p.b);
-    auto value = [&](float v) { return F16 ? v * ua * ub : v; };
     if constexpr (E == Epi::Lse) {
         if (blockIdx.x == 0 && threadIdx.x == 0) *p.done = 0;
         const int64_t slot = (m0 / BM) * WM + wm;
@@ -414,7 +410,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
             for (int i = 0; i < S::TM; ++i)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float v = acc[i][j][e] = value(acc[i][j][e]);
+                    const float v = acc[i][j][e];
                     if (mw + i * 32 + 8 * (e / 4) + e % 4 < p.M) top = top > v || top != top ? top : v;
                 }
             const float o = __shfl_xor(top, 32);
@@ -441,19 +437,17 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
         }
     }
     if constexpr (E == Epi::Dlogits) {
-        // Through LDS, a token's row of kRow elements, and out in whole rows. The second plane
-        // starts from the product again. The token's weight stays out of G (dhidden takes it as
-        // a factor, dweight with hidden), so that its values lie in [-1, 1] and need no peak of
-        // their own.
-        const float unit = p.planes ? (float)(1 << kPeak) : 1.0f;
-        for (int part = 0; part < max(p.planes, 1); ++part) {
+        // Through LDS, a token's row of kRow elements, and out in whole rows. Each part starts from
+        // the product again. The token's weight stays out of G (dhidden takes it as a factor,
+        // dweight with hidden).
+        auto make = [&](auto part) {
 #pragma unroll
             for (int j = 0; j < S::TN; ++j) {
                 const int64_t n = nw + j * 32;
                 const bool in = n < p.N;
                 const int32_t target = in ? p.tokens.target(n) : -1;
                 const float lse = in ? p.lse[n] : 0.0f;
-                const float scale = target == -2 ? NAN : unit;  // out of range: loud
+                const float scale = target == -2 ? NAN : 1.0f;  // out of range: loud
                 const int t = (int)max((int64_t)-1, min((int64_t)S::TM * 32, target - p.v0 - mw));
                 // an ignored token and the padding are exactly 0, whatever the logit
                 const int rows = target == -1 ? 0 : (int)max((int64_t)0, min((int64_t)S::TM * 32, p.M - mw));
@@ -467,10 +461,11 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
                         uint32_t v16[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float q = e2((value(acc[i][j][e + k]) - lse) * kLog2e) - (t == at + k ? 1.0f : 0.0f);
+                            const float q = e2((acc[i][j][e + k] - lse) * kLog2e) - (t == at + k ? 1.0f : 0.0f);
                             float v = at + k < rows ? q * scale : 0.0f;
-                            if (part > 0) take_f16(v);
-                            v16[k] = p.planes ? take_f16(v) : f32_to_bf16(v);
+#pragma unroll
+                            for (int before = 0; before < part; ++before) v -= bf16_to_f32(f32_to_bf16(v));
+                            v16[k] = f32_to_bf16(v);
                         }
                         *(SSM_LDS u32x2 *)(to + at * 2) = u32x2{v16[0] | v16[1] << 16, v16[2] | v16[3] << 16};
                     }
@@ -483,7 +478,10 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
                     *(u32x4 *)(g + (n0 + n) * p.ldg + m0 + m) = *(const SSM_LDS u32x4 *)(lds + n * (S::kRow * 2) + m * 2);
             }
             __syncthreads();
-        }
+        };
+        make(std::integral_constant<int, 0>{});
+        if (p.parts > 1) make(std::integral_constant<int, 1>{});
+        if (p.parts > 2) make(std::integral_constant<int, 2>{});
     }
     if constexpr (E == Epi::Out) {
         const float same = p.factor == Factor::None ? 1.0f : p.tokens.same();
@@ -506,7 +504,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
 #pragma unroll
                 for (int e = 0; e < 16; e += 4)
                     *(SSM_LDS f32x4 *)(mine + (lane & 31) * kTurn + 4 * half + i * 32 + 2 * e) =
-                        f32x4{value(acc[i][j][e]), value(acc[i][j][e + 1]), value(acc[i][j][e + 2]), value(acc[i][j][e + 3])};
+                        f32x4{acc[i][j][e], acc[i][j][e + 1], acc[i][j][e + 2], acc[i][j][e + 3]};
             __syncthreads();
             if (wide) {
                 constexpr int kLanes = kWide / 4, kRows = 64 / kLanes;
@@ -553,32 +551,29 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
 }
 
 // ---------------------------------------------------------------- operands
-// What a row of an array is: of the vocabulary; a token, where an ignored one may hold anything
-// and does not count for the largest value; in Used it is 0 in the copy too, so that nothing of
-// it reaches a sum; in Weighed the others are multiplied by their tokens' weights.
-enum class Rows { Vocabulary, Tokens, Used, Weighed };
+// What a row of an array is: a token may be ignored, and may then hold anything; in Used it is 0 in
+// the copy, so that nothing of it reaches a sum; in Weighed the others are multiplied by their
+// tokens' weights.
+enum class Rows { All, Used, Weighed };
 
-// An array to be copied; with a peak, its largest value is found first and the copy is scaled. The
-// arrays of a call share a launch: blocks first .. of its grid are this one's.
+// An array to be copied. The arrays of a call share a launch: blocks first .. of its grid are this
+// one's.
 struct Array {
     const void *src;         // [rows][cols]
     int64_t rows, cols;
     Rows kind;
-    uint32_t *peak, *part;   // null: not scaled; part[kPeakBlocks]: the blocks' largest
-    unsigned peak_first, peak_blocks;
-    int across;              // lanes along a row in the search
-    uint16_t *dst;           // [planes][rows_out][ld], planes `plane` apart
+    uint16_t *dst;           // [parts][rows_out][ld], the parts `plane` apart
     int64_t rows_out, ld, plane;
+    int parts;
     unsigned first, blocks;
 };
 struct Arrays {
-    Array a[4];
+    Array a[3];
     int n;
 };
 
-// dst[plane][r][ld] for r < rows_out: src and 0 past its columns and rows. With a peak, its scaled
-// planes; without one, a copy of bfloat16. 16 bytes of a row a thread; the loads may start at any
-// element.
+// dst[part][r][ld] for r < rows_out: the parts of src, and 0 past its columns and rows. 16 bytes of
+// a row a thread; the loads may start at any element.
 template <typename IO>
 __global__ void __launch_bounds__(256) k_pack(Arrays arrays, Tokens tokens) {
     constexpr int N = 16 / sizeof(IO);
@@ -587,21 +582,9 @@ __global__ void __launch_bounds__(256) k_pack(Arrays arrays, Tokens tokens) {
     while (n + 1 < arrays.n && blockIdx.x >= arrays.a[n + 1].first) ++n;
     const Array &a = arrays.a[n];
     const unsigned block = blockIdx.x - a.first;
-    float scale = 1.0f;
-    if (a.peak) {
-        __shared__ uint32_t sh[4];
-        uint32_t top = threadIdx.x < a.peak_blocks ? a.part[threadIdx.x] : 0;
-        static_assert(kPeakBlocks <= 256, "one for each thread");
-        for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-        if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
-        __syncthreads();
-        top = max(max(sh[0], sh[1]), max(sh[2], sh[3]));
-        if (block == 0 && threadIdx.x == 0) *a.peak = top;
-        scale = exp2i(scale_exp(top));
-    }
     const IO *src = (const IO *)a.src;
     const int64_t rows = a.rows, cols = a.cols, across = a.ld / N, total = a.rows_out * across;
-    const bool drop = a.kind == Rows::Used || a.kind == Rows::Weighed, weigh = a.kind == Rows::Weighed;
+    const bool drop = a.kind != Rows::All, weigh = a.kind == Rows::Weighed;
     const float same = weigh ? tokens.same() : 0.0f;
     for (int64_t e = (int64_t)block * 256 + threadIdx.x; e < total; e += (int64_t)a.blocks * 256) {
         const int64_t r = e / across, c = (e - r * across) * N;
@@ -622,7 +605,7 @@ __global__ void __launch_bounds__(256) k_pack(Arrays arrays, Tokens tokens) {
         uint16_t *to = a.dst + r * a.ld + c;
         typedef uint16_t u16xN __attribute__((ext_vector_type(N)));
         if constexpr (sizeof(IO) == 2)
-            if (!a.peak) {
+            if (!weigh) {
                 *(u16xN *)to = from;
                 continue;
             }
@@ -631,84 +614,15 @@ __global__ void __launch_bounds__(256) k_pack(Arrays arrays, Tokens tokens) {
 #pragma unroll
         for (int k = 0; k < N; ++k) {
             const IO x = from[k];
-            v[k] = Io<IO>::ld(&x) * f * scale;
+            v[k] = Io<IO>::ld(&x) * f;
         }
-#pragma unroll
-        for (int q = 0; q < (sizeof(IO) == 4 ? kParts : 1); ++q) {
+        for (int q = 0; q < a.parts; ++q) {
             u16xN h;
 #pragma unroll
-            for (int k = 0; k < N; ++k) h[k] = (uint16_t)take_f16(v[k]);
+            for (int k = 0; k < N; ++k) h[k] = take_part(v[k]);
             *(u16xN *)(to + q * a.plane) = h;
         }
     }
-}
-
-// The largest finite |value| that a thread sees, 16 bytes at a time.
-template <typename IO>
-struct Peak {
-    static constexpr int N = 16 / sizeof(IO);
-    typedef IO iov __attribute__((ext_vector_type(N), aligned(sizeof(IO))));
-    uint32_t top = 0;
-    __device__ __forceinline__ void see(IO e, float f) {
-        const uint32_t b = __float_as_uint(Io<IO>::ld(&e) * f) & 0x7fffffffu;
-        top = b < 0x7f800000u ? max(top, b) : top;
-    }
-    // Of an array whose rows are all alike: as one row.
-    __device__ __forceinline__ void flat(const Array &a) {
-        const IO *src = (const IO *)a.src;
-        const int64_t total = a.rows * a.cols, whole = total / N, step = (int64_t)a.peak_blocks * kPeakThreads;
-        const int64_t at = (int64_t)(blockIdx.x - a.peak_first) * kPeakThreads + threadIdx.x;
-#pragma unroll 4
-        for (int64_t e = at; e < whole; e += step) {
-            const iov v = *(const iov *)(src + e * N);
-#pragma unroll
-            for (int k = 0; k < N; ++k) see(v[k], 1.0f);
-        }
-        if (at < total - whole * N) see(src[whole * N + at], 1.0f);
-    }
-    // Of the rows of tokens.
-    __device__ __forceinline__ void by_rows(const Array &a, const Tokens &tokens) {
-        const IO *src = (const IO *)a.src;
-        const int down = kPeakThreads / a.across;
-        const int64_t c0 = (int64_t)(threadIdx.x % a.across) * N, step = (int64_t)a.peak_blocks * down;
-        const bool weigh = a.kind == Rows::Weighed;
-        const float same = weigh ? tokens.same() : 0.0f;
-        for (int64_t r = (int64_t)(blockIdx.x - a.peak_first) * down + threadIdx.x / a.across; r < a.rows; r += step) {
-            if (tokens.target(r) == -1) continue;
-            const float f = weigh ? tokens.weight(r, same) : 1.0f;
-            for (int64_t c = c0; c < a.cols; c += a.across * N) {
-                const IO *at = src + r * a.cols + c;
-                if (c + N <= a.cols) {
-                    const iov v = *(const iov *)at;
-#pragma unroll
-                    for (int k = 0; k < N; ++k) see(v[k], f);
-                } else {
-                    for (int64_t k = c; k < a.cols; ++k) see(src[r * a.cols + k], f);
-                }
-            }
-        }
-    }
-};
-
-// part[block] = the bits of the largest finite |value|. Of tokens, a block of 1024 has
-// 1024 / across rows at a time. Its few blocks leave so few values that every block that needs the largest of them
-// looks through all: no atomics, and nothing to be cleared first.
-template <typename IO>
-__global__ void __launch_bounds__(kPeakThreads) k_peak(Arrays arrays, Tokens tokens) {
-    __shared__ uint32_t sh[kPeakThreads / 64];
-    int n = 0;
-    while (n + 1 < arrays.n && blockIdx.x >= arrays.a[n + 1].peak_first) ++n;
-    const Array &a = arrays.a[n];
-    Peak<IO> peak;
-    if (a.kind == Rows::Vocabulary) peak.flat(a);
-    else peak.by_rows(a, tokens);
-    uint32_t top = peak.top;
-    for (int o = 32; o > 0; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
-    __syncthreads();
-    if (threadIdx.x) return;
-    for (int k = 1; k < kPeakThreads / 64; ++k) top = max(top, sh[k]);
-    a.part[blockIdx.x - a.peak_first] = top;
 }
 
 // (m, s) += (m2, s2): sums of exponentials under their maxima.
@@ -837,8 +751,8 @@ constexpr int kBig = 256, kSmall = 128;
 // units, in microseconds as measured: a step of k takes 1.72 with a large tile and 1.14 with two
 // small ones, which share a compute unit (8192 x 8192 x 4096: 1250 against 950 TFLOP/s) but waste
 // less at the edges and in the last round, or 0.9 with one alone; each round has its start and its
-// end; the partial products of a split go through memory and a launch that joins them (1000 x 1000 x 48000 in float16: 140 us in 8 parts
-// of small tiles, 112 in 16 of large ones). A part has 2 steps at least.
+// end; the partial sums of a split go through memory and a launch that joins them (1000 x 1000 x
+// 48000: 140 us in 8 parts of small tiles, 112 in 16 of large ones). A part has 2 steps at least.
 struct Tiling {
     int tile, splits;
 };
@@ -864,14 +778,14 @@ Tiling tiling(int64_t M, int64_t N, int64_t steps, bool may_split) {
     return best;
 }
 
-template <Epi E, bool F16, bool TA = false, bool TB = false>
+template <Epi E, bool TA = false, bool TB = false>
 hipError_t product(ProductArgs p, int tile, hipStream_t s) {
     p.tiles_m = (int32_t)blocks(p.M, tile);
     p.tiles_n = (int32_t)blocks(p.N, tile);
     const dim3 grid((unsigned)(p.tiles_m * p.tiles_n), (unsigned)p.splits);
-    if (tile == kBig) k_product<256, 256, 2, 4, 2, E, F16, TA, TB><<<grid, 512, 0, s>>>(p);
-    else if ((int64_t)grid.x * grid.y <= kCus) k_product<128, 128, 2, 2, 4, E, F16, TA, TB><<<grid, 256, 0, s>>>(p);
-    else k_product<128, 128, 2, 2, 2, E, F16, TA, TB><<<grid, 256, 0, s>>>(p);
+    if (tile == kBig) k_product<256, 256, 2, 4, 2, E, TA, TB><<<grid, 512, 0, s>>>(p);
+    else if ((int64_t)grid.x * grid.y <= kCus) k_product<128, 128, 2, 2, 4, E, TA, TB><<<grid, 256, 0, s>>>(p);
+    else k_product<128, 128, 2, 2, 2, E, TA, TB><<<grid, 256, 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -887,22 +801,43 @@ struct Arena {
     }
 };
 
+// The partial products of operands of `a` and `b` parts: x_i y_j is left out where it is no larger
+// than what the operands' own bits leave out. Small ones first.
+Terms terms_of(int a, int b) {
+    Terms t{};
+    for (int sum = std::max(a, b) - 1; sum >= 0; --sum)
+        for (int i = 0; i <= sum; ++i)
+            if (i < a && sum - i < b) {
+                t.a |= (uint32_t)i << 2 * t.n;
+                t.b |= (uint32_t)(sum - i) << 2 * t.n;
+                ++t.n;
+            }
+    return t;
+}
+
+// G in two parts up to here in bfloat16: one step of k for each part of dweight's sum. With more tokens
+// the roundings of G's entries, each up to 2^-8, average out (2.0e-3 to 2.2e-3 of dweight from 100
+// tokens on, where its own rounding is 1.7e-3), and a second part would double the products (256 x
+// 4096 x 32000: 513 us instead of 426).
+constexpr int64_t kFewTokens = 64;
+
 // What a call lays out in its workspace.
 struct Layout {
-    int planes, terms;           // of an operand, of a product
+    int parts, parts_w, parts_g;  // of hidden and weight, of w hidden, of G
+    Terms logits, to_w, to_h;    // of the products
     int64_t ldk, rows_t, piece;  // padded dim and tokens; vocabulary rows of a piece
     Tiling lse, out_w, out_h;
     bool pack;                   // weight is copied: float32, or rows not in steps of 64
     uint16_t *hidden, *weight;   // copies for the logits
-    uint16_t *hidden_w, *piece_w, *g;  // for the gradients: hidden, a piece of weight, G
-    uint32_t *peak, *peak_part, *done;
+    uint16_t *hidden_w, *g;      // for the gradients: (w) hidden, G
+    uint32_t *done;
     Losses *losses;
     float *at, *sum, *split_w, *split_h;
     float2 *part;
     size_t bytes;
 };
 
-// G of a piece holds about 2^27 values, 256 MB in bfloat16: 8192 tokens take pieces of 16384 rows.
+// G of a piece holds about 2^27 numbers of 16 bits, 256 MB: 8192 tokens take pieces of 16384 rows.
 // dhidden's partial sum is read and written once for each piece, so that more of them cost more
 // (2^26, 2^27 and 2^28 values: 7.32, 7.27 and 7.22 ms for 8192 x 4096 x 32000, 8.34, 8.05 and
 // 8.05 ms for 2000 x 4096 x 128000), and larger ones would begin to be the whole array.
@@ -912,34 +847,36 @@ constexpr int64_t kPieceValues = (int64_t)1 << 27;
 // many tokens, many threads for each where there are few.
 int join_tokens(int64_t T) { return T >= 4096 ? 32 : T >= 256 ? 16 : 2; }
 
-Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, char *ws) {
+// weighed: the tokens have weights of their own.
+Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, bool weighed, char *ws) {
     Layout l{};
     Arena a{ws};
-    l.planes = io ? 1 : kParts;
-    l.terms = io ? 1 : 3;
+    l.parts = io ? 1 : kMostParts;
+    l.logits = terms_of(l.parts, l.parts);
     l.ldk = up(K, kBK);
     l.rows_t = up(T, kBK);
     l.pack = !io || K % kBK != 0 || !aligned;
     // sized as if the operands had to be copied: their alignment is not known to the query
-    l.hidden = a.take<uint16_t>(T * l.ldk * l.planes);
-    l.weight = a.take<uint16_t>(V * l.ldk * l.planes);
-    l.peak = a.take<uint32_t>(kPeaks);
-    l.peak_part = a.take<uint32_t>(kPeaks * kPeakBlocks);
+    l.hidden = a.take<uint16_t>(T * l.ldk * l.parts);
+    l.weight = a.take<uint16_t>(V * l.ldk * l.parts);
     if (!bwd) {
-        l.lse = tiling(V, T, l.ldk / kBK * l.terms, false);
+        l.lse = tiling(V, T, l.ldk / kBK * l.logits.n, false);
         l.part = a.take<float2>((int64_t)blocks(V, l.lse.tile) * 2 * T);
         l.at = a.take<float>(T);
         l.losses = a.take<Losses>(blocks(T, join_tokens(T)));
         l.done = a.take<uint32_t>(1);
     } else {
-        l.piece = std::min(up(V, kBig), std::max<int64_t>(1024, kPieceValues / l.rows_t / kBig * kBig));
+        l.parts_w = io ? (weighed ? 2 : 1) : kMostParts;
+        l.parts_g = io ? (T <= kFewTokens ? 2 : 1) : kMostParts;
+        l.to_w = terms_of(l.parts_w, l.parts_g);
+        l.to_h = terms_of(l.parts, l.parts_g);
+        l.piece = std::min(up(V, kBig), std::max<int64_t>(1024, kPieceValues / l.parts_g / l.rows_t / kBig * kBig));
         const int64_t most = std::min(V, l.piece);
-        l.out_w = tiling(K, most, l.rows_t / kBK * l.terms, true);
-        l.out_h = tiling(K, T, up(most, kBK) / kBK * l.terms, true);
+        l.out_w = tiling(K, most, l.rows_t / kBK * l.to_w.n, true);
+        l.out_h = tiling(K, T, up(most, kBK) / kBK * l.to_h.n, true);
         l.sum = a.take<float>(V > l.piece ? T * K : 0);
-        l.hidden_w = a.take<uint16_t>(l.rows_t * l.ldk * l.planes);
-        l.piece_w = a.take<uint16_t>(io ? most * l.ldk : 0);
-        l.g = a.take<uint16_t>(l.rows_t * up(most, kBK) * l.planes);
+        l.hidden_w = a.take<uint16_t>(l.rows_t * l.ldk * l.parts_w);
+        l.g = a.take<uint16_t>(l.rows_t * up(most, kBK) * l.parts_g);
         l.split_w = a.take<float>(l.out_w.splits > 1 ? l.out_w.splits * most * K : 0);
         l.split_h = a.take<float>(l.out_h.splits > 1 ? l.out_h.splits * T * K : 0);
     }
@@ -954,10 +891,9 @@ template <typename IO>
 struct Copies {
     Arrays list{};
     static constexpr int kWide = 16 / sizeof(IO);  // elements of a load
-    unsigned peak_grid = 0, grid = 0;
-    // src [rows][cols] to dst [planes][rows_out][ld]; peak: of l.peak, or -1 for a plain copy.
-    // Returns the copy as an operand.
-    Operand add(const Layout &l, const void *src, int64_t rows, int64_t cols, uint16_t *dst, int64_t rows_out, int peak,
+    unsigned grid = 0;
+    // src [rows][cols] to dst [parts][rows_out][ld]. Returns the copy as an operand.
+    Operand add(const Layout &l, const void *src, int64_t rows, int64_t cols, uint16_t *dst, int64_t rows_out, int parts,
                 Rows kind) {
         Array &a = list.a[list.n++];
         a.src = src;
@@ -968,26 +904,13 @@ struct Copies {
         a.rows_out = rows_out;
         a.ld = l.ldk;
         a.plane = rows_out * l.ldk;
+        a.parts = parts;
         a.first = grid;
-        // a scaled one looks through the largest values first: more rows for a block
-        a.blocks = (unsigned)std::min<int64_t>((rows_out * l.ldk / kWide + 255) / 256, peak < 0 ? kMostBlocks : 4096);
+        a.blocks = (unsigned)std::min<int64_t>((rows_out * l.ldk / kWide + 255) / 256, kMostBlocks);
         grid += a.blocks;
-        a.peak_first = peak_grid;
-        if (peak >= 0) {
-            const int64_t lanes = blocks(cols, kWide);
-            a.peak = l.peak + peak;
-            a.part = l.peak_part + peak * kPeakBlocks;
-            a.across = 16;
-            while (a.across < lanes && a.across < kPeakThreads) a.across *= 2;
-            const int64_t most = kind == Rows::Vocabulary ? (rows * cols / kWide + kPeakThreads) / kPeakThreads
-                                                          : blocks(rows, kPeakThreads / a.across);
-            a.peak_blocks = (unsigned)std::min<int64_t>(most, kPeakBlocks);
-            peak_grid += a.peak_blocks;
-        }
-        return {dst, l.ldk, a.plane, a.peak, rows_out};
+        return {dst, l.ldk, a.plane, rows_out};
     }
     hipError_t launch(const Tokens &tokens, hipStream_t s) {
-        if (peak_grid) k_peak<IO><<<dim3(peak_grid), kPeakThreads, 0, s>>>(list, tokens);
         if (grid) k_pack<IO><<<dim3(grid), 256, 0, s>>>(list, tokens);
         return hipGetLastError();
     }
@@ -1005,19 +928,18 @@ bool rows_aligned(const XentArgs &a) { return ((uintptr_t)a.hidden | (uintptr_t)
 // there already.
 template <typename IO>
 ProductArgs logits_product(const XentArgs &a, const Layout &l, const Tokens &tokens, const Operand *made, Copies<IO> &copies) {
-    constexpr bool planes = sizeof(IO) == 4;
     ProductArgs p{};
     p.tokens = tokens;
     if (l.pack) {
-        p.a = copies.add(l, a.weight, a.V, a.K, l.weight, a.V, planes ? kPeakW : -1, Rows::Vocabulary);
-        p.b = made ? *made : copies.add(l, a.hidden, a.T, a.K, l.hidden, a.T, planes ? kPeakH : -1, Rows::Tokens);
+        p.a = copies.add(l, a.weight, a.V, a.K, l.weight, a.V, l.parts, Rows::All);
+        p.b = made ? *made : copies.add(l, a.hidden, a.T, a.K, l.hidden, a.T, l.parts, Rows::All);
     } else {
-        p.a = {(const uint16_t *)a.weight, l.ldk, 0, nullptr, a.V};
-        p.b = made ? *made : Operand{(const uint16_t *)a.hidden, l.ldk, 0, nullptr, a.T};
+        p.a = {(const uint16_t *)a.weight, l.ldk, 0, a.V};
+        p.b = made ? *made : Operand{(const uint16_t *)a.hidden, l.ldk, 0, a.T};
     }
     p.N = a.T;
     p.steps = (int32_t)(l.ldk / kBK);
-    p.terms = l.terms;
+    p.terms = l.logits;
     p.splits = 1;
     return p;
 }
@@ -1028,7 +950,7 @@ hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
         k_zero<<<dim3(1), 256, 0, s>>>(a.mean, (int64_t)2);
         return hipGetLastError();
     }
-    const Layout l = lay_out(a.T, a.K, a.V, io, false, rows_aligned(a), (char *)a.ws);
+    const Layout l = lay_out(a.T, a.K, a.V, io, false, rows_aligned(a), false, (char *)a.ws);
     const Tokens tokens{a.targets, a.ignore, a.V, nullptr, nullptr, nullptr};
     Copies<IO> copies;
     ProductArgs p = logits_product<IO>(a, l, tokens, nullptr, copies);
@@ -1037,7 +959,7 @@ hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
     p.part = l.part;
     p.at = l.at;
     p.done = l.done;
-    SSM_TRY((product<Epi::Lse, sizeof(IO) == 4>(p, l.lse.tile, s)));
+    SSM_TRY(product<Epi::Lse>(p, l.lse.tile, s));
     const int64_t n = (int64_t)blocks(a.V, l.lse.tile) * 2;
     const int most = join_tokens(a.T);
     auto join = most == 32 ? k_xent_join<32> : most == 16 ? k_xent_join<16> : k_xent_join<2>;
@@ -1062,16 +984,15 @@ ProductArgs gradient(ProductArgs p, Tiling t, float *split, void *dst, bool bf16
 }
 
 // dweight's product w and dhidden's h, where they are wanted.
-template <bool F16>
 hipError_t gradients(const ProductArgs *w, int tile_w, const ProductArgs *h, int tile_h, hipStream_t s) {
     if (w && h && tile_w == kSmall && tile_h == kSmall) {
         const int64_t n = (int64_t)w->tiles_m * w->tiles_n * w->splits + (int64_t)h->tiles_m * h->tiles_n * h->splits;
-        if (n <= kCus) k_gradients<4, F16><<<dim3((unsigned)n), 256, 0, s>>>(*w, *h);
-        else k_gradients<2, F16><<<dim3((unsigned)n), 256, 0, s>>>(*w, *h);
+        if (n <= kCus) k_gradients<4><<<dim3((unsigned)n), 256, 0, s>>>(*w, *h);
+        else k_gradients<2><<<dim3((unsigned)n), 256, 0, s>>>(*w, *h);
         return hipGetLastError();
     }
-    if (w) SSM_TRY((product<Epi::Out, F16, true, true>(*w, tile_w, s)));
-    if (h) SSM_TRY((product<Epi::Out, F16, true, false>(*h, tile_h, s)));
+    if (w) SSM_TRY((product<Epi::Out, true, true>(*w, tile_w, s)));
+    if (h) SSM_TRY((product<Epi::Out, true, false>(*h, tile_h, s)));
     return hipSuccess;
 }
 
@@ -1081,25 +1002,17 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
         if (a.dweight) k_zero<IO><<<dim3((unsigned)std::min((a.V * a.K + 255) / 256, kMostBlocks)), 256, 0, s>>>((IO *)a.dweight, a.V * a.K);
         return hipGetLastError();
     }
-    const Layout l = lay_out(a.T, a.K, a.V, io, true, rows_aligned(a), (char *)a.ws);
+    const bool weighed = a.dloss != nullptr;  // else one weight for all tokens: a factor at the end
+    const Layout l = lay_out(a.T, a.K, a.V, io, true, rows_aligned(a), weighed, (char *)a.ws);
     const Tokens tokens{a.targets, a.ignore, a.V, a.dloss, a.dmean, a.mean};
-    // one weight for all tokens: it is a factor at the end, and bfloat16 serves for the rest
-    const bool f16 = sizeof(IO) == 4 || a.dloss;
     Copies<IO> copies;
-    Operand hidden_w{}, piece_w{};
+    Operand hidden_w{};
     if (a.dweight)
-        hidden_w = copies.add(l, a.hidden, a.T, a.K, l.hidden_w, l.rows_t, f16 ? kPeakWH : -1, f16 ? Rows::Weighed : Rows::Used);
-    ProductArgs logits = logits_product<IO>(a, l, tokens, a.dweight && !f16 ? &hidden_w : nullptr, copies);
-    // where the logits' operand is bfloat16 and the gradient's float16: a plane of a piece
-    const auto copy_piece = [&](int64_t v0, Copies<IO> &c) {
-        const int64_t nv = std::min(l.piece, a.V - v0);
-        piece_w = c.add(l, (const IO *)a.weight + v0 * a.K, nv, a.K, l.piece_w, nv, kPeakW, Rows::Vocabulary);
-    };
-    const bool pieces = a.dhidden && f16 && sizeof(IO) == 2;
-    if (pieces) copy_piece(0, copies);
+        hidden_w = copies.add(l, a.hidden, a.T, a.K, l.hidden_w, l.rows_t, l.parts_w, weighed ? Rows::Weighed : Rows::Used);
+    ProductArgs logits = logits_product<IO>(a, l, tokens, a.dweight && !weighed ? &hidden_w : nullptr, copies);
     SSM_TRY(copies.launch(tokens, s));
     logits.lse = a.lse;
-    logits.planes = f16 ? l.planes : 0;
+    logits.parts = l.parts_g;
     logits.g = l.g;
     logits.rows_g = l.rows_t;
     for (int64_t v0 = 0; v0 < a.V; v0 += l.piece) {
@@ -1111,8 +1024,8 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
         p.v0 = v0;
         p.ldg = ldg;
         p.gplane = l.rows_t * ldg;
-        SSM_TRY((product<Epi::Dlogits, sizeof(IO) == 4>(p, tiling(nv, a.T, p.steps * l.terms, false).tile, s)));
-        const Operand g{l.g, ldg, p.gplane, nullptr, l.rows_t};
+        SSM_TRY(product<Epi::Dlogits>(p, tiling(nv, a.T, p.steps * p.terms.n, false).tile, s));
+        const Operand g{l.g, ldg, p.gplane, l.rows_t};
         JoinPair join{};
         ProductArgs to_w{}, to_h{};
         if (a.dweight) {
@@ -1123,31 +1036,25 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
             q.M = a.K;
             q.N = nv;
             q.steps = (int32_t)(l.rows_t / kBK);
-            q.terms = l.terms;
-            q.factor = f16 ? Factor::None : Factor::Same;
+            q.terms = l.to_w;
+            q.factor = weighed ? Factor::None : Factor::Same;
             to_w = gradient(q, l.out_w, l.split_w, (IO *)a.dweight + v0 * a.K, io, nullptr, false, &join.j[0]);
         }
         if (a.dhidden) {
             ProductArgs q{};
             q.tokens = tokens;
-            if (pieces && v0 > 0) {
-                Copies<IO> next;
-                copy_piece(v0, next);
-                SSM_TRY(next.launch(tokens, s));
-            }
-            q.a = pieces ? piece_w : p.a;
+            q.a = p.a;
             q.b = g;
             q.factor = Factor::Row;
             q.M = a.K;
             q.N = a.T;
             q.steps = (int32_t)(ldg / kBK);
-            q.terms = l.terms;
+            q.terms = l.to_h;
             const bool end = v0 + nv == a.V;
             to_h = gradient(q, l.out_h, l.split_h, end ? a.dhidden : l.sum, end && io, l.sum, v0 > 0, &join.j[1]);
         }
         const ProductArgs *const pw = a.dweight ? &to_w : nullptr, *const ph = a.dhidden ? &to_h : nullptr;
-        SSM_TRY(f16 ? gradients<true>(pw, l.out_w.tile, ph, l.out_h.tile, s)
-                    : gradients<false>(pw, l.out_w.tile, ph, l.out_h.tile, s));
+        SSM_TRY(gradients(pw, l.out_w.tile, ph, l.out_h.tile, s));
         const int64_t most = std::max(join.j[0].count, join.j[1].count);
         if (most > 0) k_join_splits<<<dim3(blocks(most, 256), 2), 256, 0, s>>>(join);
     }
@@ -1157,10 +1064,12 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
 }  // namespace
 
 size_t xent_fwd_ws(int64_t T, int64_t K, int64_t V, int io) {
-    return T > 0 ? lay_out(T, K, V, io, false, false, nullptr).bytes : 0;
+    return T > 0 ? lay_out(T, K, V, io, false, false, false, nullptr).bytes : 0;
 }
+// For any call of these sizes: the tilings, and with them the splits, go by the partial products.
 size_t xent_bwd_ws(int64_t T, int64_t K, int64_t V, int io) {
-    return T > 0 ? lay_out(T, K, V, io, true, false, nullptr).bytes : 0;
+    return T > 0 ? std::max(lay_out(T, K, V, io, true, false, false, nullptr).bytes,
+                            lay_out(T, K, V, io, true, false, true, nullptr).bytes) : 0;
 }
 hipError_t launch_xent_fwd(const XentArgs &a, int io, hipStream_t s) {
     return io ? xent_fwd<bf16_bits>(a, io, s) : xent_fwd<float>(a, io, s);
