@@ -63,7 +63,8 @@ __device__ __forceinline__ Gate gate(float r, float i, float ck) {
 // registers. A wave reduces its steps to the pair (P, H): the state leaving them is
 // P h_in + H, P = prod a. The waves' pairs meet in LDS, the tiles' pairs in global memory:
 // a tile publishes its pair, takes the state that enters it from its predecessors' words,
-// publishes the state that leaves it, and only then walks its steps with the true state. So each
+// publishes the state that leaves it, and only then walks its steps with the true state. (What
+// leaves a tile with a reset does not depend on what enters: it is published at once.) So each
 // input is read once, where summary and rescan passes read it twice. What bounds it is the
 // bytes: 8 a step and channel in bfloat16 forwards, 14 backwards. 262144 steps of 4096 channels
 // take 1.61 ms (8.6 GB at 5.3 TB/s, where a large copy moves 4.9), and 2 x 4096 steps of 8192
@@ -77,19 +78,18 @@ __device__ __forceinline__ Gate gate(float r, float i, float ck) {
 constexpr uint64_t kValid = 1ull << 63, kFinal = 1ull << 62;
 
 __device__ __forceinline__ uint64_t pack_word(float P, float H, uint64_t flags) {
-    // a NaN decay has made H a NaN too, and P's bits must stay clear of the flags
+    // a NaN decay has made H a NaN too (a tile with a reset has no P), and P's bits must stay clear
+    // of the flags
     const uint32_t p = P == P ? __float_as_uint(P) : 0u;
     return flags | (uint64_t)p << 32 | __float_as_uint(H);
 }
 __device__ __forceinline__ float word_H(uint64_t w) { return __uint_as_float((uint32_t)w); }
 __device__ __forceinline__ float word_P(uint64_t w) { return __uint_as_float((uint32_t)(w >> 32) & 0x3fffffffu); }
 
-// c after steps with the pair (P, H). With resets a P of 0 cuts: nothing of c passes, a NaN
-// neither.
-template <bool RESET>
-__device__ __forceinline__ float through(float P, float H, float c) {
-    return RESET && P == 0.0f ? H : fmaf(P, c, H);
-}
+// c after steps with the pair (P, H). Where a reset is among the steps nothing of c passes, a NaN
+// neither. That is a mark of its own, the same for all channels: a P of 0 is not one, since products
+// underflow (and 0 c is NaN where c is), and a P that is NaN may have a reset behind it.
+__device__ __forceinline__ float through(bool cut, float P, float H, float c) { return cut ? H : fmaf(P, c, H); }
 
 // The state that enters a tile of the walk, for a lane's CPL channels; word j is the j-th tile
 // at words + j stride, and `carry` comes in as the state before the first. Reads the words
@@ -101,7 +101,7 @@ __device__ __forceinline__ float through(float P, float H, float c) {
 // take 1.96, 1.64, 1.60, 1.61, 1.77 and 2.39 ms with a kAhead of 1, 2, 3, 4, 8 and 12. Where
 // few channels run side by side (far, below), the walk itself is what takes time, a round trip
 // for every kAhead tiles.
-template <bool RESET, int CPL, int kAhead>
+template <int CPL, int kAhead>
 __device__ __forceinline__ void look_back(const uint64_t *words, int64_t stride, int64_t tile, bool in,
                                           float (&carry)[CPL]) {
     for (;;) {
@@ -123,8 +123,8 @@ __device__ __forceinline__ void look_back(const uint64_t *words, int64_t stride,
 #pragma unroll
             for (int q = kAhead - 1; q >= 0; --q) {
                 const float P = word_P(w[q][c]), H = word_H(w[q][c]);
-                const bool valid = w[q][c] & kValid, last = (w[q][c] & kFinal) || (RESET && P == 0.0f);
-                state[c] = last ? H : through<RESET>(P, H, state[c]);
+                const bool valid = w[q][c] & kValid, last = w[q][c] & kFinal;
+                state[c] = last ? H : fmaf(P, state[c], H);
                 have = valid && (last || have);
             }
             all = all && have;
@@ -203,7 +203,7 @@ template <typename IO, int CPL, bool RESET, int FAR>
 __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint32_t *ticket, uint64_t *words) {
     constexpr int R = kFwdRows, CW = 64 * CPL;
     __shared__ float sP[kWaves][CW], sH[kWaves][CW], sC[CW];
-    __shared__ int sid;
+    __shared__ int sid, sCut[kWaves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cols = (int)((p.D + CW - 1) / CW);
     const Place at = take_tile(p, ticket, cols, &sid);
@@ -258,34 +258,40 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint3
         sP[wave][lane * CPL + c] = P[c];
         sH[wave][lane * CPL + c] = H[c];
     }
+    if (RESET && lane == 0) sCut[wave] = cut != 0;
     __syncthreads();
+    const auto cuts = [&](int w) { return RESET && sCut[w]; };
     // the first wave: the tile's pair, the state that enters the tile, the state that leaves
     if (wave == 0) {
         float tP[CPL], tH[CPL], carry[CPL];
         uint64_t *mine = words ? words + (at.b * n_tiles + at.j) * p.D + d : nullptr;
+        bool tcut = cuts(0);
+        for (int w = 1; w < kWaves; ++w) tcut = tcut || cuts(w);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
             tP[c] = P[c];
             tH[c] = H[c];
             carry[c] = p.h0 ? p.h0[at.b * p.D + dc + c] : 0.0f;
             for (int w = 1; w < kWaves; ++w) {
-                tH[c] = through<RESET>(sP[w][lane * CPL + c], sH[w][lane * CPL + c], tH[c]);
+                tH[c] = through(cuts(w), sP[w][lane * CPL + c], sH[w][lane * CPL + c], tH[c]);
                 tP[c] *= sP[w][lane * CPL + c];
             }
-            if (in && at.j > 0 && at.j + 1 < n_tiles)
-                __hip_atomic_store(mine + c, pack_word(tP[c], tH[c], kValid), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (in && (at.j > 0 || tcut) && at.j + 1 < n_tiles)
+                __hip_atomic_store(mine + c, tcut ? pack_word(0.0f, tH[c], kValid | kFinal) : pack_word(tP[c], tH[c], kValid),
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (at.j > 0) look_back<RESET, CPL, FAR ? FAR : 3>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
+        if (at.j > 0) look_back<CPL, FAR ? FAR : 3>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
-            const float out = through<RESET>(tP[c], tH[c], carry[c]);
+            const float out = through(tcut, tP[c], tH[c], carry[c]);
             sC[lane * CPL + c] = carry[c];
             if (!in) continue;
-            if (at.j + 1 < n_tiles)
+            if (at.j + 1 == n_tiles) {
+                if (p.h_final) p.h_final[at.b * p.D + d + c] = out;
+            } else if (!tcut) {
                 __hip_atomic_store(mine + c, pack_word(0.0f, out, kValid | kFinal), __ATOMIC_RELAXED,
                                    __HIP_MEMORY_SCOPE_AGENT);
-            else if (p.h_final)
-                p.h_final[at.b * p.D + d + c] = out;
+            }
         }
     }
     __syncthreads();
@@ -294,7 +300,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint3
 #pragma unroll
     for (int c = 0; c < CPL; ++c) {
         h[c] = sC[lane * CPL + c];
-        for (int w = 0; w < wave; ++w) h[c] = through<RESET>(sP[w][lane * CPL + c], sH[w][lane * CPL + c], h[c]);
+        for (int w = 0; w < wave; ++w) h[c] = through(cuts(w), sP[w][lane * CPL + c], sH[w][lane * CPL + c], h[c]);
     }
     if (!in) return;
     if (p.states && t0 % SSM_GATED_STATE_EVERY == 0)
@@ -322,7 +328,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
                                                               float *sums) {
     constexpr int R = kBwdRows, CW = 64 * CPL;
     __shared__ float sP[kWaves][CW], sH[kWaves][CW], sU[kWaves][CW], sC[CW];
-    __shared__ int sid;
+    __shared__ int sid, sCut[kWaves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cols = (int)((p.D + CW - 1) / CW);
     const Place at = take_tile(p, ticket, cols, &sid);
@@ -378,7 +384,7 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
                 if (!there) continue;
                 const float b = g.beta * g.si * xv[c];
                 H[c] = z ? b : fmaf(g.a, H[c], b);
-                P[c] = z ? 0.0f : P[c] * g.a;
+                P[c] *= g.a;
             }
         }
 #pragma unroll
@@ -396,33 +402,39 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
         sH[wave][lane * CPL + c] = H[c];
         sU[wave][lane * CPL + c] = U[c];
     }
+    if (RESET && lane == 0) sCut[wave] = cut != 0;
     __syncthreads();
+    const auto cuts = [&](int w) { return RESET && sCut[w]; };
     if (wave == 0) {
         float tP[CPL], tU[CPL], carry[CPL];
         uint64_t *mine = words ? words + (at.b * n_tiles + at.j) * p.D + d : nullptr;
+        bool tcut = false;
+        for (int w = 0; w < kWaves; ++w) tcut = tcut || cuts(w);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
             tP[c] = 1.0f;
             tU[c] = 0.0f;
             carry[c] = p.dh_final ? p.dh_final[at.b * p.D + dc + c] : 0.0f;
             for (int w = kWaves - 1; w >= 0; --w) {
-                tU[c] = through<RESET>(sP[w][lane * CPL + c], sU[w][lane * CPL + c], tU[c]);
+                tU[c] = through(cuts(w), sP[w][lane * CPL + c], sU[w][lane * CPL + c], tU[c]);
                 tP[c] *= sP[w][lane * CPL + c];
             }
-            if (in && at.j > 0 && at.j + 1 < n_tiles)
-                __hip_atomic_store(mine + c, pack_word(tP[c], tU[c], kValid), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (in && (at.j > 0 || tcut) && at.j + 1 < n_tiles)
+                __hip_atomic_store(mine + c, tcut ? pack_word(0.0f, tU[c], kValid | kFinal) : pack_word(tP[c], tU[c], kValid),
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
-        if (at.j > 0) look_back<RESET, CPL, FAR ? FAR : 2>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
+        if (at.j > 0) look_back<CPL, FAR ? FAR : 2>(words + at.b * n_tiles * p.D + dc, p.D, at.j, in, carry);
 #pragma unroll
         for (int c = 0; c < CPL; ++c) {
-            const float out = through<RESET>(tP[c], tU[c], carry[c]);
+            const float out = through(tcut, tP[c], tU[c], carry[c]);
             sC[lane * CPL + c] = carry[c];
             if (!in) continue;
-            if (at.j + 1 < n_tiles)
+            if (at.j + 1 == n_tiles) {
+                if (p.dh0) p.dh0[at.b * p.D + d + c] = out;
+            } else if (!tcut) {
                 __hip_atomic_store(mine + c, pack_word(0.0f, out, kValid | kFinal), __ATOMIC_RELAXED,
                                    __HIP_MEMORY_SCOPE_AGENT);
-            else if (p.dh0)
-                p.dh0[at.b * p.D + d + c] = out;
+            }
         }
     }
     __syncthreads();
@@ -431,8 +443,8 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
     for (int c = 0; c < CPL; ++c) {
         u[c] = sC[lane * CPL + c];
         sum[c] = 0.0f;
-        for (int w = kWaves - 1; w > wave; --w) u[c] = through<RESET>(sP[w][lane * CPL + c], sU[w][lane * CPL + c], u[c]);
-        for (int w = 0; w < wave; ++w) h[c] = through<RESET>(sP[w][lane * CPL + c], sH[w][lane * CPL + c], h[c]);
+        for (int w = kWaves - 1; w > wave; --w) u[c] = through(cuts(w), sP[w][lane * CPL + c], sU[w][lane * CPL + c], u[c]);
+        for (int w = 0; w < wave; ++w) h[c] = through(cuts(w), sP[w][lane * CPL + c], sH[w][lane * CPL + c], h[c]);
     }
     by_rows<R>(rows, [&](auto full) {
         float before[R][CPL];
