@@ -81,13 +81,15 @@ def _entry(name: str) -> int:
     return at
 
 
-def _scratch(workspace, need: int, device):
+def _scratch(workspace, need, device):
     """The caller's workspace or a new one (which must live until the call is enqueued), its
     address and its bytes."""
     if workspace is None:
         if not need:
             return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():  # its address goes to the kernels
+        raise ValueError(f"workspace must be a contiguous tensor on {device}, got one on {workspace.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
