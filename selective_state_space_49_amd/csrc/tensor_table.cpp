@@ -8,13 +8,15 @@
 //
 // The entry points of the library come as addresses, from the binding that has loaded it. A call
 // returns what it has made; the status where the library refuses; None where an argument is not
-// as it should be.
+// as it should be. The tensors' GPU is the current one during the call: a default stream is
+// that of the current GPU, whichever tensor it was asked for.
 #include "ssm_scan.h"
 
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -149,6 +151,7 @@ PyObject *gated_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
             Py_DECREF(out);
             Py_RETURN_NONE;
         }
+        const c10::DeviceGuard on(x.device());
         ssm_status st;
         Py_BEGIN_ALLOW_THREADS
         st = entry(h, xp, r, i, decay, (float)c, y, all[0], all[1], all[2], io == at::kFloat ? SSM_F32 : SSM_BF16, stream);
@@ -187,6 +190,7 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
             gs = (const float *)address(args[9], at::kFloat, THPVariable_Unpack(args[9]).sizes(), t.device, &ok);
         }
         if (!ok) Py_RETURN_NONE;
+        const c10::OptionalDeviceGuard on(t.device < 0 ? c10::optional<c10::Device>() : c10::Device(c10::kCUDA, (c10::DeviceIndex)t.device));
         ssm_status st;
         Py_BEGIN_ALLOW_THREADS
         st = entry((int32_t)t.params.size(), t.params.data(), t.grads.data(), t.sizes.data(), t.kinds.data(),
@@ -270,6 +274,7 @@ PyObject *gated_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         if (!k.ok) Py_RETURN_NONE;
         const size_t bytes = size(b, L, D);
         const at::Tensor ws = bytes ? k.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        const c10::DeviceGuard on(k.first.device());
         ssm_status st;
         Py_BEGIN_ALLOW_THREADS
         st = entry(x, r, i, decay, h0, reset, c, at_of(y), (float *)at_of(h), (float *)at_of(states), b, L, D, k.kind(),
@@ -306,6 +311,7 @@ PyObject *gated_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const at::Tensor dh0 = args[12] == Py_True ? k.fresh(at::kFloat, ends) : at::Tensor();
         const size_t bytes = size(b, L, D);
         const at::Tensor ws = bytes ? k.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        const c10::DeviceGuard on(k.first.device());
         ssm_status st;
         Py_BEGIN_ALLOW_THREADS
         st = entry(x, r, i, decay, states, reset, c, dy, dh, at_of(dx), at_of(dr), at_of(di), (float *)at_of(dd),
@@ -336,6 +342,7 @@ PyObject *xent_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         if (!k.ok) Py_RETURN_NONE;
         const size_t bytes = size(T, K, V, k.kind());
         const at::Tensor ws = bytes ? k.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        const c10::DeviceGuard on(k.first.device());
         ssm_status st;
         Py_BEGIN_ALLOW_THREADS
         st = entry(hidden, weight, targets, ignore, (float *)at_of(loss), (float *)at_of(lse), (float *)at_of(mean), T, K, V,
@@ -373,6 +380,7 @@ PyObject *xent_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         const at::Tensor dw = args[12] == Py_True ? k.fresh(k.io, head) : at::Tensor();
         const size_t bytes = size(T, K, V, k.kind());
         const at::Tensor ws = bytes ? k.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        const c10::DeviceGuard on(k.first.device());
         ssm_status st;
         Py_BEGIN_ALLOW_THREADS
         st = entry(hidden, weight, targets, ignore, lse, mean, dloss, dmean, at_of(dh), at_of(dw), T, K, V, k.kind(),

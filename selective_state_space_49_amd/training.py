@@ -28,12 +28,13 @@ _IO = {_f32: SSM_F32, torch.bfloat16: SSM_BF16}
 # way: through the _tensor_table extension, which takes a call whose arguments are right and whose
 # workspace is not the caller's. What it does not take goes on here, argument by argument: one
 # comparison where it is right, and _dev's checks only to say what is wrong with it.
-def _need(t: Optional[torch.Tensor], name: str, shape, dtype):
-    """The address of a contiguous GPU tensor of this shape and dtype, or None."""
+def _need(t: Optional[torch.Tensor], name: str, shape, dtype, device):
+    """The address of a contiguous tensor of this shape and dtype on this GPU, or None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.device != device:
         _dev(t, name, shape, dtype)
+        raise ValueError(f"{name} must be on {device}, like the call's first tensor, not on {t.device}")
     return t.data_ptr()
 
 
@@ -45,8 +46,15 @@ def _kind(t: torch.Tensor) -> int:
 
 
 def _stream(t: torch.Tensor) -> int:
-    """torch's current stream on the tensor's GPU, as a hipStream_t."""
+    """torch's current stream on the tensor's GPU, as a hipStream_t. A default stream is that of the
+    current GPU, so the tensor's has to be current during the call (_called, or the extension)."""
     return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _called(t: torch.Tensor, entry, *args):
+    """One of the library's entry points on the tensor's GPU and torch's current stream there."""
+    with torch.cuda.device(t.device):
+        _check(entry(*args, _stream(t)))
 
 
 _table_loaded = None
@@ -110,10 +118,10 @@ def _states_rows(L: int) -> int:
     return -(-L // GATED_STATE_EVERY)
 
 
-def _reset(reset: Optional[torch.Tensor], shape):
+def _reset(reset: Optional[torch.Tensor], shape, device):
     if reset is not None and reset.dtype not in (torch.bool, torch.uint8):
         raise TypeError(f"reset: expected bool or uint8, got {reset.dtype}")
-    return None if reset is None else _need(reset, "reset", shape, reset.dtype)
+    return None if reset is None else _need(reset, "reset", shape, reset.dtype, device)
 
 
 def ssm_gated_fwd(x, r, i, decay, h0=None, reset=None, *, c=8.0, y=None, h_final=None, states=None,
@@ -131,7 +139,7 @@ def _gated_fwd(x, r, i, decay, h0, reset, c, y, h_final, states, workspace, want
         if got is not None:
             return _made(got)
     lib = load_library()
-    shape, io, kind = x.shape, x.dtype, _kind(x)
+    shape, io, kind, dev = x.shape, x.dtype, _kind(x), x.device
     b, L, D = shape
     if y is None:
         y = torch.empty_like(x)
@@ -140,12 +148,10 @@ def _gated_fwd(x, r, i, decay, h0, reset, c, y, h_final, states, workspace, want
     if states is None and save:
         states = torch.empty((b, _states_rows(L), D), dtype=_f32, device=x.device)
     ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_gated_fwd_workspace(b, L, D), x.device)
-    _check(lib.ssm_gated_fwd(_need(x, "x", shape, io), _need(r, "r", shape, io), _need(i, "i", shape, io),
-                             _need(decay, "decay", (D,), _f32), _need(h0, "h0", (b, D), _f32),
-                             _reset(reset, (b, L)), c, _need(y, "y", shape, io),
-                             _need(h_final, "h_final", (b, D), _f32),
-                             _need(states, "states", (b, _states_rows(L), D), _f32), b, L, D, kind, ws_at,
-                             ws_bytes, _stream(x)))
+    _called(x, lib.ssm_gated_fwd, _need(x, "x", shape, io, dev), _need(r, "r", shape, io, dev), _need(i, "i", shape, io, dev),
+            _need(decay, "decay", (D,), _f32, dev), _need(h0, "h0", (b, D), _f32, dev), _reset(reset, (b, L), dev), c,
+            _need(y, "y", shape, io, dev), _need(h_final, "h_final", (b, D), _f32, dev),
+            _need(states, "states", (b, _states_rows(L), D), _f32, dev), b, L, D, kind, ws_at, ws_bytes)
     return y, h_final, states
 
 
@@ -166,18 +172,17 @@ def ssm_gated_bwd(x, r, i, decay, states, reset=None, *, dy, dh_final=None, c=8.
         if got is not None:
             return dict(zip(("dx", "dr", "di", "ddecay", "dh0"), _made(got)))
     lib = load_library()
-    shape, io, kind = x.shape, x.dtype, _kind(x)
+    shape, io, kind, dev = x.shape, x.dtype, _kind(x), x.device
     b, L, D = shape
     dx, dr, di = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
     ddecay = torch.empty_like(decay)
     dh0 = torch.empty((b, D), dtype=_f32, device=x.device) if want_dh0 else None
     ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_gated_bwd_workspace(b, L, D), x.device)
-    _check(lib.ssm_gated_bwd(_need(x, "x", shape, io), _need(r, "r", shape, io), _need(i, "i", shape, io),
-                             _need(decay, "decay", (D,), _f32),
-                             _need(states, "states", (b, _states_rows(L), D), _f32), _reset(reset, (b, L)), c,
-                             _need(dy, "dy", shape, io), _need(dh_final, "dh_final", (b, D), _f32),
-                             dx.data_ptr(), dr.data_ptr(), di.data_ptr(), ddecay.data_ptr(),
-                             None if dh0 is None else dh0.data_ptr(), b, L, D, kind, ws_at, ws_bytes, _stream(x)))
+    _called(x, lib.ssm_gated_bwd, _need(x, "x", shape, io, dev), _need(r, "r", shape, io, dev), _need(i, "i", shape, io, dev),
+            _need(decay, "decay", (D,), _f32, dev), _need(states, "states", (b, _states_rows(L), D), _f32, dev),
+            _reset(reset, (b, L), dev), c, _need(dy, "dy", shape, io, dev), _need(dh_final, "dh_final", (b, D), _f32, dev),
+            dx.data_ptr(), dr.data_ptr(), di.data_ptr(), ddecay.data_ptr(), None if dh0 is None else dh0.data_ptr(),
+            b, L, D, kind, ws_at, ws_bytes)
     return {"dx": dx, "dr": dr, "di": di, "ddecay": ddecay, "dh0": dh0}
 
 
@@ -191,8 +196,8 @@ def ssm_gated_step(h, x_t, r_t, i_t, decay, *, c=8.0, y_t=None):
         _kind(x_t)
         for t, name, of, dtype in ((h, "h", shape, _f32), (x_t, "x_t", shape, io), (r_t, "r_t", shape, io),
                                    (i_t, "i_t", shape, io), (decay, "decay", (Ln, D), _f32), (y_t, "y_t", shape, io)):
-            _need(t, name, of, dtype)
-        raise ValueError("h, r_t, i_t, decay and y_t must be on x_t's GPU")
+            _need(t, name, of, dtype, x_t.device)
+        raise ValueError("h, x_t, r_t, i_t and decay must be given")
     return _made(got)
 
 
@@ -236,15 +241,16 @@ def ssm_xent_bwd_workspace(tokens, dim, vocab, io=SSM_BF16) -> int:
 def _head(hidden, weight, targets):
     """The sizes, the io type, and the addresses of a head's inputs."""
     (T, K), V, io = hidden.shape, weight.shape[0], hidden.dtype
-    return T, K, V, _kind(hidden), (_need(hidden, "hidden", (T, K), io), _need(weight, "weight", (V, K), io),
-                                    _need(targets, "targets", (T,), torch.int64))
+    dev = hidden.device
+    return T, K, V, _kind(hidden), (_need(hidden, "hidden", (T, K), io, dev), _need(weight, "weight", (V, K), io, dev),
+                                    _need(targets, "targets", (T,), torch.int64, dev))
 
 
-def _one(t: Optional[torch.Tensor], name: str):
+def _one(t: Optional[torch.Tensor], name: str, device):
     """The address of one float32 value on the GPU, or None."""
     if t is not None and t.numel() != 1:
         raise ValueError(f"{name} must hold one value")
-    return None if t is None else _need(t, name, t.shape, _f32)
+    return None if t is None else _need(t, name, t.shape, _f32, device)
 
 
 def ssm_xent_fwd(hidden, weight, targets, *, ignore_index=-100, loss=None, lse=None, mean=None,
@@ -264,8 +270,8 @@ def ssm_xent_fwd(hidden, weight, targets, *, ignore_index=-100, loss=None, lse=N
     lse = torch.empty(T, dtype=_f32, device=dev) if lse is None else lse
     mean = torch.empty(2, dtype=_f32, device=dev) if mean is None else mean
     ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_xent_fwd_workspace(T, K, V, kind), dev)
-    _check(lib.ssm_xent_fwd(*inputs, ignore_index, _need(loss, "loss", (T,), _f32), _need(lse, "lse", (T,), _f32),
-                            _need(mean, "mean", (2,), _f32), T, K, V, kind, ws_at, ws_bytes, _stream(hidden)))
+    _called(hidden, lib.ssm_xent_fwd, *inputs, ignore_index, _need(loss, "loss", (T,), _f32, dev),
+            _need(lse, "lse", (T,), _f32, dev), _need(mean, "mean", (2,), _f32, dev), T, K, V, kind, ws_at, ws_bytes)
     return loss, lse, mean
 
 
@@ -281,14 +287,14 @@ def ssm_xent_bwd(hidden, weight, targets, lse, mean, *, dloss=None, dmean=None, 
             return _made(got)
     lib = load_library()
     T, K, V, kind, inputs = _head(hidden, weight, targets)
+    dev = hidden.device
     dhidden = torch.empty_like(hidden) if want_dhidden else None
     dweight = torch.empty_like(weight) if want_dweight else None
-    ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_xent_bwd_workspace(T, K, V, kind), hidden.device)
-    _check(lib.ssm_xent_bwd(*inputs, ignore_index, _need(lse, "lse", (T,), _f32), _need(mean, "mean", (2,), _f32),
-                            _need(dloss, "dloss", (T,), _f32), _one(dmean, "dmean"),
-                            None if dhidden is None else dhidden.data_ptr(),
-                            None if dweight is None else dweight.data_ptr(), T, K, V, kind, ws_at, ws_bytes,
-                            _stream(hidden)))
+    ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_xent_bwd_workspace(T, K, V, kind), dev)
+    _called(hidden, lib.ssm_xent_bwd, *inputs, ignore_index, _need(lse, "lse", (T,), _f32, dev),
+            _need(mean, "mean", (2,), _f32, dev), _need(dloss, "dloss", (T,), _f32, dev), _one(dmean, "dmean", dev),
+            None if dhidden is None else dhidden.data_ptr(), None if dweight is None else dweight.data_ptr(),
+            T, K, V, kind, ws_at, ws_bytes)
     return dhidden, dweight
 
 
@@ -349,9 +355,9 @@ def ssm_adamw_step(params, grads, exp_avg, exp_avg_sq, avg_scale=None, avg_sq_sc
                                   (exp_avg_sq, "exp_avg_sq", total, torch.uint8 if codes else _f32),
                                   (avg_scale, "avg_scale", total // ADAMW_BLOCK, _f32),
                                   (avg_sq_scale, "avg_sq_scale", total // ADAMW_BLOCK, _f32)):
-            _need(t, name, (n,), dtype)
-        _one(grad_scale, "grad_scale")
-        raise ValueError("the moments, their scales and grad_scale must be given and on the parameters' GPU")
+            _need(t, name, (n,), dtype, params[0].device)
+        _one(grad_scale, "grad_scale", params[0].device)
+        raise ValueError("the moments must be given, and avg_scale and avg_sq_scale together or not at all")
     _check(status)
 
 
@@ -360,10 +366,10 @@ def ssm_adamw_values(exp_avg, exp_avg_sq, avg_scale, avg_sq_scale):
     n = exp_avg.numel()
     scales = (n // ADAMW_BLOCK,)
     m, v = (torch.empty(n, dtype=_f32, device=exp_avg.device) for _ in range(2))
-    _check(load_library().ssm_adamw_values(
-        _need(exp_avg, "exp_avg", (n,), torch.int8), _need(exp_avg_sq, "exp_avg_sq", (n,), torch.uint8),
-        _need(avg_scale, "avg_scale", scales, _f32), _need(avg_sq_scale, "avg_sq_scale", scales, _f32),
-        m.data_ptr(), v.data_ptr(), n, _stream(exp_avg)))
+    dev = exp_avg.device
+    _called(exp_avg, load_library().ssm_adamw_values, _need(exp_avg, "exp_avg", (n,), torch.int8, dev),
+            _need(exp_avg_sq, "exp_avg_sq", (n,), torch.uint8, dev), _need(avg_scale, "avg_scale", scales, _f32, dev),
+            _need(avg_sq_scale, "avg_sq_scale", scales, _f32, dev), m.data_ptr(), v.data_ptr(), n)
     return m, v
 
 
