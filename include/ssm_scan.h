@@ -705,7 +705,9 @@ ssm_status ssm_xent_bwd(const void *hidden, const void *weight, const int64_t *t
  * The step takes one launch for every SSM_ADAMW_TENSORS tensors, needs no workspace and
  * copies the tables by value, so the host arrays may be reused at once.
  * Alignment: params and grads one element; exp_avg, exp_avg_sq 16 bytes; scales 4 bytes.
- * params, grads and the state must not overlap. */
+ * What is written (parameters that have a gradient, the state) must not overlap anything else that
+ * is given, so no parameter may be listed twice; gradients may overlap each other
+ * (SSM_ERR_UNSUPPORTED). */
 #define SSM_ADAMW_BLOCK 256
 #define SSM_ADAMW_TENSORS 96
 int64_t ssm_adamw_state_size(int32_t n_tensors, const int64_t *sizes);

@@ -5,8 +5,12 @@
 #include <hip/hip_runtime.h>
 
 #include <math.h>
+#include <stdio.h>
 
+#include <algorithm>
 #include <initializer_list>
+#include <new>
+#include <vector>
 
 #include "ssm_scan.h"
 #include "ssm_status.h"
@@ -81,6 +85,66 @@ ssm_status check_xent(const void *hidden, const void *weight, const int64_t *tar
     const size_t eb = io_bytes(io);
     if (!aligned(hidden, eb) || !aligned(weight, eb) || !aligned(targets, 8))
         return fail(SSM_ERR_ALIGN, "pointer alignment (targets 8 B, hidden and weight element)");
+    return SSM_OK;
+}
+
+// What a step over many tensors writes, by address, to find what must not meet it.
+struct Written {
+    struct Piece {
+        uintptr_t at, end;
+        int32_t k;  // the tensor; < 0: of the state
+    };
+    std::vector<Piece> pieces;
+
+    void add(const void *p, size_t bytes, int32_t k) {
+        if (p && bytes) pieces.push_back({(uintptr_t)p, (uintptr_t)p + bytes, k});
+    }
+    // In the order of addresses, which tensors allocated one after another mostly have already. Two
+    // pieces that meet, as neighbours; null: none do.
+    const Piece *sort() {
+        const auto before = [](const Piece &a, const Piece &b) { return a.at < b.at; };
+        if (!std::is_sorted(pieces.begin(), pieces.end(), before)) std::sort(pieces.begin(), pieces.end(), before);
+        for (size_t j = 1; j < pieces.size(); ++j)
+            if (pieces[j].at < pieces[j - 1].end) return &pieces[j - 1];
+        return nullptr;
+    }
+    // The piece that meets [p, p + bytes), after sort() has found none that meet each other.
+    const Piece *meets(const void *p, size_t bytes) const {
+        if (!p || !bytes) return nullptr;
+        const auto it = std::lower_bound(pieces.begin(), pieces.end(), (uintptr_t)p,
+                                         [](const Piece &a, uintptr_t at) { return a.end <= at; });
+        return it != pieces.end() && it->at < (uintptr_t)p + bytes ? &*it : nullptr;
+    }
+};
+
+// The step reads and writes its tensors in no order: none of what it writes may be written or read
+// under another name, so a tensor given twice is refused.
+ssm_status check_adamw_apart(int32_t n, void *const *params, const void *const *grads, const int64_t *sizes,
+                             const int32_t *param_io, const int32_t *grad_io, const void *m, const void *v,
+                             const float *ms, const float *vs, const float *grad_scale, int64_t total) {
+    static const char *const state[] = {"exp_avg", "exp_avg_sq", "avg_scale", "avg_sq_scale"};
+    const size_t moment = (size_t)total * (ms ? 1 : 4), scale = (size_t)(total / SSM_ADAMW_BLOCK) * 4;
+    Written w;
+    w.pieces.reserve((size_t)n + 4);
+    for (int32_t k = 0; k < n; ++k)
+        if (grads[k]) w.add(params[k], (size_t)sizes[k] * io_bytes(param_io[k]), k);
+    w.add(m, moment, -1);
+    w.add(v, moment, -2);
+    w.add(ms, scale, -3);
+    w.add(vs, scale, -4);
+    const auto name = [&](const Written::Piece &p, char *to) {
+        if (p.k < 0) snprintf(to, 32, "%s", state[-1 - p.k]);
+        else snprintf(to, 32, "parameter %d", p.k);
+        return to;
+    };
+    char a[32], b[32];
+    if (const Written::Piece *p = w.sort())
+        return fail(SSM_ERR_UNSUPPORTED, "%s must not overlap %s", name(p[0], a), name(p[1], b));
+    for (int32_t k = 0; k < n; ++k)
+        if (const Written::Piece *p = w.meets(grads[k], (size_t)sizes[k] * io_bytes(grad_io[k])))
+            return fail(SSM_ERR_UNSUPPORTED, "gradient %d must not overlap %s", k, name(*p, a));
+    if (const Written::Piece *p = w.meets(grad_scale, 4))
+        return fail(SSM_ERR_UNSUPPORTED, "grad_scale must not overlap %s", name(*p, a));
     return SSM_OK;
 }
 
@@ -267,14 +331,19 @@ ssm_status ssm_adamw_step(int32_t n_tensors, void *const *params, const void *co
         if (!params[k]) return fail(SSM_ERR_NULL, "tensor %d has a gradient and no parameter", k);
         if (!aligned(params[k], io_bytes(param_io[k])) || !aligned(grads[k], io_bytes(grad_io[k])))
             return fail(SSM_ERR_ALIGN, "tensor %d is not aligned to its element", k);
-        if (overlaps(params[k], (size_t)sizes[k] * io_bytes(param_io[k]), grads[k], (size_t)sizes[k] * io_bytes(grad_io[k])))
-            return fail(SSM_ERR_UNSUPPORTED, "tensor %d: the parameter must not overlap its gradient", k);
     }
     if (!any) return ok();
     if (!exp_avg || !exp_avg_sq) return fail(SSM_ERR_NULL, "exp_avg and exp_avg_sq are required");
     if (!aligned(exp_avg, 16) || !aligned(exp_avg_sq, 16) || !aligned(avg_scale, 4) || !aligned(avg_sq_scale, 4) ||
         !aligned(grad_scale, 4))
         return fail(SSM_ERR_ALIGN, "pointer alignment (exp_avg, exp_avg_sq 16 B; scales 4 B)");
+    try {
+        const ssm_status st = check_adamw_apart(n_tensors, params, grads, sizes, param_io, grad_io, exp_avg, exp_avg_sq, avg_scale,
+                                                avg_sq_scale, grad_scale, ssm_adamw_state_size(n_tensors, sizes));
+        if (st != SSM_OK) return st;
+    } catch (const std::bad_alloc &) {
+        return fail(SSM_ERR_WORKSPACE, "no host memory for the table of %d tensors", n_tensors);
+    }
     ssm::AdamwArgs a{};
     a.m = exp_avg; a.v = exp_avg_sq; a.m_scale = avg_scale; a.v_scale = avg_sq_scale; a.grad_scale = grad_scale;
     a.beta1 = (float)beta1; a.omb1 = (float)(1.0 - beta1);
