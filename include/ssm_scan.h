@@ -657,8 +657,9 @@ ssm_status ssm_gated_step(float *h, const void *x_t, const void *r_t, const void
  * The workspace (ssm_xent_fwd_workspace / ssm_xent_bwd_workspace bytes, 256-byte aligned)
  * holds one piece at a time. Sums run in a fixed order. Outputs must not overlap inputs or
  * each other. Alignment: targets 8 bytes, float32 arrays 4 bytes, the others one element.
- * tokens and vocab are at most 2^30, dim at most 2^22; tokens == 0 gives mean = 0 and
- * dweight = 0. */
+ * tokens is below 2^29, vocab at most 2^30, dim at most 2^22, and a product's tiles are those of
+ * one launch (for the forward 2^23 of 256 x 256, 5.5e11 logits): SSM_ERR_SHAPE otherwise.
+ * tokens == 0 gives mean = 0 and dweight = 0. */
 size_t ssm_xent_fwd_workspace(int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io);
 size_t ssm_xent_bwd_workspace(int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io);
 ssm_status ssm_xent_fwd(const void *hidden, const void *weight, const int64_t *targets,

@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(256) k_adamw(AdamwArgs a) {
 
 // Four codes of each moment a lane; bound by the bytes: 236 M parameters, 2.4 GB, take 0.39 ms.
 __global__ void __launch_bounds__(256) k_adamw_values(const int8_t *m, const uint8_t *v, const float *ms,
-                                                      const float *vs, float *mo, float *vo, int64_t n) {
-    const int64_t e = (int64_t)blockIdx.x * 1024 + threadIdx.x * 4;
+                                                      const float *vs, float *mo, float *vo, int64_t from, int64_t n) {
+    const int64_t e = from + (int64_t)blockIdx.x * 1024 + threadIdx.x * 4;
     if (e >= n) return;
     *(f32x4 *)(mo + e) = m_values(*(const i8x4 *)(m + e), ms[e / kBlock]);
     *(f32x4 *)(vo + e) = v_values(*(const u8x4 *)(v + e), vs[e / kBlock]);
@@ -295,8 +295,14 @@ hipError_t launch_adamw(const AdamwArgs &a, int32_t blocks, hipStream_t s) {
 
 hipError_t launch_adamw_values(const int8_t *m, const uint8_t *v, const float *ms, const float *vs, float *mo,
                                float *vo, int64_t n, hipStream_t s) {
-    k_adamw_values<<<dim3((unsigned)((n + 1023) / 1024)), 256, 0, s>>>(m, v, ms, vs, mo, vo, n);
-    return hipGetLastError();
+    const int64_t most = (int64_t)1 << 33;  // a launch's work-items are fewer than 2^32
+    for (int64_t from = 0; from < n; from += most) {
+        const int64_t to = from + most < n ? from + most : n;
+        k_adamw_values<<<dim3((unsigned)((to - from + 1023) / 1024)), 256, 0, s>>>(m, v, ms, vs, mo, vo, from, to);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace ssm

@@ -69,18 +69,18 @@ ssm_status check_gated(int64_t batch, int64_t L, int64_t D, ssm_dtype io, float 
     return SSM_OK;
 }
 
-bool xent_shape_ok(int64_t T, int64_t K, int64_t V) {
+bool xent_shape_ok(int64_t T, int64_t K, int64_t V, int io, bool bwd) {
     const int64_t most = (int64_t)1 << 30;
     return T >= 0 && T <= most && K >= 1 && K <= ((int64_t)1 << 22) && V >= 1 && V <= most &&
-           // rows of a tile by 32-bit offsets, tiles of 128 x 128 and blocks of a fill within the grid
+           // rows of a tile by 32-bit offsets, tiles of 128 x 128 by 32-bit numbers
            (double)(T / 128 + 1) * (double)(V / 128 + 1) <= 2147483647.0 &&
-           (double)(K / 128 + 1) * (double)((T > V ? T : V) / 128 + 1) <= 2147483647.0 && (double)V * K <= 2.7e11;
+           (double)(K / 128 + 1) * (double)((T > V ? T : V) / 128 + 1) <= 2147483647.0 && (double)V * K <= 2.7e11 && ssm::xent_fits(T, K, V, io == SSM_BF16, bwd);
 }
 
 ssm_status check_xent(const void *hidden, const void *weight, const int64_t *targets, int64_t T, int64_t K,
-                      int64_t V, ssm_dtype io) {
+                      int64_t V, ssm_dtype io, bool bwd) {
     if (!valid_io(io)) return fail(SSM_ERR_DTYPE, "io dtype %d unknown", (int)io);
-    if (!xent_shape_ok(T, K, V)) return fail(SSM_ERR_SHAPE, "tokens must be in 0..2^30, dim in 1..2^22, vocab in 1..2^30, and their products within the grid");
+    if (!xent_shape_ok(T, K, V, io, bwd)) return fail(SSM_ERR_SHAPE, "tokens must be in 0..2^29 - 1, dim in 1..2^22, vocab in 1..2^30, and their products within a launch");
     if (T > 0 && (!hidden || !weight || !targets)) return fail(SSM_ERR_NULL, "hidden, weight and targets are required");
     const size_t eb = io_bytes(io);
     if (!aligned(hidden, eb) || !aligned(weight, eb) || !aligned(targets, 8))
@@ -242,16 +242,16 @@ ssm_status ssm_gated_step(float *h, const void *x_t, const void *r_t, const void
 
 // ---------------------------------------------------------------- vocabulary cross entropy
 size_t ssm_xent_fwd_workspace(int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io) {
-    return valid_io(io) && xent_shape_ok(tokens, dim, vocab) ? ssm::xent_fwd_ws(tokens, dim, vocab, io == SSM_BF16) : 0;
+    return valid_io(io) && xent_shape_ok(tokens, dim, vocab, io, false) ? ssm::xent_fwd_ws(tokens, dim, vocab, io == SSM_BF16) : 0;
 }
 size_t ssm_xent_bwd_workspace(int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io) {
-    return valid_io(io) && xent_shape_ok(tokens, dim, vocab) ? ssm::xent_bwd_ws(tokens, dim, vocab, io == SSM_BF16) : 0;
+    return valid_io(io) && xent_shape_ok(tokens, dim, vocab, io, true) ? ssm::xent_bwd_ws(tokens, dim, vocab, io == SSM_BF16) : 0;
 }
 
 ssm_status ssm_xent_fwd(const void *hidden, const void *weight, const int64_t *targets, int64_t ignore_index,
                         float *loss, float *lse, float *mean, int64_t tokens, int64_t dim, int64_t vocab,
                         ssm_dtype io, void *workspace, size_t workspace_bytes, void *hip_stream) {
-    ssm_status st = check_xent(hidden, weight, targets, tokens, dim, vocab, io);
+    ssm_status st = check_xent(hidden, weight, targets, tokens, dim, vocab, io, false);
     if (st != SSM_OK) return st;
     if (!mean || (tokens > 0 && (!loss || !lse))) return fail(SSM_ERR_NULL, "loss, lse and mean are required");
     if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(mean, 4))
@@ -274,7 +274,7 @@ ssm_status ssm_xent_bwd(const void *hidden, const void *weight, const int64_t *t
                         const float *lse, const float *mean, const float *dloss, const float *dmean, void *dhidden,
                         void *dweight, int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io, void *workspace,
                         size_t workspace_bytes, void *hip_stream) {
-    ssm_status st = check_xent(hidden, weight, targets, tokens, dim, vocab, io);
+    ssm_status st = check_xent(hidden, weight, targets, tokens, dim, vocab, io, true);
     if (st != SSM_OK) return st;
     if (tokens > 0 && (!lse || (dmean && !mean))) return fail(SSM_ERR_NULL, "lse is required, and mean with dmean");
     const size_t eb = io_bytes(io), tb = (size_t)tokens * 4;
@@ -360,7 +360,7 @@ ssm_status ssm_adamw_step(int32_t n_tensors, void *const *params, const void *co
             const int64_t most = (int64_t)1 << 34;
             const int64_t n = sizes[k] - from < most ? sizes[k] - from : most;
             const int64_t nb = ssm::adamw_blocks(n, codes);
-            if (a.n_tensors == SSM_ADAMW_TENSORS || (a.n_tensors > 0 && blocks + nb > 0x7fffffff)) {
+            if (a.n_tensors == SSM_ADAMW_TENSORS || (a.n_tensors > 0 && blocks + nb > ssm::kAdamwMostBlocks)) {
                 const ssm_status st = launch_status(ssm::launch_adamw(a, (int32_t)blocks, (hipStream_t)hip_stream), "AdamW launch");
                 if (st != SSM_OK) return st;
                 a.n_tensors = 0;

@@ -166,12 +166,13 @@ __device__ __forceinline__ void by_rows(int rows, F fn) {
     else if (rows > 0) fn(std::false_type{});
 }
 
-// Where a block works: the j-th tile of the walk of batch row b, channels from d0.
+// Where a block works: the j-th tile of the walk of batch row b, channels from d0. `first`: the blocks
+// of the call's launches before this one (the counter goes on from launch to launch by itself).
 struct Place {
     int64_t j, b, d0;
 };
-__device__ __forceinline__ Place take_tile(const GatedArgs &p, uint32_t *ticket, int cols, int *sh) {
-    uint32_t id = blockIdx.x;
+__device__ __forceinline__ Place take_tile(const GatedArgs &p, uint32_t *ticket, uint32_t first, int cols, int *sh) {
+    uint32_t id = first + blockIdx.x;
     if (ticket) {
         if (threadIdx.x == 0) *sh = (int)__hip_atomic_fetch_add(ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         __syncthreads();
@@ -200,13 +201,14 @@ size_t words_bytes(int64_t batch, int64_t L, int64_t D, int tile) {
 // lane are in flight before the first gate, and the 2 x 32 floats of (a, b) still leave room
 // for four waves a SIMD.
 template <typename IO, int CPL, bool RESET, int FAR>
-__global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint32_t *ticket, uint64_t *words) {
+__global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint32_t first, uint32_t *ticket,
+                                                              uint64_t *words) {
     constexpr int R = kFwdRows, CW = 64 * CPL;
     __shared__ float sP[kWaves][CW], sH[kWaves][CW], sC[CW];
     __shared__ int sid, sCut[kWaves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cols = (int)((p.D + CW - 1) / CW);
-    const Place at = take_tile(p, ticket, cols, &sid);
+    const Place at = take_tile(p, ticket, first, cols, &sid);
     const int64_t d = at.d0 * CW + lane * CPL, n_tiles = tiles_of(p.L, kFwdTile);
     const int64_t dc = min(d, p.D - CPL);  // lanes past the last channel work on it and store nothing
     const bool in = d < p.D;
@@ -324,14 +326,14 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_fwd(GatedArgs p, uint3
 // u_{t+1}. The states come from the stored row that enters the tile, through the waves'
 // forward pairs.
 template <typename IO, int CPL, bool RESET, int FAR>
-__global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint32_t *ticket, uint64_t *words,
-                                                              float *sums) {
+__global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint32_t first, uint32_t *ticket,
+                                                              uint64_t *words, float *sums) {
     constexpr int R = kBwdRows, CW = 64 * CPL;
     __shared__ float sP[kWaves][CW], sH[kWaves][CW], sU[kWaves][CW], sC[CW];
     __shared__ int sid, sCut[kWaves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int cols = (int)((p.D + CW - 1) / CW);
-    const Place at = take_tile(p, ticket, cols, &sid);
+    const Place at = take_tile(p, ticket, first, cols, &sid);
     const int64_t d = at.d0 * CW + lane * CPL, n_tiles = tiles_of(p.L, kBwdTile);
     const int64_t dc = min(d, p.D - CPL), tile = n_tiles - 1 - at.j;
     const bool in = d < p.D;
@@ -503,12 +505,12 @@ __global__ void __launch_bounds__(64 * kWaves, 4) k_gated_bwd(GatedArgs p, uint3
 }
 
 // ddecay[d] = sigmoid(decay) / softplus(decay) * sum over the n tiles' sums: 16 threads for a
-// channel, in double, so that the order of thousands of them costs nothing.
+// channel, in double, so that the order of thousands of them costs nothing. Channels from d0.
 __global__ void __launch_bounds__(1024) k_gated_ddecay(const float *sums, const float *decay, float *out, int64_t n,
-                                                       int64_t D) {
+                                                       int64_t D, int64_t d0) {
     __shared__ double sh[16][64];
     const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-    const int64_t d = (int64_t)blockIdx.x * 64 + x;
+    const int64_t d = d0 + (int64_t)blockIdx.x * 64 + x;
     double s = 0.0;
     if (d < D)
         for (int64_t j = y; j < n; j += 16) s += (double)sums[j * D + d];
@@ -521,8 +523,7 @@ __global__ void __launch_bounds__(1024) k_gated_ddecay(const float *sums, const 
 }
 
 __global__ void __launch_bounds__(256) k_clear(uint4 *p, int64_t n) {
-    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (j < n) p[j] = make_uint4(0, 0, 0, 0);
+    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < n; j += (int64_t)gridDim.x * 256) p[j] = make_uint4(0, 0, 0, 0);
 }
 
 // dst = src (or 0), n floats.
@@ -606,25 +607,42 @@ int far(const GatedArgs &a) {
     return side <= 8 ? 12 : side <= 32 ? 8 : 0;
 }
 
+// launch(first, n) for as many blocks as a launch may have, until `blocks` of them are enqueued or one
+// launch fails: a grid's work-items are fewer than 2^32.
+template <typename F>
+hipError_t in_launches(int64_t blocks, int threads, F launch) {
+    const int64_t most = 0xffffffffll / threads;
+    for (int64_t first = 0; first < blocks; first += most) {
+        launch(first, (unsigned)std::min(most, blocks - first));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <typename IO, int CPL, int FAR>
-void run_fwd(const GatedArgs &a, uint32_t *ticket, uint64_t *words, hipStream_t s) {
-    const dim3 grid((unsigned)(tiles_of(a.D, 64 * CPL) * a.batch * tiles_of(a.L, kFwdTile)));
-    if (a.reset) k_gated_fwd<IO, CPL, true, FAR><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words);
-    else k_gated_fwd<IO, CPL, false, FAR><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words);
+hipError_t run_fwd(const GatedArgs &a, uint32_t *ticket, uint64_t *words, hipStream_t s) {
+    return in_launches(tiles_of(a.D, 64 * CPL) * a.batch * tiles_of(a.L, kFwdTile), 64 * kWaves, [&](int64_t first, unsigned n) {
+        if (a.reset) k_gated_fwd<IO, CPL, true, FAR><<<dim3(n), 64 * kWaves, 0, s>>>(a, (uint32_t)first, ticket, words);
+        else k_gated_fwd<IO, CPL, false, FAR><<<dim3(n), 64 * kWaves, 0, s>>>(a, (uint32_t)first, ticket, words);
+    });
 }
 template <typename IO, int CPL, int FAR>
-void run_bwd(const GatedArgs &a, uint32_t *ticket, uint64_t *words, float *sums, hipStream_t s) {
-    const dim3 grid((unsigned)(tiles_of(a.D, 64 * CPL) * a.batch * tiles_of(a.L, kBwdTile)));
-    if (a.reset) k_gated_bwd<IO, CPL, true, FAR><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words, sums);
-    else k_gated_bwd<IO, CPL, false, FAR><<<grid, 64 * kWaves, 0, s>>>(a, ticket, words, sums);
+hipError_t run_bwd(const GatedArgs &a, uint32_t *ticket, uint64_t *words, float *sums, hipStream_t s) {
+    return in_launches(tiles_of(a.D, 64 * CPL) * a.batch * tiles_of(a.L, kBwdTile), 64 * kWaves, [&](int64_t first, unsigned n) {
+        if (a.reset) k_gated_bwd<IO, CPL, true, FAR><<<dim3(n), 64 * kWaves, 0, s>>>(a, (uint32_t)first, ticket, words, sums);
+        else k_gated_bwd<IO, CPL, false, FAR><<<dim3(n), 64 * kWaves, 0, s>>>(a, (uint32_t)first, ticket, words, sums);
+    });
 }
 
 // The counter and the words of a call with several tiles, cleared; null for one tile.
-void set_up(const GatedArgs &a, int tile, uint32_t **ticket, uint64_t **words, hipStream_t s) {
+hipError_t set_up(const GatedArgs &a, int tile, uint32_t **ticket, uint64_t **words, hipStream_t s) {
     const size_t n = words_bytes(a.batch, a.L, a.D, tile);
     *ticket = n ? (uint32_t *)a.ws : nullptr;
     *words = n ? (uint64_t *)((char *)a.ws + kTrainWsAlign) : nullptr;
-    if (n) k_clear<<<dim3((unsigned)((n / 16 + 255) / 256)), 256, 0, s>>>((uint4 *)a.ws, (int64_t)(n / 16));
+    if (n)
+        k_clear<<<dim3((unsigned)std::min<size_t>((n / 16 + 255) / 256, 1 << 20)), 256, 0, s>>>((uint4 *)a.ws, (int64_t)(n / 16));
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -633,14 +651,13 @@ hipError_t launch_gated_fwd(const GatedArgs &a, int io, hipStream_t s) {
     if (a.L == 0) return fill(a.h_final, a.h0, a.batch * a.D, s);
     uint32_t *ticket;
     uint64_t *words;
-    set_up(a, kFwdTile, &ticket, &words, s);
+    const hipError_t e = set_up(a, kFwdTile, &ticket, &words, s);
+    if (e != hipSuccess) return e;
     const int ahead = far(a);
-    if (ahead == 12) io ? run_fwd<bf16_bits, 1, 12>(a, ticket, words, s) : run_fwd<float, 1, 12>(a, ticket, words, s);
-    else if (ahead == 8) io ? run_fwd<bf16_bits, 1, 8>(a, ticket, words, s) : run_fwd<float, 1, 8>(a, ticket, words, s);
-    else if (!io) run_fwd<float, 1, 0>(a, ticket, words, s);
-    else if (pairs(a, io)) run_fwd<bf16_bits, 2, 0>(a, ticket, words, s);
-    else run_fwd<bf16_bits, 1, 0>(a, ticket, words, s);
-    return hipGetLastError();
+    if (ahead == 12) return io ? run_fwd<bf16_bits, 1, 12>(a, ticket, words, s) : run_fwd<float, 1, 12>(a, ticket, words, s);
+    if (ahead == 8) return io ? run_fwd<bf16_bits, 1, 8>(a, ticket, words, s) : run_fwd<float, 1, 8>(a, ticket, words, s);
+    if (!io) return run_fwd<float, 1, 0>(a, ticket, words, s);
+    return pairs(a, io) ? run_fwd<bf16_bits, 2, 0>(a, ticket, words, s) : run_fwd<bf16_bits, 1, 0>(a, ticket, words, s);
 }
 
 hipError_t launch_gated_bwd(const GatedArgs &a, int io, hipStream_t s) {
@@ -650,17 +667,19 @@ hipError_t launch_gated_bwd(const GatedArgs &a, int io, hipStream_t s) {
     }
     uint32_t *ticket;
     uint64_t *words;
-    set_up(a, kBwdTile, &ticket, &words, s);
+    hipError_t e = set_up(a, kBwdTile, &ticket, &words, s);
+    if (e != hipSuccess) return e;
     float *sums = (float *)((char *)a.ws + words_bytes(a.batch, a.L, a.D, kBwdTile));
     const int ahead = far(a);
-    if (ahead == 12) io ? run_bwd<bf16_bits, 1, 12>(a, ticket, words, sums, s) : run_bwd<float, 1, 12>(a, ticket, words, sums, s);
-    else if (ahead == 8) io ? run_bwd<bf16_bits, 1, 8>(a, ticket, words, sums, s) : run_bwd<float, 1, 8>(a, ticket, words, sums, s);
-    else if (!io) run_bwd<float, 1, 0>(a, ticket, words, sums, s);
-    else if (pairs(a, io)) run_bwd<bf16_bits, 2, 0>(a, ticket, words, sums, s);
-    else run_bwd<bf16_bits, 1, 0>(a, ticket, words, sums, s);
-    k_gated_ddecay<<<dim3((unsigned)((a.D + 63) / 64)), 1024, 0, s>>>(sums, a.decay, a.ddecay,
-                                                                     a.batch * tiles_of(a.L, kBwdTile), a.D);
-    return hipGetLastError();
+    if (ahead == 12) e = io ? run_bwd<bf16_bits, 1, 12>(a, ticket, words, sums, s) : run_bwd<float, 1, 12>(a, ticket, words, sums, s);
+    else if (ahead == 8) e = io ? run_bwd<bf16_bits, 1, 8>(a, ticket, words, sums, s) : run_bwd<float, 1, 8>(a, ticket, words, sums, s);
+    else if (!io) e = run_bwd<float, 1, 0>(a, ticket, words, sums, s);
+    else if (pairs(a, io)) e = run_bwd<bf16_bits, 2, 0>(a, ticket, words, sums, s);
+    else e = run_bwd<bf16_bits, 1, 0>(a, ticket, words, sums, s);
+    if (e != hipSuccess) return e;  // there are no sums then
+    return in_launches(tiles_of(a.D, 64), 1024, [&](int64_t first, unsigned n) {
+        k_gated_ddecay<<<dim3(n), 1024, 0, s>>>(sums, a.decay, a.ddecay, a.batch * tiles_of(a.L, kBwdTile), a.D, first * 64);
+    });
 }
 
 namespace {

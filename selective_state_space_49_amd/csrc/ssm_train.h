@@ -53,6 +53,8 @@ struct XentArgs {
 };
 size_t xent_fwd_ws(int64_t T, int64_t K, int64_t V, int io);
 size_t xent_bwd_ws(int64_t T, int64_t K, int64_t V, int io);
+// Whether every launch of a call stays below 2^32 work-items.
+bool xent_fits(int64_t T, int64_t K, int64_t V, int io, bool bwd);
 hipError_t launch_xent_fwd(const XentArgs &a, int io, hipStream_t s);
 hipError_t launch_xent_bwd(const XentArgs &a, int io, hipStream_t s);
 
@@ -75,6 +77,7 @@ struct AdamwArgs {
     float beta1, omb1, beta2, omb2, rs2, eps, keep, rate;  // in the order of the formula
     bool plain;                // eps >= 2^-60, rs2 <= 2^10: no extreme denominators
 };
+constexpr int64_t kAdamwMostBlocks = 0xffffff;  // of a launch: 256 threads each, fewer than 2^32 in all
 int32_t adamw_blocks(int64_t n, bool codes);  // thread blocks of a tensor of n elements
 hipError_t launch_adamw(const AdamwArgs &a, int32_t blocks, hipStream_t s);
 hipError_t launch_adamw_values(const int8_t *m, const uint8_t *v, const float *ms, const float *vs,

@@ -1071,6 +1071,28 @@ size_t xent_bwd_ws(int64_t T, int64_t K, int64_t V, int io) {
     return T > 0 ? std::max(lay_out(T, K, V, io, true, false, false, nullptr).bytes,
                             lay_out(T, K, V, io, true, false, true, nullptr).bytes) : 0;
 }
+bool xent_fits(int64_t T, int64_t K, int64_t V, int io, bool bwd) {
+    const int64_t most = 0xffffffffll;
+    const auto tiles = [](int64_t M, int64_t N, int tile) { return (int64_t)blocks(M, tile) * blocks(N, tile); };
+    const auto fits = [&](int64_t M, int64_t N, int tile) { return tiles(M, N, tile) * (tile == kBig ? 512 : 256) <= most; };
+    if (T == 0) return true;
+    if ((int64_t)blocks(T, join_tokens(T)) * 256 > most) return false;
+    // most calls, whichever tiles they take
+    if (tiles(V, T, kSmall) < 1 << 22 && tiles(K, std::max(T, V), kSmall) < 1 << 22) return true;
+    if (!bwd) return fits(V, T, lay_out(T, K, V, io, false, false, false, nullptr).lse.tile);
+    for (const bool weighed : {false, true}) {
+        const Layout l = lay_out(T, K, V, io, true, false, weighed, nullptr);
+        const int64_t longest = std::min(V, l.piece), last = (V - 1) % l.piece + 1;
+        for (const int64_t nv : {longest, last})
+            if (!fits(nv, T, tiling(nv, T, l.ldk / kBK * l.logits.n, false).tile)) return false;
+        if (!fits(K, longest, l.out_w.tile) || !fits(K, T, l.out_h.tile)) return false;
+        // both gradients in one launch
+        if (l.out_w.tile == kSmall && l.out_h.tile == kSmall &&
+            (tiles(K, longest, kSmall) * l.out_w.splits + tiles(K, T, kSmall) * l.out_h.splits) * 256 > most)
+            return false;
+    }
+    return true;
+}
 hipError_t launch_xent_fwd(const XentArgs &a, int io, hipStream_t s) {
     return io ? xent_fwd<bf16_bits>(a, io, s) : xent_fwd<float>(a, io, s);
 }
