@@ -111,6 +111,14 @@ void *optional(PyObject *o, at::ScalarType type, at::IntArrayRef sizes, int devi
     return o == Py_None ? nullptr : address(o, type, sizes, device, ok);
 }
 
+// Autograd is told that a tensor was written: what saved it for a backward must not use it.
+void written(const at::Tensor &t) {
+    if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(PyObject *o) {
+    if (o != Py_None) written(THPVariable_Unpack(o));
+}
+
 template <typename F>
 PyObject *no_exceptions(F fn) {
     try {
@@ -156,7 +164,11 @@ PyObject *gated_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
         Py_BEGIN_ALLOW_THREADS
         st = entry(h, xp, r, i, decay, (float)c, y, all[0], all[1], all[2], io == at::kFloat ? SSM_F32 : SSM_BF16, stream);
         Py_END_ALLOW_THREADS
-        if (st == SSM_OK) return out;
+        if (st == SSM_OK) {
+            written(args[2]);
+            written(args[8]);
+            return out;
+        }
         Py_DECREF(out);
         return PyLong_FromLong(st);
     });
@@ -196,6 +208,11 @@ PyObject *adamw_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
         st = entry((int32_t)t.params.size(), t.params.data(), t.grads.data(), t.sizes.data(), t.kinds.data(),
                    t.grad_kinds.data(), m, v, ms, vs, gs, f[0], f[1], f[2], f[3], f[4], step, stream);
         Py_END_ALLOW_THREADS
+        if (st == SSM_OK) {
+            for (size_t k = 0; k < t.params.size(); ++k)
+                if (t.grads[k]) written(PyList_GET_ITEM(args[3], (Py_ssize_t)k));
+            for (int k = 5; k < 9; ++k) written(args[k]);
+        }
         return PyLong_FromLong(st);
     });
 }
@@ -280,6 +297,8 @@ PyObject *gated_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         st = entry(x, r, i, decay, h0, reset, c, at_of(y), (float *)at_of(h), (float *)at_of(states), b, L, D, k.kind(),
                    at_of(ws), bytes, stream);
         Py_END_ALLOW_THREADS
+        if (st == SSM_OK)
+            for (int k = 10; k < 13; ++k) written(args[k]);
         return result(st, {y, h, states});
     });
 }
@@ -348,6 +367,8 @@ PyObject *xent_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         st = entry(hidden, weight, targets, ignore, (float *)at_of(loss), (float *)at_of(lse), (float *)at_of(mean), T, K, V,
                    k.kind(), at_of(ws), bytes, stream);
         Py_END_ALLOW_THREADS
+        if (st == SSM_OK)
+            for (int k = 7; k < 10; ++k) written(args[k]);
         return result(st, {loss, lse, mean});
     });
 }

@@ -51,10 +51,12 @@ def _stream(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-def _called(t: torch.Tensor, entry, *args):
-    """One of the library's entry points on the tensor's GPU and torch's current stream there."""
+def _called(t: torch.Tensor, entry, *args, written=()):
+    """One of the library's entry points on the tensor's GPU and torch's current stream there.
+    Autograd is told of the tensors that it has written."""
     with torch.cuda.device(t.device):
         _check(entry(*args, _stream(t)))
+    torch.autograd.graph.increment_version([w for w in written if w is not None and not w.is_inference()])
 
 
 _table_loaded = None
@@ -151,7 +153,8 @@ def _gated_fwd(x, r, i, decay, h0, reset, c, y, h_final, states, workspace, want
     _called(x, lib.ssm_gated_fwd, _need(x, "x", shape, io, dev), _need(r, "r", shape, io, dev), _need(i, "i", shape, io, dev),
             _need(decay, "decay", (D,), _f32, dev), _need(h0, "h0", (b, D), _f32, dev), _reset(reset, (b, L), dev), c,
             _need(y, "y", shape, io, dev), _need(h_final, "h_final", (b, D), _f32, dev),
-            _need(states, "states", (b, _states_rows(L), D), _f32, dev), b, L, D, kind, ws_at, ws_bytes)
+            _need(states, "states", (b, _states_rows(L), D), _f32, dev), b, L, D, kind, ws_at, ws_bytes,
+            written=(y, h_final, states))
     return y, h_final, states
 
 
@@ -271,7 +274,8 @@ def ssm_xent_fwd(hidden, weight, targets, *, ignore_index=-100, loss=None, lse=N
     mean = torch.empty(2, dtype=_f32, device=dev) if mean is None else mean
     ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_xent_fwd_workspace(T, K, V, kind), dev)
     _called(hidden, lib.ssm_xent_fwd, *inputs, ignore_index, _need(loss, "loss", (T,), _f32, dev),
-            _need(lse, "lse", (T,), _f32, dev), _need(mean, "mean", (2,), _f32, dev), T, K, V, kind, ws_at, ws_bytes)
+            _need(lse, "lse", (T,), _f32, dev), _need(mean, "mean", (2,), _f32, dev), T, K, V, kind, ws_at, ws_bytes,
+            written=(loss, lse, mean))
     return loss, lse, mean
 
 
