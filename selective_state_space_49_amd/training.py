@@ -13,6 +13,7 @@ import os
 from typing import Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import SSM_BF16, SSM_F32, _check, _dev, load_library
 
@@ -216,6 +217,7 @@ class _GatedScan(torch.autograd.Function):
         return y, h_final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh_final):
         x, r, i, decay, states, reset = ctx.saved_tensors
         dy = torch.zeros_like(x) if dy is None else dy.to(x.dtype).contiguous()
@@ -228,7 +230,7 @@ class _GatedScan(torch.autograd.Function):
 
 def gated_scan(x, r, i, decay, h0=None, reset=None, *, c=8.0):
     """The gated recurrence as a differentiable function: (y, h_final), with gradients for x,
-    r, i, decay and h0."""
+    r, i, decay and h0 (which have none of their own: a second derivative is refused)."""
     return _GatedScan.apply(x, r, i, decay, h0, reset, c)
 
 
@@ -314,6 +316,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
         return mean[0], loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dmean, dloss):
         hidden, weight, targets, lse, mean = ctx.saved_tensors
         one = lambda t: None if t is None else t.float().contiguous()  # noqa: E731
@@ -326,7 +329,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
 def linear_cross_entropy(hidden, weight, targets, *, ignore_index=-100, reduction="mean"):
     """Softmax cross entropy of a linear head, differentiable in hidden [..., K] and weight
     [V, K]: the mean over the tokens that are not ignored (0 where all are), or with
-    reduction="none" every token's loss in targets' shape."""
+    reduction="none" every token's loss in targets' shape. Second derivatives are refused."""
     if reduction not in ("mean", "none"):
         raise ValueError(f"reduction must be 'mean' or 'none', got {reduction!r}")
     mean, loss = _LinearCrossEntropy.apply(hidden.reshape(-1, hidden.shape[-1]), weight, targets.reshape(-1),
