@@ -313,7 +313,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
         ctx.save_for_backward(hidden, weight, targets, lse, mean)
         ctx.ignore_index = ignore_index
         ctx.set_materialize_grads(False)  # a loss that is not used has no gradient: the mean's alone is cheaper
-        return mean[0], loss
+        return mean[0].clone(), loss  # a view could not be changed in place, as in `loss /= n`
 
     @staticmethod
     @once_differentiable
