@@ -382,14 +382,18 @@ def ssm_adamw_values(exp_avg, exp_avg_sq, avg_scale, avg_sq_scale):
 
 class AdamW:
     """AdamW over a list of parameters (float32 and bfloat16, on one GPU), one library call a
-    step. bits: 32, or 8 for moments held in 8-bit codes with a scale for 256 of them."""
+    step. bits: 32, or 8 for moments held in 8-bit codes with a scale for 256 of them.
+
+    A parameter's bias corrections go by its own steps, those in which it had a gradient
+    (``steps``): one that gets its first gradient late starts like any other. Parameters with
+    different counts take a library call for each count."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, bits=32):
         if bits not in (8, 32):
             raise ValueError(f"bits must be 8 or 32, got {bits}")
         self.params = list(params)
         self.lr, self.betas, self.eps, self.weight_decay, self.bits = lr, betas, eps, weight_decay, bits
-        self.steps = 0
+        self.steps = [0] * len(self.params)
         n = ssm_adamw_state_size(p.numel() for p in self.params)
         dev = self.params[0].device if self.params else None
         zeros = lambda k, dtype: torch.zeros(k, dtype=dtype, device=dev)  # noqa: E731
@@ -400,19 +404,40 @@ class AdamW:
 
     @torch.no_grad()
     def step(self, grad_scale=None):
-        """Updates every parameter that has a gradient; grad_scale multiplies the gradients."""
-        self.steps += 1
-        ssm_adamw_step([p.detach() for p in self.params], [p.grad for p in self.params], self.exp_avg,
-                       self.exp_avg_sq, self.avg_scale, self.avg_sq_scale, lr=self.lr, beta1=self.betas[0],
-                       beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay, step=self.steps,
-                       grad_scale=grad_scale)
+        """Updates every parameter that has a gradient; grad_scale multiplies the gradients. A
+        call that is refused changes nothing and counts as no step."""
+        params, grads = [p.detach() for p in self.params], [p.grad for p in self.params]
+        counts = {}
+        for k, g in enumerate(grads):
+            if g is not None:
+                counts.setdefault(self.steps[k], []).append(k)
+        if len(counts) > 1:  # all of them before the first call
+            self._refuse_gradients(params, grads)
+        for count, which in counts.items():
+            chosen = grads
+            if len(counts) > 1:
+                chosen = [None] * len(grads)
+                for k in which:
+                    chosen[k] = grads[k]
+            ssm_adamw_step(params, chosen, self.exp_avg, self.exp_avg_sq, self.avg_scale, self.avg_sq_scale, lr=self.lr,
+                           beta1=self.betas[0], beta2=self.betas[1], eps=self.eps, weight_decay=self.weight_decay,
+                           step=count + 1, grad_scale=grad_scale)
+            for k in which:
+                self.steps[k] += 1
+
+    @staticmethod
+    def _refuse_gradients(params, grads):
+        for k, (p, g) in enumerate(zip(params, grads)):
+            if g is not None and not (g.shape == p.shape and g.dtype in _IO and g.device == p.device and g.is_contiguous()):
+                raise ValueError(f"gradient {k} must be a contiguous float32 or bfloat16 tensor of its parameter's shape "
+                                 "on its GPU")
 
     def zero_grad(self):
         for p in self.params:
             p.grad = None
 
     def state_dict(self):
-        return {"steps": self.steps, "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq,
+        return {"steps": list(self.steps), "exp_avg": self.exp_avg, "exp_avg_sq": self.exp_avg_sq,
                 "avg_scale": self.avg_scale, "avg_sq_scale": self.avg_sq_scale}
 
     def load_state_dict(self, state):
@@ -422,7 +447,11 @@ class AdamW:
             if (mine is None) != (theirs is None) or (
                     mine is not None and (mine.shape != theirs.shape or mine.dtype != theirs.dtype)):
                 raise ValueError(f"{name} does not fit this optimizer's parameters and bits")
+        steps = state["steps"]  # a count for each parameter, or one for all of them
+        steps = [int(steps)] * len(self.params) if isinstance(steps, int) else [int(n) for n in steps]
+        if len(steps) != len(self.params):
+            raise ValueError(f"steps has {len(steps)} counts for {len(self.params)} parameters")
         for name in names:
             if getattr(self, name) is not None:
                 getattr(self, name).copy_(state[name])
-        self.steps = int(state["steps"])
+        self.steps = steps
