@@ -36,7 +36,7 @@ __all__ = [
     "ssm_gated_fwd_workspace", "ssm_gated_bwd_workspace", "ssm_gated_states_bytes",
     "gated_scan", "GATED_STATE_EVERY",
     "ssm_xent_fwd", "ssm_xent_bwd", "ssm_xent_fwd_workspace", "ssm_xent_bwd_workspace",
-    "linear_cross_entropy",
+    "ssm_xent_fwd_workspace_for", "ssm_xent_bwd_workspace_for", "linear_cross_entropy",
     "ssm_adamw_step", "ssm_adamw_values", "ssm_adamw_state_size", "ADAMW_BLOCK", "AdamW",
 ]
 
@@ -64,6 +64,7 @@ EXPORTED_SYMBOLS = [
     "ssm_gated_fwd", "ssm_gated_bwd", "ssm_gated_step", "ssm_gated_fwd_workspace",
     "ssm_gated_bwd_workspace", "ssm_gated_states_bytes",
     "ssm_xent_fwd", "ssm_xent_bwd", "ssm_xent_fwd_workspace", "ssm_xent_bwd_workspace",
+    "ssm_xent_fwd_workspace_for", "ssm_xent_bwd_workspace_for",
     "ssm_adamw_step", "ssm_adamw_values", "ssm_adamw_state_size",
 ]
 # Steps between the states ssm_scan_fwd_save stores for ssm_scan_bwd_saved.
@@ -152,6 +153,8 @@ def load_library():
     sig["ssm_gated_bwd"] = ([vp] * 6 + [f32] + [vp] * 7 + [i64, i64, i64, ci, vp, sz, vp], ci)
     sig["ssm_gated_step"] = ([vp] * 5 + [f32, vp, i64, i64, i64, ci, vp], ci)
     sig["ssm_xent_fwd_workspace"] = sig["ssm_xent_bwd_workspace"] = ([i64, i64, i64, ci], sz)
+    sig["ssm_xent_fwd_workspace_for"] = ([vp, vp, i64, i64, i64, ci], sz)
+    sig["ssm_xent_bwd_workspace_for"] = ([vp, vp, vp, i64, i64, i64, ci], sz)
     sig["ssm_xent_fwd"] = ([vp] * 3 + [i64] + [vp] * 3 + [i64, i64, i64, ci, vp, sz, vp], ci)
     sig["ssm_xent_bwd"] = ([vp] * 3 + [i64] + [vp] * 6 + [i64, i64, i64, ci, vp, sz, vp], ci)
     sig["ssm_adamw_state_size"] = ([i32, vp], i64)
@@ -960,4 +963,5 @@ from .training import (  # noqa: E402  (the training operators use the helpers a
     ADAMW_BLOCK, GATED_STATE_EVERY, AdamW, gated_scan, linear_cross_entropy, ssm_adamw_state_size,
     ssm_adamw_step, ssm_adamw_values, ssm_gated_bwd, ssm_gated_bwd_workspace, ssm_gated_fwd,
     ssm_gated_fwd_save, ssm_gated_fwd_workspace, ssm_gated_states_bytes, ssm_gated_step,
-    ssm_xent_bwd, ssm_xent_bwd_workspace, ssm_xent_fwd, ssm_xent_fwd_workspace)
+    ssm_xent_bwd, ssm_xent_bwd_workspace, ssm_xent_bwd_workspace_for, ssm_xent_fwd,
+    ssm_xent_fwd_workspace, ssm_xent_fwd_workspace_for)

@@ -242,10 +242,19 @@ ssm_status ssm_gated_step(float *h, const void *x_t, const void *r_t, const void
 
 // ---------------------------------------------------------------- vocabulary cross entropy
 size_t ssm_xent_fwd_workspace(int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io) {
-    return valid_io(io) && xent_shape_ok(tokens, dim, vocab, io, false) ? ssm::xent_fwd_ws(tokens, dim, vocab, io == SSM_BF16) : 0;
+    return valid_io(io) && xent_shape_ok(tokens, dim, vocab, io, false) ? ssm::xent_fwd_ws_any(tokens, dim, vocab, io == SSM_BF16) : 0;
+}
+size_t ssm_xent_fwd_workspace_for(const void *hidden, const void *weight, int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io) {
+    return valid_io(io) && xent_shape_ok(tokens, dim, vocab, io, false)
+               ? ssm::xent_fwd_ws(tokens, dim, vocab, io == SSM_BF16, hidden, weight) : 0;
+}
+size_t ssm_xent_bwd_workspace_for(const void *hidden, const void *weight, const float *dloss, int64_t tokens, int64_t dim,
+                                  int64_t vocab, ssm_dtype io) {
+    return valid_io(io) && xent_shape_ok(tokens, dim, vocab, io, true)
+               ? ssm::xent_bwd_ws(tokens, dim, vocab, io == SSM_BF16, hidden, weight, dloss != nullptr) : 0;
 }
 size_t ssm_xent_bwd_workspace(int64_t tokens, int64_t dim, int64_t vocab, ssm_dtype io) {
-    return valid_io(io) && xent_shape_ok(tokens, dim, vocab, io, true) ? ssm::xent_bwd_ws(tokens, dim, vocab, io == SSM_BF16) : 0;
+    return valid_io(io) && xent_shape_ok(tokens, dim, vocab, io, true) ? ssm::xent_bwd_ws_any(tokens, dim, vocab, io == SSM_BF16) : 0;
 }
 
 ssm_status ssm_xent_fwd(const void *hidden, const void *weight, const int64_t *targets, int64_t ignore_index,
@@ -261,7 +270,7 @@ ssm_status ssm_xent_fwd(const void *hidden, const void *weight, const int64_t *t
                       {"targets", targets, (size_t)tokens * 8}},
                      {{"loss", loss, tb}, {"lse", lse, tb}, {"mean", mean, 8}});
     if (st != SSM_OK) return st;
-    st = check_workspace(workspace, workspace_bytes, ssm::xent_fwd_ws(tokens, dim, vocab, io == SSM_BF16));
+    st = check_workspace(workspace, workspace_bytes, ssm::xent_fwd_ws(tokens, dim, vocab, io == SSM_BF16, hidden, weight));
     if (st != SSM_OK) return st;
     ssm::XentArgs a{};
     a.hidden = hidden; a.weight = weight; a.targets = targets; a.ignore = ignore_index;
@@ -286,7 +295,7 @@ ssm_status ssm_xent_bwd(const void *hidden, const void *weight, const int64_t *t
                       {"lse", lse, tb}, {"mean", mean, 8}, {"dloss", dloss, tb}, {"dmean", dmean, 4}},
                      {{"dhidden", dhidden, nh}, {"dweight", dweight, nw}});
     if (st != SSM_OK) return st;
-    st = check_workspace(workspace, workspace_bytes, ssm::xent_bwd_ws(tokens, dim, vocab, io == SSM_BF16));
+    st = check_workspace(workspace, workspace_bytes, ssm::xent_bwd_ws(tokens, dim, vocab, io == SSM_BF16, hidden, weight, dloss != nullptr));
     if (st != SSM_OK) return st;
     if (!dhidden && !dweight) return ok();
     ssm::XentArgs a{};

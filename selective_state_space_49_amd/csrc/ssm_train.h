@@ -51,8 +51,10 @@ struct XentArgs {
     int64_t T, K, V;
     void *ws;
 };
-size_t xent_fwd_ws(int64_t T, int64_t K, int64_t V, int io);
-size_t xent_bwd_ws(int64_t T, int64_t K, int64_t V, int io);
+size_t xent_fwd_ws(int64_t T, int64_t K, int64_t V, int io, const void *hidden, const void *weight);
+size_t xent_bwd_ws(int64_t T, int64_t K, int64_t V, int io, const void *hidden, const void *weight, bool weighed);
+size_t xent_fwd_ws_any(int64_t T, int64_t K, int64_t V, int io);  // enough for any pointers
+size_t xent_bwd_ws_any(int64_t T, int64_t K, int64_t V, int io);
 // Whether every launch of a call stays below 2^32 work-items.
 bool xent_fits(int64_t T, int64_t K, int64_t V, int io, bool bwd);
 hipError_t launch_xent_fwd(const XentArgs &a, int io, hipStream_t s);

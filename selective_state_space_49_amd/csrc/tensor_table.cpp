@@ -346,7 +346,7 @@ PyObject *xent_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 10) return PyErr_Format(PyExc_TypeError, "10 arguments expected, got %zd", n);
     return no_exceptions([&]() -> PyObject * {
         const auto entry = (decltype(&ssm_xent_fwd))PyLong_AsVoidPtr(args[0]);
-        const auto size = (decltype(&ssm_xent_fwd_workspace))PyLong_AsVoidPtr(args[1]);
+        const auto size = (decltype(&ssm_xent_fwd_workspace_for))PyLong_AsVoidPtr(args[1]);
         void *const stream = PyLong_AsVoidPtr(args[2]);
         const int64_t ignore = PyLong_AsLongLong(args[6]);
         if (PyErr_Occurred()) return nullptr;
@@ -359,7 +359,7 @@ PyObject *xent_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         if (!k.ok) Py_RETURN_NONE;
         const at::Tensor loss = k.out(args[7], at::kFloat, T), lse = k.out(args[8], at::kFloat, T), mean = k.out(args[9], at::kFloat, 2);
         if (!k.ok) Py_RETURN_NONE;
-        const size_t bytes = size(T, K, V, k.kind());
+        const size_t bytes = size(hidden, weight, T, K, V, k.kind());
         const at::Tensor ws = bytes ? k.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
         const c10::DeviceGuard on(k.first.device());
         ssm_status st;
@@ -379,7 +379,7 @@ PyObject *xent_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 13) return PyErr_Format(PyExc_TypeError, "13 arguments expected, got %zd", n);
     return no_exceptions([&]() -> PyObject * {
         const auto entry = (decltype(&ssm_xent_bwd))PyLong_AsVoidPtr(args[0]);
-        const auto size = (decltype(&ssm_xent_bwd_workspace))PyLong_AsVoidPtr(args[1]);
+        const auto size = (decltype(&ssm_xent_bwd_workspace_for))PyLong_AsVoidPtr(args[1]);
         void *const stream = PyLong_AsVoidPtr(args[2]);
         const int64_t ignore = PyLong_AsLongLong(args[6]);
         if (PyErr_Occurred()) return nullptr;
@@ -399,7 +399,7 @@ PyObject *xent_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
         if (!k.ok) Py_RETURN_NONE;
         const at::Tensor dh = args[11] == Py_True ? k.fresh(k.io, k.first.sizes()) : at::Tensor();
         const at::Tensor dw = args[12] == Py_True ? k.fresh(k.io, head) : at::Tensor();
-        const size_t bytes = size(T, K, V, k.kind());
+        const size_t bytes = size(hidden, weight, dloss, T, K, V, k.kind());
         const at::Tensor ws = bytes ? k.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
         const c10::DeviceGuard on(k.first.device());
         ssm_status st;

@@ -426,7 +426,7 @@ __device__ __forceinline__ void epilogue(const ProductArgs &p, f32x16 (&acc)[S::
             s += __shfl_xor(s, 32);
             if (n >= p.N) continue;
             if (half == 0) p.part[slot * p.N + n] = make_float2(top, s);
-            const int64_t t = p.tokens.targets[n] - mw;  // the lane's rows are t = 32 i + 8 (e / 4) + e % 4
+            const int64_t t = p.tokens.targets[n] - p.v0 - mw;  // the lane's rows are t = 32 i + 8 (e / 4) + e % 4
             if (t >= 0 && t < S::TM * 32 && (t & 4) == 0) {
 #pragma unroll
                 for (int i = 0; i < S::TM; ++i)
@@ -825,10 +825,10 @@ constexpr int64_t kFewTokens = 64;
 struct Layout {
     int parts, parts_w, parts_g;  // of hidden and weight, of w hidden, of G
     Terms logits, to_w, to_h;    // of the products
-    int64_t ldk, rows_t, piece;  // padded dim and tokens; vocabulary rows of a piece
+    int64_t ldk, rows_t, piece;  // padded dim and tokens; vocabulary rows of a piece (V: all in one)
     Tiling lse, out_w, out_h;
-    bool pack;                   // weight is copied: float32, or rows not in steps of 64
-    uint16_t *hidden, *weight;   // copies for the logits
+    bool pack;                   // hidden and weight are copied: float32, or rows not in steps of 64
+    uint16_t *hidden, *weight;   // the copies, of weight a piece's
     uint16_t *hidden_w, *g;      // for the gradients: (w) hidden, G
     uint32_t *done;
     Losses *losses;
@@ -840,25 +840,32 @@ struct Layout {
 // G of a piece holds about 2^27 numbers of 16 bits, 256 MB: 8192 tokens take pieces of 16384 rows.
 // dhidden's partial sum is read and written once for each piece, so that more of them cost more
 // (2^26, 2^27 and 2^28 values: 7.32, 7.27 and 7.22 ms for 8192 x 4096 x 32000, 8.34, 8.05 and
-// 8.05 ms for 2000 x 4096 x 128000), and larger ones would begin to be the whole array.
+// 8.05 ms for 2000 x 4096 x 128000), and larger ones would begin to be the whole array. A copy of
+// weight, where there is one, is that of a piece too, and no larger.
 constexpr int64_t kPieceValues = (int64_t)1 << 27;
 
 // Tokens of a block that joins: whole lines of the partial pairs and few blocks where there are
 // many tokens, many threads for each where there are few.
 int join_tokens(int64_t T) { return T >= 4096 ? 32 : T >= 256 ? 16 : 2; }
 
-// weighed: the tokens have weights of their own.
-Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, bool weighed, char *ws) {
+// pack: hidden and weight have to be copied; weighed: the tokens have weights of their own.
+Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool pack, bool weighed, char *ws) {
     Layout l{};
     Arena a{ws};
     l.parts = io ? 1 : kMostParts;
     l.logits = terms_of(l.parts, l.parts);
     l.ldk = up(K, kBK);
     l.rows_t = up(T, kBK);
-    l.pack = !io || K % kBK != 0 || !aligned;
-    // sized as if the operands had to be copied: their alignment is not known to the query
-    l.hidden = a.take<uint16_t>(T * l.ldk * l.parts);
-    l.weight = a.take<uint16_t>(V * l.ldk * l.parts);
+    l.pack = pack;
+    const auto rows_of = [](int64_t numbers) { return std::max<int64_t>(1024, kPieceValues / numbers / kBig * kBig); };
+    l.piece = std::min(V, pack ? rows_of(l.ldk * l.parts) : V);
+    if (bwd) {
+        l.parts_w = io ? (weighed ? 2 : 1) : kMostParts;
+        l.parts_g = io ? (T <= kFewTokens ? 2 : 1) : kMostParts;
+        l.piece = std::min(l.piece, rows_of(l.rows_t * l.parts_g));
+    }
+    l.hidden = a.take<uint16_t>(pack ? T * l.ldk * l.parts : 0);
+    l.weight = a.take<uint16_t>(pack ? l.piece * l.ldk * l.parts : 0);
     if (!bwd) {
         l.lse = tiling(V, T, l.ldk / kBK * l.logits.n, false);
         l.part = a.take<float2>((int64_t)blocks(V, l.lse.tile) * 2 * T);
@@ -866,22 +873,23 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool aligned, 
         l.losses = a.take<Losses>(blocks(T, join_tokens(T)));
         l.done = a.take<uint32_t>(1);
     } else {
-        l.parts_w = io ? (weighed ? 2 : 1) : kMostParts;
-        l.parts_g = io ? (T <= kFewTokens ? 2 : 1) : kMostParts;
         l.to_w = terms_of(l.parts_w, l.parts_g);
         l.to_h = terms_of(l.parts, l.parts_g);
-        l.piece = std::min(up(V, kBig), std::max<int64_t>(1024, kPieceValues / l.parts_g / l.rows_t / kBig * kBig));
-        const int64_t most = std::min(V, l.piece);
-        l.out_w = tiling(K, most, l.rows_t / kBK * l.to_w.n, true);
-        l.out_h = tiling(K, T, up(most, kBK) / kBK * l.to_h.n, true);
+        l.out_w = tiling(K, l.piece, l.rows_t / kBK * l.to_w.n, true);
+        l.out_h = tiling(K, T, up(l.piece, kBK) / kBK * l.to_h.n, true);
         l.sum = a.take<float>(V > l.piece ? T * K : 0);
         l.hidden_w = a.take<uint16_t>(l.rows_t * l.ldk * l.parts_w);
-        l.g = a.take<uint16_t>(l.rows_t * up(most, kBK) * l.parts_g);
-        l.split_w = a.take<float>(l.out_w.splits > 1 ? l.out_w.splits * most * K : 0);
+        l.g = a.take<uint16_t>(l.rows_t * up(l.piece, kBK) * l.parts_g);
+        l.split_w = a.take<float>(l.out_w.splits > 1 ? l.out_w.splits * l.piece * K : 0);
         l.split_h = a.take<float>(l.out_h.splits > 1 ? l.out_h.splits * T * K : 0);
     }
     l.bytes = a.used;
     return l;
+}
+
+// Copies are needed but of bfloat16 rows in steps of 64 from 16 bytes on.
+bool packs(int64_t K, int io, const void *hidden, const void *weight) {
+    return !io || K % kBK != 0 || ((uintptr_t)hidden | (uintptr_t)weight) % 16 != 0;
 }
 
 constexpr int64_t kMostBlocks = (int64_t)1 << 20;
@@ -912,6 +920,8 @@ struct Copies {
     }
     hipError_t launch(const Tokens &tokens, hipStream_t s) {
         if (grid) k_pack<IO><<<dim3(grid), 256, 0, s>>>(list, tokens);
+        list = {};
+        grid = 0;
         return hipGetLastError();
     }
 };
@@ -922,21 +932,23 @@ struct Copies {
         if (try_e != hipSuccess) return try_e;     \
     } while (0)
 
-bool rows_aligned(const XentArgs &a) { return ((uintptr_t)a.hidden | (uintptr_t)a.weight) % 16 == 0; }
+// Rows v0 .. of weight as an operand, as they are or copied.
+template <typename IO>
+Operand weight_rows(const XentArgs &a, const Layout &l, int64_t v0, Copies<IO> &copies) {
+    const int64_t nv = std::min(l.piece, a.V - v0);
+    const IO *from = (const IO *)a.weight + v0 * a.K;
+    if (l.pack) return copies.add(l, from, nv, a.K, l.weight, nv, l.parts, Rows::All);
+    return {(const uint16_t *)from, l.ldk, 0, nv};
+}
 
-// The product of the logits, its operands as they are or copied. `made`: a copy of hidden that is
-// there already.
+// The product of the logits but for its weight. `made`: a copy of hidden that is there already.
 template <typename IO>
 ProductArgs logits_product(const XentArgs &a, const Layout &l, const Tokens &tokens, const Operand *made, Copies<IO> &copies) {
     ProductArgs p{};
     p.tokens = tokens;
-    if (l.pack) {
-        p.a = copies.add(l, a.weight, a.V, a.K, l.weight, a.V, l.parts, Rows::All);
-        p.b = made ? *made : copies.add(l, a.hidden, a.T, a.K, l.hidden, a.T, l.parts, Rows::All);
-    } else {
-        p.a = {(const uint16_t *)a.weight, l.ldk, 0, a.V};
-        p.b = made ? *made : Operand{(const uint16_t *)a.hidden, l.ldk, 0, a.T};
-    }
+    if (made) p.b = *made;
+    else if (l.pack) p.b = copies.add(l, a.hidden, a.T, a.K, l.hidden, a.T, l.parts, Rows::All);
+    else p.b = {(const uint16_t *)a.hidden, l.ldk, 0, a.T};
     p.N = a.T;
     p.steps = (int32_t)(l.ldk / kBK);
     p.terms = l.logits;
@@ -950,16 +962,20 @@ hipError_t xent_fwd(const XentArgs &a, int io, hipStream_t s) {
         k_zero<<<dim3(1), 256, 0, s>>>(a.mean, (int64_t)2);
         return hipGetLastError();
     }
-    const Layout l = lay_out(a.T, a.K, a.V, io, false, rows_aligned(a), false, (char *)a.ws);
+    const Layout l = lay_out(a.T, a.K, a.V, io, false, packs(a.K, io, a.hidden, a.weight), false, (char *)a.ws);
     const Tokens tokens{a.targets, a.ignore, a.V, nullptr, nullptr, nullptr};
     Copies<IO> copies;
     ProductArgs p = logits_product<IO>(a, l, tokens, nullptr, copies);
-    SSM_TRY(copies.launch(tokens, s));
-    p.M = a.V;
-    p.part = l.part;
     p.at = l.at;
     p.done = l.done;
-    SSM_TRY(product<Epi::Lse>(p, l.lse.tile, s));
+    for (int64_t v0 = 0; v0 < a.V; v0 += l.piece) {  // a piece is whole tiles, or all there is
+        p.a = weight_rows<IO>(a, l, v0, copies);
+        p.M = p.a.rows;
+        p.v0 = v0;
+        p.part = l.part + v0 / l.lse.tile * 2 * a.T;
+        SSM_TRY(copies.launch(tokens, s));
+        SSM_TRY(product<Epi::Lse>(p, l.lse.tile, s));
+    }
     const int64_t n = (int64_t)blocks(a.V, l.lse.tile) * 2;
     const int most = join_tokens(a.T);
     auto join = most == 32 ? k_xent_join<32> : most == 16 ? k_xent_join<16> : k_xent_join<2>;
@@ -1003,14 +1019,13 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
         return hipGetLastError();
     }
     const bool weighed = a.dloss != nullptr;  // else one weight for all tokens: a factor at the end
-    const Layout l = lay_out(a.T, a.K, a.V, io, true, rows_aligned(a), weighed, (char *)a.ws);
+    const Layout l = lay_out(a.T, a.K, a.V, io, true, packs(a.K, io, a.hidden, a.weight), weighed, (char *)a.ws);
     const Tokens tokens{a.targets, a.ignore, a.V, a.dloss, a.dmean, a.mean};
     Copies<IO> copies;
     Operand hidden_w{};
     if (a.dweight)
         hidden_w = copies.add(l, a.hidden, a.T, a.K, l.hidden_w, l.rows_t, l.parts_w, weighed ? Rows::Weighed : Rows::Used);
     ProductArgs logits = logits_product<IO>(a, l, tokens, a.dweight && !weighed ? &hidden_w : nullptr, copies);
-    SSM_TRY(copies.launch(tokens, s));
     logits.lse = a.lse;
     logits.parts = l.parts_g;
     logits.g = l.g;
@@ -1018,8 +1033,8 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
     for (int64_t v0 = 0; v0 < a.V; v0 += l.piece) {
         const int64_t nv = std::min(l.piece, a.V - v0), ldg = up(nv, kBK);
         ProductArgs p = logits;
-        p.a.p += v0 * l.ldk;
-        p.a.rows = nv;
+        p.a = weight_rows<IO>(a, l, v0, copies);
+        SSM_TRY(copies.launch(tokens, s));
         p.M = nv;
         p.v0 = v0;
         p.ldg = ldg;
@@ -1063,13 +1078,23 @@ hipError_t xent_bwd(const XentArgs &a, int io, hipStream_t s) {
 
 }  // namespace
 
-size_t xent_fwd_ws(int64_t T, int64_t K, int64_t V, int io) {
-    return T > 0 ? lay_out(T, K, V, io, false, false, false, nullptr).bytes : 0;
+size_t xent_fwd_ws(int64_t T, int64_t K, int64_t V, int io, const void *hidden, const void *weight) {
+    return T > 0 ? lay_out(T, K, V, io, false, packs(K, io, hidden, weight), false, nullptr).bytes : 0;
 }
-// For any call of these sizes: the tilings, and with them the splits, go by the partial products.
-size_t xent_bwd_ws(int64_t T, int64_t K, int64_t V, int io) {
-    return T > 0 ? std::max(lay_out(T, K, V, io, true, false, false, nullptr).bytes,
-                            lay_out(T, K, V, io, true, false, true, nullptr).bytes) : 0;
+size_t xent_bwd_ws(int64_t T, int64_t K, int64_t V, int io, const void *hidden, const void *weight, bool weighed) {
+    return T > 0 ? lay_out(T, K, V, io, true, packs(K, io, hidden, weight), weighed, nullptr).bytes : 0;
+}
+// For any pointers: the most of all, since the tilings, and with them the splits, go by the partial
+// products and the pieces.
+size_t xent_fwd_ws_any(int64_t T, int64_t K, int64_t V, int io) {
+    const void *const odd = (const void *)1;
+    return std::max(xent_fwd_ws(T, K, V, io, nullptr, nullptr), xent_fwd_ws(T, K, V, io, odd, odd));
+}
+size_t xent_bwd_ws_any(int64_t T, int64_t K, int64_t V, int io) {
+    size_t most = 0;
+    for (const void *p : {(const void *)nullptr, (const void *)1})
+        for (const bool weighed : {false, true}) most = std::max(most, xent_bwd_ws(T, K, V, io, p, p, weighed));
+    return most;
 }
 bool xent_fits(int64_t T, int64_t K, int64_t V, int io, bool bwd) {
     const int64_t most = 0xffffffffll;
@@ -1079,9 +1104,9 @@ bool xent_fits(int64_t T, int64_t K, int64_t V, int io, bool bwd) {
     if ((int64_t)blocks(T, join_tokens(T)) * 256 > most) return false;
     // most calls, whichever tiles they take
     if (tiles(V, T, kSmall) < 1 << 22 && tiles(K, std::max(T, V), kSmall) < 1 << 22) return true;
-    if (!bwd) return fits(V, T, lay_out(T, K, V, io, false, false, false, nullptr).lse.tile);
-    for (const bool weighed : {false, true}) {
-        const Layout l = lay_out(T, K, V, io, true, false, weighed, nullptr);
+    if (!bwd) return fits(V, T, lay_out(T, K, V, io, false, true, false, nullptr).lse.tile);
+    for (const int kind : {0, 1, 2, 3}) {
+        const Layout l = lay_out(T, K, V, io, true, kind & 1, kind & 2, nullptr);
         const int64_t longest = std::min(V, l.piece), last = (V - 1) % l.piece + 1;
         for (const int64_t nv : {longest, last})
             if (!fits(nv, T, tiling(nv, T, l.ldk / kBK * l.logits.n, false).tile)) return false;

@@ -243,6 +243,22 @@ def ssm_xent_bwd_workspace(tokens, dim, vocab, io=SSM_BF16) -> int:
     return int(load_library().ssm_xent_bwd_workspace(tokens, dim, vocab, io))
 
 
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def ssm_xent_fwd_workspace_for(hidden, weight) -> int:
+    """The bytes of ssm_xent_fwd's workspace for these tensors, at most ssm_xent_fwd_workspace's."""
+    return int(load_library().ssm_xent_fwd_workspace_for(_at(hidden), _at(weight), *hidden.shape, weight.shape[0],
+                                                         _kind(hidden)))
+
+
+def ssm_xent_bwd_workspace_for(hidden, weight, dloss=None) -> int:
+    """The bytes of ssm_xent_bwd's workspace for these tensors, at most ssm_xent_bwd_workspace's."""
+    return int(load_library().ssm_xent_bwd_workspace_for(_at(hidden), _at(weight), _at(dloss), *hidden.shape,
+                                                         weight.shape[0], _kind(hidden)))
+
+
 def _head(hidden, weight, targets):
     """The sizes, the io type, and the addresses of a head's inputs."""
     (T, K), V, io = hidden.shape, weight.shape[0], hidden.dtype
@@ -264,8 +280,8 @@ def ssm_xent_fwd(hidden, weight, targets, *, ignore_index=-100, loss=None, lse=N
     the logits in memory: loss [T], lse [T] and mean [2] (the mean over the tokens that are
     not ignored, and 1 over their number), all float32."""
     if workspace is None and hidden.is_cuda:
-        got = _table_module().xent_fwd(_entry("ssm_xent_fwd"), _entry("ssm_xent_fwd_workspace"), _stream(hidden), hidden,
-                                       weight, targets, ignore_index, loss, lse, mean)
+        got = _table_module().xent_fwd(_entry("ssm_xent_fwd"), _entry("ssm_xent_fwd_workspace_for"), _stream(hidden),
+                                       hidden, weight, targets, ignore_index, loss, lse, mean)
         if got is not None:
             return _made(got)
     lib = load_library()
@@ -274,7 +290,7 @@ def ssm_xent_fwd(hidden, weight, targets, *, ignore_index=-100, loss=None, lse=N
     loss = torch.empty(T, dtype=_f32, device=dev) if loss is None else loss
     lse = torch.empty(T, dtype=_f32, device=dev) if lse is None else lse
     mean = torch.empty(2, dtype=_f32, device=dev) if mean is None else mean
-    ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_xent_fwd_workspace(T, K, V, kind), dev)
+    ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_xent_fwd_workspace_for(*inputs[:2], T, K, V, kind), dev)
     _called(hidden, lib.ssm_xent_fwd, *inputs, ignore_index, _need(loss, "loss", (T,), _f32, dev),
             _need(lse, "lse", (T,), _f32, dev), _need(mean, "mean", (2,), _f32, dev), T, K, V, kind, ws_at, ws_bytes,
             written=(loss, lse, mean))
@@ -286,8 +302,8 @@ def ssm_xent_bwd(hidden, weight, targets, lse, mean, *, dloss=None, dmean=None, 
     """Gradients of sum(dloss loss) + dmean mean[0] (dloss [T] float32, dmean one float32 on
     the GPU; None = 0): dhidden [T, K] and dweight [V, K] (None where not wanted)."""
     if workspace is None and hidden.is_cuda:
-        got = _table_module().xent_bwd(_entry("ssm_xent_bwd"), _entry("ssm_xent_bwd_workspace"), _stream(hidden), hidden,
-                                       weight, targets, ignore_index, lse, mean, dloss, dmean, bool(want_dhidden),
+        got = _table_module().xent_bwd(_entry("ssm_xent_bwd"), _entry("ssm_xent_bwd_workspace_for"), _stream(hidden),
+                                       hidden, weight, targets, ignore_index, lse, mean, dloss, dmean, bool(want_dhidden),
                                        bool(want_dweight))
         if got is not None:
             return _made(got)
@@ -296,7 +312,7 @@ def ssm_xent_bwd(hidden, weight, targets, lse, mean, *, dloss=None, dmean=None, 
     dev = hidden.device
     dhidden = torch.empty_like(hidden) if want_dhidden else None
     dweight = torch.empty_like(weight) if want_dweight else None
-    ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_xent_bwd_workspace(T, K, V, kind), dev)
+    ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_xent_bwd_workspace_for(*inputs[:2], _at(dloss), T, K, V, kind), dev)
     _called(hidden, lib.ssm_xent_bwd, *inputs, ignore_index, _need(lse, "lse", (T,), _f32, dev),
             _need(mean, "mean", (2,), _f32, dev), _need(dloss, "dloss", (T,), _f32, dev), _one(dmean, "dmean", dev),
             None if dhidden is None else dhidden.data_ptr(), None if dweight is None else dweight.data_ptr(),
