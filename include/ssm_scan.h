@@ -591,8 +591,12 @@ ssm_status ssm_scan_fwd_mimo_profiled(const void *x, const void *dt, const float
  *   h0, h_final : [batch, d_inner] float32, NULL = zero / not wanted
  *   reset       : [batch, L] bytes, NULL = none. A non-zero byte marks the first step of a
  *                 document: h_{t-1} is taken as 0 there, so that nothing of an earlier
- *                 document, NaN and Inf included, reaches a later one, in the outputs or
- *                 in the gradients.
+ *                 document, NaN and Inf included, reaches a later one, in the outputs, or
+ *                 the other way in the gradients. A step without a reset lets both through
+ *                 (an infinity may become a NaN).
+ *                 The factor sqrt(1 - a_t^2) is the same at such a step as at any other.
+ *                 (Weights trained with 1 in its place at a document's first step need x_t
+ *                 divided by it there before the call.)
  *   states      : NULL, or what ssm_gated_bwd needs: the state entering every
  *                 SSM_GATED_STATE_EVERY-th step, [batch, ceil(L / SSM_GATED_STATE_EVERY),
  *                 d_inner] float32 (ssm_gated_states_bytes bytes).
@@ -656,7 +660,7 @@ ssm_status ssm_gated_step(float *h, const void *x_t, const void *r_t, const void
  * as two parts (bfloat16) or three (float32).
  * The workspace (256-byte aligned) holds one piece at a time: at most about 256 MB of dlogits
  * and, where weight has to be copied (float32, or bfloat16 rows that do not all start on 16 bytes
- * or are no multiple of 64 long), 256 MB of that copy; copies of hidden; and, with several pieces,
+ * or are no multiple of 64 long), 512 MB of that copy; copies of hidden; and, with several pieces,
  * dhidden in float32. ssm_xent_fwd_workspace / ssm_xent_bwd_workspace give the bytes that any call
  * of these sizes may need; the ones that end in _for those of the call with these pointers (what
  * counts is their alignment, and whether dloss is NULL), which may be far fewer. Sums run in a

@@ -841,8 +841,8 @@ struct Layout {
 // dhidden's partial sum is read and written once for each piece, so that more of them cost more
 // (2^26, 2^27 and 2^28 values: 7.32, 7.27 and 7.22 ms for 8192 x 4096 x 32000, 8.34, 8.05 and
 // 8.05 ms for 2000 x 4096 x 128000), and larger ones would begin to be the whole array. A copy of
-// weight, where there is one, is that of a piece too, and no larger.
-constexpr int64_t kPieceValues = (int64_t)1 << 27;
+// weight, where there is one, is that of a piece too, of 512 MB at most.
+constexpr int64_t kPieceValues = (int64_t)1 << 27, kCopyValues = (int64_t)1 << 28;
 
 // Tokens of a block that joins: whole lines of the partial pairs and few blocks where there are
 // many tokens, many threads for each where there are few.
@@ -857,12 +857,12 @@ Layout lay_out(int64_t T, int64_t K, int64_t V, int io, bool bwd, bool pack, boo
     l.ldk = up(K, kBK);
     l.rows_t = up(T, kBK);
     l.pack = pack;
-    const auto rows_of = [](int64_t numbers) { return std::max<int64_t>(1024, kPieceValues / numbers / kBig * kBig); };
-    l.piece = std::min(V, pack ? rows_of(l.ldk * l.parts) : V);
+    const auto rows_of = [](int64_t most, int64_t numbers) { return std::max<int64_t>(1024, most / numbers / kBig * kBig); };
+    l.piece = std::min(V, pack ? rows_of(kCopyValues, l.ldk * l.parts) : V);
     if (bwd) {
         l.parts_w = io ? (weighed ? 2 : 1) : kMostParts;
         l.parts_g = io ? (T <= kFewTokens ? 2 : 1) : kMostParts;
-        l.piece = std::min(l.piece, rows_of(l.rows_t * l.parts_g));
+        l.piece = std::min(l.piece, rows_of(kPieceValues, l.rows_t * l.parts_g));
     }
     l.hidden = a.take<uint16_t>(pack ? T * l.ldk * l.parts : 0);
     l.weight = a.take<uint16_t>(pack ? l.piece * l.ldk * l.parts : 0);

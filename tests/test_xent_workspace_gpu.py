@@ -43,10 +43,10 @@ def test_exact_size(T, K, V, shift, io, each):
         assert bitwise_equal(t, want[k]), k
 
 
-@pytest.mark.parametrize("T,K,V,io", [(90, 1000, 50001, F32), (20, 2000, 70001, BF16)])
+@pytest.mark.parametrize("T,K,V,io", [(90, 1000, 100001, F32), (20, 2000, 140001, BF16)])
 def test_copies_in_pieces(T, K, V, io):
     say("xent copies in pieces", T, K, V, io)
     hidden, weight, target = make(T, K, V, io, seed=5)
-    target[-3:] = torch.tensor([V - 1, V - 2, 43520])
+    target[-3:] = torch.tensor([V - 1, V - 2, 87040])
     ref = train_ref.xent(hidden, weight, target, dmean=1.0)
     check(hidden, weight, target, ref, call(hidden, weight, target, None, torch.ones((), device="cuda")), io, 1)

@@ -26,8 +26,8 @@ def test_bounds(T, K, V, io):
     # a piece of dlogits and one of weight's copy; two copies of hidden in up to three parts of 16 bits
     # (padded to 64); dhidden in float32; the partial sums of few tiles; pairs for every 64 logits
     piece, rows = 1 << 28, -(-T // 64) * 64 * -(-K // 64) * 64
-    most = 2 * piece + 2 * rows * 6 + T * K * 4 + (64 << 20) + 4096
-    assert bwd <= most and fwd <= piece + rows * 6 + T * V // 8 + 64 * T + 16 * V + 4096
+    most = 3 * piece + 2 * rows * 6 + T * K * 4 + (64 << 20) + 4096
+    assert bwd <= most and fwd <= 2 * piece + rows * 6 + T * V // 8 + 64 * T + 16 * V + 4096
     for at in (ALIGNED, ODD):
         for each in (False, True):
             f, b = needs(T, K, V, io, at, each)
