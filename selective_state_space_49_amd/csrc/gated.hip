@@ -17,7 +17,7 @@ namespace ssm {
 namespace {
 
 // 1 - a^2 = -expm1(-2k) with relative precision: its series below 2k = 1/4 (the first term
-// left out is below 5e-8 of the sum), 1 - a a above, where nothing cancels by more than a
+// left out is below 6e-8 of the sum), 1 - a a above, where nothing cancels by more than a
 // factor of 5.
 __device__ __forceinline__ float one_minus_a2(float k, float a) {
     const float x = k + k;
