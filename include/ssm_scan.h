@@ -660,8 +660,8 @@ ssm_status ssm_gated_step(float *h, const void *x_t, const void *r_t, const void
  * as two parts (bfloat16) or three (float32).
  * The workspace (256-byte aligned) holds one piece at a time: at most about 256 MB of dlogits
  * and, where weight has to be copied (float32, or bfloat16 rows that do not all start on 16 bytes
- * or are no multiple of 64 long), 512 MB of that copy; copies of hidden; and, with several pieces,
- * dhidden in float32. ssm_xent_fwd_workspace / ssm_xent_bwd_workspace give the bytes that any call
+ * or are no multiple of 64 long), 512 MB of that copy (but 1024 rows of the vocabulary at least);
+ * copies of hidden; and, with several pieces, dhidden in float32. ssm_xent_fwd_workspace / ssm_xent_bwd_workspace give the bytes that any call
  * of these sizes may need; the ones that end in _for those of the call with these pointers (what
  * counts is their alignment, and whether dloss is NULL), which may be far fewer. Sums run in a
  * fixed order. Outputs must not overlap inputs or each other. Alignment: targets 8 bytes, float32
