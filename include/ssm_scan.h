@@ -661,11 +661,12 @@ ssm_status ssm_gated_step(float *h, const void *x_t, const void *r_t, const void
  * The workspace (256-byte aligned) holds one piece at a time: at most about 256 MB of dlogits
  * and, where weight has to be copied (float32, or bfloat16 rows that do not all start on 16 bytes
  * or are no multiple of 64 long), 512 MB of that copy (but 1024 rows of the vocabulary at least);
- * copies of hidden; and, with several pieces, dhidden in float32. ssm_xent_fwd_workspace / ssm_xent_bwd_workspace give the bytes that any call
- * of these sizes may need; the ones that end in _for those of the call with these pointers (what
- * counts is their alignment, and whether dloss is NULL), which may be far fewer. Sums run in a
- * fixed order. Outputs must not overlap inputs or each other. Alignment: targets 8 bytes, float32
- * arrays 4 bytes, the others one element.
+ * copies of hidden; and, with several pieces, dhidden in float32. ssm_xent_fwd_workspace /
+ * ssm_xent_bwd_workspace give the bytes that any call of these sizes may need; the ones that end
+ * in _for those of the call with these pointers (what counts is their alignment, and whether
+ * dloss is NULL), which may be far fewer. Sums run in a fixed order. Outputs must not overlap
+ * inputs or each other. Alignment: targets 8 bytes, float32 arrays 4 bytes, the others one
+ * element.
  * tokens is below 2^29, vocab at most 2^30, dim at most 2^22, and a product's tiles are those of
  * one launch (for the forward 2^23 of 256 x 256, 5.5e11 logits): SSM_ERR_SHAPE otherwise.
  * tokens == 0 gives mean = 0 and dweight = 0. */
