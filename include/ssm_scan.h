@@ -737,6 +737,130 @@ ssm_status ssm_adamw_values(const int8_t *exp_avg, const uint8_t *exp_avg_sq,
                             const float *avg_scale, const float *avg_sq_scale, float *avg_out,
                             float *avg_sq_out, int64_t n, void *hip_stream);
 
+/* ------------------------------------------------------------------ linear attention
+ * A recurrence with a matrix state for each head h, whose decay is one number for a token and head
+ * (or for a head):
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,        o_t = scale q_t^T S_t      (S [d_k, d_v])
+ *   q, k       : [batch, L, groups, d_k] of io. Head h reads group h / (heads / groups).
+ *   v, o       : [batch, L, heads, d_v] of io
+ *   log_decay  : g, float32: [batch, L, heads] where per_token is not 0, else [heads]. Below -104,
+ *                -infinity included, exp(g) is 0 in float32 and the step is a cut, the start of a
+ *                document: nothing of an earlier step's state reaches it or what follows, and the
+ *                gradient of its g is 0. A NaN makes NaN. A g above 0 (growth) is taken as it is.
+ *   h0, h_final: [batch, heads, d_k, d_v] float32, NULL = zero / not wanted
+ *   states     : NULL, or what ssm_linattn_bwd needs: the state that enters every chunk
+ *                (SSM_LINATTN_CHUNK_BF16 or _F32 steps), [batch, heads, ceil(L / chunk), d_k, d_v]
+ *                float32 (ssm_linattn_states_bytes bytes).
+ * A head of more than 128 columns of v is two heads that read the same group.
+ * Products are made a chunk at a time on the matrix cores and summed in float32; sums of g in
+ * 64 bits. float32 inputs are multiplied in float32. Of bfloat16 ones, the chunk's scores and, where
+ * it makes an output of bfloat16, the state enter a product rounded to bfloat16 (relative 2^-9 each,
+ * like the output's own rounding); factors of a float32 result (states, dlog_decay) keep 24 bits.
+ * q, k, v (and d_o, states) must be finite: what is not, in a token, can reach the outputs of all
+ * of its chunk, and with its state all that follows until a cut in a later chunk; never another
+ * sequence or head (in the gradients, the heads of a group).
+ * ssm_linattn_bwd gives the gradients of sum(d_o o) + sum(dh_final h_final): dq, dk, dv of io,
+ * dlog_decay (float32, in log_decay's shape), dh0 [batch, heads, d_k, d_v] float32 (NULL = not
+ * wanted; dh_final NULL = 0). It reads q, k, v, log_decay and scale as the forward had them, and its
+ * states. Gradients of a shared group, and of a [heads] decay, are sums in a fixed order: equal calls
+ * give equal bits.
+ * workspace: at least ssm_linattn_fwd_workspace(...) / ssm_linattn_bwd_workspace(...) bytes, 256-byte
+ * aligned (0 is possible, then it may be NULL); its contents on entry are ignored. Outputs must not
+ * overlap inputs or each other (SSM_ERR_UNSUPPORTED). Alignment: float32 arrays 4 bytes, the others
+ * one element (rows that start on 16 bytes are read fastest). d_k and d_v are 1 to 128, heads a
+ * multiple of groups, batch x heads at most 2^20. L == 0 writes h_final = h0 (dh0 = dh_final, and 0
+ * for a [heads] decay). */
+#define SSM_LINATTN_CHUNK_BF16 64
+#define SSM_LINATTN_CHUNK_F32 32
+size_t ssm_linattn_states_bytes(int64_t batch, int64_t L, int32_t heads, int32_t d_k, int32_t d_v,
+                                ssm_dtype io);
+size_t ssm_linattn_fwd_workspace(int64_t batch, int64_t L, int32_t heads, int32_t groups,
+                                 int32_t d_k, int32_t d_v, ssm_dtype io);
+size_t ssm_linattn_bwd_workspace(int64_t batch, int64_t L, int32_t heads, int32_t groups,
+                                 int32_t d_k, int32_t d_v, int32_t per_token, ssm_dtype io);
+ssm_status ssm_linattn_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                           int32_t per_token, const float *h0, float scale, void *o,
+                           float *h_final, float *states, int64_t batch, int64_t L,
+                           int32_t heads, int32_t groups, int32_t d_k, int32_t d_v, ssm_dtype io,
+                           void *workspace, size_t workspace_bytes, void *hip_stream);
+ssm_status ssm_linattn_bwd(const void *q, const void *k, const void *v, const float *log_decay,
+                           int32_t per_token, const float *states, const void *d_o,
+                           const float *dh_final, float scale, void *dq, void *dk, void *dv,
+                           float *dlog_decay, float *dh0, int64_t batch, int64_t L,
+                           int32_t heads, int32_t groups, int32_t d_k, int32_t d_v, ssm_dtype io,
+                           void *workspace, size_t workspace_bytes, void *hip_stream);
+/* One token for every (layer, sequence): h [n_layers, n_seq, heads, d_k, d_v] float32 in place; q_t,
+ * k_t [n_layers, n_seq, groups, d_k], v_t, o_t [n_layers, n_seq, heads, d_v] of io; log_decay
+ * [n_layers, n_seq, heads] where per_token is not 0, else [n_layers, heads]. All in float32; o_t is
+ * rounded once. n_layers x n_seq x heads is at most 2^20. */
+ssm_status ssm_linattn_step(float *h, const void *q_t, const void *k_t, const void *v_t,
+                            const float *log_decay, int32_t per_token, float scale, void *o_t,
+                            int64_t n_layers, int64_t n_seq, int32_t heads, int32_t groups,
+                            int32_t d_k, int32_t d_v, ssm_dtype io, void *hip_stream);
+
+/* ------------------------------------------------------------------ RMS norm
+ * The norm of a row, after the residual's addition:
+ *     s = x + residual, rounded to res_io (s = x where residual is NULL, then res_io must be io)
+ *     r = 1 / sqrt(mean(s^2) + eps),      y = s r weight
+ *   x, y         : [rows, dim] of io
+ *   residual, residual_out (s) : [rows, dim] of res_io, both NULL or both given; residual_out may be
+ *                  residual itself. res_io is io, or float32 beside a bfloat16 x.
+ *   weight       : [dim] float32
+ *   rstd         : [rows] float32 (r), NULL = not wanted
+ * The mean is held in 64 bits, y is made in float32 and rounded once.
+ * ssm_rmsnorm_fwd_q8 writes y as codes of 8 bits [rows, dim]: SSM_E4M3 (4 bits of exponent, 3 of
+ * mantissa, largest value 448) or SSM_INT8 (-127 to 127), with a float32 scale for every `group`
+ * values of a row (32, 64 or 128; the last may be shorter) or for the row (group 0):
+ *     scale = max |y| / 448 (or 127),    code = the nearest to y / scale, ties to even
+ * scales: [rows, ceil(dim / group)] or [rows, 1]. y and its quotients are made in 64 bits. Where a
+ * group holds a NaN or an infinity its scale is one, so its values are NaN or infinite; where all of
+ * it is 0, so are scale and codes. ssm_q8_values gives the float32 values code * scale.
+ * ssm_rmsnorm_bwd gives the gradients of sum(dy y) + sum(ds s), with n = s r:
+ *     d = r (weight dy - n mean(weight dy n)) + ds,    dweight = sum over rows of dy n
+ * dx is d in io, dresidual d in res_io (NULL = not wanted), dweight [dim] float32; s is what the
+ * forward wrote (x where it had no residual; then res_io is io), ds NULL = 0. dweight is summed in a
+ * fixed order. workspace: ssm_rmsnorm_bwd_workspace bytes, 256-byte aligned.
+ * Apart from residual_out, outputs must not overlap inputs or each other. Alignment: float32 arrays 4
+ * bytes, the others one element. rows is at most 2^22, dim 1 to 65536. */
+typedef enum { SSM_E4M3 = 1, SSM_INT8 = 2 } ssm_code;
+ssm_status ssm_rmsnorm_fwd(const void *x, const void *residual, const float *weight, double eps,
+                           void *y, void *residual_out, float *rstd, int64_t rows, int32_t dim,
+                           ssm_dtype io, ssm_dtype res_io, void *hip_stream);
+ssm_status ssm_rmsnorm_fwd_q8(const void *x, const void *residual, const float *weight,
+                              double eps, void *codes, float *scales, ssm_code code,
+                              int32_t group, void *residual_out, int64_t rows, int32_t dim,
+                              ssm_dtype io, ssm_dtype res_io, void *hip_stream);
+ssm_status ssm_q8_values(const void *codes, const float *scales, ssm_code code, int32_t group,
+                         float *out, int64_t rows, int32_t dim, void *hip_stream);
+size_t ssm_rmsnorm_bwd_workspace(int64_t rows, int32_t dim);
+ssm_status ssm_rmsnorm_bwd(const void *dy, const void *s, const void *ds, const float *weight,
+                           const float *rstd, void *dx, void *dresidual, float *dweight,
+                           int64_t rows, int32_t dim, ssm_dtype io, ssm_dtype res_io,
+                           void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/* ------------------------------------------------------------------ sampling
+ * The next token of every row from its logits [rows, vocab] of io and one number u of [0, 1) a row:
+ *     w_i = exp((logit_i - max) / temperature)
+ *     in the order of falling logits, equal ones by index: the first top_k are kept (0 or less:
+ *     all); of these the ones before which less than top_p of their mass lies (1 or more: all; the
+ *     first always stays); of these the ones with w >= min_p (0: all; above 1 is 1);
+ *     the token is the first index at which the sum of the kept w up to it exceeds u times all.
+ * temperature, top_p, min_p float32 and top_k int32 [rows], or NULL: the value that ends in _all for
+ * every row. A temperature of 0 takes the first of the largest logits. tokens [rows] int64; logprob
+ * [rows] float32 (NULL = not wanted): the logarithm of the token's share of the kept mass.
+ * Masses are whole multiples of 2^-46 (vocab up to 2^16; one bit less for each doubling) from
+ * exponentials in 64 bits: sums do not depend on an order, and a token of less has no mass.
+ * A logit of -infinity is never drawn; beside one of +infinity only such ones are. A row without a
+ * finite logit or +infinity, with a NaN among its logits, or with a temperature or u that is NaN or a
+ * negative temperature, gives token -1 and a NaN. A u below 0 draws the first kept token, one of 1
+ * and more the last. rows is at most 65535, vocab 2^24. */
+size_t ssm_sample_workspace(int64_t rows, int64_t vocab);
+ssm_status ssm_sample(const void *logits, const float *u, const float *temperature,
+                      float temperature_all, const int32_t *top_k, int32_t top_k_all,
+                      const float *top_p, float top_p_all, const float *min_p, float min_p_all,
+                      int64_t *tokens, float *logprob, int64_t rows, int64_t vocab, ssm_dtype io,
+                      void *workspace, size_t workspace_bytes, void *hip_stream);
+
 /* ------------------------------------------------------------------ misc */
 const char *ssm_status_str(ssm_status s);   /* static string, never NULL */
 const char *ssm_last_error(void);           /* this thread's last detail, "" if none */

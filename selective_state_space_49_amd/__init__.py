@@ -38,6 +38,12 @@ __all__ = [
     "ssm_xent_fwd", "ssm_xent_bwd", "ssm_xent_fwd_workspace", "ssm_xent_bwd_workspace",
     "ssm_xent_fwd_workspace_for", "ssm_xent_bwd_workspace_for", "linear_cross_entropy",
     "ssm_adamw_step", "ssm_adamw_values", "ssm_adamw_state_size", "ADAMW_BLOCK", "AdamW",
+    "ssm_linattn_fwd", "ssm_linattn_fwd_save", "ssm_linattn_bwd", "ssm_linattn_step",
+    "ssm_linattn_fwd_workspace", "ssm_linattn_bwd_workspace", "ssm_linattn_states_bytes",
+    "linear_attention", "LINATTN_CHUNK",
+    "ssm_rmsnorm_fwd", "ssm_rmsnorm_fwd_q8", "ssm_q8_values", "ssm_rmsnorm_bwd",
+    "ssm_rmsnorm_bwd_workspace", "rms_norm",
+    "ssm_sample", "ssm_sample_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -66,6 +72,10 @@ EXPORTED_SYMBOLS = [
     "ssm_xent_fwd", "ssm_xent_bwd", "ssm_xent_fwd_workspace", "ssm_xent_bwd_workspace",
     "ssm_xent_fwd_workspace_for", "ssm_xent_bwd_workspace_for",
     "ssm_adamw_step", "ssm_adamw_values", "ssm_adamw_state_size",
+    "ssm_linattn_fwd", "ssm_linattn_bwd", "ssm_linattn_step", "ssm_linattn_fwd_workspace",
+    "ssm_linattn_bwd_workspace", "ssm_linattn_states_bytes",
+    "ssm_rmsnorm_fwd", "ssm_rmsnorm_fwd_q8", "ssm_q8_values", "ssm_rmsnorm_bwd",
+    "ssm_rmsnorm_bwd_workspace", "ssm_sample", "ssm_sample_workspace",
 ]
 # Steps between the states ssm_scan_fwd_save stores for ssm_scan_bwd_saved.
 STATE_EVERY = 8
@@ -160,6 +170,20 @@ def load_library():
     sig["ssm_adamw_state_size"] = ([i32, vp], i64)
     sig["ssm_adamw_step"] = ([i32] + [vp] * 10 + [f64] * 5 + [i64, vp], ci)
     sig["ssm_adamw_values"] = ([vp] * 6 + [i64, vp], ci)
+    sig["ssm_linattn_states_bytes"] = ([i64, i64, i32, i32, i32, ci], sz)
+    sig["ssm_linattn_fwd_workspace"] = ([i64, i64, i32, i32, i32, i32, ci], sz)
+    sig["ssm_linattn_bwd_workspace"] = ([i64, i64, i32, i32, i32, i32, i32, ci], sz)
+    heads = [i64, i64, i32, i32, i32, i32, ci]
+    sig["ssm_linattn_fwd"] = ([vp] * 4 + [i32, vp, f32] + [vp] * 3 + heads + [vp, sz, vp], ci)
+    sig["ssm_linattn_bwd"] = ([vp] * 4 + [i32] + [vp] * 3 + [f32] + [vp] * 5 + heads + [vp, sz, vp], ci)
+    sig["ssm_linattn_step"] = ([vp] * 5 + [i32, f32, vp] + heads + [vp], ci)
+    sig["ssm_rmsnorm_fwd"] = ([vp] * 3 + [f64] + [vp] * 3 + [i64, i32, ci, ci, vp], ci)
+    sig["ssm_rmsnorm_fwd_q8"] = ([vp] * 3 + [f64, vp, vp, ci, i32, vp, i64, i32, ci, ci, vp], ci)
+    sig["ssm_q8_values"] = ([vp, vp, ci, i32, vp, i64, i32, vp], ci)
+    sig["ssm_rmsnorm_bwd_workspace"] = ([i64, i32], sz)
+    sig["ssm_rmsnorm_bwd"] = ([vp] * 8 + [i64, i32, ci, ci, vp, sz, vp], ci)
+    sig["ssm_sample_workspace"] = ([i64, i64], sz)
+    sig["ssm_sample"] = ([vp] * 3 + [f32, vp, i32, vp, f32, vp, f32, vp, vp, i64, i64, ci, vp, sz, vp], ci)
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
         f.argtypes, f.restype = args, res
@@ -965,3 +989,9 @@ from .training import (  # noqa: E402  (the training operators use the helpers a
     ssm_gated_fwd_save, ssm_gated_fwd_workspace, ssm_gated_states_bytes, ssm_gated_step,
     ssm_xent_bwd, ssm_xent_bwd_workspace, ssm_xent_bwd_workspace_for, ssm_xent_fwd,
     ssm_xent_fwd_workspace, ssm_xent_fwd_workspace_for)
+
+from .layers import (  # noqa: E402
+    LINATTN_CHUNK, linear_attention, rms_norm, ssm_linattn_bwd, ssm_linattn_bwd_workspace,
+    ssm_linattn_fwd, ssm_linattn_fwd_save, ssm_linattn_fwd_workspace, ssm_linattn_states_bytes,
+    ssm_linattn_step, ssm_q8_values, ssm_rmsnorm_bwd, ssm_rmsnorm_bwd_workspace, ssm_rmsnorm_fwd,
+    ssm_rmsnorm_fwd_q8, ssm_sample, ssm_sample_workspace)

@@ -26,8 +26,9 @@ OBJDIR = os.path.join(HERE, "_build")
 
 ARCH = "gfx950"
 HIP_SOURCES = ["scan_real.hip", "scan_complex.hip", "step.hip", "scan_bwd.hip", "scan_mimo.hip",
-               "input_bwd.hip", "scratch.hip", "gated.hip", "xent.hip", "adamw.hip"]
-CPP_SOURCES = ["api.cpp", "api_train.cpp"]
+               "input_bwd.hip", "scratch.hip", "gated.hip", "xent.hip", "adamw.hip",
+               "linattn.hip", "rmsnorm.hip", "sample.hip"]
+CPP_SOURCES = ["api.cpp", "api_train.cpp", "api_layers.cpp"]
 COMMON = ["-O3", "-fPIC", "-std=c++17", f"-I{INCLUDE}", f"-I{CSRC}"]
 DEVICE = [f"--offload-arch={ARCH}", "-ffp-contract=off",
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

@@ -1,0 +1,1044 @@
+// linattn.hip -- linear attention with a decay for each head: a state S [K, V] for every sequence
+// and head,
+//     S_t = exp(g_t) S_{t-1} + k_t v_t^T,    o_t = scale q_t^T S_t.
+//
+// In chunks of C tokens, with G the sums of g from the chunk's start (inclusive):
+//     o_i   = scale (e^{G_i} q_i S_in + sum_{j <= i} (q_i.k_j) e^{G_i - G_j} v_j)
+//     S_out = e^{G_C} S_in + sum_j e^{G_C - G_j} k_j v_j^T.
+// The gradients, with dS_out the gradient of what leaves the chunk (do times scale throughout):
+//     dq_i  = e^{G_i} S_in do_i + sum_{j <= i} (do_i.v_j) e^{G_i - G_j} k_j
+//     dk_j  = e^{G_C - G_j} dS_out v_j + sum_{i >= j} (do_i.v_j) e^{G_i - G_j} q_i
+//     dv_j  = e^{G_C - G_j} dS_out^T k_j + sum_{i >= j} (q_i.k_j) e^{G_i - G_j} do_i
+//     dS_in = e^{G_C} dS_out + sum_i e^{G_i} q_i do_i^T
+//     dg_t  = <what passes from before t to t and after>
+//           = sum_{j < t <= i} (q_i.k_j)(do_i.v_j) e^{G_i - G_j} + sum_{i >= t} e^{G_i} q_i S_in do_i
+//             + sum_{j < t} e^{G_C - G_j} k_j dS_out v_j + e^{G_C} <S_in, dS_out>,
+// a sum without a difference, so that dg keeps its precision where a decay is strong. A g below
+// kCut (exp(g) is 0 in float32) is a cut: decays across it are 0 by a comparison of document
+// numbers, and its g does not enter G. G is a sum in 64 bits.
+//
+// Everything is a product on the matrix cores: v_mfma_f32_32x32x16_bf16 for bfloat16 inputs, and
+// v_mfma_f32_32x32x2_f32 for float32 ones. The state stays in a wave's accumulators for a whole
+// sweep (all of K for 32 columns of V) and is an operand from there: lane l holds column l % 32 and
+// of each 8 rows the 4 of its half, and the other operand is read in the same order of the
+// contraction ("quads": 4 consecutive elements at 8 a + 4 (l / 32)).
+// bfloat16: scores, and the state where it makes an output of bfloat16, are rounded to bfloat16
+// (2^-9 each, as the output is). What goes into a float32 result (states, dg) takes factors in three
+// bfloat16 parts, which hold 24 bits.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ssm_layers.h"
+
+namespace ssm {
+namespace {
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+#define SSM_LDS __attribute__((address_space(3)))
+
+constexpr float kCut = -104.0f;  // exp of less is 0 in float32
+constexpr double kLog2e = 1.4426950408889634;
+
+// What depends on the inputs' type: tokens of a chunk (C), the contraction of a step (KS), a
+// fragment (this lane's elements of a step), and the parts that hold a float32 factor.
+template <typename T> struct Kind;
+template <> struct Kind<__bf16> {
+    static constexpr int C = 64, KS = 16, kParts = 3;
+    typedef bf16x8 Frag;
+    typedef f32x8 Wide;
+    typedef u32x2 Quad;
+};
+template <> struct Kind<float> {
+    static constexpr int C = 32, KS = 8, kParts = 1;
+    typedef f32x4 Frag;
+    typedef f32x4 Wide;
+    typedef f32x4 Quad;
+};
+
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma(f32x4 a, f32x4 b, f32x16 c) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
+    return c;
+}
+
+// x rounded to the operand's type, and x as the sum of kParts of them.
+__device__ __forceinline__ bf16x8 rounded(f32x8 x) { return __builtin_convertvector(x, bf16x8); }
+__device__ __forceinline__ f32x4 rounded(f32x4 x) { return x; }
+__device__ __forceinline__ void split(f32x8 x, bf16x8 (&p)[3]) {
+    p[0] = __builtin_convertvector(x, bf16x8);
+    x -= __builtin_convertvector(p[0], f32x8);
+    p[1] = __builtin_convertvector(x, bf16x8);
+    x -= __builtin_convertvector(p[1], f32x8);
+    p[2] = __builtin_convertvector(x, bf16x8);
+}
+__device__ __forceinline__ void split(f32x4 x, f32x4 (&p)[1]) { p[0] = x; }
+__device__ __forceinline__ f32x8 widened(bf16x8 x) { return __builtin_convertvector(x, f32x8); }
+__device__ __forceinline__ f32x4 widened(f32x4 x) { return x; }
+
+// Step s of an accumulator's 32 rows as a fragment's elements.
+template <typename T>
+__device__ __forceinline__ typename Kind<T>::Wide rows_of(const f32x16 &acc, int s) {
+    typename Kind<T>::Wide w;
+    constexpr int N = sizeof(w) / 4;
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = acc[s * N + e];
+    return w;
+}
+// The weights of a fragment's tokens (step s of a float array in LDS).
+__device__ __forceinline__ void weights_of(const float *w, int s, int half, f32x8 &out) {
+    const f32x4 lo = *(const f32x4 *)(w + 16 * s + 4 * half), hi = *(const f32x4 *)(w + 16 * s + 8 + 4 * half);
+    out = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+__device__ __forceinline__ void weights_of(const float *w, int s, int half, f32x4 &out) {
+    out = *(const f32x4 *)(w + 8 * s + 4 * half);
+}
+
+// ROWS x F elements in LDS, in quads of 4 whose places in a row are permuted (by exclusive or) so that
+// both ways of reading meet no bank twice: a quad of 32 rows (fragments whose lanes are rows), and
+// 4 rows of 32 neighbouring columns (fragments whose lanes are columns).
+template <typename T, int ROWS, int F>
+struct Tile {
+    typedef Kind<T> N;
+    static constexpr int W = F / 4, kBytes = ROWS * F * (int)sizeof(T);
+    static __device__ __forceinline__ int swizzle(int r) {
+        if constexpr (sizeof(T) == 2) {
+            if constexpr (W == 32) return (r & 3) << 3 | (r >> 2 & 7);
+            else return (r >> 1 & 1) << 3 | (r >> 2 & 7);  // W = 16
+        } else {
+            if constexpr (W == 8) return r >> 1 & 7;
+            else return (r & 3) | (r >> 2 & 1) << 3 | (r >> 3 & 1) << 2 | (W == 32 ? (r >> 4 & 1) << 4 : 0);
+        }
+    }
+    static __device__ __forceinline__ int at(int row, int quad) {
+        return (row * W + (quad ^ swizzle(row))) * 4 * (int)sizeof(T);
+    }
+    // lanes: rows; contraction: columns KS s .. KS s + KS - 1
+    static __device__ __forceinline__ typename N::Frag by_row(const char *t, int row, int s, int half) {
+        if constexpr (sizeof(T) == 2) {
+            const bf16x4 lo = *(const bf16x4 *)(t + at(row, 4 * s + half)), hi = *(const bf16x4 *)(t + at(row, 4 * s + 2 + half));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            return *(const f32x4 *)(t + at(row, 2 * s + half));
+        }
+    }
+    // lanes: columns 32 block + l % 32; contraction: rows KS s .. KS s + KS - 1
+    static __device__ __forceinline__ typename N::Frag by_column(const char *t, int block, int s, int lane) {
+        const int half = lane >> 5;
+        if constexpr (sizeof(T) == 2) {
+            const int i = lane & 15, row = 16 * s + 4 * half + (i >> 2), quad = 8 * block + (lane >> 4 & 1) * 4 + (i & 3);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)(t + at(row, quad)));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)(t + at(row + 8, quad)));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            f32x4 f;
+            const int c = lane & 31;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                f[e] = *(const float *)(t + at(8 * s + 4 * half + e, 8 * block + (c >> 2)) + (c & 3) * 4);
+            return f;
+        }
+    }
+    // One quad of a row, from four float32 values.
+    static __device__ __forceinline__ void put(char *t, int row, int quad, f32x4 x) {
+        if constexpr (sizeof(T) == 2) *(bf16x4 *)(t + at(row, quad)) = __builtin_convertvector(x, bf16x4);
+        else *(f32x4 *)(t + at(row, quad)) = x;
+    }
+};
+
+// A tile's way from global memory to LDS through registers: rows of `width` elements, `stride`
+// apart; rows past `rows` and columns past `width` become 0.
+template <typename T, int ROWS, int F, int THREADS>
+struct Stage {
+    static constexpr int kElems = 16 / sizeof(T), kPerRow = F / kElems, N = (ROWS * kPerRow + THREADS - 1) / THREADS;
+    static constexpr bool kWhole = ROWS * kPerRow % THREADS == 0;
+    u32x4 r[N];
+    __device__ __forceinline__ void load(const T *p, int64_t stride, int rows, int width, bool wide) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int e = threadIdx.x + n * THREADS, row = e / kPerRow, c = e % kPerRow * kElems;
+            const T *from = p + row * stride + c;
+            u32x4 got = {0, 0, 0, 0};
+            if (row < rows && c < width) {  // rows <= ROWS
+                if (wide) {
+                    got = *(const u32x4 *)from;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kElems; ++k)
+                        if (c + k < width) {
+                            if constexpr (sizeof(T) == 2) got[k / 2] |= (uint32_t)((const uint16_t *)from)[k] << (k % 2 * 16);
+                            else got[k] = ((const uint32_t *)from)[k];
+                        }
+                }
+            }
+            r[n] = got;
+        }
+    }
+    __device__ __forceinline__ void store(char *t) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int e = threadIdx.x + n * THREADS, row = e / kPerRow, c = e % kPerRow;
+            if (!kWhole && row >= ROWS) break;
+            if constexpr (sizeof(T) == 2) {
+                *(u32x2 *)(t + Tile<T, ROWS, F>::at(row, 2 * c)) = u32x2{r[n][0], r[n][1]};
+                *(u32x2 *)(t + Tile<T, ROWS, F>::at(row, 2 * c + 1)) = u32x2{r[n][2], r[n][3]};
+            } else {
+                *(u32x4 *)(t + Tile<T, ROWS, F>::at(row, c)) = r[n];
+            }
+        }
+    }
+};
+
+// The decays of a chunk, made by one wave: G in units of log 2, document numbers, and the decays
+// from the start to a token, from a token to the end, and over all of it.
+template <int C>
+struct Decays {
+    double G[C];
+    float start[C], end[C];
+    int doc[C];
+    float whole;
+
+    __device__ __forceinline__ void make(float g, int lane) {
+        const bool cut = g < kCut;
+        double sum = cut ? 0.0 : (double)g * kLog2e;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const double up = __shfl_up(sum, d);
+            if (lane >= d) sum += up;
+        }
+        const uint64_t cuts = __ballot(cut);
+        const uint64_t upto = cuts & (~0ull >> (63 - lane));
+        const double all = __shfl(sum, C - 1);
+        if (lane < C) {
+            G[lane] = sum;
+            doc[lane] = __popcll(upto);
+            start[lane] = upto ? 0.0f : __builtin_amdgcn_exp2f((float)sum);
+            end[lane] = upto == cuts ? __builtin_amdgcn_exp2f((float)(all - sum)) : 0.0f;
+            if (lane == 0) whole = cuts ? 0.0f : __builtin_amdgcn_exp2f((float)all);
+        }
+    }
+    // the decay from token j to token i, 0 for j > i and across a cut
+    __device__ __forceinline__ float between(double Gi, int di, double Gj, int dj, bool causal) const {
+        return causal && di == dj ? __builtin_amdgcn_exp2f((float)(Gi - Gj)) : 0.0f;
+    }
+};
+
+// b, head and piece of a block. Blocks of one XCD (every eighth) take neighbouring work, which
+// shares q and k: heads of a group and slices of V.
+__device__ __forceinline__ uint32_t work_of_block() {
+    const uint32_t n = gridDim.x, id = blockIdx.x, x = id % 8, per = n / 8, rem = n % 8;
+    return x * per + min(x, rem) + id / 8;
+}
+
+struct SweepArgs {
+    const void *q, *k, *v;
+    const float *g, *first;   // first: the entering state of every sequence (null: 0)
+    const float *seg_in;      // the entering state of every segment, or null
+    float *seg_out, *seg_fac;  // the state pass: what a segment adds, and its decay
+    void *o;
+    float *last, *states;
+    int64_t L, g_batch, g_token;  // strides of g (0, 0 for [H])
+    int32_t H, Hk, K, V, nseg, nchunk, per_seg, slices;
+    float scale;
+    bool wide_k, wide_v, wide_o;
+    bool reverse;             // the state pass runs from the end, with weights scale e^{G_i}
+};
+
+template <int TILES>
+__device__ __forceinline__ void state_load(f32x16 (&S)[TILES], const float *p, int K, int V, int v, int half) {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int k = t * 32 + 8 * (r / 4) + 4 * half + r % 4;
+            S[t][r] = p && k < K && v < V ? p[(int64_t)k * V + v] : 0.0f;
+        }
+}
+template <int TILES>
+__device__ __forceinline__ void state_store(const f32x16 (&S)[TILES], float *p, int K, int V, int v, int half) {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int k = t * 32 + 8 * (r / 4) + 4 * half + r % 4;
+            if (k < K && v < V) p[(int64_t)k * V + v] = S[t][r];
+        }
+}
+
+// S = whole S + sum over the chunk's tokens of w_j k_j v_j^T: k by columns of its tile, the wave's v
+// fragments weighed in float32 and split.
+template <typename T, int C, int KP, int TILES>
+__device__ __forceinline__ void state_add(f32x16 (&S)[TILES], const char *k_tile, const typename Kind<T>::Frag *v,
+                                          const float *w, float whole, int lane) {
+    typedef Kind<T> N;
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[t][r] = whole == 0.0f ? 0.0f : S[t][r] * whole;
+#pragma unroll
+    for (int s = 0; s < C / N::KS; ++s) {
+        typename N::Wide wv;
+        weights_of(w, s, lane >> 5, wv);
+        typename N::Frag part[N::kParts];
+        split(widened(v[s]) * wv, part);
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            const typename N::Frag a = Tile<T, C, KP>::by_column(k_tile, t, s, lane);
+#pragma unroll
+            for (int p = 0; p < N::kParts; ++p) S[t] = mfma(a, part[p], S[t]);
+        }
+    }
+}
+
+// Four values of a row of the output, at elements e .. e + 3 of `width`.
+template <typename T>
+__device__ __forceinline__ void put_row(T *row, int e, int width, bool wide, f32x4 x) {
+    if (wide) {
+        if (e < width) {
+            if constexpr (sizeof(T) == 2) *(bf16x4 *)(row + e) = __builtin_convertvector(x, bf16x4);
+            else *(f32x4 *)(row + e) = x;
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (e + k < width) row[e + k] = (T)x[k];
+    }
+}
+
+// One sweep over a segment of a sequence's chunks for NW x 32 columns of one head's state. OUT: with
+// outputs, from the segment's entering state; else what the segment adds to the state, from 0.
+template <typename T, int KP, int NW, bool OUT>
+__global__ void __launch_bounds__(64 * NW) k_sweep(SweepArgs p) {
+    typedef Kind<T> N;
+    typedef typename N::Frag Frag;
+    constexpr int C = N::C, KS = N::KS, VT = 32 * NW, TT = C / 32, KT = KP / 32, THREADS = 64 * NW;
+    typedef Tile<T, C, KP> TK;
+    typedef Tile<T, C, VT> TV;
+    typedef Tile<T, C, C> TP;
+    __shared__ __attribute__((aligned(256))) char lds[(OUT ? 2 : 1) * TK::kBytes + TV::kBytes + (OUT ? TP::kBytes : 0)];
+    __shared__ Decays<C> dec;
+    char *const kt = lds, *const vt = lds + TK::kBytes, *const qt = vt + TV::kBytes, *const pt = qt + TK::kBytes;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, l31 = lane & 31;
+    uint32_t work = work_of_block();
+    const int slice = work % p.slices;
+    work /= p.slices;
+    const int share = p.H / p.Hk, sub = work % share;
+    work /= share;
+    int seg = work % p.nseg;
+    work /= p.nseg;
+    if (!OUT && p.reverse) seg += 1;  // a pass covers all segments but the one that nothing follows
+    const int hk = work % p.Hk, h = hk * share + sub;
+    const int64_t b = work / p.Hk, bh = b * p.H + h;
+    const int c0 = seg * p.per_seg, c1 = min(c0 + p.per_seg, p.nchunk), n = c1 - c0;
+    const int v0 = slice * VT, vcol = v0 + wave * 32 + l31;
+    const int64_t KV = (int64_t)p.K * p.V;
+    const int nseg_all = OUT ? p.nseg : p.nseg + 1;
+
+    f32x16 S[KT];
+    {
+        const float *from = nullptr;
+        if (OUT) from = p.seg_in ? p.seg_in + (bh * nseg_all + seg) * KV : p.first ? p.first + bh * KV : nullptr;
+        state_load<KT>(S, from, p.K, p.V, vcol, half);
+    }
+    Stage<T, C, KP, THREADS> kr, qr;
+    Stage<T, C, VT, THREADS> vr;
+    float g = 0.0f;
+    const int64_t ks = (int64_t)p.Hk * p.K, vs = (int64_t)p.H * p.V;
+    auto fetch = [&](int c) {
+        const int64_t t0 = (int64_t)c * C;
+        const int rows = (int)min((int64_t)C, p.L - t0);
+        const int64_t at = b * p.L + t0;
+        kr.load((const T *)p.k + at * ks + (int64_t)hk * p.K, ks, rows, p.K, p.wide_k);
+        vr.load((const T *)p.v + at * vs + (int64_t)h * p.V + v0, vs, rows, p.V - v0, p.wide_v);
+        if (OUT) qr.load((const T *)p.q + at * ks + (int64_t)hk * p.K, ks, rows, p.K, p.wide_k);
+        if (wave == 0) g = lane < rows ? p.g[b * p.g_batch + (t0 + lane) * p.g_token + h] : 0.0f;
+    };
+    const bool rev = !OUT && p.reverse;
+    if (n > 0) fetch(rev ? c1 - 1 : c0);
+    double decayed = 0.0;  // the sum of G over the segment, in units of log 2
+    bool cut = false;
+    for (int it = 0; it < n; ++it) {
+        const int c = rev ? c1 - 1 - it : c0 + it;
+        kr.store(kt);
+        vr.store(vt);
+        if (OUT) qr.store(qt);
+        if (wave == 0) {
+            dec.make(g, lane);
+            if (rev && lane < C) dec.start[lane] *= p.scale;
+        }
+        __syncthreads();
+        if (it + 1 < n) fetch(rev ? c - 1 : c + 1);
+        if (OUT) {
+            if (p.states) state_store<KT>(S, p.states + (bh * p.nchunk + c) * KV, p.K, p.V, vcol, half);
+            // scores q k^T e^{G_i - G_j}, lanes i, in quads of j
+            for (int t = wave; t < TT * (TT + 1) / 2; t += NW) {
+                const int it2 = t > 0, jt = t == 2, i = it2 * 32 + l31;
+                f32x16 acc = {};
+#pragma unroll
+                for (int s = 0; s < KP / KS; ++s)
+                    acc = mfma(TK::by_row(kt, jt * 32 + l31, s, half), TK::by_row(qt, i, s, half), acc);
+                const double Gi = dec.G[i];
+                const int di = dec.doc[i];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    f32x4 x;
+                    const int j0 = jt * 32 + 8 * a + 4 * half;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = acc[4 * a + e] * (p.scale * dec.between(Gi, di, dec.G[j0 + e], dec.doc[j0 + e], j0 + e <= i));
+                    TP::put(pt, i, j0 / 4, x);
+                }
+            }
+            __syncthreads();
+        }
+        Frag v[C / KS];
+#pragma unroll
+        for (int s = 0; s < C / KS; ++s) v[s] = TV::by_column(vt, wave, s, lane);
+        if (OUT) {
+            f32x16 o[TT] = {};
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int s = 0; s < 32 / KS; ++s) {
+                    const Frag a = rounded(rows_of<T>(S[t], s));
+#pragma unroll
+                    for (int i = 0; i < TT; ++i) o[i] = mfma(a, TK::by_row(qt, i * 32 + l31, t * (32 / KS) + s, half), o[i]);
+                }
+            const int64_t t0 = (int64_t)c * C;
+#pragma unroll
+            for (int i = 0; i < TT; ++i) {
+                const float w = dec.start[i * 32 + l31] * p.scale;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[i][r] = w == 0.0f ? 0.0f : o[i][r] * w;
+#pragma unroll
+                for (int s = 0; s < (i + 1) * (32 / KS); ++s) o[i] = mfma(v[s], TP::by_row(pt, i * 32 + l31, s, half), o[i]);
+                const int64_t t = t0 + i * 32 + l31;
+                if (t < p.L) {
+                    T *const row = (T *)p.o + ((b * p.L + t) * p.H + h) * p.V;
+#pragma unroll
+                    for (int a = 0; a < 4; ++a)
+                        put_row<T>(row, v0 + wave * 32 + 8 * a + 4 * half, p.V, p.wide_o,
+                                   f32x4{o[i][4 * a], o[i][4 * a + 1], o[i][4 * a + 2], o[i][4 * a + 3]});
+                }
+            }
+        }
+        state_add<T, C, KP, KT>(S, kt, v, rev ? dec.start : dec.end, dec.whole, lane);
+        if (!OUT) {
+            decayed += dec.G[C - 1];
+            cut |= dec.whole == 0.0f;
+        }
+        __syncthreads();
+    }
+    if (OUT) {
+        if (p.last && seg == p.nseg - 1) state_store<KT>(S, p.last + bh * KV, p.K, p.V, vcol, half);
+    } else {
+        const int64_t at = bh * nseg_all + seg;
+        state_store<KT>(S, p.seg_out + at * KV, p.K, p.V, vcol, half);
+        if (threadIdx.x == 0 && slice == 0) p.seg_fac[at] = cut ? 0.0f : __builtin_amdgcn_exp2f((float)decayed);
+    }
+}
+
+// What the segments add becomes what enters them (forwards), or what comes back to them (reverse).
+__global__ void __launch_bounds__(256) k_join(float *seg, const float *fac, const float *first, int64_t KV, int64_t heads,
+                                              int nseg, bool reverse) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= heads * KV) return;
+    const int64_t bh = e / KV, at = e % KV;
+    float cur = first ? first[e] : 0.0f;
+    for (int i = 0; i < nseg; ++i) {
+        const int s = reverse ? nseg - 1 - i : i;
+        float *const p = seg + (bh * nseg + s) * KV + at;
+        if (i + 1 < nseg) {
+            const float f = fac[bh * nseg + s], add = *p;
+            *p = cur;
+            cur = f == 0.0f ? add : f * cur + add;
+        } else {
+            *p = cur;
+        }
+    }
+}
+
+struct BwdArgs {
+    const void *q, *k, *v, *do_;
+    const float *g, *states, *seg_in, *dlast;
+    void *dq, *dk, *dv;  // dq, dk: of T [B, L, Hk, K], or float32 [B, L, H, K] where heads share
+    float *dg, *dfirst;  // dg [B, L, H]
+    int64_t L, g_batch, g_token;
+    int32_t H, Hk, K, V, nseg, nchunk, per_seg;
+    float scale;
+    bool wide_k, wide_v, wide_s, wide_dk, wide_dv;
+};
+
+// The gradients of a segment, from its end. VP / 32 waves hold dS by columns of V and make dv;
+// KP / 32 waves hold it transposed, by columns of K, and make dk and dq.
+template <typename T, int KP, int VP>
+__global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
+    typedef Kind<T> N;
+    typedef typename N::Frag Frag;
+    constexpr int C = N::C, KS = N::KS, TT = C / 32, KT = KP / 32, VW = VP / 32, NW = KT + VW, THREADS = 64 * NW;
+    constexpr int kMost = KT > VW ? KT : VW;
+    typedef Tile<T, C, KP> TK;
+    typedef Tile<T, C, VP> TV;
+    typedef Tile<T, C, C> TP;
+    typedef Tile<float, C, C> TM;
+    __shared__ __attribute__((aligned(256))) char lds[2 * TK::kBytes + 2 * TV::kBytes + 3 * TP::kBytes + TM::kBytes];
+    __shared__ Decays<C> dec;
+    __shared__ float back[C];             // scale e^{G_i}
+    __shared__ float came[KT][C], left[KT][C], through[KT];
+    char *const qt = lds, *const kt = qt + TK::kBytes, *const vt = kt + TK::kBytes, *const dt = vt + TV::kBytes;
+    char *const at = dt + TV::kBytes, *const bt = at + TP::kBytes, *const bn = bt + TP::kBytes, *const mt = bn + TP::kBytes;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, l31 = lane & 31;
+    uint32_t work = work_of_block();
+    const int share = p.H / p.Hk, sub = work % share;
+    work /= share;
+    const int seg = work % p.nseg;
+    work /= p.nseg;
+    const int hk = work % p.Hk, h = hk * share + sub;
+    const int64_t b = work / p.Hk, bh = b * p.H + h;
+    const int c0 = seg * p.per_seg, c1 = min(c0 + p.per_seg, p.nchunk), n = c1 - c0;
+    const int64_t KV = (int64_t)p.K * p.V;
+    const bool of_v = wave < VW;          // this wave makes dv
+    const int part = of_v ? wave : wave - VW, col = part * 32 + l31;
+
+    f32x16 S[kMost];                      // dS [k rows][col of V], or dS^T [v rows][col of K]
+    {
+        const float *from = p.seg_in ? p.seg_in + (bh * p.nseg + seg) * KV : p.dlast ? p.dlast + bh * KV : nullptr;
+#pragma unroll
+        for (int t = 0; t < kMost; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = t * 32 + 8 * (r / 4) + 4 * half + r % 4, k = of_v ? row : col, v = of_v ? col : row;
+                S[t][r] = from && k < p.K && v < p.V ? from[(int64_t)k * p.V + v] : 0.0f;
+            }
+    }
+    Stage<T, C, KP, THREADS> qr, kr;
+    Stage<T, C, VP, THREADS> vr, dr;
+    float g = 0.0f;
+    const int64_t ks = (int64_t)p.Hk * p.K, vs = (int64_t)p.H * p.V;
+    auto fetch = [&](int c) {
+        const int64_t t0 = (int64_t)c * C;
+        const int rows = (int)min((int64_t)C, p.L - t0);
+        const int64_t from = b * p.L + t0;
+        qr.load((const T *)p.q + from * ks + (int64_t)hk * p.K, ks, rows, p.K, p.wide_k);
+        kr.load((const T *)p.k + from * ks + (int64_t)hk * p.K, ks, rows, p.K, p.wide_k);
+        vr.load((const T *)p.v + from * vs + (int64_t)h * p.V, vs, rows, p.V, p.wide_v);
+        dr.load((const T *)p.do_ + from * vs + (int64_t)h * p.V, vs, rows, p.V, p.wide_v);
+        if (wave == 0) g = lane < rows ? p.g[b * p.g_batch + (t0 + lane) * p.g_token + h] : 0.0f;
+    };
+    if (n > 0) fetch(c1 - 1);
+    for (int c = c1 - 1; c >= c0; --c) {
+        const int64_t t0 = (int64_t)c * C;
+        qr.store(qt);
+        kr.store(kt);
+        vr.store(vt);
+        dr.store(dt);
+        if (wave == 0) {
+            dec.make(g, lane);
+            if (lane < C) back[lane] = dec.start[lane] * p.scale;
+        }
+        __syncthreads();
+        if (c > c0) fetch(c - 1);
+        // The state that entered this chunk, lanes k, in quads of v.
+        f32x4 in[kMost * 4];
+        if (!of_v) {
+            const float *const from = p.states + (bh * p.nchunk + c) * KV + (int64_t)col * p.V;
+#pragma unroll
+            for (int a = 0; a < VW * 4; ++a) {
+                const int v = 8 * a + 4 * half;
+                f32x4 x = {0, 0, 0, 0};
+                if (col < p.K) {
+                    if (p.wide_s) {
+                        if (v < p.V) x = *(const f32x4 *)(from + v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (v + e < p.V) x[e] = from[v + e];
+                    }
+                }
+                in[a] = x;
+            }
+        }
+        // Scores: q k^T and do v^T with their decays. Tiles below the diagonal, each twice: lanes j
+        // (both products, and theirs for dg), and lanes i (do v^T).
+        for (int task = wave; task < TT * (TT + 1); task += NW) {
+            const int t = task >> 1, it = t > 0, jt = t == 2;
+            if (task & 1) {
+                const int i = it * 32 + l31;
+                f32x16 acc = {};
+#pragma unroll
+                for (int s = 0; s < VP / KS; ++s) acc = mfma(TV::by_row(vt, jt * 32 + l31, s, half), TV::by_row(dt, i, s, half), acc);
+                const double Gi = dec.G[i];
+                const int di = dec.doc[i];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    f32x4 x;
+                    const int j0 = jt * 32 + 8 * a + 4 * half;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = acc[4 * a + e] * (p.scale * dec.between(Gi, di, dec.G[j0 + e], dec.doc[j0 + e], j0 + e <= i));
+                    TP::put(bn, i, j0 / 4, x);
+                }
+            } else {
+                const int j = jt * 32 + l31;
+                f32x16 qk = {}, dov = {};
+#pragma unroll
+                for (int s = 0; s < KP / KS; ++s) qk = mfma(TK::by_row(qt, it * 32 + l31, s, half), TK::by_row(kt, j, s, half), qk);
+#pragma unroll
+                for (int s = 0; s < VP / KS; ++s) dov = mfma(TV::by_row(dt, it * 32 + l31, s, half), TV::by_row(vt, j, s, half), dov);
+                const double Gj = dec.G[j];
+                const int dj = dec.doc[j];
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    f32x4 x, y, m;
+                    const int i0 = it * 32 + 8 * a + 4 * half;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float w = p.scale * dec.between(dec.G[i0 + e], dec.doc[i0 + e], Gj, dj, j <= i0 + e);
+                        x[e] = qk[4 * a + e] * w;
+                        y[e] = dov[4 * a + e] * w;
+                        m[e] = j < i0 + e ? x[e] * dov[4 * a + e] : 0.0f;
+                    }
+                    TP::put(at, j, i0 / 4, x);
+                    TP::put(bt, j, i0 / 4, y);
+                    TM::put(mt, j, i0 / 4, m);
+                }
+            }
+        }
+        __syncthreads();
+        if (of_v) {
+            f32x16 acc[TT] = {};
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int s = 0; s < 32 / KS; ++s) {
+                    const Frag a = rounded(rows_of<T>(S[t], s));
+#pragma unroll
+                    for (int j = 0; j < TT; ++j) acc[j] = mfma(a, TK::by_row(kt, j * 32 + l31, t * (32 / KS) + s, half), acc[j]);
+                }
+            Frag d[C / KS];
+#pragma unroll
+            for (int s = 0; s < C / KS; ++s) d[s] = TV::by_column(dt, part, s, lane);
+#pragma unroll
+            for (int j = 0; j < TT; ++j) {
+                const float w = dec.end[j * 32 + l31];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[j][r] = w == 0.0f ? 0.0f : acc[j][r] * w;
+#pragma unroll
+                for (int s = j * (32 / KS); s < C / KS; ++s) acc[j] = mfma(d[s], TP::by_row(at, j * 32 + l31, s, half), acc[j]);
+                const int64_t t = t0 + j * 32 + l31;
+                if (t < p.L) {
+                    T *const row = (T *)p.dv + ((b * p.L + t) * p.H + h) * p.V;
+#pragma unroll
+                    for (int a = 0; a < 4; ++a)
+                        put_row<T>(row, part * 32 + 8 * a + 4 * half, p.V, p.wide_dv,
+                                   f32x4{acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]});
+                }
+            }
+            f32x16(&D)[KT] = reinterpret_cast<f32x16(&)[KT]>(S);
+            state_add<T, C, KP, KT>(D, qt, d, back, dec.whole, lane);
+        } else {
+            f32x16 ak[TT] = {}, aq[TT] = {};
+            float x = 0.0f;
+#pragma unroll
+            for (int t = 0; t < VW; ++t)
+#pragma unroll
+                for (int s = 0; s < 32 / KS; ++s) {
+                    typename N::Wide w = rows_of<T>(S[t], s), u;
+                    constexpr int Q = sizeof(w) / 16;  // quads of a fragment
+#pragma unroll
+                    for (int e = 0; e < 4 * Q; ++e) {
+                        u[e] = in[(t * (32 / KS) + s) * Q + e / 4][e % 4];
+                        x += u[e] * w[e];
+                    }
+                    Frag pk[N::kParts], pq[N::kParts];
+                    split(w, pk);
+                    split(u, pq);
+                    const int step = t * (32 / KS) + s;
+#pragma unroll
+                    for (int j = 0; j < TT; ++j) {
+                        const Frag fv = TV::by_row(vt, j * 32 + l31, step, half), fd = TV::by_row(dt, j * 32 + l31, step, half);
+#pragma unroll
+                        for (int e = 0; e < N::kParts; ++e) {
+                            ak[j] = mfma(pk[e], fv, ak[j]);
+                            aq[j] = mfma(pq[e], fd, aq[j]);
+                        }
+                    }
+                }
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
+            if (lane == 0) through[part] = dec.whole == 0.0f ? 0.0f : x * dec.whole;
+            Frag fq[C / KS];
+#pragma unroll
+            for (int s = 0; s < C / KS; ++s) fq[s] = TK::by_column(qt, part, s, lane);
+#pragma unroll
+            for (int j = 0; j < TT; ++j) {
+                const float wk = dec.end[j * 32 + l31], wq = back[j * 32 + l31];
+                float ck = 0.0f, cq = 0.0f;
+#pragma unroll
+                for (int s = 0; s < 32 / KS; ++s) {  // this wave's 32 columns of k and q, in quads
+                    const typename N::Wide xk = widened(TK::by_row(kt, j * 32 + l31, part * (32 / KS) + s, half));
+                    const typename N::Wide xq = widened(TK::by_row(qt, j * 32 + l31, part * (32 / KS) + s, half));
+                    constexpr int E = sizeof(xk) / 4;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const float rk = wk == 0.0f ? 0.0f : ak[j][s * E + e] * wk, rq = wq == 0.0f ? 0.0f : aq[j][s * E + e] * wq;
+                        ak[j][s * E + e] = rk;
+                        aq[j][s * E + e] = rq;
+                        ck += xk[e] * rk;
+                        cq += xq[e] * rq;
+                    }
+                }
+                ck += __shfl_xor(ck, 32);
+                cq += __shfl_xor(cq, 32);
+                if (half == 0) {
+                    left[part][j * 32 + l31] = ck;
+                    came[part][j * 32 + l31] = cq;
+                }
+#pragma unroll
+                for (int s = j * (32 / KS); s < C / KS; ++s) ak[j] = mfma(fq[s], TP::by_row(bt, j * 32 + l31, s, half), ak[j]);
+#pragma unroll
+                for (int s = 0; s < (j + 1) * (32 / KS); ++s)
+                    aq[j] = mfma(TK::by_column(kt, part, s, lane), TP::by_row(bn, j * 32 + l31, s, half), aq[j]);
+                const int64_t t = t0 + j * 32 + l31;
+                if (t < p.L) {
+                    const int64_t tok = b * p.L + t;
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        const int e = part * 32 + 8 * a + 4 * half;
+                        const f32x4 xk = {ak[j][4 * a], ak[j][4 * a + 1], ak[j][4 * a + 2], ak[j][4 * a + 3]};
+                        const f32x4 xq = {aq[j][4 * a], aq[j][4 * a + 1], aq[j][4 * a + 2], aq[j][4 * a + 3]};
+                        if (share == 1) {
+                            put_row<T>((T *)p.dk + (tok * p.H + h) * p.K, e, p.K, p.wide_dk, xk);
+                            put_row<T>((T *)p.dq + (tok * p.H + h) * p.K, e, p.K, p.wide_dk, xq);
+                        } else {
+                            put_row<float>((float *)p.dk + (tok * p.H + h) * p.K, e, p.K, p.wide_dk, xk);
+                            put_row<float>((float *)p.dq + (tok * p.H + h) * p.K, e, p.K, p.wide_dk, xq);
+                        }
+                    }
+                }
+            }
+            f32x16(&D)[VW] = reinterpret_cast<f32x16(&)[VW]>(S);
+            state_add<T, C, VP, VW>(D, dt, fq, back, dec.whole, lane);
+        }
+        __syncthreads();
+        if (wave == 0) {
+            // dg. Row j of the pairs becomes its sums from i on; then token t adds the rows before it.
+            if (lane < C) {
+                float sum = 0.0f;
+                for (int a = C / 4 - 1; a >= 0; --a) {
+                    f32x4 *const q4 = (f32x4 *)(mt + TM::at(lane, a));
+                    f32x4 m = *q4;
+#pragma unroll
+                    for (int e = 3; e >= 0; --e) {
+                        sum += m[e];
+                        m[e] = sum;
+                    }
+                    *q4 = m;
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+            float d = 0.0f, a = 0.0f, e = 0.0f;
+            if (lane < C) {
+                for (int j = 0; j < C - 1; ++j) {
+                    const float m = *(const float *)(mt + TM::at(j, lane >> 2) + (lane & 3) * 4);
+                    d += j < lane ? m : 0.0f;
+                }
+                float x = 0.0f;
+#pragma unroll
+                for (int w = 0; w < KT; ++w) {
+                    a += came[w][lane];
+                    e += left[w][lane];
+                    x += through[w];
+                }
+                d += x;
+            }
+            float before = e;  // sums of what left before t, and of what came from t on
+#pragma unroll
+            for (int k = 1; k < C; k *= 2) {
+                const float up = __shfl_up(before, k), down = __shfl_down(a, k);
+                if (lane >= k) before += up;
+                if (lane + k < C) a += down;
+            }
+            before = __shfl_up(before, 1);
+            if (lane > 0) d += before;
+            d += a;
+            if (lane < C && t0 + lane < p.L) p.dg[(b * p.L + t0 + lane) * p.H + h] = d;
+        }
+    }
+    if (p.dfirst && seg == 0) {
+        float *const to = p.dfirst + bh * KV;
+        if (of_v) {
+            f32x16(&D)[KT] = reinterpret_cast<f32x16(&)[KT]>(S);
+            state_store<KT>(D, to, p.K, p.V, col, half);
+        }
+    }
+}
+
+// Gradients of shared heads: the sum over a group's heads, rounded once.
+template <typename T>
+__global__ void __launch_bounds__(256) k_groups(const float *dq, const float *dk, T *oq, T *ok, int64_t n, int32_t K, int32_t share) {
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= n) return;
+    const int64_t group = e / K, at = group * share * K + e % K;
+    float q = 0.0f, k = 0.0f;
+    for (int s = 0; s < share; ++s) {
+        q += dq[at + (int64_t)s * K];
+        k += dk[at + (int64_t)s * K];
+    }
+    oq[e] = (T)q;
+    ok[e] = (T)k;
+}
+
+// Gradient of a decay that all tokens of a head share: the sum over them, in 64 bits.
+__global__ void __launch_bounds__(256) k_decay_sum(const float *dg, float *out, int64_t tokens, int32_t H) {
+    const int h = blockIdx.x;
+    double sum = 0.0;
+    for (int64_t t = threadIdx.x; t < tokens; t += 256) sum += dg[t * H + h];
+    __shared__ double part[4];
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) out[h] = (float)(part[0] + part[1] + part[2] + part[3]);
+}
+
+// One token: a block has 32 columns of V of one head's state, 8 lanes of 4 (or 32 of 1) for a row.
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(256) k_step(LinattnStepArgs p) {
+    constexpr int E = WIDE ? 4 : 1, kLanes = 32 / E, kRows = 256 / kLanes;
+    typedef float fv __attribute__((ext_vector_type(E)));
+    const int slices = (p.V + 31) / 32, slice = blockIdx.x % slices;
+    const int64_t nh = blockIdx.x / slices, n = nh / p.H;
+    const int h = (int)(nh % p.H), hk = h / (p.H / p.Hk);
+    const int v = slice * 32 + threadIdx.x % kLanes * E, r0 = threadIdx.x / kLanes;
+    const bool live = v < p.V;
+    const float g = p.g[(p.per_token ? n : n / p.seqs) * p.H + h];
+    const float a = g < kCut ? 0.0f : __expf(g);
+    const T *const q = (const T *)p.q + (n * p.Hk + hk) * p.K, *const k = (const T *)p.k + (n * p.Hk + hk) * p.K;
+    fv x = {};
+    if (live) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = (float)((const T *)p.v + nh * p.V)[v + e];
+    }
+    float *const S = p.h + nh * p.K * p.V;
+    fv o = {};
+    if (live) {
+#pragma unroll 4
+        for (int r = r0; r < p.K; r += kRows) {
+            fv *const at = (fv *)(S + (int64_t)r * p.V + v);
+            fv s = *at;
+            const float kr = (float)k[r], qr = (float)q[r];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                s[e] = (a == 0.0f ? 0.0f : a * s[e]) + kr * x[e];
+                o[e] += qr * s[e];
+            }
+            *at = s;
+        }
+    }
+    __shared__ fv sum[kRows][kLanes];
+    sum[r0][threadIdx.x % kLanes] = o;
+    __syncthreads();
+    if (threadIdx.x < kLanes && live) {
+        fv t = {};
+        for (int r = 0; r < kRows; ++r) t += sum[r][threadIdx.x];
+        T *const out = (T *)p.o + nh * p.V + v;
+#pragma unroll
+        for (int e = 0; e < E; ++e) out[e] = (T)(t[e] * p.scale);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+bool aligned_to(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
+int chunk_of(int io) { return io ? Kind<__bf16>::C : Kind<float>::C; }
+size_t up(size_t v) { return (v + 255) / 256 * 256; }
+
+// Segments of a sequence: enough blocks for the GPU, but none shorter than 8 chunks, since a sweep
+// over the segments' keys and values comes first where there are several.
+struct Plan {
+    int64_t nchunk;
+    int nseg, per_seg, slices;
+};
+Plan plan(int64_t B, int64_t L, int32_t H, int32_t V, int io, bool bwd) {
+    Plan p;
+    p.nchunk = (L + chunk_of(io) - 1) / chunk_of(io);
+    const int vp = V > 64 ? 128 : 64;
+    p.slices = 1;
+    if (!bwd && vp == 128 && B * H < 512) p.slices = 2;
+    const int64_t blocks = B * H * p.slices, want = bwd ? 256 : 512;
+    int64_t n = blocks > 0 ? (want + blocks - 1) / blocks : 1;
+    n = std::min(n, std::max<int64_t>(p.nchunk / 8, 1));
+    const int64_t per = std::max<int64_t>((p.nchunk + n - 1) / std::max<int64_t>(n, 1), 1);
+    p.per_seg = (int)per;
+    p.nseg = (int)std::max<int64_t>((p.nchunk + per - 1) / per, 1);
+    return p;
+}
+
+template <typename T, bool OUT>
+void sweep(const SweepArgs &a, int64_t blocks, hipStream_t s) {
+    const bool k128 = a.K > 64;
+    const int width = (a.V > 64 ? 128 : 64) / a.slices;
+    if (k128) {
+        if (width == 128) k_sweep<T, 128, 4, OUT><<<blocks, 256, 0, s>>>(a);
+        else k_sweep<T, 128, 2, OUT><<<blocks, 128, 0, s>>>(a);
+    } else {
+        if (width == 128) k_sweep<T, 64, 4, OUT><<<blocks, 256, 0, s>>>(a);
+        else k_sweep<T, 64, 2, OUT><<<blocks, 128, 0, s>>>(a);
+    }
+}
+
+template <typename T>
+hipError_t run_fwd(const LinattnArgs &a, hipStream_t s) {
+    const int io = sizeof(T) == 2;
+    const Plan pl = plan(a.B, a.L, a.H, a.V, io, false);
+    const int64_t heads = a.B * a.H, KV = (int64_t)a.K * a.V;
+    float *const seg = (float *)a.ws, *const fac = pl.nseg > 1 ? seg + heads * pl.nseg * KV : nullptr;
+    SweepArgs p{};
+    p.q = a.q; p.k = a.k; p.v = a.v; p.g = a.g;
+    p.L = a.L; p.H = a.H; p.Hk = a.Hk; p.K = a.K; p.V = a.V;
+    p.g_batch = a.per_token ? a.L * a.H : 0;
+    p.g_token = a.per_token ? a.H : 0;
+    p.nchunk = (int)pl.nchunk; p.per_seg = pl.per_seg; p.slices = pl.slices;
+    p.scale = a.scale;
+    constexpr int E = 16 / sizeof(T);
+    p.wide_k = a.K % E == 0 && aligned_to(a.q, 16) && aligned_to(a.k, 16);
+    p.wide_v = a.V % E == 0 && aligned_to(a.v, 16);
+    p.wide_o = a.V % 4 == 0 && aligned_to(a.o, 4 * sizeof(T));
+    if (pl.nseg > 1) {
+        SweepArgs q = p;
+        q.nseg = pl.nseg - 1;
+        q.seg_out = seg;
+        q.seg_fac = fac;
+        sweep<T, false>(q, heads * q.nseg * q.slices, s);
+        k_join<<<(heads * KV + 255) / 256, 256, 0, s>>>(seg, fac, a.h0, KV, heads, pl.nseg, false);
+        p.seg_in = seg;
+    }
+    p.nseg = pl.nseg;
+    p.first = a.h0;
+    p.o = a.o; p.last = a.h_final; p.states = a.states;
+    sweep<T, true>(p, heads * p.nseg * p.slices, s);
+    return hipGetLastError();
+}
+
+// The backward's workspace: the segments' gradients of the state and their decays, the gradients of
+// shared heads, and dg by token.
+struct BwdPlan {
+    Plan seg, pass;
+    size_t fac, dq, dk, dg, bytes;
+};
+BwdPlan bwd_plan(int64_t B, int64_t L, int32_t H, int32_t Hk, int32_t K, int32_t V, bool per_token, int io) {
+    BwdPlan p;
+    p.seg = plan(B, L, H, V, io, true);
+    p.pass = p.seg;
+    p.pass.slices = V > 64 ? 2 : 1;
+    size_t at = 0;
+    if (p.seg.nseg > 1) at = up((size_t)B * H * p.seg.nseg * K * V * 4);
+    p.fac = at;
+    if (p.seg.nseg > 1) at = up(at + (size_t)B * H * p.seg.nseg * 4);
+    p.dq = at;
+    if (H != Hk) at = up(at + (size_t)B * L * H * K * 4);
+    p.dk = at;
+    if (H != Hk) at = up(at + (size_t)B * L * H * K * 4);
+    p.dg = at;
+    if (!per_token) at = up(at + (size_t)B * L * H * 4);
+    p.bytes = at;
+    return p;
+}
+
+template <typename T>
+hipError_t run_bwd(const LinattnArgs &a, hipStream_t s) {
+    const int io = sizeof(T) == 2;
+    const BwdPlan pl = bwd_plan(a.B, a.L, a.H, a.Hk, a.K, a.V, a.per_token, io);
+    const int64_t heads = a.B * a.H, KV = (int64_t)a.K * a.V;
+    char *const ws = (char *)a.ws;
+    float *const seg = (float *)ws, *const fac = (float *)(ws + pl.fac);
+    constexpr int E = 16 / sizeof(T);
+    BwdArgs p{};
+    p.q = a.q; p.k = a.k; p.v = a.v; p.do_ = a.do_; p.g = a.g; p.states = a.states;
+    p.L = a.L; p.H = a.H; p.Hk = a.Hk; p.K = a.K; p.V = a.V;
+    p.g_batch = a.per_token ? a.L * a.H : 0;
+    p.g_token = a.per_token ? a.H : 0;
+    p.nchunk = (int)pl.seg.nchunk; p.per_seg = pl.seg.per_seg; p.nseg = pl.seg.nseg;
+    p.scale = a.scale;
+    p.wide_k = a.K % E == 0 && aligned_to(a.q, 16) && aligned_to(a.k, 16);
+    p.wide_v = a.V % E == 0 && aligned_to(a.v, 16) && aligned_to(a.do_, 16);
+    p.wide_s = a.V % 4 == 0 && aligned_to(a.states, 16);
+    const bool shared = a.H != a.Hk;
+    p.dq = shared ? ws + pl.dq : (char *)a.dq;
+    p.dk = shared ? ws + pl.dk : (char *)a.dk;
+    p.dv = a.dv;
+    const size_t quad = 4 * (shared ? 4 : sizeof(T));
+    p.wide_dk = a.K % 4 == 0 && aligned_to(p.dq, quad) && aligned_to(p.dk, quad);
+    p.wide_dv = a.V % 4 == 0 && aligned_to(a.dv, 4 * sizeof(T));
+    p.dg = a.per_token ? a.dg : (float *)(ws + pl.dg);
+    p.dlast = a.dh_final;
+    p.dfirst = a.dh0;
+    if (heads > 0) {
+        if (p.nseg > 1) {
+            SweepArgs q{};
+            q.k = a.q; q.v = a.do_; q.g = a.g;
+            q.L = a.L; q.H = a.H; q.Hk = a.Hk; q.K = a.K; q.V = a.V;
+            q.g_batch = p.g_batch; q.g_token = p.g_token;
+            q.nchunk = p.nchunk; q.per_seg = p.per_seg; q.nseg = p.nseg - 1; q.slices = pl.pass.slices;
+            q.scale = a.scale; q.wide_k = p.wide_k; q.wide_v = p.wide_v; q.reverse = true;
+            q.seg_out = seg; q.seg_fac = fac;
+            sweep<T, false>(q, heads * q.nseg * q.slices, s);
+            k_join<<<(heads * KV + 255) / 256, 256, 0, s>>>(seg, fac, a.dh_final, KV, heads, p.nseg, true);
+            p.seg_in = seg;
+        }
+        const int64_t blocks = heads * p.nseg;
+        if (a.K > 64) {
+            if (a.V > 64) k_bwd<T, 128, 128><<<blocks, 512, 0, s>>>(p);
+            else k_bwd<T, 128, 64><<<blocks, 384, 0, s>>>(p);
+        } else {
+            if (a.V > 64) k_bwd<T, 64, 128><<<blocks, 384, 0, s>>>(p);
+            else k_bwd<T, 64, 64><<<blocks, 256, 0, s>>>(p);
+        }
+        if (shared && a.L > 0) {
+            const int64_t n = a.B * a.L * a.Hk * a.K;
+            k_groups<T><<<(n + 255) / 256, 256, 0, s>>>((const float *)p.dq, (const float *)p.dk, (T *)a.dq, (T *)a.dk, n, a.K,
+                                                        a.H / a.Hk);
+        }
+    }
+    if (!a.per_token) k_decay_sum<<<a.H, 256, 0, s>>>(p.dg, a.dg, a.B * a.L, a.H);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int32_t linattn_state_every(int io) { return chunk_of(io); }
+size_t linattn_fwd_ws(int64_t B, int64_t L, int32_t H, int32_t K, int32_t V, int io) {
+    const Plan p = plan(B, L, H, V, io, false);
+    return p.nseg > 1 ? (size_t)B * H * p.nseg * ((size_t)K * V + 1) * 4 : 0;
+}
+size_t linattn_bwd_ws(int64_t B, int64_t L, int32_t H, int32_t Hk, int32_t K, int32_t V, bool per_token, int io) {
+    return bwd_plan(B, L, H, Hk, K, V, per_token, io).bytes;
+}
+hipError_t launch_linattn_fwd(const LinattnArgs &a, int io, hipStream_t s) {
+    return io ? run_fwd<__bf16>(a, s) : run_fwd<float>(a, s);
+}
+hipError_t launch_linattn_bwd(const LinattnArgs &a, int io, hipStream_t s) {
+    return io ? run_bwd<__bf16>(a, s) : run_bwd<float>(a, s);
+}
+hipError_t launch_linattn_step(const LinattnStepArgs &a, int io, hipStream_t s) {
+    const int64_t blocks = a.layers * a.seqs * a.H * ((a.V + 31) / 32);
+    const bool wide = a.V % 4 == 0 && aligned_to(a.h, 16);
+    if (io) wide ? k_step<__bf16, true><<<blocks, 256, 0, s>>>(a) : k_step<__bf16, false><<<blocks, 256, 0, s>>>(a);
+    else wide ? k_step<float, true><<<blocks, 256, 0, s>>>(a) : k_step<float, false><<<blocks, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace ssm

@@ -1,0 +1,135 @@
+"""Sampling on the GPU against a sorted list on the CPU. Tokens are equal: masses are held to 2^-46
+here and to 2^-53 there, so u would have to lie within 2^-46 V of a border (about 1e-9 for these
+sizes) for another token to be right. logprob is one logarithm rounded to float32: 2^-24 of it, and
+2^-46 V of the mass."""
+import math
+
+import pytest
+import torch
+
+import selective_state_space_49_amd as ssm
+from tests import layers_ref as ref
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def check(logits, u, **settings):
+    dev = {k: t.cuda() if torch.is_tensor(t) else t for k, t in settings.items()}
+    tokens, logprob = ssm.ssm_sample(logits.cuda(), u.cuda(), **dev, want_logprob=True)
+    tokens, logprob = tokens.cpu(), logprob.cpu()
+    for r in range(logits.shape[0]):
+        one = {k: (t[r].item() if torch.is_tensor(t) else t) for k, t in settings.items()}
+        token, lp, kept = ref.sample(logits[r], u[r].item(), **one)
+        assert int(tokens[r]) == token, (r, one, u[r].item(), int(tokens[r]), token, len(kept))
+        got = float(logprob[r])
+        if math.isnan(lp):
+            assert math.isnan(got)
+        else:
+            assert abs(got - lp) <= 2.0 ** -24 * abs(lp) + 1e-7 * (lp != 0) + 1e-9, (r, one, got, lp)
+    return tokens
+
+
+def make(rows, vocab, io=F32, seed=0, spread=2.5):
+    g = torch.Generator().manual_seed(seed + vocab)
+    return (torch.randn(rows, vocab, generator=g) * spread).to(io), torch.rand(rows, generator=g)
+
+
+SETTINGS = [{}, {"temperature": 0.0}, {"temperature": 0.7}, {"temperature": 2.5}, {"top_k": 1}, {"top_k": 5},
+            {"top_k": 50, "top_p": 0.9}, {"top_k": 1000}, {"top_p": 0.5}, {"top_p": 0.95}, {"top_p": 0.0}, {"top_p": 0.999},
+            {"min_p": 0.05}, {"min_p": 1.0}, {"min_p": 2.0}, {"temperature": 0.8, "top_k": 40, "top_p": 0.95, "min_p": 0.02},
+            {"top_k": 2 ** 31 - 1}, {"top_k": -3, "top_p": 1.5, "min_p": -1.0}]
+
+
+@pytest.mark.parametrize("io", [F32, BF16], ids=str)
+@pytest.mark.parametrize("vocab", [1, 2, 63, 65, 1000, 4097, 20011])
+def test_settings(vocab, io):
+    for n, s in enumerate(SETTINGS):
+        say("sample", vocab, io, s)
+        check(*make(4, vocab, io, seed=n), **s)
+
+
+def test_settings_by_row():
+    n = 64
+    g = torch.Generator().manual_seed(3)
+    pick = lambda *of: torch.tensor(of)[torch.randint(0, len(of), (n,), generator=g)]  # noqa: E731
+    for io in (F32, BF16):
+        check(*make(n, 3001, io), temperature=pick(0.0, 0.5, 1.0, 1.7), top_k=pick(0, 1, 30, 500).to(torch.int32),
+              top_p=pick(0.3, 0.9, 1.0), min_p=pick(0.0, 0.01, 0.2))
+
+
+@pytest.mark.parametrize("settings", [{}, {"top_k": 7}, {"top_p": 0.5}, {"top_k": 700, "top_p": 0.7}, {"min_p": 0.5}], ids=str)
+def test_equal_logits(settings):
+    """Ties go to the lowest index: all equal, two values, and -0 beside 0."""
+    u = torch.tensor([0.0, 0.25, 0.5, 0.999, 1 - 2.0 ** -24])
+    for vocab in (1, 5, 64, 1000, 5000):
+        say("equal", vocab, settings)
+        check(torch.full((5, vocab), 1.5), u, **settings)
+        two = torch.zeros(5, vocab)
+        two[:, ::3] = 1.0
+        check(two, u, **settings)
+        zeros = torch.zeros(5, vocab)
+        zeros[:, ::2] = -0.0
+        check(zeros, u, **settings)
+
+
+def test_flat_and_peaked():
+    for spread in (0.0, 1e-6, 0.01, 0.3, 30.0, 1e4, 1e30):
+        for s in ({}, {"top_k": 100}, {"top_p": 0.9}, {"top_k": 2000, "top_p": 0.6}, {"min_p": 0.3}):
+            say("spread", spread, s)
+            check(*make(3, 6007, spread=spread), **s)
+    for t in (1e-30, 1e-3, 1e3, 1e30, math.inf):
+        check(*make(3, 500), temperature=t)
+        check(*make(3, 500), temperature=t, top_p=0.8)
+
+
+def test_masked():
+    logits, u = make(9, 300)
+    logits[0, :] = -math.inf                  # nothing is left
+    logits[1, 5:] = -math.inf
+    logits[2, :299] = -math.inf               # one is left, the last
+    logits[3, 7] = math.nan
+    logits[4, 11], logits[4, 200] = math.inf, math.inf
+    logits[5, ::2] = -math.inf
+    logits[6, 0], logits[6, 1] = math.inf, math.nan
+    for s in ({}, {"temperature": 0.0}, {"top_k": 3}, {"top_p": 0.4}, {"min_p": 0.1}, {"top_k": 200, "top_p": 0.9}):
+        for io in (F32, BF16):
+            say("masked", s, io)
+            t = check(logits.to(io), u, **s)
+            assert t[0] == -1 and t[3] == -1 and t[6] == -1 and t[2] == 299 and t[4] in (11, 200)
+    check(logits, u, temperature=torch.tensor([1.0, -1.0, math.nan, 1.0, 0.0, -0.0, 1.0, 0.5, math.inf]))
+
+
+def test_borders_of_u():
+    logits, _ = make(5, 40)
+    check(logits, torch.tensor([0.0, 1 - 2.0 ** -24, 0.5, math.nan, 2.0 ** -149]))
+    t = ssm.ssm_sample(logits.cuda(), torch.tensor([-1.0, 1.0, 2.0, math.inf, -math.inf]).cuda())
+    assert t.tolist() == [0, 39, 39, 39, 0]
+    weights = torch.tensor([[1.0, 1.0, 2.0, 4.0]]).log().repeat(4, 1)  # borders at 1/8, 1/4, 1/2
+    assert ssm.ssm_sample(weights.cuda(), torch.tensor([0.1249, 0.1251, 0.2499, 0.5001]).cuda()).tolist() == [0, 1, 1, 3]
+
+
+def test_shares():
+    """As many draws as u is spread evenly: each token comes as often as its share says, to one draw."""
+    logits = torch.randn(1, 50, generator=torch.Generator().manual_seed(2))
+    n = 20000
+    u = (torch.arange(n) + 0.5) / n
+    t = ssm.ssm_sample(logits.repeat(n, 1).cuda(), u.cuda(), temperature=0.9)
+    got = torch.bincount(t.cpu(), minlength=50).double()
+    want = torch.softmax(logits[0].double() / float(torch.tensor(0.9)), 0) * n
+    assert float((got - want).abs().max()) <= 1.0 + 1e-3 * n * 2.0 ** -24 + 1e-6 * n
+
+
+def test_large_vocabularies():
+    for vocab, io in ((131072, F32), (100003, BF16)):
+        for s in ({}, {"top_k": 3000}, {"top_p": 0.9}, {"top_k": 64, "top_p": 0.99}, {"min_p": 0.001, "top_p": 0.97}):
+            say("large", vocab, io, s)
+            check(*make(2, vocab, io), **s)
+
+
+def test_many_rows_and_none():
+    logits, u = make(3000, 17)
+    check(logits, u, top_p=0.7)
+    t = ssm.ssm_sample(torch.empty(0, 5, device="cuda"), torch.empty(0, device="cuda"))
+    assert t.shape == (0,)
