@@ -848,7 +848,7 @@ ssm_status ssm_rmsnorm_bwd(const void *dy, const void *s, const void *ds, const 
  * temperature, top_p, min_p float32 and top_k int32 [rows], or NULL: the value that ends in _all for
  * every row. A temperature of 0 takes the first of the largest logits. tokens [rows] int64; logprob
  * [rows] float32 (NULL = not wanted): the logarithm of the token's share of the kept mass.
- * Masses are whole multiples of 2^-46 (vocab up to 2^16; one bit less for each doubling) from
+ * Masses are whole multiples of 2^-44 (vocab up to 2^18; one bit less for each doubling) from
  * exponentials in 64 bits: sums do not depend on an order, and a token of less has no mass.
  * A logit of -infinity is never drawn; beside one of +infinity only such ones are. A row without a
  * finite logit or +infinity, with a NaN among its logits, or with a temperature or u that is NaN or a

@@ -1,7 +1,7 @@
-"""Sampling on the GPU against a sorted list on the CPU. Tokens are equal: masses are held to 2^-46
-here and to 2^-53 there, so u would have to lie within 2^-46 V of a border (about 1e-9 for these
+"""Sampling on the GPU against a sorted list on the CPU. Tokens are equal: masses are held to 2^-44
+here and to 2^-53 there, so u would have to lie within 2^-44 V of a border (about 1e-8 for these
 sizes) for another token to be right. logprob is one logarithm rounded to float32: 2^-24 of it, and
-2^-46 V of the mass."""
+2^-44 V of the mass."""
 import math
 
 import pytest
