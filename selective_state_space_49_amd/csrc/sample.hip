@@ -93,18 +93,24 @@ __device__ __forceinline__ u64 block_scan(u64 x, u64 *part, u64 &all) {
 struct Masses {
     double max, inv2, least;  // 1 / temperature in units of log 2; the mass of the least weight
     int shift;
+    // A step of the polynomial with its coefficient in scalar registers, which the compiler would copy to
+    // vector registers for every step.
+    static __device__ __forceinline__ double step(double p, double f, double c) {
+        double r;
+        asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(p), "v"(f), "s"(c));
+        return r;
+    }
     __device__ __forceinline__ double operator()(float x) const {
         const double t = fmax(((double)x - max) * inv2, -1000.0);
         const double n = __builtin_rint(t), f = t - n;
-        double p = 1.0210919981407892e-07;
-        p = __builtin_fma(p, f, 1.3258537495951731e-06);
-        p = __builtin_fma(p, f, 1.5252645306585149e-05);
-        p = __builtin_fma(p, f, 0.00015403439922121213);
-        p = __builtin_fma(p, f, 0.0013333558250865102);
-        p = __builtin_fma(p, f, 0.009618129182540224);
-        p = __builtin_fma(p, f, 0.055504108664325015);
-        p = __builtin_fma(p, f, 0.24022650695717282);
-        p = __builtin_fma(p, f, 0.6931471805599514);
+        double p = f * 1.0210919981407892e-07 + 1.3258537495951731e-06;
+        p = step(p, f, 1.5252645306585149e-05);
+        p = step(p, f, 0.00015403439922121213);
+        p = step(p, f, 0.0013333558250865102);
+        p = step(p, f, 0.009618129182540224);
+        p = step(p, f, 0.055504108664325015);
+        p = step(p, f, 0.24022650695717282);
+        p = step(p, f, 0.6931471805599514);
         p = __builtin_fma(p, f, 1.0);
         return __builtin_rint(__builtin_amdgcn_ldexp(p, (int)n + shift));
     }
@@ -322,7 +328,7 @@ __device__ __forceinline__ Plan plan_ends(Shared &sh, const Settings &s, const S
 }
 
 // 3. The masses of a range of entries: what is certainly kept, to its entry; sums (of a thread) of what
-// top_k keeps before its last step and outside the list, and of the certain part of it; and the list.
+// lies before top_k's last step, and of the certain part of it; and the list.
 template <typename T>
 __device__ __forceinline__ void weigh(const Logits<T> &l, int from, int to, const Settings &s, const Steps &st, const Plan &pl,
                                       const Masses &mass, u64 *entry, u64 *list, uint32_t *count, u64 &all, u64 &kept) {
@@ -331,39 +337,49 @@ __device__ __forceinline__ void weigh(const Logits<T> &l, int from, int to, cons
     const bool filtered = s.by_k || s.by_p, choosy = mass.least > 0.0;
     const float end = pl.end_k < kBins ? (float)pl.end_k : kInfinity, past = pl.end_k < kBins ? (float)(pl.end_k + 1) : kInfinity;
     const float p0 = s.by_p ? (float)pl.p_from : end, p1 = s.by_p ? (pl.p_to < kBins - 1 ? (float)(pl.p_to + 1) : kInfinity) : end;
+    const float last = s.by_k ? past : p1;  // of the list
     double sum = 0.0, sure = 0.0, mine = 0.0;
     const auto tile = [&](const float(&x)[E], int64_t i, int64_t) {
+        if (!filtered) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const double m = mass(x[e]);
+                mine += choosy && m < mass.least ? 0.0 : m;
+            }
+            return;
+        }
         float at[E];
-        bool some = false;
+        bool some = false, listed = false;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             at[e] = st.of(x[e]);
-            if (!filtered) continue;
             some |= at[e] < end;
-            if (at[e] >= p0 && at[e] < past && (at[e] < p1 || at[e] >= end)) {
-                const uint32_t n = atomicAdd(count, 1u);
-                if (n < kList) list[n] = place_of(key_of(x[e]), (uint32_t)(i + e));
-            }
+            listed |= at[e] >= p0 && at[e] < last;
         }
-        if (filtered && __ballot(some) == 0) return;
+        if (__ballot(listed)) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (at[e] >= p0 && at[e] < last && (at[e] < p1 || at[e] >= end)) {
+                    const uint32_t n = atomicAdd(count, 1u);
+                    if (n < kList) list[n] = place_of(key_of(x[e]), (uint32_t)(i + e));
+                }
+        }
+        if (__ballot(some) == 0) return;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const double m = mass(x[e]);
-            if (!filtered) {
-                mine += choosy && m < mass.least ? 0.0 : m;
-                continue;
+            const double m = mass(x[e]), yes = at[e] < p0 ? m : 0.0;
+            if (s.by_p) sum += s.by_k && !(at[e] < end) ? 0.0 : m;
+            if (choosy) {
+                sure += yes;
+                mine += m < mass.least ? 0.0 : yes;
+            } else {
+                mine += yes;
             }
-            const double yes = at[e] < p0 ? m : 0.0;
-            if (s.by_p) {
-                sum += at[e] < p0 || (at[e] >= p1 && at[e] < end) ? m : 0.0;
-                if (choosy) sure += yes;
-            }
-            mine += choosy && m < mass.least ? 0.0 : yes;
         }
     };
     if (l.per_entry == 1) {
-        for (int e = from + wave; e < to; e += 4 * kWaves)  // four entries' loads at once
-            l.template each<4>(e, std::min(e + 3 * kWaves + 1, to), kWaves, [&](const float(&x)[E], int64_t i, int64_t t) {
+        for (int e = from + wave; e < to; e += 4 * kWaves)
+            l.template each<2>(e, std::min(e + 3 * kWaves + 1, to), kWaves, [&](const float(&x)[E], int64_t i, int64_t t) {
                 mine = 0.0;
                 tile(x, i, t);
                 if (s.by_p && !choosy) sure += mine;
@@ -373,7 +389,7 @@ __device__ __forceinline__ void weigh(const Logits<T> &l, int from, int to, cons
     } else {
         for (int e = from + wave; e < to; e += kWaves) {
             mine = 0.0;
-            l.template each<4>(e * l.per_entry, std::min<int64_t>((e + 1) * l.per_entry, l.tiles), 1, tile);
+            l.template each<1>(e * l.per_entry, std::min<int64_t>((e + 1) * l.per_entry, l.tiles), 1, tile);
             if (s.by_p && !choosy) sure += mine;
             const u64 m = __ballot(mine > 0.0) ? wave_sum(mine) : 0;
             if (lane == 0) entry[e] = m;
@@ -433,7 +449,7 @@ __device__ __forceinline__ void sort_list(u64 *list, int n) {
 
 // The number and the mass of the logits from place `from` on (the slow way).
 template <typename T>
-__device__ void measure(const Logits<T> &l, const Masses &mass, u64 from, Shared &sh, u64 &count, u64 &sum) {
+__device__ __noinline__ void measure(const Logits<T> &l, const Masses &mass, u64 from, Shared &sh, u64 &count, u64 &sum) {
     constexpr int E = Logits<T>::E;
     double m = 0.0;
     u64 c = 0;
@@ -453,7 +469,7 @@ __device__ void measure(const Logits<T> &l, const Masses &mass, u64 from, Shared
 
 // The last kept place by bisection, and the entries with it.
 template <typename T>
-__device__ u64 bisect(const Logits<T> &l, const Masses &mass, const Settings &s, Shared &sh) {
+__device__ __noinline__ u64 bisect(const Logits<T> &l, const Masses &mass, const Settings &s, Shared &sh) {
     constexpr int E = Logits<T>::E;
     u64 count, all, last = 0, m;
     measure(l, mass, 0, sh, count, all);
@@ -494,9 +510,9 @@ __device__ u64 bisect(const Logits<T> &l, const Masses &mass, const Settings &s,
 }
 
 // The last kept place from the list, whose kept ones go to their entries; 0: the list does not tell. all:
-// the mass of what top_k keeps outside the list; kept: of that, what lies before the list.
+// the mass before top_k's last step; kept: of that, what lies before the list.
 template <typename T>
-__device__ u64 resolve(const Logits<T> &l, const Masses &mass, const Settings &s, const Steps &st, const Plan &pl, u64 all, u64 kept,
+__device__ __forceinline__ u64 resolve(const Logits<T> &l, const Masses &mass, const Settings &s, const Steps &st, const Plan &pl, u64 all, u64 kept,
                        Shared &sh) {
     const int tid = threadIdx.x, n = (int)sh.count;
     if (n > kList || n == 0) return 0;
@@ -525,8 +541,11 @@ __device__ u64 resolve(const Logits<T> &l, const Masses &mass, const Settings &s
             }
     }
     if (s.by_p) {
-        block_scan(m[0] + m[1], sh.part, whole);
-        const double part = (double)s.top_p * (double)(all + whole);
+        if (pl.end_k < kBins) {  // and what top_k keeps of that step
+            block_scan((in_k[0] ? m[0] : 0) + (in_k[1] ? m[1] : 0), sh.part, whole);
+            all += whole;
+        }
+        const double part = (double)s.top_p * (double)all;
         const u64 x0 = in_p[0] ? m[0] : 0, x1 = in_p[1] ? m[1] : 0;
         const u64 upto = kept + block_scan(x0 + x1, sh.part, whole);
         // the end lies in these steps: not before them, and not after, unless nothing is left there
@@ -553,7 +572,7 @@ __device__ u64 resolve(const Logits<T> &l, const Masses &mass, const Settings &s
 
 // 4. The entry in which the sum exceeds u times all, and the token in it.
 template <typename T>
-__device__ void draw(const Logits<T> &l, const Masses &mass, const Settings &s, u64 last, Shared &sh, int64_t *token, float *logprob) {
+__device__ __forceinline__ void draw(const Logits<T> &l, const Masses &mass, const Settings &s, u64 last, Shared &sh, int64_t *token, float *logprob) {
     constexpr int E = Logits<T>::E;
     const int tid = threadIdx.x, lane = tid & 63;
     __syncthreads();
