@@ -767,8 +767,8 @@ ssm_status ssm_adamw_values(const int8_t *exp_avg, const uint8_t *exp_avg_sq,
  * workspace: at least ssm_linattn_fwd_workspace(...) / ssm_linattn_bwd_workspace(...) bytes, 256-byte
  * aligned (0 is possible, then it may be NULL); its contents on entry are ignored. Outputs must not
  * overlap inputs or each other (SSM_ERR_UNSUPPORTED). Alignment: float32 arrays 4 bytes, the others
- * one element (rows that start on 16 bytes are read fastest). d_k and d_v are 1 to 128, heads a
- * multiple of groups, batch x heads at most 2^20. L == 0 writes h_final = h0 (dh0 = dh_final, and 0
+ * one element (rows that start on 16 bytes are read fastest). d_k and d_v are 1 to 128, heads at
+ * most 2^15 and a multiple of groups, batch x heads at most 2^20. L == 0 writes h_final = h0 (dh0 = dh_final, and 0
  * for a [heads] decay). */
 #define SSM_LINATTN_CHUNK_BF16 64
 #define SSM_LINATTN_CHUNK_F32 32

@@ -52,18 +52,18 @@ ssm_status check_workspace(const void *ws, size_t have, size_t need) {
     return SSM_OK;
 }
 
-// Blocks of at most 512 threads: fewer than 2^32 work-items in a launch, and arrays whose sizes in
-// bytes fit 64 bits.
+// Blocks of at most 512 threads: fewer than 2^32 work-items in a launch; a chunk's rows, 64 x heads x 128
+// values, by offsets in 31 bits; and arrays whose sizes in bytes fit 64 bits.
 bool linattn_shape_ok(int64_t batch, int64_t L, int64_t heads, int64_t groups, int64_t K, int64_t V) {
     return batch >= 0 && L >= 0 && heads >= 1 && groups >= 1 && heads % groups == 0 && K >= 1 && K <= 128 && V >= 1 && V <= 128 &&
-           heads <= ((int64_t)1 << 20) && (double)batch * heads <= 1048576.0 && L <= ((int64_t)1 << 36) &&
+           heads <= 32768 && (double)batch * heads <= 1048576.0 && L <= ((int64_t)1 << 36) &&
            (double)batch * L * heads * 128 <= 8.8e12 && (double)batch * heads * 16384 * (double)(L / 32 + 1) <= 2.2e12;
 }
 
 ssm_status check_linattn(int64_t batch, int64_t L, int64_t heads, int64_t groups, int64_t K, int64_t V, ssm_dtype io, float scale) {
     if (!valid_io(io)) return fail(SSM_ERR_DTYPE, "io dtype %d unknown", (int)io);
     if (!linattn_shape_ok(batch, L, heads, groups, K, V))
-        return fail(SSM_ERR_SHAPE, "batch and L >= 0, heads a multiple of groups, batch x heads at most 2^20, d_k and d_v in 1..128");
+        return fail(SSM_ERR_SHAPE, "batch and L >= 0, heads at most 2^15 and a multiple of groups, batch x heads at most 2^20, d_k and d_v in 1..128");
     if (!isfinite(scale)) return fail(SSM_ERR_UNSUPPORTED, "scale must be finite");
     return SSM_OK;
 }

@@ -87,6 +87,9 @@ __device__ __forceinline__ void split(f32x4 x, f32x4 (&p)[1]) { p[0] = x; }
 __device__ __forceinline__ f32x8 widened(bf16x8 x) { return __builtin_convertvector(x, f32x8); }
 __device__ __forceinline__ f32x4 widened(f32x4 x) { return x; }
 
+// The compiler would read every fragment of a chunk from LDS before the first product, and spill.
+__device__ __forceinline__ void fence() { __builtin_amdgcn_sched_barrier(0); }
+
 // Step s of an accumulator's 32 rows as a fragment's elements.
 template <typename T>
 __device__ __forceinline__ typename Kind<T>::Wide rows_of(const f32x16 &acc, int s) {
@@ -124,29 +127,37 @@ struct Tile {
     static __device__ __forceinline__ int at(int row, int quad) {
         return (row * W + (quad ^ swizzle(row))) * 4 * (int)sizeof(T);
     }
-    // lanes: rows; contraction: columns KS s .. KS s + KS - 1
-    static __device__ __forceinline__ typename N::Frag by_row(const char *t, int row, int s, int half) {
+    // Rows start on multiples of their size, so a step or a block changes a lane's address by an exclusive
+    // or and a constant, and a lane keeps one number for each way of reading.
+    // lanes: rows; contraction: columns KS s .. KS s + KS - 1. from: at(row, half).
+    static __device__ __forceinline__ typename N::Frag by_row(const char *t, int from, int s) {
         if constexpr (sizeof(T) == 2) {
-            const bf16x4 lo = *(const bf16x4 *)(t + at(row, 4 * s + half)), hi = *(const bf16x4 *)(t + at(row, 4 * s + 2 + half));
+            const bf16x4 lo = *(const bf16x4 *)(t + (from ^ s * 32)), hi = *(const bf16x4 *)(t + (from ^ s * 32 ^ 16));
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
-            return *(const f32x4 *)(t + at(row, 2 * s + half));
+            return *(const f32x4 *)(t + (from ^ s * 32));
         }
     }
-    // lanes: columns 32 block + l % 32; contraction: rows KS s .. KS s + KS - 1
-    static __device__ __forceinline__ typename N::Frag by_column(const char *t, int block, int s, int lane) {
+    // lanes: columns 32 block + l % 32; contraction: rows KS s .. KS s + KS - 1. from: column_base(lane).
+    static __device__ __forceinline__ int column_base(int lane) {
         const int half = lane >> 5;
+        if constexpr (sizeof(T) == 2) return at(4 * half + (lane >> 2 & 3), (lane >> 4 & 1) * 4 + (lane & 3));
+        else return at(4 * half, lane >> 2 & 7) + (lane & 3) * 4;
+    }
+    static __device__ __forceinline__ typename N::Frag by_column(const char *t, int from, int block, int s) {
+        constexpr int kRow = W * 4 * (int)sizeof(T);
         if constexpr (sizeof(T) == 2) {
-            const int i = lane & 15, row = 16 * s + 4 * half + (i >> 2), quad = 8 * block + (lane >> 4 & 1) * 4 + (i & 3);
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)(t + at(row, quad)));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)(t + at(row + 8, quad)));
+            const int c = (s & 1) * 32 | block * 64;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)(t + (from ^ c) + s * 16 * kRow));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)(t + (from ^ c ^ 16) + (s * 16 + 8) * kRow));
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             f32x4 f;
-            const int c = lane & 31;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                f[e] = *(const float *)(t + at(8 * s + 4 * half + e, 8 * block + (c >> 2)) + (c & 3) * 4);
+            for (int e = 0; e < 4; ++e) {
+                const int c = (e | (s & 1) << 2 | (W == 32 ? (s >> 1 & 1) << 4 : 0)) * 16 ^ block * 128;
+                f[e] = *(const float *)(t + (from ^ c) + (8 * s + e) * kRow);
+            }
             return f;
         }
     }
@@ -157,39 +168,66 @@ struct Tile {
     }
 };
 
-// A tile's way from global memory to LDS through registers: rows of `width` elements, `stride`
-// apart; rows past `rows` and columns past `width` become 0.
-template <typename T, int ROWS, int F, int THREADS>
-struct Stage {
-    static constexpr int kElems = 16 / sizeof(T), kPerRow = F / kElems, N = (ROWS * kPerRow + THREADS - 1) / THREADS;
-    static constexpr bool kWhole = ROWS * kPerRow % THREADS == 0;
-    u32x4 r[N];
-    __device__ __forceinline__ void load(const T *p, int64_t stride, int rows, int width, bool wide) {
+// A range of global memory by offsets in 32 bits: what lies outside reads as 0 and is not written. All of an
+// offset is given as the vector one, since the scalar one is not compared with the range. kOut is outside of
+// every range, and so is what is added to it here.
+constexpr int kOut = (int)0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t range_of(const void *p, int64_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)bytes, 0x00020000);
+}
+// Four float32 or bfloat16 values at element e of a row that starts at byte `at`; `width` elements long.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void put_quad(__amdgpu_buffer_rsrc_t to, int at, int e, int width, f32x4 x) {
+    if constexpr (WIDE) {
+        const int o = e < width ? at + e * (int)sizeof(T) : kOut;
+        if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(x, bf16x4)), to, o, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), to, o, 0, 0);
+    } else {
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int e = threadIdx.x + n * THREADS, row = e / kPerRow, c = e % kPerRow * kElems;
-            const T *from = p + row * stride + c;
-            u32x4 got = {0, 0, 0, 0};
-            if (row < rows && c < width) {  // rows <= ROWS
-                if (wide) {
-                    got = *(const u32x4 *)from;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kElems; ++k)
-                        if (c + k < width) {
-                            if constexpr (sizeof(T) == 2) got[k / 2] |= (uint32_t)((const uint16_t *)from)[k] << (k % 2 * 16);
-                            else got[k] = ((const uint32_t *)from)[k];
-                        }
-                }
-            }
-            r[n] = got;
+        for (int k = 0; k < 4; ++k) {
+            const int o = e + k < width ? at + (e + k) * (int)sizeof(T) : kOut;
+            if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (__bf16)x[k]), to, o, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[k]), to, o, 0, 0);
         }
     }
-    __device__ __forceinline__ void store(char *t) const {
+}
+
+// A tile's way from global memory to LDS through registers: rows of `width` elements, `stride` bytes
+// apart; rows past `rows` and columns past `width` become 0.
+template <typename T, int ROWS, int F, int THREADS, bool WIDE>
+struct Stage {
+    static constexpr int kElems = 16 / sizeof(T), kPerRow = F / kElems, kStep = THREADS / kPerRow;
+    static constexpr int N = (ROWS + kStep - 1) / kStep;
+    static_assert(THREADS % kPerRow == 0, "a thread keeps its column");
+    u32x4 r[N];
+    __device__ __forceinline__ void load(const T *p, int stride, int rows, int width, int tid) {
+        const int row = tid / kPerRow, c = tid % kPerRow * kElems;
+        const __amdgpu_buffer_rsrc_t from = range_of(p, (int64_t)(rows - 1) * stride + width * (int64_t)sizeof(T));
+        const int o = row * stride + c * (int)sizeof(T);
+        if constexpr (WIDE) {
+            const int at = c < width ? o : kOut;
+#pragma unroll
+            for (int n = 0; n < N; ++n) r[n] = __builtin_amdgcn_raw_buffer_load_b128(from, at + n * kStep * stride, 0, 0);
+        } else {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                u32x4 got = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < kElems; ++k) {
+                    const int at = c + k < width ? o + k * (int)sizeof(T) : kOut;
+                    if constexpr (sizeof(T) == 2) got[k / 2] |= (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(from, at + n * kStep * stride, 0, 0) << (k % 2 * 16);
+                    else got[k] = __builtin_amdgcn_raw_buffer_load_b32(from, at + n * kStep * stride, 0, 0);
+                }
+                r[n] = got;
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(char *t, int tid) const {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int e = threadIdx.x + n * THREADS, row = e / kPerRow, c = e % kPerRow;
-            if (!kWhole && row >= ROWS) break;
+            const int row = tid / kPerRow + n * kStep, c = tid % kPerRow;
+            if (ROWS % kStep != 0 && row >= ROWS) break;
             if constexpr (sizeof(T) == 2) {
                 *(u32x2 *)(t + Tile<T, ROWS, F>::at(row, 2 * c)) = u32x2{r[n][0], r[n][1]};
                 *(u32x2 *)(t + Tile<T, ROWS, F>::at(row, 2 * c + 1)) = u32x2{r[n][2], r[n][3]};
@@ -251,36 +289,36 @@ struct SweepArgs {
     int64_t L, g_batch, g_token;  // strides of g (0, 0 for [H])
     int32_t H, Hk, K, V, nseg, nchunk, per_seg, slices;
     float scale;
-    bool wide_k, wide_v, wide_o;
     bool reverse;             // the state pass runs from the end, with weights scale e^{G_i}
 };
 
+// A state [K][V] and an accumulator whose lanes are columns of V: row 32 t + 8 (r / 4) + 4 half + r % 4.
 template <int TILES>
 __device__ __forceinline__ void state_load(f32x16 (&S)[TILES], const float *p, int K, int V, int v, int half) {
+    const __amdgpu_buffer_rsrc_t from = range_of(p, p ? (int64_t)K * V * 4 : 0);
+    const int at = v < V ? (4 * half * V + v) * 4 : kOut;
 #pragma unroll
     for (int t = 0; t < TILES; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int k = t * 32 + 8 * (r / 4) + 4 * half + r % 4;
-            S[t][r] = p && k < K && v < V ? p[(int64_t)k * V + v] : 0.0f;
-        }
+        for (int r = 0; r < 16; ++r)
+            S[t][r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(from, at + (t * 32 + 8 * (r / 4) + r % 4) * V * 4, 0, 0));
 }
 template <int TILES>
 __device__ __forceinline__ void state_store(const f32x16 (&S)[TILES], float *p, int K, int V, int v, int half) {
+    const __amdgpu_buffer_rsrc_t to = range_of(p, (int64_t)K * V * 4);
+    const int at = v < V ? (4 * half * V + v) * 4 : kOut;
 #pragma unroll
     for (int t = 0; t < TILES; ++t)
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int k = t * 32 + 8 * (r / 4) + 4 * half + r % 4;
-            if (k < K && v < V) p[(int64_t)k * V + v] = S[t][r];
-        }
+        for (int r = 0; r < 16; ++r)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[t][r]), to, at + (t * 32 + 8 * (r / 4) + r % 4) * V * 4, 0, 0);
 }
 
 // S = whole S + sum over the chunk's tokens of w_j k_j v_j^T: k by columns of its tile, the wave's v
 // fragments weighed in float32 and split.
 template <typename T, int C, int KP, int TILES>
 __device__ __forceinline__ void state_add(f32x16 (&S)[TILES], const char *k_tile, const typename Kind<T>::Frag *v,
-                                          const float *w, float whole, int lane) {
+                                          const float *w, float whole, int half, int columns) {
     typedef Kind<T> N;
 #pragma unroll
     for (int t = 0; t < TILES; ++t)
@@ -289,36 +327,22 @@ __device__ __forceinline__ void state_add(f32x16 (&S)[TILES], const char *k_tile
 #pragma unroll
     for (int s = 0; s < C / N::KS; ++s) {
         typename N::Wide wv;
-        weights_of(w, s, lane >> 5, wv);
+        weights_of(w, s, half, wv);
         typename N::Frag part[N::kParts];
         split(widened(v[s]) * wv, part);
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-            const typename N::Frag a = Tile<T, C, KP>::by_column(k_tile, t, s, lane);
+            const typename N::Frag a = Tile<T, C, KP>::by_column(k_tile, columns, t, s);
 #pragma unroll
             for (int p = 0; p < N::kParts; ++p) S[t] = mfma(a, part[p], S[t]);
         }
-    }
-}
-
-// Four values of a row of the output, at elements e .. e + 3 of `width`.
-template <typename T>
-__device__ __forceinline__ void put_row(T *row, int e, int width, bool wide, f32x4 x) {
-    if (wide) {
-        if (e < width) {
-            if constexpr (sizeof(T) == 2) *(bf16x4 *)(row + e) = __builtin_convertvector(x, bf16x4);
-            else *(f32x4 *)(row + e) = x;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (e + k < width) row[e + k] = (T)x[k];
+        fence();
     }
 }
 
 // One sweep over a segment of a sequence's chunks for NW x 32 columns of one head's state. OUT: with
 // outputs, from the segment's entering state; else what the segment adds to the state, from 0.
-template <typename T, int KP, int NW, bool OUT>
+template <typename T, int KP, int NW, bool OUT, bool WIDE>
 __global__ void __launch_bounds__(64 * NW) k_sweep(SweepArgs p) {
     typedef Kind<T> N;
     typedef typename N::Frag Frag;
@@ -330,7 +354,7 @@ __global__ void __launch_bounds__(64 * NW) k_sweep(SweepArgs p) {
     __shared__ Decays<C> dec;
     char *const kt = lds, *const vt = lds + TK::kBytes, *const qt = vt + TV::kBytes, *const pt = qt + TK::kBytes;
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, l31 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t work = work_of_block();
     const int slice = work % p.slices;
     work /= p.slices;
@@ -342,27 +366,27 @@ __global__ void __launch_bounds__(64 * NW) k_sweep(SweepArgs p) {
     const int hk = work % p.Hk, h = hk * share + sub;
     const int64_t b = work / p.Hk, bh = b * p.H + h;
     const int c0 = seg * p.per_seg, c1 = min(c0 + p.per_seg, p.nchunk), n = c1 - c0;
-    const int v0 = slice * VT, vcol = v0 + wave * 32 + l31;
+    const int v0 = slice * VT;
     const int64_t KV = (int64_t)p.K * p.V;
     const int nseg_all = OUT ? p.nseg : p.nseg + 1;
 
+    int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l31 = lane & 31, vcol = v0 + wave * 32 + l31;
     f32x16 S[KT];
     {
         const float *from = nullptr;
         if (OUT) from = p.seg_in ? p.seg_in + (bh * nseg_all + seg) * KV : p.first ? p.first + bh * KV : nullptr;
         state_load<KT>(S, from, p.K, p.V, vcol, half);
     }
-    Stage<T, C, KP, THREADS> kr, qr;
-    Stage<T, C, VT, THREADS> vr;
+    Stage<T, C, KP, THREADS, WIDE> kr, qr;
+    Stage<T, C, VT, THREADS, WIDE> vr;
     float g = 0.0f;
-    const int64_t ks = (int64_t)p.Hk * p.K, vs = (int64_t)p.H * p.V;
+    const int ks = p.Hk * p.K * (int)sizeof(T), vs = p.H * p.V * (int)sizeof(T);  // bytes of a token
     auto fetch = [&](int c) {
-        const int64_t t0 = (int64_t)c * C;
+        const int64_t t0 = (int64_t)c * C, at = b * p.L + t0;
         const int rows = (int)min((int64_t)C, p.L - t0);
-        const int64_t at = b * p.L + t0;
-        kr.load((const T *)p.k + at * ks + (int64_t)hk * p.K, ks, rows, p.K, p.wide_k);
-        vr.load((const T *)p.v + at * vs + (int64_t)h * p.V + v0, vs, rows, p.V - v0, p.wide_v);
-        if (OUT) qr.load((const T *)p.q + at * ks + (int64_t)hk * p.K, ks, rows, p.K, p.wide_k);
+        kr.load((const T *)((const char *)p.k + at * ks) + (int64_t)hk * p.K, ks, rows, p.K, tid);
+        vr.load((const T *)((const char *)p.v + at * vs) + (int64_t)h * p.V + v0, vs, rows, p.V - v0, tid);
+        if (OUT) qr.load((const T *)((const char *)p.q + at * ks) + (int64_t)hk * p.K, ks, rows, p.K, tid);
         if (wave == 0) g = lane < rows ? p.g[b * p.g_batch + (t0 + lane) * p.g_token + h] : 0.0f;
     };
     const bool rev = !OUT && p.reverse;
@@ -371,15 +395,23 @@ __global__ void __launch_bounds__(64 * NW) k_sweep(SweepArgs p) {
     bool cut = false;
     for (int it = 0; it < n; ++it) {
         const int c = rev ? c1 - 1 - it : c0 + it;
-        kr.store(kt);
-        vr.store(vt);
-        if (OUT) qr.store(qt);
+        // Lanes' addresses are made anew in every chunk: kept over the loop, they fill the registers.
+        asm volatile("" : "+v"(tid));
+        lane = tid & 63;
+        half = lane >> 5;
+        l31 = lane & 31;
+        vcol = v0 + wave * 32 + l31;
+        kr.store(kt, tid);
+        vr.store(vt, tid);
+        if (OUT) qr.store(qt, tid);
         if (wave == 0) {
             dec.make(g, lane);
             if (rev && lane < C) dec.start[lane] *= p.scale;
         }
         __syncthreads();
         if (it + 1 < n) fetch(rev ? c - 1 : c + 1);
+        const int kcol = TK::column_base(lane), krow = TK::at(l31, half), prow = TP::at(l31, half);
+        constexpr int kDown = 32 * TK::kBytes / C, pDown = 32 * TP::kBytes / C;  // 32 rows further
         if (OUT) {
             if (p.states) state_store<KT>(S, p.states + (bh * p.nchunk + c) * KV, p.K, p.V, vcol, half);
             // scores q k^T e^{G_i - G_j}, lanes i, in quads of j
@@ -387,8 +419,10 @@ __global__ void __launch_bounds__(64 * NW) k_sweep(SweepArgs p) {
                 const int it2 = t > 0, jt = t == 2, i = it2 * 32 + l31;
                 f32x16 acc = {};
 #pragma unroll
-                for (int s = 0; s < KP / KS; ++s)
-                    acc = mfma(TK::by_row(kt, jt * 32 + l31, s, half), TK::by_row(qt, i, s, half), acc);
+                for (int s = 0; s < KP / KS; ++s) {
+                    acc = mfma(TK::by_row(kt + jt * kDown, krow, s), TK::by_row(qt + it2 * kDown, krow, s), acc);
+                    if (s % 4 == 3) fence();
+                }
                 const double Gi = dec.G[i];
                 const int di = dec.doc[i];
 #pragma unroll
@@ -399,13 +433,17 @@ __global__ void __launch_bounds__(64 * NW) k_sweep(SweepArgs p) {
                     for (int e = 0; e < 4; ++e)
                         x[e] = acc[4 * a + e] * (p.scale * dec.between(Gi, di, dec.G[j0 + e], dec.doc[j0 + e], j0 + e <= i));
                     TP::put(pt, i, j0 / 4, x);
+                    fence();
                 }
             }
             __syncthreads();
         }
         Frag v[C / KS];
+        {
+            const int vcolumn = TV::column_base(lane);
 #pragma unroll
-        for (int s = 0; s < C / KS; ++s) v[s] = TV::by_column(vt, wave, s, lane);
+            for (int s = 0; s < C / KS; ++s) v[s] = TV::by_column(vt, vcolumn ^ (wave * 32 * (int)sizeof(T)), 0, s);
+        }
         if (OUT) {
             f32x16 o[TT] = {};
 #pragma unroll
@@ -414,27 +452,29 @@ __global__ void __launch_bounds__(64 * NW) k_sweep(SweepArgs p) {
                 for (int s = 0; s < 32 / KS; ++s) {
                     const Frag a = rounded(rows_of<T>(S[t], s));
 #pragma unroll
-                    for (int i = 0; i < TT; ++i) o[i] = mfma(a, TK::by_row(qt, i * 32 + l31, t * (32 / KS) + s, half), o[i]);
+                    for (int i = 0; i < TT; ++i) o[i] = mfma(a, TK::by_row(qt + i * kDown, krow, t * (32 / KS) + s), o[i]);
+                    if (s % 2) fence();
                 }
             const int64_t t0 = (int64_t)c * C;
+            const int rows = (int)min((int64_t)C, p.L - t0);
+            const __amdgpu_buffer_rsrc_t to = range_of((const char *)p.o + (b * p.L + t0) * vs + (int64_t)h * p.V * (int)sizeof(T),
+                                                       (int64_t)(rows - 1) * vs + p.V * (int64_t)sizeof(T));
 #pragma unroll
             for (int i = 0; i < TT; ++i) {
                 const float w = dec.start[i * 32 + l31] * p.scale;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[i][r] = w == 0.0f ? 0.0f : o[i][r] * w;
 #pragma unroll
-                for (int s = 0; s < (i + 1) * (32 / KS); ++s) o[i] = mfma(v[s], TP::by_row(pt, i * 32 + l31, s, half), o[i]);
-                const int64_t t = t0 + i * 32 + l31;
-                if (t < p.L) {
-                    T *const row = (T *)p.o + ((b * p.L + t) * p.H + h) * p.V;
+                for (int s = 0; s < (i + 1) * (32 / KS); ++s) o[i] = mfma(v[s], TP::by_row(pt + i * pDown, prow, s), o[i]);
+                const int row = i * 32 + l31;
 #pragma unroll
-                    for (int a = 0; a < 4; ++a)
-                        put_row<T>(row, v0 + wave * 32 + 8 * a + 4 * half, p.V, p.wide_o,
-                                   f32x4{o[i][4 * a], o[i][4 * a + 1], o[i][4 * a + 2], o[i][4 * a + 3]});
-                }
+                for (int a = 0; a < 4; ++a)
+                    put_quad<T, WIDE>(to, row < rows ? row * vs : kOut, v0 + wave * 32 + 8 * a + 4 * half, row < rows ? p.V : 0,
+                                f32x4{o[i][4 * a], o[i][4 * a + 1], o[i][4 * a + 2], o[i][4 * a + 3]});
+                fence();
             }
         }
-        state_add<T, C, KP, KT>(S, kt, v, rev ? dec.start : dec.end, dec.whole, lane);
+        state_add<T, C, KP, KT>(S, kt, v, rev ? dec.start : dec.end, dec.whole, half, kcol);
         if (!OUT) {
             decayed += dec.G[C - 1];
             cut |= dec.whole == 0.0f;
@@ -478,12 +518,11 @@ struct BwdArgs {
     int64_t L, g_batch, g_token;
     int32_t H, Hk, K, V, nseg, nchunk, per_seg;
     float scale;
-    bool wide_k, wide_v, wide_s, wide_dk, wide_dv;
 };
 
 // The gradients of a segment, from its end. VP / 32 waves hold dS by columns of V and make dv;
 // KP / 32 waves hold it transposed, by columns of K, and make dk and dq.
-template <typename T, int KP, int VP>
+template <typename T, int KP, int VP, bool WIDE>
 __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     typedef Kind<T> N;
     typedef typename N::Frag Frag;
@@ -500,7 +539,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     char *const qt = lds, *const kt = qt + TK::kBytes, *const vt = kt + TK::kBytes, *const dt = vt + TV::kBytes;
     char *const at = dt + TV::kBytes, *const bt = at + TP::kBytes, *const bn = bt + TP::kBytes, *const mt = bn + TP::kBytes;
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = lane >> 5, l31 = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t work = work_of_block();
     const int share = p.H / p.Hk, sub = work % share;
     work /= share;
@@ -511,64 +550,76 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     const int c0 = seg * p.per_seg, c1 = min(c0 + p.per_seg, p.nchunk), n = c1 - c0;
     const int64_t KV = (int64_t)p.K * p.V;
     const bool of_v = wave < VW;          // this wave makes dv
-    const int part = of_v ? wave : wave - VW, col = part * 32 + l31;
+    const int part = of_v ? wave : wave - VW;
+    int tid = threadIdx.x, lane = tid & 63, half = lane >> 5, l31 = lane & 31;
 
     f32x16 S[kMost];                      // dS [k rows][col of V], or dS^T [v rows][col of K]
+    f32x16(&SV)[KT] = reinterpret_cast<f32x16(&)[KT]>(S);
+    f32x16(&SK)[VW] = reinterpret_cast<f32x16(&)[VW]>(S);
     {
         const float *from = p.seg_in ? p.seg_in + (bh * p.nseg + seg) * KV : p.dlast ? p.dlast + bh * KV : nullptr;
+        if (of_v) {
+            state_load<KT>(SV, from, p.K, p.V, part * 32 + l31, half);
+        } else {
+            const __amdgpu_buffer_rsrc_t rows = range_of(from, from ? KV * 4 : 0);
+            const int at = ((part * 32 + l31) * p.V + 4 * half) * 4;
 #pragma unroll
-        for (int t = 0; t < kMost; ++t)
+            for (int t = 0; t < VW; ++t)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int row = t * 32 + 8 * (r / 4) + 4 * half + r % 4, k = of_v ? row : col, v = of_v ? col : row;
-                S[t][r] = from && k < p.K && v < p.V ? from[(int64_t)k * p.V + v] : 0.0f;
-            }
+                for (int r = 0; r < 16; ++r) {
+                    const int v = t * 32 + 8 * (r / 4) + r % 4;
+                    SK[t][r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rows, v + 4 * half < p.V ? at + 4 * v : kOut, 0, 0));
+                }
+        }
     }
-    Stage<T, C, KP, THREADS> qr, kr;
-    Stage<T, C, VP, THREADS> vr, dr;
+    Stage<T, C, KP, THREADS, WIDE> qr, kr;
+    Stage<T, C, VP, THREADS, WIDE> vr, dr;
     float g = 0.0f;
-    const int64_t ks = (int64_t)p.Hk * p.K, vs = (int64_t)p.H * p.V;
+    const int ks = p.Hk * p.K * (int)sizeof(T), vs = p.H * p.V * (int)sizeof(T);  // bytes of a token
+    const int dks = share == 1 ? ks : p.H * p.K * 4;                              // and of one of dq and dk
     auto fetch = [&](int c) {
-        const int64_t t0 = (int64_t)c * C;
+        const int64_t t0 = (int64_t)c * C, from = b * p.L + t0;
         const int rows = (int)min((int64_t)C, p.L - t0);
-        const int64_t from = b * p.L + t0;
-        qr.load((const T *)p.q + from * ks + (int64_t)hk * p.K, ks, rows, p.K, p.wide_k);
-        kr.load((const T *)p.k + from * ks + (int64_t)hk * p.K, ks, rows, p.K, p.wide_k);
-        vr.load((const T *)p.v + from * vs + (int64_t)h * p.V, vs, rows, p.V, p.wide_v);
-        dr.load((const T *)p.do_ + from * vs + (int64_t)h * p.V, vs, rows, p.V, p.wide_v);
+        qr.load((const T *)((const char *)p.q + from * ks) + (int64_t)hk * p.K, ks, rows, p.K, tid);
+        kr.load((const T *)((const char *)p.k + from * ks) + (int64_t)hk * p.K, ks, rows, p.K, tid);
+        vr.load((const T *)((const char *)p.v + from * vs) + (int64_t)h * p.V, vs, rows, p.V, tid);
+        dr.load((const T *)((const char *)p.do_ + from * vs) + (int64_t)h * p.V, vs, rows, p.V, tid);
         if (wave == 0) g = lane < rows ? p.g[b * p.g_batch + (t0 + lane) * p.g_token + h] : 0.0f;
     };
     if (n > 0) fetch(c1 - 1);
     for (int c = c1 - 1; c >= c0; --c) {
         const int64_t t0 = (int64_t)c * C;
-        qr.store(qt);
-        kr.store(kt);
-        vr.store(vt);
-        dr.store(dt);
+        const int rows = (int)min((int64_t)C, p.L - t0);
+        asm volatile("" : "+v"(tid));  // addresses are made anew, as in the sweep
+        lane = tid & 63;
+        half = lane >> 5;
+        l31 = lane & 31;
+        qr.store(qt, tid);
+        kr.store(kt, tid);
+        vr.store(vt, tid);
+        dr.store(dt, tid);
         if (wave == 0) {
             dec.make(g, lane);
             if (lane < C) back[lane] = dec.start[lane] * p.scale;
         }
         __syncthreads();
-        if (c > c0) fetch(c - 1);
+        constexpr int kDown = 32 * TK::kBytes / C, vDown = 32 * TV::kBytes / C, pDown = 32 * TP::kBytes / C;  // 32 rows further
+        const int krow = TK::at(l31, half), vrow = TV::at(l31, half), prow = TP::at(l31, half);
         // The state that entered this chunk, lanes k, in quads of v.
-        f32x4 in[kMost * 4];
+        f32x4 in[VW * 4];
         if (!of_v) {
-            const float *const from = p.states + (bh * p.nchunk + c) * KV + (int64_t)col * p.V;
+            const __amdgpu_buffer_rsrc_t from = range_of(p.states + (bh * p.nchunk + c) * KV, KV * 4);
+            const int at = ((part * 32 + l31) * p.V + 4 * half) * 4;
 #pragma unroll
             for (int a = 0; a < VW * 4; ++a) {
                 const int v = 8 * a + 4 * half;
-                f32x4 x = {0, 0, 0, 0};
-                if (col < p.K) {
-                    if (p.wide_s) {
-                        if (v < p.V) x = *(const f32x4 *)(from + v);
-                    } else {
+                if constexpr (WIDE) {
+                    in[a] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, v < p.V ? at + 32 * a : kOut, 0, 0));
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (v + e < p.V) x[e] = from[v + e];
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        in[a][e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(from, v + e < p.V ? at + 32 * a + 4 * e : kOut, 0, 0));
                 }
-                in[a] = x;
             }
         }
         // Scores: q k^T and do v^T with their decays. Tiles below the diagonal, each twice: lanes j
@@ -579,7 +630,10 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                 const int i = it * 32 + l31;
                 f32x16 acc = {};
 #pragma unroll
-                for (int s = 0; s < VP / KS; ++s) acc = mfma(TV::by_row(vt, jt * 32 + l31, s, half), TV::by_row(dt, i, s, half), acc);
+                for (int s = 0; s < VP / KS; ++s) {
+                    acc = mfma(TV::by_row(vt + jt * vDown, vrow, s), TV::by_row(dt + it * vDown, vrow, s), acc);
+                    if (s % 4 == 3) fence();
+                }
                 const double Gi = dec.G[i];
                 const int di = dec.doc[i];
 #pragma unroll
@@ -590,14 +644,21 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                     for (int e = 0; e < 4; ++e)
                         x[e] = acc[4 * a + e] * (p.scale * dec.between(Gi, di, dec.G[j0 + e], dec.doc[j0 + e], j0 + e <= i));
                     TP::put(bn, i, j0 / 4, x);
+                    fence();
                 }
             } else {
                 const int j = jt * 32 + l31;
                 f32x16 qk = {}, dov = {};
 #pragma unroll
-                for (int s = 0; s < KP / KS; ++s) qk = mfma(TK::by_row(qt, it * 32 + l31, s, half), TK::by_row(kt, j, s, half), qk);
+                for (int s = 0; s < KP / KS; ++s) {
+                    qk = mfma(TK::by_row(qt + it * kDown, krow, s), TK::by_row(kt + jt * kDown, krow, s), qk);
+                    if (s % 4 == 3) fence();
+                }
 #pragma unroll
-                for (int s = 0; s < VP / KS; ++s) dov = mfma(TV::by_row(dt, it * 32 + l31, s, half), TV::by_row(vt, j, s, half), dov);
+                for (int s = 0; s < VP / KS; ++s) {
+                    dov = mfma(TV::by_row(dt + it * vDown, vrow, s), TV::by_row(vt + jt * vDown, vrow, s), dov);
+                    if (s % 4 == 3) fence();
+                }
                 const double Gj = dec.G[j];
                 const int dj = dec.doc[j];
 #pragma unroll
@@ -614,124 +675,155 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                     TP::put(at, j, i0 / 4, x);
                     TP::put(bt, j, i0 / 4, y);
                     TM::put(mt, j, i0 / 4, m);
+                    fence();
                 }
             }
         }
         __syncthreads();
+        const int kcol = TK::column_base(lane), vcol = TV::column_base(lane);
         if (of_v) {
+            if (c > c0) fetch(c - 1);
             f32x16 acc[TT] = {};
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int s = 0; s < 32 / KS; ++s) {
-                    const Frag a = rounded(rows_of<T>(S[t], s));
+                    const Frag a = rounded(rows_of<T>(SV[t], s));
 #pragma unroll
-                    for (int j = 0; j < TT; ++j) acc[j] = mfma(a, TK::by_row(kt, j * 32 + l31, t * (32 / KS) + s, half), acc[j]);
+                    for (int j = 0; j < TT; ++j) acc[j] = mfma(a, TK::by_row(kt + j * kDown, krow, t * (32 / KS) + s), acc[j]);
+                    if (s % 2) fence();
                 }
             Frag d[C / KS];
 #pragma unroll
-            for (int s = 0; s < C / KS; ++s) d[s] = TV::by_column(dt, part, s, lane);
+            for (int s = 0; s < C / KS; ++s) d[s] = TV::by_column(dt, vcol ^ (part * 32 * (int)sizeof(T)), 0, s);
+            const __amdgpu_buffer_rsrc_t to = range_of((const char *)p.dv + (b * p.L + t0) * vs + (int64_t)h * p.V * (int)sizeof(T),
+                                                       (int64_t)(rows - 1) * vs + p.V * (int64_t)sizeof(T));
 #pragma unroll
             for (int j = 0; j < TT; ++j) {
                 const float w = dec.end[j * 32 + l31];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[j][r] = w == 0.0f ? 0.0f : acc[j][r] * w;
 #pragma unroll
-                for (int s = j * (32 / KS); s < C / KS; ++s) acc[j] = mfma(d[s], TP::by_row(at, j * 32 + l31, s, half), acc[j]);
-                const int64_t t = t0 + j * 32 + l31;
-                if (t < p.L) {
-                    T *const row = (T *)p.dv + ((b * p.L + t) * p.H + h) * p.V;
+                for (int s = j * (32 / KS); s < C / KS; ++s) acc[j] = mfma(d[s], TP::by_row(at + j * pDown, prow, s), acc[j]);
+                const int row = j * 32 + l31;
 #pragma unroll
-                    for (int a = 0; a < 4; ++a)
-                        put_row<T>(row, part * 32 + 8 * a + 4 * half, p.V, p.wide_dv,
-                                   f32x4{acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]});
-                }
+                for (int a = 0; a < 4; ++a)
+                    put_quad<T, WIDE>(to, row < rows ? row * vs : kOut, part * 32 + 8 * a + 4 * half, row < rows ? p.V : 0,
+                                f32x4{acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]});
+                fence();
             }
-            f32x16(&D)[KT] = reinterpret_cast<f32x16(&)[KT]>(S);
-            state_add<T, C, KP, KT>(D, qt, d, back, dec.whole, lane);
+            state_add<T, C, KP, KT>(SV, qt, d, back, dec.whole, half, kcol);
         } else {
-            f32x16 ak[TT] = {}, aq[TT] = {};
-            float x = 0.0f;
+            // What of dq comes from earlier chunks, then what of dk comes from later ones; each with its share of
+            // dg, before the chunk's own part is added. The next chunk is loaded in between, into the
+            // registers that held the entering state.
+            const auto own = [&](f32x16(&acc)[TT], const char *tile, const float *decay, float *share_of) {
 #pragma unroll
-            for (int t = 0; t < VW; ++t)
+                for (int j = 0; j < TT; ++j) {
+                    const float w = decay[j * 32 + l31];
+                    float sum = 0.0f;
 #pragma unroll
-                for (int s = 0; s < 32 / KS; ++s) {
-                    typename N::Wide w = rows_of<T>(S[t], s), u;
-                    constexpr int Q = sizeof(w) / 16;  // quads of a fragment
+                    for (int s = 0; s < 32 / KS; ++s) {  // this wave's 32 columns of k or q, in quads
+                        const typename N::Wide x = widened(TK::by_row(tile + j * kDown, krow ^ (part * 32 * (int)sizeof(T)), s));
+                        constexpr int E = sizeof(x) / 4;
 #pragma unroll
-                    for (int e = 0; e < 4 * Q; ++e) {
-                        u[e] = in[(t * (32 / KS) + s) * Q + e / 4][e % 4];
-                        x += u[e] * w[e];
-                    }
-                    Frag pk[N::kParts], pq[N::kParts];
-                    split(w, pk);
-                    split(u, pq);
-                    const int step = t * (32 / KS) + s;
-#pragma unroll
-                    for (int j = 0; j < TT; ++j) {
-                        const Frag fv = TV::by_row(vt, j * 32 + l31, step, half), fd = TV::by_row(dt, j * 32 + l31, step, half);
-#pragma unroll
-                        for (int e = 0; e < N::kParts; ++e) {
-                            ak[j] = mfma(pk[e], fv, ak[j]);
-                            aq[j] = mfma(pq[e], fd, aq[j]);
+                        for (int e = 0; e < E; ++e) {
+                            const float r = w == 0.0f ? 0.0f : acc[j][s * E + e] * w;
+                            acc[j][s * E + e] = r;
+                            sum += x[e] * r;
                         }
                     }
+                    sum += __shfl_xor(sum, 32);
+                    if (half == 0) share_of[j * 32 + l31] = sum;
                 }
+            };
+            const auto put = [&](const f32x16(&acc)[TT], void *out) {
+                const int esz = share == 1 ? (int)sizeof(T) : 4;
+                const __amdgpu_buffer_rsrc_t to = range_of((const char *)out + (b * p.L + t0) * dks + (int64_t)(share == 1 ? hk : h) * p.K * esz,
+                                                           (int64_t)(rows - 1) * dks + p.K * (int64_t)esz);
+#pragma unroll
+                for (int j = 0; j < TT; ++j) {
+                    const int row = j * 32 + l31, width = row < rows ? p.K : 0;
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) {
+                        const int e = part * 32 + 8 * a + 4 * half;
+                        const f32x4 x = {acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]};
+                        if (share == 1) put_quad<T, WIDE>(to, row * dks, e, width, x);
+                        else put_quad<float, WIDE>(to, row * dks, e, width, x);
+                    }
+                    fence();
+                }
+            };
+            constexpr int Q = sizeof(typename N::Wide) / 16;  // quads of a fragment
+            float x = 0.0f;
+            const int column = kcol ^ (part * 32 * (int)sizeof(T));
+            {
+                f32x16 acc[TT] = {};
+#pragma unroll
+                for (int t = 0; t < VW; ++t)
+#pragma unroll
+                    for (int s = 0; s < 32 / KS; ++s) {
+                        const typename N::Wide w = rows_of<T>(SK[t], s);
+                        typename N::Wide u;
+#pragma unroll
+                        for (int e = 0; e < 4 * Q; ++e) {
+                            u[e] = in[(t * (32 / KS) + s) * Q + e / 4][e % 4];
+                            x += u[e] * w[e];
+                        }
+                        Frag pq[N::kParts];
+                        split(u, pq);
+#pragma unroll
+                        for (int j = 0; j < TT; ++j) {
+                            const Frag f = TV::by_row(dt + j * vDown, vrow, t * (32 / KS) + s);
+#pragma unroll
+                            for (int e = 0; e < N::kParts; ++e) acc[j] = mfma(pq[e], f, acc[j]);
+                        }
+                        fence();
+                    }
+                own(acc, qt, back, came[part]);
+#pragma unroll
+                for (int s = 0; s < C / KS; ++s) {
+                    const Frag f = TK::by_column(kt, column, 0, s);
+#pragma unroll
+                    for (int j = s / (32 / KS); j < TT; ++j) acc[j] = mfma(f, TP::by_row(bn + j * pDown, prow, s), acc[j]);
+                }
+                put(acc, p.dq);
+            }
+            if (c > c0) fetch(c - 1);
+            fence();
+            {
+                f32x16 acc[TT] = {};
+#pragma unroll
+                for (int t = 0; t < VW; ++t)
+#pragma unroll
+                    for (int s = 0; s < 32 / KS; ++s) {
+                        const typename N::Wide w = rows_of<T>(SK[t], s);
+                        Frag pk[N::kParts];
+                        split(w, pk);
+#pragma unroll
+                        for (int j = 0; j < TT; ++j) {
+                            const Frag f = TV::by_row(vt + j * vDown, vrow, t * (32 / KS) + s);
+#pragma unroll
+                            for (int e = 0; e < N::kParts; ++e) acc[j] = mfma(pk[e], f, acc[j]);
+                        }
+                        fence();
+                    }
+                own(acc, kt, dec.end, left[part]);
+#pragma unroll
+                for (int s = 0; s < C / KS; ++s) {
+                    const Frag f = TK::by_column(qt, column, 0, s);
+#pragma unroll
+                    for (int j = 0; j <= s / (32 / KS); ++j) acc[j] = mfma(f, TP::by_row(bt + j * pDown, prow, s), acc[j]);
+                }
+                put(acc, p.dk);
+            }
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
             if (lane == 0) through[part] = dec.whole == 0.0f ? 0.0f : x * dec.whole;
             Frag fq[C / KS];
 #pragma unroll
-            for (int s = 0; s < C / KS; ++s) fq[s] = TK::by_column(qt, part, s, lane);
-#pragma unroll
-            for (int j = 0; j < TT; ++j) {
-                const float wk = dec.end[j * 32 + l31], wq = back[j * 32 + l31];
-                float ck = 0.0f, cq = 0.0f;
-#pragma unroll
-                for (int s = 0; s < 32 / KS; ++s) {  // this wave's 32 columns of k and q, in quads
-                    const typename N::Wide xk = widened(TK::by_row(kt, j * 32 + l31, part * (32 / KS) + s, half));
-                    const typename N::Wide xq = widened(TK::by_row(qt, j * 32 + l31, part * (32 / KS) + s, half));
-                    constexpr int E = sizeof(xk) / 4;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float rk = wk == 0.0f ? 0.0f : ak[j][s * E + e] * wk, rq = wq == 0.0f ? 0.0f : aq[j][s * E + e] * wq;
-                        ak[j][s * E + e] = rk;
-                        aq[j][s * E + e] = rq;
-                        ck += xk[e] * rk;
-                        cq += xq[e] * rq;
-                    }
-                }
-                ck += __shfl_xor(ck, 32);
-                cq += __shfl_xor(cq, 32);
-                if (half == 0) {
-                    left[part][j * 32 + l31] = ck;
-                    came[part][j * 32 + l31] = cq;
-                }
-#pragma unroll
-                for (int s = j * (32 / KS); s < C / KS; ++s) ak[j] = mfma(fq[s], TP::by_row(bt, j * 32 + l31, s, half), ak[j]);
-#pragma unroll
-                for (int s = 0; s < (j + 1) * (32 / KS); ++s)
-                    aq[j] = mfma(TK::by_column(kt, part, s, lane), TP::by_row(bn, j * 32 + l31, s, half), aq[j]);
-                const int64_t t = t0 + j * 32 + l31;
-                if (t < p.L) {
-                    const int64_t tok = b * p.L + t;
-#pragma unroll
-                    for (int a = 0; a < 4; ++a) {
-                        const int e = part * 32 + 8 * a + 4 * half;
-                        const f32x4 xk = {ak[j][4 * a], ak[j][4 * a + 1], ak[j][4 * a + 2], ak[j][4 * a + 3]};
-                        const f32x4 xq = {aq[j][4 * a], aq[j][4 * a + 1], aq[j][4 * a + 2], aq[j][4 * a + 3]};
-                        if (share == 1) {
-                            put_row<T>((T *)p.dk + (tok * p.H + h) * p.K, e, p.K, p.wide_dk, xk);
-                            put_row<T>((T *)p.dq + (tok * p.H + h) * p.K, e, p.K, p.wide_dk, xq);
-                        } else {
-                            put_row<float>((float *)p.dk + (tok * p.H + h) * p.K, e, p.K, p.wide_dk, xk);
-                            put_row<float>((float *)p.dq + (tok * p.H + h) * p.K, e, p.K, p.wide_dk, xq);
-                        }
-                    }
-                }
-            }
-            f32x16(&D)[VW] = reinterpret_cast<f32x16(&)[VW]>(S);
-            state_add<T, C, VP, VW>(D, dt, fq, back, dec.whole, lane);
+            for (int s = 0; s < C / KS; ++s) fq[s] = TK::by_column(qt, column, 0, s);
+            state_add<T, C, VP, VW>(SK, dt, fq, back, dec.whole, half, vcol);
         }
         __syncthreads();
         if (wave == 0) {
@@ -778,13 +870,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
             if (lane < C && t0 + lane < p.L) p.dg[(b * p.L + t0 + lane) * p.H + h] = d;
         }
     }
-    if (p.dfirst && seg == 0) {
-        float *const to = p.dfirst + bh * KV;
-        if (of_v) {
-            f32x16(&D)[KT] = reinterpret_cast<f32x16(&)[KT]>(S);
-            state_store<KT>(D, to, p.K, p.V, col, half);
-        }
-    }
+    if (p.dfirst && seg == 0 && of_v) state_store<KT>(SV, p.dfirst + bh * KV, p.K, p.V, part * 32 + l31, half);
 }
 
 // Gradients of shared heads: the sum over a group's heads, rounded once.
@@ -887,16 +973,20 @@ Plan plan(int64_t B, int64_t L, int32_t H, int32_t V, int io, bool bwd) {
     return p;
 }
 
+// wide: rows and pointers allow vectors of 16 bytes. Others are read element by element, by the kernels of
+// the largest sizes.
 template <typename T, bool OUT>
-void sweep(const SweepArgs &a, int64_t blocks, hipStream_t s) {
-    const bool k128 = a.K > 64;
+void sweep(const SweepArgs &a, bool wide, int64_t blocks, hipStream_t s) {
     const int width = (a.V > 64 ? 128 : 64) / a.slices;
-    if (k128) {
-        if (width == 128) k_sweep<T, 128, 4, OUT><<<blocks, 256, 0, s>>>(a);
-        else k_sweep<T, 128, 2, OUT><<<blocks, 128, 0, s>>>(a);
+    if (!wide) {
+        if (width == 128) k_sweep<T, 128, 4, OUT, false><<<blocks, 256, 0, s>>>(a);
+        else k_sweep<T, 128, 2, OUT, false><<<blocks, 128, 0, s>>>(a);
+    } else if (a.K > 64) {
+        if (width == 128) k_sweep<T, 128, 4, OUT, true><<<blocks, 256, 0, s>>>(a);
+        else k_sweep<T, 128, 2, OUT, true><<<blocks, 128, 0, s>>>(a);
     } else {
-        if (width == 128) k_sweep<T, 64, 4, OUT><<<blocks, 256, 0, s>>>(a);
-        else k_sweep<T, 64, 2, OUT><<<blocks, 128, 0, s>>>(a);
+        if (width == 128) k_sweep<T, 64, 4, OUT, true><<<blocks, 256, 0, s>>>(a);
+        else k_sweep<T, 64, 2, OUT, true><<<blocks, 128, 0, s>>>(a);
     }
 }
 
@@ -914,22 +1004,20 @@ hipError_t run_fwd(const LinattnArgs &a, hipStream_t s) {
     p.nchunk = (int)pl.nchunk; p.per_seg = pl.per_seg; p.slices = pl.slices;
     p.scale = a.scale;
     constexpr int E = 16 / sizeof(T);
-    p.wide_k = a.K % E == 0 && aligned_to(a.q, 16) && aligned_to(a.k, 16);
-    p.wide_v = a.V % E == 0 && aligned_to(a.v, 16);
-    p.wide_o = a.V % 4 == 0 && aligned_to(a.o, 4 * sizeof(T));
+    const bool wide = a.K % E == 0 && a.V % E == 0 && aligned_to(a.q, 16) && aligned_to(a.k, 16) && aligned_to(a.v, 16) && aligned_to(a.o, 16);
     if (pl.nseg > 1) {
         SweepArgs q = p;
         q.nseg = pl.nseg - 1;
         q.seg_out = seg;
         q.seg_fac = fac;
-        sweep<T, false>(q, heads * q.nseg * q.slices, s);
+        sweep<T, false>(q, wide, heads * q.nseg * q.slices, s);
         k_join<<<(heads * KV + 255) / 256, 256, 0, s>>>(seg, fac, a.h0, KV, heads, pl.nseg, false);
         p.seg_in = seg;
     }
     p.nseg = pl.nseg;
     p.first = a.h0;
     p.o = a.o; p.last = a.h_final; p.states = a.states;
-    sweep<T, true>(p, heads * p.nseg * p.slices, s);
+    sweep<T, true>(p, wide, heads * p.nseg * p.slices, s);
     return hipGetLastError();
 }
 
@@ -973,16 +1061,13 @@ hipError_t run_bwd(const LinattnArgs &a, hipStream_t s) {
     p.g_token = a.per_token ? a.H : 0;
     p.nchunk = (int)pl.seg.nchunk; p.per_seg = pl.seg.per_seg; p.nseg = pl.seg.nseg;
     p.scale = a.scale;
-    p.wide_k = a.K % E == 0 && aligned_to(a.q, 16) && aligned_to(a.k, 16);
-    p.wide_v = a.V % E == 0 && aligned_to(a.v, 16) && aligned_to(a.do_, 16);
-    p.wide_s = a.V % 4 == 0 && aligned_to(a.states, 16);
+    bool wide = a.K % E == 0 && a.V % E == 0;
+    for (const void *x : {a.q, a.k, a.v, a.do_, (const void *)a.states, (const void *)a.dq, (const void *)a.dk, (const void *)a.dv})
+        wide &= aligned_to(x, 16);
     const bool shared = a.H != a.Hk;
     p.dq = shared ? ws + pl.dq : (char *)a.dq;
     p.dk = shared ? ws + pl.dk : (char *)a.dk;
     p.dv = a.dv;
-    const size_t quad = 4 * (shared ? 4 : sizeof(T));
-    p.wide_dk = a.K % 4 == 0 && aligned_to(p.dq, quad) && aligned_to(p.dk, quad);
-    p.wide_dv = a.V % 4 == 0 && aligned_to(a.dv, 4 * sizeof(T));
     p.dg = a.per_token ? a.dg : (float *)(ws + pl.dg);
     p.dlast = a.dh_final;
     p.dfirst = a.dh0;
@@ -993,19 +1078,21 @@ hipError_t run_bwd(const LinattnArgs &a, hipStream_t s) {
             q.L = a.L; q.H = a.H; q.Hk = a.Hk; q.K = a.K; q.V = a.V;
             q.g_batch = p.g_batch; q.g_token = p.g_token;
             q.nchunk = p.nchunk; q.per_seg = p.per_seg; q.nseg = p.nseg - 1; q.slices = pl.pass.slices;
-            q.scale = a.scale; q.wide_k = p.wide_k; q.wide_v = p.wide_v; q.reverse = true;
+            q.scale = a.scale; q.reverse = true;
             q.seg_out = seg; q.seg_fac = fac;
-            sweep<T, false>(q, heads * q.nseg * q.slices, s);
+            sweep<T, false>(q, wide, heads * q.nseg * q.slices, s);
             k_join<<<(heads * KV + 255) / 256, 256, 0, s>>>(seg, fac, a.dh_final, KV, heads, p.nseg, true);
             p.seg_in = seg;
         }
         const int64_t blocks = heads * p.nseg;
-        if (a.K > 64) {
-            if (a.V > 64) k_bwd<T, 128, 128><<<blocks, 512, 0, s>>>(p);
-            else k_bwd<T, 128, 64><<<blocks, 384, 0, s>>>(p);
+        if (!wide) {
+            k_bwd<T, 128, 128, false><<<blocks, 512, 0, s>>>(p);
+        } else if (a.K > 64) {
+            if (a.V > 64) k_bwd<T, 128, 128, true><<<blocks, 512, 0, s>>>(p);
+            else k_bwd<T, 128, 64, true><<<blocks, 384, 0, s>>>(p);
         } else {
-            if (a.V > 64) k_bwd<T, 64, 128><<<blocks, 384, 0, s>>>(p);
-            else k_bwd<T, 64, 64><<<blocks, 256, 0, s>>>(p);
+            if (a.V > 64) k_bwd<T, 64, 128, true><<<blocks, 384, 0, s>>>(p);
+            else k_bwd<T, 64, 64, true><<<blocks, 256, 0, s>>>(p);
         }
         if (shared && a.L > 0) {
             const int64_t n = a.B * a.L * a.Hk * a.K;
