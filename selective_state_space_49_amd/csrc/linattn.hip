@@ -320,22 +320,26 @@ template <typename T, int C, int KP, int TILES>
 __device__ __forceinline__ void state_add(f32x16 (&S)[TILES], const char *k_tile, const typename Kind<T>::Frag *v,
                                           const float *w, float whole, int half, int columns) {
     typedef Kind<T> N;
+    if (__builtin_amdgcn_readfirstlane(__float_as_int(whole)) == 0) {
 #pragma unroll
-    for (int t = 0; t < TILES; ++t)
+        for (int t = 0; t < TILES; ++t) S[t] = f32x16{};
+    } else {
 #pragma unroll
-        for (int r = 0; r < 16; ++r) S[t][r] = whole == 0.0f ? 0.0f : S[t][r] * whole;
+        for (int t = 0; t < TILES; ++t) S[t] *= whole;
+    }
 #pragma unroll
     for (int s = 0; s < C / N::KS; ++s) {
         typename N::Wide wv;
         weights_of(w, s, half, wv);
         typename N::Frag part[N::kParts];
         split(widened(v[s]) * wv, part);
+        typename N::Frag a[TILES];
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) {
-            const typename N::Frag a = Tile<T, C, KP>::by_column(k_tile, columns, t, s);
+        for (int t = 0; t < TILES; ++t) a[t] = Tile<T, C, KP>::by_column(k_tile, columns, t, s);
 #pragma unroll
-            for (int p = 0; p < N::kParts; ++p) S[t] = mfma(a, part[p], S[t]);
-        }
+        for (int p = 0; p < N::kParts; ++p)
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) S[t] = mfma(a[t], part[p], S[t]);
         fence();
     }
 }
@@ -343,7 +347,7 @@ __device__ __forceinline__ void state_add(f32x16 (&S)[TILES], const char *k_tile
 // One sweep over a segment of a sequence's chunks for NW x 32 columns of one head's state. OUT: with
 // outputs, from the segment's entering state; else what the segment adds to the state, from 0.
 template <typename T, int KP, int NW, bool OUT, bool WIDE>
-__global__ void __launch_bounds__(64 * NW) k_sweep(SweepArgs p) {
+__global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
     typedef Kind<T> N;
     typedef typename N::Frag Frag;
     constexpr int C = N::C, KS = N::KS, VT = 32 * NW, TT = C / 32, KT = KP / 32, THREADS = 64 * NW;
@@ -962,11 +966,13 @@ Plan plan(int64_t B, int64_t L, int32_t H, int32_t V, int io, bool bwd) {
     Plan p;
     p.nchunk = (L + chunk_of(io) - 1) / chunk_of(io);
     const int vp = V > 64 ? 128 : 64;
-    p.slices = 1;
-    if (!bwd && vp == 128 && B * H < 512) p.slices = 2;
-    const int64_t blocks = B * H * p.slices, want = bwd ? 256 : 512;
+    // Two blocks of 4 waves a compute unit. Two slices of V, which read q and k twice, where even segments
+    // of 8 chunks are too few.
+    const int64_t want = bwd ? 256 : 512, most = std::max<int64_t>(p.nchunk / 8, 1);
+    p.slices = !bwd && vp == 128 && B * H * most < want ? 2 : 1;
+    const int64_t blocks = B * H * p.slices;
     int64_t n = blocks > 0 ? (want + blocks - 1) / blocks : 1;
-    n = std::min(n, std::max<int64_t>(p.nchunk / 8, 1));
+    n = std::min(n, most);
     const int64_t per = std::max<int64_t>((p.nchunk + n - 1) / std::max<int64_t>(n, 1), 1);
     p.per_seg = (int)per;
     p.nseg = (int)std::max<int64_t>((p.nchunk + per - 1) / per, 1);
