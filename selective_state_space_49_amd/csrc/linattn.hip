@@ -192,6 +192,36 @@ __device__ __forceinline__ void put_quad(__amdgpu_buffer_rsrc_t to, int at, int 
     }
 }
 
+// Rows of a finished tile in LDS to global memory, 16 bytes a lane.
+template <typename T, int ROWS, int F, int THREADS, bool WIDE>
+__device__ __forceinline__ void put_rows(const char *t, __amdgpu_buffer_rsrc_t to, int stride, int rows, int width, int tid) {
+    constexpr int kElems = 16 / sizeof(T), kPerRow = F / kElems, kStep = THREADS / kPerRow, N = (ROWS + kStep - 1) / kStep;
+    const int c = tid % kPerRow;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int row = tid / kPerRow + n * kStep;
+        if (ROWS % kStep != 0 && row >= ROWS) break;
+        u32x4 x;
+        if constexpr (sizeof(T) == 2) {
+            const u32x2 lo = *(const u32x2 *)(t + Tile<T, ROWS, F>::at(row, 2 * c)), hi = *(const u32x2 *)(t + Tile<T, ROWS, F>::at(row, 2 * c + 1));
+            x = u32x4{lo[0], lo[1], hi[0], hi[1]};
+        } else {
+            x = *(const u32x4 *)(t + Tile<T, ROWS, F>::at(row, c));
+        }
+        const int o = row < rows ? row * stride + c * 16 : kOut, e = c * kElems;
+        if constexpr (WIDE) {
+            __builtin_amdgcn_raw_buffer_store_b128(x, to, e < width ? o : kOut, 0, 0);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kElems; ++k) {
+                const int w = e + k < width ? o + k * (int)sizeof(T) : kOut;
+                if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16((short)(x[k / 2] >> (k % 2 * 16)), to, w, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b32(x[k], to, w, 0, 0);
+            }
+        }
+    }
+}
+
 // A tile's way from global memory to LDS through registers: rows of `width` elements, `stride` bytes
 // apart; rows past `rows` and columns past `width` become 0.
 template <typename T, int ROWS, int F, int THREADS, bool WIDE>
@@ -202,7 +232,7 @@ struct Stage {
     u32x4 r[N];
     __device__ __forceinline__ void load(const T *p, int stride, int rows, int width, int tid) {
         const int row = tid / kPerRow, c = tid % kPerRow * kElems;
-        const __amdgpu_buffer_rsrc_t from = range_of(p, (int64_t)(rows - 1) * stride + width * (int64_t)sizeof(T));
+        const __amdgpu_buffer_rsrc_t from = range_of(p, rows > 0 ? (int64_t)(rows - 1) * stride + width * (int64_t)sizeof(T) : 0);
         const int o = row * stride + c * (int)sizeof(T);
         if constexpr (WIDE) {
             const int at = c < width ? o : kOut;
@@ -238,6 +268,16 @@ struct Stage {
     }
 };
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double x) {  // by DPP, 0 where no lane sends
+    const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(x), CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(x), CTRL, ROWS, 0xf, false);
+    return __hiloint2double(hi, lo);
+}
+__device__ __forceinline__ double lane_of(double x, int lane) {
+    return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(x), lane), __builtin_amdgcn_readlane(__double2loint(x), lane));
+}
+
 // The decays of a chunk, made by one wave: G in units of log 2, document numbers, and the decays
 // from the start to a token, from a token to the end, and over all of it.
 template <int C>
@@ -250,14 +290,15 @@ struct Decays {
     __device__ __forceinline__ void make(float g, int lane) {
         const bool cut = g < kCut;
         double sum = cut ? 0.0 : (double)g * kLog2e;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const double up = __shfl_up(sum, d);
-            if (lane >= d) sum += up;
-        }
+        sum += moved<0x111, 0xf>(sum);  // inclusive: within rows of 16 lanes, then of the rows
+        sum += moved<0x112, 0xf>(sum);
+        sum += moved<0x114, 0xf>(sum);
+        sum += moved<0x118, 0xf>(sum);
+        sum += moved<0x142, 0xa>(sum);
+        sum += moved<0x143, 0xc>(sum);
         const uint64_t cuts = __ballot(cut);
         const uint64_t upto = cuts & (~0ull >> (63 - lane));
-        const double all = __shfl(sum, C - 1);
+        const double all = lane_of(sum, C - 1);
         if (lane < C) {
             G[lane] = sum;
             doc[lane] = __popcll(upto);
@@ -354,9 +395,9 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
     typedef Tile<T, C, KP> TK;
     typedef Tile<T, C, VT> TV;
     typedef Tile<T, C, C> TP;
-    __shared__ __attribute__((aligned(256))) char lds[(OUT ? 2 : 1) * TK::kBytes + TV::kBytes + (OUT ? TP::kBytes : 0)];
-    __shared__ Decays<C> dec;
-    char *const kt = lds, *const vt = lds + TK::kBytes, *const qt = vt + TV::kBytes, *const pt = qt + TK::kBytes;
+    __shared__ __attribute__((aligned(256))) char lds[(OUT ? 2 : 1) * TK::kBytes + (OUT ? 2 : 1) * TV::kBytes + (OUT ? TP::kBytes : 0)];
+    __shared__ Decays<C> decays[2];
+    char *const kt = lds, *const vt = lds + TK::kBytes, *const qt = vt + TV::kBytes, *const pt = qt + TK::kBytes, *const ot = pt + TP::kBytes;
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t work = work_of_block();
@@ -383,41 +424,76 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
     }
     Stage<T, C, KP, THREADS, WIDE> kr, qr;
     Stage<T, C, VT, THREADS, WIDE> vr;
-    float g = 0.0f;
     const int ks = p.Hk * p.K * (int)sizeof(T), vs = p.H * p.V * (int)sizeof(T);  // bytes of a token
-    auto fetch = [&](int c) {
-        const int64_t t0 = (int64_t)c * C, at = b * p.L + t0;
-        const int rows = (int)min((int64_t)C, p.L - t0);
+    const bool rev = !OUT && p.reverse;
+    const auto chunk = [&](int it) { return rev ? c1 - 1 - it : c0 + it; };
+    const auto rows_at = [&](int c) { return (int)min((int64_t)C, p.L - (int64_t)c * C); };
+    // Past the last chunk nothing is read, but the registers are written: a fetch that is left out would keep
+    // their old contents alive through a chunk.
+    auto fetch = [&](int it) {
+        const int c = chunk(min(it, n - 1)), rows = it < n ? rows_at(c) : 0;
+        const int64_t at = b * p.L + (int64_t)c * C;
         kr.load((const T *)((const char *)p.k + at * ks) + (int64_t)hk * p.K, ks, rows, p.K, tid);
         vr.load((const T *)((const char *)p.v + at * vs) + (int64_t)h * p.V + v0, vs, rows, p.V - v0, tid);
         if (OUT) qr.load((const T *)((const char *)p.q + at * ks) + (int64_t)hk * p.K, ks, rows, p.K, tid);
-        if (wave == 0) g = lane < rows ? p.g[b * p.g_batch + (t0 + lane) * p.g_token + h] : 0.0f;
     };
-    const bool rev = !OUT && p.reverse;
-    if (n > 0) fetch(rev ? c1 - 1 : c0);
+    // One wave makes the decays, a chunk ahead, from a g that was loaded another chunk ahead.
+    const bool decides = wave == NW - 1;
+    float g = 0.0f;
+    const auto load_g = [&](int it) {
+        if (it >= n) return;
+        const int c = chunk(it);
+        const int64_t t = (int64_t)c * C + lane;
+        g = lane < rows_at(c) ? p.g[b * p.g_batch + t * p.g_token + h] : 0.0f;
+    };
+    const auto decide = [&](int it) {
+        Decays<C> &d = decays[it & 1];
+        d.make(g, lane);
+        if (rev && lane < C) d.start[lane] *= p.scale;
+    };
+    // The outputs of a chunk wait in LDS until the next one's loads are due: stores that are issued before
+    // loads are not waited for with them.
+    const auto put_outputs = [&](int c) {
+        const int rows = rows_at(c);
+        put_rows<T, C, VT, THREADS, WIDE>(ot, range_of((const char *)p.o + (b * p.L + (int64_t)c * C) * vs + ((int64_t)h * p.V + v0) * (int)sizeof(T),
+                                                       (int64_t)(rows - 1) * vs + (p.V - v0) * (int64_t)sizeof(T)),
+                                          vs, rows, p.V - v0, tid);
+    };
+    if (n > 0) {
+        if (decides) {
+            load_g(0);
+            decide(0);
+            load_g(1);
+        }
+        fetch(0);
+    }
     double decayed = 0.0;  // the sum of G over the segment, in units of log 2
     bool cut = false;
     for (int it = 0; it < n; ++it) {
-        const int c = rev ? c1 - 1 - it : c0 + it;
+        const int c = chunk(it);
         // Lanes' addresses are made anew in every chunk: kept over the loop, they fill the registers.
         asm volatile("" : "+v"(tid));
         lane = tid & 63;
         half = lane >> 5;
         l31 = lane & 31;
         vcol = v0 + wave * 32 + l31;
+        const Decays<C> &dec = decays[it & 1];
         kr.store(kt, tid);
         vr.store(vt, tid);
         if (OUT) qr.store(qt, tid);
-        if (wave == 0) {
-            dec.make(g, lane);
-            if (rev && lane < C) dec.start[lane] *= p.scale;
-        }
         __syncthreads();
-        if (it + 1 < n) fetch(rev ? c - 1 : c + 1);
+        if (OUT) {
+            if (p.states) state_store<KT>(S, p.states + (bh * p.nchunk + c) * KV, p.K, p.V, vcol, half);
+            if (it > 0) put_outputs(c - 1);
+        }
+        fetch(it + 1);
+        if (decides && it + 1 < n) {
+            decide(it + 1);
+            load_g(it + 2);
+        }
         const int kcol = TK::column_base(lane), krow = TK::at(l31, half), prow = TP::at(l31, half);
         constexpr int kDown = 32 * TK::kBytes / C, pDown = 32 * TP::kBytes / C;  // 32 rows further
         if (OUT) {
-            if (p.states) state_store<KT>(S, p.states + (bh * p.nchunk + c) * KV, p.K, p.V, vcol, half);
             // scores q k^T e^{G_i - G_j}, lanes i, in quads of j
             for (int t = wave; t < TT * (TT + 1) / 2; t += NW) {
                 const int it2 = t > 0, jt = t == 2, i = it2 * 32 + l31;
@@ -459,10 +535,6 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
                     for (int i = 0; i < TT; ++i) o[i] = mfma(a, TK::by_row(qt + i * kDown, krow, t * (32 / KS) + s), o[i]);
                     if (s % 2) fence();
                 }
-            const int64_t t0 = (int64_t)c * C;
-            const int rows = (int)min((int64_t)C, p.L - t0);
-            const __amdgpu_buffer_rsrc_t to = range_of((const char *)p.o + (b * p.L + t0) * vs + (int64_t)h * p.V * (int)sizeof(T),
-                                                       (int64_t)(rows - 1) * vs + p.V * (int64_t)sizeof(T));
 #pragma unroll
             for (int i = 0; i < TT; ++i) {
                 const float w = dec.start[i * 32 + l31] * p.scale;
@@ -470,11 +542,9 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
                 for (int r = 0; r < 16; ++r) o[i][r] = w == 0.0f ? 0.0f : o[i][r] * w;
 #pragma unroll
                 for (int s = 0; s < (i + 1) * (32 / KS); ++s) o[i] = mfma(v[s], TP::by_row(pt + i * pDown, prow, s), o[i]);
-                const int row = i * 32 + l31;
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
-                    put_quad<T, WIDE>(to, row < rows ? row * vs : kOut, v0 + wave * 32 + 8 * a + 4 * half, row < rows ? p.V : 0,
-                                f32x4{o[i][4 * a], o[i][4 * a + 1], o[i][4 * a + 2], o[i][4 * a + 3]});
+                    TV::put(ot, i * 32 + l31, wave * 8 + 2 * a + half, f32x4{o[i][4 * a], o[i][4 * a + 1], o[i][4 * a + 2], o[i][4 * a + 3]});
                 fence();
             }
         }
@@ -486,6 +556,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
         __syncthreads();
     }
     if (OUT) {
+        if (n > 0) put_outputs(c1 - 1);
         if (p.last && seg == p.nseg - 1) state_store<KT>(S, p.last + bh * KV, p.K, p.V, vcol, half);
     } else {
         const int64_t at = bh * nseg_all + seg;
@@ -536,12 +607,13 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     typedef Tile<T, C, VP> TV;
     typedef Tile<T, C, C> TP;
     typedef Tile<float, C, C> TM;
-    __shared__ __attribute__((aligned(256))) char lds[2 * TK::kBytes + 2 * TV::kBytes + 3 * TP::kBytes + TM::kBytes];
-    __shared__ Decays<C> dec;
-    __shared__ float back[C];             // scale e^{G_i}
+    __shared__ __attribute__((aligned(256))) char lds[3 * TK::kBytes + 3 * TV::kBytes + 3 * TP::kBytes + TM::kBytes];
+    __shared__ Decays<C> decays[2];
+    __shared__ float backs[2][C];         // scale e^{G_i}
     __shared__ float came[KT][C], left[KT][C], through[KT];
     char *const qt = lds, *const kt = qt + TK::kBytes, *const vt = kt + TK::kBytes, *const dt = vt + TV::kBytes;
     char *const at = dt + TV::kBytes, *const bt = at + TP::kBytes, *const bn = bt + TP::kBytes, *const mt = bn + TP::kBytes;
+    char *const ov = mt + TM::kBytes, *const oq = ov + TV::kBytes;  // dv and dq on their way out
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint32_t work = work_of_block();
@@ -578,22 +650,54 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     }
     Stage<T, C, KP, THREADS, WIDE> qr, kr;
     Stage<T, C, VP, THREADS, WIDE> vr, dr;
-    float g = 0.0f;
     const int ks = p.Hk * p.K * (int)sizeof(T), vs = p.H * p.V * (int)sizeof(T);  // bytes of a token
-    const int dks = share == 1 ? ks : p.H * p.K * 4;                              // and of one of dq and dk
-    auto fetch = [&](int c) {
-        const int64_t t0 = (int64_t)c * C, from = b * p.L + t0;
-        const int rows = (int)min((int64_t)C, p.L - t0);
+    const bool shared = share > 1;
+    const int ksz = shared ? 4 : (int)sizeof(T), dks = shared ? p.H * p.K * 4 : ks;  // of an element and a token of dq and dk
+    const auto rows_at = [&](int c) { return (int)min((int64_t)C, p.L - (int64_t)c * C); };
+    auto fetch = [&](int next) {
+        const int c = max(next, c0), rows = next >= c0 ? rows_at(c) : 0;
+        const int64_t from = b * p.L + (int64_t)c * C;
         qr.load((const T *)((const char *)p.q + from * ks) + (int64_t)hk * p.K, ks, rows, p.K, tid);
         kr.load((const T *)((const char *)p.k + from * ks) + (int64_t)hk * p.K, ks, rows, p.K, tid);
         vr.load((const T *)((const char *)p.v + from * vs) + (int64_t)h * p.V, vs, rows, p.V, tid);
         dr.load((const T *)((const char *)p.do_ + from * vs) + (int64_t)h * p.V, vs, rows, p.V, tid);
-        if (wave == 0) g = lane < rows ? p.g[b * p.g_batch + (t0 + lane) * p.g_token + h] : 0.0f;
     };
-    if (n > 0) fetch(c1 - 1);
+    const auto range_v = [&](int c) {
+        return range_of((const char *)p.dv + (b * p.L + (int64_t)c * C) * vs + (int64_t)h * p.V * (int)sizeof(T),
+                        (int64_t)(rows_at(c) - 1) * vs + p.V * (int64_t)sizeof(T));
+    };
+    const auto range_k = [&](void *out, int c) {
+        return range_of((const char *)out + (b * p.L + (int64_t)c * C) * dks + (int64_t)(shared ? h : hk) * p.K * ksz,
+                        (int64_t)(rows_at(c) - 1) * dks + p.K * (int64_t)ksz);
+    };
+    // As in the sweep: dv and dq (of T) wait in LDS until the next chunk's loads are due.
+    const auto put_outputs = [&](int c) {
+        put_rows<T, C, VP, THREADS, WIDE>(ov, range_v(c), vs, rows_at(c), p.V, tid);
+        if (!shared) put_rows<T, C, KP, THREADS, WIDE>(oq, range_k(p.dq, c), dks, rows_at(c), p.K, tid);
+    };
+    // And one wave makes the decays a chunk ahead.
+    const bool decides = wave == VW - 1;
+    float g = 0.0f;
+    const auto load_g = [&](int c) {
+        if (c >= c0) g = lane < rows_at(c) ? p.g[b * p.g_batch + ((int64_t)c * C + lane) * p.g_token + h] : 0.0f;
+    };
+    const auto decide = [&](int c) {
+        decays[c & 1].make(g, lane);
+        if (lane < C) backs[c & 1][lane] = decays[c & 1].start[lane] * p.scale;
+    };
+    if (n > 0) {
+        if (decides) {
+            load_g(c1 - 1);
+            decide(c1 - 1);
+            load_g(c1 - 2);
+        }
+        fetch(c1 - 1);
+    }
     for (int c = c1 - 1; c >= c0; --c) {
         const int64_t t0 = (int64_t)c * C;
-        const int rows = (int)min((int64_t)C, p.L - t0);
+        const int rows = rows_at(c);
+        const Decays<C> &dec = decays[c & 1];
+        const float *const back = backs[c & 1];
         asm volatile("" : "+v"(tid));  // addresses are made anew, as in the sweep
         lane = tid & 63;
         half = lane >> 5;
@@ -602,30 +706,29 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
         kr.store(kt, tid);
         vr.store(vt, tid);
         dr.store(dt, tid);
-        if (wave == 0) {
-            dec.make(g, lane);
-            if (lane < C) back[lane] = dec.start[lane] * p.scale;
-        }
         __syncthreads();
+        if (c + 1 < c1) put_outputs(c + 1);
         constexpr int kDown = 32 * TK::kBytes / C, vDown = 32 * TV::kBytes / C, pDown = 32 * TP::kBytes / C;  // 32 rows further
         const int krow = TK::at(l31, half), vrow = TV::at(l31, half), prow = TP::at(l31, half);
-        // The state that entered this chunk, lanes k, in quads of v.
-        f32x4 in[VW * 4];
-        if (!of_v) {
+        // The state that entered this chunk, lanes k, in quads of v; half of V at a time.
+        constexpr int kIn = VW * 2;
+        f32x4 in[kIn];
+        const auto load_in = [&](int part_v) {
             const __amdgpu_buffer_rsrc_t from = range_of(p.states + (bh * p.nchunk + c) * KV, KV * 4);
             const int at = ((part * 32 + l31) * p.V + 4 * half) * 4;
 #pragma unroll
-            for (int a = 0; a < VW * 4; ++a) {
-                const int v = 8 * a + 4 * half;
+            for (int a = 0; a < kIn; ++a) {
+                const int v = 8 * (a + part_v * kIn) + 4 * half;
                 if constexpr (WIDE) {
-                    in[a] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, v < p.V ? at + 32 * a : kOut, 0, 0));
+                    in[a] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, v < p.V ? at + 32 * (a + part_v * kIn) : kOut, 0, 0));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        in[a][e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(from, v + e < p.V ? at + 32 * a + 4 * e : kOut, 0, 0));
+                        in[a][e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(from, v + e < p.V ? at + 32 * (a + part_v * kIn) + 4 * e : kOut, 0, 0));
                 }
             }
-        }
+        };
+        if (!of_v) load_in(0);
         // Scores: q k^T and do v^T with their decays. Tiles below the diagonal, each twice: lanes j
         // (both products, and theirs for dg), and lanes i (do v^T).
         for (int task = wave; task < TT * (TT + 1); task += NW) {
@@ -685,8 +788,12 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
         }
         __syncthreads();
         const int kcol = TK::column_base(lane), vcol = TV::column_base(lane);
+        float pairs = 0.0f;
         if (of_v) {
-            if (c > c0) fetch(c - 1);
+            if (decides && c > c0) {
+                decide(c - 1);
+                load_g(c - 2);
+            }
             f32x16 acc[TT] = {};
 #pragma unroll
             for (int t = 0; t < KT; ++t)
@@ -700,8 +807,6 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
             Frag d[C / KS];
 #pragma unroll
             for (int s = 0; s < C / KS; ++s) d[s] = TV::by_column(dt, vcol ^ (part * 32 * (int)sizeof(T)), 0, s);
-            const __amdgpu_buffer_rsrc_t to = range_of((const char *)p.dv + (b * p.L + t0) * vs + (int64_t)h * p.V * (int)sizeof(T),
-                                                       (int64_t)(rows - 1) * vs + p.V * (int64_t)sizeof(T));
 #pragma unroll
             for (int j = 0; j < TT; ++j) {
                 const float w = dec.end[j * 32 + l31];
@@ -709,18 +814,41 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                 for (int r = 0; r < 16; ++r) acc[j][r] = w == 0.0f ? 0.0f : acc[j][r] * w;
 #pragma unroll
                 for (int s = j * (32 / KS); s < C / KS; ++s) acc[j] = mfma(d[s], TP::by_row(at + j * pDown, prow, s), acc[j]);
-                const int row = j * 32 + l31;
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
-                    put_quad<T, WIDE>(to, row < rows ? row * vs : kOut, part * 32 + 8 * a + 4 * half, row < rows ? p.V : 0,
-                                f32x4{acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]});
+                    TV::put(ov, j * 32 + l31, part * 8 + 2 * a + half, f32x4{acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]});
                 fence();
             }
+            fetch(c - 1);
+            fence();
             state_add<T, C, KP, KT>(SV, qt, d, back, dec.whole, half, kcol);
+            if (wave == 0) {
+                // dg's pairs. Row j becomes its sums from i on; then token t adds the rows before it.
+                if (lane < C) {
+                    float sum = 0.0f;
+                    for (int a = C / 4 - 1; a >= 0; --a) {
+                        f32x4 *const q4 = (f32x4 *)(mt + TM::at(lane, a));
+                        f32x4 m = *q4;
+#pragma unroll
+                        for (int e = 3; e >= 0; --e) {
+                            sum += m[e];
+                            m[e] = sum;
+                        }
+                        *q4 = m;
+                    }
+                }
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+                if (lane < C)
+#pragma unroll 8
+                    for (int j = 0; j < C - 1; ++j) {
+                        const float m = *(const float *)(mt + TM::at(j, lane >> 2) + (lane & 3) * 4);
+                        pairs += j < lane ? m : 0.0f;
+                    }
+            }
         } else {
-            // What of dq comes from earlier chunks, then what of dk comes from later ones; each with its share of
-            // dg, before the chunk's own part is added. The next chunk is loaded in between, into the
-            // registers that held the entering state.
+            // What of dq comes from earlier chunks and what of dk comes from later ones, each with its share of
+            // dg before the chunk's own part is added. The entering state is read in halves, so that its
+            // second half and the next chunk's tiles are on their way while others are worked on.
             const auto own = [&](f32x16(&acc)[TT], const char *tile, const float *decay, float *share_of) {
 #pragma unroll
                 for (int j = 0; j < TT; ++j) {
@@ -742,9 +870,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                 }
             };
             const auto put = [&](const f32x16(&acc)[TT], void *out) {
-                const int esz = share == 1 ? (int)sizeof(T) : 4;
-                const __amdgpu_buffer_rsrc_t to = range_of((const char *)out + (b * p.L + t0) * dks + (int64_t)(share == 1 ? hk : h) * p.K * esz,
-                                                           (int64_t)(rows - 1) * dks + p.K * (int64_t)esz);
+                const __amdgpu_buffer_rsrc_t to = range_k(out, c);
 #pragma unroll
                 for (int j = 0; j < TT; ++j) {
                     const int row = j * 32 + l31, width = row < rows ? p.K : 0;
@@ -752,7 +878,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                     for (int a = 0; a < 4; ++a) {
                         const int e = part * 32 + 8 * a + 4 * half;
                         const f32x4 x = {acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]};
-                        if (share == 1) put_quad<T, WIDE>(to, row * dks, e, width, x);
+                        if (!shared) put_quad<T, WIDE>(to, row * dks, e, width, x);
                         else put_quad<float, WIDE>(to, row * dks, e, width, x);
                     }
                     fence();
@@ -761,13 +887,13 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
             constexpr int Q = sizeof(typename N::Wide) / 16;  // quads of a fragment
             float x = 0.0f;
             const int column = kcol ^ (part * 32 * (int)sizeof(T));
-            {
-                f32x16 acc[TT] = {};
+            f32x16 aq[TT] = {};
+            const auto add_in = [&](int part_v) {  // half of V's share of dq
 #pragma unroll
-                for (int t = 0; t < VW; ++t)
+                for (int t = 0; t < VW / 2; ++t)
 #pragma unroll
                     for (int s = 0; s < 32 / KS; ++s) {
-                        const typename N::Wide w = rows_of<T>(SK[t], s);
+                        const typename N::Wide w = rows_of<T>(SK[t + part_v * (VW / 2)], s);
                         typename N::Wide u;
 #pragma unroll
                         for (int e = 0; e < 4 * Q; ++e) {
@@ -778,22 +904,15 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                         split(u, pq);
 #pragma unroll
                         for (int j = 0; j < TT; ++j) {
-                            const Frag f = TV::by_row(dt + j * vDown, vrow, t * (32 / KS) + s);
+                            const Frag f = TV::by_row(dt + j * vDown, vrow, (t + part_v * (VW / 2)) * (32 / KS) + s);
 #pragma unroll
-                            for (int e = 0; e < N::kParts; ++e) acc[j] = mfma(pq[e], f, acc[j]);
+                            for (int e = 0; e < N::kParts; ++e) aq[j] = mfma(pq[e], f, aq[j]);
                         }
                         fence();
                     }
-                own(acc, qt, back, came[part]);
-#pragma unroll
-                for (int s = 0; s < C / KS; ++s) {
-                    const Frag f = TK::by_column(kt, column, 0, s);
-#pragma unroll
-                    for (int j = s / (32 / KS); j < TT; ++j) acc[j] = mfma(f, TP::by_row(bn + j * pDown, prow, s), acc[j]);
-                }
-                put(acc, p.dq);
-            }
-            if (c > c0) fetch(c - 1);
+            };
+            add_in(0);
+            load_in(1);
             fence();
             {
                 f32x16 acc[TT] = {};
@@ -821,6 +940,26 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                 }
                 put(acc, p.dk);
             }
+            fetch(c - 1);
+            fence();
+            add_in(1);
+            own(aq, qt, back, came[part]);
+#pragma unroll
+            for (int s = 0; s < C / KS; ++s) {
+                const Frag f = TK::by_column(kt, column, 0, s);
+#pragma unroll
+                for (int j = s / (32 / KS); j < TT; ++j) aq[j] = mfma(f, TP::by_row(bn + j * pDown, prow, s), aq[j]);
+            }
+            if (shared) {
+                put(aq, p.dq);
+            } else {
+#pragma unroll
+                for (int j = 0; j < TT; ++j)
+#pragma unroll
+                    for (int a = 0; a < 4; ++a)
+                        TK::put(oq, j * 32 + l31, part * 8 + 2 * a + half, f32x4{aq[j][4 * a], aq[j][4 * a + 1], aq[j][4 * a + 2], aq[j][4 * a + 3]});
+            }
+            fence();
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
             if (lane == 0) through[part] = dec.whole == 0.0f ? 0.0f : x * dec.whole;
@@ -830,36 +969,15 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
             state_add<T, C, VP, VW>(SK, dt, fq, back, dec.whole, half, vcol);
         }
         __syncthreads();
-        if (wave == 0) {
-            // dg. Row j of the pairs becomes its sums from i on; then token t adds the rows before it.
+        if (wave == 0) {  // dg
+            float d = pairs, a = 0.0f, e = 0.0f;
             if (lane < C) {
-                float sum = 0.0f;
-                for (int a = C / 4 - 1; a >= 0; --a) {
-                    f32x4 *const q4 = (f32x4 *)(mt + TM::at(lane, a));
-                    f32x4 m = *q4;
-#pragma unroll
-                    for (int e = 3; e >= 0; --e) {
-                        sum += m[e];
-                        m[e] = sum;
-                    }
-                    *q4 = m;
-                }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
-            float d = 0.0f, a = 0.0f, e = 0.0f;
-            if (lane < C) {
-                for (int j = 0; j < C - 1; ++j) {
-                    const float m = *(const float *)(mt + TM::at(j, lane >> 2) + (lane & 3) * 4);
-                    d += j < lane ? m : 0.0f;
-                }
-                float x = 0.0f;
 #pragma unroll
                 for (int w = 0; w < KT; ++w) {
                     a += came[w][lane];
                     e += left[w][lane];
-                    x += through[w];
+                    d += through[w];
                 }
-                d += x;
             }
             float before = e;  // sums of what left before t, and of what came from t on
 #pragma unroll
@@ -874,6 +992,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
             if (lane < C && t0 + lane < p.L) p.dg[(b * p.L + t0 + lane) * p.H + h] = d;
         }
     }
+    if (n > 0) put_outputs(c0);
     if (p.dfirst && seg == 0 && of_v) state_store<KT>(SV, p.dfirst + bh * KV, p.K, p.V, part * 32 + l31, half);
 }
 
