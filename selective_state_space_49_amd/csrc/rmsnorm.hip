@@ -260,26 +260,56 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_bwd(NormBwdArgs p, in
     for (int k = 0; k < NV; ++k) store8(to, (tid + k * TPR) * E, D, wide, dw[k]);
 }
 
+// 16 columns by 16 rows of partial sums at a time; a thread's rows, then the 16 threads of a column.
 __global__ void __launch_bounds__(256) k_dweight(const float *part, float *out, int sets, int D) {
-    __shared__ double sum[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, at = blockIdx.x * 64 + lane;
-    double x = 0.0;
-    if (at < D)
-        for (int s = wave; s < sets; s += 4) x += part[(int64_t)s * D + at];
-    sum[wave][lane] = x;
+    __shared__ double sum[16][17];
+    const int x = threadIdx.x & 15, y = threadIdx.x >> 4, at = blockIdx.x * 16 + x;
+    double s = 0.0;
+    if (at < D) {
+#pragma unroll 8
+        for (int r = y; r < sets; r += 16) s += part[(int64_t)r * D + at];
+    }
+    sum[y][x] = s;
     __syncthreads();
-    if (wave == 0 && at < D) out[at] = (float)(sum[0][lane] + sum[1][lane] + sum[2][lane] + sum[3][lane]);
+    if (y == 0 && at < D) {
+#pragma unroll
+        for (int k = 1; k < 16; ++k) s += sum[k][x];
+        out[at] = (float)s;
+    }
 }
 
+// WIDE: 8 codes a thread (a group is a multiple of 8), else one.
+template <bool WIDE>
 __global__ void __launch_bounds__(256) k_values(const uint8_t *codes, const float *scales, float *out, int64_t rows, int D, int group,
                                                 int code) {
-    const int64_t n = rows * D, groups = group ? (D + group - 1) / group : 1;
-    const int64_t stride = (int64_t)gridDim.x * 256;
+    constexpr int N = WIDE ? 8 : 1;
+    const uint32_t per_row = D / N, groups = group ? (D + group - 1) / group : 1;
+    const int64_t n = rows * per_row, stride = (int64_t)gridDim.x * 256;
     for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += stride) {
-        const int64_t row = e / D;
-        const float scale = scales[row * groups + (group ? (e - row * D) / group : 0)];
-        const float v = code == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)codes[e], 0) : (float)(int8_t)codes[e];
-        out[e] = v * scale;
+        const int64_t row = n <= 0xffffffff ? (uint32_t)e / per_row : e / per_row;
+        const int at = (int)(e - row * per_row) * N;
+        const float scale = scales[row * groups + (group ? at / group : 0)];
+        if constexpr (WIDE) {
+            const u32x2 c = *(const u32x2 *)(codes + e * 8);
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (code == 1) {
+                    v[4 * k] = __builtin_amdgcn_cvt_f32_fp8((int)c[k], 0);
+                    v[4 * k + 1] = __builtin_amdgcn_cvt_f32_fp8((int)c[k], 1);
+                    v[4 * k + 2] = __builtin_amdgcn_cvt_f32_fp8((int)c[k], 2);
+                    v[4 * k + 3] = __builtin_amdgcn_cvt_f32_fp8((int)c[k], 3);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[4 * k + j] = (float)(int8_t)(c[k] >> (8 * j));
+                }
+            }
+            float4 *const to = (float4 *)(out + e * 8);
+            to[0] = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+            to[1] = make_float4(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale);
+        } else {
+            out[e] = (code == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)codes[e], 0) : (float)(int8_t)codes[e]) * scale;
+        }
     }
 }
 
@@ -327,7 +357,7 @@ void run_bwd(const NormBwdArgs &a, hipStream_t s) {
         const int blocks = (sets + kThreads / TPR - 1) / (kThreads / TPR);
         k_bwd<T, R, TPR, NV><<<blocks, kThreads, 0, s>>>(a, sets, wide);
     });
-    k_dweight<<<(a.dim + 63) / 64, 256, 0, s>>>((const float *)a.ws, a.dweight, sets, a.dim);
+    k_dweight<<<(a.dim + 15) / 16, 256, 0, s>>>((const float *)a.ws, a.dweight, sets, a.dim);
 }
 
 }  // namespace
@@ -347,8 +377,10 @@ hipError_t launch_rmsnorm_bwd(const NormBwdArgs &a, int io, int res_io, hipStrea
 }
 hipError_t launch_q8_values(const void *codes, const float *scales, float *out, int64_t rows, int32_t dim, int32_t group,
                             int code, hipStream_t s) {
-    const int64_t blocks = std::min<int64_t>((rows * dim + 255) / 256, 16384);
-    k_values<<<blocks, 256, 0, s>>>((const uint8_t *)codes, scales, out, rows, dim, group, code);
+    const bool wide = dim % 8 == 0 && aligned_to(codes, 8) && aligned_to(out, 16);
+    const int64_t blocks = std::min<int64_t>((rows * dim / (wide ? 8 : 1) + 255) / 256, 1 << 20);
+    if (wide) k_values<true><<<blocks, 256, 0, s>>>((const uint8_t *)codes, scales, out, rows, dim, group, code);
+    else k_values<false><<<blocks, 256, 0, s>>>((const uint8_t *)codes, scales, out, rows, dim, group, code);
     return hipGetLastError();
 }
 

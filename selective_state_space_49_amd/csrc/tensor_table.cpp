@@ -19,6 +19,7 @@
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <cstdint>
 #include <exception>
 #include <initializer_list>
@@ -411,6 +412,299 @@ PyObject *xent_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     });
 }
 
+// A tensor's number of dimensions, -1 for anything else.
+int64_t dims_of(PyObject *o) { return THPVariable_Check(o) ? THPVariable_Unpack(o).dim() : -1; }
+
+// What the calls of the linear attention share: the sizes, and the addresses of q, k, v and the decays.
+// args: q, k, v, log_decay.
+struct Linattn {
+    int64_t b, L, H, Hk, K, V;
+    const void *q, *k, *v;
+    const float *g;
+    int32_t per_token;
+    bool read(Call &c, PyObject *const *args, bool step) {
+        if (dims_of(args[2]) != 4) return false;
+        const at::IntArrayRef qs = c.first.sizes(), vs = THPVariable_Unpack(args[2]).sizes();
+        b = qs[0], L = qs[1], Hk = qs[2], K = qs[3], H = vs[2], V = vs[3];
+        const int64_t value[4] = {b, L, H, V}, token[3] = {b, L, H}, layer[2] = {b, H};
+        per_token = dims_of(args[3]) == 3;
+        q = c.need(args[0], c.io, qs);
+        k = c.need(args[1], c.io, qs);
+        v = c.need(args[2], c.io, value);
+        g = (const float *)(per_token ? c.need(args[3], at::kFloat, token)
+                                      : step ? c.need(args[3], at::kFloat, layer) : c.need(args[3], at::kFloat, H));
+        return c.ok && H <= INT32_MAX && Hk <= INT32_MAX && K <= INT32_MAX && V <= INT32_MAX;
+    }
+};
+float scale_of(PyObject *o, int64_t K) { return o == Py_None ? (float)(1.0 / std::sqrt((double)K)) : (float)PyFloat_AsDouble(o); }
+
+// linattn_fwd(entry, workspace size's entry, stream, q, k, v, log_decay, h0, scale, o, h_final, states,
+// want_h_final, save): (o, h_final, states).
+PyObject *linattn_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 14) return PyErr_Format(PyExc_TypeError, "14 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_linattn_fwd))PyLong_AsVoidPtr(args[0]);
+        const auto size = (decltype(&ssm_linattn_fwd_workspace))PyLong_AsVoidPtr(args[1]);
+        void *const stream = PyLong_AsVoidPtr(args[2]);
+        if (dims_of(args[3]) != 4) Py_RETURN_NONE;
+        Call c(args[3], 4);
+        Linattn t;
+        if (!c.ok || !t.read(c, args + 3, false)) Py_RETURN_NONE;
+        const float scale = scale_of(args[8], t.K);
+        if (PyErr_Occurred()) return nullptr;
+        const int64_t every = c.io == at::kFloat ? SSM_LINATTN_CHUNK_F32 : SSM_LINATTN_CHUNK_BF16;
+        const int64_t out[4] = {t.b, t.L, t.H, t.V}, state[4] = {t.b, t.H, t.K, t.V},
+                      rows[5] = {t.b, t.H, (t.L + every - 1) / every, t.K, t.V};
+        const float *const h0 = (const float *)c.in(args[7], at::kFloat, state);
+        if (!c.ok) Py_RETURN_NONE;
+        const at::Tensor o = c.out(args[9], c.io, out);
+        const at::Tensor h = args[10] != Py_None || args[12] == Py_True ? c.out(args[10], at::kFloat, state) : at::Tensor();
+        const at::Tensor states = args[11] != Py_None || args[13] == Py_True ? c.out(args[11], at::kFloat, rows) : at::Tensor();
+        if (!c.ok) Py_RETURN_NONE;
+        const size_t bytes = size(t.b, t.L, (int32_t)t.H, (int32_t)t.Hk, (int32_t)t.K, (int32_t)t.V, c.kind());
+        const at::Tensor ws = bytes ? c.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        const c10::DeviceGuard on(c.first.device());
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(t.q, t.k, t.v, t.g, t.per_token, h0, scale, at_of(o), (float *)at_of(h), (float *)at_of(states), t.b, t.L, (int32_t)t.H,
+                   (int32_t)t.Hk, (int32_t)t.K, (int32_t)t.V, c.kind(), at_of(ws), bytes, stream);
+        Py_END_ALLOW_THREADS
+        if (st == SSM_OK)
+            for (int k = 9; k < 12; ++k) written(args[k]);
+        return result(st, {o, h, states});
+    });
+}
+
+// linattn_bwd(entry, workspace size's entry, stream, q, k, v, log_decay, states, do, dh_final, scale,
+// want_dh0): (dq, dk, dv, dlog_decay, dh0).
+PyObject *linattn_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 12) return PyErr_Format(PyExc_TypeError, "12 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_linattn_bwd))PyLong_AsVoidPtr(args[0]);
+        const auto size = (decltype(&ssm_linattn_bwd_workspace))PyLong_AsVoidPtr(args[1]);
+        void *const stream = PyLong_AsVoidPtr(args[2]);
+        if (dims_of(args[3]) != 4) Py_RETURN_NONE;
+        Call c(args[3], 4);
+        Linattn t;
+        if (!c.ok || !t.read(c, args + 3, false)) Py_RETURN_NONE;
+        const float scale = scale_of(args[10], t.K);
+        if (PyErr_Occurred()) return nullptr;
+        const int64_t every = c.io == at::kFloat ? SSM_LINATTN_CHUNK_F32 : SSM_LINATTN_CHUNK_BF16;
+        const int64_t out[4] = {t.b, t.L, t.H, t.V}, state[4] = {t.b, t.H, t.K, t.V},
+                      rows[5] = {t.b, t.H, (t.L + every - 1) / every, t.K, t.V};
+        const float *const states = (const float *)c.need(args[7], at::kFloat, rows);
+        const void *const d_o = c.need(args[8], c.io, out);
+        const float *const dh = (const float *)c.in(args[9], at::kFloat, state);
+        if (!c.ok) Py_RETURN_NONE;
+        const at::Tensor dq = c.fresh(c.io, c.first.sizes()), dk = c.fresh(c.io, c.first.sizes()), dv = c.fresh(c.io, out);
+        const at::Tensor dg = c.fresh(at::kFloat, THPVariable_Unpack(args[6]).sizes());
+        const at::Tensor dh0 = args[11] == Py_True ? c.fresh(at::kFloat, state) : at::Tensor();
+        const size_t bytes = size(t.b, t.L, (int32_t)t.H, (int32_t)t.Hk, (int32_t)t.K, (int32_t)t.V, t.per_token, c.kind());
+        const at::Tensor ws = bytes ? c.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        const c10::DeviceGuard on(c.first.device());
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(t.q, t.k, t.v, t.g, t.per_token, states, d_o, dh, scale, at_of(dq), at_of(dk), at_of(dv), (float *)at_of(dg),
+                   (float *)at_of(dh0), t.b, t.L, (int32_t)t.H, (int32_t)t.Hk, (int32_t)t.K, (int32_t)t.V, c.kind(), at_of(ws), bytes, stream);
+        Py_END_ALLOW_THREADS
+        return result(st, {dq, dk, dv, dg, dh0});
+    });
+}
+
+// linattn_step(entry, stream, h, q_t, k_t, v_t, log_decay, scale, o_t or None): o_t.
+PyObject *linattn_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 9) return PyErr_Format(PyExc_TypeError, "9 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_linattn_step))PyLong_AsVoidPtr(args[0]);
+        void *const stream = PyLong_AsVoidPtr(args[1]);
+        if (dims_of(args[3]) != 4) Py_RETURN_NONE;
+        Call c(args[3], 4);
+        Linattn t;
+        if (!c.ok || !t.read(c, args + 3, true)) Py_RETURN_NONE;
+        const float scale = scale_of(args[7], t.K);
+        if (PyErr_Occurred()) return nullptr;
+        const int64_t out[4] = {t.b, t.L, t.H, t.V}, state[5] = {t.b, t.L, t.H, t.K, t.V};
+        float *const h = (float *)c.need(args[2], at::kFloat, state);
+        if (!c.ok) Py_RETURN_NONE;
+        const at::Tensor o = c.out(args[8], c.io, out);
+        if (!c.ok) Py_RETURN_NONE;
+        const c10::DeviceGuard on(c.first.device());
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(h, t.q, t.k, t.v, t.g, t.per_token, scale, at_of(o), t.b, t.L, (int32_t)t.H, (int32_t)t.Hk, (int32_t)t.K, (int32_t)t.V,
+                   c.kind(), stream);
+        Py_END_ALLOW_THREADS
+        if (st != SSM_OK) return PyLong_FromLong(st);
+        written(args[2]);
+        written(args[8]);
+        return wrap(o);
+    });
+}
+
+// The norm's inputs: x [..., dim], weight [dim], residual or None in x's type or float32.
+struct Norm {
+    int64_t rows = 0, dim = 0;
+    at::ScalarType res;
+    const void *x, *residual;
+    const float *weight;
+    bool read(Call &c, PyObject *x_, PyObject *weight_, PyObject *residual_) {
+        const at::IntArrayRef all = c.first.sizes();
+        if (all.empty()) return false;
+        dim = all.back();
+        if (dim < 1 || dim > INT32_MAX) return false;
+        rows = c.first.numel() / dim;
+        res = c.io;
+        if (residual_ != Py_None && THPVariable_Check(residual_) && THPVariable_Unpack(residual_).scalar_type() == at::kFloat) res = at::kFloat;
+        x = c.need(x_, c.io, all);
+        residual = c.in(residual_, res, all);
+        weight = (const float *)c.need(weight_, at::kFloat, dim);
+        return c.ok;
+    }
+    ssm_dtype res_kind() const { return res == at::kFloat ? SSM_F32 : SSM_BF16; }
+};
+
+// rmsnorm_fwd(entry, stream, x, weight, residual, eps, y, residual_out, rstd, want_rstd): (y, residual_out, rstd).
+PyObject *rmsnorm_fwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 10) return PyErr_Format(PyExc_TypeError, "10 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_rmsnorm_fwd))PyLong_AsVoidPtr(args[0]);
+        void *const stream = PyLong_AsVoidPtr(args[1]);
+        const double eps = PyFloat_AsDouble(args[5]);
+        if (PyErr_Occurred()) return nullptr;
+        if (dims_of(args[2]) < 1) Py_RETURN_NONE;
+        Call c(args[2], (size_t)dims_of(args[2]));
+        Norm t;
+        if (!c.ok || !t.read(c, args[2], args[3], args[4])) Py_RETURN_NONE;
+        if (args[4] == Py_None && args[7] != Py_None) Py_RETURN_NONE;
+        const at::IntArrayRef all = c.first.sizes(), lead = all.slice(0, all.size() - 1);
+        const at::Tensor y = c.out(args[6], c.io, all);
+        const at::Tensor added = args[4] != Py_None ? c.out(args[7], t.res, all) : at::Tensor();
+        const at::Tensor rstd = args[8] != Py_None || args[9] == Py_True ? c.out(args[8], at::kFloat, lead) : at::Tensor();
+        if (!c.ok) Py_RETURN_NONE;
+        const c10::DeviceGuard on(c.first.device());
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(t.x, t.residual, t.weight, eps, at_of(y), at_of(added), (float *)at_of(rstd), t.rows, (int32_t)t.dim, c.kind(), t.res_kind(),
+                   stream);
+        Py_END_ALLOW_THREADS
+        if (st == SSM_OK)
+            for (int k = 6; k < 9; ++k) written(args[k]);
+        return result(st, {y, added, rstd});
+    });
+}
+
+// rmsnorm_fwd_q8(entry, stream, x, weight, residual, eps, code, group, codes, scales, residual_out):
+// (codes, scales, residual_out).
+PyObject *rmsnorm_fwd_q8(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 11) return PyErr_Format(PyExc_TypeError, "11 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_rmsnorm_fwd_q8))PyLong_AsVoidPtr(args[0]);
+        void *const stream = PyLong_AsVoidPtr(args[1]);
+        const double eps = PyFloat_AsDouble(args[5]);
+        const long code = PyLong_AsLong(args[6]), group = PyLong_AsLong(args[7]);
+        if (PyErr_Occurred()) return nullptr;
+        if (dims_of(args[2]) < 1 || group < 0 || group > INT32_MAX) Py_RETURN_NONE;
+        Call c(args[2], (size_t)dims_of(args[2]));
+        Norm t;
+        if (!c.ok || !t.read(c, args[2], args[3], args[4])) Py_RETURN_NONE;
+        if (args[4] == Py_None && args[10] != Py_None) Py_RETURN_NONE;
+        const at::IntArrayRef all = c.first.sizes();
+        std::vector<int64_t> scale(all.begin(), all.end());
+        scale.back() = group ? (t.dim + group - 1) / group : 1;
+        const at::Tensor codes = c.out(args[8], code == SSM_E4M3 ? at::kFloat8_e4m3fn : at::kChar, all);
+        const at::Tensor scales = c.out(args[9], at::kFloat, scale);
+        const at::Tensor added = args[4] != Py_None ? c.out(args[10], t.res, all) : at::Tensor();
+        if (!c.ok) Py_RETURN_NONE;
+        const c10::DeviceGuard on(c.first.device());
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(t.x, t.residual, t.weight, eps, at_of(codes), (float *)at_of(scales), (ssm_code)code, (int32_t)group, at_of(added), t.rows,
+                   (int32_t)t.dim, c.kind(), t.res_kind(), stream);
+        Py_END_ALLOW_THREADS
+        if (st == SSM_OK)
+            for (int k = 8; k < 11; ++k) written(args[k]);
+        return result(st, {codes, scales, added});
+    });
+}
+
+// rmsnorm_bwd(entry, workspace size's entry, stream, dy, s, weight, rstd, ds): (dx, dresidual or None, dweight).
+PyObject *rmsnorm_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 8) return PyErr_Format(PyExc_TypeError, "8 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_rmsnorm_bwd))PyLong_AsVoidPtr(args[0]);
+        const auto size = (decltype(&ssm_rmsnorm_bwd_workspace))PyLong_AsVoidPtr(args[1]);
+        void *const stream = PyLong_AsVoidPtr(args[2]);
+        if (PyErr_Occurred()) return nullptr;
+        if (dims_of(args[3]) < 1 || args[4] == Py_None) Py_RETURN_NONE;
+        Call c(args[3], (size_t)dims_of(args[3]));
+        Norm t;
+        if (!c.ok || !t.read(c, args[3], args[5], args[4])) Py_RETURN_NONE;
+        const at::IntArrayRef all = c.first.sizes();
+        const float *const rstd = (const float *)c.need(args[6], at::kFloat, all.slice(0, all.size() - 1));
+        const void *const ds = c.in(args[7], t.res, all);
+        if (!c.ok) Py_RETURN_NONE;
+        const at::Tensor dx = c.fresh(c.io, all), dres = t.res == c.io ? at::Tensor() : c.fresh(t.res, all), dw = c.fresh(at::kFloat, t.dim);
+        const size_t bytes = size(t.rows, (int32_t)t.dim);
+        const at::Tensor ws = bytes ? c.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        const c10::DeviceGuard on(c.first.device());
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(t.x, t.residual, ds, t.weight, rstd, at_of(dx), at_of(dres), (float *)at_of(dw), t.rows, (int32_t)t.dim, c.kind(), t.res_kind(),
+                   at_of(ws), bytes, stream);
+        Py_END_ALLOW_THREADS
+        return result(st, {dx, dres, dw});
+    });
+}
+
+// A setting of the sampling: a tensor with a value for every row, or a number for all.
+template <typename T>
+const T *setting(Call &c, PyObject *o, at::ScalarType type, int64_t rows, double *all) {
+    if (THPVariable_Check(o)) {
+        *all = 0;
+        return (const T *)c.need(o, type, rows);
+    }
+    *all = PyFloat_AsDouble(o);
+    return nullptr;
+}
+
+// sample(entry, workspace size's entry, stream, logits, u, temperature, top_k, top_p, min_p, tokens, logprob,
+// want_logprob): (tokens, logprob or None).
+PyObject *sample(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 12) return PyErr_Format(PyExc_TypeError, "12 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_sample))PyLong_AsVoidPtr(args[0]);
+        const auto size = (decltype(&ssm_sample_workspace))PyLong_AsVoidPtr(args[1]);
+        void *const stream = PyLong_AsVoidPtr(args[2]);
+        if (PyErr_Occurred()) return nullptr;
+        if (dims_of(args[3]) != 2) Py_RETURN_NONE;
+        Call c(args[3], 2);
+        if (!c.ok) Py_RETURN_NONE;
+        const int64_t rows = c.first.size(0), vocab = c.first.size(1);
+        double t_all, k_all, p_all, m_all;
+        const void *const logits = c.need(args[3], c.io, c.first.sizes());
+        const float *const u = (const float *)c.need(args[4], at::kFloat, rows);
+        const float *const t = setting<float>(c, args[5], at::kFloat, rows, &t_all);
+        const int32_t *const k = setting<int32_t>(c, args[6], at::kInt, rows, &k_all);
+        const float *const p = setting<float>(c, args[7], at::kFloat, rows, &p_all), *const m = setting<float>(c, args[8], at::kFloat, rows, &m_all);
+        if (PyErr_Occurred()) return nullptr;
+        if (!c.ok || k_all != std::floor(k_all) || k_all > INT32_MAX || k_all < INT32_MIN) Py_RETURN_NONE;
+        const at::Tensor tokens = c.out(args[9], at::kLong, rows);
+        const at::Tensor logprob = args[10] != Py_None || args[11] == Py_True ? c.out(args[10], at::kFloat, rows) : at::Tensor();
+        if (!c.ok) Py_RETURN_NONE;
+        const size_t bytes = size(rows, vocab);
+        const at::Tensor ws = bytes ? c.fresh(at::kByte, (int64_t)bytes) : at::Tensor();
+        const c10::DeviceGuard on(c.first.device());
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(logits, u, t, (float)t_all, k, (int32_t)k_all, p, (float)p_all, m, (float)m_all, (int64_t *)at_of(tokens),
+                   (float *)at_of(logprob), rows, vocab, c.kind(), at_of(ws), bytes, stream);
+        Py_END_ALLOW_THREADS
+        if (st == SSM_OK)
+            for (int i = 9; i < 11; ++i) written(args[i]);
+        return result(st, {tokens, logprob});
+    });
+}
+
 PyMethodDef methods[] = {
     {"gated_fwd", (PyCFunction)(void (*)(void))gated_fwd, METH_FASTCALL, "ssm_gated_fwd for tensors."},
     {"gated_bwd", (PyCFunction)(void (*)(void))gated_bwd, METH_FASTCALL, "ssm_gated_bwd for tensors."},
@@ -418,6 +712,13 @@ PyMethodDef methods[] = {
     {"xent_bwd", (PyCFunction)(void (*)(void))xent_bwd, METH_FASTCALL, "ssm_xent_bwd for tensors."},
     {"gated_step", (PyCFunction)(void (*)(void))gated_step, METH_FASTCALL, "ssm_gated_step for tensors."},
     {"adamw_step", (PyCFunction)(void (*)(void))adamw_step, METH_FASTCALL, "ssm_adamw_step for lists of tensors."},
+    {"linattn_fwd", (PyCFunction)(void (*)(void))linattn_fwd, METH_FASTCALL, "ssm_linattn_fwd for tensors."},
+    {"linattn_bwd", (PyCFunction)(void (*)(void))linattn_bwd, METH_FASTCALL, "ssm_linattn_bwd for tensors."},
+    {"linattn_step", (PyCFunction)(void (*)(void))linattn_step, METH_FASTCALL, "ssm_linattn_step for tensors."},
+    {"rmsnorm_fwd", (PyCFunction)(void (*)(void))rmsnorm_fwd, METH_FASTCALL, "ssm_rmsnorm_fwd for tensors."},
+    {"rmsnorm_fwd_q8", (PyCFunction)(void (*)(void))rmsnorm_fwd_q8, METH_FASTCALL, "ssm_rmsnorm_fwd_q8 for tensors."},
+    {"rmsnorm_bwd", (PyCFunction)(void (*)(void))rmsnorm_bwd, METH_FASTCALL, "ssm_rmsnorm_bwd for tensors."},
+    {"sample", (PyCFunction)(void (*)(void))sample, METH_FASTCALL, "ssm_sample for tensors."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_table", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

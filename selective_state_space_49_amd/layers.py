@@ -12,7 +12,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import SSM_BF16, load_library
-from .training import _at, _called, _f32, _kind, _need, _scratch
+from .training import _at, _called, _entry, _f32, _kind, _made, _need, _scratch, _stream, _table_module
 
 # SSM_LINATTN_CHUNK_BF16 and _F32 of ssm_scan.h, by SSM_F32 and SSM_BF16.
 LINATTN_CHUNK = (32, 64)
@@ -61,6 +61,11 @@ def ssm_linattn_fwd(q, k, v, log_decay, h0=None, *, scale=None, o=None, h_final=
 
 
 def _linattn_fwd(q, k, v, log_decay, h0, scale, o, h_final, states, workspace, want_h_final, save):
+    if workspace is None and q.is_cuda:
+        got = _table_module().linattn_fwd(_entry("ssm_linattn_fwd"), _entry("ssm_linattn_fwd_workspace"), _stream(q), q, k, v,
+                                          log_decay, h0, scale, o, h_final, states, bool(want_h_final), save)
+        if got is not None:
+            return _made(got)
     lib = load_library()
     (b, L, H, Hk, K, V, kind), inputs = _linattn_inputs(q, k, v, log_decay)
     dev, chunk = q.device, LINATTN_CHUNK[kind]
@@ -88,6 +93,11 @@ def ssm_linattn_fwd_save(q, k, v, log_decay, h0=None, *, scale=None, o=None, h_f
 def ssm_linattn_bwd(q, k, v, log_decay, states, *, do, dh_final=None, scale=None, want_dh0=True, workspace=None):
     """Gradients of sum(do o) + sum(dh_final h_final): a dict of dq, dk, dv (the inputs' dtype), dg
     (float32, log_decay's shape) and dh0 [b, H, K, V] (float32; None unless want_dh0)."""
+    if workspace is None and q.is_cuda:
+        got = _table_module().linattn_bwd(_entry("ssm_linattn_bwd"), _entry("ssm_linattn_bwd_workspace"), _stream(q), q, k, v,
+                                          log_decay, states, do, dh_final, scale, bool(want_dh0))
+        if got is not None:
+            return dict(zip(("dq", "dk", "dv", "dg", "dh0"), _made(got)))
     lib = load_library()
     (b, L, H, Hk, K, V, kind), inputs = _linattn_inputs(q, k, v, log_decay)
     dev = q.device
@@ -104,6 +114,10 @@ def ssm_linattn_bwd(q, k, v, log_decay, states, *, do, dh_final=None, scale=None
 def ssm_linattn_step(h, q_t, k_t, v_t, log_decay, *, scale=None, o_t=None):
     """One token for every (layer, sequence): h [Ln, S, H, K, V] float32 in place; q_t, k_t
     [Ln, S, groups, K]; v_t [Ln, S, H, V]; log_decay [Ln, S, H] or [Ln, H]. Returns o_t."""
+    if q_t.is_cuda:
+        got = _table_module().linattn_step(_entry("ssm_linattn_step"), _stream(q_t), h, q_t, k_t, v_t, log_decay, scale, o_t)
+        if got is not None:
+            return _made(got)
     if q_t.dim() != 4 or v_t.dim() != 4:
         raise ValueError(f"q_t and v_t must be [layers, seqs, heads, dim], got {tuple(q_t.shape)} and {tuple(v_t.shape)}")
     Ln, S, Hk, K = q_t.shape
@@ -180,6 +194,11 @@ def ssm_rmsnorm_fwd(x, weight, residual=None, *, eps=1e-6, y=None, residual_out=
     """s = x + residual, y = s / sqrt(mean(s^2) + eps) * weight over the last dimension. Returns y, s
     (residual_out, in the residual's dtype, which may be the residual itself; None without one) and
     rstd [...] float32, what ssm_rmsnorm_bwd needs. weight is float32, residual x's dtype or float32."""
+    if x.is_cuda:
+        got = _table_module().rmsnorm_fwd(_entry("ssm_rmsnorm_fwd"), _stream(x), x, weight, residual, eps, y, residual_out, rstd,
+                                          bool(want_rstd))
+        if got is not None:
+            return _made(got)
     rows, dim, kind, res_kind, residual_out, at = _norm_inputs(x, weight, residual, residual_out)
     y = torch.empty_like(x) if y is None else y
     if rstd is None and want_rstd:
@@ -200,6 +219,11 @@ def ssm_rmsnorm_fwd_q8(x, weight, residual=None, *, eps=1e-6, code="e4m3", group
     """ssm_rmsnorm_fwd with y in 8 bits: codes [..., D] (float8_e4m3fn or int8), scales [..., groups]
     float32 (one for the row with group 0, or for 32, 64 or 128 values) and s (None without a residual)."""
     number, dtype = _code(code)
+    if x.is_cuda:
+        got = _table_module().rmsnorm_fwd_q8(_entry("ssm_rmsnorm_fwd_q8"), _stream(x), x, weight, residual, eps, number, group,
+                                             codes, scales, residual_out)
+        if got is not None:
+            return _made(got)
     rows, dim, kind, res_kind, residual_out, at = _norm_inputs(x, weight, residual, residual_out)
     shape = (*x.shape[:-1], -(-dim // group) if group > 0 else 1)
     codes = torch.empty(x.shape, dtype=dtype, device=x.device) if codes is None else codes
@@ -235,6 +259,12 @@ def ssm_rmsnorm_bwd(dy, s, weight, rstd, *, ds=None, workspace=None):
     """Gradients of sum(dy y) + sum(ds s), with s and rstd as ssm_rmsnorm_fwd gave them (s is x where it
     had no residual): dx (dy's dtype), dresidual (s's dtype; dx itself where they are the same) and
     dweight [D] float32."""
+    if workspace is None and dy.is_cuda:
+        got = _table_module().rmsnorm_bwd(_entry("ssm_rmsnorm_bwd"), _entry("ssm_rmsnorm_bwd_workspace"), _stream(dy), dy, s, weight,
+                                          rstd, ds)
+        if got is not None:
+            dx, dres, dweight = _made(got)
+            return dx, dx if dres is None else dres, dweight
     lib = load_library()
     dim, dev = dy.shape[-1], dy.device
     rows = dy.numel() // dim if dim else 0
@@ -295,6 +325,12 @@ def ssm_sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
     then those at least min_p times as likely as the first. A setting is a number, or a tensor [S]
     (float32; top_k int32). A temperature of 0 takes the largest logit. With want_logprob (or logprob)
     returns (tokens, logprob), the logarithm of the token's share of what was kept."""
+    if workspace is None and logits.is_cuda:
+        got = _table_module().sample(_entry("ssm_sample"), _entry("ssm_sample_workspace"), _stream(logits), logits, u, temperature,
+                                     top_k, top_p, min_p, tokens, logprob, bool(want_logprob))
+        if got is not None:
+            tokens, logprob = _made(got)
+            return tokens if logprob is None else (tokens, logprob)
     lib = load_library()
     rows, vocab = logits.shape
     dev = logits.device
