@@ -7,7 +7,7 @@
 //
 // A row stays in registers between its sum and its output, so every array is read or written once:
 // bytes are the floor. A row of up to 1024 elements belongs to a wave, a longer one to a block of 256
-// or 1024 threads. The sum of squares is held in 64 bits (a conversion and a multiply-add an element:
+// to 1024 threads. The sum of squares is held in 64 bits (a conversion and a multiply-add an element:
 // the 64-bit rate of the vector units is that of 32 bits), so that r does not depend on the order,
 // and codes are computed in 64 bits from s on: a value next to the border of two codes takes the
 // right one.
@@ -34,46 +34,59 @@ __device__ __forceinline__ uint32_t narrow(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
-// Eight elements of a row from `at` on; what is past `width` is 0.
-template <typename T>
-__device__ __forceinline__ void load8(const T *row, int at, int width, bool wide, float (&x)[E]) {
-    if (wide) {
-        if (at < width) {
-            if constexpr (sizeof(T) == 2) {
-                const u32x4 r = *(const u32x4 *)(row + at);
+// Which elements of a row a thread holds, eight for each of its NV vectors. WIDE (rows of whole vectors
+// that start on 16 bytes): eight neighbours. Else one of every 64, so that a wave reads neighbours; a
+// wave's elements are one piece of the row in both.
+template <int TPR, int NV, bool WIDE>
+struct Piece {
+    int first;
+    __device__ __forceinline__ Piece() {
+        const int tid = threadIdx.x % TPR;
+        first = WIDE ? tid * E : tid / 64 * (64 * E * NV) + tid % 64;
+    }
+    __device__ __forceinline__ int at(int n, int e) const { return WIDE ? first + n * TPR * E + e : first + (n * E + e) * 64; }
+    // What is past the row's end is 0.
+    template <typename T>
+    __device__ __forceinline__ void load(const T *row, int n, int width, float (&x)[E]) const {
+        const int from = at(n, 0);
+        if constexpr (WIDE) {
+            if (from < width) {
+                if constexpr (sizeof(T) == 2) {
+                    const u32x4 r = *(const u32x4 *)(row + from);
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = widen(e % 2 ? r[e / 2] >> 16 : r[e / 2] & 0xffff);
+                    for (int e = 0; e < E; ++e) x[e] = widen(e % 2 ? r[e / 2] >> 16 : r[e / 2] & 0xffff);
+                } else {
+                    const float4 lo = *(const float4 *)(row + from), hi = *(const float4 *)(row + from + 4);
+                    x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+                    x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+                }
             } else {
-                const float4 lo = *(const float4 *)(row + at), hi = *(const float4 *)(row + at + 4);
-                x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-                x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] = 0.0f;
             }
-            return;
-        }
-    } else if (at < width) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = at + e < width ? (float)row[at + e] : 0.0f;
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = 0.0f;
-}
-template <typename T>
-__device__ __forceinline__ void store8(T *row, int at, int width, bool wide, const float (&x)[E]) {
-    if (at >= width) return;
-    if (wide) {
-        if constexpr (sizeof(T) == 2) {
-            *(u32x4 *)(row + at) = u32x4{narrow(x[0], x[1]), narrow(x[2], x[3]), narrow(x[4], x[5]), narrow(x[6], x[7])};
         } else {
-            *(float4 *)(row + at) = make_float4(x[0], x[1], x[2], x[3]);
-            *(float4 *)(row + at + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        }
-    } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (at + e < width) row[at + e] = (T)x[e];
+            for (int e = 0; e < E; ++e) x[e] = from + e * 64 < width ? (float)row[from + e * 64] : 0.0f;
+        }
     }
-}
+    template <typename T>
+    __device__ __forceinline__ void store(T *row, int n, int width, const float (&x)[E]) const {
+        const int to = at(n, 0);
+        if constexpr (WIDE) {
+            if (to >= width) return;
+            if constexpr (sizeof(T) == 2) {
+                *(u32x4 *)(row + to) = u32x4{narrow(x[0], x[1]), narrow(x[2], x[3]), narrow(x[4], x[5]), narrow(x[6], x[7])};
+            } else {
+                *(float4 *)(row + to) = make_float4(x[0], x[1], x[2], x[3]);
+                *(float4 *)(row + to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (to + e * 64 < width) row[to + e * 64] = (T)x[e];
+        }
+    }
+};
 template <typename T> __device__ __forceinline__ float stored(float x) {
     if constexpr (sizeof(T) == 2) return (float)(T)x;
     else return x;
@@ -107,113 +120,185 @@ __device__ __forceinline__ float to_e4m3(double u) {
     const float r = (float)((u + big) - big);
     return fminf(fmaxf(r, -448.0f), 448.0f);
 }
+// Eight codes. A quotient rounded to float32 first gives the same code as the quotient itself unless
+// float32 puts it onto the middle of two codes, or it is below the smallest normal one (2^-6, where
+// steps differ): about 1 in 10^4, which take the long way.
+__device__ __forceinline__ void code8(const double (&u)[E], int code, uint32_t (&c)[2]) {
+    float f[E];
+    if (code == 1) {
+        bool hard = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            f[e] = (float)u[e];
+            hard |= (__float_as_uint(f[e]) & 0xfffffu) == 0x80000u || !(fabsf(f[e]) >= 0x1p-6f);
+            f[e] = __builtin_amdgcn_fmed3f(f[e], -448.0f, 448.0f);
+        }
+        if (hard) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) f[e] = to_e4m3(u[e]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * k], f[4 * k + 1], 0, false);
+            c[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * k + 2], f[4 * k + 3], v, true);
+        }
+    } else {
+        c[0] = c[1] = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float r = __builtin_amdgcn_fmed3f((float)__builtin_rint(u[e]), -127.0f, 127.0f);
+            c[e / 4] |= (uint32_t)((int)r & 0xff) << (e % 4 * 8);
+        }
+    }
+}
 
-template <typename T, typename R, int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_fwd(NormArgs p, bool wide) {
+// The largest |y|, NaN where one is: the hardware's maximum leaves NaN out, so they are told apart.
+struct Top {
+    double top = 0.0;
+    bool bad = false;
+    __device__ __forceinline__ void add(double y) {
+        top = __builtin_fmax(top, __builtin_fabs(y));
+        bad |= y != y;
+    }
+    // As a whole number that compares like it, a NaN above all.
+    __device__ __forceinline__ long long bits() const { return bad ? 0x7ff8000000000000ll : __double_as_longlong(top); }
+};
+__device__ __forceinline__ long long larger(long long a, long long b) { return a > b ? a : b; }
+// The largest over `lanes` neighbouring lanes (a power of two).
+__device__ __forceinline__ long long over_lanes(long long x, int lanes) {
+    for (int d = 1; d < lanes; d *= 2) x = larger(x, __shfl_xor(x, d));
+    return x;
+}
+// The scale of values whose largest is top, and its reciprocal, by Newton's steps from the hardware's estimate
+// (relative 2^-22, 2^-44, 2^-52).
+__device__ __forceinline__ float scale_of(long long top, int code, double &inv) {
+    const float scale = (float)(__longlong_as_double(top) * (code == 1 ? 1.0 / 448.0 : 1.0 / 127.0));
+    const double s = (double)scale;
+    double x = __builtin_amdgcn_rcp(s);
+    x = __builtin_fma(x, __builtin_fma(-s, x, 1.0), x);
+    x = __builtin_fma(x, __builtin_fma(-s, x, 1.0), x);
+    inv = scale == 0.0f ? 0.0 : scale == __builtin_inff() ? 0.0 : x;
+    return scale;
+}
+
+// MODE: values, codes with a scale for a row, codes with a scale for a group.
+enum { kValues, kRowCodes, kGroupCodes };
+template <typename T, typename R, int TPR, int NV, bool WIDE, int MODE>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_fwd(NormArgs p) {
     constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
     __shared__ double part[TPR > 64 ? TPR / 64 : 1];
-    const int tid = threadIdx.x % TPR;
+    const Piece<TPR, NV, WIDE> own;
+    const int tid = threadIdx.x % TPR, lane = threadIdx.x & 63;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     if (row >= p.rows) return;  // whole waves: a row of several waves has the block to itself
     const int D = p.dim;
     const int64_t at0 = row * D;
     float s[NV][E];
-    double sum = 0.0;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const int at = (tid + n * TPR) * E;
-        load8((const T *)p.x + at0, at, D, wide, s[n]);
-        if (p.residual) {
+    for (int n = 0; n < NV; ++n) own.load((const T *)p.x + at0, n, D, s[n]);
+    if (p.residual) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
             float add[E];
-            load8((const R *)p.residual + at0, at, D, wide, add);
+            own.load((const R *)p.residual + at0, n, D, add);
 #pragma unroll
             for (int e = 0; e < E; ++e) s[n][e] = stored<R>(s[n][e] + add[e]);
-            store8((R *)p.added + at0, at, D, wide, s[n]);
+            own.store((R *)p.added + at0, n, D, s[n]);
         }
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
 #pragma unroll
         for (int e = 0; e < E; ++e) sum = __builtin_fma((double)s[n][e], (double)s[n][e], sum);
-    }
     const double r = 1.0 / sqrt(row_sum<TPR>(sum, part) / D + p.eps);
     if (p.rstd && tid == 0) p.rstd[row] = (float)r;
-    if (p.code == 0) {
+    if constexpr (MODE == kValues) {
         const float rf = (float)r;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const int at = (tid + n * TPR) * E;
             float w[E];
-            load8(p.weight, at, D, wide, w);
+            own.load(p.weight, n, D, w);
 #pragma unroll
             for (int e = 0; e < E; ++e) w[e] = s[n][e] * rf * w[e];
-            store8((T *)p.y + at0, at, D, wide, w);
+            own.store((T *)p.y + at0, n, D, w);
         }
         return;
     }
-    const double most = p.code == 1 ? 448.0 : 127.0;
-    const auto larger = [](long long a, long long b) { return a > b ? a : b; };
-    long long all = 0;
-    if (p.group == 0) {  // |y| as integers: a NaN is larger than all
+    const int group = p.group, groups = group ? (D + group - 1) / group : 1;
+    double inv = 0.0;
+    if constexpr (MODE == kRowCodes) {
+        Top top;
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             float w[E];
-            load8(p.weight, (tid + n * TPR) * E, D, wide, w);
+            own.load(p.weight, n, D, w);
 #pragma unroll
-            for (int e = 0; e < E; ++e) all = larger(all, __double_as_longlong(fabs((double)s[n][e] * r * (double)w[e])));
+            for (int e = 0; e < E; ++e) top.add((double)s[n][e] * r * (double)w[e]);
         }
-        all = over_row<TPR>(all, (long long *)part, larger);
+        const float scale = scale_of(over_row<TPR>(top.bits(), (long long *)part, larger), p.code, inv);
+        if (tid == 0) p.scales[row] = scale;
     }
-    const int groups = p.group ? (D + p.group - 1) / p.group : 1, lanes = p.group / E;
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const int at = (tid + n * TPR) * E;
         float w[E];
-        load8(p.weight, at, D, wide, w);
+        own.load(p.weight, n, D, w);
         double y[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = (double)s[n][e] * r * (double)w[e];
-        long long top = all;
-        if (p.group) {
+        if constexpr (MODE == kRowCodes) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) top = larger(top, __double_as_longlong(fabs(y[e])));
-            for (int d = 1; d < lanes; d *= 2) top = larger(top, __shfl_xor(top, d));
-        }
-        const float scale = (float)(__longlong_as_double(top) / most);
-        const double inv = scale == 0.0f ? 0.0 : 1.0 / (double)scale;
-        if (at < D && (p.group ? at % p.group == 0 : at == 0)) p.scales[row * groups + (p.group ? at / p.group : 0)] = scale;
-        uint32_t c[2];
-        if (p.code == 1) {
-            float f[E];
+            for (int e = 0; e < E; ++e) y[e] *= inv;
+        } else if constexpr (WIDE) {
+            Top top;
 #pragma unroll
-            for (int e = 0; e < E; ++e) f[e] = to_e4m3(y[e] * inv);
+            for (int e = 0; e < E; ++e) top.add(y[e]);
+            const float scale = scale_of(over_lanes(top.bits(), group / E), p.code, inv);
+            const int at = own.at(n, 0);
+            if (at < D && at % group == 0) p.scales[row * groups + at / group] = scale;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                int v = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * k], f[4 * k + 1], 0, false);
-                c[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * k + 2], f[4 * k + 3], v, true);
-            }
+            for (int e = 0; e < E; ++e) y[e] *= inv;
         } else {
-            c[0] = c[1] = 0;
+            // a group is 32 lanes of an element, the wave's 64, or these of two elements
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int q = (int)fmin(fmax(rint(y[e] * inv), -127.0), 127.0);
-                c[e / 4] |= (uint32_t)(q & 0xff) << (e % 4 * 8);
+            for (int e = 0; e < E; e += 2) {
+                Top top[2];
+                top[0].add(y[e]);
+                if (group == 128) top[0].add(y[e + 1]);
+                else top[1].add(y[e + 1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (k == 0 || group != 128) {
+                        const float scale = scale_of(over_lanes(top[k].bits(), group == 32 ? 32 : 64), p.code, inv);
+                        const int at = own.at(n, e + k);
+                        if (lane % (group == 32 ? 32 : 64) == 0 && at < D) p.scales[row * groups + at / group] = scale;
+                    }
+                    y[e + k] *= inv;
+                }
             }
         }
-        uint8_t *const to = (uint8_t *)p.y + at0 + at;
-        if (wide) {
-            if (at < D) *(u32x2 *)to = u32x2{c[0], c[1]};
+        uint32_t c[2];
+        code8(y, p.code, c);
+        uint8_t *const to = (uint8_t *)p.y + at0;
+        if constexpr (WIDE) {
+            const int at = own.at(n, 0);
+            if (at < D) *(u32x2 *)(to + at) = u32x2{c[0], c[1]};
         } else {
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                if (at + e < D) to[e] = (uint8_t)(c[e / 4] >> (e % 4 * 8));
+                if (own.at(n, e) < D) to[own.at(n, e)] = (uint8_t)(c[e / 4] >> (e % 4 * 8));
         }
+        __builtin_amdgcn_sched_barrier(0);  // a vector at a time: more rows fit a compute unit
     }
 }
 
 // Every row set (a block, or a wave of one) takes rows at a distance and keeps its sum of dweight.
-template <typename T, typename R, int TPR, int NV>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_bwd(NormBwdArgs p, int sets, bool wide) {
+template <typename T, typename R, int TPR, int NV, bool WIDE>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_bwd(NormBwdArgs p, int sets) {
     constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
     __shared__ double part[TPR > 64 ? TPR / 64 : 1];
-    const int tid = threadIdx.x % TPR, set = blockIdx.x * kRows + threadIdx.x / TPR, D = p.dim;
+    const Piece<TPR, NV, WIDE> own;
+    const int set = blockIdx.x * kRows + threadIdx.x / TPR, D = p.dim;
     if (set >= sets) return;
     float dw[NV][E] = {};
     for (int64_t row = set; row < p.rows; row += sets) {
@@ -223,11 +308,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_bwd(NormBwdArgs p, in
         double sum = 0.0;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int at = (tid + k * TPR) * E;
             float w[E];
-            load8((const R *)p.s + at0, at, D, wide, n[k]);
-            load8((const T *)p.dy + at0, at, D, wide, wd[k]);
-            load8(p.weight, at, D, wide, w);
+            own.load((const R *)p.s + at0, k, D, n[k]);
+            own.load((const T *)p.dy + at0, k, D, wd[k]);
+            own.load(p.weight, k, D, w);
             float t = 0.0f;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -241,23 +325,22 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_bwd(NormBwdArgs p, in
         const float c = (float)(row_sum<TPR>(sum, part) / D);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int at = (tid + k * TPR) * E;
             float g[E];
             if (p.ds) {
-                load8((const R *)p.ds + at0, at, D, wide, g);
+                own.load((const R *)p.ds + at0, k, D, g);
             } else {
 #pragma unroll
                 for (int e = 0; e < E; ++e) g[e] = 0.0f;
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) g[e] += (wd[k][e] - n[k][e] * c) * r;
-            store8((T *)p.dx + at0, at, D, wide, g);
-            if (p.dres) store8((R *)p.dres + at0, at, D, wide, g);
+            own.store((T *)p.dx + at0, k, D, g);
+            if (p.dres) own.store((R *)p.dres + at0, k, D, g);
         }
     }
     float *const to = (float *)p.ws + (int64_t)set * D;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) store8(to, (tid + k * TPR) * E, D, wide, dw[k]);
+    for (int k = 0; k < NV; ++k) own.store(to, k, D, dw[k]);
 }
 
 // 16 columns by 16 rows of partial sums at a time; a thread's rows, then the 16 threads of a column.
@@ -315,17 +398,18 @@ __global__ void __launch_bounds__(256) k_values(const uint8_t *codes, const floa
 
 bool aligned_to(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 
-// Threads of a row: a wave up to 1024 elements, 256 up to 8192, 1024 up to 65536.
+// Threads of a row: a wave up to 1024 elements, 256 up to 4096, 512 up to 8192, 1024 up to 65536.
 template <typename F>
 void by_size(int D, F go) {
     typedef std::integral_constant<int, 64> W;
     typedef std::integral_constant<int, 256> B;
+    typedef std::integral_constant<int, 512> M;
     typedef std::integral_constant<int, 1024> L;
     if (D <= 512) go(W(), std::integral_constant<int, 1>());
     else if (D <= 1024) go(W(), std::integral_constant<int, 2>());
     else if (D <= 2048) go(B(), std::integral_constant<int, 1>());
     else if (D <= 4096) go(B(), std::integral_constant<int, 2>());
-    else if (D <= 8192) go(B(), std::integral_constant<int, 4>());
+    else if (D <= 8192) go(M(), std::integral_constant<int, 2>());
     else if (D <= 16384) go(L(), std::integral_constant<int, 2>());
     else if (D <= 32768) go(L(), std::integral_constant<int, 4>());
     else go(L(), std::integral_constant<int, 8>());
@@ -338,7 +422,13 @@ void run_fwd(const NormArgs &a, hipStream_t s) {
     by_size(a.dim, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, kThreads = TPR < 256 ? 256 : TPR;
         const int64_t blocks = (a.rows + kThreads / TPR - 1) / (kThreads / TPR);
-        k_fwd<T, R, TPR, NV><<<blocks, kThreads, 0, s>>>(a, wide);
+        const auto go = [&](auto mode) {
+            if (wide) k_fwd<T, R, TPR, NV, true, decltype(mode)::value><<<blocks, kThreads, 0, s>>>(a);
+            else k_fwd<T, R, TPR, NV, false, decltype(mode)::value><<<blocks, kThreads, 0, s>>>(a);
+        };
+        if (a.code == 0) go(std::integral_constant<int, kValues>());
+        else if (a.group == 0) go(std::integral_constant<int, kRowCodes>());
+        else go(std::integral_constant<int, kGroupCodes>());
     });
 }
 
@@ -355,7 +445,8 @@ void run_bwd(const NormBwdArgs &a, hipStream_t s) {
     by_size(a.dim, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, kThreads = TPR < 256 ? 256 : TPR;
         const int blocks = (sets + kThreads / TPR - 1) / (kThreads / TPR);
-        k_bwd<T, R, TPR, NV><<<blocks, kThreads, 0, s>>>(a, sets, wide);
+        if (wide) k_bwd<T, R, TPR, NV, true><<<blocks, kThreads, 0, s>>>(a, sets);
+        else k_bwd<T, R, TPR, NV, false><<<blocks, kThreads, 0, s>>>(a, sets);
     });
     k_dweight<<<(a.dim + 15) / 16, 256, 0, s>>>((const float *)a.ws, a.dweight, sets, a.dim);
 }

@@ -145,10 +145,13 @@ def test_unaligned(types):
     b = ssm.ssm_rmsnorm_fwd(m["x"], m["weight"], m["residual"])
     for p, q in zip(a, b):
         assert (p is None) == (q is None) and (p is None or bitwise_equal(p, q))
+    # a row's sums in 32 bits run in another order where its elements are read one by one, so gradients are
+    # equal up to the two sides' own bound, 8 x 2^-24 of the terms (here at most about 10) each
     s = d["x"] if a[1] is None else a[1]
     for p, q in zip(ssm.ssm_rmsnorm_bwd(d["dy"], s, d["weight"], a[2], ds=d["ds"]),
                     ssm.ssm_rmsnorm_bwd(m["dy"], moved(s), m["weight"], moved(a[2]), ds=m["ds"])):
-        assert bitwise_equal(p, q)
+        off = (p.double() - q.double()).abs()
+        assert bool((off <= 2 * 8 * 2.0 ** -24 * 10 + (2 * 2.0 ** -8 * p.double().abs() if p.dtype is BF16 else 0)).all())
     for p, q in zip(ssm.ssm_rmsnorm_fwd_q8(d["x"], d["weight"], d["residual"], group=64),
                     ssm.ssm_rmsnorm_fwd_q8(m["x"], m["weight"], m["residual"], group=64)):
         assert (p is None) == (q is None) and (p is None or torch.equal(p.float(), q.float()))
