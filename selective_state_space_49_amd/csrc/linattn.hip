@@ -572,15 +572,22 @@ __global__ void __launch_bounds__(256) k_join(float *seg, const float *fac, cons
     if (e >= heads * KV) return;
     const int64_t bh = e / KV, at = e % KV;
     float cur = first ? first[e] : 0.0f;
-    for (int i = 0; i < nseg; ++i) {
-        const int s = reverse ? nseg - 1 - i : i;
-        float *const p = seg + (bh * nseg + s) * KV + at;
-        if (i + 1 < nseg) {
-            const float f = fac[bh * nseg + s], add = *p;
-            *p = cur;
-            cur = f == 0.0f ? add : f * cur + add;
-        } else {
-            *p = cur;
+    constexpr int N = 8;  // loads at once
+    for (int i0 = 0; i0 < nseg; i0 += N) {
+        float add[N], f[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int s = reverse ? nseg - 1 - (i0 + k) : i0 + k;
+            const bool there = i0 + k + 1 < nseg;  // what the last one adds is not asked for
+            add[k] = there ? seg[(bh * nseg + s) * KV + at] : 0.0f;
+            f[k] = there ? fac[bh * nseg + s] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            if (i0 + k >= nseg) break;
+            const int s = reverse ? nseg - 1 - (i0 + k) : i0 + k;
+            seg[(bh * nseg + s) * KV + at] = cur;
+            cur = f[k] == 0.0f ? add[k] : f[k] * cur + add[k];
         }
     }
 }
@@ -1075,8 +1082,10 @@ bool aligned_to(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 int chunk_of(int io) { return io ? Kind<__bf16>::C : Kind<float>::C; }
 size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
-// Segments of a sequence: enough blocks for the GPU, but none shorter than 8 chunks, since a sweep
-// over the segments' keys and values comes first where there are several.
+// Segments of a sequence: enough blocks for the GPU, of two chunks at least. A sweep over the segments' keys
+// and values comes first where there are several; with few heads the time is that of a chunk after
+// another, so short segments pay all the same (3 x 1001 tokens of 6 heads, float32: 8 chunks a segment
+// took 75 us forwards, 2 take 31).
 struct Plan {
     int64_t nchunk;
     int nseg, per_seg, slices;
@@ -1085,9 +1094,9 @@ Plan plan(int64_t B, int64_t L, int32_t H, int32_t V, int io, bool bwd) {
     Plan p;
     p.nchunk = (L + chunk_of(io) - 1) / chunk_of(io);
     const int vp = V > 64 ? 128 : 64;
-    // Two blocks of 4 waves a compute unit. Two slices of V, which read q and k twice, where even segments
-    // of 8 chunks are too few.
-    const int64_t want = bwd ? 256 : 512, most = std::max<int64_t>(p.nchunk / 8, 1);
+    // Two blocks of 4 waves a compute unit. Two slices of V, which read q and k twice, where even the shortest
+    // segments are too few.
+    const int64_t want = bwd ? 256 : 512, most = std::max<int64_t>(p.nchunk / 2, 1);
     p.slices = !bwd && vp == 128 && B * H * most < want ? 2 : 1;
     const int64_t blocks = B * H * p.slices;
     int64_t n = blocks > 0 ? (want + blocks - 1) / blocks : 1;
