@@ -76,12 +76,22 @@ __device__ __forceinline__ f32x16 mfma(f32x4 a, f32x4 b, f32x16 c) {
 // x rounded to the operand's type, and x as the sum of kParts of them.
 __device__ __forceinline__ bf16x8 rounded(f32x8 x) { return __builtin_convertvector(x, bf16x8); }
 __device__ __forceinline__ f32x4 rounded(f32x4 x) { return x; }
+// By truncation: 8 bits of 24 each, and nothing is left.
 __device__ __forceinline__ void split(f32x8 x, bf16x8 (&p)[3]) {
-    p[0] = __builtin_convertvector(x, bf16x8);
-    x -= __builtin_convertvector(p[0], f32x8);
-    p[1] = __builtin_convertvector(x, bf16x8);
-    x -= __builtin_convertvector(p[1], f32x8);
-    p[2] = __builtin_convertvector(x, bf16x8);
+    u32x4 q[3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float a = x[2 * e], b = x[2 * e + 1];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t ha = __float_as_uint(a) & 0xffff0000u, hb = __float_as_uint(b) & 0xffff0000u;
+            q[k][e] = __builtin_amdgcn_perm(hb, ha, 0x07060302u);
+            a -= __uint_as_float(ha);
+            b -= __uint_as_float(hb);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) p[k] = __builtin_bit_cast(bf16x8, q[k]);
 }
 __device__ __forceinline__ void split(f32x4 x, f32x4 (&p)[1]) { p[0] = x; }
 __device__ __forceinline__ f32x8 widened(bf16x8 x) { return __builtin_convertvector(x, f32x8); }
@@ -108,35 +118,30 @@ __device__ __forceinline__ void weights_of(const float *w, int s, int half, f32x
     out = *(const f32x4 *)(w + 8 * s + 4 * half);
 }
 
-// ROWS x F elements in LDS, in quads of 4 whose places in a row are permuted (by exclusive or) so that
-// both ways of reading meet no bank twice: a quad of 32 rows (fragments whose lanes are rows), and
-// 4 rows of 32 neighbouring columns (fragments whose lanes are columns).
+// ROWS x F elements in LDS, in quads of 4 whose places in a row are permuted (by exclusive or, 16 bytes at a
+// time) so that both ways of reading meet no bank twice: 16 bytes of 16 rows (fragments whose lanes are
+// rows), and 4 rows of 32 neighbouring columns (fragments whose lanes are columns). bfloat16: the two quads
+// of a lane's fragment, 8 elements apart, lie next to each other.
 template <typename T, int ROWS, int F>
 struct Tile {
     typedef Kind<T> N;
-    static constexpr int W = F / 4, kBytes = ROWS * F * (int)sizeof(T);
-    static __device__ __forceinline__ int swizzle(int r) {
-        if constexpr (sizeof(T) == 2) {
-            if constexpr (W == 32) return (r & 3) << 3 | (r >> 2 & 7);
-            else return (r >> 1 & 1) << 3 | (r >> 2 & 7);  // W = 16
-        } else {
-            if constexpr (W == 8) return r >> 1 & 7;
-            else return (r & 3) | (r >> 2 & 1) << 3 | (r >> 3 & 1) << 2 | (W == 32 ? (r >> 4 & 1) << 4 : 0);
-        }
-    }
+    static constexpr int W = F / 4, kRow = F * (int)sizeof(T), kBytes = ROWS * kRow;
     static __device__ __forceinline__ int at(int row, int quad) {
-        return (row * W + (quad ^ swizzle(row))) * 4 * (int)sizeof(T);
+        if constexpr (sizeof(T) == 2) {
+            const int f = W == 32 ? (row & 3) << 2 | (row >> 2 & 3) : (row >> 1 & 1) << 2 | (row >> 2 & 3);
+            const int place = (quad >> 2) * 2 + (quad & 1);
+            return row * kRow + ((place ^ f) * 2 + (quad >> 1 & 1)) * 8;
+        } else {
+            const int f = W == 8 ? row >> 1 & 7
+                                 : (row & 3) | (row >> 2 & 1) << 3 | (row >> 3 & 1) << 2 | (W == 32 ? (row >> 4 & 1) << 4 : 0);
+            return row * kRow + (quad ^ f) * 16;
+        }
     }
     // Rows start on multiples of their size, so a step or a block changes a lane's address by an exclusive
     // or and a constant, and a lane keeps one number for each way of reading.
     // lanes: rows; contraction: columns KS s .. KS s + KS - 1. from: at(row, half).
     static __device__ __forceinline__ typename N::Frag by_row(const char *t, int from, int s) {
-        if constexpr (sizeof(T) == 2) {
-            const bf16x4 lo = *(const bf16x4 *)(t + (from ^ s * 32)), hi = *(const bf16x4 *)(t + (from ^ s * 32 ^ 16));
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        } else {
-            return *(const f32x4 *)(t + (from ^ s * 32));
-        }
+        return *(const typename N::Frag *)(t + (from ^ s * 32));
     }
     // lanes: columns 32 block + l % 32; contraction: rows KS s .. KS s + KS - 1. from: column_base(lane).
     static __device__ __forceinline__ int column_base(int lane) {
@@ -145,11 +150,10 @@ struct Tile {
         else return at(4 * half, lane >> 2 & 7) + (lane & 3) * 4;
     }
     static __device__ __forceinline__ typename N::Frag by_column(const char *t, int from, int block, int s) {
-        constexpr int kRow = W * 4 * (int)sizeof(T);
         if constexpr (sizeof(T) == 2) {
-            const int c = (s & 1) * 32 | block * 64;
+            const int c = block * 64;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)(t + (from ^ c) + s * 16 * kRow));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)(t + (from ^ c ^ 16) + (s * 16 + 8) * kRow));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((SSM_LDS s16x4 *)(t + (from ^ c ^ 32) + (s * 16 + 8) * kRow));
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             f32x4 f;
@@ -826,9 +830,6 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                     TV::put(ov, j * 32 + l31, part * 8 + 2 * a + half, f32x4{acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]});
                 fence();
             }
-            fetch(c - 1);
-            fence();
-            state_add<T, C, KP, KT>(SV, qt, d, back, dec.whole, half, kcol);
             if (wave == 0) {
                 // dg's pairs. Row j becomes its sums from i on; then token t adds the rows before it.
                 if (lane < C) {
@@ -947,8 +948,6 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                 }
                 put(acc, p.dk);
             }
-            fetch(c - 1);
-            fence();
             add_in(1);
             own(aq, qt, back, came[part]);
 #pragma unroll
@@ -970,10 +969,20 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
 #pragma unroll
             for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
             if (lane == 0) through[part] = dec.whole == 0.0f ? 0.0f : x * dec.whole;
-            Frag fq[C / KS];
+        }
+        // Here the roles meet, so that the next chunk's registers are the same ones in both.
+        fence();
+        fetch(c - 1);
+        fence();
+        Frag f[C / KS];
+        if (of_v) {
 #pragma unroll
-            for (int s = 0; s < C / KS; ++s) fq[s] = TK::by_column(qt, column, 0, s);
-            state_add<T, C, VP, VW>(SK, dt, fq, back, dec.whole, half, vcol);
+            for (int s = 0; s < C / KS; ++s) f[s] = TV::by_column(dt, vcol ^ (part * 32 * (int)sizeof(T)), 0, s);
+            state_add<T, C, KP, KT>(SV, qt, f, back, dec.whole, half, kcol);
+        } else {
+#pragma unroll
+            for (int s = 0; s < C / KS; ++s) f[s] = TK::by_column(qt, kcol ^ (part * 32 * (int)sizeof(T)), 0, s);
+            state_add<T, C, VP, VW>(SK, dt, f, back, dec.whole, half, vcol);
         }
         __syncthreads();
         if (wave == 0) {  // dg
@@ -1084,8 +1093,8 @@ size_t up(size_t v) { return (v + 255) / 256 * 256; }
 
 // Segments of a sequence: enough blocks for the GPU, of two chunks at least. A sweep over the segments' keys
 // and values comes first where there are several; with few heads the time is that of a chunk after
-// another, so short segments pay all the same (3 x 1001 tokens of 6 heads, float32: 8 chunks a segment
-// took 75 us forwards, 2 take 31).
+// another, so short segments pay all the same (3 x 1001 tokens of 6 heads, float32: 73 us forwards and 149
+// back with 8 chunks a segment, 46 and 63 with 2).
 struct Plan {
     int64_t nchunk;
     int nseg, per_seg, slices;
