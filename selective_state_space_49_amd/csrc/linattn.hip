@@ -29,6 +29,8 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
+#include <type_traits>
 
 #include "ssm_layers.h"
 
@@ -44,6 +46,10 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #define SSM_LDS __attribute__((address_space(3)))
+
+// How rows are read and written: whole vectors of 16 bytes that start on 16 bytes; vectors that start on any
+// element, the last of a row ending with it (rows of a vector at least); or elements.
+enum Access { kWide, kAny, kElements };
 
 constexpr float kCut = -104.0f;  // exp of less is 0 in float32
 constexpr double kLog2e = 1.4426950408889634;
@@ -180,13 +186,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t range_of(const void *p, int64_
     return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, (int)bytes, 0x00020000);
 }
 // Four float32 or bfloat16 values at element e of a row that starts at byte `at`; `width` elements long.
-template <typename T, bool WIDE>
+template <typename T, Access ACC>
 __device__ __forceinline__ void put_quad(__amdgpu_buffer_rsrc_t to, int at, int e, int width, f32x4 x) {
-    if constexpr (WIDE) {
-        const int o = e < width ? at + e * (int)sizeof(T) : kOut;
+    if (ACC != kElements) {
+        const int o = e + 4 <= width ? at + e * (int)sizeof(T) : kOut;
         if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, __builtin_convertvector(x, bf16x4)), to, o, 0, 0);
         else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), to, o, 0, 0);
-    } else {
+    }
+    if (ACC == kElements || (ACC == kAny && e < width && e + 4 > width)) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int o = e + k < width ? at + (e + k) * (int)sizeof(T) : kOut;
@@ -195,10 +202,24 @@ __device__ __forceinline__ void put_quad(__amdgpu_buffer_rsrc_t to, int at, int 
         }
     }
 }
+// The last vector of a row is read so that it ends with the row; its elements from d on are the asked ones
+// (d of a vector or more: none, the load was out of range), and what is past the row is 0.
+template <typename T>
+__device__ __forceinline__ u32x4 moved_down(u32x4 r, int d) {
+    const int dwords = sizeof(T) == 2 ? d >> 1 : d;
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t bits = (d & 1) * 16;
+        r = u32x4{__builtin_amdgcn_alignbit(r[1], r[0], bits), __builtin_amdgcn_alignbit(r[2], r[1], bits),
+                  __builtin_amdgcn_alignbit(r[3], r[2], bits), __builtin_amdgcn_alignbit(0u, r[3], bits)};
+    }
+    if (dwords & 1) r = u32x4{r[1], r[2], r[3], 0u};
+    if (dwords & 2) r = u32x4{r[2], r[3], 0u, 0u};
+    return r;
+}
 
 // Rows of a finished tile in LDS to global memory, 16 bytes a lane.
-template <typename T, int ROWS, int F, int THREADS, bool WIDE>
-__device__ __forceinline__ void put_rows(const char *t, __amdgpu_buffer_rsrc_t to, int stride, int rows, int width, int tid) {
+template <typename T, int ROWS, int F, int THREADS, Access ACC>
+__device__ __forceinline__ void put_rows(const char *t, __amdgpu_buffer_rsrc_t to, int stride, int rows, int width, int tid, int c0 = 0) {
     constexpr int kElems = 16 / sizeof(T), kPerRow = F / kElems, kStep = THREADS / kPerRow, N = (ROWS + kStep - 1) / kStep;
     const int c = tid % kPerRow;
 #pragma unroll
@@ -212,10 +233,9 @@ __device__ __forceinline__ void put_rows(const char *t, __amdgpu_buffer_rsrc_t t
         } else {
             x = *(const u32x4 *)(t + Tile<T, ROWS, F>::at(row, c));
         }
-        const int o = row < rows ? row * stride + c * 16 : kOut, e = c * kElems;
-        if constexpr (WIDE) {
-            __builtin_amdgcn_raw_buffer_store_b128(x, to, e < width ? o : kOut, 0, 0);
-        } else {
+        const int e = c0 + c * kElems, o = row < rows ? row * stride + e * (int)sizeof(T) : kOut;
+        if (ACC != kElements) __builtin_amdgcn_raw_buffer_store_b128(x, to, e + kElems <= width ? o : kOut, 0, 0);
+        if (ACC == kElements || (ACC == kAny && e < width && e + kElems > width)) {
 #pragma unroll
             for (int k = 0; k < kElems; ++k) {
                 const int w = e + k < width ? o + k * (int)sizeof(T) : kOut;
@@ -227,19 +247,24 @@ __device__ __forceinline__ void put_rows(const char *t, __amdgpu_buffer_rsrc_t t
 }
 
 // A tile's way from global memory to LDS through registers: rows of `width` elements, `stride` bytes
-// apart; rows past `rows` and columns past `width` become 0.
-template <typename T, int ROWS, int F, int THREADS, bool WIDE>
+// apart, from column c0 on; rows past `rows` and columns past `width` become 0.
+template <typename T, int ROWS, int F, int THREADS, Access ACC>
 struct Stage {
     static constexpr int kElems = 16 / sizeof(T), kPerRow = F / kElems, kStep = THREADS / kPerRow;
     static constexpr int N = (ROWS + kStep - 1) / kStep;
     static_assert(THREADS % kPerRow == 0, "a thread keeps its column");
     u32x4 r[N];
-    __device__ __forceinline__ void load(const T *p, int stride, int rows, int width, int tid) {
-        const int row = tid / kPerRow, c = tid % kPerRow * kElems;
+    __device__ __forceinline__ void load(const T *p, int stride, int rows, int width, int tid, int c0 = 0) {
+        const int row = tid / kPerRow, c = c0 + tid % kPerRow * kElems;
         const __amdgpu_buffer_rsrc_t from = range_of(p, rows > 0 ? (int64_t)(rows - 1) * stride + width * (int64_t)sizeof(T) : 0);
         const int o = row * stride + c * (int)sizeof(T);
-        if constexpr (WIDE) {
+        if constexpr (ACC == kWide) {
             const int at = c < width ? o : kOut;
+#pragma unroll
+            for (int n = 0; n < N; ++n) r[n] = __builtin_amdgcn_raw_buffer_load_b128(from, at + n * kStep * stride, 0, 0);
+        } else if constexpr (ACC == kAny) {
+            // moved down when it is stored: the loads stay on their way
+            const int first = min(c, width - kElems), at = c - first < kElems ? row * stride + first * (int)sizeof(T) : kOut;
 #pragma unroll
             for (int n = 0; n < N; ++n) r[n] = __builtin_amdgcn_raw_buffer_load_b128(from, at + n * kStep * stride, 0, 0);
         } else {
@@ -257,16 +282,18 @@ struct Stage {
             }
         }
     }
-    __device__ __forceinline__ void store(char *t, int tid) const {
+    __device__ __forceinline__ void store(char *t, int tid, int width, int c0 = 0) const {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int row = tid / kPerRow + n * kStep, c = tid % kPerRow;
             if (ROWS % kStep != 0 && row >= ROWS) break;
+            u32x4 x = r[n];
+            if constexpr (ACC == kAny) x = moved_down<T>(x, c0 + c * kElems - min(c0 + c * kElems, width - kElems));
             if constexpr (sizeof(T) == 2) {
-                *(u32x2 *)(t + Tile<T, ROWS, F>::at(row, 2 * c)) = u32x2{r[n][0], r[n][1]};
-                *(u32x2 *)(t + Tile<T, ROWS, F>::at(row, 2 * c + 1)) = u32x2{r[n][2], r[n][3]};
+                *(u32x2 *)(t + Tile<T, ROWS, F>::at(row, 2 * c)) = u32x2{x[0], x[1]};
+                *(u32x2 *)(t + Tile<T, ROWS, F>::at(row, 2 * c + 1)) = u32x2{x[2], x[3]};
             } else {
-                *(u32x4 *)(t + Tile<T, ROWS, F>::at(row, c)) = r[n];
+                *(u32x4 *)(t + Tile<T, ROWS, F>::at(row, c)) = x;
             }
         }
     }
@@ -391,7 +418,7 @@ __device__ __forceinline__ void state_add(f32x16 (&S)[TILES], const char *k_tile
 
 // One sweep over a segment of a sequence's chunks for NW x 32 columns of one head's state. OUT: with
 // outputs, from the segment's entering state; else what the segment adds to the state, from 0.
-template <typename T, int KP, int NW, bool OUT, bool WIDE>
+template <typename T, int KP, int NW, bool OUT, Access ACC>
 __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
     typedef Kind<T> N;
     typedef typename N::Frag Frag;
@@ -426,8 +453,8 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
         if (OUT) from = p.seg_in ? p.seg_in + (bh * nseg_all + seg) * KV : p.first ? p.first + bh * KV : nullptr;
         state_load<KT>(S, from, p.K, p.V, vcol, half);
     }
-    Stage<T, C, KP, THREADS, WIDE> kr, qr;
-    Stage<T, C, VT, THREADS, WIDE> vr;
+    Stage<T, C, KP, THREADS, ACC> kr, qr;
+    Stage<T, C, VT, THREADS, ACC> vr;
     const int ks = p.Hk * p.K * (int)sizeof(T), vs = p.H * p.V * (int)sizeof(T);  // bytes of a token
     const bool rev = !OUT && p.reverse;
     const auto chunk = [&](int it) { return rev ? c1 - 1 - it : c0 + it; };
@@ -438,7 +465,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
         const int c = chunk(min(it, n - 1)), rows = it < n ? rows_at(c) : 0;
         const int64_t at = b * p.L + (int64_t)c * C;
         kr.load((const T *)((const char *)p.k + at * ks) + (int64_t)hk * p.K, ks, rows, p.K, tid);
-        vr.load((const T *)((const char *)p.v + at * vs) + (int64_t)h * p.V + v0, vs, rows, p.V - v0, tid);
+        vr.load((const T *)((const char *)p.v + at * vs) + (int64_t)h * p.V, vs, rows, p.V, tid, v0);
         if (OUT) qr.load((const T *)((const char *)p.q + at * ks) + (int64_t)hk * p.K, ks, rows, p.K, tid);
     };
     // One wave makes the decays, a chunk ahead, from a g that was loaded another chunk ahead.
@@ -459,9 +486,9 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
     // loads are not waited for with them.
     const auto put_outputs = [&](int c) {
         const int rows = rows_at(c);
-        put_rows<T, C, VT, THREADS, WIDE>(ot, range_of((const char *)p.o + (b * p.L + (int64_t)c * C) * vs + ((int64_t)h * p.V + v0) * (int)sizeof(T),
-                                                       (int64_t)(rows - 1) * vs + (p.V - v0) * (int64_t)sizeof(T)),
-                                          vs, rows, p.V - v0, tid);
+        put_rows<T, C, VT, THREADS, ACC>(ot, range_of((const char *)p.o + (b * p.L + (int64_t)c * C) * vs + (int64_t)h * p.V * (int)sizeof(T),
+                                                      (int64_t)(rows - 1) * vs + p.V * (int64_t)sizeof(T)),
+                                         vs, rows, p.V, tid, v0);
     };
     if (n > 0) {
         if (decides) {
@@ -482,9 +509,9 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
         l31 = lane & 31;
         vcol = v0 + wave * 32 + l31;
         const Decays<C> &dec = decays[it & 1];
-        kr.store(kt, tid);
-        vr.store(vt, tid);
-        if (OUT) qr.store(qt, tid);
+        kr.store(kt, tid, p.K);
+        vr.store(vt, tid, p.V, v0);
+        if (OUT) qr.store(qt, tid, p.K);
         __syncthreads();
         if (OUT) {
             if (p.states) state_store<KT>(S, p.states + (bh * p.nchunk + c) * KV, p.K, p.V, vcol, half);
@@ -608,7 +635,7 @@ struct BwdArgs {
 
 // The gradients of a segment, from its end. VP / 32 waves hold dS by columns of V and make dv;
 // KP / 32 waves hold it transposed, by columns of K, and make dk and dq.
-template <typename T, int KP, int VP, bool WIDE>
+template <typename T, int KP, int VP, Access ACC>
 __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     typedef Kind<T> N;
     typedef typename N::Frag Frag;
@@ -659,8 +686,8 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                 }
         }
     }
-    Stage<T, C, KP, THREADS, WIDE> qr, kr;
-    Stage<T, C, VP, THREADS, WIDE> vr, dr;
+    Stage<T, C, KP, THREADS, ACC> qr, kr;
+    Stage<T, C, VP, THREADS, ACC> vr, dr;
     const int ks = p.Hk * p.K * (int)sizeof(T), vs = p.H * p.V * (int)sizeof(T);  // bytes of a token
     const bool shared = share > 1;
     const int ksz = shared ? 4 : (int)sizeof(T), dks = shared ? p.H * p.K * 4 : ks;  // of an element and a token of dq and dk
@@ -683,8 +710,8 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     };
     // As in the sweep: dv and dq (of T) wait in LDS until the next chunk's loads are due.
     const auto put_outputs = [&](int c) {
-        put_rows<T, C, VP, THREADS, WIDE>(ov, range_v(c), vs, rows_at(c), p.V, tid);
-        if (!shared) put_rows<T, C, KP, THREADS, WIDE>(oq, range_k(p.dq, c), dks, rows_at(c), p.K, tid);
+        put_rows<T, C, VP, THREADS, ACC>(ov, range_v(c), vs, rows_at(c), p.V, tid);
+        if (!shared) put_rows<T, C, KP, THREADS, ACC>(oq, range_k(p.dq, c), dks, rows_at(c), p.K, tid);
     };
     // And one wave makes the decays a chunk ahead.
     const bool decides = wave == VW - 1;
@@ -713,10 +740,10 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
         lane = tid & 63;
         half = lane >> 5;
         l31 = lane & 31;
-        qr.store(qt, tid);
-        kr.store(kt, tid);
-        vr.store(vt, tid);
-        dr.store(dt, tid);
+        qr.store(qt, tid, p.K);
+        kr.store(kt, tid, p.K);
+        vr.store(vt, tid, p.V);
+        dr.store(dt, tid, p.V);
         __syncthreads();
         if (c + 1 < c1) put_outputs(c + 1);
         constexpr int kDown = 32 * TK::kBytes / C, vDown = 32 * TV::kBytes / C, pDown = 32 * TP::kBytes / C;  // 32 rows further
@@ -730,8 +757,12 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
 #pragma unroll
             for (int a = 0; a < kIn; ++a) {
                 const int v = 8 * (a + part_v * kIn) + 4 * half;
-                if constexpr (WIDE) {
+                if constexpr (ACC == kWide) {
                     in[a] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, v < p.V ? at + 32 * (a + part_v * kIn) : kOut, 0, 0));
+                } else if constexpr (ACC == kAny) {
+                    const int first = min(v, p.V - 4);
+                    const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(from, v < p.V ? at + 4 * (first - 4 * half) : kOut, 0, 0);
+                    in[a] = __builtin_bit_cast(f32x4, moved_down<float>(x, v - first));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -886,8 +917,8 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                     for (int a = 0; a < 4; ++a) {
                         const int e = part * 32 + 8 * a + 4 * half;
                         const f32x4 x = {acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]};
-                        if (!shared) put_quad<T, WIDE>(to, row * dks, e, width, x);
-                        else put_quad<float, WIDE>(to, row * dks, e, width, x);
+                        if (!shared) put_quad<T, ACC>(to, row * dks, e, width, x);
+                        else put_quad<float, ACC>(to, row * dks, e, width, x);
                     }
                     fence();
                 }
@@ -1116,21 +1147,48 @@ Plan plan(int64_t B, int64_t L, int32_t H, int32_t V, int io, bool bwd) {
     return p;
 }
 
-// wide: rows and pointers allow vectors of 16 bytes. Others are read element by element, by the kernels of
-// the largest sizes.
+template <typename T>
+Access access(int32_t K, int32_t V, std::initializer_list<const void *> arrays) {
+    constexpr int E = 16 / sizeof(T);
+    if (K < E || V < E) return kElements;
+    for (const void *p : arrays)
+        if (!aligned_to(p, 16)) return kAny;
+    return K % E == 0 && V % E == 0 ? kWide : kAny;
+}
+
+// Rows shorter than a vector are read by the kernels of the largest sizes only.
 template <typename T, bool OUT>
-void sweep(const SweepArgs &a, bool wide, int64_t blocks, hipStream_t s) {
+void sweep(const SweepArgs &a, Access access, int64_t blocks, hipStream_t s) {
     const int width = (a.V > 64 ? 128 : 64) / a.slices;
-    if (!wide) {
-        if (width == 128) k_sweep<T, 128, 4, OUT, false><<<blocks, 256, 0, s>>>(a);
-        else k_sweep<T, 128, 2, OUT, false><<<blocks, 128, 0, s>>>(a);
-    } else if (a.K > 64) {
-        if (width == 128) k_sweep<T, 128, 4, OUT, true><<<blocks, 256, 0, s>>>(a);
-        else k_sweep<T, 128, 2, OUT, true><<<blocks, 128, 0, s>>>(a);
-    } else {
-        if (width == 128) k_sweep<T, 64, 4, OUT, true><<<blocks, 256, 0, s>>>(a);
-        else k_sweep<T, 64, 2, OUT, true><<<blocks, 128, 0, s>>>(a);
-    }
+    const auto go = [&](auto acc) {
+        constexpr Access A = decltype(acc)::value;
+        if (a.K > 64 || A == kElements) {
+            if (width == 128) k_sweep<T, 128, 4, OUT, A><<<blocks, 256, 0, s>>>(a);
+            else k_sweep<T, 128, 2, OUT, A><<<blocks, 128, 0, s>>>(a);
+        } else {
+            if (width == 128) k_sweep<T, 64, 4, OUT, A><<<blocks, 256, 0, s>>>(a);
+            else k_sweep<T, 64, 2, OUT, A><<<blocks, 128, 0, s>>>(a);
+        }
+    };
+    if (access == kWide) go(std::integral_constant<Access, kWide>());
+    else if (access == kAny) go(std::integral_constant<Access, kAny>());
+    else go(std::integral_constant<Access, kElements>());
+}
+template <typename T>
+void bwd(const BwdArgs &a, Access access, int64_t blocks, hipStream_t s) {
+    const auto go = [&](auto acc) {
+        constexpr Access A = decltype(acc)::value;
+        if (a.K > 64) {
+            if (a.V > 64) k_bwd<T, 128, 128, A><<<blocks, 512, 0, s>>>(a);
+            else k_bwd<T, 128, 64, A><<<blocks, 384, 0, s>>>(a);
+        } else {
+            if (a.V > 64) k_bwd<T, 64, 128, A><<<blocks, 384, 0, s>>>(a);
+            else k_bwd<T, 64, 64, A><<<blocks, 256, 0, s>>>(a);
+        }
+    };
+    if (access == kWide) go(std::integral_constant<Access, kWide>());
+    else if (access == kAny) go(std::integral_constant<Access, kAny>());
+    else k_bwd<T, 128, 128, kElements><<<blocks, 512, 0, s>>>(a);
 }
 
 template <typename T>
@@ -1146,21 +1204,20 @@ hipError_t run_fwd(const LinattnArgs &a, hipStream_t s) {
     p.g_token = a.per_token ? a.H : 0;
     p.nchunk = (int)pl.nchunk; p.per_seg = pl.per_seg; p.slices = pl.slices;
     p.scale = a.scale;
-    constexpr int E = 16 / sizeof(T);
-    const bool wide = a.K % E == 0 && a.V % E == 0 && aligned_to(a.q, 16) && aligned_to(a.k, 16) && aligned_to(a.v, 16) && aligned_to(a.o, 16);
+    const Access acc = access<T>(a.K, a.V, {a.q, a.k, a.v, a.o});
     if (pl.nseg > 1) {
         SweepArgs q = p;
         q.nseg = pl.nseg - 1;
         q.seg_out = seg;
         q.seg_fac = fac;
-        sweep<T, false>(q, wide, heads * q.nseg * q.slices, s);
+        sweep<T, false>(q, acc, heads * q.nseg * q.slices, s);
         k_join<<<(heads * KV + 255) / 256, 256, 0, s>>>(seg, fac, a.h0, KV, heads, pl.nseg, false);
         p.seg_in = seg;
     }
     p.nseg = pl.nseg;
     p.first = a.h0;
     p.o = a.o; p.last = a.h_final; p.states = a.states;
-    sweep<T, true>(p, wide, heads * p.nseg * p.slices, s);
+    sweep<T, true>(p, acc, heads * p.nseg * p.slices, s);
     return hipGetLastError();
 }
 
@@ -1196,7 +1253,6 @@ hipError_t run_bwd(const LinattnArgs &a, hipStream_t s) {
     const int64_t heads = a.B * a.H, KV = (int64_t)a.K * a.V;
     char *const ws = (char *)a.ws;
     float *const seg = (float *)ws, *const fac = (float *)(ws + pl.fac);
-    constexpr int E = 16 / sizeof(T);
     BwdArgs p{};
     p.q = a.q; p.k = a.k; p.v = a.v; p.do_ = a.do_; p.g = a.g; p.states = a.states;
     p.L = a.L; p.H = a.H; p.Hk = a.Hk; p.K = a.K; p.V = a.V;
@@ -1204,9 +1260,7 @@ hipError_t run_bwd(const LinattnArgs &a, hipStream_t s) {
     p.g_token = a.per_token ? a.H : 0;
     p.nchunk = (int)pl.seg.nchunk; p.per_seg = pl.seg.per_seg; p.nseg = pl.seg.nseg;
     p.scale = a.scale;
-    bool wide = a.K % E == 0 && a.V % E == 0;
-    for (const void *x : {a.q, a.k, a.v, a.do_, (const void *)a.states, (const void *)a.dq, (const void *)a.dk, (const void *)a.dv})
-        wide &= aligned_to(x, 16);
+    const Access acc = access<T>(a.K, a.V, {a.q, a.k, a.v, a.do_, a.states, a.dq, a.dk, a.dv});
     const bool shared = a.H != a.Hk;
     p.dq = shared ? ws + pl.dq : (char *)a.dq;
     p.dk = shared ? ws + pl.dk : (char *)a.dk;
@@ -1223,20 +1277,12 @@ hipError_t run_bwd(const LinattnArgs &a, hipStream_t s) {
             q.nchunk = p.nchunk; q.per_seg = p.per_seg; q.nseg = p.nseg - 1; q.slices = pl.pass.slices;
             q.scale = a.scale; q.reverse = true;
             q.seg_out = seg; q.seg_fac = fac;
-            sweep<T, false>(q, wide, heads * q.nseg * q.slices, s);
+            sweep<T, false>(q, acc, heads * q.nseg * q.slices, s);
             k_join<<<(heads * KV + 255) / 256, 256, 0, s>>>(seg, fac, a.dh_final, KV, heads, p.nseg, true);
             p.seg_in = seg;
         }
         const int64_t blocks = heads * p.nseg;
-        if (!wide) {
-            k_bwd<T, 128, 128, false><<<blocks, 512, 0, s>>>(p);
-        } else if (a.K > 64) {
-            if (a.V > 64) k_bwd<T, 128, 128, true><<<blocks, 512, 0, s>>>(p);
-            else k_bwd<T, 128, 64, true><<<blocks, 384, 0, s>>>(p);
-        } else {
-            if (a.V > 64) k_bwd<T, 64, 128, true><<<blocks, 384, 0, s>>>(p);
-            else k_bwd<T, 64, 64, true><<<blocks, 256, 0, s>>>(p);
-        }
+        bwd<T>(p, acc, blocks, s);
         if (shared && a.L > 0) {
             const int64_t n = a.B * a.L * a.Hk * a.K;
             k_groups<T><<<(n + 255) / 256, 256, 0, s>>>((const float *)p.dq, (const float *)p.dk, (T *)a.dq, (T *)a.dk, n, a.K,

@@ -270,3 +270,24 @@ def test_autograd():
     with pytest.raises(RuntimeError):
         gq, = torch.autograd.grad(o.sum(), c["q"], create_graph=True)
         gq.sum().backward()
+
+
+ODD = [(2, 70, 2, 2, 8, 9), (1, 65, 2, 1, 9, 8), (1, 100, 3, 3, 17, 33), (2, 64, 2, 2, 31, 66), (1, 90, 2, 1, 67, 15),
+       (1, 130, 2, 2, 70, 121), (1, 129, 4, 2, 12, 20), (1, 33, 2, 2, 7, 40), (1, 80, 2, 2, 100, 5), (1, 66, 1, 1, 113, 126)]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", ODD, ids=str)
+def test_odd_widths(size, io):
+    """Rows that are no whole vectors, the last of which ends with the row; and rows shorter than one.
+    What lies beside the outputs stays."""
+    say("linattn odd", size, io)
+    d = make(*size, io=io, cuts=0.05, h0=True)
+    got, _ = against(d)
+    c = dev(d)
+    n = d["v"].numel()
+    room = torch.full((n + 600,), 7.0, dtype=IO[io], device="cuda")
+    at = 257
+    ssm.ssm_linattn_fwd(c["q"], c["k"], c["v"], c["g"], c["h0"], o=room[at:at + n].view(d["v"].shape))
+    assert bitwise_equal(room[at:at + n].view(d["v"].shape).clone(), got["o"])
+    assert bool((room[:at] == 7).all()) and bool((room[at + n:] == 7).all())
