@@ -165,7 +165,7 @@ struct Tile {
             f32x4 f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int c = (e | (s & 1) << 2 | (W == 32 ? (s >> 1 & 1) << 4 : 0)) * 16 ^ block * 128;
+                const int c = W == 8 ? (e >> 1 | (s & 1) << 2) * 16 : (e | (s & 1) << 2 | (W == 32 ? (s >> 1 & 1) << 4 : 0)) * 16 ^ block * 128;
                 f[e] = *(const float *)(t + (from ^ c) + (8 * s + e) * kRow);
             }
             return f;
@@ -1071,49 +1071,58 @@ __global__ void __launch_bounds__(256) k_decay_sum(const float *dg, float *out, 
     if (threadIdx.x == 0) out[h] = (float)(part[0] + part[1] + part[2] + part[3]);
 }
 
-// One token: a block has 32 columns of V of one head's state, 8 lanes of 4 (or 32 of 1) for a row.
-template <typename T, bool WIDE>
+// One token: a block has 32 columns of V of one head's state, 8 lanes of 4 for a row (which may start on any
+// element; the row's last lane may have fewer).
+typedef f32x4 __attribute__((aligned(4))) any_f32x4;
+template <typename T>
 __global__ void __launch_bounds__(256) k_step(LinattnStepArgs p) {
-    constexpr int E = WIDE ? 4 : 1, kLanes = 32 / E, kRows = 256 / kLanes;
-    typedef float fv __attribute__((ext_vector_type(E)));
     const int slices = (p.V + 31) / 32, slice = blockIdx.x % slices;
     const int64_t nh = blockIdx.x / slices, n = nh / p.H;
     const int h = (int)(nh % p.H), hk = h / (p.H / p.Hk);
-    const int v = slice * 32 + threadIdx.x % kLanes * E, r0 = threadIdx.x / kLanes;
-    const bool live = v < p.V;
+    const int v = slice * 32 + threadIdx.x % 8 * 4, r0 = threadIdx.x / 8, live = min(max(p.V - v, 0), 4);
     const float g = p.g[(p.per_token ? n : n / p.seqs) * p.H + h];
     const float a = g < kCut ? 0.0f : __expf(g);
     const T *const q = (const T *)p.q + (n * p.Hk + hk) * p.K, *const k = (const T *)p.k + (n * p.Hk + hk) * p.K;
-    fv x = {};
-    if (live) {
+    f32x4 x = {0, 0, 0, 0}, o = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = (float)((const T *)p.v + nh * p.V)[v + e];
-    }
-    float *const S = p.h + nh * p.K * p.V;
-    fv o = {};
-    if (live) {
+    for (int e = 0; e < 4; ++e)
+        if (e < live) x[e] = (float)((const T *)p.v + nh * p.V)[v + e];
+    float *const S = p.h + nh * p.K * p.V + v;
+    const auto add = [&](f32x4 s, int r) {
+        const float kr = (float)k[r], qr = (float)q[r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            s[e] = (a == 0.0f ? 0.0f : a * s[e]) + kr * x[e];
+            o[e] += qr * s[e];
+        }
+        return s;
+    };
+    if (live == 4) {
 #pragma unroll 4
-        for (int r = r0; r < p.K; r += kRows) {
-            fv *const at = (fv *)(S + (int64_t)r * p.V + v);
-            fv s = *at;
-            const float kr = (float)k[r], qr = (float)q[r];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                s[e] = (a == 0.0f ? 0.0f : a * s[e]) + kr * x[e];
-                o[e] += qr * s[e];
-            }
-            *at = s;
+        for (int r = r0; r < p.K; r += 32) {
+            any_f32x4 *const at = (any_f32x4 *)(S + (int64_t)r * p.V);
+            *at = add(*at, r);
+        }
+    } else if (live > 0) {
+        for (int r = r0; r < p.K; r += 32) {
+            float *const at = S + (int64_t)r * p.V;
+            f32x4 s = {0, 0, 0, 0};
+            for (int e = 0; e < live; ++e) s[e] = at[e];
+            s = add(s, r);
+            for (int e = 0; e < live; ++e) at[e] = s[e];
         }
     }
-    __shared__ fv sum[kRows][kLanes];
-    sum[r0][threadIdx.x % kLanes] = o;
+    __shared__ f32x4 sum[32][8];
+    sum[r0][threadIdx.x % 8] = o;
     __syncthreads();
-    if (threadIdx.x < kLanes && live) {
-        fv t = {};
-        for (int r = 0; r < kRows; ++r) t += sum[r][threadIdx.x];
+    if (threadIdx.x < 8) {
+        f32x4 t = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < 32; ++r) t += sum[r][threadIdx.x];
         T *const out = (T *)p.o + nh * p.V + v;
 #pragma unroll
-        for (int e = 0; e < E; ++e) out[e] = (T)(t[e] * p.scale);
+        for (int e = 0; e < 4; ++e)
+            if (e < live) out[e] = (T)(t[e] * p.scale);
     }
 }
 
@@ -1165,6 +1174,11 @@ void sweep(const SweepArgs &a, Access access, int64_t blocks, hipStream_t s) {
         if (a.K > 64 || A == kElements) {
             if (width == 128) k_sweep<T, 128, 4, OUT, A><<<blocks, 256, 0, s>>>(a);
             else k_sweep<T, 128, 2, OUT, A><<<blocks, 128, 0, s>>>(a);
+        } else if (sizeof(T) == 4 && a.K <= 32) {  // products in float32 are what bounds it
+            if constexpr (sizeof(T) == 4 && A != kElements) {
+                if (width == 128) k_sweep<T, 32, 4, OUT, A><<<blocks, 256, 0, s>>>(a);
+                else k_sweep<T, 32, 2, OUT, A><<<blocks, 128, 0, s>>>(a);
+            }
         } else {
             if (width == 128) k_sweep<T, 64, 4, OUT, A><<<blocks, 256, 0, s>>>(a);
             else k_sweep<T, 64, 2, OUT, A><<<blocks, 128, 0, s>>>(a);
@@ -1181,6 +1195,11 @@ void bwd(const BwdArgs &a, Access access, int64_t blocks, hipStream_t s) {
         if (a.K > 64) {
             if (a.V > 64) k_bwd<T, 128, 128, A><<<blocks, 512, 0, s>>>(a);
             else k_bwd<T, 128, 64, A><<<blocks, 384, 0, s>>>(a);
+        } else if (sizeof(T) == 4 && a.K <= 32) {
+            if constexpr (sizeof(T) == 4) {
+                if (a.V > 64) k_bwd<T, 32, 128, A><<<blocks, 320, 0, s>>>(a);
+                else k_bwd<T, 32, 64, A><<<blocks, 192, 0, s>>>(a);
+            }
         } else {
             if (a.V > 64) k_bwd<T, 64, 128, A><<<blocks, 384, 0, s>>>(a);
             else k_bwd<T, 64, 64, A><<<blocks, 256, 0, s>>>(a);
@@ -1311,9 +1330,8 @@ hipError_t launch_linattn_bwd(const LinattnArgs &a, int io, hipStream_t s) {
 }
 hipError_t launch_linattn_step(const LinattnStepArgs &a, int io, hipStream_t s) {
     const int64_t blocks = a.layers * a.seqs * a.H * ((a.V + 31) / 32);
-    const bool wide = a.V % 4 == 0 && aligned_to(a.h, 16);
-    if (io) wide ? k_step<__bf16, true><<<blocks, 256, 0, s>>>(a) : k_step<__bf16, false><<<blocks, 256, 0, s>>>(a);
-    else wide ? k_step<float, true><<<blocks, 256, 0, s>>>(a) : k_step<float, false><<<blocks, 256, 0, s>>>(a);
+    if (io) k_step<__bf16><<<blocks, 256, 0, s>>>(a);
+    else k_step<float><<<blocks, 256, 0, s>>>(a);
     return hipGetLastError();
 }
 

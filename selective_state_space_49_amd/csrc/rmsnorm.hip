@@ -34,56 +34,60 @@ __device__ __forceinline__ uint32_t narrow(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
-// Which elements of a row a thread holds, eight for each of its NV vectors. WIDE (rows of whole vectors
-// that start on 16 bytes): eight neighbours. Else one of every 64, so that a wave reads neighbours; a
-// wave's elements are one piece of the row in both.
-template <int TPR, int NV, bool WIDE>
+// A thread's elements of a row: eight neighbours for each of its NV vectors. A vector may start on any
+// element (the hardware reads and writes 16 bytes there); the last of a row may be shorter, then the
+// one thread that has it goes by elements.
+typedef u32x4 __attribute__((aligned(2))) any_u32x4;
+typedef u32x2 __attribute__((aligned(1))) any_u32x2;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 __attribute__((aligned(4))) any_f32x4;
+
+template <int TPR>
 struct Piece {
     int first;
-    __device__ __forceinline__ Piece() {
-        const int tid = threadIdx.x % TPR;
-        first = WIDE ? tid * E : tid / 64 * (64 * E * NV) + tid % 64;
-    }
-    __device__ __forceinline__ int at(int n, int e) const { return WIDE ? first + n * TPR * E + e : first + (n * E + e) * 64; }
+    __device__ __forceinline__ Piece() { first = threadIdx.x % TPR * E; }
+    __device__ __forceinline__ int at(int n) const { return first + n * TPR * E; }
     // What is past the row's end is 0.
     template <typename T>
     __device__ __forceinline__ void load(const T *row, int n, int width, float (&x)[E]) const {
-        const int from = at(n, 0);
-        if constexpr (WIDE) {
-            if (from < width) {
-                if constexpr (sizeof(T) == 2) {
-                    const u32x4 r = *(const u32x4 *)(row + from);
+        const int from = at(n);
+        if (from + E <= width) {
+            if constexpr (sizeof(T) == 2) {
+                const u32x4 r = *(const any_u32x4 *)(row + from);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) x[e] = widen(e % 2 ? r[e / 2] >> 16 : r[e / 2] & 0xffff);
-                } else {
-                    const float4 lo = *(const float4 *)(row + from), hi = *(const float4 *)(row + from + 4);
-                    x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
-                    x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
-                }
+                for (int e = 0; e < E; ++e) x[e] = widen(e % 2 ? r[e / 2] >> 16 : r[e / 2] & 0xffff);
             } else {
+                const f32x4 lo = *(const any_f32x4 *)(row + from), hi = *(const any_f32x4 *)(row + from + 4);
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = 0.0f;
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = lo[e];
+                    x[4 + e] = hi[e];
+                }
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = from + e * 64 < width ? (float)row[from + e * 64] : 0.0f;
+            for (int e = 0; e < E; ++e) x[e] = 0.0f;
+            if (from < width) {
+#pragma unroll
+                for (int e = 0; e < E - 1; ++e)
+                    if (from + e < width) x[e] = (float)row[from + e];
+            }
         }
     }
     template <typename T>
     __device__ __forceinline__ void store(T *row, int n, int width, const float (&x)[E]) const {
-        const int to = at(n, 0);
-        if constexpr (WIDE) {
-            if (to >= width) return;
+        const int to = at(n);
+        if (to + E <= width) {
             if constexpr (sizeof(T) == 2) {
-                *(u32x4 *)(row + to) = u32x4{narrow(x[0], x[1]), narrow(x[2], x[3]), narrow(x[4], x[5]), narrow(x[6], x[7])};
+                *(any_u32x4 *)(row + to) = u32x4{narrow(x[0], x[1]), narrow(x[2], x[3]), narrow(x[4], x[5]), narrow(x[6], x[7])};
             } else {
-                *(float4 *)(row + to) = make_float4(x[0], x[1], x[2], x[3]);
-                *(float4 *)(row + to + 4) = make_float4(x[4], x[5], x[6], x[7]);
+                *(any_f32x4 *)(row + to) = f32x4{x[0], x[1], x[2], x[3]};
+                *(any_f32x4 *)(row + to + 4) = f32x4{x[4], x[5], x[6], x[7]};
             }
-        } else {
+        } else if (to < width) {
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (to + e * 64 < width) row[to + e * 64] = (T)x[e];
+            for (int e = 0; e < E - 1; ++e)
+                if (to + e < width) row[to + e] = (T)x[e];
         }
     }
 };
@@ -183,12 +187,12 @@ __device__ __forceinline__ float scale_of(long long top, int code, double &inv) 
 
 // MODE: values, codes with a scale for a row, codes with a scale for a group.
 enum { kValues, kRowCodes, kGroupCodes };
-template <typename T, typename R, int TPR, int NV, bool WIDE, int MODE>
+template <typename T, typename R, int TPR, int NV, int MODE>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_fwd(NormArgs p) {
     constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
     __shared__ double part[TPR > 64 ? TPR / 64 : 1];
-    const Piece<TPR, NV, WIDE> own;
-    const int tid = threadIdx.x % TPR, lane = threadIdx.x & 63;
+    const Piece<TPR> own;
+    const int tid = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     if (row >= p.rows) return;  // whole waves: a row of several waves has the block to itself
     const int D = p.dim;
@@ -249,55 +253,37 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_fwd(NormArgs p) {
         if constexpr (MODE == kRowCodes) {
 #pragma unroll
             for (int e = 0; e < E; ++e) y[e] *= inv;
-        } else if constexpr (WIDE) {
+        } else {
             Top top;
 #pragma unroll
             for (int e = 0; e < E; ++e) top.add(y[e]);
             const float scale = scale_of(over_lanes(top.bits(), group / E), p.code, inv);
-            const int at = own.at(n, 0);
+            const int at = own.at(n);
             if (at < D && at % group == 0) p.scales[row * groups + at / group] = scale;
 #pragma unroll
             for (int e = 0; e < E; ++e) y[e] *= inv;
-        } else {
-            // a group is 32 lanes of an element, the wave's 64, or these of two elements
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                Top top[2];
-                top[0].add(y[e]);
-                if (group == 128) top[0].add(y[e + 1]);
-                else top[1].add(y[e + 1]);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (k == 0 || group != 128) {
-                        const float scale = scale_of(over_lanes(top[k].bits(), group == 32 ? 32 : 64), p.code, inv);
-                        const int at = own.at(n, e + k);
-                        if (lane % (group == 32 ? 32 : 64) == 0 && at < D) p.scales[row * groups + at / group] = scale;
-                    }
-                    y[e + k] *= inv;
-                }
-            }
         }
         uint32_t c[2];
         code8(y, p.code, c);
         uint8_t *const to = (uint8_t *)p.y + at0;
-        if constexpr (WIDE) {
-            const int at = own.at(n, 0);
-            if (at < D) *(u32x2 *)(to + at) = u32x2{c[0], c[1]};
-        } else {
+        const int at = own.at(n);
+        if (at + E <= D) {
+            *(any_u32x2 *)(to + at) = u32x2{c[0], c[1]};
+        } else if (at < D) {
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (own.at(n, e) < D) to[own.at(n, e)] = (uint8_t)(c[e / 4] >> (e % 4 * 8));
+            for (int e = 0; e < E - 1; ++e)
+                if (at + e < D) to[at + e] = (uint8_t)(c[e / 4] >> (e % 4 * 8));
         }
         __builtin_amdgcn_sched_barrier(0);  // a vector at a time: more rows fit a compute unit
     }
 }
 
 // Every row set (a block, or a wave of one) takes rows at a distance and keeps its sum of dweight.
-template <typename T, typename R, int TPR, int NV, bool WIDE>
+template <typename T, typename R, int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_bwd(NormBwdArgs p, int sets) {
     constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
     __shared__ double part[TPR > 64 ? TPR / 64 : 1];
-    const Piece<TPR, NV, WIDE> own;
+    const Piece<TPR> own;
     const int set = blockIdx.x * kRows + threadIdx.x / TPR, D = p.dim;
     if (set >= sets) return;
     float dw[NV][E] = {};
@@ -361,42 +347,37 @@ __global__ void __launch_bounds__(256) k_dweight(const float *part, float *out, 
     }
 }
 
-// WIDE: 8 codes a thread (a group is a multiple of 8), else one.
-template <bool WIDE>
+// 8 codes of a row a thread (a group is a multiple of 8); the row's last may be fewer.
 __global__ void __launch_bounds__(256) k_values(const uint8_t *codes, const float *scales, float *out, int64_t rows, int D, int group,
                                                 int code) {
-    constexpr int N = WIDE ? 8 : 1;
-    const uint32_t per_row = D / N, groups = group ? (D + group - 1) / group : 1;
+    const uint32_t per_row = (D + 7) / 8, groups = group ? (D + group - 1) / group : 1;
     const int64_t n = rows * per_row, stride = (int64_t)gridDim.x * 256;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += stride) {
-        const int64_t row = n <= 0xffffffff ? (uint32_t)e / per_row : e / per_row;
-        const int at = (int)(e - row * per_row) * N;
+    for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < n; v += stride) {
+        const int64_t row = n <= 0xffffffff ? (uint32_t)v / per_row : v / per_row;
+        const int at = (int)(v - row * per_row) * 8;
         const float scale = scales[row * groups + (group ? at / group : 0)];
-        if constexpr (WIDE) {
-            const u32x2 c = *(const u32x2 *)(codes + e * 8);
-            float v[8];
+        const uint8_t *const from = codes + row * D + at;
+        float *const to = out + row * D + at;
+        if (at + 8 <= D) {
+            const u32x2 c = *(const any_u32x2 *)from;
+            f32x4 x[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 if (code == 1) {
-                    v[4 * k] = __builtin_amdgcn_cvt_f32_fp8((int)c[k], 0);
-                    v[4 * k + 1] = __builtin_amdgcn_cvt_f32_fp8((int)c[k], 1);
-                    v[4 * k + 2] = __builtin_amdgcn_cvt_f32_fp8((int)c[k], 2);
-                    v[4 * k + 3] = __builtin_amdgcn_cvt_f32_fp8((int)c[k], 3);
+                    x[k] = f32x4{__builtin_amdgcn_cvt_f32_fp8((int)c[k], 0), __builtin_amdgcn_cvt_f32_fp8((int)c[k], 1),
+                                 __builtin_amdgcn_cvt_f32_fp8((int)c[k], 2), __builtin_amdgcn_cvt_f32_fp8((int)c[k], 3)};
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[4 * k + j] = (float)(int8_t)(c[k] >> (8 * j));
+                    for (int j = 0; j < 4; ++j) x[k][j] = (float)(int8_t)(c[k] >> (8 * j));
                 }
+                x[k] *= scale;
+                *(any_f32x4 *)(to + 4 * k) = x[k];
             }
-            float4 *const to = (float4 *)(out + e * 8);
-            to[0] = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
-            to[1] = make_float4(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale);
         } else {
-            out[e] = (code == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)codes[e], 0) : (float)(int8_t)codes[e]) * scale;
+            for (int e = 0; at + e < D; ++e) to[e] = (code == 1 ? __builtin_amdgcn_cvt_f32_fp8((int)from[e], 0) : (float)(int8_t)from[e]) * scale;
         }
     }
 }
-
-bool aligned_to(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 
 // Threads of a row: a wave up to 1024 elements, 256 up to 4096, 512 up to 8192, 1024 up to 65536.
 template <typename F>
@@ -417,36 +398,27 @@ void by_size(int D, F go) {
 
 template <typename T, typename R>
 void run_fwd(const NormArgs &a, hipStream_t s) {
-    const bool wide = a.dim % E == 0 && aligned_to(a.x, 16) && aligned_to(a.residual, 16) && aligned_to(a.added, 16) &&
-                      aligned_to(a.weight, 16) && aligned_to(a.y, a.code ? 8 : 16);
     by_size(a.dim, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, kThreads = TPR < 256 ? 256 : TPR;
         const int64_t blocks = (a.rows + kThreads / TPR - 1) / (kThreads / TPR);
-        const auto go = [&](auto mode) {
-            if (wide) k_fwd<T, R, TPR, NV, true, decltype(mode)::value><<<blocks, kThreads, 0, s>>>(a);
-            else k_fwd<T, R, TPR, NV, false, decltype(mode)::value><<<blocks, kThreads, 0, s>>>(a);
-        };
-        if (a.code == 0) go(std::integral_constant<int, kValues>());
-        else if (a.group == 0) go(std::integral_constant<int, kRowCodes>());
-        else go(std::integral_constant<int, kGroupCodes>());
+        if (a.code == 0) k_fwd<T, R, TPR, NV, kValues><<<blocks, kThreads, 0, s>>>(a);
+        else if (a.group == 0) k_fwd<T, R, TPR, NV, kRowCodes><<<blocks, kThreads, 0, s>>>(a);
+        else k_fwd<T, R, TPR, NV, kGroupCodes><<<blocks, kThreads, 0, s>>>(a);
     });
 }
 
 // Row sets of the backward: enough for the GPU, each with several rows where there are many.
 int row_sets(int64_t rows, int32_t dim) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(rows, dim <= 1024 ? 2048 : dim <= 8192 ? 512 : 256));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(rows, dim <= 1024 ? 2048 : 512));
 }
 
 template <typename T, typename R>
 void run_bwd(const NormBwdArgs &a, hipStream_t s) {
-    const bool wide = a.dim % E == 0 && aligned_to(a.s, 16) && aligned_to(a.dy, 16) && aligned_to(a.ds, 16) &&
-                      aligned_to(a.weight, 16) && aligned_to(a.dx, 16) && aligned_to(a.dres, 16);
     const int sets = row_sets(a.rows, a.dim);
     by_size(a.dim, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, kThreads = TPR < 256 ? 256 : TPR;
         const int blocks = (sets + kThreads / TPR - 1) / (kThreads / TPR);
-        if (wide) k_bwd<T, R, TPR, NV, true><<<blocks, kThreads, 0, s>>>(a, sets);
-        else k_bwd<T, R, TPR, NV, false><<<blocks, kThreads, 0, s>>>(a, sets);
+        k_bwd<T, R, TPR, NV><<<blocks, kThreads, 0, s>>>(a, sets);
     });
     k_dweight<<<(a.dim + 15) / 16, 256, 0, s>>>((const float *)a.ws, a.dweight, sets, a.dim);
 }
@@ -468,10 +440,8 @@ hipError_t launch_rmsnorm_bwd(const NormBwdArgs &a, int io, int res_io, hipStrea
 }
 hipError_t launch_q8_values(const void *codes, const float *scales, float *out, int64_t rows, int32_t dim, int32_t group,
                             int code, hipStream_t s) {
-    const bool wide = dim % 8 == 0 && aligned_to(codes, 8) && aligned_to(out, 16);
-    const int64_t blocks = std::min<int64_t>((rows * dim / (wide ? 8 : 1) + 255) / 256, 1 << 20);
-    if (wide) k_values<true><<<blocks, 256, 0, s>>>((const uint8_t *)codes, scales, out, rows, dim, group, code);
-    else k_values<false><<<blocks, 256, 0, s>>>((const uint8_t *)codes, scales, out, rows, dim, group, code);
+    const int64_t blocks = std::min<int64_t>((rows * ((dim + 7) / 8) + 255) / 256, 1 << 20);
+    k_values<<<blocks, 256, 0, s>>>((const uint8_t *)codes, scales, out, rows, dim, group, code);
     return hipGetLastError();
 }
 
