@@ -821,7 +821,7 @@ ssm_status ssm_linattn_step(float *h, const void *q_t, const void *k_t, const vo
  * forward wrote (x where it had no residual; then res_io is io), ds NULL = 0. dweight is summed in a
  * fixed order. workspace: ssm_rmsnorm_bwd_workspace bytes, 256-byte aligned.
  * Apart from residual_out, outputs must not overlap inputs or each other. Alignment: float32 arrays 4
- * bytes, the others one element. rows is at most 2^22, dim 1 to 65536. */
+ * bytes, the others one element. rows is below 2^31, dim 1 to 65536. */
 typedef enum { SSM_E4M3 = 1, SSM_INT8 = 2 } ssm_code;
 ssm_status ssm_rmsnorm_fwd(const void *x, const void *residual, const float *weight, double eps,
                            void *y, void *residual_out, float *rstd, int64_t rows, int32_t dim,

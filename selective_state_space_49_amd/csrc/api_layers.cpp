@@ -183,8 +183,8 @@ ssm_status ssm_linattn_step(float *h, const void *q_t, const void *k_t, const vo
 static ssm_status check_norm(int64_t rows, int32_t dim, ssm_dtype io, ssm_dtype res_io) {
     if (!valid_io(io) || !valid_io(res_io)) return fail(SSM_ERR_DTYPE, "io dtype %d or %d unknown", (int)io, (int)res_io);
     if (io == SSM_F32 && res_io != SSM_F32) return fail(SSM_ERR_DTYPE, "a float32 x takes a float32 residual");
-    if (rows < 0 || rows > ((int64_t)1 << 22) || dim < 1 || dim > 65536)
-        return fail(SSM_ERR_SHAPE, "rows must be in 0..2^22 and dim in 1..65536");
+    if (rows < 0 || rows > INT32_MAX || dim < 1 || dim > 65536)
+        return fail(SSM_ERR_SHAPE, "rows must be in 0..2^31 - 1 and dim in 1..65536");
     return SSM_OK;
 }
 static ssm_status check_group(int32_t group) {

@@ -6,8 +6,8 @@
 //     n = s r:  ds' = r (weight dy - n mean(weight dy n)) + ds,   dweight = sum over rows of dy n
 //
 // A row stays in registers between its sum and its output, so every array is read or written once:
-// bytes are the floor. A row of up to 1024 elements belongs to a wave, a longer one to a block of 256
-// to 1024 threads. The sum of squares is held in 64 bits (a conversion and a multiply-add an element:
+// bytes are the floor. A row of up to 1024 elements belongs to a wave or a part of one, a longer one to a
+// block of 256 to 1024 threads. The sum of squares is held in 64 bits (a conversion and a multiply-add an element:
 // the 64-bit rate of the vector units is that of 32 bits), so that r does not depend on the order,
 // and codes are computed in 64 bits from s on: a value next to the border of two codes takes the
 // right one.
@@ -100,7 +100,7 @@ template <typename T> __device__ __forceinline__ float stored(float x) {
 template <int TPR, typename V, typename F>
 __device__ __forceinline__ V over_row(V x, V *part, F join) {
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) x = join(x, __shfl_xor(x, d));
+    for (int d = 1; d < (TPR < 64 ? TPR : 64); d *= 2) x = join(x, __shfl_xor(x, d));
     if constexpr (TPR > 64) {
         __syncthreads();
         if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = x;
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_fwd(NormArgs p) {
     const Piece<TPR> own;
     const int tid = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
-    if (row >= p.rows) return;  // whole waves: a row of several waves has the block to itself
+    if (row >= p.rows) return;  // whole rows: one of several waves has the block to itself
     const int D = p.dim;
     const int64_t at0 = row * D;
     float s[NV][E];
@@ -278,39 +278,50 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_fwd(NormArgs p) {
     }
 }
 
-// Every row set (a block, or a wave of one) takes rows at a distance and keeps its sum of dweight.
+// Every row set (a block, or a wave of one) takes rows at a distance and keeps its sum of dweight; a wave that
+// has several rows at a time adds theirs at the end. A row of more than 16384 elements is read a second time, from
+// the cache where it fits, after its sum: it does not fit the registers beside dweight's (2048 rows of 9216 in
+// 35 us; 1024 of 20000 in 129, held in registers and memory behind them 177).
 template <typename T, typename R, int TPR, int NV>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_bwd(NormBwdArgs p, int sets) {
     constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
     __shared__ double part[TPR > 64 ? TPR / 64 : 1];
-    const Piece<TPR> own;
-    const int set = blockIdx.x * kRows + threadIdx.x / TPR, D = p.dim;
+    Piece<TPR> own;
+    constexpr int kOfSet = TPR < 64 ? 64 / TPR : 1, KEPT = NV <= 2 ? NV : 1;
+    const int line = blockIdx.x * kRows + threadIdx.x / TPR, set = line / kOfSet, D = p.dim;
     if (set >= sets) return;
     float dw[NV][E] = {};
-    for (int64_t row = set; row < p.rows; row += sets) {
+    for (int64_t row = line; row < p.rows; row += (int64_t)sets * kOfSet) {
         const int64_t at0 = row * D;
         const float r = p.rstd[row];
-        float n[NV][E], wd[NV][E];
-        double sum = 0.0;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
+        const float *weight = p.weight;
+        if constexpr (TPR == 1024) asm volatile("" : "+s"(weight), "+v"(own.first));  // for each row anew: no registers are left (9216: 35 us, 57)
+        float n[KEPT][E], wd[KEPT][E];
+        const auto load = [&](int k, float (&n)[E], float (&wd)[E], bool first) {
             float w[E];
-            own.load((const R *)p.s + at0, k, D, n[k]);
-            own.load((const T *)p.dy + at0, k, D, wd[k]);
-            own.load(p.weight, k, D, w);
+            own.load((const R *)p.s + at0, k, D, n);
+            own.load((const T *)p.dy + at0, k, D, wd);
+            own.load(weight, k, D, w);
             float t = 0.0f;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                n[k][e] *= r;
-                dw[k][e] += wd[k][e] * n[k][e];
-                wd[k][e] *= w[e];
-                t += wd[k][e] * n[k][e];
+                n[e] *= r;
+                if (first) dw[k][e] += wd[e] * n[e];
+                wd[e] *= w[e];
+                t += wd[e] * n[e];
             }
-            sum += t;
+            return t;
+        };
+        double sum = 0.0;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            sum += load(k, n[k % KEPT], wd[k % KEPT], true);
+            if (KEPT < NV) __builtin_amdgcn_sched_barrier(0);
         }
         const float c = (float)(row_sum<TPR>(sum, part) / D);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
+            if constexpr (KEPT < NV) load(k, n[0], wd[0], false);
             float g[E];
             if (p.ds) {
                 own.load((const R *)p.ds + at0, k, D, g);
@@ -319,10 +330,20 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_bwd(NormBwdArgs p, in
                 for (int e = 0; e < E; ++e) g[e] = 0.0f;
             }
 #pragma unroll
-            for (int e = 0; e < E; ++e) g[e] += (wd[k][e] - n[k][e] * c) * r;
+            for (int e = 0; e < E; ++e) g[e] += (wd[k % KEPT][e] - n[k % KEPT][e] * c) * r;
             own.store((T *)p.dx + at0, k, D, g);
             if (p.dres) own.store((R *)p.dres + at0, k, D, g);
+            if (KEPT < NV) __builtin_amdgcn_sched_barrier(0);
         }
+    }
+    if constexpr (TPR < 64) {
+#pragma unroll
+        for (int d = TPR; d < 64; d *= 2)
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int e = 0; e < E; ++e) dw[k][e] += __shfl_xor(dw[k][e], d);
+        if ((threadIdx.x & 63) >= TPR) return;
     }
     float *const to = (float *)p.ws + (int64_t)set * D;
 #pragma unroll
@@ -379,14 +400,20 @@ __global__ void __launch_bounds__(256) k_values(const uint8_t *codes, const floa
     }
 }
 
-// Threads of a row: a wave up to 1024 elements, 256 up to 4096, 512 up to 8192, 1024 up to 65536.
+// Threads of a row: 16 up to 128 elements (heads), 32 up to 256, a wave up to 1024, 256 up to 4096, 512 up to 8192,
+// 1024 up to 65536. 524288 rows of 128 in bf16: forward 53 us, backward 124; with a wave for a row 170 and 339.
+constexpr int kNarrow = 128, kHalf = 256;
 template <typename F>
 void by_size(int D, F go) {
+    typedef std::integral_constant<int, 16> N;
+    typedef std::integral_constant<int, 32> H;
     typedef std::integral_constant<int, 64> W;
     typedef std::integral_constant<int, 256> B;
     typedef std::integral_constant<int, 512> M;
     typedef std::integral_constant<int, 1024> L;
-    if (D <= 512) go(W(), std::integral_constant<int, 1>());
+    if (D <= kNarrow) go(N(), std::integral_constant<int, 1>());
+    else if (D <= kHalf) go(H(), std::integral_constant<int, 1>());
+    else if (D <= 512) go(W(), std::integral_constant<int, 1>());
     else if (D <= 1024) go(W(), std::integral_constant<int, 2>());
     else if (D <= 2048) go(B(), std::integral_constant<int, 1>());
     else if (D <= 4096) go(B(), std::integral_constant<int, 2>());
@@ -400,16 +427,32 @@ template <typename T, typename R>
 void run_fwd(const NormArgs &a, hipStream_t s) {
     by_size(a.dim, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, kThreads = TPR < 256 ? 256 : TPR;
-        const int64_t blocks = (a.rows + kThreads / TPR - 1) / (kThreads / TPR);
-        if (a.code == 0) k_fwd<T, R, TPR, NV, kValues><<<blocks, kThreads, 0, s>>>(a);
-        else if (a.group == 0) k_fwd<T, R, TPR, NV, kRowCodes><<<blocks, kThreads, 0, s>>>(a);
-        else k_fwd<T, R, TPR, NV, kGroupCodes><<<blocks, kThreads, 0, s>>>(a);
+        const int groups = a.group ? (a.dim + a.group - 1) / a.group : 1;
+        // A launch has fewer than 2^32 threads.
+        const int64_t most = (int64_t)(1 << 21) * (kThreads / TPR);
+        for (int64_t first = 0; first < a.rows; first += most) {
+            NormArgs p = a;
+            p.rows = std::min(a.rows - first, most);
+            p.x = (const T *)a.x + first * a.dim;
+            if (a.residual) {
+                p.residual = (const R *)a.residual + first * a.dim;
+                p.added = (R *)a.added + first * a.dim;
+            }
+            p.y = (char *)a.y + first * a.dim * (a.code ? 1 : (int)sizeof(T));
+            if (a.rstd) p.rstd = a.rstd + first;
+            if (a.scales) p.scales = a.scales + first * groups;
+            const int64_t blocks = (p.rows + kThreads / TPR - 1) / (kThreads / TPR);
+            if (a.code == 0) k_fwd<T, R, TPR, NV, kValues><<<blocks, kThreads, 0, s>>>(p);
+            else if (a.group == 0) k_fwd<T, R, TPR, NV, kRowCodes><<<blocks, kThreads, 0, s>>>(p);
+            else k_fwd<T, R, TPR, NV, kGroupCodes><<<blocks, kThreads, 0, s>>>(p);
+        }
     });
 }
 
 // Row sets of the backward: enough for the GPU, each with several rows where there are many.
 int row_sets(int64_t rows, int32_t dim) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(rows, dim <= 1024 ? 2048 : 512));
+    const int64_t at_once = dim <= kNarrow ? 4 : dim <= kHalf ? 2 : 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>((rows + at_once - 1) / at_once, dim <= 1024 ? 2048 : 512));
 }
 
 template <typename T, typename R>
@@ -417,7 +460,8 @@ void run_bwd(const NormBwdArgs &a, hipStream_t s) {
     const int sets = row_sets(a.rows, a.dim);
     by_size(a.dim, [&](auto tpr, auto nv) {
         constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value, kThreads = TPR < 256 ? 256 : TPR;
-        const int blocks = (sets + kThreads / TPR - 1) / (kThreads / TPR);
+        constexpr int kSets = TPR < 256 ? 256 / (TPR < 64 ? 64 : TPR) : 1;
+        const int blocks = (sets + kSets - 1) / kSets;
         k_bwd<T, R, TPR, NV><<<blocks, kThreads, 0, s>>>(a, sets);
     });
     k_dweight<<<(a.dim + 15) / 16, 256, 0, s>>>((const float *)a.ws, a.dweight, sets, a.dim);

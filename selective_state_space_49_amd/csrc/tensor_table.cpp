@@ -656,6 +656,41 @@ PyObject *rmsnorm_bwd(PyObject *, PyObject *const *args, Py_ssize_t n) {
     });
 }
 
+// q8_values(entry, stream, codes, scales, group, out): out.
+PyObject *q8_values(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 6) return PyErr_Format(PyExc_TypeError, "6 arguments expected, got %zd", n);
+    return no_exceptions([&]() -> PyObject * {
+        const auto entry = (decltype(&ssm_q8_values))PyLong_AsVoidPtr(args[0]);
+        void *const stream = PyLong_AsVoidPtr(args[1]);
+        const long group = PyLong_AsLong(args[4]);
+        if (PyErr_Occurred()) return nullptr;
+        if (dims_of(args[2]) < 1 || group < 0 || group > INT32_MAX) Py_RETURN_NONE;
+        const at::Tensor &codes = THPVariable_Unpack(args[2]);
+        const at::ScalarType type = codes.scalar_type();
+        const at::IntArrayRef all = codes.sizes();
+        if (!codes.is_cuda() || !codes.is_contiguous() || (type != at::kFloat8_e4m3fn && type != at::kChar)) Py_RETURN_NONE;
+        const int64_t dim = all.back(), rows = dim > 0 ? codes.numel() / dim : 0;
+        if (dim < 1 || dim > INT32_MAX) Py_RETURN_NONE;
+        std::vector<int64_t> scale(all.begin(), all.end());
+        scale.back() = group ? (dim + group - 1) / group : 1;
+        const int device = (int)codes.get_device();
+        bool ok = true;
+        const float *const scales = (const float *)address(args[3], at::kFloat, scale, device, &ok);
+        float *given = (float *)optional(args[5], at::kFloat, all, device, &ok);
+        if (!ok) Py_RETURN_NONE;
+        const at::Tensor out = given ? THPVariable_Unpack(args[5]) : at::empty(all, codes.options().dtype(at::kFloat));
+        const c10::DeviceGuard on(codes.device());
+        ssm_status st;
+        Py_BEGIN_ALLOW_THREADS
+        st = entry(codes.data_ptr(), scales, type == at::kChar ? SSM_INT8 : SSM_E4M3, (int32_t)group, (float *)out.data_ptr(), rows,
+                   (int32_t)dim, stream);
+        Py_END_ALLOW_THREADS
+        if (st != SSM_OK) return PyLong_FromLong(st);
+        written(args[5]);
+        return wrap(out);
+    });
+}
+
 // A setting of the sampling: a tensor with a value for every row, or a number for all.
 template <typename T>
 const T *setting(Call &c, PyObject *o, at::ScalarType type, int64_t rows, double *all) {
@@ -718,6 +753,7 @@ PyMethodDef methods[] = {
     {"rmsnorm_fwd", (PyCFunction)(void (*)(void))rmsnorm_fwd, METH_FASTCALL, "ssm_rmsnorm_fwd for tensors."},
     {"rmsnorm_fwd_q8", (PyCFunction)(void (*)(void))rmsnorm_fwd_q8, METH_FASTCALL, "ssm_rmsnorm_fwd_q8 for tensors."},
     {"rmsnorm_bwd", (PyCFunction)(void (*)(void))rmsnorm_bwd, METH_FASTCALL, "ssm_rmsnorm_bwd for tensors."},
+    {"q8_values", (PyCFunction)(void (*)(void))q8_values, METH_FASTCALL, "ssm_q8_values for tensors."},
     {"sample", (PyCFunction)(void (*)(void))sample, METH_FASTCALL, "ssm_sample for tensors."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_table", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

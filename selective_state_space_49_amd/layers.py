@@ -247,6 +247,10 @@ def ssm_q8_values(codes, scales, *, group=None, out=None):
         if len(fits) != 1:
             raise ValueError(f"{count} scales for {dim} values: give the group")
         group = fits[0]
+    if codes.is_cuda:
+        got = _table_module().q8_values(_entry("ssm_q8_values"), _stream(codes), codes, scales, group, out)
+        if got is not None:
+            return _made(got)
     shape = (*codes.shape[:-1], -(-dim // group) if group > 0 else 1)
     out = torch.empty(codes.shape, dtype=_f32, device=dev) if out is None else out
     _called(codes, load_library().ssm_q8_values, _need(codes, "codes", codes.shape, codes.dtype, dev),

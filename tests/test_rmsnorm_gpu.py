@@ -19,7 +19,7 @@ pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
 TYPES = [(F32, None), (F32, F32), (BF16, None), (BF16, BF16), (BF16, F32)]
 SIZES = [(1, 1), (1, 4096), (3, 7), (5, 16), (65, 100), (33, 512), (7, 1000), (4, 1024), (9, 2047), (3, 2048), (2, 5001), (2, 8192),
-         (2, 10000), (1, 16384), (1, 30001), (2, 65536), (700, 24)]
+         (2, 10000), (1, 16384), (1, 30001), (2, 65536), (700, 24), (129, 128), (70, 129), (37, 256), (8501, 40), (4200, 200)]
 EPS = 1e-5
 
 
