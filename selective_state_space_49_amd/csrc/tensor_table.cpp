@@ -17,10 +17,12 @@
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <torch/csrc/autograd/python_cpp_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <exception>
 #include <initializer_list>
 #include <vector>
@@ -740,6 +742,24 @@ PyObject *sample(PyObject *, PyObject *const *args, Py_ssize_t n) {
     });
 }
 
+// leaves_elsewhere(next_functions, stream_id): whether a leaf among the functions that a node's gradients go
+// to has its gradient gathered on another stream than this one.
+PyObject *leaves_elsewhere(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 2 || !PyTuple_Check(args[0])) return PyErr_Format(PyExc_TypeError, "a tuple and a stream's id expected");
+    return no_exceptions([&]() -> PyObject * {
+        const int64_t stream = PyLong_AsLongLong(args[1]);
+        if (PyErr_Occurred()) return nullptr;
+        for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(args[0]); ++i) {
+            PyObject *const edge = PyTuple_GET_ITEM(args[0], i);
+            PyObject *const to = PyTuple_Check(edge) && PyTuple_GET_SIZE(edge) > 0 ? PyTuple_GET_ITEM(edge, 0) : Py_None;
+            if (std::strcmp(Py_TYPE(to)->tp_name, "AccumulateGrad") != 0) continue;
+            const auto on = ((torch::autograd::THPCppFunction *)to)->cdata->stream();
+            if (on && on->id() != stream) Py_RETURN_TRUE;
+        }
+        Py_RETURN_FALSE;
+    });
+}
+
 PyMethodDef methods[] = {
     {"gated_fwd", (PyCFunction)(void (*)(void))gated_fwd, METH_FASTCALL, "ssm_gated_fwd for tensors."},
     {"gated_bwd", (PyCFunction)(void (*)(void))gated_bwd, METH_FASTCALL, "ssm_gated_bwd for tensors."},
@@ -754,6 +774,7 @@ PyMethodDef methods[] = {
     {"rmsnorm_fwd_q8", (PyCFunction)(void (*)(void))rmsnorm_fwd_q8, METH_FASTCALL, "ssm_rmsnorm_fwd_q8 for tensors."},
     {"rmsnorm_bwd", (PyCFunction)(void (*)(void))rmsnorm_bwd, METH_FASTCALL, "ssm_rmsnorm_bwd for tensors."},
     {"q8_values", (PyCFunction)(void (*)(void))q8_values, METH_FASTCALL, "ssm_q8_values for tensors."},
+    {"leaves_elsewhere", (PyCFunction)(void (*)(void))leaves_elsewhere, METH_FASTCALL, "Whether a leaf's gradient is gathered on another stream."},
     {"sample", (PyCFunction)(void (*)(void))sample, METH_FASTCALL, "ssm_sample for tensors."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_table", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

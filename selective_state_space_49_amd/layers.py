@@ -20,6 +20,16 @@ LINATTN_CHUNK = (32, 64)
 _CODES = {"e4m3": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
 
 
+def _refuse_leaves_elsewhere(ctx):
+    """A leaf's gradient is gathered on the stream of the oldest living graph that has it. In a capture
+    that graph's stream would be made to wait for the captured one, which ends the process: an error
+    instead, before the gradients leave."""
+    if torch.cuda.is_current_stream_capturing():
+        if _table_module().leaves_elsewhere(ctx.next_functions, torch.cuda.current_stream().stream_id):
+            raise RuntimeError("a backward pass cannot be captured while a graph that was built on another stream "
+                               "holds the same leaves: drop that graph's outputs first")
+
+
 # ------------------------------------------------------------------ linear attention
 def ssm_linattn_states_bytes(batch, L, heads, d_k, d_v, io=SSM_BF16) -> int:
     return int(load_library().ssm_linattn_states_bytes(batch, L, heads, d_k, d_v, io))
@@ -149,6 +159,7 @@ class _LinearAttention(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, do, dh_final):
+        _refuse_leaves_elsewhere(ctx)
         q, k, v, log_decay, states = ctx.saved_tensors
         do = torch.zeros_like(v) if do is None else do.to(v.dtype).contiguous()
         g = ssm_linattn_bwd(q, k, v, log_decay, states, do=do, scale=ctx.scale,
@@ -297,6 +308,7 @@ class _RmsNorm(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, ds=None):
+        _refuse_leaves_elsewhere(ctx)
         s, weight, rstd = ctx.saved_tensors
         dy = torch.zeros(s.shape, dtype=ctx.io, device=s.device) if dy is None else dy.to(ctx.io).contiguous()
         dx, dres, dweight = ssm_rmsnorm_bwd(dy, s, weight, rstd, ds=None if ds is None else ds.to(s.dtype).contiguous())
