@@ -417,7 +417,12 @@ __device__ __forceinline__ void state_add(f32x16 (&S)[TILES], const char *k_tile
 }
 
 // One sweep over a segment of a sequence's chunks for NW x 32 columns of one head's state. OUT: with
-// outputs, from the segment's entering state; else what the segment adds to the state, from 0.
+// outputs, from the segment's entering state; else what the segment adds to the state, from 0. A wave has all
+// of K for its 32 columns, so its state never leaves the accumulators; the block's waves share the chunk's q, k
+// and scores in LDS, and two blocks share a compute unit so that one's products run beside the other's decays
+// and roundings. Those vector instructions and the reads of LDS bound it (each busy half the time, the matrix
+// cores 28 %): 262144 tokens x 32 heads of 128 x 128 in bf16, 1.90 ms with outputs and 1.09 without, for 1.2 ms
+// of bytes; 2 x 4096 tokens 101 and 43 us.
 template <typename T, int KP, int NW, bool OUT, Access ACC>
 __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
     typedef Kind<T> N;
@@ -596,7 +601,8 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
     }
 }
 
-// What the segments add becomes what enters them (forwards), or what comes back to them (reverse).
+// What the segments add becomes what enters them (forwards), or what comes back to them (reverse). Bound by the
+// bytes of the segments' states: 64 heads of 128 x 128 in 7 segments, 59 MB, 11 us (5 TB/s).
 __global__ void __launch_bounds__(256) k_join(float *seg, const float *fac, const float *first, int64_t KV, int64_t heads,
                                               int nseg, bool reverse) {
     const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -634,7 +640,11 @@ struct BwdArgs {
 };
 
 // The gradients of a segment, from its end. VP / 32 waves hold dS by columns of V and make dv;
-// KP / 32 waves hold it transposed, by columns of K, and make dk and dq.
+// KP / 32 waves hold it transposed, by columns of K, and make dk and dq: each role's gradients need dS as an
+// operand in another order, and holding it twice costs a product where turning it around costs LDS that is
+// already full. A chunk's tiles take 145 KB of LDS with all heads of 128, so a block has the compute unit to
+// itself, and what bounds it are vector and LDS instructions between its barriers: 2 x 4096 tokens x 32 heads of
+// 128 x 128 in bf16, 247 us (740 MB with states, 3.0 TB/s).
 template <typename T, int KP, int VP, Access ACC>
 __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     typedef Kind<T> N;
@@ -1348,7 +1358,8 @@ hipError_t launch_linattn_bwd(const LinattnArgs &a, int io, hipStream_t s) {
 }
 hipError_t launch_linattn_step(const LinattnStepArgs &a, int io, hipStream_t s) {
     // Whole rows where there are heads enough for the GPU (13203 of 25 x 46 in bf16: 43 us, 64 in slices of
-    // 32 columns; 32768 of 128 x 128: 833 us, 903 in slices).
+    // 32 columns; 32768 of 128 x 128: 833 us, 903 in slices). With few heads slices of 32 columns (32 heads of
+    // 128 x 128: 4.7 us, 5.5 in slices of 16).
     const int64_t heads = a.layers * a.seqs * a.H;
     const int lanes = heads < 1024 || a.V <= 32 ? 8 : a.V <= 64 ? 16 : 32;
     const int64_t blocks = heads * ((a.V + 4 * lanes - 1) / (4 * lanes));
