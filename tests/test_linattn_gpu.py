@@ -291,3 +291,11 @@ def test_odd_widths(size, io):
     ssm.ssm_linattn_fwd(c["q"], c["k"], c["v"], c["g"], c["h0"], o=room[at:at + n].view(d["v"].shape))
     assert bitwise_equal(room[at:at + n].view(d["v"].shape).clone(), got["o"])
     assert bool((room[:at] == 7).all()) and bool((room[at + n:] == 7).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(1, 390, 100, 50, 9, 11), (3, 260, 45, 45, 8, 70), (2, 700, 150, 10, 40, 8)], ids=str)
+def test_segments_of_many_heads(size, io):
+    """Several segments, and more blocks than the GPU takes at once."""
+    say("linattn many heads", size, io)
+    against(make(*size, io=io, cuts=0.01, h0=True))
