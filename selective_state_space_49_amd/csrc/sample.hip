@@ -18,7 +18,7 @@
 //
 // What bounds it are the vector instructions of the last two passes, one block a row: 256 rows of 131072
 // float32 logits in 129 us (1.0 TB/s), one row of 32000 in
-// 32 us: extremes 5, histogram 4, its plan 2, masses 8, the list's end 10, the draw 2.
+// 28 us with a top_k of some tens: extremes 5, histogram 4, its plan 2, the list 4, its end 10, the draw 2.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -284,13 +284,16 @@ __device__ __forceinline__ void count_steps(const Logits<T> &l, int64_t from, in
 }
 
 // Where the kept ones end: the step of top_k's last (kBins: it keeps all that has mass) and the number
-// before that step; the steps in which top_p's last lies.
+// before that step; the steps in which top_p's last lies. Where top_k keeps so few that the list holds them all
+// with their last step (`whole`), they need no masses but in the list (one row of 32000 with 50 of them: 28
+// us, 32 without this).
 struct Plan {
     int end_k, p_from, p_to;
     u64 before_k;
+    bool whole;
 };
 __device__ __forceinline__ Plan plan_ends(Shared &sh, const Settings &s, const Steps &st) {
-    Plan pl{kBins, kBins, kBins, 0};
+    Plan pl{kBins, kBins, kBins, 0, false};
     const int tid = threadIdx.x, b = 2 * tid;
     const u64 b0 = sh.bins[b], b1 = sh.bins[b + 1];
     const uint32_t n0 = (uint32_t)b0, n1 = (uint32_t)b1;
@@ -302,14 +305,19 @@ __device__ __forceinline__ Plan plan_ends(Shared &sh, const Settings &s, const S
             const bool second = start + n0 < k;
             sh.few[0] = b + second;
             sh.few[1] = (uint32_t)(start + (second ? n0 : 0));
+            sh.few[3] = (uint32_t)(second ? upto : start + n0);
         }
         __syncthreads();
         if (sh.few[0] < kBins - 1) {
             pl.end_k = (int)sh.few[0];
             pl.before_k = sh.few[1];
+            pl.whole = sh.few[3] <= kThreads;
         }
     }
-    if (s.by_p) {
+    if (pl.whole) {
+        pl.p_from = 0;
+        pl.p_to = pl.end_k;
+    } else if (s.by_p) {
         // Masses estimated by the middle of a step's logits: a step is 1/61 of a unit at most, so they
         // are right to (1/61)^2 / 8 = 3e-5. By the step's middle they were off by half a percent, and
         // one heavy token by more than the mass of many steps of light ones.
@@ -354,6 +362,21 @@ __device__ __forceinline__ void weigh(const Logits<T> &l, int from, int to, cons
         }
         float at[E];
         bool some = false, listed = false;
+        if (pl.whole) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                at[e] = st.of(x[e]);
+                listed |= at[e] < past;
+            }
+            if (__ballot(listed) == 0) return;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (at[e] < past) {
+                    const uint32_t n = atomicAdd(count, 1u);
+                    if (n < kList) list[n] = place_of(key_of(x[e]), (uint32_t)(i + e));
+                }
+            return;
+        }
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             at[e] = st.of(x[e]);
@@ -545,7 +568,9 @@ __device__ __forceinline__ u64 resolve(const Logits<T> &l, const Masses &mass, c
             }
     }
     if (s.by_p) {
-        if (pl.end_k < kBins) {  // and what top_k keeps of that step
+        if (pl.whole) {
+            block_scan(m[0] + m[1], sh.part, all);
+        } else if (pl.end_k < kBins) {  // and what top_k keeps of that step
             block_scan((in_k[0] ? m[0] : 0) + (in_k[1] ? m[1] : 0), sh.part, whole);
             all += whole;
         }
@@ -659,7 +684,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs p, int shift) {
     bool slow = ends.high == kInfinity;
     if (!slow) {
         const Steps st(ends, s);
-        Plan pl{kBins, kBins, kBins, 0};
+        Plan pl{kBins, kBins, kBins, 0, false};
         if (s.by_k || s.by_p) {
             count_steps(l, 0, l.tiles, st, sh.bins);
             __syncthreads();
