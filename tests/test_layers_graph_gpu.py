@@ -364,3 +364,43 @@ def test_inference_tensors():
         linattn({k: t.cuda() for k, t in linattn_inputs(0, BF16).items()})
         sample({k: t.cuda() for k, t in sample_inputs(0, BF16).items()})
     torch.cuda.synchronize()
+
+
+def test_refusals():
+    """Strides, shapes and types that the kernels do not read are errors, and leave the outputs as they were."""
+    d = {k: t.cuda() for k, t in linattn_inputs(0, F32).items()}
+    o = torch.full_like(d["v"], 7.0)
+    args = lambda **c: [(d | c)[k] for k in ("q", "k", "v", "g", "h0")]  # noqa: E731
+    strided = torch.empty(1, 3, 700, 40, device="cuda").transpose(1, 2)
+    for bad in ({"v": strided}, {"q": d["q"].bfloat16()}, {"k": d["k"][:, :-1]}, {"g": d["g"].double()}, {"h0": d["h0"][..., :-1]},
+                {"g": d["g"][0]}, {"h0": d["h0"].cpu()}, {"v": d["v"].expand(2, -1, -1, -1)}):
+        with pytest.raises((TypeError, ValueError)):
+            ssm.ssm_linattn_fwd(*args(**bad), o=o)
+    with pytest.raises((TypeError, ValueError)):
+        ssm.ssm_linattn_fwd(*args(), o=o.bfloat16())
+    with pytest.raises(ssm.SsmError, match="overlap"):
+        ssm.ssm_linattn_fwd(*args(v=o), o=o)
+    ws = torch.empty(ssm.ssm_linattn_fwd_workspace(1, 700, 3, 1, 24, 40, ssm.SSM_F32) + 16, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ssm.SsmError, match="256"):
+        ssm.ssm_linattn_fwd(*args(), o=o, workspace=ws[16:])
+    n = {k: t.cuda() for k, t in norm_inputs(0, F32).items()}
+    y = torch.full_like(n["x"], 7.0)
+    for bad in ((n["x"].t(), n["w"]), (n["x"], n["w"][1:]), (n["x"], n["w"].bfloat16()), (n["x"], n["w"], n["r"][1:]),
+                (n["x"], n["w"], n["r"].bfloat16())):
+        with pytest.raises((TypeError, ValueError)):
+            ssm.ssm_rmsnorm_fwd(*bad, y=y)
+    with pytest.raises(ssm.SsmError, match="overlap"):
+        ssm.ssm_rmsnorm_fwd(y, n["w"], y=y)
+    with pytest.raises(ssm.SsmError, match="group"):
+        ssm.ssm_rmsnorm_fwd_q8(n["x"], n["w"], group=16)
+    s = {k: t.cuda() for k, t in sample_inputs(0, F32).items()}
+    tokens = torch.full((9,), 7, device="cuda")
+    for bad in ({"top_k": s["k"].long()}, {"temperature": s["t"].double()}, {"top_p": s["t"][1:]}, {"min_p": s["t"].cpu()}):
+        with pytest.raises((TypeError, ValueError)):
+            ssm.ssm_sample(s["logits"], s["u"], tokens=tokens, **bad)
+    with pytest.raises((TypeError, ValueError)):
+        ssm.ssm_sample(s["logits"].t(), s["u"], tokens=tokens)
+    with pytest.raises(ssm.SsmError, match="temperature"):
+        ssm.ssm_sample(s["logits"], s["u"], temperature=-1.0, tokens=tokens)
+    torch.cuda.synchronize()
+    assert bool((o == 7).all()) and bool((y == 7).all()) and bool((tokens == 7).all())
