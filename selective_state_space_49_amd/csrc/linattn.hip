@@ -1181,13 +1181,14 @@ Plan plan(int64_t B, int64_t L, int32_t H, int32_t V, int io, bool bwd) {
     // with 6, 517 with 7. Forwards, where blocks share compute units, 148 with 12 and 169 with 13; the most that
     // this rule loses there to the fewest segments that fill the GPU is 4 % (4096 x 300 heads: 658 with 5, 633 with 2).
     const int64_t blocks = std::max<int64_t>(B * H * p.slices, 1);
-    int64_t per = std::max<int64_t>(p.nchunk, 1), best = INT64_MAX;
-    for (int64_t n = 1; n <= most && (n == 1 || blocks * n <= 4 * want); ++n) {
-        const int64_t chunks = (p.nchunk + n - 1) / n, rounds = (blocks * n + want - 1) / want;
-        const int64_t cost = rounds * (chunks + 1) * (n > 1 ? 5 : 4);
+    int64_t per = std::max<int64_t>(p.nchunk, 1), best = ((blocks + want - 1) / want) * (per + 1) * 4;
+    for (int64_t rounds = 1; rounds <= 4; ++rounds) {
+        const int64_t n = std::min(rounds * want / blocks, most);  // the most segments that take so many rounds
+        if (n < 2) continue;
+        const int64_t chunks = (p.nchunk + n - 1) / n, cost = ((blocks * n + want - 1) / want) * (chunks + 1) * 5;
         if (cost < best) {
             best = cost;
-            per = std::max<int64_t>(chunks, 1);
+            per = chunks;
         }
     }
     p.per_seg = (int)per;
