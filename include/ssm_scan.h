@@ -753,9 +753,9 @@ ssm_status ssm_adamw_values(const int8_t *exp_avg, const uint8_t *exp_avg_sq,
  *                float32 (ssm_linattn_states_bytes bytes).
  * A head of more than 128 columns of v is two heads that read the same group.
  * Products are made a chunk at a time on the matrix cores and summed in float32; sums of g in
- * 64 bits. float32 inputs are multiplied in float32. Of bfloat16 ones, the chunk's scores and, where
- * it makes an output of bfloat16, the state enter a product rounded to bfloat16 (relative 2^-9 each,
- * like the output's own rounding); factors of a float32 result (states, dlog_decay) keep 24 bits.
+ * 64 bits. float32 inputs are multiplied in float32. Beside bfloat16 ones, the chunk's scores and, where
+ * it makes an output of bfloat16, the state enter a product with 17 bits (two bfloat16 parts), so that
+ * an output's error is its own rounding; factors of a float32 result (states, dlog_decay) keep 24 bits.
  * q, k, v (and d_o, states) must be finite: what is not, in a token, can reach the outputs of all
  * of its chunk, and with its state all that follows until a cut in a later chunk; never another
  * sequence or head (in the gradients, the heads of a group).

@@ -22,9 +22,10 @@
 // sweep (all of K for 32 columns of V) and is an operand from there: lane l holds column l % 32 and
 // of each 8 rows the 4 of its half, and the other operand is read in the same order of the
 // contraction ("quads": 4 consecutive elements at 8 a + 4 (l / 32)).
-// bfloat16: scores, and the state where it makes an output of bfloat16, are rounded to bfloat16
-// (2^-9 each, as the output is). What goes into a float32 result (states, dg) takes factors in three
-// bfloat16 parts, which hold 24 bits.
+// bfloat16: scores, and the state where it makes an output of bfloat16, enter a product as the sum of two
+// bfloat16 parts, which hold 17 bits: an output's error is its own rounding. (Of one part, 8 bits, the errors
+// were 2.35e-3 of norm where the rounding is 1.66e-3.) What goes into a float32 result (states, dg) takes
+// factors in three parts, which hold 24 bits.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -55,16 +56,17 @@ constexpr float kCut = -104.0f;  // exp of less is 0 in float32
 constexpr double kLog2e = 1.4426950408889634;
 
 // What depends on the inputs' type: tokens of a chunk (C), the contraction of a step (KS), a
-// fragment (this lane's elements of a step), and the parts that hold a float32 factor.
+// fragment (this lane's elements of a step), and the parts that hold a float32 factor of a float32 result and
+// of an output.
 template <typename T> struct Kind;
 template <> struct Kind<__bf16> {
-    static constexpr int C = 64, KS = 16, kParts = 3;
+    static constexpr int C = 64, KS = 16, kParts = 3, kOut = 2;
     typedef bf16x8 Frag;
     typedef f32x8 Wide;
     typedef u32x2 Quad;
 };
 template <> struct Kind<float> {
-    static constexpr int C = 32, KS = 8, kParts = 1;
+    static constexpr int C = 32, KS = 8, kParts = 1, kOut = 1;
     typedef f32x4 Frag;
     typedef f32x4 Wide;
     typedef f32x4 Quad;
@@ -79,10 +81,12 @@ __device__ __forceinline__ f32x16 mfma(f32x4 a, f32x4 b, f32x16 c) {
     return c;
 }
 
-// x rounded to the operand's type, and x as the sum of kParts of them.
-__device__ __forceinline__ bf16x8 rounded(f32x8 x) { return __builtin_convertvector(x, bf16x8); }
-__device__ __forceinline__ f32x4 rounded(f32x4 x) { return x; }
-// By truncation: 8 bits of 24 each, and nothing is left.
+// x as the sum of operands. Two of them are rounded: 2^-18 of x is left at most.
+__device__ __forceinline__ void split(f32x8 x, bf16x8 (&p)[2]) {
+    p[0] = __builtin_convertvector(x, bf16x8);
+    p[1] = __builtin_convertvector(x - __builtin_convertvector(p[0], f32x8), bf16x8);
+}
+// Three by truncation: 8 bits of 24 each, and nothing is left.
 __device__ __forceinline__ void split(f32x8 x, bf16x8 (&p)[3]) {
     u32x4 q[3];
 #pragma unroll
@@ -175,6 +179,35 @@ struct Tile {
     static __device__ __forceinline__ void put(char *t, int row, int quad, f32x4 x) {
         if constexpr (sizeof(T) == 2) *(bf16x4 *)(t + at(row, quad)) = __builtin_convertvector(x, bf16x4);
         else *(f32x4 *)(t + at(row, quad)) = x;
+    }
+};
+
+// Scores in kOut parts: rows i and columns j <= i of the chunk (BELOW), or rows j and columns i >= j. Of their
+// four tiles of 32 x 32 (bfloat16) one is empty, so the second parts of the row of tiles that has one tile lie
+// in it, and those of the other 32 rows behind the first parts: two blocks of the sweep still share a compute
+// unit, and the backward's tiles fit one.
+template <typename T, int C, bool BELOW>
+struct Scores {
+    typedef Tile<T, C, C> P;
+    static constexpr int kDown = 32 * P::kRow, kBytes = P::kBytes + (Kind<T>::kOut - 1) * kDown;
+    static __device__ __forceinline__ int at(int row, int quad) { return P::at(row, quad); }
+    static __device__ __forceinline__ void put(char *t, int row, int quad, f32x4 x) {
+        if constexpr (Kind<T>::kOut == 1) {
+            P::put(t, row, quad, x);
+        } else {
+            const int o = P::at(row, quad);
+            const bf16x4 first = __builtin_convertvector(x, bf16x4);
+            *(bf16x4 *)(t + o) = first;
+            const bool alone = BELOW == (row < 32);
+            *(bf16x4 *)(t + (alone ? o ^ 64 : o + (BELOW ? 1 : 2) * kDown)) =
+                __builtin_convertvector(x - __builtin_convertvector(first, f32x4), bf16x4);
+        }
+    }
+    // lanes: rows 32 tile + l % 32; contraction: step s. from: at(l % 32, half).
+    static __device__ __forceinline__ typename Kind<T>::Frag by_row(const char *t, int from, int tile, int s, int part) {
+        if (part == 0) return P::by_row(t + tile * kDown, from, s);
+        if (BELOW == (tile == 0)) return P::by_row(t + tile * kDown, from, s ^ 2);
+        return P::by_row(t + 2 * kDown, from, s);
     }
 };
 
@@ -430,7 +463,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
     constexpr int C = N::C, KS = N::KS, VT = 32 * NW, TT = C / 32, KT = KP / 32, THREADS = 64 * NW;
     typedef Tile<T, C, KP> TK;
     typedef Tile<T, C, VT> TV;
-    typedef Tile<T, C, C> TP;
+    typedef Scores<T, C, true> TP;
     __shared__ __attribute__((aligned(256))) char lds[(OUT ? 2 : 1) * TK::kBytes + (OUT ? 2 : 1) * TV::kBytes + (OUT ? TP::kBytes : 0)];
     __shared__ Decays<C> decays[2];
     char *const kt = lds, *const vt = lds + TK::kBytes, *const qt = vt + TV::kBytes, *const pt = qt + TK::kBytes, *const ot = pt + TP::kBytes;
@@ -528,7 +561,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
             load_g(it + 2);
         }
         const int kcol = TK::column_base(lane), krow = TK::at(l31, half), prow = TP::at(l31, half);
-        constexpr int kDown = 32 * TK::kBytes / C, pDown = 32 * TP::kBytes / C;  // 32 rows further
+        constexpr int kDown = 32 * TK::kBytes / C;  // 32 rows further
         if (OUT) {
             // scores q k^T e^{G_i - G_j}, lanes i, in quads of j
             for (int t = wave; t < TT * (TT + 1) / 2; t += NW) {
@@ -566,9 +599,15 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int s = 0; s < 32 / KS; ++s) {
-                    const Frag a = rounded(rows_of<T>(S[t], s));
+                    Frag a[N::kOut];
+                    split(rows_of<T>(S[t], s), a);
+                    Frag f[TT];
 #pragma unroll
-                    for (int i = 0; i < TT; ++i) o[i] = mfma(a, TK::by_row(qt + i * kDown, krow, t * (32 / KS) + s), o[i]);
+                    for (int i = 0; i < TT; ++i) f[i] = TK::by_row(qt + i * kDown, krow, t * (32 / KS) + s);
+#pragma unroll
+                    for (int e = 0; e < N::kOut; ++e)
+#pragma unroll
+                        for (int i = 0; i < TT; ++i) o[i] = mfma(a[e], f[i], o[i]);
                     if (s % 2) fence();
                 }
 #pragma unroll
@@ -576,8 +615,15 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
                 const float w = dec.start[i * 32 + l31] * p.scale;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[i][r] = w == 0.0f ? 0.0f : o[i][r] * w;
+            }
 #pragma unroll
-                for (int s = 0; s < (i + 1) * (32 / KS); ++s) o[i] = mfma(v[s], TP::by_row(pt + i * pDown, prow, s), o[i]);
+            for (int s = 0; s < C / KS; ++s)
+#pragma unroll
+                for (int e = 0; e < N::kOut; ++e)
+#pragma unroll
+                    for (int i = s / (32 / KS); i < TT; ++i) o[i] = mfma(v[s], TP::by_row(pt, prow, i, s, e), o[i]);
+#pragma unroll
+            for (int i = 0; i < TT; ++i) {
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
                     TV::put(ot, i * 32 + l31, wave * 8 + 2 * a + half, f32x4{o[i][4 * a], o[i][4 * a + 1], o[i][4 * a + 2], o[i][4 * a + 3]});
@@ -653,14 +699,15 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     constexpr int kMost = KT > VW ? KT : VW;
     typedef Tile<T, C, KP> TK;
     typedef Tile<T, C, VP> TV;
-    typedef Tile<T, C, C> TP;
+    typedef Scores<T, C, true> TP;   // rows i
+    typedef Scores<T, C, false> TQ;  // rows j
     typedef Tile<float, C, C> TM;
-    __shared__ __attribute__((aligned(256))) char lds[3 * TK::kBytes + 3 * TV::kBytes + 3 * TP::kBytes + TM::kBytes];
+    __shared__ __attribute__((aligned(256))) char lds[3 * TK::kBytes + 3 * TV::kBytes + TP::kBytes + 2 * TQ::kBytes + TM::kBytes];
     __shared__ Decays<C> decays[2];
     __shared__ float backs[2][C];         // scale e^{G_i}
     __shared__ float came[KT][C], left[KT][C], through[KT];
     char *const qt = lds, *const kt = qt + TK::kBytes, *const vt = kt + TK::kBytes, *const dt = vt + TV::kBytes;
-    char *const at = dt + TV::kBytes, *const bt = at + TP::kBytes, *const bn = bt + TP::kBytes, *const mt = bn + TP::kBytes;
+    char *const at = dt + TV::kBytes, *const bt = at + TQ::kBytes, *const bn = bt + TQ::kBytes, *const mt = bn + TP::kBytes;
     char *const ov = mt + TM::kBytes, *const oq = ov + TV::kBytes;  // dv and dq on their way out
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -756,7 +803,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
         dr.store(dt, tid, p.V);
         __syncthreads();
         if (c + 1 < c1) put_outputs(c + 1);
-        constexpr int kDown = 32 * TK::kBytes / C, vDown = 32 * TV::kBytes / C, pDown = 32 * TP::kBytes / C;  // 32 rows further
+        constexpr int kDown = 32 * TK::kBytes / C, vDown = 32 * TV::kBytes / C;  // 32 rows further
         const int krow = TK::at(l31, half), vrow = TV::at(l31, half), prow = TP::at(l31, half);
         // The state that entered this chunk, lanes k, in quads of v; half of V at a time.
         constexpr int kIn = VW * 2;
@@ -830,8 +877,8 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                         y[e] = dov[4 * a + e] * w;
                         m[e] = j < i0 + e ? x[e] * dov[4 * a + e] : 0.0f;
                     }
-                    TP::put(at, j, i0 / 4, x);
-                    TP::put(bt, j, i0 / 4, y);
+                    TQ::put(at, j, i0 / 4, x);
+                    TQ::put(bt, j, i0 / 4, y);
                     TM::put(mt, j, i0 / 4, m);
                     fence();
                 }
@@ -850,9 +897,14 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
             for (int t = 0; t < KT; ++t)
 #pragma unroll
                 for (int s = 0; s < 32 / KS; ++s) {
-                    const Frag a = rounded(rows_of<T>(SV[t], s));
+                    Frag a[N::kOut];
+                    split(rows_of<T>(SV[t], s), a);
 #pragma unroll
-                    for (int j = 0; j < TT; ++j) acc[j] = mfma(a, TK::by_row(kt + j * kDown, krow, t * (32 / KS) + s), acc[j]);
+                    for (int j = 0; j < TT; ++j) {
+                        const Frag f = TK::by_row(kt + j * kDown, krow, t * (32 / KS) + s);
+#pragma unroll
+                        for (int e = 0; e < N::kOut; ++e) acc[j] = mfma(a[e], f, acc[j]);
+                    }
                     if (s % 2) fence();
                 }
             Frag d[C / KS];
@@ -864,7 +916,9 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[j][r] = w == 0.0f ? 0.0f : acc[j][r] * w;
 #pragma unroll
-                for (int s = j * (32 / KS); s < C / KS; ++s) acc[j] = mfma(d[s], TP::by_row(at + j * pDown, prow, s), acc[j]);
+                for (int s = j * (32 / KS); s < C / KS; ++s)
+#pragma unroll
+                    for (int e = 0; e < N::kOut; ++e) acc[j] = mfma(d[s], TQ::by_row(at, prow, j, s, e), acc[j]);
 #pragma unroll
                 for (int a = 0; a < 4; ++a)
                     TV::put(ov, j * 32 + l31, part * 8 + 2 * a + half, f32x4{acc[j][4 * a], acc[j][4 * a + 1], acc[j][4 * a + 2], acc[j][4 * a + 3]});
@@ -990,7 +1044,9 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                 for (int s = 0; s < C / KS; ++s) {
                     const Frag f = TK::by_column(qt, column, 0, s);
 #pragma unroll
-                    for (int j = 0; j <= s / (32 / KS); ++j) acc[j] = mfma(f, TP::by_row(bt + j * pDown, prow, s), acc[j]);
+                    for (int j = 0; j <= s / (32 / KS); ++j)
+#pragma unroll
+                        for (int e = 0; e < N::kOut; ++e) acc[j] = mfma(f, TQ::by_row(bt, prow, j, s, e), acc[j]);
                 }
                 put(acc, p.dk);
             }
@@ -1000,7 +1056,9 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
             for (int s = 0; s < C / KS; ++s) {
                 const Frag f = TK::by_column(kt, column, 0, s);
 #pragma unroll
-                for (int j = s / (32 / KS); j < TT; ++j) aq[j] = mfma(f, TP::by_row(bn + j * pDown, prow, s), aq[j]);
+                for (int j = s / (32 / KS); j < TT; ++j)
+#pragma unroll
+                    for (int e = 0; e < N::kOut; ++e) aq[j] = mfma(f, TP::by_row(bn, prow, j, s, e), aq[j]);
             }
             if (shared) {
                 put(aq, p.dq);

@@ -1,0 +1,42 @@
+"""Outputs of bfloat16 linear attention entry by entry.
+
+An entry is a sum of products; T is the sum of their absolute values (the same forms of |q|, |k|, |v| in 64
+bits). What enters a product beside the inputs, which are exact, has two bfloat16 parts: off by 2^-18 of itself,
+in two products one after the other 2^-17. Sums in float32: a term passes at most 128 additions of a
+contraction and 64 of a chunk or of the state, and a decay for every chunk, 200 x 2^-24 = 2^-16.4; its decay's
+exponent of up to 32 is rounded to float32, 2^-20. Together below 2^-15.5 T. Then the entry is rounded, 2^-8
+of it."""
+import pytest
+import torch
+
+from tests import layers_ref as ref
+from tests.gpu_util import say
+from tests.test_linattn_gpu import make, run
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+def inputs(size, seed):
+    """Two columns of q, k, v and do are not 0, so that T is not much more than the entry."""
+    d = make(*size, io="bf16", seed=seed)
+    for k, n in (("q", size[4]), ("k", size[4]), ("v", size[5]), ("do", size[5])):
+        keep = torch.zeros(n, dtype=torch.bool)
+        keep[[n // 3, n - 1]] = True
+        d[k] = torch.where(keep, d[k], torch.zeros((), dtype=BF16))
+    return d
+
+
+@pytest.mark.parametrize("size", [(1, 64, 2, 2, 128, 128), (1, 700, 2, 1, 128, 128), (2, 300, 2, 2, 64, 64), (1, 200, 2, 1, 40, 72),
+                                  (1, 130, 2, 2, 5, 6)], ids=str)
+def test_entries(size):
+    for seed in (0, 1):
+        say("linattn precision", size, seed)
+        d = inputs(size, seed)
+        got = run(d)
+        want = ref.linattn(d["q"], d["k"], d["v"], d["g"], None, None, d["do"])
+        terms = ref.linattn(d["q"].abs(), d["k"].abs(), d["v"].abs(), d["g"], None, None, d["do"].abs())
+        for name in ("o", "dq", "dk", "dv"):
+            err = (got[name].double().cpu() - want[name]).abs()
+            most = 2.0 ** -8 * want[name].abs() + 2.0 ** -15.5 * terms[name]
+            assert bool((err <= most).all()), (name, float((err - most).max()), int((err > most).sum()))
