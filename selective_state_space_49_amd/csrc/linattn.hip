@@ -342,6 +342,13 @@ __device__ __forceinline__ double lane_of(double x, int lane) {
     return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(x), lane), __builtin_amdgcn_readlane(__double2loint(x), lane));
 }
 
+// 2^x to float32's last place: the raw instruction takes a float32 x, whose whole part would cost the
+// fraction its bits, and gives no denormals.
+__device__ __forceinline__ float exp2_of(double x) {
+    const double n = __builtin_rint(x);
+    return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)fmin(fmax(n, -1000.0), 1000.0));
+}
+
 // The decays of a chunk, made by one wave: G in units of log 2, document numbers, and the decays
 // from the start to a token, from a token to the end, and over all of it.
 template <int C>
@@ -366,9 +373,9 @@ struct Decays {
         if (lane < C) {
             G[lane] = sum;
             doc[lane] = __popcll(upto);
-            start[lane] = upto ? 0.0f : __builtin_amdgcn_exp2f((float)sum);
-            end[lane] = upto == cuts ? __builtin_amdgcn_exp2f((float)(all - sum)) : 0.0f;
-            if (lane == 0) whole = cuts ? 0.0f : __builtin_amdgcn_exp2f((float)all);
+            start[lane] = upto ? 0.0f : exp2_of(sum);
+            end[lane] = upto == cuts ? exp2_of(all - sum) : 0.0f;
+            if (lane == 0) whole = cuts ? 0.0f : exp2_of(all);
         }
     }
     // the decay from token j to token i, 0 for j > i and across a cut
@@ -643,7 +650,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
     } else {
         const int64_t at = bh * nseg_all + seg;
         state_store<KT>(S, p.seg_out + at * KV, p.K, p.V, vcol, half);
-        if (threadIdx.x == 0 && slice == 0) p.seg_fac[at] = cut ? 0.0f : __builtin_amdgcn_exp2f((float)decayed);
+        if (threadIdx.x == 0 && slice == 0) p.seg_fac[at] = cut ? 0.0f : exp2_of(decayed);
     }
 }
 
@@ -1167,7 +1174,7 @@ __global__ void __launch_bounds__(256) k_step(LinattnStepArgs p) {
     const int h = (int)(nh % p.H), hk = h / (p.H / p.Hk);
     const int v = slice * 4 * LANES + threadIdx.x % LANES * 4, r0 = threadIdx.x / LANES, live = min(max(p.V - v, 0), 4);
     const float g = p.g[(p.per_token ? n : n / p.seqs) * p.H + h];
-    const float a = g < kCut ? 0.0f : __expf(g);
+    const float a = g < kCut ? 0.0f : exp2_of((double)g * kLog2e);
     const T *const q = (const T *)p.q + (n * p.Hk + hk) * p.K, *const k = (const T *)p.k + (n * p.Hk + hk) * p.K;
     f32x4 x = {0, 0, 0, 0}, o = {0, 0, 0, 0};
 #pragma unroll

@@ -1,4 +1,4 @@
-"""Outputs of bfloat16 linear attention entry by entry.
+"""Outputs of bfloat16 linear attention entry by entry, and the token's decay.
 
 An entry is a sum of products; T is the sum of their absolute values (the same forms of |q|, |k|, |v| in 64
 bits). What enters a product beside the inputs, which are exact, has two bfloat16 parts: off by 2^-18 of itself,
@@ -9,6 +9,7 @@ of it."""
 import pytest
 import torch
 
+import selective_state_space_49_amd as ssm
 from tests import layers_ref as ref
 from tests.gpu_util import say
 from tests.test_linattn_gpu import make, run
@@ -40,3 +41,17 @@ def test_entries(size):
             err = (got[name].double().cpu() - want[name]).abs()
             most = 2.0 ** -8 * want[name].abs() + 2.0 ** -15.5 * terms[name]
             assert bool((err <= most).all()), (name, float((err - most).max()), int((err > most).sum()))
+
+
+@pytest.mark.parametrize("io", [torch.float32, BF16])
+def test_the_token_keeps_its_decay(io):
+    """A state that a strong decay brings down keeps float32's bits: exp to its last place or two, the product, an
+    added 0."""
+    g = -torch.linspace(1.0, 87.0, 64)
+    h = (1 + torch.rand(1, 1, 64, 4, 8, generator=torch.Generator().manual_seed(1))) * 1e30
+    want = h.double() * torch.exp(g.double())[:, None, None]
+    z = lambda *s: torch.zeros(*s, dtype=io, device="cuda")  # noqa: E731
+    got = h.cuda()
+    ssm.ssm_linattn_step(got, z(1, 1, 64, 4), z(1, 1, 64, 4), z(1, 1, 64, 8), g[None].cuda())
+    err = ((got.double().cpu() - want) / want).abs().amax((0, 1, 3, 4))
+    assert float(err.max()) <= 4 * 2.0 ** -24, err * 2.0 ** 24
