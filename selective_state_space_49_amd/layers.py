@@ -20,6 +20,13 @@ LINATTN_CHUNK = (32, 64)
 _CODES = {"e4m3": (1, torch.float8_e4m3fn), "int8": (2, torch.int8)}
 
 
+def _int32(value, name):
+    """A size that the library takes in 32 bits: ctypes would cut off what is above them."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {value}")
+    return value
+
+
 def _refuse_leaves_elsewhere(ctx):
     """A leaf's gradient is gathered on the stream of the oldest living graph that has it. In a capture
     that graph's stream would be made to wait for the captured one, which ends the process: an error
@@ -31,16 +38,20 @@ def _refuse_leaves_elsewhere(ctx):
 
 
 # ------------------------------------------------------------------ linear attention
+def _sizes(*sizes):
+    return [_int32(n, "heads, groups, d_k and d_v") for n in sizes]
+
+
 def ssm_linattn_states_bytes(batch, L, heads, d_k, d_v, io=SSM_BF16) -> int:
-    return int(load_library().ssm_linattn_states_bytes(batch, L, heads, d_k, d_v, io))
+    return int(load_library().ssm_linattn_states_bytes(batch, L, *_sizes(heads, d_k, d_v), io))
 
 
 def ssm_linattn_fwd_workspace(batch, L, heads, groups, d_k, d_v, io=SSM_BF16) -> int:
-    return int(load_library().ssm_linattn_fwd_workspace(batch, L, heads, groups, d_k, d_v, io))
+    return int(load_library().ssm_linattn_fwd_workspace(batch, L, *_sizes(heads, groups, d_k, d_v), io))
 
 
 def ssm_linattn_bwd_workspace(batch, L, heads, groups, d_k, d_v, per_token=True, io=SSM_BF16) -> int:
-    return int(load_library().ssm_linattn_bwd_workspace(batch, L, heads, groups, d_k, d_v, int(per_token), io))
+    return int(load_library().ssm_linattn_bwd_workspace(batch, L, *_sizes(heads, groups, d_k, d_v), int(per_token), io))
 
 
 def _decay(log_decay, lead, heads, other, device):
@@ -56,6 +67,7 @@ def _linattn_inputs(q, k, v, log_decay):
         raise ValueError(f"q and v must be [batch, L, heads, dim], got {tuple(q.shape)} and {tuple(v.shape)}")
     b, L, Hk, K = q.shape
     H, V = v.shape[2:]
+    _sizes(H, Hk, K, V)
     io, dev = q.dtype, q.device
     at, per_token = _decay(log_decay, (b, L), H, (H,), dev)
     return (b, L, H, Hk, K, V, _kind(q)), (_need(q, "q", q.shape, io, dev), _need(k, "k", (b, L, Hk, K), io, dev),
@@ -132,6 +144,7 @@ def ssm_linattn_step(h, q_t, k_t, v_t, log_decay, *, scale=None, o_t=None):
         raise ValueError(f"q_t and v_t must be [layers, seqs, heads, dim], got {tuple(q_t.shape)} and {tuple(v_t.shape)}")
     Ln, S, Hk, K = q_t.shape
     H, V = v_t.shape[2:]
+    _sizes(H, Hk, K, V)
     io, dev = q_t.dtype, q_t.device
     kind = _kind(q_t)
     at, per_token = _decay(log_decay, (Ln, S), H, (Ln, H), dev)
@@ -177,14 +190,14 @@ def linear_attention(q, k, v, log_decay, h0=None, *, scale=None):
 
 # ------------------------------------------------------------------ RMS norm
 def ssm_rmsnorm_bwd_workspace(rows, dim) -> int:
-    return int(load_library().ssm_rmsnorm_bwd_workspace(rows, dim))
+    return int(load_library().ssm_rmsnorm_bwd_workspace(rows, _int32(dim, "dim")))
 
 
 def _norm_inputs(x, weight, residual, residual_out):
     """Rows, dim, the types, residual_out, and the addresses of x, residual and weight."""
     if x.dim() < 1:
         raise ValueError("x must have at least one dimension")
-    dim, dev = x.shape[-1], x.device
+    dim, dev = _int32(x.shape[-1], "dim"), x.device
     rows = x.numel() // dim if dim else 0
     kind, res_kind = _kind(x), _kind(x if residual is None else residual)
     if residual is not None and residual.dtype is not x.dtype and residual.dtype is not _f32:
@@ -230,6 +243,7 @@ def ssm_rmsnorm_fwd_q8(x, weight, residual=None, *, eps=1e-6, code="e4m3", group
     """ssm_rmsnorm_fwd with y in 8 bits: codes [..., D] (float8_e4m3fn or int8), scales [..., groups]
     float32 (one for the row with group 0, or for 32, 64 or 128 values) and s (None without a residual)."""
     number, dtype = _code(code)
+    _int32(group, "group")
     if x.is_cuda:
         got = _table_module().rmsnorm_fwd_q8(_entry("ssm_rmsnorm_fwd_q8"), _stream(x), x, weight, residual, eps, number, group,
                                              codes, scales, residual_out)
@@ -251,13 +265,14 @@ def ssm_q8_values(codes, scales, *, group=None, out=None):
     number = {dtype: n for n, dtype in _CODES.values()}.get(codes.dtype)
     if number is None:
         raise TypeError(f"codes must be float8_e4m3fn or int8, got {codes.dtype}")
-    dim, dev = codes.shape[-1], codes.device
+    dim, dev = _int32(codes.shape[-1], "dim"), codes.device
     count = scales.shape[-1]
     if group is None:
         fits = [0] if count == 1 else [g for g in (32, 64, 128) if -(-dim // g) == count]
         if len(fits) != 1:
             raise ValueError(f"{count} scales for {dim} values: give the group")
         group = fits[0]
+    _int32(group, "group")
     if codes.is_cuda:
         got = _table_module().q8_values(_entry("ssm_q8_values"), _stream(codes), codes, scales, group, out)
         if got is not None:
@@ -281,7 +296,7 @@ def ssm_rmsnorm_bwd(dy, s, weight, rstd, *, ds=None, workspace=None):
             dx, dres, dweight = _made(got)
             return dx, dx if dres is None else dres, dweight
     lib = load_library()
-    dim, dev = dy.shape[-1], dy.device
+    dim, dev = _int32(dy.shape[-1], "dim"), dy.device
     rows = dy.numel() // dim if dim else 0
     kind, res_kind = _kind(dy), _kind(s)
     at = (_need(dy, "dy", dy.shape, dy.dtype, dev), _need(s, "s", dy.shape, s.dtype, dev), _need(ds, "ds", dy.shape, s.dtype, dev),
