@@ -349,6 +349,13 @@ def _setting(value, name, rows, dtype, device):
     return None, value
 
 
+def _top_k(value):
+    """A top_k for all rows, in 32 bits: a whole number, of which 0 and less keep all."""
+    if not float(value).is_integer():
+        raise ValueError(f"top_k must be a whole number, got {value}")
+    return max(0, min(int(value), 2 ** 31 - 1))
+
+
 def ssm_sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, logprob=None,
                want_logprob=False, workspace=None):
     """The next token [S] int64 of every row of logits [S, V], from one uniform number of [0, 1) a row
@@ -362,12 +369,13 @@ def ssm_sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
         if got is not None:
             tokens, logprob = _made(got)
             return tokens if logprob is None else (tokens, logprob)
+    k_all = 0 if torch.is_tensor(top_k) else _top_k(top_k)
     lib = load_library()
     rows, vocab = logits.shape
     dev = logits.device
     kind = _kind(logits)
     t, t_all = _setting(temperature, "temperature", rows, _f32, dev)
-    k, k_all = _setting(top_k, "top_k", rows, torch.int32, dev)
+    k = _setting(top_k, "top_k", rows, torch.int32, dev)[0]
     p, p_all = _setting(top_p, "top_p", rows, _f32, dev)
     m, m_all = _setting(min_p, "min_p", rows, _f32, dev)
     tokens = torch.empty(rows, dtype=torch.int64, device=dev) if tokens is None else tokens
@@ -375,6 +383,6 @@ def ssm_sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tok
         logprob = torch.empty(rows, dtype=_f32, device=dev)
     ws, ws_at, ws_bytes = _scratch(workspace, lib.ssm_sample_workspace(rows, vocab), dev)
     _called(logits, lib.ssm_sample, _need(logits, "logits", logits.shape, logits.dtype, dev), _need(u, "u", (rows,), _f32, dev),
-            t, t_all, k, min(int(k_all), 2 ** 31 - 1), p, p_all, m, m_all, _need(tokens, "tokens", (rows,), torch.int64, dev),
+            t, t_all, k, k_all, p, p_all, m, m_all, _need(tokens, "tokens", (rows,), torch.int64, dev),
             _need(logprob, "logprob", (rows,), _f32, dev), rows, vocab, kind, ws_at, ws_bytes, written=(tokens, logprob))
     return tokens if logprob is None else (tokens, logprob)
