@@ -18,6 +18,7 @@
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_cpp_function.h>
+#include <torch/csrc/autograd/python_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -25,6 +26,8 @@
 #include <cstring>
 #include <exception>
 #include <initializer_list>
+#include <memory>
+#include <unordered_set>
 #include <vector>
 
 namespace {
@@ -742,19 +745,33 @@ PyObject *sample(PyObject *, PyObject *const *args, Py_ssize_t n) {
     });
 }
 
-// leaves_elsewhere(next_functions, stream_id): whether a leaf among the functions that a node's gradients go
-// to has its gradient gathered on another stream than this one.
+// The node behind a Python object of autograd's graph, or none.
+std::shared_ptr<torch::autograd::Node> node_of(PyObject *o) {
+    if (torch::autograd::THPCppFunction_Check(o)) return ((torch::autograd::THPCppFunction *)o)->cdata;
+    if (THPFunction_Check(o)) return ((THPFunction *)o)->cdata.lock();
+    return nullptr;
+}
+
+// leaves_elsewhere(next_functions, stream_id): whether a function that a node's gradients come to, the leaves at
+// the end among them, works on another stream than this one.
 PyObject *leaves_elsewhere(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 2 || !PyTuple_Check(args[0])) return PyErr_Format(PyExc_TypeError, "a tuple and a stream's id expected");
     return no_exceptions([&]() -> PyObject * {
         const int64_t stream = PyLong_AsLongLong(args[1]);
         if (PyErr_Occurred()) return nullptr;
+        std::vector<std::shared_ptr<torch::autograd::Node>> todo;
         for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(args[0]); ++i) {
             PyObject *const edge = PyTuple_GET_ITEM(args[0], i);
-            PyObject *const to = PyTuple_Check(edge) && PyTuple_GET_SIZE(edge) > 0 ? PyTuple_GET_ITEM(edge, 0) : Py_None;
-            if (std::strcmp(Py_TYPE(to)->tp_name, "AccumulateGrad") != 0) continue;
-            const auto on = ((torch::autograd::THPCppFunction *)to)->cdata->stream();
+            if (PyTuple_Check(edge) && PyTuple_GET_SIZE(edge) > 0) todo.push_back(node_of(PyTuple_GET_ITEM(edge, 0)));
+        }
+        std::unordered_set<torch::autograd::Node *> seen;
+        while (!todo.empty()) {
+            const std::shared_ptr<torch::autograd::Node> node = std::move(todo.back());
+            todo.pop_back();
+            if (!node || !seen.insert(node.get()).second) continue;
+            const auto on = node->stream();
             if (on && on->id() != stream) Py_RETURN_TRUE;
+            for (const auto &edge : node->next_edges()) todo.push_back(edge.function);
         }
         Py_RETURN_FALSE;
     });
@@ -774,7 +791,7 @@ PyMethodDef methods[] = {
     {"rmsnorm_fwd_q8", (PyCFunction)(void (*)(void))rmsnorm_fwd_q8, METH_FASTCALL, "ssm_rmsnorm_fwd_q8 for tensors."},
     {"rmsnorm_bwd", (PyCFunction)(void (*)(void))rmsnorm_bwd, METH_FASTCALL, "ssm_rmsnorm_bwd for tensors."},
     {"q8_values", (PyCFunction)(void (*)(void))q8_values, METH_FASTCALL, "ssm_q8_values for tensors."},
-    {"leaves_elsewhere", (PyCFunction)(void (*)(void))leaves_elsewhere, METH_FASTCALL, "Whether a leaf's gradient is gathered on another stream."},
+    {"leaves_elsewhere", (PyCFunction)(void (*)(void))leaves_elsewhere, METH_FASTCALL, "Whether a gradient goes to another stream."},
     {"sample", (PyCFunction)(void (*)(void))sample, METH_FASTCALL, "ssm_sample for tensors."},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensor_table", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
