@@ -27,6 +27,7 @@
 #include <exception>
 #include <initializer_list>
 #include <memory>
+#include <unordered_map>
 #include <unordered_set>
 #include <vector>
 
@@ -753,8 +754,9 @@ std::shared_ptr<torch::autograd::Node> node_of(PyObject *o) {
 }
 
 // leaves_elsewhere(next_functions, stream_id): whether a function that a node's gradients come to, the leaves at
-// the end among them, works on another stream than this one.
-PyObject *leaves_elsewhere(PyObject *, PyObject *const *args, Py_ssize_t n) {
+// the end among them, works on a stream that is neither this one nor, by the module's `capturing`, part of
+// the same capture.
+PyObject *leaves_elsewhere(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     if (n != 2 || !PyTuple_Check(args[0])) return PyErr_Format(PyExc_TypeError, "a tuple and a stream's id expected");
     return no_exceptions([&]() -> PyObject * {
         const int64_t stream = PyLong_AsLongLong(args[1]);
@@ -765,12 +767,27 @@ PyObject *leaves_elsewhere(PyObject *, PyObject *const *args, Py_ssize_t n) {
             if (PyTuple_Check(edge) && PyTuple_GET_SIZE(edge) > 0) todo.push_back(node_of(PyTuple_GET_ITEM(edge, 0)));
         }
         std::unordered_set<torch::autograd::Node *> seen;
+        std::unordered_map<int64_t, bool> captured;
+        captured[stream] = true;
         while (!todo.empty()) {
             const std::shared_ptr<torch::autograd::Node> node = std::move(todo.back());
             todo.pop_back();
             if (!node || !seen.insert(node.get()).second) continue;
-            const auto on = node->stream();
-            if (on && on->id() != stream) Py_RETURN_TRUE;
+            if (const auto on = node->stream()) {
+                const auto known = captured.find(on->id());
+                bool yes;
+                if (known != captured.end()) {
+                    yes = known->second;
+                } else {
+                    PyObject *const asked = PyObject_CallMethod(self, "capturing", "Lii", (long long)on->id(), (int)on->device_index(),
+                                                                (int)on->device_type());
+                    const int truth = asked ? PyObject_IsTrue(asked) : -1;
+                    Py_XDECREF(asked);
+                    if (truth < 0) return nullptr;
+                    yes = captured[on->id()] = truth != 0;
+                }
+                if (!yes) Py_RETURN_TRUE;
+            }
             for (const auto &edge : node->next_edges()) todo.push_back(edge.function);
         }
         Py_RETURN_FALSE;

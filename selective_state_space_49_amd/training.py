@@ -63,6 +63,14 @@ def _called(t: torch.Tensor, entry, *args, written=()):
 _table_loaded = None
 
 
+def _capturing(stream_id: int, device_index: int, device_type: int) -> bool:
+    """Whether a stream is being captured. The default one (0) never is; it may not even be asked then."""
+    if stream_id == 0:
+        return False
+    with torch.cuda.stream(torch.cuda.Stream(stream_id=stream_id, device_index=device_index, device_type=device_type)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _table_module():
     """The extension that reads tensors for short calls (csrc/tensor_table.cpp)."""
     global _table_loaded
@@ -71,6 +79,7 @@ def _table_module():
         if not os.path.exists(path):
             raise ImportError(f"{path} is missing: build it with `python -m selective_state_space_49_amd.build`")
         _table_loaded = importlib.import_module("._tensor_table", __package__)
+        _table_loaded.capturing = _capturing
     return _table_loaded
 
 

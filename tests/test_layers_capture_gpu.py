@@ -1,5 +1,5 @@
-"""Which captured backward passes are refused: those whose gradients come to a function or a leaf that works on
-another stream, however far behind the operator it is."""
+"""Which captured backward passes are refused: those whose gradients come to a function or a leaf that works on a
+stream outside the capture, however far behind the operator it is; and no others."""
 import pytest
 import torch
 
@@ -46,3 +46,32 @@ def test_refused_behind_a_cast():
             torch.autograd.grad(ssm.rms_norm(x, w.float()), w, dy)
     torch.cuda.synchronize()
     assert bool(torch.autograd.grad(eager, w, dy)[0].isfinite().all())
+
+
+def test_a_stream_of_the_capture_is_not_refused():
+    """A leaf's gradient from a stream that the capture has forked into: both streams belong to it."""
+    say("captured backward over a forked stream")
+    x, w = torch.randn(30, 50, device="cuda", requires_grad=True), torch.ones(50, device="cuda", requires_grad=True)
+    dy = [torch.randn(30, 50, device="cuda") for _ in range(2)]
+    side = torch.cuda.Stream()
+
+    def grads():
+        here = torch.cuda.current_stream()
+        first = ssm.rms_norm(x, w)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            second = ssm.rms_norm(x, w, eps=0.5)
+        here.wait_stream(side)
+        return torch.autograd.grad((first, second), (x, w), dy)
+    want = [t.clone() for t in grads()]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = grads()
+    for _ in range(3):
+        for t in got:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(bitwise_equal(a, b) for a, b in zip(got, want))
+        (torch.ones(100, device="cuda") * 2).sum()
