@@ -754,8 +754,8 @@ std::shared_ptr<torch::autograd::Node> node_of(PyObject *o) {
 }
 
 // leaves_elsewhere(next_functions, stream_id): whether a function that a node's gradients come to, the leaves at
-// the end among them, works on a stream that is neither this one nor, by the module's `capturing`, part of
-// the same capture.
+// the end among them, works on a stream that is neither this one nor, by the module's `joins`, one that can take
+// part in its capture.
 PyObject *leaves_elsewhere(PyObject *self, PyObject *const *args, Py_ssize_t n) {
     if (n != 2 || !PyTuple_Check(args[0])) return PyErr_Format(PyExc_TypeError, "a tuple and a stream's id expected");
     return no_exceptions([&]() -> PyObject * {
@@ -767,24 +767,23 @@ PyObject *leaves_elsewhere(PyObject *self, PyObject *const *args, Py_ssize_t n) 
             if (PyTuple_Check(edge) && PyTuple_GET_SIZE(edge) > 0) todo.push_back(node_of(PyTuple_GET_ITEM(edge, 0)));
         }
         std::unordered_set<torch::autograd::Node *> seen;
-        std::unordered_map<int64_t, bool> captured;
-        captured[stream] = true;
+        std::unordered_map<int64_t, bool> joins;
+        joins[stream] = true;
         while (!todo.empty()) {
             const std::shared_ptr<torch::autograd::Node> node = std::move(todo.back());
             todo.pop_back();
             if (!node || !seen.insert(node.get()).second) continue;
             if (const auto on = node->stream()) {
-                const auto known = captured.find(on->id());
+                const auto known = joins.find(on->id());
                 bool yes;
-                if (known != captured.end()) {
+                if (known != joins.end()) {
                     yes = known->second;
                 } else {
-                    PyObject *const asked = PyObject_CallMethod(self, "capturing", "Lii", (long long)on->id(), (int)on->device_index(),
-                                                                (int)on->device_type());
+                    PyObject *const asked = PyObject_CallMethod(self, "joins", "L", (long long)on->id());
                     const int truth = asked ? PyObject_IsTrue(asked) : -1;
                     Py_XDECREF(asked);
                     if (truth < 0) return nullptr;
-                    yes = captured[on->id()] = truth != 0;
+                    yes = joins[on->id()] = truth != 0;
                 }
                 if (!yes) Py_RETURN_TRUE;
             }

@@ -29,14 +29,14 @@ def _int32(value, name):
 
 def _refuse_leaves_elsewhere(ctx):
     """A leaf's gradient is gathered on the stream of the oldest living graph that has it, and every other
-    function of the graph works on the stream on which it was recorded. In a capture autograd would make such a
-    stream wait for the captured one, which ends the process unless it is part of the capture too: an error
-    instead, before the gradients leave. What is looked at are the functions that this node's gradients
-    come to, directly or through others."""
+    function of the graph works on the stream on which it was recorded. In a capture autograd makes such a
+    stream wait for the captured one, and so a part of it; the default stream cannot be one, and that ends the
+    process: an error instead, before the gradients leave. What is looked at are the functions that this node's
+    gradients come to, directly or through others."""
     if torch.cuda.is_current_stream_capturing():
         if _table_module().leaves_elsewhere(ctx.next_functions, torch.cuda.current_stream().stream_id):
-            raise RuntimeError("a backward pass cannot be captured while a graph that was built on another stream "
-                               "holds the same leaves: drop that graph's outputs first")
+            raise RuntimeError("a backward pass cannot be captured while a graph that was built on the default "
+                               "stream holds the same leaves: drop that graph's outputs first")
 
 
 # ------------------------------------------------------------------ linear attention

@@ -63,12 +63,10 @@ def _called(t: torch.Tensor, entry, *args, written=()):
 _table_loaded = None
 
 
-def _capturing(stream_id: int, device_index: int, device_type: int) -> bool:
-    """Whether a stream is being captured. The default one (0) never is; it may not even be asked then."""
-    if stream_id == 0:
-        return False
-    with torch.cuda.stream(torch.cuda.Stream(stream_id=stream_id, device_index=device_index, device_type=device_type)):
-        return torch.cuda.is_current_stream_capturing()
+def _joins(stream_id: int) -> bool:
+    """Whether a stream can take part in the capture that the current one is in: all but the default one (0),
+    which cannot be captured."""
+    return stream_id != 0 and torch.cuda.is_current_stream_capturing()
 
 
 def _table_module():
@@ -79,7 +77,7 @@ def _table_module():
         if not os.path.exists(path):
             raise ImportError(f"{path} is missing: build it with `python -m selective_state_space_49_amd.build`")
         _table_loaded = importlib.import_module("._tensor_table", __package__)
-        _table_loaded.capturing = _capturing
+        _table_loaded.joins = _joins
     return _table_loaded
 
 

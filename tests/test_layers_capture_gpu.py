@@ -1,5 +1,5 @@
-"""Which captured backward passes are refused: those whose gradients come to a function or a leaf that works on a
-stream outside the capture, however far behind the operator it is; and no others."""
+"""Which captured backward passes are refused: those whose gradients come to a function or a leaf that works on the
+default stream, however far behind the operator it is; and no others."""
 import pytest
 import torch
 
@@ -75,3 +75,35 @@ def test_a_stream_of_the_capture_is_not_refused():
         torch.cuda.synchronize()
         assert all(bitwise_equal(a, b) for a, b in zip(got, want))
         (torch.ones(100, device="cuda") * 2).sum()
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_leaves_of_a_side_stream_are_not_refused(accumulate):
+    """An eager graph of the same leaves that was built on a stream of its own, as in a warm-up: that stream becomes
+    a part of the capture."""
+    say("captured backward beside an eager graph of a side stream", accumulate)
+    x, w = torch.randn(30, 50, device="cuda", requires_grad=True), torch.ones(50, device="cuda", requires_grad=True)
+    dy = torch.randn(30, 50, device="cuda")
+    want = [t.clone() for t in torch.autograd.grad(ssm.rms_norm(x, w), (x, w), dy)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        eager = ssm.rms_norm(x, w)
+    torch.cuda.synchronize()
+    got = [torch.empty_like(t) for t in want]
+    if accumulate:
+        x.grad, w.grad = got
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        if accumulate:
+            ssm.rms_norm(x, w).backward(dy)
+        else:
+            got = torch.autograd.grad(ssm.rms_norm(x, w), (x, w), dy)
+    for _ in range(3):
+        for t in got:
+            t.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(bitwise_equal(a, b) for a, b in zip(got, want))
+        (torch.ones(100, device="cuda") * 2).sum()
+    assert all(bitwise_equal(a, b) for a, b in zip(torch.autograd.grad(eager, (x, w), dy), want))
