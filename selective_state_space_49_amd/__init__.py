@@ -845,6 +845,7 @@ class _SelectiveScan(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy, dh_final):
+        _refuse_capture(ctx)
         x, dt, A, B, C, D, z, h0, states = ctx.saved_tensors
         need = ctx.needs_input_grad
         if dy is None:
@@ -892,6 +893,7 @@ class _SelectiveScanFused(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy, dh_final):
+        _refuse_capture(ctx)
         x_in, dt_raw, A, B, C, D, z, h0, conv_w, conv_b, conv_state0, dt_bias, states, u, dt = ctx.saved_tensors
         need = ctx.needs_input_grad
         if dy is None:
@@ -984,7 +986,7 @@ def ssm_step_mimo(h, x_t, dt_t, A, B_t, C_t, D, z_t=None, *, y_t=None):
 
 
 from .training import (  # noqa: E402  (the training operators use the helpers above)
-    ADAMW_BLOCK, GATED_STATE_EVERY, AdamW, gated_scan, linear_cross_entropy, ssm_adamw_state_size,
+    _refuse_capture, ADAMW_BLOCK, GATED_STATE_EVERY, AdamW, gated_scan, linear_cross_entropy, ssm_adamw_state_size,
     ssm_adamw_step, ssm_adamw_values, ssm_gated_bwd, ssm_gated_bwd_workspace, ssm_gated_fwd,
     ssm_gated_fwd_save, ssm_gated_fwd_workspace, ssm_gated_states_bytes, ssm_gated_step,
     ssm_xent_bwd, ssm_xent_bwd_workspace, ssm_xent_bwd_workspace_for, ssm_xent_fwd,

@@ -81,6 +81,12 @@ def _table_module():
     return _table_loaded
 
 
+def _refuse_capture(ctx):
+    """See _refuse_leaves_elsewhere."""
+    from .layers import _refuse_leaves_elsewhere
+    _refuse_leaves_elsewhere(ctx)
+
+
 _entries: dict = {}
 
 
@@ -226,6 +232,7 @@ class _GatedScan(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dh_final):
+        _refuse_capture(ctx)
         x, r, i, decay, states, reset = ctx.saved_tensors
         dy = torch.zeros_like(x) if dy is None else dy.to(x.dtype).contiguous()
         g = ssm_gated_bwd(x, r, i, decay, states, reset, dy=dy, c=ctx.c,
@@ -341,6 +348,7 @@ class _LinearCrossEntropy(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dmean, dloss):
+        _refuse_capture(ctx)
         hidden, weight, targets, lse, mean = ctx.saved_tensors
         one = lambda t: None if t is None else t.float().contiguous()  # noqa: E731
         dhidden, dweight = ssm_xent_bwd(hidden, weight, targets, lse, mean, dloss=one(dloss), dmean=one(dmean),
