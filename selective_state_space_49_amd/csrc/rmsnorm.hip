@@ -279,7 +279,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_fwd(NormArgs p) {
 }
 
 // Every row set (a block, or a wave of one) takes rows at a distance and keeps its sum of dweight; a wave that
-// has several rows at a time adds theirs at the end. A row of more than 16384 elements is read a second time, from
+// has several rows at a time adds theirs at the end. A sum of many rows in 32 bits would lose the bits of a row's
+// share, so it is compensated (Kahan), which takes as many registers again and three operations an element;
+// rows of more than 8192, which have no registers left, get a set for every 64 rows instead. A row of more than 16384 elements is read a second time, from
 // the cache where it fits, after its sum: it does not fit the registers beside dweight's (2048 rows of 9216 in
 // 35 us; 1024 of 20000 in 129, held in registers and memory behind them 177).
 template <typename T, typename R, int TPR, int NV>
@@ -288,9 +290,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_bwd(NormBwdArgs p, in
     __shared__ double part[TPR > 64 ? TPR / 64 : 1];
     Piece<TPR> own;
     constexpr int kOfSet = TPR < 64 ? 64 / TPR : 1, KEPT = NV <= 2 ? NV : 1;
+    constexpr bool kCompensated = TPR < 1024;
     const int line = blockIdx.x * kRows + threadIdx.x / TPR, set = line / kOfSet, D = p.dim;
     if (set >= sets) return;
-    float dw[NV][E] = {};
+    float dw[NV][E] = {}, lost[kCompensated ? NV : 1][E] = {};  // what the sums have too much
     for (int64_t row = line; row < p.rows; row += (int64_t)sets * kOfSet) {
         const int64_t at0 = row * D;
         const float r = p.rstd[row];
@@ -306,7 +309,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_bwd(NormBwdArgs p, in
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 n[e] *= r;
-                if (first) dw[k][e] += wd[e] * n[e];
+                if constexpr (kCompensated) {
+                    const float add = __builtin_fmaf(wd[e], n[e], -lost[k][e]), up = dw[k][e] + add;
+                    lost[k][e] = (up - dw[k][e]) - add;
+                    dw[k][e] = up;
+                } else if (first) {
+                    dw[k][e] += wd[e] * n[e];
+                }
                 wd[e] *= w[e];
                 t += wd[e] * n[e];
             }
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(256) k_values(const uint8_t *codes, const floa
 
 // Threads of a row: 16 up to 128 elements (heads), 32 up to 256, a wave up to 1024, 256 up to 4096, 512 up to 8192,
 // 1024 up to 65536. 524288 rows of 128 in bf16: forward 53 us, backward 124; with a wave for a row 170 and 339.
-constexpr int kNarrow = 128, kHalf = 256;
+constexpr int kNarrow = 128, kHalf = 256, kCompensatedDim = 8192;
 template <typename F>
 void by_size(int D, F go) {
     typedef std::integral_constant<int, 16> N;
@@ -449,10 +458,14 @@ void run_fwd(const NormArgs &a, hipStream_t s) {
     });
 }
 
-// Row sets of the backward: enough for the GPU, each with several rows where there are many.
+// Row sets of the backward: enough for the GPU, each with several rows where there are many, but 64 at most
+// where their sums are not compensated (1/64 of the rows' bytes for the sets' sums). A launch has fewer than
+// 2^32 threads.
 int row_sets(int64_t rows, int32_t dim) {
     const int64_t at_once = dim <= kNarrow ? 4 : dim <= kHalf ? 2 : 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>((rows + at_once - 1) / at_once, dim <= 1024 ? 2048 : 512));
+    int64_t most = dim <= 1024 ? 2048 : 512;
+    if (dim > kCompensatedDim) most = std::min<int64_t>(std::max<int64_t>(most, (rows + 63) / 64), 1 << 21);
+    return (int)std::max<int64_t>(1, std::min<int64_t>((rows + at_once - 1) / at_once, most));
 }
 
 template <typename T, typename R>
