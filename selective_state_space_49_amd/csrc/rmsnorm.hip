@@ -124,22 +124,32 @@ __device__ __forceinline__ float to_e4m3(double u) {
     const float r = (float)((u + big) - big);
     return fminf(fmaxf(r, -448.0f), 448.0f);
 }
+// A scale, and its reciprocal (0 where there is none).
+struct Scale {
+    double s, inv;
+    // y / s: the reciprocal's error would put a quotient in the middle of two codes beside it (73.5 / 49), so
+    // what is left of y is added, after which a quotient that 64 bits hold is that one.
+    __device__ __forceinline__ double of(double y) const {
+        const double q = y * inv;
+        return __builtin_fma(__builtin_fma(-q, s, y), inv, q);
+    }
+};
 // Eight codes. A quotient rounded to float32 first gives the same code as the quotient itself unless
 // float32 puts it onto the middle of two codes, or it is below the smallest normal one (2^-6, where
 // steps differ): about 1 in 10^4, which take the long way.
-__device__ __forceinline__ void code8(const double (&u)[E], int code, uint32_t (&c)[2]) {
+__device__ __forceinline__ void code8(const double (&y)[E], Scale scale, int code, uint32_t (&c)[2]) {
     float f[E];
     if (code == 1) {
         bool hard = false;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            f[e] = (float)u[e];
+            f[e] = (float)(y[e] * scale.inv);
             hard |= (__float_as_uint(f[e]) & 0xfffffu) == 0x80000u || !(fabsf(f[e]) >= 0x1p-6f);
             f[e] = __builtin_amdgcn_fmed3f(f[e], -448.0f, 448.0f);
         }
         if (hard) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) f[e] = to_e4m3(u[e]);
+            for (int e = 0; e < E; ++e) f[e] = to_e4m3(scale.of(y[e]));
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -150,7 +160,7 @@ __device__ __forceinline__ void code8(const double (&u)[E], int code, uint32_t (
         c[0] = c[1] = 0;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const float r = __builtin_amdgcn_fmed3f((float)__builtin_rint(u[e]), -127.0f, 127.0f);
+            const float r = __builtin_amdgcn_fmed3f((float)__builtin_rint(scale.of(y[e])), -127.0f, 127.0f);
             c[e / 4] |= (uint32_t)((int)r & 0xff) << (e % 4 * 8);
         }
     }
@@ -175,13 +185,15 @@ __device__ __forceinline__ long long over_lanes(long long x, int lanes) {
 }
 // The scale of values whose largest is top, and its reciprocal, by Newton's steps from the hardware's estimate
 // (relative 2^-22, 2^-44, 2^-52).
-__device__ __forceinline__ float scale_of(long long top, int code, double &inv) {
-    const float scale = (float)(__longlong_as_double(top) * (code == 1 ? 1.0 / 448.0 : 1.0 / 127.0));
+__device__ __forceinline__ float scale_of(long long top, int code, Scale &to) {
+    const Scale most = code == 1 ? Scale{448.0, 1.0 / 448.0} : Scale{127.0, 1.0 / 127.0};
+    const double largest = __longlong_as_double(top);
+    const float scale = (float)(largest < __builtin_inf() ? most.of(largest) : largest);
     const double s = (double)scale;
     double x = __builtin_amdgcn_rcp(s);
     x = __builtin_fma(x, __builtin_fma(-s, x, 1.0), x);
     x = __builtin_fma(x, __builtin_fma(-s, x, 1.0), x);
-    inv = scale == 0.0f ? 0.0 : scale == __builtin_inff() ? 0.0 : x;
+    to = scale == 0.0f || scale == __builtin_inff() ? Scale{0.0, 0.0} : Scale{s, x};
     return scale;
 }
 
@@ -230,7 +242,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_fwd(NormArgs p) {
         return;
     }
     const int group = p.group, groups = group ? (D + group - 1) / group : 1;
-    double inv = 0.0;
+    Scale by{0.0, 0.0};
     if constexpr (MODE == kRowCodes) {
         Top top;
 #pragma unroll
@@ -240,7 +252,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_fwd(NormArgs p) {
 #pragma unroll
             for (int e = 0; e < E; ++e) top.add((double)s[n][e] * r * (double)w[e]);
         }
-        const float scale = scale_of(over_row<TPR>(top.bits(), (long long *)part, larger), p.code, inv);
+        const float scale = scale_of(over_row<TPR>(top.bits(), (long long *)part, larger), p.code, by);
         if (tid == 0) p.scales[row] = scale;
     }
 #pragma unroll
@@ -250,21 +262,16 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_fwd(NormArgs p) {
         double y[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = (double)s[n][e] * r * (double)w[e];
-        if constexpr (MODE == kRowCodes) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) y[e] *= inv;
-        } else {
+        if constexpr (MODE == kGroupCodes) {
             Top top;
 #pragma unroll
             for (int e = 0; e < E; ++e) top.add(y[e]);
-            const float scale = scale_of(over_lanes(top.bits(), group / E), p.code, inv);
+            const float scale = scale_of(over_lanes(top.bits(), group / E), p.code, by);
             const int at = own.at(n);
             if (at < D && at % group == 0) p.scales[row * groups + at / group] = scale;
-#pragma unroll
-            for (int e = 0; e < E; ++e) y[e] *= inv;
         }
         uint32_t c[2];
-        code8(y, p.code, c);
+        code8(y, by, p.code, c);
         uint8_t *const to = (uint8_t *)p.y + at0;
         const int at = own.at(n);
         if (at + E <= D) {
