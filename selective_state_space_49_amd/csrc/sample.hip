@@ -775,7 +775,8 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs p, int shift) {
     if (settled(ends, s, p.tokens + r, logprob)) return;
     const Masses mass = masses_of(ends, s, shift);
     u64 last = 0;  // the last place that is kept
-    bool lost = ends.high == kInfinity;  // no steps hold the end
+    // No steps hold the end: there is a +infinity, or float32 does not hold the distance of the smallest.
+    bool lost = !(ends.high - ends.low < kInfinity);
     if (!lost) {
         const Steps st(ends, s);
         Plan pl{kBins, kBins, kBins, 0, false};

@@ -80,3 +80,13 @@ def test_time():
         return sorted(times)[3]
     near, far = time(0.0), time(20.0)
     assert far <= 6 * near, (near, far)
+
+
+def test_distances_past_float32():
+    """A temperature so high that logits keep their mass over a distance that float32 does not hold."""
+    x = torch.tensor([3e38, -3e38, 2e38, -1e38, 1e38, -2e38, 0.0, -math.inf]).repeat(4, 3)
+    u = torch.tensor([0.05, 0.4, 0.8, 0.99])
+    for t in (1e37, 1e38, 3e38):
+        for settings in ({}, {"top_p": 0.97}, {"top_k": 20}, {"top_k": 19, "top_p": 0.9}, {"min_p": 0.01, "top_p": 0.999}):
+            say("distances", t, settings)
+            check(x, u, temperature=t, **settings)
