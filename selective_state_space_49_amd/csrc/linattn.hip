@@ -1276,18 +1276,17 @@ void sweep(const SweepArgs &a, Access access, int64_t blocks, hipStream_t s) {
     const int width = (a.V > 64 ? 128 : 64) / a.slices;
     const auto go = [&](auto acc) {
         constexpr Access A = decltype(acc)::value;
-        if (a.K > 64 || A == kElements) {
-            if (width == 128) k_sweep<T, 128, 4, OUT, A><<<blocks, 256, 0, s>>>(a);
-            else k_sweep<T, 128, 2, OUT, A><<<blocks, 128, 0, s>>>(a);
-        } else if (sizeof(T) == 4 && a.K <= 32) {  // products in float32 are what bounds it
-            if constexpr (sizeof(T) == 4 && A != kElements) {
-                if (width == 128) k_sweep<T, 32, 4, OUT, A><<<blocks, 256, 0, s>>>(a);
-                else k_sweep<T, 32, 2, OUT, A><<<blocks, 128, 0, s>>>(a);
-            }
-        } else {
-            if (width == 128) k_sweep<T, 64, 4, OUT, A><<<blocks, 256, 0, s>>>(a);
-            else k_sweep<T, 64, 2, OUT, A><<<blocks, 128, 0, s>>>(a);
+        const auto keys = [&](auto kp) {
+            constexpr int KP = decltype(kp)::value;
+            if (width == 128) k_sweep<T, KP, 4, OUT, A><<<blocks, 256, 0, s>>>(a);
+            else k_sweep<T, KP, 2, OUT, A><<<blocks, 128, 0, s>>>(a);
+        };
+        if constexpr (A != kElements) {
+            if constexpr (sizeof(T) == 4)  // products in float32 are what bounds it
+                if (a.K <= 32) return keys(std::integral_constant<int, 32>());
+            if (a.K <= 64) return keys(std::integral_constant<int, 64>());
         }
+        keys(std::integral_constant<int, 128>());
     };
     if (access == kWide) go(std::integral_constant<Access, kWide>());
     else if (access == kAny) go(std::integral_constant<Access, kAny>());

@@ -229,13 +229,13 @@ struct Ends {
     }
 };
 template <typename T>
-__device__ __forceinline__ Ends find_ends(const Logits<T> &l, int64_t from, int64_t to, bool greedy, uint32_t *few) {
+__device__ __forceinline__ Ends find_ends(const Logits<T> &l, bool greedy, uint32_t *few) {
     constexpr int E = Logits<T>::E;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     Ends r{-kInfinity, kInfinity, 0, 0xffffffffu};
     bool bad = false;
     if (greedy) {
-        l.template each<4>(from + wave, to, kWaves, [&](const float(&x)[E], int64_t i, int64_t) {
+        l.template each<4>(wave, l.tiles, kWaves, [&](const float(&x)[E], int64_t i, int64_t) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 bad |= x[e] != x[e];
@@ -246,7 +246,7 @@ __device__ __forceinline__ Ends find_ends(const Logits<T> &l, int64_t from, int6
             }
         });
     } else {
-        l.template each<4>(from + wave, to, kWaves, [&](const float(&x)[E], int64_t, int64_t) {
+        l.template each<4>(wave, l.tiles, kWaves, [&](const float(&x)[E], int64_t, int64_t) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 bad |= x[e] != x[e];
@@ -289,9 +289,9 @@ struct Steps {
 
 // 2. The number of logits in every step.
 template <typename T>
-__device__ __forceinline__ void count_steps(const Logits<T> &l, int64_t from, int64_t to, const Steps &st, u64 *bins) {
+__device__ __forceinline__ void count_steps(const Logits<T> &l, const Steps &st, u64 *bins) {
     constexpr int E = Logits<T>::E;
-    l.template each<4>(from + (threadIdx.x >> 6), to, kWaves, [&](const float(&x)[E], int64_t, int64_t) {
+    l.template each<4>(threadIdx.x >> 6, l.tiles, kWaves, [&](const float(&x)[E], int64_t, int64_t) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const float at = fminf(st.of(x[e]), (float)(kBins - 1));  // a NaN (-infinity where all are equal) too
@@ -357,10 +357,10 @@ __device__ __forceinline__ Plan plan_ends(Shared &sh, const Settings &s, const S
     return pl;
 }
 
-// 3. The masses of a range of entries: what is certainly kept, to its entry; sums (of a thread) of what
+// 3. The masses of the entries: what is certainly kept, to its entry; sums (of a thread) of what
 // lies before top_k's last step, and of the certain part of it; and the list.
 template <typename T>
-__device__ __forceinline__ void weigh(const Logits<T> &l, int from, int to, const Settings &s, const Steps &st, const Plan &pl,
+__device__ __forceinline__ void weigh(const Logits<T> &l, const Settings &s, const Steps &st, const Plan &pl,
                                       const Masses &mass, u64 *entry, u64 *list, uint32_t *count, u64 &all, u64 &kept) {
     constexpr int E = Logits<T>::E;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -423,8 +423,8 @@ __device__ __forceinline__ void weigh(const Logits<T> &l, int from, int to, cons
         }
     };
     if (l.per_entry == 1) {
-        for (int e = from + wave; e < to; e += 4 * kWaves)
-            l.template each<2>(e, std::min(e + 3 * kWaves + 1, to), kWaves, [&](const float(&x)[E], int64_t i, int64_t t) {
+        for (int e = wave; e < l.entries; e += 4 * kWaves)
+            l.template each<2>(e, std::min(e + 3 * kWaves + 1, l.entries), kWaves, [&](const float(&x)[E], int64_t i, int64_t t) {
                 mine = 0.0;
                 tile(x, i, t);
                 if (s.by_p && !choosy) sure += mine;
@@ -432,7 +432,7 @@ __device__ __forceinline__ void weigh(const Logits<T> &l, int from, int to, cons
                 if (lane == 0) entry[t] = m;
             });
     } else {
-        for (int e = from + wave; e < to; e += kWaves) {
+        for (int e = wave; e < l.entries; e += kWaves) {
             mine = 0.0;
             l.template each<1>(e * l.per_entry, std::min<int64_t>((e + 1) * l.per_entry, l.tiles), 1, tile);
             if (s.by_p && !choosy) sure += mine;
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs p, int shift) {
     if (s.by_k || s.by_p)
         for (int b = threadIdx.x; b < kBins; b += kThreads) sh.bins[b] = 0;
     if (threadIdx.x == 0) sh.count = 0;
-    const Ends ends = find_ends(l, 0, l.tiles, s.temperature == 0.0f, sh.few);
+    const Ends ends = find_ends(l, s.temperature == 0.0f, sh.few);
     if (settled(ends, s, p.tokens + r, logprob)) return;
     const Masses mass = masses_of(ends, s, shift);
     u64 last = 0;  // the last place that is kept
@@ -781,12 +781,12 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleArgs p, int shift) {
         const Steps st(ends, s);
         Plan pl{kBins, kBins, kBins, 0, false};
         if (s.by_k || s.by_p) {
-            count_steps(l, 0, l.tiles, st, sh.bins);
+            count_steps(l, st, sh.bins);
             __syncthreads();
             pl = plan_ends(sh, s, st);
         }
         u64 all, kept;
-        weigh(l, 0, l.entries, s, st, pl, mass, sh.entry, sh.list, &sh.count, all, kept);
+        weigh(l, s, st, pl, mass, sh.entry, sh.list, &sh.count, all, kept);
         if (s.by_p) {
             block_scan(all, sh.part, all);
             block_scan(kept, sh.part, kept);
