@@ -746,7 +746,8 @@ ssm_status ssm_adamw_values(const int8_t *exp_avg, const uint8_t *exp_avg_sq,
  *   log_decay  : g, float32: [batch, L, heads] where per_token is not 0, else [heads]. Below -104,
  *                -infinity included, exp(g) is 0 in float32 and the step is a cut, the start of a
  *                document: nothing of an earlier step's state reaches it or what follows, and the
- *                gradient of its g is 0. A NaN makes NaN. A g above 0 (growth) is taken as it is.
+ *                gradient of its g is 0. A NaN or +infinity makes NaN of its document from there on.
+ *                A g above 0 (growth) is taken as it is.
  *   h0, h_final: [batch, heads, d_k, d_v] float32, NULL = zero / not wanted
  *   states     : NULL, or what ssm_linattn_bwd needs: the state that enters every chunk
  *                (SSM_LINATTN_CHUNK_BF16 or _F32 steps), [batch, heads, ceil(L / chunk), d_k, d_v]
@@ -756,9 +757,12 @@ ssm_status ssm_adamw_values(const int8_t *exp_avg, const uint8_t *exp_avg_sq,
  * 64 bits. float32 inputs are multiplied in float32. Beside bfloat16 ones, the chunk's scores and, where
  * it makes an output of bfloat16, the state enter a product with 17 bits (two bfloat16 parts), so that
  * an output's error is its own rounding; factors of a float32 result (states, dlog_decay) keep 24 bits.
- * q, k, v (and d_o, states) must be finite: what is not, in a token, can reach the outputs of all
- * of its chunk, and with its state all that follows until a cut in a later chunk; never another
- * sequence or head (in the gradients, the heads of a group).
+ * What is not finite stays with what depends on it: in a token's k or v (or log_decay) it reaches the
+ * outputs of its document from that token on, in q that token's output; nothing before it, no other
+ * document, sequence or head. In the gradients one in q, k, v or d_o reaches what depends on it and,
+ * beyond that, at most its document's tokens in its chunk (and the heads of a group). So rows behind a
+ * sequence's last token may hold anything if they begin with a cut. Sums that overflow float32 are not
+ * told apart.
  * ssm_linattn_bwd gives the gradients of sum(d_o o) + sum(dh_final h_final): dq, dk, dv of io,
  * dlog_decay (float32, in log_decay's shape), dh0 [batch, heads, d_k, d_v] float32 (NULL = not
  * wanted; dh_final NULL = 0). It reads q, k, v, log_decay and scale as the forward had them, and its

@@ -175,6 +175,13 @@ struct Tile {
             return f;
         }
     }
+    static __device__ __forceinline__ f32x4 quad(const char *t, int row, int quad) {
+        if constexpr (sizeof(T) == 2) return __builtin_convertvector(*(const bf16x4 *)(t + at(row, quad)), f32x4);
+        else return *(const f32x4 *)(t + at(row, quad));
+    }
+    static __device__ __forceinline__ float one(const char *t, int row, int column) {
+        return (float)*(const T *)(t + at(row, column / 4) + column % 4 * (int)sizeof(T));
+    }
     // One quad of a row, from four float32 values.
     static __device__ __forceinline__ void put(char *t, int row, int quad, f32x4 x) {
         if constexpr (sizeof(T) == 2) *(bf16x4 *)(t + at(row, quad)) = __builtin_convertvector(x, bf16x4);
@@ -191,6 +198,7 @@ struct Scores {
     typedef Tile<T, C, C> P;
     static constexpr int kDown = 32 * P::kRow, kBytes = P::kBytes + (Kind<T>::kOut - 1) * kDown;
     static __device__ __forceinline__ int at(int row, int quad) { return P::at(row, quad); }
+    static __device__ __forceinline__ int second(int row, int o) { return BELOW == (row < 32) ? o ^ 64 : o + (BELOW ? 1 : 2) * kDown; }
     static __device__ __forceinline__ void put(char *t, int row, int quad, f32x4 x) {
         if constexpr (Kind<T>::kOut == 1) {
             P::put(t, row, quad, x);
@@ -198,10 +206,13 @@ struct Scores {
             const int o = P::at(row, quad);
             const bf16x4 first = __builtin_convertvector(x, bf16x4);
             *(bf16x4 *)(t + o) = first;
-            const bool alone = BELOW == (row < 32);
-            *(bf16x4 *)(t + (alone ? o ^ 64 : o + (BELOW ? 1 : 2) * kDown)) =
-                __builtin_convertvector(x - __builtin_convertvector(first, f32x4), bf16x4);
+            *(bf16x4 *)(t + second(row, o)) = __builtin_convertvector(x - __builtin_convertvector(first, f32x4), bf16x4);
         }
+    }
+    static __device__ __forceinline__ float one(const char *t, int row, int column) {
+        const int o = at(row, column / 4), c = column % 4 * (int)sizeof(T);
+        if constexpr (Kind<T>::kOut == 1) return *(const T *)(t + o + c);
+        else return (float)*(const T *)(t + o + c) + (float)*(const T *)(t + second(row, o) + c);
     }
     // lanes: rows 32 tile + l % 32; contraction: step s. from: at(l % 32, half).
     static __device__ __forceinline__ typename Kind<T>::Frag by_row(const char *t, int from, int tile, int s, int part) {
@@ -315,6 +326,25 @@ struct Stage {
             }
         }
     }
+    // Of what was read; a vector that ends with its row may hold its neighbours.
+    __device__ __forceinline__ bool not_finite() const {
+        if constexpr (sizeof(T) == 2) {
+            typedef short s16x2 __attribute__((ext_vector_type(2)));
+            s16x2 most = {0, 0};
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) most = __builtin_elementwise_max(most, __builtin_bit_cast(s16x2, r[n][e] & 0x7fff7fffu));
+            return most[0] >= 0x7f80 || most[1] >= 0x7f80;
+        } else {
+            float z = 0.0f;
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z = __builtin_fmaf(__uint_as_float(r[n][e]), 0.0f, z);
+            return z != z;
+        }
+    }
     __device__ __forceinline__ void store(char *t, int tid, int width, int c0 = 0) const {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
@@ -357,10 +387,11 @@ struct Decays {
     float start[C], end[C];
     int doc[C];
     float whole;
+    int odd;  // something in the chunk is not finite
 
     __device__ __forceinline__ void make(float g, int lane) {
-        const bool cut = g < kCut;
-        double sum = cut ? 0.0 : (double)g * kLog2e;
+        const bool cut = g < kCut, bad = !(g < __builtin_inff());
+        double sum = cut || bad ? 0.0 : (double)g * kLog2e;
         sum += moved<0x111, 0xf>(sum);  // inclusive: within rows of 16 lanes, then of the rows
         sum += moved<0x112, 0xf>(sum);
         sum += moved<0x114, 0xf>(sum);
@@ -368,14 +399,20 @@ struct Decays {
         sum += moved<0x142, 0xa>(sum);
         sum += moved<0x143, 0xc>(sum);
         const uint64_t cuts = __ballot(cut);
-        const uint64_t upto = cuts & (~0ull >> (63 - lane));
+        const uint64_t until = ~0ull >> (63 - lane), upto = cuts & until;
+        // a g of NaN or infinity is one for its document, from there on
+        const uint64_t bads = __ballot(bad) & until;
+        if (bads > upto) sum = __builtin_nan("");
         const double all = lane_of(sum, C - 1);
         if (lane < C) {
             G[lane] = sum;
             doc[lane] = __popcll(upto);
             start[lane] = upto ? 0.0f : exp2_of(sum);
             end[lane] = upto == cuts ? exp2_of(all - sum) : 0.0f;
-            if (lane == 0) whole = cuts ? 0.0f : exp2_of(all);
+            if (lane == 0) {
+                whole = cuts ? 0.0f : exp2_of(all);
+                odd = 0;
+            }
         }
     }
     // the decay from token j to token i, 0 for j > i and across a cut
@@ -383,6 +420,121 @@ struct Decays {
         return causal && di == dj ? __builtin_amdgcn_exp2f((float)(Gi - Gj)) : 0.0f;
     }
 };
+
+// NaN if one of these is not finite, else 0.
+__device__ __forceinline__ float not_finite(const f32x16 &x) {
+    float z = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) z = __builtin_fmaf(x[r], 0.0f, z);
+    return z;
+}
+template <int N>
+__device__ __forceinline__ bool any_not_finite(const bf16x8 (&x)[N]) {
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    s16x2 most = {0, 0};
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const u32x4 w = __builtin_bit_cast(u32x4, x[n]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most = __builtin_elementwise_max(most, __builtin_bit_cast(s16x2, w[e] & 0x7fff7fffu));
+    }
+    return __ballot(most[0] >= 0x7f80 || most[1] >= 0x7f80) != 0;
+}
+template <int N>
+__device__ __forceinline__ bool any_not_finite(const f32x4 (&x)[N]) {
+    float z = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z = __builtin_fmaf(x[n][e], 0.0f, z);
+    return __ballot(z != z) != 0;
+}
+
+// What a chunk's products on the matrix cores make of a value that is not finite: a NaN wherever its weight is 0,
+// before it and in other documents too. The sweep makes a chunk that has one pair by pair and token by token,
+// without those that do not meet: acc (lanes: tokens, rows: 32 columns of `tile` from quad `first` on) gets the scores'
+// products with the rows of the tile,
+template <typename T, int C, int F, bool BELOW, int TT>
+__device__ __forceinline__ void pairs_add(f32x16 (&acc)[TT], const char *scores, const char *tile, int first, const Decays<C> &dec,
+                                          int l31, int half) {
+#pragma unroll 1
+    for (int n = 0; n < C; ++n) {
+        f32x4 x[4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a) x[a] = Tile<T, C, F>::quad(tile, n, first + 2 * a + half);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+            const int token = j * 32 + l31;
+            const bool meet = (BELOW ? n <= token : n >= token) && dec.doc[n] == dec.doc[token];
+            const float p = meet ? Scores<T, C, BELOW>::one(scores, token, n) : 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[j][r] += meet ? x[r / 4][r % 4] * p : 0.0f;
+        }
+        fence();
+    }
+}
+// and a state the tokens of document `doc`.
+template <typename T, int C, int FK, int FV, int TILES>
+__device__ __forceinline__ void state_add_tokens(f32x16 (&S)[TILES], const char *k_tile, const char *v_tile, int column, const float *w,
+                                                 const Decays<C> &dec, int doc, int half) {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) S[t][r] = dec.whole == 0.0f ? 0.0f : S[t][r] * dec.whole;
+#pragma unroll 1
+    for (int n = 0; n < C; ++n) {
+        if (__builtin_amdgcn_readfirstlane(dec.doc[n]) != doc) continue;
+        const float v = w[n] * Tile<T, C, FV>::one(v_tile, n, column);
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const f32x4 k = Tile<T, C, FK>::quad(k_tile, n, t * 8 + 2 * a + half);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[t][4 * a + e] += k[e] * v;
+            }
+            fence();
+        }
+    }
+}
+
+// The backward leaves out the tokens that have such a value, and gives their documents NaN in this chunk: where
+// `spoilt` is NaN and, if the chunk's first is one, by the tokens' weights in what leaves the chunk. One thread a token.
+template <typename T, int C, int KP, int VP>
+__device__ __forceinline__ void take_out(char *qt, char *kt, char *vt, char *dt, const Decays<C> &dec, float *spoilt, float *back, int tid) {
+    if (tid < C) {
+        const auto row = [&](auto tile, char *t, bool clear) {
+            typedef decltype(tile) Of;
+            float z = 0.0f;
+#pragma unroll 1
+            for (int q = 0; q < Of::W; ++q) {
+                const f32x4 x = Of::quad(t, tid, q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z = __builtin_fmaf(x[e], 0.0f, z);
+                if (clear) Of::put(t, tid, q, f32x4{0, 0, 0, 0});
+            }
+            return z;
+        };
+        const Tile<T, C, KP> keys;
+        const Tile<T, C, VP> values;
+        const float z = row(keys, qt, false) + row(keys, kt, false) + row(values, vt, false) + row(values, dt, false);
+        const uint64_t bad = __ballot(z != z);  // of the first wave
+        if (z != z) {
+            row(keys, qt, true);
+            row(keys, kt, true);
+            row(values, vt, true);
+            row(values, dt, true);
+        }
+        float mine = 0.0f;
+#pragma unroll 1
+        for (int n = 0; n < C; ++n) {
+            const float x = bad >> n & 1 ? __builtin_nanf("") : 0.0f;
+            if (dec.doc[n] == dec.doc[tid]) mine += x;
+        }
+        spoilt[tid] = mine;
+        if (dec.doc[tid] == 0) back[tid] += mine;
+    }
+}
 
 // b, head and piece of a block. Blocks of one XCD (every eighth) take neighbouring work, which
 // shares q and k: heads of a group and slices of V.
@@ -579,6 +731,10 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
                     acc = mfma(TK::by_row(kt + jt * kDown, krow, s), TK::by_row(qt + it2 * kDown, krow, s), acc);
                     if (s % 4 == 3) fence();
                 }
+                if (it2 == jt) {  // every token's q and k are in these
+                    const float z = not_finite(acc);
+                    if (z != z) decays[it & 1].odd = 1;
+                }
                 const double Gi = dec.G[i];
                 const int di = dec.doc[i];
 #pragma unroll
@@ -600,6 +756,7 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
 #pragma unroll
             for (int s = 0; s < C / KS; ++s) v[s] = TV::by_column(vt, vcolumn ^ (wave * 32 * (int)sizeof(T)), 0, s);
         }
+        const bool odd = OUT && (__builtin_amdgcn_readfirstlane(dec.odd) != 0 || any_not_finite(v));
         if (OUT) {
             f32x16 o[TT] = {};
 #pragma unroll
@@ -623,12 +780,16 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[i][r] = w == 0.0f ? 0.0f : o[i][r] * w;
             }
+            if (odd) {
+                pairs_add<T, C, VT, true>(o, pt, vt, wave * 8, dec, l31, half);
+            } else {
 #pragma unroll
-            for (int s = 0; s < C / KS; ++s)
+                for (int s = 0; s < C / KS; ++s)
 #pragma unroll
-                for (int e = 0; e < N::kOut; ++e)
+                    for (int e = 0; e < N::kOut; ++e)
 #pragma unroll
-                    for (int i = s / (32 / KS); i < TT; ++i) o[i] = mfma(v[s], TP::by_row(pt, prow, i, s, e), o[i]);
+                        for (int i = s / (32 / KS); i < TT; ++i) o[i] = mfma(v[s], TP::by_row(pt, prow, i, s, e), o[i]);
+            }
 #pragma unroll
             for (int i = 0; i < TT; ++i) {
 #pragma unroll
@@ -637,7 +798,16 @@ __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
                 fence();
             }
         }
-        state_add<T, C, KP, KT>(S, kt, v, rev ? dec.start : dec.end, dec.whole, half, kcol);
+        const float *const weights = rev ? dec.start : dec.end;
+        const auto by_token = [&] { state_add_tokens<T, C, KP, VT>(S, kt, vt, wave * 32 + l31, weights, dec, rev ? 0 : dec.doc[C - 1], half); };
+        if (odd) by_token();
+        else state_add<T, C, KP, KT>(S, kt, v, weights, dec.whole, half, kcol);
+        if (!OUT && dec.whole == 0.0f) {  // else every token is of the document that goes on
+            float z = 0.0f;
+#pragma unroll
+            for (int t = 0; t < KT; ++t) z += not_finite(S[t]);
+            if (__ballot(z != z)) by_token();
+        }
         if (!OUT) {
             decayed += dec.G[C - 1];
             cut |= dec.whole == 0.0f;
@@ -713,6 +883,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     __shared__ Decays<C> decays[2];
     __shared__ float backs[2][C];         // scale e^{G_i}
     __shared__ float came[KT][C], left[KT][C], through[KT];
+    __shared__ float spoilt[C];           // NaN for the tokens of a document that has a value that is not finite
     char *const qt = lds, *const kt = qt + TK::kBytes, *const vt = kt + TK::kBytes, *const dt = vt + TV::kBytes;
     char *const at = dt + TV::kBytes, *const bt = at + TQ::kBytes, *const bn = bt + TQ::kBytes, *const mt = bn + TP::kBytes;
     char *const ov = mt + TM::kBytes, *const oq = ov + TV::kBytes;  // dv and dq on their way out
@@ -794,6 +965,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
             load_g(c1 - 2);
         }
         fetch(c1 - 1);
+        __syncthreads();  // the decays say that nothing is odd before a lane may say so
     }
     for (int c = c1 - 1; c >= c0; --c) {
         const int64_t t0 = (int64_t)c * C;
@@ -808,7 +980,13 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
         kr.store(kt, tid, p.K);
         vr.store(vt, tid, p.V);
         dr.store(dt, tid, p.V);
+        if (qr.not_finite() || kr.not_finite() || vr.not_finite() || dr.not_finite()) decays[c & 1].odd = 1;
         __syncthreads();
+        const bool odd = __builtin_amdgcn_readfirstlane(dec.odd) != 0;
+        if (odd) {  // is made without the tokens that have it; what is left of their documents is spoilt at the end
+            take_out<T, C, KP, VP>(qt, kt, vt, dt, dec, spoilt, backs[c & 1], tid);
+            __syncthreads();
+        }
         if (c + 1 < c1) put_outputs(c + 1);
         constexpr int kDown = 32 * TK::kBytes / C, vDown = 32 * TV::kBytes / C;  // 32 rows further
         const int krow = TK::at(l31, half), vrow = TV::at(l31, half), prow = TP::at(l31, half);
@@ -882,7 +1060,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                         const float w = p.scale * dec.between(dec.G[i0 + e], dec.doc[i0 + e], Gj, dj, j <= i0 + e);
                         x[e] = qk[4 * a + e] * w;
                         y[e] = dov[4 * a + e] * w;
-                        m[e] = j < i0 + e ? x[e] * dov[4 * a + e] : 0.0f;
+                        m[e] = j < i0 + e && w != 0.0f ? x[e] * dov[4 * a + e] : 0.0f;
                     }
                     TQ::put(at, j, i0 / 4, x);
                     TQ::put(bt, j, i0 / 4, y);
@@ -975,7 +1153,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
                         }
                     }
                     sum += __shfl_xor(sum, 32);
-                    if (half == 0) share_of[j * 32 + l31] = sum;
+                    if (half == 0) share_of[j * 32 + l31] = w == 0.0f ? 0.0f : sum;
                 }
             };
             const auto put = [&](const f32x16(&acc)[TT], void *out) {
@@ -1096,6 +1274,26 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
             state_add<T, C, VP, VW>(SK, dt, f, back, dec.whole, half, vcol);
         }
         __syncthreads();
+        if (odd) {  // over what has been written: dk, and dq of shared heads, are in memory, the others wait in LDS
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "agent");  // other lanes write it again
+            __syncthreads();
+            for (int r = wave; r < rows; r += NW) {
+                const float x = spoilt[r];
+                if (x == 0.0f) continue;
+                const f32x4 quad = {x, x, x, x};
+                if (lane < VP / 4) TV::put(ov, r, lane, quad);
+                if (lane < KP / 4 && !shared) TK::put(oq, r, lane, quad);
+                for (int e = lane; e < p.K; e += 64) {
+                    if (shared) {
+                        *(float *)((char *)p.dk + ((b * p.L + t0 + r) * p.H + h) * p.K * 4 + e * 4) = x;
+                        *(float *)((char *)p.dq + ((b * p.L + t0 + r) * p.H + h) * p.K * 4 + e * 4) = x;
+                    } else {
+                        ((T *)p.dk)[((b * p.L + t0 + r) * p.Hk + hk) * p.K + e] = (T)x;
+                    }
+                }
+            }
+            __syncthreads();
+        }
         if (wave == 0) {  // dg
             float d = pairs, a = 0.0f, e = 0.0f;
             if (lane < C) {
@@ -1116,6 +1314,7 @@ __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
             before = __shfl_up(before, 1);
             if (lane > 0) d += before;
             d += a;
+            if (odd && lane < C) d += spoilt[lane];
             if (lane < C && t0 + lane < p.L) p.dg[(b * p.L + t0 + lane) * p.H + h] = d;
         }
     }
