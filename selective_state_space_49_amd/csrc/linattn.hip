@@ -612,9 +612,9 @@ __device__ __forceinline__ void state_add(f32x16 (&S)[TILES], const char *k_tile
 // outputs, from the segment's entering state; else what the segment adds to the state, from 0. A wave has all
 // of K for its 32 columns, so its state never leaves the accumulators; the block's waves share the chunk's q, k
 // and scores in LDS, and two blocks share a compute unit so that one's products run beside the other's decays
-// and roundings. Those vector instructions and the reads of LDS bound it (each busy half the time, the matrix
-// cores 28 %): 262144 tokens x 32 heads of 128 x 128 in bf16, 1.90 ms with outputs and 1.09 without, for 1.2 ms
-// of bytes; 2 x 4096 tokens 101 and 43 us.
+// and roundings. Those vector instructions and the reads of LDS bound it (busy 53 % and 41 % of the time, the matrix
+// cores 32 %): 262144 tokens x 32 heads of 128 x 128 in bf16, 2.48 ms with outputs and 1.11 without, for 1.2 ms
+// of bytes; 2 x 4096 tokens 108 and 44 us.
 template <typename T, int KP, int NW, bool OUT, Access ACC>
 __global__ void __launch_bounds__(64 * NW, 2) k_sweep(SweepArgs p) {
     typedef Kind<T> N;
@@ -865,9 +865,9 @@ struct BwdArgs {
 // The gradients of a segment, from its end. VP / 32 waves hold dS by columns of V and make dv;
 // KP / 32 waves hold it transposed, by columns of K, and make dk and dq: each role's gradients need dS as an
 // operand in another order, and holding it twice costs a product where turning it around costs LDS that is
-// already full. A chunk's tiles take 145 KB of LDS with all heads of 128, so a block has the compute unit to
-// itself, and what bounds it are vector and LDS instructions between its barriers: 2 x 4096 tokens x 32 heads of
-// 128 x 128 in bf16, 247 us (740 MB with states, 3.0 TB/s).
+// already full. A chunk's tiles take 157 KB of LDS with all heads of 128, so a block has the compute unit to
+// itself, and what bounds it are vector and LDS instructions between its barriers (busy 47 % and 27 % of the time, the
+// matrix cores 25 %): 2 x 4096 tokens x 32 heads of 128 x 128 in bf16, 265 us (740 MB with states, 2.8 TB/s).
 template <typename T, int KP, int VP, Access ACC>
 __global__ void __launch_bounds__(2 * (KP + VP)) k_bwd(BwdArgs p) {
     typedef Kind<T> N;

@@ -16,12 +16,11 @@
 // the end is exact. A list that is too long for LDS is not made: bfloat16 logits around 20 lie 1/8 apart, and
 // thousands of 131072 are equal. The end is found in their steps then by their places' digits, 11 bits a pass
 // from the highest that differ on (a row of 131072 around 20, top_p 0.9: 350 us, 93 around 0; 256 of them 412 and
-// 119). So it is among all logits if the steps do not
-// hold the end, or a logit is +infinity.
+// 119). So it is among all logits if the steps do not hold the end, or a logit is +infinity.
 //
-// What bounds it are the vector instructions of the last two passes, one block a row: 256 rows of 131072
-// float32 logits in 129 us (1.0 TB/s), one row of 32000 in
-// 28 us with a top_k of some tens: extremes 5, histogram 4, its plan 2, the list 4, its end 10, the draw 2.
+// A block has a row, so a batch takes as long as its slowest row and a row as long as its chain of passes: 256 rows
+// of 131072 float32 logits, each with its own settings, in 126 us (1.1 TB/s; a compute unit has work 54 % of that
+// time, and its vector units are busy half of it), one row of 32000 in 27 us with a top_k of some tens.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -303,8 +302,8 @@ __device__ __forceinline__ void count_steps(const Logits<T> &l, const Steps &st,
 
 // Where the kept ones end: the step of top_k's last (kBins: it keeps all that has mass) and the number
 // before that step; the steps in which top_p's last lies. Where top_k keeps so few that the list holds them all
-// with their last step (`whole`), they need no masses but in the list (one row of 32000 with 50 of them: 28
-// us, 32 without this).
+// with their last step (`whole`), they need no masses but in the list (one row of 32000 with 50 of them: 27
+// us, 31 without this).
 struct Plan {
     int end_k, p_from, p_to;
     u64 before_k;
